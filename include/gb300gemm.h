@@ -307,6 +307,164 @@ int gemm_int4_repack(const uint8_t* q, int K, int N, int ldq, uint8_t* qk, cudaS
 int gemm_attention(int B, int Hq, int Hkv, int Sq, int Sk, int D, const gemm_bf16_t* Q, const gemm_bf16_t* K,
                    const gemm_bf16_t* V, gemm_bf16_t* O, float scale, int causal, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A serving step's operators around the GEMMs: a paged key/value cache held
+ * in 8 bits (append with the position rotation, attention over it) and
+ * sampling of the LM head's logits.  The source pages name none of them; they
+ * are this library's additions.
+ * ------------------------------------------------------------------------ */
+
+/* Element formats of a paged cache: one byte a value, times the scale of its
+ * page and head. */
+typedef enum {
+  GEMM_KV_E4M3 = 0, /* OCP E4M3, largest value 448 */
+  GEMM_KV_INT8 = 1  /* two's complement, -127 .. 127 */
+} gemm_kv_format;
+
+/*
+ * A paged key/value cache.  Token t of sequence b lives in page
+ * g = table[b*table_stride + t / page_tokens] at row r = t % page_tokens, and
+ * value d of its head h is
+ *
+ *     k[g*page_stride + h*head_stride + r*token_stride + d] * k_scale[g*heads + h]
+ *
+ * (v and v_scale alike; strides are in bytes, shared by k and v).  Everything
+ * but the struct itself is DEVICE memory owned by the caller; the struct is
+ * read during the call only.  The fast kernels need dim 64 or 128, page_tokens
+ * 16, 32, 64 or 128 and k, v and the strides multiples of 16 bytes; others run a
+ * generic kernel (dim at most 512).  A cache whose codes, scales or table
+ * disagree with the call (a page number outside 0 .. pages-1, a token past the
+ * table's columns) is not followed out of bounds: the kernel skips what it
+ * cannot place, and gemm_device_status() reports GEMM_ERR_INVALID_ARG.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale; /* pages x heads, contiguous */
+  float* v_scale;
+  const int* table; /* seqs x table_cols page numbers */
+  long long page_stride, head_stride, token_stride;
+  long long table_stride; /* in elements, >= table_cols */
+  int format;             /* gemm_kv_format */
+  int pages, page_tokens, heads, dim;
+  int seqs, table_cols;
+} gemm_kv_cache;
+
+/*
+ * Append new tokens to a paged cache, rotating queries and keys by position
+ * on the way.
+ *
+ * Sequence b's new tokens are rows start[b] .. start[b+1]-1 of Q, K and V
+ * (seqs+1 ints), at positions base[b], base[b]+1, ... of the sequence (base[b]
+ * tokens are in the cache already).  start == NULL: one token a sequence, row
+ * b.  No sequence has more than max_new of them.  A row holds its heads side by
+ * side, dim values each; ldq, ldk, ldv, ldqo are the elements between rows, so
+ * Q, K and V may be columns of one matrix.
+ *
+ * The rotation turns the first `rotated` values x of each query and key head by
+ * the angles of its position p (cos and sin: positions x rotated/2 fp32,
+ * contiguous): pairs (x[j], x[j + rotated/2]), or (x[2j], x[2j+1]) when
+ * interleaved != 0, become
+ *
+ *     (a*cos - b*sin, b*cos + a*sin)
+ *
+ * with every product and sum rounded to fp32 by itself.  rotated is even, 0 to
+ * dim (0: cos and sin may be NULL).  Rotated queries are rounded once to bf16
+ * into Qout (Hq heads; Hq == 0: no queries, Q and Qout may be NULL; Qout may be
+ * Q).  Values past `rotated`, and V, are taken as they are.
+ *
+ * For each page and head that the call writes, and for K and V apart, with a the
+ * largest magnitude among the call's tokens there and qmax 448 or 127:
+ *
+ *     s = a / qmax, or 0 below 2^-126; if the page holds earlier tokens, the
+ *         larger of that and the page's present scale
+ *     code = x * (1/s) rounded to nearest even on the format's grid, at most
+ *            qmax in magnitude; 0 when s is 0
+ *
+ * and when s is larger than the page's present scale s0, the earlier tokens'
+ * codes c become (c * s0) * (1/s), rounded the same way.  So no value is ever
+ * clipped, and appending again what is there changes nothing.  A page that a
+ * sequence enters at its first row starts with a new scale.  Infinities are
+ * stored as the largest finite value of a page whose scale is FLT_MAX / qmax;
+ * NaN is ignored in a, and stored as E4M3's NaN or as INT8's 0.
+ *
+ * Pages that the call writes belong to one sequence each (two sequences may
+ * share pages that only hold earlier tokens).  At most 65535 heads; tokens
+ * past the table, or at positions >= `positions`, are not stored (see
+ * gemm_kv_cache).  Asynchronous, no allocation, deterministic.
+ */
+int gemm_kv_append(const gemm_kv_cache* cache, int tokens, int Hq, const gemm_bf16_t* Q, long long ldq,
+                   const gemm_bf16_t* K, long long ldk, const gemm_bf16_t* V, long long ldv, gemm_bf16_t* Qout,
+                   long long ldqo, const float* cos, const float* sin, int positions, int rotated,
+                   int interleaved, const int* base, const int* start, int max_new, cudaStream_t stream);
+
+/*
+ * Attention of each sequence's newest tokens over its paged cache:
+ *
+ *     O = softmax(Q K^T * scale) V,   K and V as gemm_kv_cache defines their values
+ *
+ * lengths[b] tokens of sequence b are in the cache, the newest n = start[b+1] -
+ * start[b] of them with queries in rows start[b] .. of Q (start == NULL: n = 1,
+ * row b); no sequence has more than max_new.  Query i of the n sees keys j <=
+ * lengths[b] - n + i.  A row that sees no key is 0 (lengths[b] == 0, or fewer
+ * keys than queries).  Cache rows past a sequence's length are never used,
+ * whatever they hold.  Q and O have Hq heads of dim values side by side in a row,
+ * ldq and ldo elements between rows; Hq is a multiple of the cache's heads, and
+ * query head h reads head h / (Hq / heads).  scale == 0 means 1/sqrt(dim).
+ *
+ * Scores, softmax statistics and sums are fp32; the codes, and the queries after
+ * an exact power-of-two scaling of each row, enter the products in fp16 (a query
+ * value 2^40 times smaller than its row's largest may lose bits), and so do the
+ * probabilities times the page's scale.  O is rounded once to bf16.
+ *
+ * workspace: gemm_kv_attention_workspace() bytes of DEVICE memory, 16-byte
+ * aligned, zeroed once before its first use and owned by one call at a time (every
+ * call leaves it ready for the next of any shape that it is large enough for).
+ * After gemm_device_status() has reported a timeout, zero it again.
+ * Asynchronous, no allocation, deterministic.
+ */
+int gemm_kv_attention(const gemm_kv_cache* cache, int tokens, int Hq, const gemm_bf16_t* Q, long long ldq,
+                      gemm_bf16_t* O, long long ldo, const int* lengths, const int* start, int max_new,
+                      float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace of a gemm_kv_attention call on the current device (0 on bad
+ * arguments). */
+size_t gemm_kv_attention_workspace(int seqs, int heads, int Hq, int dim, int max_new);
+
+/*
+ * Sampling: one token of each row of logits (rows x vocab, ld elements between
+ * rows; bf16 or fp32), from one given uniform number u[row] in [0, 1).
+ *
+ * With l the row's logits, t its temperature and m the largest l:
+ *
+ *     w[i] = expf((l[i] - m) * (1/t)),  mass[i] = floor(2^40 * w[i])
+ *
+ * Masses are whole numbers, so their sums are the same in any order.  Tokens rank
+ * by l, largest first, equal ones by lowest index.  Kept are
+ *     top_k:  the first top_k ranks (top_k <= 0: all);
+ *     top_p:  of those, with M their total mass, the ranks with less than
+ *             top_p * M before them, the first always;
+ *     min_p:  of those, the tokens with w >= min_p, the first rank always.
+ * With T the kept tokens' total mass, the token is the first, in index order, at
+ * which the running mass of the kept exceeds floor(u * T) (products with u and
+ * top_p in fp64; u outside [0, 1) is taken to the nearest of the range, NaN to
+ * 0).  t <= 0 (or below 2^-126): the first rank.  logprob = (l - m) * (1/t) -
+ * log(T / 2^40), the token's log-probability among the kept (0 for t <= 0).
+ *
+ * NaN logits count as -inf; a logit of -inf is never taken.  A row whose logits
+ * are all -inf gives token -1 and logprob -inf.  Where some are +inf, they alone
+ * have weight, 1 each.  temperature (NULL: 1), top_k, top_p and min_p (NULL:
+ * off), u, token and logprob (NULL: not wanted) are DEVICE arrays of `rows`
+ * values.  vocab is at most 2^20 (GEMM_ERR_UNSUPPORTED above).  Asynchronous, no
+ * allocation, deterministic.
+ */
+int gemm_sample_bf16(int rows, int vocab, const gemm_bf16_t* logits, long long ld, const float* temperature,
+                     const int* top_k, const float* top_p, const float* min_p, const float* u, int* token,
+                     float* logprob, cudaStream_t stream);
+int gemm_sample_f32(int rows, int vocab, const float* logits, long long ld, const float* temperature,
+                    const int* top_k, const float* top_p, const float* min_p, const float* u, int* token,
+                    float* logprob, cudaStream_t stream);
+
 /*
  * Message for the last non-OK return on the calling host thread ("" if none).
  * The string is owned by the library and valid until the next call on this
@@ -321,7 +479,9 @@ const char* gemm_get_last_error(void);
  * every stream and host thread: a failure recorded by a kernel on another
  * stream is either in the value taken or left for the next call, never lost.
  * Returns GEMM_OK, GEMM_ERR_DEVICE_TIMEOUT (a kernel gave up a bounded wait
- * and returned early; its C is unspecified), or GEMM_ERR_CUDA if the launch
+ * and returned early; its C is unspecified), GEMM_ERR_INVALID_ARG (a paged
+ * cache's kernel met a page number, length or row range that does not fit the
+ * call, and skipped it), or GEMM_ERR_CUDA if the launch
  * or synchronisation itself failed.  If `where` is not NULL it receives the
  * kernel-specific location code of the first failure (0 if none).  The
  * `where` argument is this library's addition to the surveyed
@@ -345,8 +505,11 @@ typedef enum {
                              the per-byte fallback reports GEMM_PATH_GENERIC) */
   GEMM_PATH_W4 = 6,       /* INT4-weight decode GEMM, tcgen05 kernel (reported only;
                              its one-thread-per-element fallback reports GEMM_PATH_GENERIC) */
-  GEMM_PATH_ATTN = 7      /* attention, tcgen05 kernel (reported only; its
+  GEMM_PATH_ATTN = 7,     /* attention, tcgen05 kernel (reported only; its
                              one-block-per-row fallback reports GEMM_PATH_GENERIC) */
+  GEMM_PATH_KV = 8,       /* paged cache, fast append or attention kernel (reported only; the
+                             fallbacks report GEMM_PATH_GENERIC) */
+  GEMM_PATH_SAMPLE = 9    /* sampling (reported only) */
 } gemm_path;
 
 /*

@@ -31,18 +31,21 @@ GEMM_ERR_UNSUPPORTED = 3
 GEMM_ERR_CUDA = 4
 GEMM_ERR_DEVICE_TIMEOUT = 5
 
-PATH_AUTO, PATH_GENERIC, PATH_F32_SIMT, PATH_BF16_TC, PATH_SKINNY, PATH_INT4, PATH_W4, PATH_ATTN = range(8)
+PATH_AUTO, PATH_GENERIC, PATH_F32_SIMT, PATH_BF16_TC, PATH_SKINNY, PATH_INT4, PATH_W4, PATH_ATTN, \
+    PATH_KV, PATH_SAMPLE = range(10)
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = range(4)
 FP8_E4M3, FP8_E5M2 = 0, 1
+KV_E4M3, KV_INT8 = 0, 1
 PATH_NAMES = {PATH_AUTO: "none", PATH_GENERIC: "generic", PATH_F32_SIMT: "f32_simt",
               PATH_BF16_TC: "bf16_tc", PATH_SKINNY: "skinny", PATH_INT4: "int4", PATH_W4: "w4",
-              PATH_ATTN: "attention"}
+              PATH_ATTN: "attention", PATH_KV: "kv", PATH_SAMPLE: "sample"}
 
 # every symbol the public header declares
 EXPORTS = ("gemm_f32", "gemm_f32_noalloc", "gemm_bf16", "gemm_bf16_f32out", "gemm_f32_ex", "gemm_bf16_ex",
            "gemm_bf16_f32out_ex", "gemm_bf16_swiglu", "gemm_fp8", "gemm_fp8_f32out",
            "gemm_int4_dequant", "gemm_int4_dequant_f32", "gemm_w4a16", "gemm_w4a16_f32out",
-           "gemm_int4_repack", "gemm_w4_packed_bytes", "gemm_attention", "gemm_get_last_error",
+           "gemm_int4_repack", "gemm_w4_packed_bytes", "gemm_attention", "gemm_kv_append", "gemm_kv_attention",
+           "gemm_kv_attention_workspace", "gemm_sample_bf16", "gemm_sample_f32", "gemm_get_last_error",
            "gemm_device_status", "gemm_force_path", "gemm_last_path", "gemm_force_tile_n",
            "gemm_last_tile_n", "gemm_force_tc_pair", "gemm_last_tc_pair", "gemm_force_split_tiles",
            "gemm_last_k_split", "gemm_set_wait_timeout_ns",
@@ -50,6 +53,17 @@ EXPORTS = ("gemm_f32", "gemm_f32_noalloc", "gemm_bf16", "gemm_bf16_f32out", "gem
 
 _lib = None
 _lock = threading.Lock()
+
+
+class KVCacheStruct(ctypes.Structure):
+    """gemm_kv_cache of the C ABI."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("page_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("token_stride", ctypes.c_longlong), ("table_stride", ctypes.c_longlong),
+                ("format", ctypes.c_int), ("pages", ctypes.c_int), ("page_tokens", ctypes.c_int),
+                ("heads", ctypes.c_int), ("dim", ctypes.c_int), ("seqs", ctypes.c_int),
+                ("table_cols", ctypes.c_int)]
 
 
 class GemmError(RuntimeError):
@@ -99,6 +113,17 @@ def load(path: str | None = None):
         lib.gemm_int4_repack.restype = i
         lib.gemm_attention.argtypes = [i, i, i, i, i, i, vp, vp, vp, vp, f, i, vp]
         lib.gemm_attention.restype = i
+        ll, sz = ctypes.c_longlong, ctypes.c_size_t
+        lib.gemm_kv_append.argtypes = [vp, i, i, vp, ll, vp, ll, vp, ll, vp, ll, vp, vp, i, i, i, vp, vp, i, vp]
+        lib.gemm_kv_append.restype = i
+        lib.gemm_kv_attention.argtypes = [vp, i, i, vp, ll, vp, ll, vp, vp, i, f, vp, sz, vp]
+        lib.gemm_kv_attention.restype = i
+        lib.gemm_kv_attention_workspace.argtypes = [i, i, i, i, i]
+        lib.gemm_kv_attention_workspace.restype = sz
+        for name in ("gemm_sample_bf16", "gemm_sample_f32"):
+            fn = getattr(lib, name)
+            fn.argtypes = [i, i, vp, ll, vp, vp, vp, vp, vp, vp, vp, vp]
+            fn.restype = i
         lib.gemm_w4_packed_bytes.argtypes = [i, i]
         lib.gemm_w4_packed_bytes.restype = ctypes.c_size_t
         for name in ("gemm_fp8", "gemm_fp8_f32out"):
@@ -211,6 +236,34 @@ def gemm_int4_repack(q, K, N, ldq, qk, stream=0):
 
 def gemm_attention(B, Hq, Hkv, Sq, Sk, D, Q, K, V, O, scale=0.0, causal=0, stream=0):
     _check(load().gemm_attention(B, Hq, Hkv, Sq, Sk, D, Q, K, V, O, scale, causal, stream))
+
+
+def gemm_kv_append(cache, tokens, Hq, Q, ldq, K, ldk, V, ldv, Qout, ldqo, cos, sin, positions, rotated,
+                   interleaved, base, start, max_new, stream=0):
+    """`cache`: a KVCacheStruct."""
+    _check(load().gemm_kv_append(ctypes.addressof(cache), tokens, Hq, Q, ldq, K, ldk, V, ldv, Qout, ldqo, cos, sin,
+                                 positions, rotated, interleaved, base, start, max_new, stream))
+
+
+def gemm_kv_attention(cache, tokens, Hq, Q, ldq, O, ldo, lengths, start, max_new, scale, workspace, workspace_bytes,
+                      stream=0):
+    """`cache`: a KVCacheStruct."""
+    _check(load().gemm_kv_attention(ctypes.addressof(cache), tokens, Hq, Q, ldq, O, ldo, lengths, start, max_new,
+                                    scale, workspace, workspace_bytes, stream))
+
+
+def gemm_kv_attention_workspace(seqs, heads, Hq, dim, max_new) -> int:
+    return int(load().gemm_kv_attention_workspace(seqs, heads, Hq, dim, max_new))
+
+
+def gemm_sample_bf16(rows, vocab, logits, ld, temperature, top_k, top_p, min_p, u, token, logprob, stream=0):
+    _check(load().gemm_sample_bf16(rows, vocab, logits, ld, temperature, top_k, top_p, min_p, u, token, logprob,
+                                   stream))
+
+
+def gemm_sample_f32(rows, vocab, logits, ld, temperature, top_k, top_p, min_p, u, token, logprob, stream=0):
+    _check(load().gemm_sample_f32(rows, vocab, logits, ld, temperature, top_k, top_p, min_p, u, token, logprob,
+                                  stream))
 
 
 def device_status(stream=0) -> tuple[int, int]:
@@ -415,3 +468,164 @@ def attention(Q, K, V, O, scale: float = 0.0, causal: bool = False, stream=None)
     gemm_attention(B, Hq, Hkv, Sq, Sk, D, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
                    float(scale), int(bool(causal)), s)
     return O
+
+
+class KVCache:
+    """A paged key/value cache of CUDA tensors held in 8 bits (gemm_kv_cache).
+
+    k, v: [pages][heads][page_tokens][dim] codes, any strides with dim contiguous
+    and the same for both: float8_e4m3fn or int8, or uint8 with `fmt` (KV_E4M3,
+    KV_INT8).  k_scale, v_scale: [pages][heads] fp32.  table: [seqs][columns]
+    int32 page numbers, the columns contiguous.  The tensors are the caller's and
+    are used in place; `rows(n)` is the same cache with the first n table rows.
+    """
+
+    def __init__(self, k, v, k_scale, v_scale, table, fmt: int | None = None):
+        import torch
+        fmts = {torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_INT8, torch.uint8: fmt}
+        if k.dim() != 4 or fmts.get(k.dtype) is None or v.dtype != k.dtype:
+            raise TypeError("KVCache: k and v are 4-D tensors of float8_e4m3fn, int8 or (with fmt) uint8 codes")
+        if fmt is not None and fmts[k.dtype] != fmt:
+            raise TypeError("KVCache: fmt does not fit the codes' type")
+        pages, heads, page_tokens, dim = k.shape
+        if v.shape != k.shape or v.stride() != k.stride() or (dim > 1 and k.stride(3) != 1):
+            raise ValueError("KVCache: k and v have one shape and one set of strides, with dim contiguous")
+        for s in (k_scale, v_scale):
+            if s.dtype != torch.float32 or tuple(s.shape) != (pages, heads) or not s.is_contiguous():
+                raise TypeError("KVCache: scales are contiguous fp32 [pages][heads]")
+        if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise TypeError("KVCache: table is int32 [seqs][columns] with contiguous columns")
+        if not all(t.is_cuda and t.device == k.device for t in (k, v, k_scale, v_scale, table)):
+            raise ValueError("KVCache takes CUDA tensors of one device")
+        self.k, self.v, self.k_scale, self.v_scale, self.table = k, v, k_scale, v_scale, table
+        self.heads, self.dim, self.seqs, self.device = heads, dim, table.shape[0], k.device
+        self.struct = KVCacheStruct(
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), k.stride(0),
+            k.stride(1), max(k.stride(2), dim), max(table.stride(0), table.shape[1]), fmts[k.dtype], pages,
+            page_tokens, heads, dim, table.shape[0], table.shape[1])
+
+    def rows(self, n: int) -> "KVCache":
+        return KVCache(self.k, self.v, self.k_scale, self.v_scale, self.table[:n], self.struct.format)
+
+
+def _heads(t, name: str, heads: int, dim: int, tokens: int) -> int:
+    """Elements between the rows of a bf16 CUDA tensor [tokens][heads][dim] whose
+    heads lie side by side."""
+    import torch
+    if t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} is a bf16 CUDA tensor")
+    if tuple(t.shape) != (tokens, heads, dim):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {(tokens, heads, dim)}")
+    s = t.stride()
+    if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
+        raise ValueError(f"{name}: a row's heads lie side by side")
+    return max(s[0], heads * dim)
+
+
+def _ints(t, name: str, n: int) -> int:
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise TypeError(f"{name} is a contiguous int32 CUDA tensor of {n} values")
+    return t.data_ptr()
+
+
+def kv_append(cache: KVCache, Q, K, V, cos, sin, base, Qout=None, start=None, max_new: int = 1,
+              interleaved: bool = False, stream=None):
+    """Store new tokens' K and V ([tokens][heads][dim] bf16) in the cache behind
+    the base[b] tokens that sequence b has there, with Q ([tokens][Hq][dim], into
+    Qout, default Q itself; or None) and K rotated by position with the tables cos
+    and sin (fp32 [positions][pairs]; None: no rotation).  Sequence b's rows are
+    start[b] .. start[b+1]-1, at most max_new (start None: row b).  Argument
+    marshalling only."""
+    import torch
+    tokens, H, D = K.shape
+    ldk, ldv = _heads(K, "K", cache.heads, cache.dim, tokens), _heads(V, "V", cache.heads, cache.dim, tokens)
+    Hq = ldq = ldo = q = o = 0
+    if Q is not None:
+        Qout = Q if Qout is None else Qout
+        Hq = Q.shape[1]
+        ldq, ldo = _heads(Q, "Q", Hq, D, tokens), _heads(Qout, "Qout", Hq, D, tokens)
+        q, o = Q.data_ptr(), Qout.data_ptr()
+    positions, pairs, c, s = 0x7fffffff, 0, 0, 0
+    if cos is not None:
+        if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape or \
+                not (cos.is_cuda and sin.is_cuda and cos.is_contiguous() and sin.is_contiguous()):
+            raise TypeError("cos and sin are contiguous fp32 CUDA tensors [positions][pairs]")
+        positions, pairs = cos.shape
+        c, s = cos.data_ptr(), sin.data_ptr()
+    st = stream if stream is not None else torch.cuda.current_stream(cache.device).cuda_stream
+    gemm_kv_append(cache.struct, tokens, Hq, q, ldq, K.data_ptr(), ldk, V.data_ptr(), ldv, o, ldo, c, s, positions,
+                   2 * pairs, int(interleaved), _ints(base, "base", cache.seqs),
+                   None if start is None else _ints(start, "start", cache.seqs + 1), int(max_new), st)
+    return Qout
+
+
+# kv_attention's workspaces, one for each device and stream (the C ABI leaves them
+# to the caller): zeroed when made, ready again after every call
+_kv_workspaces: dict = {}
+
+
+def _kv_workspace(device, stream: int, size: int):
+    import torch
+    key = (device.index, stream)
+    w = _kv_workspaces.get(key)
+    if w is None or w.numel() < size:
+        # made on the stream that uses it, so that the zeros are there before
+        # the call and the old one's memory is not reused before its last call
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+            w = torch.zeros((max(size, 1 << 20),), dtype=torch.uint8, device=device)
+        _kv_workspaces[key] = w
+    return w
+
+
+def kv_attention(cache: KVCache, Q, O, lengths, start=None, max_new: int = 1, scale: float = 0.0, workspace=None,
+                 stream=None):
+    """O = softmax(Q K^T * scale) V of each sequence's newest tokens over the
+    cache (scale 0: 1/sqrt(dim)).  Q, O: [tokens][Hq][dim] bf16; lengths[b] tokens
+    are in the cache, the newest of them with queries in rows start[b] ..
+    start[b+1]-1, at most max_new (start None: one token, row b); query i of n
+    sees keys j <= lengths[b] - n + i.  workspace: zeroed uint8 tensor of
+    gemm_kv_attention_workspace() bytes, or None for one that this module keeps
+    for the stream.  Argument marshalling only."""
+    import torch
+    tokens, Hq, D = Q.shape
+    ldq, ldo = _heads(Q, "Q", Hq, cache.dim, tokens), _heads(O, "O", Hq, cache.dim, tokens)
+    st = stream if stream is not None else torch.cuda.current_stream(cache.device).cuda_stream
+    if workspace is None:
+        need = gemm_kv_attention_workspace(cache.seqs, cache.heads, Hq, cache.dim, max_new)
+        workspace = _kv_workspace(cache.device, st, need)
+    gemm_kv_attention(cache.struct, tokens, Hq, Q.data_ptr(), ldq, O.data_ptr(), ldo,
+                      _ints(lengths, "lengths", cache.seqs),
+                      None if start is None else _ints(start, "start", cache.seqs + 1), int(max_new), float(scale),
+                      workspace.data_ptr(), workspace.numel(), st)
+    return O
+
+
+def sample(logits, u, token, logprob=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """One token of each row of logits ([rows][vocab], bf16 or fp32) from the
+    uniform numbers u: token (int32) and, if given, its log-probability among the
+    kept.  temperature, top_p, min_p (fp32) and top_k (int32) are CUDA tensors of
+    one value a row, or None (1, off).  Argument marshalling only."""
+    import torch
+    rows, vocab = logits.shape
+
+    def of(t, name, dtype):
+        if t is None:
+            return None
+        if t.dtype != dtype or not t.is_cuda or t.dim() != 1 or t.shape[0] != rows or not t.is_contiguous():
+            raise TypeError(f"{name} is a contiguous {dtype} CUDA tensor of one value a row")
+        return t.data_ptr()
+    if not logits.is_cuda:
+        raise ValueError("sample() takes CUDA tensors")
+    f32, i32 = torch.float32, torch.int32
+    s = stream if stream is not None else torch.cuda.current_stream(logits.device).cuda_stream
+    args = (rows, vocab, logits.data_ptr(), _ld(logits), of(temperature, "temperature", f32), of(top_k, "top_k", i32),
+            of(top_p, "top_p", f32), of(min_p, "min_p", f32), of(u, "u", f32), of(token, "token", i32),
+            of(logprob, "logprob", f32), s)
+    if logits.dtype == torch.bfloat16:
+        gemm_sample_bf16(*args)
+    elif logits.dtype == f32:
+        gemm_sample_f32(*args)
+    else:
+        raise TypeError(f"unsupported logits dtype {logits.dtype}")
+    return token

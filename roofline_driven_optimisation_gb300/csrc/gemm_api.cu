@@ -630,6 +630,194 @@ int attention(int B, int Hq, int Hkv, int Sq, int Sk, int D, const void* Q, cons
   return GEMM_OK;
 }
 
+// ---------------------------------------------------------------- paged cache
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+// Checks a gemm_kv_cache and fills the kernels' form of it.  `used`: whether the
+// call has any row, so that the cache's memory is touched.
+int kv_cache(const gemm_kv_cache* c, bool used, KvCache* out) {
+  if (c == nullptr) return fail(GEMM_ERR_INVALID_ARG, "cache is NULL");
+  if (c->format != GEMM_KV_E4M3 && c->format != GEMM_KV_INT8)
+    return fail(GEMM_ERR_INVALID_ARG, "unknown cache format %d", c->format);
+  if (c->pages < 0 || c->page_tokens < 1 || c->heads < 1 || c->dim < 1 || c->seqs < 0 || c->table_cols < 0)
+    return fail(GEMM_ERR_INVALID_ARG, "bad cache sizes pages=%d page_tokens=%d heads=%d dim=%d seqs=%d table_cols=%d",
+                c->pages, c->page_tokens, c->heads, c->dim, c->seqs, c->table_cols);
+  if (c->dim > 512) return fail(GEMM_ERR_UNSUPPORTED, "head dimension %d above 512", c->dim);
+  if (c->token_stride < c->dim || c->page_stride < 0 || c->head_stride < 0 || c->table_stride < c->table_cols)
+    return fail(GEMM_ERR_INVALID_ARG, "bad cache strides page=%lld head=%lld token=%lld table=%lld", c->page_stride,
+                c->head_stride, c->token_stride, c->table_stride);
+  // positions are held in 32 bits
+  if ((long long)c->table_cols * c->page_tokens > 0x7fffffffll)
+    return fail(GEMM_ERR_UNSUPPORTED, "table of %d pages of %d tokens: more than 2^31 - 1 positions", c->table_cols,
+                c->page_tokens);
+  if (used && (c->k == nullptr || c->v == nullptr || c->k_scale == nullptr || c->v_scale == nullptr ||
+               c->table == nullptr))
+    return fail(GEMM_ERR_INVALID_ARG, "a cache pointer is NULL");
+  if (!aligned4(c->k_scale) || !aligned4(c->v_scale) || !aligned4(c->table))
+    return fail(GEMM_ERR_MISALIGNED, "a cache pointer is not aligned to 4 bytes");
+  out->k = static_cast<uint8_t*>(c->k);
+  out->v = static_cast<uint8_t*>(c->v);
+  out->ks = c->k_scale;
+  out->vs = c->v_scale;
+  out->table = c->table;
+  out->ps = c->page_stride;
+  out->hs = c->head_stride;
+  out->ts = c->token_stride;
+  out->tstride = c->table_stride;
+  out->fmt = c->format;
+  out->pages = c->pages;
+  out->P = c->page_tokens;
+  out->H = c->heads;
+  out->D = c->dim;
+  out->seqs = c->seqs;
+  out->cols = c->table_cols;
+  return GEMM_OK;
+}
+
+// The sizes that the two calls share: rows, sequences and query heads.
+int kv_sizes(const gemm_kv_cache* c, int tokens, int Hq, const int* start, int max_new) {
+  if (tokens < 0 || Hq < 0 || max_new < 0) return fail(GEMM_ERR_INVALID_ARG, "negative size");
+  if (tokens > 0 && (c->seqs < 1 || max_new < 1))
+    return fail(GEMM_ERR_INVALID_ARG, "%d tokens of %d sequences, at most %d each", tokens, c->seqs, max_new);
+  if (start == nullptr && tokens > 0 && tokens != c->seqs)
+    return fail(GEMM_ERR_INVALID_ARG, "without start there is one token a sequence: %d tokens, %d sequences", tokens,
+                c->seqs);
+  if (!aligned4(start)) return fail(GEMM_ERR_MISALIGNED, "start is not aligned to 4 bytes");
+  return GEMM_OK;
+}
+
+// Rows of `heads` heads, `ld` elements apart.
+bool kv_ld_bad(long long ld, int heads, int dim) { return ld < (long long)heads * dim; }
+
+int kv_append(const gemm_kv_cache* cache, int tokens, int Hq, const void* Q, long long ldq, const void* K,
+              long long ldk, const void* V, long long ldv, void* Qout, long long ldqo, const float* cosine,
+              const float* sine, int positions, int rotated, int interleaved, const int* base, const int* start,
+              int max_new, cudaStream_t stream) {
+  t_msg[0] = '\0';
+  t_last_path = GEMM_PATH_AUTO;
+  t_last_k_split = 1;
+  KvAppendArgs a;
+  int rc = kv_cache(cache, tokens > 0, &a.c);
+  if (rc != GEMM_OK) return rc;
+  if ((rc = kv_sizes(cache, tokens, Hq, start, max_new)) != GEMM_OK) return rc;
+  const int D = a.c.D;
+  if (rotated < 0 || rotated > D || rotated % 2 != 0)
+    return fail(GEMM_ERR_INVALID_ARG, "rotated (%d) must be even, 0 to dim (%d)", rotated, D);
+  if (positions < 0) return fail(GEMM_ERR_INVALID_ARG, "negative size");
+  if ((long long)Hq + 2ll * a.c.H > 65535)
+    return fail(GEMM_ERR_UNSUPPORTED, "%d query and %d key heads: Hq + 2*heads exceeds 65535", Hq, a.c.H);
+  if (kv_ld_bad(ldk, a.c.H, D) || kv_ld_bad(ldv, a.c.H, D) ||
+      (Hq > 0 && (kv_ld_bad(ldq, Hq, D) || kv_ld_bad(ldqo, Hq, D))))
+    return fail(GEMM_ERR_INVALID_ARG, "leading dimension too small (ldq=%lld ldk=%lld ldv=%lld ldqo=%lld)", ldq, ldk,
+                ldv, ldqo);
+  if (tokens == 0) return GEMM_OK;
+  if (K == nullptr || V == nullptr || base == nullptr || (Hq > 0 && (Q == nullptr || Qout == nullptr)))
+    return fail(GEMM_ERR_INVALID_ARG, "Q, K, V, Qout or base is NULL");
+  if (rotated > 0 && (cosine == nullptr || sine == nullptr))
+    return fail(GEMM_ERR_INVALID_ARG, "cos or sin is NULL");
+  if (!aligned2(Q) || !aligned2(K) || !aligned2(V) || !aligned2(Qout) || !aligned4(cosine) || !aligned4(sine) ||
+      !aligned4(base))
+    return fail(GEMM_ERR_MISALIGNED, "a pointer is not aligned to its element size");
+  DeviceInfo* dev = nullptr;
+  if ((rc = device_info(&dev)) != GEMM_OK) return rc;
+  a.tokens = tokens;
+  a.Hq = Hq;
+  a.Q = Q; a.K = K; a.V = V; a.Qo = Qout;
+  a.ldq = ldq; a.ldk = ldk; a.ldv = ldv; a.ldqo = ldqo;
+  a.cos = cosine; a.sin = sine;
+  a.positions = positions; a.rot = rotated; a.interleaved = interleaved ? 1 : 0;
+  a.base = base; a.start = start;
+  a.max_new = max_new;
+  a.status = dev->status;
+  const bool fast = false;
+  const int err = launch_kv_append(a, fast, dev->num_sms, stream);
+  if (err != cudaSuccess)
+    return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
+  t_last_path = fast ? GEMM_PATH_KV : GEMM_PATH_GENERIC;
+  return GEMM_OK;
+}
+
+size_t kv_attention_workspace(int seqs, int heads, int Hq, int dim, int max_new) {
+  if (seqs < 0 || heads < 1 || Hq < 0 || dim < 1 || max_new < 0 || Hq % heads != 0) return 0;
+  return 16;
+}
+
+int kv_attention(const gemm_kv_cache* cache, int tokens, int Hq, const void* Q, long long ldq, void* O, long long ldo,
+                 const int* lengths, const int* start, int max_new, float scale, void* workspace,
+                 size_t workspace_bytes, cudaStream_t stream) {
+  trim_maps();
+  t_msg[0] = '\0';
+  t_last_path = GEMM_PATH_AUTO;
+  t_last_k_split = 1;
+  KvAttnArgs a;
+  int rc = kv_cache(cache, tokens > 0 && Hq > 0, &a.c);
+  if (rc != GEMM_OK) return rc;
+  if ((rc = kv_sizes(cache, tokens, Hq, start, max_new)) != GEMM_OK) return rc;
+  const int D = a.c.D;
+  if (Hq % a.c.H != 0)
+    return fail(GEMM_ERR_INVALID_ARG, "Hq (%d) must be a multiple of the cache's heads (%d)", Hq, a.c.H);
+  if (Hq > 65535) return fail(GEMM_ERR_UNSUPPORTED, "Hq %d exceeds 65535", Hq);
+  if (!(scale >= 0.f) || !std::isfinite(scale)) return fail(GEMM_ERR_INVALID_ARG, "bad scale");
+  if (Hq > 0 && (kv_ld_bad(ldq, Hq, D) || kv_ld_bad(ldo, Hq, D)))
+    return fail(GEMM_ERR_INVALID_ARG, "leading dimension too small (ldq=%lld ldo=%lld)", ldq, ldo);
+  if (tokens == 0 || Hq == 0) return GEMM_OK;
+  if (Q == nullptr || O == nullptr || lengths == nullptr)
+    return fail(GEMM_ERR_INVALID_ARG, "Q, O or lengths is NULL");
+  if (!aligned2(Q) || !aligned2(O) || !aligned4(lengths))
+    return fail(GEMM_ERR_MISALIGNED, "a pointer is not aligned to its element size");
+  if (workspace == nullptr || workspace_bytes < kv_attention_workspace(cache->seqs, a.c.H, Hq, D, max_new))
+    return fail(GEMM_ERR_INVALID_ARG, "workspace of %zu bytes: %zu are needed", workspace ? workspace_bytes : 0,
+                kv_attention_workspace(cache->seqs, a.c.H, Hq, D, max_new));
+  if (!aligned16(workspace)) return fail(GEMM_ERR_MISALIGNED, "workspace is not aligned to 16 bytes");
+  DeviceInfo* dev = nullptr;
+  if ((rc = device_info(&dev)) != GEMM_OK) return rc;
+  a.tokens = tokens;
+  a.Hq = Hq;
+  a.Q = Q; a.ldq = ldq; a.O = O; a.ldo = ldo;
+  a.lengths = lengths; a.start = start;
+  a.max_new = max_new;
+  a.scale = scale == 0.f ? 1.f / std::sqrt((float)D) : scale;
+  a.ws = workspace;
+  a.status = dev->status;
+  a.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
+  const int err = launch_kv_attention_generic(a, stream);
+  if (err != cudaSuccess)
+    return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
+  t_last_path = GEMM_PATH_GENERIC;
+  return GEMM_OK;
+}
+
+int sample(int rows, int vocab, const void* logits, bool bf16, long long ld, const float* temperature,
+           const int* top_k, const float* top_p, const float* min_p, const float* u, int* token, float* logprob,
+           cudaStream_t stream) {
+  t_msg[0] = '\0';
+  t_last_path = GEMM_PATH_AUTO;
+  t_last_k_split = 1;
+  if (rows < 0 || vocab < 0) return fail(GEMM_ERR_INVALID_ARG, "negative size rows=%d vocab=%d", rows, vocab);
+  if (rows == 0) return GEMM_OK;
+  if (vocab == 0) return fail(GEMM_ERR_INVALID_ARG, "an empty vocabulary has no token to take");
+  if (vocab > kSampleMaxVocab) return fail(GEMM_ERR_UNSUPPORTED, "vocab %d above %d", vocab, kSampleMaxVocab);
+  if (ld < vocab) return fail(GEMM_ERR_INVALID_ARG, "leading dimension too small (ld=%lld, vocab=%d)", ld, vocab);
+  if (logits == nullptr || u == nullptr || token == nullptr)
+    return fail(GEMM_ERR_INVALID_ARG, "logits, u or token is NULL");
+  if (!(bf16 ? aligned2(logits) : aligned4(logits)) || !aligned4(temperature) || !aligned4(top_k) ||
+      !aligned4(top_p) || !aligned4(min_p) || !aligned4(u) || !aligned4(token) || !aligned4(logprob))
+    return fail(GEMM_ERR_MISALIGNED, "a pointer is not aligned to its element size");
+  DeviceInfo* dev = nullptr;
+  int rc = device_info(&dev);
+  if (rc != GEMM_OK) return rc;
+  SampleArgs a;
+  a.rows = rows; a.vocab = vocab; a.logits = logits; a.ld = ld; a.bf16 = bf16;
+  a.temperature = temperature; a.top_k = top_k; a.top_p = top_p; a.min_p = min_p; a.u = u;
+  a.token = token; a.logprob = logprob;
+  const int err = launch_sample(a, dev->num_sms, stream);
+  if (err != cudaSuccess)
+    return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
+  t_last_path = GEMM_PATH_SAMPLE;
+  return GEMM_OK;
+}
+
 __global__ void selftest_wait_kernel(int* status, uint64_t timeout_ns) {
   __shared__ uint64_t bar;
   if (threadIdx.x == 0) {
@@ -709,6 +897,37 @@ int gemm_int4_dequant_f32(const uint8_t* q, int K, int N, int ldq, const gemm_bf
 int gemm_attention(int B, int Hq, int Hkv, int Sq, int Sk, int D, const gemm_bf16_t* Q, const gemm_bf16_t* K,
                    const gemm_bf16_t* V, gemm_bf16_t* O, float scale, int causal, cudaStream_t stream) {
   return g3::attention(B, Hq, Hkv, Sq, Sk, D, Q, K, V, O, scale, causal, stream);
+}
+
+int gemm_kv_append(const gemm_kv_cache* cache, int tokens, int Hq, const gemm_bf16_t* Q, long long ldq,
+                   const gemm_bf16_t* K, long long ldk, const gemm_bf16_t* V, long long ldv, gemm_bf16_t* Qout,
+                   long long ldqo, const float* cos, const float* sin, int positions, int rotated,
+                   int interleaved, const int* base, const int* start, int max_new, cudaStream_t stream) {
+  return g3::kv_append(cache, tokens, Hq, Q, ldq, K, ldk, V, ldv, Qout, ldqo, cos, sin, positions, rotated,
+                       interleaved, base, start, max_new, stream);
+}
+
+size_t gemm_kv_attention_workspace(int seqs, int heads, int Hq, int dim, int max_new) {
+  return g3::kv_attention_workspace(seqs, heads, Hq, dim, max_new);
+}
+
+int gemm_kv_attention(const gemm_kv_cache* cache, int tokens, int Hq, const gemm_bf16_t* Q, long long ldq,
+                      gemm_bf16_t* O, long long ldo, const int* lengths, const int* start, int max_new,
+                      float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return g3::kv_attention(cache, tokens, Hq, Q, ldq, O, ldo, lengths, start, max_new, scale, workspace,
+                          workspace_bytes, stream);
+}
+
+int gemm_sample_bf16(int rows, int vocab, const gemm_bf16_t* logits, long long ld, const float* temperature,
+                     const int* top_k, const float* top_p, const float* min_p, const float* u, int* token,
+                     float* logprob, cudaStream_t stream) {
+  return g3::sample(rows, vocab, logits, true, ld, temperature, top_k, top_p, min_p, u, token, logprob, stream);
+}
+
+int gemm_sample_f32(int rows, int vocab, const float* logits, long long ld, const float* temperature,
+                    const int* top_k, const float* top_p, const float* min_p, const float* u, int* token,
+                    float* logprob, cudaStream_t stream) {
+  return g3::sample(rows, vocab, logits, false, ld, temperature, top_k, top_p, min_p, u, token, logprob, stream);
 }
 
 size_t gemm_w4_packed_bytes(int K, int N) { return g3::w4_packed_bytes(K, N); }

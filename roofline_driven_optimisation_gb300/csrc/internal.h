@@ -82,6 +82,9 @@ enum WaitSite : int {
   kSiteAttnMma = 51,
   kSiteAttnSoftmax = 52,
   kSiteAttnDrain = 53,
+  kSiteKvAppend = 60,      // a row range, position or page number that does not fit the call
+  kSiteKvAttn = 61,        // the same, in attention over the paged cache
+  kSiteKvAttnLoad = 62,    // a wait for a tile of the paged cache
 };
 
 // Each launcher returns a cudaError_t (as int) from the launch.
@@ -198,6 +201,63 @@ int launch_attention(int B, int Hq, int Hkv, int Sq, int Sk, int D, const void* 
                      const void* V, void* O, float scale, int causal, const CUtensorMap* mQ,
                      const CUtensorMap* mK, const CUtensorMap* mV, bool fast, int* status,
                      uint64_t timeout_ns, cudaStream_t s);
+
+// A paged 8-bit key/value cache (gemm_kv_cache) after validation.
+struct KvCache {
+  uint8_t *k, *v;
+  float *ks, *vs;                 // pages x H
+  const int* table;
+  long long ps, hs, ts, tstride;  // page, head and token strides in bytes; table row stride
+  int fmt, pages, P, H, D, seqs, cols;
+};
+
+// Appending rotated keys and values (gemm_kv_append).
+struct KvAppendArgs {
+  KvCache c;
+  int tokens, Hq;
+  const void *Q, *K, *V;          // bf16 rows, heads side by side
+  long long ldq, ldk, ldv, ldqo;  // elements between rows
+  void* Qo;
+  const float *cos, *sin;         // positions x rot/2
+  int positions, rot, interleaved;
+  const int *base, *start;
+  int max_new;
+  int* status;
+};
+// fast: D 64 or 128, P a power of two 16..128, rot == D, 16-byte-aligned rows.
+int launch_kv_append(const KvAppendArgs& a, bool fast, int num_sms, cudaStream_t s);
+
+// Attention over the paged cache (gemm_kv_attention).
+struct KvAttnArgs {
+  KvCache c;
+  int tokens, Hq;
+  const void* Q;
+  long long ldq;
+  void* O;
+  long long ldo;
+  const int *lengths, *start;
+  int max_new;
+  float scale;
+  void* ws;
+  int* status;
+  uint64_t timeout_ns;
+};
+int launch_kv_attention_generic(const KvAttnArgs& a, cudaStream_t s);
+
+// Sampling (gemm_sample_*).
+struct SampleArgs {
+  int rows, vocab;
+  const void* logits;
+  long long ld;
+  bool bf16;
+  const float* temperature;
+  const int* top_k;
+  const float *top_p, *min_p, *u;
+  int* token;
+  float* logprob;
+};
+constexpr int kSampleMaxVocab = 1 << 20;
+int launch_sample(const SampleArgs& a, int num_sms, cudaStream_t s);
 
 int launch_selftest_wait(int* status, uint64_t timeout_ns, cudaStream_t s);
 
