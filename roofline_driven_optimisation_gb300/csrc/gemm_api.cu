@@ -216,6 +216,35 @@ int make_map_3d(const void* ptr, uint64_t cols, uint64_t rows, uint64_t depth, u
   return GEMM_OK;
 }
 
+// A paged cache's codes as a 4-D tensor of bytes (dim, page row, head, page) with
+// boxes of dim x rows codes of one page and head.
+int make_map_kv(const void* ptr, const KvCache& c, uint32_t rows, const CUtensorMap** out) {
+  // pages and heads are bounded by 2^31, so they pack into one field of the key
+  MapKey key{reinterpret_cast<uintptr_t>(ptr), ((uint64_t)c.pages << 32) | (uint32_t)c.H, (uint64_t)c.P,
+             (uint64_t)c.ts, (uint32_t)c.D, rows, 4u, 4u, (uint64_t)c.hs, (uint64_t)c.ps};
+  auto it = t_maps.find(key);
+  if (it != t_maps.end()) {
+    *out = &it->second;
+    return GEMM_OK;
+  }
+  EncodeFn fn = encode_fn();
+  if (!fn) return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  CUtensorMap map;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.P, (cuuint64_t)c.H, (cuuint64_t)c.pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)c.ts, (cuuint64_t)c.hs, (cuuint64_t)c.ps};
+  const cuuint32_t box[4] = {(cuuint32_t)c.D, rows, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled (paged cache) failed (%d)", (int)r);
+  auto ins = t_maps.emplace(key, map);
+  *out = &ins.first->second;
+  return GEMM_OK;
+}
+
 // ---------------------------------------------------------------- dispatch
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -661,8 +690,9 @@ int kv_cache(const gemm_kv_cache* c, bool used, KvCache* out) {
   out->ks = c->k_scale;
   out->vs = c->v_scale;
   out->table = c->table;
-  out->ps = c->page_stride;
-  out->hs = c->head_stride;
+  // a stride that nothing steps over may hold anything: D stands in for it
+  out->ps = c->pages > 1 ? c->page_stride : c->dim;
+  out->hs = c->heads > 1 ? c->head_stride : c->dim;
   out->ts = c->token_stride;
   out->tstride = c->table_stride;
   out->fmt = c->format;
@@ -740,7 +770,7 @@ int kv_append(const gemm_kv_cache* cache, int tokens, int Hq, const void* Q, lon
 
 size_t kv_attention_workspace(int seqs, int heads, int Hq, int dim, int max_new) {
   if (seqs < 0 || heads < 1 || Hq < 0 || dim < 1 || max_new < 0 || Hq % heads != 0) return 0;
-  return 16;
+  return kv_attention_ws_bytes(seqs, heads, Hq / heads, max_new);
 }
 
 int kv_attention(const gemm_kv_cache* cache, int tokens, int Hq, const void* Q, long long ldq, void* O, long long ldo,
@@ -781,10 +811,25 @@ int kv_attention(const gemm_kv_cache* cache, int tokens, int Hq, const void* Q, 
   a.ws = workspace;
   a.status = dev->status;
   a.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
-  const int err = launch_kv_attention_generic(a, stream);
+  // the tensor map's rules: 16-byte-aligned base and strides; a page is a whole
+  // number of boxes of at most 32 rows
+  const KvCache& c = a.c;
+  const bool fast = (D == 64 || D == 128) && (c.P == 16 || c.P == 32 || c.P == 64 || c.P == 128) && aligned16(c.k) &&
+                    aligned16(c.v) && (c.ps | c.hs | c.ts) % 16 == 0 && c.ps > 0 && c.hs > 0 && c.ps < (1ll << 40) && c.hs < (1ll << 40) &&
+                    c.ts < (1ll << 40) && c.seqs <= kKvMaxSeqs && c.pages > 0 && t_forced_path != GEMM_PATH_GENERIC;
+  int err;
+  if (fast) {
+    const CUtensorMap *mK = nullptr, *mV = nullptr;
+    const uint32_t rows = c.P < kKvSlab ? (uint32_t)c.P : (uint32_t)kKvSlab;
+    if ((rc = make_map_kv(c.k, c, rows, &mK)) != GEMM_OK) return rc;
+    if ((rc = make_map_kv(c.v, c, rows, &mV)) != GEMM_OK) return rc;
+    err = launch_kv_attention(a, mK, mV, dev->num_sms, stream);
+  } else {
+    err = launch_kv_attention_generic(a, stream);
+  }
   if (err != cudaSuccess)
     return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
-  t_last_path = GEMM_PATH_GENERIC;
+  t_last_path = fast ? GEMM_PATH_KV : GEMM_PATH_GENERIC;
   return GEMM_OK;
 }
 

@@ -243,6 +243,13 @@ struct KvAttnArgs {
   uint64_t timeout_ns;
 };
 int launch_kv_attention_generic(const KvAttnArgs& a, cudaStream_t s);
+// D 64 or 128, P 16, 32, 64 or 128, 16-byte-aligned codes and strides, at most
+// kKvMaxSeqs sequences.  mK, mV: 4-D maps (dim, page row, head, page) with boxes of
+// D x min(P, 32) codes, swizzle of D bytes.
+int launch_kv_attention(const KvAttnArgs& a, const CUtensorMap* mK, const CUtensorMap* mV, int num_sms,
+                        cudaStream_t s);
+constexpr int kKvMaxSeqs = 16384, kKvSlab = 32;
+size_t kv_attention_ws_bytes(int seqs, int heads, int group, int max_new);
 
 // Sampling (gemm_sample_*).
 struct SampleArgs {

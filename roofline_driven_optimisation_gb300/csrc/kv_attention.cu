@@ -1,8 +1,32 @@
 // Attention of a sequence's newest tokens over its paged 8-bit cache
 // (gemm_kv_attention; the header states the mathematics).
+//
+// A decode step reads every code of the cache once and does 2 * group * n FLOPs with
+// each, so for the usual groups it is bound by HBM.  The fast kernel is built to
+// keep enough bytes in flight and to do little else:
+//   * the unit of work is a slab, 32 keys of one sequence, head and row tile.  All
+//     slabs of the call form one line (sequence, head, row tile, keys); every warp of
+//     a persistent grid takes an equal, contiguous piece of it, so ragged batches
+//     and a single long sequence fill the GPU alike;
+//   * a warp is its own producer and consumer: one lane streams the slab's K and V
+//     by TMA (4-D map over the page pool) through the warp's ring of stages, so warps
+//     never wait for one another;
+//   * S^T = K Q^T and O^T = V^T P^T run on mma.m16n8k16 (fp16 in, fp32 out) with keys
+//     and values as the 16-row operand and 8 query rows as the columns: 8-bit codes
+//     are exact in fp16, and a decode step's 1 to 8 rows fill the tile.  The operand
+//     orders are chosen so that ldmatrix on bytes feeds both products (an inner
+//     dimension may be summed in any order, if both operands agree);
+//   * a page's scale of K multiplies its scores, that of V its probabilities;
+//   * a slab line's piece ends inside an item at most twice a warp; such partial
+//     results (running maximum, sum, unnormalised O) meet in shared memory, and what
+//     crosses blocks meets in the workspace, where the last block to arrive adds the
+//     parts in block order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+
+#include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv_cache.cuh"
@@ -117,6 +141,796 @@ __global__ void __launch_bounds__(GT) kv_attention_generic_kernel(const KvAttnAr
   }
 }
 
+
+// ------------------------------------------------------------------ fast
+using u64 = unsigned long long;
+constexpr int NW = 8;                    // warps of a block, one block an SM
+constexpr int SLAB = kKvSlab;
+constexpr int MAX_CTAS = 160;            // blocks that the workspace has room for
+constexpr int MAX_ROWS = 32;             // rows of a tile, at most
+constexpr int RING = 3 * 2 * SLAB * 128; // bytes of a warp's ring
+constexpr int PV_EXP = 14;               // P times the page's scale is below 2^PV_EXP in fp16
+constexpr int MIN_EXP = -112;
+
+template <int D>
+struct Cfg {
+  static constexpr int TILE = SLAB * D;              // bytes of a slab's keys
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int STAGES = RING / STAGE;        // 3 (D 128) or 6
+};
+
+// A partial result: O [rows][D], then m [rows], l [rows].  In the workspace: two of
+// every block (its first and last item may go on in other blocks), one of every
+// warp (its first item's, while its ring is in use), then a counter for each item.
+// The parts' places are of fixed size, so that no call's parts reach another's
+// counters.
+constexpr int PART_FLOATS = MAX_ROWS * 128 + 2 * MAX_ROWS;
+static_assert(PART_FLOATS * 4 <= RING, "a partial result fits in a drained ring");
+constexpr size_t PARTS = (size_t)MAX_CTAS * (2 + NW);
+
+struct StageMeta {
+  float ks[2], vs[2];   // scales of the slab's one or two pages
+  int ok[2];            // whether the page could be placed
+  int pad[2];
+};
+
+struct Slot {           // a warp's partial result
+  u64 unit;             // first unit of its item (~0: none)
+  float* part;          // in shared memory or in the workspace
+  int b, idx;           // sequence; head * tiles + tile
+};
+
+struct Open {           // an item that more than one warp worked on
+  u64 unit;
+  int e0, e1;           // its parts: slots e0 .. e1 (warp * 2 + slot)
+  int S, rows, h, t, first, n;
+  int count;            // index of its counter
+  bool whole;           // no other block has a part of it
+};
+
+struct Shared {
+  StageMeta meta[NW][6];
+  u64 full[NW][6];
+  Slot slot[NW * 2];
+  Open open[NW + 1];
+  int opens;
+  u64 scan[NW];
+  int last[NW + 1];     // this block finishes the item
+  int abort;
+};
+
+// Units of sequence b: heads * tiles * slabs
+struct Seq {
+  int len, first, n, S, tiles;
+};
+
+struct Plan {
+  const KvAttnArgs* a;
+  int group, rt;        // query heads of a head; rows of a tile
+  __device__ __forceinline__ Seq seq(int b) const {
+    Seq q;
+    q.len = kv_length(*a, b);
+    kv_rows(a->start, b, a->tokens, a->max_new, a->status, kSiteKvAttn, q.first, q.n);
+    q.S = max(1, (q.len + SLAB - 1) / SLAB);
+    q.tiles = (q.n * group + rt - 1) / rt;
+    return q;
+  }
+  __device__ __forceinline__ u64 units(const Seq& q) const { return (u64)a->c.H * q.tiles * q.S; }
+  // keys that the last row of tile t sees
+  __device__ __forceinline__ int visible(const Seq& q, int t) const {
+    const int i = (min(q.n * group, (t + 1) * rt) - 1) / group;
+    return q.len - q.n + i + 1;
+  }
+};
+
+// A place on the line of slabs
+struct Walk {
+  int b, idx, s;        // sequence, head * tiles + tile, slab
+  int h, t;
+  Seq q;
+  __device__ __forceinline__ void split() {
+    h = idx / q.tiles;
+    t = idx - h * q.tiles;
+  }
+  __device__ __forceinline__ void next(const Plan& p) {
+    if (++s < q.S) return;
+    s = 0;
+    if (++idx < p.a->c.H * q.tiles) {
+      split();
+      return;
+    }
+    idx = 0;
+    do {
+      if (++b >= p.a->c.seqs) return;
+      q = p.seq(b);
+    } while (q.tiles == 0);
+    split();
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }   // -126 <= e <= 127
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Four codes of a register as fp16 pairs.  INT8: the byte plus 128 under the high
+// byte of fp16's 1024 is 1024 + 128 + code; subtracting 1152 is exact.
+__device__ __forceinline__ uint32_t sub_1152(uint32_t x) {
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// (bytes 0,1), (bytes 2,3)
+template <int FMT>
+__device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == kKvE4M3) {
+    lo = e4m3x2_to_f16x2(x & 0xffffu);
+    hi = e4m3x2_to_f16x2(x >> 16);
+  } else {
+    x ^= 0x80808080u;
+    lo = sub_1152(__byte_perm(x, 0x64646464u, 0x4140));
+    hi = sub_1152(__byte_perm(x, 0x64646464u, 0x4342));
+  }
+}
+// (bytes 0,2), (bytes 1,3)
+template <int FMT>
+__device__ __forceinline__ void widen_pairs(uint32_t x, uint32_t& even, uint32_t& odd) {
+  if constexpr (FMT == kKvE4M3) {
+    widen<FMT>(__byte_perm(x, 0u, 0x3120), even, odd);
+  } else {
+    x ^= 0x80808080u;
+    even = sub_1152(__byte_perm(x, 0x64646464u, 0x4240));
+    odd = sub_1152(__byte_perm(x, 0x64646464u, 0x4341));
+  }
+}
+
+// fp16 pair mask of keys k0, k0 + 1 below lim
+__device__ __forceinline__ uint32_t key_mask(int k0, int lim) {
+  return (k0 < lim ? 0xffffu : 0u) | (k0 + 1 < lim ? 0xffff0000u : 0u);
+}
+
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(NW * 32, 1)
+    kv_attention_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                        const __grid_constant__ KvAttnArgs a, const int group, const int max_tiles,
+                        const int vec) {
+  using C = Cfg<D>;
+  constexpr int ST = C::STAGES, CH = D / 16, RT = NT * 8;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* base_ptr = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t4 = lane % 4;
+  uint8_t* ring_ptr = base_ptr + warp * RING;
+  const uint32_t ring = smem_u32(ring_ptr);
+  const Plan plan{&a, group, RT};
+  const int npg = a.c.P < SLAB ? 2 : 1;           // pages of a slab
+
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&mapK);
+    tma_prefetch_desc(&mapV);
+    for (int w = 0; w < NW; ++w)
+      for (int s = 0; s < ST; ++s) mbar_init(smem_u32(&sh.full[w][s]), 2 * npg);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+
+  // ---- the line of slabs: units before each sequence, in the ring's memory
+  u64* pref = reinterpret_cast<u64*>(base_ptr);
+  const int per = (a.c.seqs + NW * 32 - 1) / (NW * 32);
+  const int b_lo = min(a.c.seqs, (int)threadIdx.x * per), b_hi = min(a.c.seqs, b_lo + per);
+  u64 mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const u64 n = plan.units(plan.seq(b));
+    pref[b] = n;
+    mine += n;
+  }
+  u64 incl = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sh.scan[warp] = incl;
+  __syncthreads();
+  u64 at = incl - mine, T = 0;
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) at += sh.scan[w];
+    T += sh.scan[w];
+  }
+  for (int b = b_lo; b < b_hi; ++b) {
+    const u64 n = pref[b];
+    pref[b] = at;
+    at += n;
+  }
+  __syncthreads();
+  const u64 G = T < gridDim.x ? T : gridDim.x;   // every block up to G has a unit
+  const u64 cta = blockIdx.x;
+  if (cta >= G) return;
+  const u64 W = G * NW, me = cta * NW + warp;
+  const u64 u0 = me * T / W, u1 = (me + 1) * T / W;
+  const u64 A = cta * T / G, B = (cta + 1) * T / G;
+  Walk cw;
+  if (u0 < u1) {
+    int lo = 0, hi = a.c.seqs;                    // the last b with pref[b] <= u0 that has units
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (pref[mid] <= u0) lo = mid;
+      else hi = mid;
+    }
+    cw.b = lo;
+    cw.q = plan.seq(lo);
+    const u64 rel = u0 - pref[lo];
+    cw.idx = (int)(rel / cw.q.S);
+    cw.s = (int)(rel - (u64)cw.idx * cw.q.S);
+    cw.split();
+  }
+  __syncthreads();                                // pref's memory becomes the rings
+  fence_proxy_async_smem();
+
+  // ---- producer side
+  const int total = (int)(u1 - u0);
+  // page of the slab's part that this lane fetches, -1 if it has none to fetch
+  auto page_of = [&](const Walk& w) -> int {
+    if (lane >= npg) return -1;
+    const int key = w.s * SLAB + lane * 16;
+    if (key >= plan.visible(w.q, w.t)) return -1;
+    const int p = a.c.table[(long long)w.b * a.c.tstride + key / a.c.P];
+    if (p < 0 || p >= a.c.pages) {
+      report_status(a.status, 1, kSiteKvAttn);
+      return -1;
+    }
+    return p;
+  };
+  auto issue = [&](int st, const Walk& w, int p) {
+    if (lane < npg) {
+      const uint32_t bar = smem_u32(&sh.full[warp][st]);
+      StageMeta& m = sh.meta[warp][st];
+      m.ok[lane] = p >= 0;
+      if (p >= 0) {
+        const int key = w.s * SLAB + lane * 16, rows = SLAB / npg;
+        const uint32_t dst = ring + st * C::STAGE + lane * 16 * D;
+        mbar_arrive_expect_tx(bar, 2 * rows * D);
+        tma_load_4d(dst, &mapK, bar, 0, key % a.c.P, w.h, p);
+        tma_load_4d(dst + C::TILE, &mapV, bar, 0, key % a.c.P, w.h, p);
+        cp_async_4(smem_u32(&m.ks[lane]), a.c.ks + (long long)p * a.c.H + w.h);
+        cp_async_4(smem_u32(&m.vs[lane]), a.c.vs + (long long)p * a.c.H + w.h);
+      } else {
+        m.ks[lane] = m.vs[lane] = 0.f;
+        mbar_arrive(bar);
+      }
+      cp_async_arrive(bar);
+    }
+  };
+
+  if (lane < 2) sh.slot[warp * 2 + lane].unit = ~0ull;
+  if (total > 0) {
+    Walk pw = cw;                                 // next slab to fetch
+    int issued = 0, pg;
+    {
+      Walk ws[ST];
+      int ps[ST];
+#pragma unroll
+      for (int i = 0; i < ST; ++i) {
+        ws[i] = pw;
+        ps[i] = i < total ? page_of(pw) : -1;
+        if (i < total) pw.next(plan);
+      }
+#pragma unroll
+      for (int i = 0; i < ST; ++i)
+        if (i < total) issue(i, ws[i], ps[i]);
+      issued = min(ST, total);
+      pg = issued < total ? page_of(pw) : -1;
+    }
+
+    // ---- consumer state of one item
+    uint32_t qf[NT][CH][2];
+    float acc[NT][CH][4];
+    float m[NT][2], l[NT][2], rs[NT][2];
+    int lim[NT][2];                               // keys that this lane's columns see
+    int ev = MIN_EXP;                             // V's pages so far have scales below 2^ev
+    int lim_min = 0, lim_max = 0;
+    bool head = false;                            // the item began before this warp's piece
+
+    int st = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int j = 0; j < total; ++j) {
+      const Seq& q = cw.q;
+      if (j == 0 || cw.s == 0) {
+        // ---- a new item: its query rows, scaled to fp16 by a power of two a row
+        head = cw.s != 0;
+        const int rows = min(RT, q.n * group - cw.t * RT);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = nt * 8 + g, rr = cw.t * RT + r;
+          float x[CH][4];
+          float mx = 0.f;
+          const bool have = r < rows;
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.Q) +
+                                     (have ? (long long)(q.first + rr / group) * a.ldq +
+                                                 (long long)(cw.h * group + rr % group) * D : 0);
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            uint2 v = make_uint2(0u, 0u);
+            if (have) {
+              if (vec) {
+                v = *reinterpret_cast<const uint2*>(src + c * 16 + t4 * 4);
+              } else {
+                const uint16_t* e = reinterpret_cast<const uint16_t*>(src + c * 16 + t4 * 4);
+                v = make_uint2(e[0] | ((uint32_t)e[1] << 16), e[2] | ((uint32_t)e[3] << 16));
+              }
+            }
+            x[c][0] = __uint_as_float(v.x << 16);
+            x[c][1] = __uint_as_float(v.x & 0xffff0000u);
+            x[c][2] = __uint_as_float(v.y << 16);
+            x[c][3] = __uint_as_float(v.y & 0xffff0000u);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fabsf(x[c][k]));
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          // the largest magnitude of the row lands in [2^14, 2^15)
+          const int e = max(-112, (int)(__float_as_uint(mx) >> 23) - 127);
+          const float f = pow2i(14 - e);
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            qf[nt][c][0] = pack_f16(x[c][0] * f, x[c][1] * f);
+            qf[nt][c][1] = pack_f16(x[c][2] * f, x[c][3] * f);
+          }
+          const float back = a.scale * 1.4426950408889634f * pow2i(e - 14);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            rs[nt][k] = __shfl_sync(0xffffffffu, back, (2 * t4 + k) * 4);
+            const int col = cw.t * RT + nt * 8 + 2 * t4 + k;
+            lim[nt][k] = q.len - q.n + min(col / group, q.n - 1) + 1;
+            m[nt][k] = -INFINITY;
+            l[nt][k] = 0.f;
+          }
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[nt][c][k] = 0.f;
+        }
+        ev = MIN_EXP;
+        lim_min = q.len - q.n + cw.t * RT / group + 1;
+        lim_max = plan.visible(q, cw.t);
+      }
+
+      // ---- the slab
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.full[warp][st]), phase, a.timeout_ns, &sh.abort));
+      if (!ok) break;
+      const int k0 = cw.s * SLAB;
+      const StageMeta& meta = sh.meta[warp][st];
+      const int ok0 = meta.ok[0], ok1 = npg == 2 ? meta.ok[1] : ok0;
+      if (k0 < lim_max && (ok0 | ok1)) {
+        const uint32_t kt = ring + st * C::STAGE, vt = kt + C::TILE;
+        float ks[2], vs[2];
+        ks[0] = meta.ks[0];
+        vs[0] = meta.vs[0];
+        ks[1] = npg == 2 ? meta.ks[1] : ks[0];
+        vs[1] = npg == 2 ? meta.vs[1] : vs[0];
+        // every key of the slab is there for every row
+        const bool whole = k0 + SLAB <= lim_min && (ok0 & ok1);
+
+        // S^T = K Q^T.  ldmatrix gives lane (g, t4) bytes 4*t4 .. 4*t4+3 of row g of
+        // each 16-byte chunk: the first two are the operand's k = 2*t4, 2*t4+1, the
+        // others its k + 8; Q is held in the same order.
+        float sc[2][NT][4];
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc[sub][nt][k] = 0.f;
+          const int r = sub * 16 + (lane & 15);
+          const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+#pragma unroll
+          for (int c = 0; c < CH; c += 2) {
+            uint32_t x[4], a0, a1, a2, a3;
+            ldsm_x4(kt + r * D + (((c + (lane >> 4)) ^ sw) << 4), x);
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              widen<FMT>(x[2 * cc], a0, a2);
+              widen<FMT>(x[2 * cc + 1], a1, a3);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(sc[sub][nt], a0, a1, a2, a3, qf[nt][c + cc][0], qf[nt][c + cc][1]);
+            }
+          }
+        }
+
+        // V's scale enters through P; the accumulators' unit is 2^(ev - PV_EXP)
+        const int e_new = max(ev, (int)((__float_as_uint(fmaxf(fabsf(vs[0]), fabsf(vs[1]))) >> 23) & 255u) - 126);
+        const float grow = pow2i(max(ev - e_new, -126));
+        const bool grew = e_new > ev;
+        ev = e_new;
+        const float unit = pow2i(PV_EXP - ev);
+        const float cv[2] = {vs[0] * unit, vs[1] * unit};
+
+        uint32_t pf[2][NT][2];
+        float al[NT][2];
+        bool rescale = grew;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float x = sc[sub][nt][k] * (rs[nt][k & 1] * ks[sub]);
+              if (!whole) {
+                const int key = k0 + sub * 16 + g + (k >> 1) * 8;
+                if (key >= lim[nt][k & 1] || !(sub ? ok1 : ok0)) x = -INFINITY;
+              }
+              sc[sub][nt][k] = x;
+              mx[k & 1] = fmaxf(mx[k & 1], x);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float v = mx[k];
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            const float mn = fmaxf(m[nt][k], v), mu = mn == -INFINITY ? 0.f : mn;
+            al[nt][k] = ex2(m[nt][k] - mu);
+            rescale |= mn != m[nt][k];
+            m[nt][k] = mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                const float p = ex2(sc[sub][nt][hh * 2 + k] - mu);
+                sc[sub][nt][hh * 2 + k] = p;
+                sum += p;
+              }
+            l[nt][k] = l[nt][k] * al[nt][k] + sum;
+          }
+          // P^T as the second operand: transpose 8 x 8 blocks (keys x rows)
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+              pf[sub][nt][hh] =
+                  movm_t(pack_f16(sc[sub][nt][2 * hh] * cv[sub], sc[sub][nt][2 * hh + 1] * cv[sub]));
+        }
+        if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float f0 = al[nt][0] * grow, f1 = al[nt][1] * grow;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              acc[nt][c][0] *= f0;
+              acc[nt][c][1] *= f1;
+              acc[nt][c][2] *= f0;
+              acc[nt][c][3] *= f1;
+            }
+          }
+        }
+
+        // O^T += V^T P^T.  Transposed ldmatrix of byte pairs: lane (g, t4) has values
+        // 2g, 2g+1 of keys 2*t4, 2*t4+1; row g of the operand is value 2g, row g + 8
+        // value 2g + 1.
+        auto products = [&](int limit, int query) {
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub) {
+            const int kk = k0 + sub * 16 + 2 * t4;
+            const bool there = (sub ? ok1 : ok0) != 0;
+            const uint32_t mk0 = query < 0 ? ~0u : there ? key_mask(kk, limit) : 0u;
+            const uint32_t mk1 = query < 0 ? ~0u : there ? key_mask(kk + 8, limit) : 0u;
+            const int r = sub * 16 + (lane & 15);
+            const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+#pragma unroll
+            for (int c = 0; c < CH; c += 2) {
+              uint32_t x[4], a0, a1, a2, a3;
+              ldsm_x4_t(vt + r * D + (((c + (lane >> 4)) ^ sw) << 4), x);
+#pragma unroll
+              for (int cc = 0; cc < 2; ++cc) {
+                widen_pairs<FMT>(x[2 * cc], a0, a1);
+                widen_pairs<FMT>(x[2 * cc + 1], a2, a3);
+                if (query >= 0) {
+                  a0 &= mk0;
+                  a1 &= mk0;
+                  a2 &= mk1;
+                  a3 &= mk1;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  if (query < 0) {
+                    mma16816(acc[nt][c + cc], a0, a1, a2, a3, pf[sub][nt][0], pf[sub][nt][1]);
+                  } else {
+                    float y[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma16816(y, a0, a1, a2, a3, pf[sub][nt][0], pf[sub][nt][1]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[nt][c + cc][k] += lim[nt][k & 1] == limit ? y[k] : 0.f;
+                  }
+                }
+              }
+            }
+          }
+        };
+        if (whole) {
+          products(0, -1);
+        } else {
+          // a zero probability does not hide a NaN, so keys that a query does not see
+          // are cut out of V itself, and only that query's rows take the product
+          const int q_lo = cw.t * RT / group, q_hi = (min(q.n * group, (cw.t + 1) * RT) - 1) / group;
+          for (int i = q_lo; i <= q_hi; ++i) {
+            const int limit = q.len - q.n + i + 1;
+            if (limit > k0) products(limit, i);
+          }
+        }
+      }
+      // ---- the stage is free: fetch ahead
+      __syncwarp();
+      const Walk done = cw;
+      if (issued < total) {
+        issue(st, pw, pg);
+        if (++issued < total) {
+          pw.next(plan);
+          pg = page_of(pw);
+        }
+      }
+      if (++st == ST) {
+        st = 0;
+        phase ^= 1u;
+      }
+      // ---- the item ends here, or this warp's piece of it
+      const bool ends = done.s + 1 == done.q.S;
+      if (ends || j + 1 == total) {
+        const int rows = min(RT, done.q.n * group - done.t * RT);
+        const float unit = pow2i(max(ev - PV_EXP, -126));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float v = l[nt][k];
+            v += __shfl_xor_sync(0xffffffffu, v, 4);
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            v += __shfl_xor_sync(0xffffffffu, v, 16);
+            l[nt][k] = v;
+          }
+        if (ends && !head) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int r = nt * 8 + 2 * t4 + k, rr = done.t * RT + r;
+              if (r >= rows) continue;
+              const float inv = l[nt][k] == 0.f ? 0.f : unit / l[nt][k];
+              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.O) + (long long)(done.q.first + rr / group) * a.ldo +
+                                 (long long)(done.h * group + rr % group) * D + 2 * g;
+#pragma unroll
+              for (int c = 0; c < CH; ++c) {
+                const float lo = acc[nt][c][k] * inv, hi = acc[nt][c][2 + k] * inv;
+                if (vec) {
+                  *reinterpret_cast<__nv_bfloat162*>(o + c * 16) = __floats2bfloat162_rn(lo, hi);
+                } else {
+                  o[c * 16] = __float2bfloat16_rn(lo);
+                  o[c * 16 + 1] = __float2bfloat16_rn(hi);
+                }
+              }
+            }
+        } else {
+          // into the drained ring, or into the workspace while the ring is in use
+          float* part = j + 1 == total ? reinterpret_cast<float*>(ring_ptr)
+                                       : static_cast<float*>(a.ws) + (MAX_CTAS * 2 + me) * (size_t)PART_FLOATS;
+          if (lane == 0) {
+            Slot& s = sh.slot[warp * 2 + (head ? 0 : 1)];
+            s.unit = u0 + j - done.s;
+            s.part = part;
+            s.b = done.b;
+            s.idx = done.idx;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int r = nt * 8 + 2 * t4 + k;
+              if (r >= rows) continue;
+#pragma unroll
+              for (int c = 0; c < CH; ++c)
+                *reinterpret_cast<float2*>(part + r * D + c * 16 + 2 * g) =
+                    make_float2(acc[nt][c][k] * unit, acc[nt][c][2 + k] * unit);
+              if (g == 0) {
+                part[RT * D + r] = m[nt][k];
+                part[RT * D + RT + r] = l[nt][k];
+              }
+            }
+        }
+      }
+      if (j + 1 < total) cw.next(plan);
+    }
+    if (!ok) {
+      // a copy did not arrive: leave, but not before the copies in flight have landed
+      if (lane == 0) report_status(a.status, 5, kSiteKvAttnLoad);
+      sh.abort = 1;
+      for (int i = 0; i < ST; ++i)
+        if (lane == 0) mbar_wait(smem_u32(&sh.full[warp][i]), i < st ? phase ^ 1u : phase, kDrainWaitNs / 8, nullptr);
+    }
+  }
+
+  // ---- parts of items that more than one warp worked on
+  __syncthreads();
+  if (sh.abort) return;
+  if (threadIdx.x == 0) {
+    int n = 0;
+    for (int e = 0; e < NW * 2; ++e) {
+      const Slot& s = sh.slot[e];
+      if (s.unit == ~0ull) continue;
+      if (n > 0 && sh.open[n - 1].unit == s.unit) {
+        sh.open[n - 1].e1 = e;
+        continue;
+      }
+      Open& o = sh.open[n];
+      const Seq q = plan.seq(s.b);
+      o.unit = s.unit;
+      o.e0 = o.e1 = e;
+      o.S = q.S;
+      o.h = s.idx / q.tiles;
+      o.t = s.idx % q.tiles;
+      o.rows = min(RT, q.n * group - o.t * RT);
+      o.first = q.first;
+      o.n = q.n;
+      o.count = (s.b * a.c.H + o.h) * max_tiles + o.t;
+      o.whole = s.unit >= A && s.unit + q.S <= B;
+      ++n;
+    }
+    sh.opens = n;
+  }
+  __syncthreads();
+  float* parts = static_cast<float*>(a.ws);
+  int* counters = reinterpret_cast<int*>(parts + PARTS * PART_FLOATS);
+  constexpr int QUADS = RT * (D / 4);
+  auto store = [&](const Open& o, int r, int d4, float4 x, float sum) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int rr = o.t * RT + r;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.O) + (long long)(o.first + rr / group) * a.ldo +
+                         (long long)(o.h * group + rr % group) * D + d4 * 4;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x * inv, x.y * inv), hi = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+    if (vec) {
+      reinterpret_cast<__nv_bfloat162*>(out)[0] = lo;
+      reinterpret_cast<__nv_bfloat162*>(out)[1] = hi;
+    } else {
+      out[0] = lo.x;
+      out[1] = lo.y;
+      out[2] = hi.x;
+      out[3] = hi.y;
+    }
+  };
+  auto add = [](float4& x, float w, const float4& y) {
+    x.x = fmaf(w, y.x, x.x);
+    x.y = fmaf(w, y.y, x.y);
+    x.z = fmaf(w, y.z, x.z);
+    x.w = fmaf(w, y.w, x.w);
+  };
+  const int opens = sh.opens;
+  for (int i = threadIdx.x; i < opens * QUADS; i += NW * 32) {
+    const Open& o = sh.open[i / QUADS];
+    const int r = i % QUADS / (D / 4), d4 = i % (D / 4);
+    if (r >= o.rows) continue;
+    float M = -INFINITY;
+    for (int e = o.e0; e <= o.e1; ++e)
+      if (sh.slot[e].unit == o.unit) M = fmaxf(M, sh.slot[e].part[RT * D + r]);
+    const float Mu = M == -INFINITY ? 0.f : M;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int e = o.e0; e <= o.e1; ++e) {
+      if (sh.slot[e].unit != o.unit) continue;
+      const float* p = sh.slot[e].part;
+      const float w = ex2(p[RT * D + r] - Mu);
+      sum = fmaf(w, p[RT * D + RT + r], sum);
+      add(x, w, *reinterpret_cast<const float4*>(p + r * D + d4 * 4));
+    }
+    if (o.whole) {
+      store(o, r, d4, x, sum);
+    } else {
+      float* p = parts + (cta * 2 + (o.unit < A ? 0 : 1)) * PART_FLOATS;
+      *reinterpret_cast<float4*>(p + r * D + d4 * 4) = x;
+      if (d4 == 0) {
+        p[RT * D + r] = M;
+        p[RT * D + RT + r] = sum;
+      }
+    }
+  }
+  // ---- and more than one block: the last to arrive adds the blocks' parts in order
+  bool any = false;
+  for (int i = 0; i < opens; ++i) any |= !sh.open[i].whole;
+  if (!any) return;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x < opens) {
+    const Open& o = sh.open[threadIdx.x];
+    int last = 0;
+    if (!o.whole) {
+      const int c0 = (int)(((o.unit + 1) * G - 1) / T), c1 = (int)(((o.unit + o.S) * G - 1) / T);
+      last = atomicAdd(counters + o.count, 1) == c1 - c0;
+      if (last) counters[o.count] = 0;             // ready for the next call
+    }
+    sh.last[threadIdx.x] = last;
+  }
+  __syncthreads();
+  for (int j = 0; j < opens; ++j) {
+    if (!sh.last[j]) continue;
+    __threadfence();
+    const Open& o = sh.open[j];
+    const int c0 = (int)(((o.unit + 1) * G - 1) / T), c1 = (int)(((o.unit + o.S) * G - 1) / T);
+    for (int i = threadIdx.x; i < o.rows * (D / 4); i += NW * 32) {
+      const int r = i / (D / 4), d4 = i % (D / 4);
+      auto part = [&](int c) { return parts + ((u64)c * 2 + (o.unit < (u64)c * T / G ? 0 : 1)) * PART_FLOATS; };
+      float M = -INFINITY;
+      for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part(c) + RT * D + r));
+      const float Mu = M == -INFINITY ? 0.f : M;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+      for (int c = c0; c <= c1; ++c) {
+        const float* p = part(c);
+        const float w = ex2(__ldcg(p + RT * D + r) - Mu);
+        sum = fmaf(w, __ldcg(p + RT * D + RT + r), sum);
+        add(x, w, __ldcg(reinterpret_cast<const float4*>(p + r * D + d4 * 4)));
+      }
+      store(o, r, d4, x, sum);
+    }
+  }
+}
+
+template <int FMT, int D, int NT>
+int launch_fast(const KvAttnArgs& a, const CUtensorMap* mK, const CUtensorMap* mV, int group, int max_tiles, int vec,
+                int num_sms, cudaStream_t s) {
+  static std::atomic<uint64_t> smem_set{0};
+  constexpr int smem = NW * RING + 1024;
+  cudaError_t e = set_smem_once(smem_set, kv_attention_kernel<FMT, D, NT>, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(num_sms < MAX_CTAS ? num_sms : MAX_CTAS));
+  cfg.blockDim = dim3(NW * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<FMT, D, NT>, *mK, *mV, a, group, max_tiles, vec);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Rows of a tile for a call whose sequences have up to `rows` query rows a head.
+int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+
 template <class Kernel>
 int launch(Kernel kernel, dim3 grid, dim3 block, const KvAttnArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
@@ -133,6 +947,34 @@ int launch(Kernel kernel, dim3 grid, dim3 block, const KvAttnArgs& a, cudaStream
 }
 
 }  // namespace
+
+size_t kv_attention_ws_bytes(int seqs, int heads, int group, int max_new) {
+  const long long rows = (long long)max_new * group;
+  const long long tiles = rows > 0x7fffffff ? 0 : (rows + tile_rows((int)rows) - 1) / tile_rows((int)rows);
+  return PARTS * PART_FLOATS * sizeof(float) + (((size_t)seqs * heads * tiles + 3) / 4) * 16;
+}
+
+int launch_kv_attention(const KvAttnArgs& a, const CUtensorMap* mK, const CUtensorMap* mV, int num_sms,
+                        cudaStream_t s) {
+  const int group = a.Hq / a.c.H, rows = a.max_new * group, rt = tile_rows(rows), tiles = (rows + rt - 1) / rt;
+  // pairs of outputs and quads of queries as one access
+  const int vec = reinterpret_cast<uintptr_t>(a.Q) % 8 == 0 && a.ldq % 4 == 0 &&
+                  reinterpret_cast<uintptr_t>(a.O) % 4 == 0 && a.ldo % 2 == 0;
+  auto go = [&](auto fmt, auto dim) -> int {
+    constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
+    switch (rt) {
+      case 8: return launch_fast<F, D, 1>(a, mK, mV, group, tiles, vec, num_sms, s);
+      case 16: return launch_fast<F, D, 2>(a, mK, mV, group, tiles, vec, num_sms, s);
+      default: return launch_fast<F, D, 4>(a, mK, mV, group, tiles, vec, num_sms, s);
+    }
+  };
+  using std::integral_constant;
+  if (a.c.fmt == kKvE4M3)
+    return a.c.D == 128 ? go(integral_constant<int, kKvE4M3>{}, integral_constant<int, 128>{})
+                        : go(integral_constant<int, kKvE4M3>{}, integral_constant<int, 64>{});
+  return a.c.D == 128 ? go(integral_constant<int, kKvInt8>{}, integral_constant<int, 128>{})
+                      : go(integral_constant<int, kKvInt8>{}, integral_constant<int, 64>{});
+}
 
 int launch_kv_attention_generic(const KvAttnArgs& a, cudaStream_t s) {
   const dim3 grid((unsigned)a.tokens, (unsigned)a.Hq);
