@@ -11,6 +11,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cfloat>
 
 #include "internal.h"
@@ -265,6 +266,562 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
   }
 }
 
+
+// ------------------------------------------------------------------ a row in registers
+// A cluster of C blocks holds a row: thread for thread E logits, a warp's 32 * E
+// next to one another (so that warps, then blocks, are in index order).  The logits
+// are read once; everything after that works on registers, with one histogram or
+// list in shared memory and a few exchanges over the cluster.
+constexpr int FT = 512, FW = FT / 32;         // threads and warps of a block
+constexpr int MAX_C = 8;
+constexpr int LIST = 4096;                    // candidates that the first block can sort
+constexpr int LOCAL = 2048;                   // candidates that a block can gather
+constexpr int GROUPS = 4;                     // a thread's logits in groups, for the threshold
+constexpr int TOP_K_LIST = GROUPS * FT / 2;   // largest top_k for the candidate list
+constexpr float ZERO_Z = 28.f;                // expf(-28) < 2^-40: no mass
+
+// A cut by rank: kept are larger keys, and equal ones up to index idx
+struct Place {
+  uint32_t key;
+  int idx;
+  __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= idx); }
+};
+
+struct Cluster {
+  ull mass[2][FT];          // histograms by turns: one is read by the cluster while the other fills
+  unsigned count[2][FT];
+  ull list[LIST];           // first block: candidates, key << 32 | ~index
+  ull local[LOCAL];
+  ull all[MAX_C * FW];      // every warp's kept mass
+  ull warp_mass[FW];        // read by the cluster
+  unsigned warp_count[FW];  // read by the cluster
+  unsigned red[2][FW];
+  unsigned top, low;        // read by the cluster
+  unsigned lo[2], hi[2];    // read by the cluster, by turns
+  unsigned list_n;          // first block: candidates of the cluster
+  unsigned local_n, local_at;
+  unsigned best, n_above;
+  ull m_above;
+  ull scan_m[FW];
+  unsigned scan_c[FW];
+  Place cut;                // first block's, or the tie's owner's: read by the cluster
+};
+
+__device__ __forceinline__ void sync_cluster(int C) {
+  if (C == 1) __syncthreads();
+  else cluster_sync();
+}
+// `p` of this block's shared memory, in block r of the cluster
+template <typename T>
+__device__ __forceinline__ T* in_block(T* p, int r) {
+  uint64_t out;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(out) : "l"(reinterpret_cast<uint64_t>(p)), "r"(r));
+  return reinterpret_cast<T*>(out);
+}
+
+// Sums of all lower threads' values over the block; `c` and `m` become exclusive
+// prefixes.  Ends with shared memory free for the next call after a barrier.
+__device__ __forceinline__ void block_prefix(Cluster& sh, unsigned& c, ull& m) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const unsigned c0 = c;
+  const ull m0 = m;
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned x = __shfl_up_sync(0xffffffffu, c, o);
+    const ull y = __shfl_up_sync(0xffffffffu, m, o);
+    if (lane >= o) {
+      c += x;
+      m += y;
+    }
+  }
+  if (lane == 31) {
+    sh.scan_c[warp] = c;
+    sh.scan_m[warp] = m;
+  }
+  __syncthreads();
+  c -= c0;
+  m -= m0;
+  for (int w = 0; w < warp; ++w) {
+    c += sh.scan_c[w];
+    m += sh.scan_m[w];
+  }
+}
+
+template <typename T, int E>
+struct RowPart {
+  float x[E];               // NaN and what is past the row as -inf
+  int base;                 // index of x[0]
+  __device__ __forceinline__ int index(int j) const { return base + j * 32; }
+};
+
+template <typename T, int E>
+__global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(const SampleArgs a, const int C) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Cluster& sh = *reinterpret_cast<Cluster*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int rank = C == 1 ? 0 : (int)cluster_ctarank();
+  const int r = blockIdx.x / C;
+  griddep_wait();
+  if (tid == 0) griddep_launch_dependents();
+  const float t_in = a.temperature ? a.temperature[r] : 1.f;
+  const int k = a.top_k ? a.top_k[r] : 0;
+  const float p = a.top_p ? a.top_p[r] : 1.f;
+  const float least = a.min_p ? a.min_p[r] : 0.f;
+  const float u = a.u[r];
+  const bool greedy = !(t_in >= FLT_MIN) || k == 1;
+  const float t = t_in >= FLT_MIN ? t_in : 1.f;
+
+  RowPart<T, E> part;
+  part.base = (rank * FW + warp) * 32 * E + lane;
+  {
+    const T* row = static_cast<const T*>(a.logits) + (long long)r * a.ld;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const int i = part.index(j);
+      float l = -INFINITY;
+      if (i < a.vocab) {
+        if constexpr (sizeof(T) == 2) l = __bfloat162float(row[i]);
+        else l = row[i];
+      }
+      part.x[j] = l != l ? -INFINITY : l + 0.f;      // -0 as 0
+    }
+  }
+  for (int i = tid; i < FT; i += FT) {
+    sh.mass[0][i] = 0;
+    sh.count[0][i] = 0;
+  }
+  if (tid == 0) {
+    sh.list_n = 0;
+    sh.local_n = 0;
+  }
+  if (C > 1) cluster_arrive();                       // list_n is ready
+
+  // ---- the block's largest logit, and its smallest one above -inf
+  float group[GROUPS];
+  float lmin = INFINITY;
+#pragma unroll
+  for (int q = 0; q < GROUPS; ++q) {
+    group[q] = -INFINITY;
+#pragma unroll
+    for (int j = q * E / GROUPS; j < (q + 1) * E / GROUPS; ++j) {
+      group[q] = fmaxf(group[q], part.x[j]);
+      lmin = fminf(lmin, part.x[j] == -INFINITY ? INFINITY : part.x[j]);
+    }
+  }
+  float lmax = fmaxf(fmaxf(group[0], group[1]), fmaxf(group[2], group[3]));
+  {
+    const unsigned hi = __reduce_max_sync(0xffffffffu, order_key(lmax));
+    const unsigned lo = __reduce_min_sync(0xffffffffu, order_key(lmin));
+    if (lane == 0) {
+      sh.red[0][warp] = hi;
+      sh.red[1][warp] = lo;
+    }
+  }
+  __syncthreads();
+  unsigned top = sh.red[0][0], low = sh.red[1][0];
+  for (int w = 1; w < FW; ++w) {
+    top = max(top, sh.red[0][w]);
+    low = min(low, sh.red[1][w]);
+  }
+  if (tid == 0) {
+    sh.top = top;
+    sh.low = low;
+  }
+
+  const bool cuts = !greedy && ((k > 0 && k < a.vocab) || !(p >= 1.f));
+  const bool by_list = cuts && k > 0 && k <= TOP_K_LIST;
+  if (by_list) {
+    // ---- candidates for the first k ranks.  Every group's largest logit is an
+    // element, so the k-th largest of them bounds the block's k-th rank from below;
+    // a histogram of them finds a bound just under it.  What has no mass is no
+    // candidate.
+    const float ltop = key_logit(top);
+    const unsigned floor_key =
+        top <= kKeyNegInf ? 0xffffffffu : ltop == INFINITY ? top : max(kKeyNegInf + 1, order_key(ltop - ZERO_Z * t));
+    unsigned gmin = 0xffffffffu;
+#pragma unroll
+    for (int q = 0; q < GROUPS; ++q) {
+      const unsigned key = order_key(group[q]);
+      if (key >= floor_key) gmin = min(gmin, key);
+    }
+    gmin = __reduce_min_sync(0xffffffffu, gmin);
+    __syncthreads();                                 // red has been read
+    if (lane == 0) sh.red[0][warp] = gmin;
+    __syncthreads();
+    for (int w = 0; w < FW; ++w) gmin = min(gmin, sh.red[0][w]);
+    unsigned bound = floor_key;
+    if (gmin <= top) {
+      const int shift = max(0, 32 - __clz(top - gmin) - 9);
+#pragma unroll
+      for (int q = 0; q < GROUPS; ++q) {
+        const unsigned key = order_key(group[q]);
+        if (key >= gmin) atomicAdd(&sh.count[0][(top - key) >> shift], 1u);
+      }
+      __syncthreads();
+      unsigned c = sh.count[0][tid];
+      ull none = 0;
+      const unsigned own = c;
+      block_prefix(sh, c, none);
+      if (tid == 0) sh.best = FT;
+      __syncthreads();
+      if (c < (unsigned)k && c + own >= (unsigned)k) sh.best = tid;
+      __syncthreads();
+      if (sh.best < FT) {
+        // the lowest key of that bin
+        const unsigned span = ((sh.best + 1u) << shift) - 1u;
+        bound = span >= top ? floor_key : max(floor_key, top - span);
+      }
+      sh.count[0][tid] = 0;
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const unsigned key = order_key(part.x[j]);
+      if (key >= bound) {
+        const unsigned at = atomicAdd(&sh.local_n, 1u);
+        if (at < LOCAL) sh.local[at] = ((ull)key << 32) | (unsigned)~part.index(j);
+      }
+    }
+    __syncthreads();
+    if (C > 1) cluster_wait();
+    const unsigned n = sh.local_n;
+    if (tid == 0) sh.local_at = atomicAdd(in_block(&sh.list_n, 0), n > LOCAL ? LIST + 1u : n);
+    __syncthreads();
+    const unsigned at = sh.local_at;
+    if (n <= LOCAL && at + n <= LIST) {
+      ull* list = in_block(&sh.list[0], 0);
+      for (unsigned i = tid; i < n; i += FT) list[at + i] = sh.local[i];
+    }
+  } else if (C > 1) {
+    cluster_wait();
+  }
+  sync_cluster(C);
+  for (int c = 0; c < C; ++c) {
+    top = max(top, *in_block(&sh.top, c));
+    low = min(low, *in_block(&sh.low, c));
+  }
+  if (top <= kKeyNegInf) {                           // nothing can be taken
+    if (rank == 0 && tid == 0) {
+      a.token[r] = -1;
+      if (a.logprob) a.logprob[r] = -INFINITY;
+    }
+    sync_cluster(C);                                 // nobody leaves while its memory is read
+    return;
+  }
+  const Row row{key_logit(top), __fdiv_rn(1.f, t)};
+  auto mass_at = [&](float l) { return mass_of(logit_weight(row, l)); };
+
+  // ---- cuts, as the last place kept
+  Place cut{0u, 0x7fffffff};
+  bool by_search = cuts;
+  if (greedy) {
+    // the first place of the largest key: a search for one rank without its histogram
+    unsigned first = 0x7fffffffu;
+#pragma unroll
+    for (int j = E - 1; j >= 0; --j)
+      if (order_key(part.x[j]) == top) first = part.index(j);
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) sh.warp_count[warp] = first;
+    sync_cluster(C);
+    first = tid < C * FW ? *in_block(&sh.warp_count[tid % FW], tid / FW) : 0x7fffffffu;
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) sh.red[0][warp] = first;
+    __syncthreads();
+    for (int w = 0; w < FW; ++w) first = min(first, sh.red[0][w]);
+    cut = Place{top, (int)first};
+    sync_cluster(C);                                 // warp_count has been read
+  } else if (by_list) {
+    const unsigned n = *in_block(&sh.list_n, 0);
+    if (n <= LIST) {
+      by_search = false;
+      if (rank == 0) {
+        // sort, largest first
+        int n2 = 64;
+        while (n2 < (int)n) n2 <<= 1;
+        for (int i = n + tid; i < n2; i += FT) sh.list[i] = 0;
+        __syncthreads();
+        for (int size = 2; size <= n2; size <<= 1)
+          for (int step = size >> 1; step > 0; step >>= 1) {
+            for (int i = tid; i < n2 / 2; i += FT) {
+              const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
+              const ull x = sh.list[lo], y = sh.list[hi];
+              if ((x < y) == ((lo & size) == 0)) {
+                sh.list[lo] = y;
+                sh.list[hi] = x;
+              }
+            }
+            // steps up to 32 stay within the 64 places of a warp
+            if (step > 32 || (step == 1 && size >= 64)) __syncthreads();
+            else __syncwarp();
+          }
+        __syncthreads();
+        const int kept = min((int)n, k);
+        constexpr int PER = TOP_K_LIST / FT;         // ranks of a thread
+        ull m[PER], mine = 0;
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+          const int i = tid * PER + q;
+          m[q] = i < kept ? mass_at(key_logit((uint32_t)(sh.list[i] >> 32))) : 0;
+          mine += m[q];
+        }
+        unsigned none = 0;
+        ull before = mine;
+        block_prefix(sh, none, before);
+        ull total = 0;
+        for (int w = 0; w < FW; ++w) total += sh.scan_m[w];
+        const double bound = __dmul_rn((double)p, __ull2double_rn(total));
+        int ranks = 0;                               // of this thread that top-p keeps
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+          const int i = tid * PER + q;
+          if (i < kept && (p >= 1.f || i == 0 || __ull2double_rn(before) < bound)) ranks = i + 1;
+          before += m[q];
+        }
+        ranks = __reduce_max_sync(0xffffffffu, ranks);
+        if (lane == 0) sh.red[0][warp] = ranks;
+        __syncthreads();
+        for (int w = 0; w < FW; ++w) ranks = max(ranks, (int)sh.red[0][w]);
+        if (tid == 0) {
+          const ull x = sh.list[ranks - 1];
+          sh.cut = Place{(uint32_t)(x >> 32), (int)~(unsigned)x};
+        }
+      }
+      sync_cluster(C);
+      cut = *in_block(&sh.cut, 0);
+    }
+  }
+  if (by_search) {
+    // ---- the general search.  First bins even in the logit over the range that has
+    // mass, then bins even in the key, until one key is left
+    int turn = 0;                                    // histogram in use; it is zero
+    auto search = [&](auto keep) {
+      const float range = fminf(ZERO_Z * t, row.top - key_logit(low));
+      const float scale = range > 0.f ? 511.9f / range : 0.f;
+      auto first_bin = [&](float l) { return min(FT - 1, (int)((row.top - l) * scale)); };
+      unsigned n_above = 0, lo = 0, hi = 0;
+      ull m_above = 0;
+      int bin0 = -1, shift = 0;
+      while (true) {
+        auto in = [&](int j, unsigned key) {
+          if (!cut.keeps(key, part.index(j))) return false;
+          return bin0 < 0 || (key >= lo && key <= hi && first_bin(part.x[j]) == bin0);
+        };
+        // histogram
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const unsigned key = order_key(part.x[j]);
+          if (key > kKeyNegInf && in(j, key)) {
+            const ull m = mass_at(part.x[j]);
+            if (m) {
+              const int b = bin0 < 0 ? first_bin(part.x[j]) : (int)((hi - key) >> shift);
+              atomicAdd(&sh.count[turn][b], 1u);
+              atomicAdd(&sh.mass[turn][b], m);
+            }
+          }
+        }
+        sync_cluster(C);
+        sh.count[turn ^ 1][tid] = 0;                 // the last turn's: every block has read it by now
+        sh.mass[turn ^ 1][tid] = 0;
+        unsigned c = 0;
+        ull m = 0;
+        for (int q = 0; q < C; ++q) {
+          c += in_block(&sh.count[turn][0], q)[tid];
+          m += in_block(&sh.mass[turn][0], q)[tid];
+        }
+        const unsigned own = c;
+        block_prefix(sh, c, m);
+        c += n_above;
+        m += m_above;
+        if (tid == 0) sh.best = 0;
+        __syncthreads();
+        if (own && keep(c, m)) atomicMax(&sh.best, (unsigned)tid);
+        __syncthreads();
+        if (tid == (int)sh.best) {
+          sh.n_above = c;
+          sh.m_above = m;
+          sh.red[0][0] = own;
+        }
+        __syncthreads();
+        const unsigned best = sh.best, n_equal = sh.red[0][0];
+        n_above = sh.n_above;
+        m_above = sh.m_above;
+        if (bin0 < 0) {
+          // the keys in that bin
+          bin0 = (int)best;
+          lo = 0xffffffffu;
+          hi = 0;
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            const unsigned key = order_key(part.x[j]);
+            if (key > kKeyNegInf && cut.keeps(key, part.index(j)) && first_bin(part.x[j]) == bin0 &&
+                mass_at(part.x[j])) {
+              lo = min(lo, key);
+              hi = max(hi, key);
+            }
+          }
+          lo = __reduce_min_sync(0xffffffffu, lo);
+          hi = __reduce_max_sync(0xffffffffu, hi);
+          __syncthreads();
+          if (lane == 0) {
+            sh.red[0][warp] = lo;
+            sh.red[1][warp] = hi;
+          }
+          __syncthreads();
+          if (tid == 0) {
+            for (int w = 1; w < FW; ++w) {
+              lo = min(lo, sh.red[0][w]);
+              hi = max(hi, sh.red[1][w]);
+            }
+            sh.lo[0] = lo;
+            sh.hi[0] = hi;
+          }
+          sync_cluster(C);
+          for (int q = 0; q < C; ++q) {
+            lo = min(lo, *in_block(&sh.lo[0], q));
+            hi = max(hi, *in_block(&sh.hi[0], q));
+          }
+        } else {
+          const unsigned from = best << shift;       // bins are counted from hi down
+          const unsigned span = (1u << shift) - 1u;
+          hi -= from;
+          lo = max(lo, hi >= span ? hi - span : 0u);
+        }
+        turn ^= 1;
+        if (lo == hi) {
+          // one key: how many of its n_equal tokens, lowest index first
+          const ull one = mass_at(key_logit(hi));
+          unsigned least_n = 1, most = n_equal;
+          while (least_n < most) {
+            const unsigned mid = (least_n + most + 1) / 2;
+            if (keep(n_above + mid - 1, m_above + (ull)(mid - 1) * one)) least_n = mid;
+            else most = mid - 1;
+          }
+          if (least_n == n_equal) {
+            if (hi > cut.key) cut = Place{hi, 0x7fffffff};
+            return;
+          }
+          // the index of that token
+          unsigned seen = 0;
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            const unsigned key = order_key(part.x[j]);
+            seen += __popc(__ballot_sync(0xffffffffu, key == hi && cut.keeps(key, part.index(j))));
+          }
+          sync_cluster(C);                           // warp_count is free
+          if (lane == 0) sh.warp_count[warp] = seen;
+          sync_cluster(C);
+          unsigned before = 0;
+          for (int q = lane; q < rank * FW + warp; q += 32) before += *in_block(&sh.warp_count[q % FW], q / FW);
+          before = __reduce_add_sync(0xffffffffu, before);
+          if (before < least_n && least_n <= before + seen) {
+            unsigned at = before;
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+              const unsigned key = order_key(part.x[j]);
+              const bool mine = key == hi && cut.keeps(key, part.index(j));
+              const unsigned eq = __ballot_sync(0xffffffffu, mine);
+              if (mine && at + __popc(eq & ((2u << lane) - 1u)) == least_n)
+                for (int q = 0; q < C; ++q) *in_block(&sh.cut, q) = Place{hi, part.index(j)};
+              at += __popc(eq);
+            }
+          }
+          sync_cluster(C);
+          cut = sh.cut;
+          return;
+        }
+        shift = max(0, 32 - __clz(hi - lo) - 9);
+      }
+    };
+    if (k > 0 && k < a.vocab) search([&](unsigned c, ull) { return c < (unsigned)k; });
+    if (!(p >= 1.f)) {
+      ull m = 0;
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (cut.keeps(order_key(part.x[j]), part.index(j))) m += mass_at(part.x[j]);
+      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+      if (lane == 0) sh.warp_mass[warp] = m;
+      sync_cluster(C);
+      m = tid < C * FW ? in_block(&sh.warp_mass[0], tid / FW)[tid % FW] : 0;
+      unsigned none = 0;
+      block_prefix(sh, none, m);
+      ull total = 0;
+      for (int w = 0; w < FW; ++w) total += sh.scan_m[w];
+      const double bound = __dmul_rn((double)p, __ull2double_rn(total));
+      sync_cluster(C);                               // warp_mass has been read
+      search([&](unsigned c, ull before) { return c == 0 || __ull2double_rn(before) < bound; });
+    }
+  }
+
+  // ---- the draw: every warp's kept mass, then the warp in which the target falls
+  auto kept = [&](float l, int i) -> ull {
+    const unsigned key = order_key(l);
+    if (!cut.keeps(key, i) || key <= kKeyNegInf) return 0;
+    const float w = logit_weight(row, l);
+    return w >= least || key == top ? mass_of(w) : 0;
+  };
+  ull m = 0;
+#pragma unroll
+  for (int j = 0; j < E; ++j) m += kept(part.x[j], part.index(j));
+  for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+  if (lane == 0) sh.warp_mass[warp] = m;
+  sync_cluster(C);
+  {
+    ull before = tid < C * FW ? in_block(&sh.warp_mass[0], tid / FW)[tid % FW] : 0;
+    unsigned none = 0;
+    block_prefix(sh, none, before);
+    if (tid < C * FW) sh.all[tid] = before;
+  }
+  __syncthreads();
+  ull total = 0;
+  for (int w = 0; w < FW; ++w) total += sh.scan_m[w];
+  const double at = __dmul_rn((double)u, __ull2double_rn(total));
+  ull target = at > 0.0 ? __double2ull_rz(at) : 0;   // NaN: 0
+  if (target >= total) target = total - 1;
+  ull before = sh.all[rank * FW + warp];
+  if (before <= target && target < before + m) {
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const ull x = found ? 0 : kept(part.x[j], part.index(j));
+      if (!__any_sync(0xffffffffu, x != 0)) continue;
+      ull run = x;
+      for (int o = 1; o < 32; o <<= 1) {
+        const ull y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + run > target);
+      if (past && lane == __ffs(past) - 1) {
+        a.token[r] = part.index(j);
+        if (a.logprob)
+          a.logprob[r] = logit_z(row, part.x[j]) - logf((float)(__ull2double_rn(total) * 0x1p-40));
+      }
+      found = past != 0;
+      before += __shfl_sync(0xffffffffu, run, 31);
+    }
+  }
+  if (C > 1) cluster_sync();                         // nobody leaves while its memory is read
+}
+
+template <typename T, int E>
+int launch_cluster(const SampleArgs& a, int C, cudaStream_t s) {
+  static std::atomic<uint64_t> smem_set{0};
+  cudaError_t e = set_smem_once(smem_set, sample_cluster_kernel<T, E>, (int)sizeof(Cluster));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)C;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)a.rows * (unsigned)C);
+  cfg.blockDim = dim3(FT);
+  cfg.dynamicSmemBytes = sizeof(Cluster);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, sample_cluster_kernel<T, E>, a, C);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <class Kernel>
 int launch(Kernel kernel, dim3 grid, const SampleArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
@@ -280,12 +837,28 @@ int launch(Kernel kernel, dim3 grid, const SampleArgs& a, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+
+template <typename T>
+int launch_any(const SampleArgs& a, cudaStream_t s) {
+  // the fewest logits a thread that fit a cluster of eight
+  auto blocks = [&](int E) {
+    int C = 1;
+    while (C * FT * E < a.vocab) C <<= 1;
+    return C;
+  };
+  if (a.rows <= 0x7fffffff / MAX_C) {
+    if (blocks(8) <= MAX_C) return launch_cluster<T, 8>(a, blocks(8), s);
+    if (blocks(32) <= MAX_C) return launch_cluster<T, 32>(a, blocks(32), s);
+    if (blocks(64) <= MAX_C) return launch_cluster<T, 64>(a, blocks(64), s);
+  }
+  return launch(sample_kernel<T>, dim3((unsigned)a.rows), a, s);
+}
+
 }  // namespace
 
 int launch_sample(const SampleArgs& a, int num_sms, cudaStream_t s) {
   (void)num_sms;
-  if (a.bf16) return launch(sample_kernel<__nv_bfloat16>, dim3((unsigned)a.rows), a, s);
-  return launch(sample_kernel<float>, dim3((unsigned)a.rows), a, s);
+  return a.bf16 ? launch_any<__nv_bfloat16>(a, s) : launch_any<float>(a, s);
 }
 
 }  // namespace g3
