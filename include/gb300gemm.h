@@ -444,7 +444,7 @@ size_t gemm_kv_attention_workspace(int seqs, int heads, int Hq, int dim, int max
  *     top_k:  the first top_k ranks (top_k <= 0: all);
  *     top_p:  of those, with M their total mass, the ranks with less than
  *             top_p * M before them, the first always;
- *     min_p:  of those, the tokens with w >= min_p, the first rank always.
+ *     min_p:  of those, the tokens with w >= min_p, the first rank always (it has w = 1).
  * With T the kept tokens' total mass, the token is the first, in index order, at
  * which the running mass of the kept exceeds floor(u * T) (products with u and
  * top_p in fp64; u outside [0, 1) is taken to the nearest of the range, NaN to

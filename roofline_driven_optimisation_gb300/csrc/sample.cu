@@ -139,11 +139,12 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
   const int r = blockIdx.x, vocab = a.vocab, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const Logits<T> logit{static_cast<const T*>(a.logits) + (long long)r * a.ld};
   const float t = a.temperature ? a.temperature[r] : 1.f;
-  const bool greedy = !(t >= FLT_MIN);
   const int k = a.top_k ? a.top_k[r] : 0;
   const float p = a.top_p ? a.top_p[r] : 1.f;
   const float least = a.min_p ? a.min_p[r] : 0.f;
   const float u = a.u[r];
+  // only the first rank: also where no weight, 1 at most, can reach min_p
+  const bool greedy = !(t >= FLT_MIN) || k == 1 || !(least <= 1.f);
 
   // the largest key and the first index that has it
   uint32_t top = 0;
@@ -160,13 +161,13 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     }
     return;
   }
-  const Row row{key_logit(top), greedy ? 1.f : __fdiv_rn(1.f, t)};
+  const Row row{key_logit(top), __fdiv_rn(1.f, t >= FLT_MIN ? t : 1.f)};
 
   // cuts; key 0 keeps everything
   Cut cut{0u, vocab};
   unsigned n_above = 0, n_equal = 0;
   ull m_above = 0;
-  if (greedy || k == 1) {
+  if (greedy) {
     cut = Cut{top, 1};
   } else {
     if (k > 0 && k < vocab) {
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     seen += __popc(eq);
     if (!in) return 0;
     const float w = logit_weight(row, l);
-    return w >= least || key == top ? mass_of(w) : 0;
+    return w >= least || greedy ? mass_of(w) : 0;
   };
   ull m = 0;
   unsigned seen = ties_before;
@@ -267,17 +268,19 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
 }
 
 
-// ------------------------------------------------------------------ a row in registers
-// A cluster of C blocks holds a row: thread for thread E logits, a warp's 32 * E
-// next to one another (so that warps, then blocks, are in index order).  The logits
-// are read once; everything after that works on registers, with one histogram or
-// list in shared memory and a few exchanges over the cluster.
+// ------------------------------------------------------------------ a row in a cluster
+// A cluster of C blocks holds a row as keys in shared memory, a warp's 128 * Q next to
+// one another (so that warps, then blocks, are in index order).  The logits are read
+// once; everything after that works on the keys, with one histogram or list and a
+// few exchanges over the cluster.  Quad q of a lane holds the keys of indices
+// base + (4 q + k) * 32 + lane, k = 0 .. 3.
 constexpr int FT = 512, FW = FT / 32;         // threads and warps of a block
 constexpr int MAX_C = 8;
-constexpr int LIST = 4096;                    // candidates that the first block can sort
-constexpr int LOCAL = 2048;                   // candidates that a block can gather
-constexpr int GROUPS = 4;                     // a thread's logits in groups, for the threshold
-constexpr int TOP_K_LIST = GROUPS * FT / 2;   // largest top_k for the candidate list
+constexpr int MAX_Q = 22;                     // quads of a thread: 8 * FT * 88 logits, 180 KB of keys
+constexpr int LIST = 2048;                    // candidates that the first block can sort
+constexpr int LOCAL = 1024;                   // candidates that a block can gather
+constexpr int TOP_K_LIST = 1024;              // largest top_k for the candidate list: half of the 4 * FT groups
+constexpr int SAMPLE_Q = 4;                   // quads of a thread before a row takes more blocks
 constexpr float ZERO_Z = 28.f;                // expf(-28) < 2^-40: no mass
 
 // A cut by rank: kept are larger keys, and equal ones up to index idx
@@ -287,7 +290,7 @@ struct Place {
   __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= idx); }
 };
 
-struct Cluster {
+struct alignas(16) Cluster {
   ull mass[2][FT];          // histograms by turns: one is read by the cluster while the other fills
   unsigned count[2][FT];
   ull list[LIST];           // first block: candidates, key << 32 | ~index
@@ -296,7 +299,7 @@ struct Cluster {
   ull warp_mass[FW];        // read by the cluster
   unsigned warp_count[FW];  // read by the cluster
   unsigned red[2][FW];
-  unsigned top, low;        // read by the cluster
+  unsigned top;             // read by the cluster
   unsigned lo[2], hi[2];    // read by the cluster, by turns
   unsigned list_n;          // first block: candidates of the cluster
   unsigned local_n, local_at;
@@ -346,45 +349,185 @@ __device__ __forceinline__ void block_prefix(Cluster& sh, unsigned& c, ull& m) {
   }
 }
 
-template <typename T, int E>
-struct RowPart {
-  float x[E];               // NaN and what is past the row as -inf
-  int base;                 // index of x[0]
-  __device__ __forceinline__ int index(int j) const { return base + j * 32; }
-};
+// Sorts list[0 .. n2) (n2 a power of two, 64 .. LIST), largest first; whole block.
+__device__ __forceinline__ void sort_list(Cluster& sh, int n2) {
+  const int tid = threadIdx.x;
+  if (n2 <= FT) {
+    // a value a thread: steps within a warp by shuffles, others through shared
+    // memory, in two buffers by turns
+    ull x = tid < n2 ? sh.list[tid] : 0;
+    ull* other = sh.local;
+    for (int size = 2; size <= n2; size <<= 1)
+      for (int step = size >> 1; step > 0; step >>= 1) {
+        ull y;
+        if (step < 32) {
+          y = __shfl_xor_sync(0xffffffffu, x, step);
+        } else {
+          other[tid] = x;
+          __syncthreads();
+          y = other[tid ^ step];
+          other = other == sh.local ? sh.local + FT : sh.local;
+        }
+        // the lower place of a pair keeps the larger value in a descending run
+        const bool larger = ((tid & step) == 0) == ((tid & size) == 0);
+        x = (x < y) == larger ? y : x;
+      }
+    __syncthreads();
+    if (tid < n2) sh.list[tid] = x;
+    __syncthreads();
+    return;
+  }
+  for (int size = 2; size <= n2; size <<= 1)
+    for (int step = size >> 1; step > 0; step >>= 1) {
+      for (int i = tid; i < n2 / 2; i += FT) {
+        const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
+        const ull x = sh.list[lo], y = sh.list[hi];
+        if ((x < y) == ((lo & size) == 0)) {
+          sh.list[lo] = y;
+          sh.list[hi] = x;
+        }
+      }
+      __syncthreads();
+    }
+}
 
-template <typename T, int E>
-__global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(const SampleArgs a, const int C) {
+// The draw where the first block's list holds every token that can be kept: both
+// cuts in rank order, then the running mass in index order.
+__device__ __forceinline__ void draw_from_list(const SampleArgs& a, Cluster& sh, int r, int n, int k, float p, float least,
+                               float u, float t) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  constexpr int PER = TOP_K_LIST / FT;               // places of a thread
+  auto pad = [&](int m) {                            // zeros up to a power of two
+    int n2 = 64;
+    while (n2 < m) n2 <<= 1;
+    for (int i = m + tid; i < n2; i += FT) sh.list[i] = 0;
+    __syncthreads();
+    return n2;
+  };
+  sort_list(sh, pad(n));
+  const unsigned top = (unsigned)(sh.list[0] >> 32);
+  const Row row{key_logit(top), __fdiv_rn(1.f, t)};
+  int kept = min(n, k);
+  auto totals = [&]() {
+    ull total = 0;
+    for (int w = 0; w < FW; ++w) total += sh.scan_m[w];
+    return total;
+  };
+  if (!(p >= 1.f)) {
+    ull m[PER], before = 0;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int i = tid * PER + q;
+      m[q] = i < kept ? mass_of(logit_weight(row, key_logit((unsigned)(sh.list[i] >> 32)))) : 0;
+      before += m[q];
+    }
+    unsigned none = 0;
+    block_prefix(sh, none, before);
+    const double bound = __dmul_rn((double)p, __ull2double_rn(totals()));
+    int ranks = 0;                                   // of this thread that top-p keeps
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int i = tid * PER + q;
+      if (i < kept && (i == 0 || __ull2double_rn(before) < bound)) ranks = i + 1;
+      before += m[q];
+    }
+    ranks = __reduce_max_sync(0xffffffffu, ranks);
+    if (lane == 0) sh.red[0][warp] = ranks;
+    __syncthreads();
+    for (int w = 0; w < FW; ++w) ranks = max(ranks, (int)sh.red[0][w]);
+    kept = ranks;
+  }
+  // by index: ~index << 32 | key, largest first
+  __syncthreads();                                   // list[0] has been read
+  for (int i = tid; i < kept; i += FT) {
+    const ull x = sh.list[i];
+    sh.list[i] = (x << 32) | (x >> 32);
+  }
+  const int n2 = pad(kept);
+  sort_list(sh, n2);
+  ull m[PER], before = 0;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int i = tid * PER + q;
+    m[q] = 0;
+    if (i < kept) {
+      const unsigned key = (unsigned)sh.list[i];
+      const float w = logit_weight(row, key_logit(key));
+      if (w >= least) m[q] = mass_of(w);
+    }
+    before += m[q];
+  }
+  unsigned none = 0;
+  block_prefix(sh, none, before);
+  const ull total = totals();
+  const double at = __dmul_rn((double)u, __ull2double_rn(total));
+  ull target = at > 0.0 ? __double2ull_rz(at) : 0;   // NaN: 0
+  if (target >= total) target = total - 1;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    if (before <= target && target < before + m[q]) {
+      const ull x = sh.list[tid * PER + q];
+      a.token[r] = (int)~(unsigned)(x >> 32);
+      if (a.logprob)
+        a.logprob[r] = logit_z(row, key_logit((unsigned)x)) - logf((float)(__ull2double_rn(total) * 0x1p-40));
+    }
+    before += m[q];
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs a, const int C, const int Q) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Cluster& sh = *reinterpret_cast<Cluster*>(smem_raw);
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  uint4* const keys = reinterpret_cast<uint4*>(smem_raw + sizeof(Cluster)) + warp * Q * 32 + lane;   // quad q at [q * 32]
   const int rank = C == 1 ? 0 : (int)cluster_ctarank();
   const int r = blockIdx.x / C;
+  const int base = (rank * FW + warp) * 128 * Q + lane;   // index of key k of quad q: base + (4 q + k) * 32
   griddep_wait();
   if (tid == 0) griddep_launch_dependents();
+
+  // ---- read the row.  Groups are the keys at one place k of a thread's quads.
+  unsigned group[4] = {0, 0, 0, 0};
+  {
+    const T* row = static_cast<const T*>(a.logits) + (long long)r * a.ld;
+#pragma unroll 4
+    for (int q = 0; q < Q; ++q) {
+      unsigned key[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = base + (4 * q + k) * 32;
+        float l = -INFINITY;
+        if (i < a.vocab) {
+          if constexpr (sizeof(T) == 2) l = __bfloat162float(row[i]);
+          else l = row[i];
+        }
+        key[k] = order_key(l);
+        group[k] = max(group[k], key[k]);
+      }
+      keys[q * 32] = make_uint4(key[0], key[1], key[2], key[3]);
+    }
+  }
   const float t_in = a.temperature ? a.temperature[r] : 1.f;
   const int k = a.top_k ? a.top_k[r] : 0;
   const float p = a.top_p ? a.top_p[r] : 1.f;
   const float least = a.min_p ? a.min_p[r] : 0.f;
   const float u = a.u[r];
-  const bool greedy = !(t_in >= FLT_MIN) || k == 1;
+  // only the first rank: also where no weight, 1 at most, can reach min_p
+  const bool greedy = !(t_in >= FLT_MIN) || k == 1 || !(least <= 1.f);
   const float t = t_in >= FLT_MIN ? t_in : 1.f;
-
-  RowPart<T, E> part;
-  part.base = (rank * FW + warp) * 32 * E + lane;
-  {
-    const T* row = static_cast<const T*>(a.logits) + (long long)r * a.ld;
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const int i = part.index(j);
-      float l = -INFINITY;
-      if (i < a.vocab) {
-        if constexpr (sizeof(T) == 2) l = __bfloat162float(row[i]);
-        else l = row[i];
-      }
-      part.x[j] = l != l ? -INFINITY : l + 0.f;      // -0 as 0
+  // f(key, index) for this thread's keys, in index order
+  auto each = [&](auto f) {
+#pragma unroll 2
+    for (int q = 0; q < Q; ++q) {
+      const uint4 x = keys[q * 32];
+      const int i = base + q * 128;
+      f(x.x, i);
+      f(x.y, i + 32);
+      f(x.z, i + 64);
+      f(x.w, i + 96);
     }
-  }
+  };
   for (int i = tid; i < FT; i += FT) {
     sh.mass[0][i] = 0;
     sh.count[0][i] = 0;
@@ -395,37 +538,13 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
   }
   if (C > 1) cluster_arrive();                       // list_n is ready
 
-  // ---- the block's largest logit, and its smallest one above -inf
-  float group[GROUPS];
-  float lmin = INFINITY;
-#pragma unroll
-  for (int q = 0; q < GROUPS; ++q) {
-    group[q] = -INFINITY;
-#pragma unroll
-    for (int j = q * E / GROUPS; j < (q + 1) * E / GROUPS; ++j) {
-      group[q] = fmaxf(group[q], part.x[j]);
-      lmin = fminf(lmin, part.x[j] == -INFINITY ? INFINITY : part.x[j]);
-    }
-  }
-  float lmax = fmaxf(fmaxf(group[0], group[1]), fmaxf(group[2], group[3]));
-  {
-    const unsigned hi = __reduce_max_sync(0xffffffffu, order_key(lmax));
-    const unsigned lo = __reduce_min_sync(0xffffffffu, order_key(lmin));
-    if (lane == 0) {
-      sh.red[0][warp] = hi;
-      sh.red[1][warp] = lo;
-    }
-  }
+  // ---- the block's largest key
+  unsigned top = max(max(group[0], group[1]), max(group[2], group[3]));
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) sh.red[0][warp] = top;
   __syncthreads();
-  unsigned top = sh.red[0][0], low = sh.red[1][0];
-  for (int w = 1; w < FW; ++w) {
-    top = max(top, sh.red[0][w]);
-    low = min(low, sh.red[1][w]);
-  }
-  if (tid == 0) {
-    sh.top = top;
-    sh.low = low;
-  }
+  for (int w = 0; w < FW; ++w) top = max(top, sh.red[0][w]);
+  if (tid == 0) sh.top = top;
 
   const bool cuts = !greedy && ((k > 0 && k < a.vocab) || !(p >= 1.f));
   const bool by_list = cuts && k > 0 && k <= TOP_K_LIST;
@@ -439,10 +558,8 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
         top <= kKeyNegInf ? 0xffffffffu : ltop == INFINITY ? top : max(kKeyNegInf + 1, order_key(ltop - ZERO_Z * t));
     unsigned gmin = 0xffffffffu;
 #pragma unroll
-    for (int q = 0; q < GROUPS; ++q) {
-      const unsigned key = order_key(group[q]);
-      if (key >= floor_key) gmin = min(gmin, key);
-    }
+    for (int q = 0; q < 4; ++q)
+      if (group[q] >= floor_key) gmin = min(gmin, group[q]);
     gmin = __reduce_min_sync(0xffffffffu, gmin);
     __syncthreads();                                 // red has been read
     if (lane == 0) sh.red[0][warp] = gmin;
@@ -450,12 +567,12 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
     for (int w = 0; w < FW; ++w) gmin = min(gmin, sh.red[0][w]);
     unsigned bound = floor_key;
     if (gmin <= top) {
-      const int shift = max(0, 32 - __clz(top - gmin) - 9);
+      // bins even in the logit; an infinite range falls into one bin
+      const float range = ltop - key_logit(gmin);
+      const float scale = range > 0.f && range < INFINITY ? 511.9f / range : 0.f;
 #pragma unroll
-      for (int q = 0; q < GROUPS; ++q) {
-        const unsigned key = order_key(group[q]);
-        if (key >= gmin) atomicAdd(&sh.count[0][(top - key) >> shift], 1u);
-      }
+      for (int q = 0; q < 4; ++q)
+        if (group[q] >= gmin) atomicAdd(&sh.count[0][min(FT - 1, (int)((ltop - key_logit(group[q])) * scale))], 1u);
       __syncthreads();
       unsigned c = sh.count[0][tid];
       ull none = 0;
@@ -465,21 +582,16 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
       __syncthreads();
       if (c < (unsigned)k && c + own >= (unsigned)k) sh.best = tid;
       __syncthreads();
-      if (sh.best < FT) {
-        // the lowest key of that bin
-        const unsigned span = ((sh.best + 1u) << shift) - 1u;
-        bound = span >= top ? floor_key : max(floor_key, top - span);
-      }
+      // the lower edge of that bin, less what the bins' rounding may be off
+      if (sh.best < FT) bound = scale > 0.f ? max(gmin, order_key(ltop - (sh.best + 1.01f) / scale)) : gmin;
       sh.count[0][tid] = 0;
     }
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const unsigned key = order_key(part.x[j]);
+    each([&](unsigned key, int i) {
       if (key >= bound) {
         const unsigned at = atomicAdd(&sh.local_n, 1u);
-        if (at < LOCAL) sh.local[at] = ((ull)key << 32) | (unsigned)~part.index(j);
+        if (at < LOCAL) sh.local[at] = ((ull)key << 32) | (unsigned)~i;
       }
-    }
+    });
     __syncthreads();
     if (C > 1) cluster_wait();
     const unsigned n = sh.local_n;
@@ -494,10 +606,27 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
     cluster_wait();
   }
   sync_cluster(C);
-  for (int c = 0; c < C; ++c) {
-    top = max(top, *in_block(&sh.top, c));
-    low = min(low, *in_block(&sh.low, c));
+  if (by_list) {
+    const unsigned n = *in_block(&sh.list_n, 0);
+    if (n <= LIST) {
+      // the first block has all there is to choose from
+      if (rank != 0) {
+        cluster_arrive();                            // it has been read; nobody reads this block
+        return;
+      }
+      if (n == 0) {
+        if (tid == 0) {
+          a.token[r] = -1;
+          if (a.logprob) a.logprob[r] = -INFINITY;
+        }
+      } else {
+        draw_from_list(a, sh, r, (int)n, k, p, least, u, t);
+      }
+      if (C > 1) cluster_sync();
+      return;
+    }
   }
+  for (int c = 0; c < C; ++c) top = max(top, *in_block(&sh.top, c));
   if (top <= kKeyNegInf) {                           // nothing can be taken
     if (rank == 0 && tid == 0) {
       a.token[r] = -1;
@@ -507,17 +636,16 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
     return;
   }
   const Row row{key_logit(top), __fdiv_rn(1.f, t)};
-  auto mass_at = [&](float l) { return mass_of(logit_weight(row, l)); };
+  auto mass_at = [&](unsigned key) { return mass_of(logit_weight(row, key_logit(key))); };
 
   // ---- cuts, as the last place kept
   Place cut{0u, 0x7fffffff};
-  bool by_search = cuts;
   if (greedy) {
     // the first place of the largest key: a search for one rank without its histogram
     unsigned first = 0x7fffffffu;
-#pragma unroll
-    for (int j = E - 1; j >= 0; --j)
-      if (order_key(part.x[j]) == top) first = part.index(j);
+    each([&](unsigned key, int i) {
+      if (key == top) first = min(first, (unsigned)i);
+    });
     first = __reduce_min_sync(0xffffffffu, first);
     if (lane == 0) sh.warp_count[warp] = first;
     sync_cluster(C);
@@ -528,95 +656,42 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
     for (int w = 0; w < FW; ++w) first = min(first, sh.red[0][w]);
     cut = Place{top, (int)first};
     sync_cluster(C);                                 // warp_count has been read
-  } else if (by_list) {
-    const unsigned n = *in_block(&sh.list_n, 0);
-    if (n <= LIST) {
-      by_search = false;
-      if (rank == 0) {
-        // sort, largest first
-        int n2 = 64;
-        while (n2 < (int)n) n2 <<= 1;
-        for (int i = n + tid; i < n2; i += FT) sh.list[i] = 0;
-        __syncthreads();
-        for (int size = 2; size <= n2; size <<= 1)
-          for (int step = size >> 1; step > 0; step >>= 1) {
-            for (int i = tid; i < n2 / 2; i += FT) {
-              const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
-              const ull x = sh.list[lo], y = sh.list[hi];
-              if ((x < y) == ((lo & size) == 0)) {
-                sh.list[lo] = y;
-                sh.list[hi] = x;
-              }
-            }
-            // steps up to 32 stay within the 64 places of a warp
-            if (step > 32 || (step == 1 && size >= 64)) __syncthreads();
-            else __syncwarp();
-          }
-        __syncthreads();
-        const int kept = min((int)n, k);
-        constexpr int PER = TOP_K_LIST / FT;         // ranks of a thread
-        ull m[PER], mine = 0;
-#pragma unroll
-        for (int q = 0; q < PER; ++q) {
-          const int i = tid * PER + q;
-          m[q] = i < kept ? mass_at(key_logit((uint32_t)(sh.list[i] >> 32))) : 0;
-          mine += m[q];
-        }
-        unsigned none = 0;
-        ull before = mine;
-        block_prefix(sh, none, before);
-        ull total = 0;
-        for (int w = 0; w < FW; ++w) total += sh.scan_m[w];
-        const double bound = __dmul_rn((double)p, __ull2double_rn(total));
-        int ranks = 0;                               // of this thread that top-p keeps
-#pragma unroll
-        for (int q = 0; q < PER; ++q) {
-          const int i = tid * PER + q;
-          if (i < kept && (p >= 1.f || i == 0 || __ull2double_rn(before) < bound)) ranks = i + 1;
-          before += m[q];
-        }
-        ranks = __reduce_max_sync(0xffffffffu, ranks);
-        if (lane == 0) sh.red[0][warp] = ranks;
-        __syncthreads();
-        for (int w = 0; w < FW; ++w) ranks = max(ranks, (int)sh.red[0][w]);
-        if (tid == 0) {
-          const ull x = sh.list[ranks - 1];
-          sh.cut = Place{(uint32_t)(x >> 32), (int)~(unsigned)x};
-        }
-      }
-      sync_cluster(C);
-      cut = *in_block(&sh.cut, 0);
-    }
   }
-  if (by_search) {
+  if (cuts) {
     // ---- the general search.  First bins even in the logit over the range that has
     // mass, then bins even in the key, until one key is left
     int turn = 0;                                    // histogram in use; it is zero
+    unsigned low = top;                              // the lowest key above -inf
+    each([&](unsigned key, int) {
+      if (key > kKeyNegInf) low = min(low, key);
+    });
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (lane == 0) sh.warp_count[warp] = low;
+    sync_cluster(C);
+    if (tid < C * FW) low = *in_block(&sh.warp_count[tid % FW], tid / FW);
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (lane == 0) sh.red[0][warp] = low;
+    __syncthreads();
+    for (int w = 0; w < FW; ++w) low = min(low, sh.red[0][w]);
+    sync_cluster(C);                                 // warp_count has been read
     auto search = [&](auto keep) {
       const float range = fminf(ZERO_Z * t, row.top - key_logit(low));
       const float scale = range > 0.f ? 511.9f / range : 0.f;
-      auto first_bin = [&](float l) { return min(FT - 1, (int)((row.top - l) * scale)); };
+      auto first_bin = [&](unsigned key) { return min(FT - 1, (int)((row.top - key_logit(key)) * scale)); };
       unsigned n_above = 0, lo = 0, hi = 0;
       ull m_above = 0;
       int bin0 = -1, shift = 0;
       while (true) {
-        auto in = [&](int j, unsigned key) {
-          if (!cut.keeps(key, part.index(j))) return false;
-          return bin0 < 0 || (key >= lo && key <= hi && first_bin(part.x[j]) == bin0);
-        };
         // histogram
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const unsigned key = order_key(part.x[j]);
-          if (key > kKeyNegInf && in(j, key)) {
-            const ull m = mass_at(part.x[j]);
-            if (m) {
-              const int b = bin0 < 0 ? first_bin(part.x[j]) : (int)((hi - key) >> shift);
-              atomicAdd(&sh.count[turn][b], 1u);
-              atomicAdd(&sh.mass[turn][b], m);
-            }
-          }
-        }
+        each([&](unsigned key, int i) {
+          if (key <= kKeyNegInf || !cut.keeps(key, i)) return;
+          if (bin0 >= 0 && (key < lo || key > hi || first_bin(key) != bin0)) return;
+          const ull m = mass_at(key);
+          if (m == 0) return;
+          const int b = bin0 < 0 ? first_bin(key) : (int)((hi - key) >> shift);
+          atomicAdd(&sh.count[turn][b], 1u);
+          atomicAdd(&sh.mass[turn][b], m);
+        });
         sync_cluster(C);
         sh.count[turn ^ 1][tid] = 0;                 // the last turn's: every block has read it by now
         sh.mass[turn ^ 1][tid] = 0;
@@ -648,15 +723,12 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
           bin0 = (int)best;
           lo = 0xffffffffu;
           hi = 0;
-#pragma unroll
-          for (int j = 0; j < E; ++j) {
-            const unsigned key = order_key(part.x[j]);
-            if (key > kKeyNegInf && cut.keeps(key, part.index(j)) && first_bin(part.x[j]) == bin0 &&
-                mass_at(part.x[j])) {
+          each([&](unsigned key, int i) {
+            if (key > kKeyNegInf && cut.keeps(key, i) && first_bin(key) == bin0 && mass_at(key)) {
               lo = min(lo, key);
               hi = max(hi, key);
             }
-          }
+          });
           lo = __reduce_min_sync(0xffffffffu, lo);
           hi = __reduce_max_sync(0xffffffffu, hi);
           __syncthreads();
@@ -687,7 +759,7 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
         turn ^= 1;
         if (lo == hi) {
           // one key: how many of its n_equal tokens, lowest index first
-          const ull one = mass_at(key_logit(hi));
+          const ull one = mass_at(hi);
           unsigned least_n = 1, most = n_equal;
           while (least_n < most) {
             const unsigned mid = (least_n + most + 1) / 2;
@@ -700,11 +772,9 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
           }
           // the index of that token
           unsigned seen = 0;
-#pragma unroll
-          for (int j = 0; j < E; ++j) {
-            const unsigned key = order_key(part.x[j]);
-            seen += __popc(__ballot_sync(0xffffffffu, key == hi && cut.keeps(key, part.index(j))));
-          }
+          each([&](unsigned key, int i) {
+            seen += __popc(__ballot_sync(0xffffffffu, key == hi && cut.keeps(key, i)));
+          });
           sync_cluster(C);                           // warp_count is free
           if (lane == 0) sh.warp_count[warp] = seen;
           sync_cluster(C);
@@ -713,15 +783,13 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
           before = __reduce_add_sync(0xffffffffu, before);
           if (before < least_n && least_n <= before + seen) {
             unsigned at = before;
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-              const unsigned key = order_key(part.x[j]);
-              const bool mine = key == hi && cut.keeps(key, part.index(j));
+            each([&](unsigned key, int i) {
+              const bool mine = key == hi && cut.keeps(key, i);
               const unsigned eq = __ballot_sync(0xffffffffu, mine);
               if (mine && at + __popc(eq & ((2u << lane) - 1u)) == least_n)
-                for (int q = 0; q < C; ++q) *in_block(&sh.cut, q) = Place{hi, part.index(j)};
+                for (int q = 0; q < C; ++q) *in_block(&sh.cut, q) = Place{hi, i};
               at += __popc(eq);
-            }
+            });
           }
           sync_cluster(C);
           cut = sh.cut;
@@ -733,9 +801,9 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
     if (k > 0 && k < a.vocab) search([&](unsigned c, ull) { return c < (unsigned)k; });
     if (!(p >= 1.f)) {
       ull m = 0;
-#pragma unroll
-      for (int j = 0; j < E; ++j)
-        if (cut.keeps(order_key(part.x[j]), part.index(j))) m += mass_at(part.x[j]);
+      each([&](unsigned key, int i) {
+        if (cut.keeps(key, i)) m += mass_at(key);
+      });
       for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
       if (lane == 0) sh.warp_mass[warp] = m;
       sync_cluster(C);
@@ -751,15 +819,13 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
   }
 
   // ---- the draw: every warp's kept mass, then the warp in which the target falls
-  auto kept = [&](float l, int i) -> ull {
-    const unsigned key = order_key(l);
+  auto kept = [&](unsigned key, int i) -> ull {
     if (!cut.keeps(key, i) || key <= kKeyNegInf) return 0;
-    const float w = logit_weight(row, l);
-    return w >= least || key == top ? mass_of(w) : 0;
+    const float w = logit_weight(row, key_logit(key));
+    return w >= least || greedy ? mass_of(w) : 0;
   };
   ull m = 0;
-#pragma unroll
-  for (int j = 0; j < E; ++j) m += kept(part.x[j], part.index(j));
+  each([&](unsigned key, int i) { m += kept(key, i); });
   for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
   if (lane == 0) sh.warp_mass[warp] = m;
   sync_cluster(C);
@@ -778,10 +844,9 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
   ull before = sh.all[rank * FW + warp];
   if (before <= target && target < before + m) {
     bool found = false;
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const ull x = found ? 0 : kept(part.x[j], part.index(j));
-      if (!__any_sync(0xffffffffu, x != 0)) continue;
+    each([&](unsigned key, int i) {
+      const ull x = found ? 0 : kept(key, i);
+      if (!__any_sync(0xffffffffu, x != 0)) return;
       ull run = x;
       for (int o = 1; o < 32; o <<= 1) {
         const ull y = __shfl_up_sync(0xffffffffu, run, o);
@@ -789,21 +854,23 @@ __global__ void __launch_bounds__(FT, E <= 32 ? 2 : 1) sample_cluster_kernel(con
       }
       const unsigned past = __ballot_sync(0xffffffffu, before + run > target);
       if (past && lane == __ffs(past) - 1) {
-        a.token[r] = part.index(j);
+        a.token[r] = i;
         if (a.logprob)
-          a.logprob[r] = logit_z(row, part.x[j]) - logf((float)(__ull2double_rn(total) * 0x1p-40));
+          a.logprob[r] = logit_z(row, key_logit(key)) - logf((float)(__ull2double_rn(total) * 0x1p-40));
       }
       found = past != 0;
       before += __shfl_sync(0xffffffffu, run, 31);
-    }
+    });
   }
   if (C > 1) cluster_sync();                         // nobody leaves while its memory is read
 }
 
-template <typename T, int E>
-int launch_cluster(const SampleArgs& a, int C, cudaStream_t s) {
+template <typename T>
+int launch_cluster(const SampleArgs& a, int C, int Q, cudaStream_t s) {
+  constexpr int most = (int)sizeof(Cluster) + MAX_Q * FT * 16;
+  static_assert(most <= 227 * 1024, "shared memory");
   static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = set_smem_once(smem_set, sample_cluster_kernel<T, E>, (int)sizeof(Cluster));
+  cudaError_t e = set_smem_once(smem_set, sample_cluster_kernel<T>, most);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -814,11 +881,11 @@ int launch_cluster(const SampleArgs& a, int C, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)a.rows * (unsigned)C);
   cfg.blockDim = dim3(FT);
-  cfg.dynamicSmemBytes = sizeof(Cluster);
+  cfg.dynamicSmemBytes = sizeof(Cluster) + (size_t)Q * FT * 16;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, sample_cluster_kernel<T, E>, a, C);
+  e = cudaLaunchKernelEx(&cfg, sample_cluster_kernel<T>, a, C, Q);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -840,18 +907,13 @@ int launch(Kernel kernel, dim3 grid, const SampleArgs& a, cudaStream_t s) {
 
 template <typename T>
 int launch_any(const SampleArgs& a, cudaStream_t s) {
-  // the fewest logits a thread that fit a cluster of eight
-  auto blocks = [&](int E) {
-    int C = 1;
-    while (C * FT * E < a.vocab) C <<= 1;
-    return C;
-  };
-  if (a.rows <= 0x7fffffff / MAX_C) {
-    if (blocks(8) <= MAX_C) return launch_cluster<T, 8>(a, blocks(8), s);
-    if (blocks(32) <= MAX_C) return launch_cluster<T, 32>(a, blocks(32), s);
-    if (blocks(64) <= MAX_C) return launch_cluster<T, 64>(a, blocks(64), s);
-  }
-  return launch(sample_kernel<T>, dim3((unsigned)a.rows), a, s);
+  const long long most = (long long)MAX_C * FT * 4 * MAX_Q;
+  if (a.vocab > most || a.rows > 0x7fffffff / MAX_C)
+    return launch(sample_kernel<T>, dim3((unsigned)a.rows), a, s);
+  int C = 1;
+  while (C < MAX_C && C * FT * SAMPLE_Q * 4 < a.vocab) C <<= 1;
+  const int Q = (a.vocab + C * FT * 4 - 1) / (C * FT * 4);
+  return launch_cluster<T>(a, C, Q, s);
 }
 
 }  // namespace
