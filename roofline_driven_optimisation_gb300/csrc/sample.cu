@@ -53,6 +53,23 @@ struct Cut {
   int ties;
 };
 
+// The smallest whole number x with double(x) >= bound, so that m < x just when
+// double(m) < bound: one conversion in place of one a token (fp64 is slow here).
+__device__ __forceinline__ ull whole_bound(double bound) {
+  if (!(bound > 0.0)) return 0;
+  if (bound >= 0x1p63) return ~0ull;
+  ull x = __double2ull_ru(bound);
+  // from 2^53 on, numbers a little below may round up to the bound
+  while (x > 0 && __ull2double_rn(x - 1) >= bound) --x;
+  return x;
+}
+// floor(u * total) within 0 .. total - 1; u NaN or negative: 0
+__device__ __forceinline__ ull draw_target(float u, ull total) {
+  const double at = __dmul_rn((double)u, __ull2double_rn(total));
+  const ull target = at > 0.0 ? __double2ull_rz(at) : 0;
+  return target < total ? target : total - 1;
+}
+
 struct Shared {
   ull mass[256];
   unsigned count[256];
@@ -188,9 +205,9 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
       m = 0;
       for (int w = 0; w < WARPS; ++w) m += sh.warp_mass[w];
       if (cut.key > kKeyNegInf) m += (ull)cut.ties * mass_of(logit_weight(row, key_logit(cut.key)));
-      const double bound = __dmul_rn((double)p, __ull2double_rn(m));
+      const ull bound = whole_bound(__dmul_rn((double)p, __ull2double_rn(m)));
       const uint32_t key = search(logit, vocab, row, cut.key, [&](unsigned c, ull before) {
-        return c == 0 || __ull2double_rn(before) < bound;
+        return c == 0 || before < bound;
       }, sh, n_above, m_above, n_equal);
       // how many of the equal ones have less than the bound before them
       const ull one = key > kKeyNegInf ? mass_of(logit_weight(row, key_logit(key))) : 0;
@@ -198,7 +215,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
       if (key == cut.key) hi = min(hi, cut.ties);
       while (lo < hi) {   // the first always; the j-th (from 0) if before + j * one is below
         const int mid = (lo + hi + 1) / 2;
-        if (__ull2double_rn(m_above + (ull)(mid - 1) * one) < bound) lo = mid;
+        if (m_above + (ull)(mid - 1) * one < bound) lo = mid;
         else hi = mid - 1;
       }
       cut = Cut{key, lo};
@@ -240,9 +257,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     if (w < warp) before += sh.warp_mass[w];
     total += sh.warp_mass[w];
   }
-  const double at = __dmul_rn((double)u, __ull2double_rn(total));
-  ull target = at > 0.0 ? __double2ull_rz(at) : 0;   // NaN: 0
-  if (target >= total) target = total - 1;
+  const ull target = draw_target(u, total);
   if (before <= target && target < before + m) {     // one warp holds the token
     seen = ties_before;
     for (int i0 = from; i0 < to; i0 += 32) {
@@ -258,7 +273,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
           const int i = i0 + lane;
           a.token[r] = i;
           // greedy: T is one token's mass, and z is 0
-          if (a.logprob) a.logprob[r] = logit_z(row, logit(i)) - logf((float)(__ull2double_rn(total) * 0x1p-40));
+          if (a.logprob) a.logprob[r] = logit_z(row, logit(i)) - logf(__ull2float_rn(total) * 0x1p-40f);
         }
         break;
       }
@@ -278,7 +293,9 @@ constexpr int FT = 512, FW = FT / 32;         // threads and warps of a block
 constexpr int MAX_C = 8;
 constexpr int MAX_Q = 22;                     // quads of a thread: 8 * FT * 88 logits, 180 KB of keys
 constexpr int LIST = 2048;                    // candidates that the first block can sort
-constexpr int LOCAL = 1024;                   // candidates that a block can gather
+constexpr int LOCAL = 2048;                   // candidates that a block can gather
+constexpr int SMALL_K = 64;                   // largest top_k whose ranks fit two to a lane of one warp
+constexpr int SEG = LIST / MAX_C;             // a block's part of the list then
 constexpr int TOP_K_LIST = 1024;              // largest top_k for the candidate list: half of the 4 * FT groups
 constexpr int SAMPLE_Q = 4;                   // quads of a thread before a row takes more blocks
 constexpr float ZERO_Z = 28.f;                // expf(-28) < 2^-40: no mass
@@ -302,6 +319,9 @@ struct alignas(16) Cluster {
   unsigned top;             // read by the cluster
   unsigned lo[2], hi[2];    // read by the cluster, by turns
   unsigned list_n;          // first block: candidates of the cluster
+  unsigned seg_n[MAX_C];    // first block: of each block, in parts of the list
+  ull few[SMALL_K];         // the first ranks
+  ulonglong2 few_mass[SMALL_K];   // index, mass
   unsigned local_n, local_at;
   unsigned best, n_above;
   ull m_above;
@@ -355,7 +375,8 @@ __device__ __forceinline__ void sort_list(Cluster& sh, int n2) {
   if (n2 <= FT) {
     // a value a thread: steps within a warp by shuffles, others through shared
     // memory, in two buffers by turns
-    ull x = tid < n2 ? sh.list[tid] : 0;
+    if (tid < n2) {
+    ull x = sh.list[tid];
     ull* other = sh.local;
     for (int size = 2; size <= n2; size <<= 1)
       for (int step = size >> 1; step > 0; step >>= 1) {
@@ -364,7 +385,7 @@ __device__ __forceinline__ void sort_list(Cluster& sh, int n2) {
           y = __shfl_xor_sync(0xffffffffu, x, step);
         } else {
           other[tid] = x;
-          __syncthreads();
+          asm volatile("bar.sync 1, %0;" ::"r"(n2) : "memory");   // the warps that hold values
           y = other[tid ^ step];
           other = other == sh.local ? sh.local + FT : sh.local;
         }
@@ -372,8 +393,8 @@ __device__ __forceinline__ void sort_list(Cluster& sh, int n2) {
         const bool larger = ((tid & step) == 0) == ((tid & size) == 0);
         x = (x < y) == larger ? y : x;
       }
-    __syncthreads();
-    if (tid < n2) sh.list[tid] = x;
+    sh.list[tid] = x;
+    }
     __syncthreads();
     return;
   }
@@ -423,12 +444,17 @@ __device__ __forceinline__ void draw_from_list(const SampleArgs& a, Cluster& sh,
     }
     unsigned none = 0;
     block_prefix(sh, none, before);
-    const double bound = __dmul_rn((double)p, __ull2double_rn(totals()));
+    if (warp == 0) {
+      const ull x = whole_bound(__dmul_rn((double)p, __ull2double_rn(totals())));
+      if (lane == 0) sh.m_above = x;
+    }
+    __syncthreads();
+    const ull bound = sh.m_above;
     int ranks = 0;                                   // of this thread that top-p keeps
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int i = tid * PER + q;
-      if (i < kept && (i == 0 || __ull2double_rn(before) < bound)) ranks = i + 1;
+      if (i < kept && (i == 0 || before < bound)) ranks = i + 1;
       before += m[q];
     }
     ranks = __reduce_max_sync(0xffffffffu, ranks);
@@ -460,19 +486,164 @@ __device__ __forceinline__ void draw_from_list(const SampleArgs& a, Cluster& sh,
   unsigned none = 0;
   block_prefix(sh, none, before);
   const ull total = totals();
-  const double at = __dmul_rn((double)u, __ull2double_rn(total));
-  ull target = at > 0.0 ? __double2ull_rz(at) : 0;   // NaN: 0
-  if (target >= total) target = total - 1;
+  if (warp == 0) {
+    const ull x = draw_target(u, total);
+    if (lane == 0) sh.m_above = x;
+  }
+  __syncthreads();
+  const ull target = sh.m_above;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     if (before <= target && target < before + m[q]) {
       const ull x = sh.list[tid * PER + q];
       a.token[r] = (int)~(unsigned)(x >> 32);
       if (a.logprob)
-        a.logprob[r] = logit_z(row, key_logit((unsigned)x)) - logf((float)(__ull2double_rn(total) * 0x1p-40));
+        a.logprob[r] = logit_z(row, key_logit((unsigned)x)) - logf(__ull2float_rn(total) * 0x1p-40f);
     }
     before += m[q];
   }
+}
+
+// The bin of sh.count[0] in which the k-th count is, FT if there are fewer; one warp
+__device__ __forceinline__ unsigned kth_bin(const Cluster& sh, int k) {
+  constexpr int PER = FT / 32;
+  const int lane = threadIdx.x % 32;
+  unsigned c[PER], own = 0;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    c[q] = sh.count[0][lane * PER + q];
+    own += c[q];
+  }
+  unsigned before = own;
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  before -= own;
+  unsigned best = FT;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    if (before < (unsigned)k && before + c[q] >= (unsigned)k) best = lane * PER + q;
+    before += c[q];
+  }
+  return __reduce_min_sync(0xffffffffu, best);
+}
+
+// The same for k up to SMALL_K, with the candidates in the list's C parts: ranks by
+// counting, then one warp with two ranks a lane.
+__device__ __forceinline__ void draw_from_few(const SampleArgs& a, Cluster& sh, int r, int C, int k, float p, float least,
+                              float u, float t) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  int n = 0;
+  for (int c = 0; c < C; ++c) {
+    const int m = (int)sh.seg_n[c];
+    for (int i = tid; i < m; i += FT) sh.local[n + i] = sh.list[c * SEG + i];
+    n += m;
+  }
+  __syncthreads();
+  const ull* list = sh.local;
+  if (n > FT / 4) {
+    // far more than k of them: a histogram of all leaves the k first and their bin's
+    unsigned hi = 0, lo = 0xffffffffu;
+    for (int i = tid; i < n; i += FT) {
+      const unsigned key = (unsigned)(list[i] >> 32);
+      hi = max(hi, key);
+      lo = min(lo, key);
+    }
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    if (lane == 0) {
+      sh.red[0][warp] = hi;
+      sh.red[1][warp] = lo;
+    }
+    if (tid == 0) sh.local_n = 0;
+    __syncthreads();
+    hi = __reduce_max_sync(0xffffffffu, sh.red[0][lane % FW]);
+    lo = __reduce_min_sync(0xffffffffu, sh.red[1][lane % FW]);
+    const float ltop = key_logit(hi), range = ltop - key_logit(lo);
+    const float scale = range > 0.f && range < INFINITY ? 511.9f / range : 0.f;
+    auto bin = [&](ull x) { return min(FT - 1, (int)((ltop - key_logit((unsigned)(x >> 32))) * scale)); };
+    for (int i = tid; i < n; i += FT) atomicAdd(&sh.count[0][bin(list[i])], 1u);
+    __syncthreads();
+    if (warp == 0) {
+      const unsigned best = kth_bin(sh, k);
+      if (lane == 0) sh.best = best;
+    }
+    __syncthreads();
+    const int best = (int)sh.best;
+    for (int i = tid; i < n; i += FT) {
+      const ull x = list[i];
+      if (bin(x) <= best) sh.list[atomicAdd(&sh.local_n, 1u)] = x;
+    }
+    __syncthreads();
+    list = sh.list;
+    n = (int)sh.local_n;
+  }
+  // P lanes count how many candidates are larger than one of them
+  const int P = n <= FT / 16 ? 16 : n <= FT / 8 ? 8 : n <= FT / 4 ? 4 : n <= FT / 2 ? 2 : 1, part = tid % P;
+  for (int i0 = 0; i0 < n; i0 += FT / P) {
+    const int i = i0 + tid / P;
+    const ull x = i < n ? list[i] : ~0ull;
+    int larger = 0;
+#pragma unroll 4
+    for (int j = part; j < n; j += P) larger += list[j] > x;
+    for (int o = 1; o < P; o <<= 1) larger += __shfl_xor_sync(0xffffffffu, larger, o);
+    if (part == 0 && larger < k && i < n) sh.few[larger] = x;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  const int kept = min(n, k);
+  const ull x[2] = {lane < kept ? sh.few[lane] : 0, lane + 32 < kept ? sh.few[lane + 32] : 0};
+  const Row row{key_logit((unsigned)(sh.few[0] >> 32)), __fdiv_rn(1.f, t)};
+  ull m[2];
+  float z[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float l = key_logit((unsigned)(x[q] >> 32)), w = logit_weight(row, l);
+    z[q] = logit_z(row, l);
+    m[q] = x[q] == 0 ? 0 : mass_of(w);
+  }
+  auto prefix = [&](ull v) {                         // sum of the lower lanes' and this one's
+    for (int o = 1; o < 32; o <<= 1) {
+      const ull y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    return v;
+  };
+  int ranks = kept;
+  if (!(p >= 1.f)) {
+    const ull p0 = prefix(m[0]), all0 = __shfl_sync(0xffffffffu, p0, 31);
+    const ull p1 = all0 + prefix(m[1]), total = __shfl_sync(0xffffffffu, p1, 31);
+    const ull bound = whole_bound(__dmul_rn((double)p, __ull2double_rn(total)));
+    ranks = __popc(__ballot_sync(0xffffffffu, lane < kept && (lane == 0 || p0 - m[0] < bound))) +
+            __popc(__ballot_sync(0xffffffffu, lane + 32 < kept && p1 - m[1] < bound));
+  }
+  // min-p, and the running mass in index order
+  ull sum = 0;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int i = lane + 32 * q;
+    if (i >= ranks || !(logit_weight(row, key_logit((unsigned)(x[q] >> 32))) >= least)) m[q] = 0;
+    sh.few_mass[i] = make_ulonglong2((unsigned)~(unsigned)x[q], m[q]);
+    sum += m[q];
+  }
+  __syncwarp();
+  const ull total = __shfl_sync(0xffffffffu, prefix(sum), 31);
+  const ull target = draw_target(u, total);
+  ull before[2] = {0, 0};
+#pragma unroll 4
+  for (int j = 0; j < ranks; ++j) {
+    const ulonglong2 y = sh.few_mass[j];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if ((unsigned)y.x < (unsigned)~(unsigned)x[q]) before[q] += y.y;
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    if (before[q] <= target && target < before[q] + m[q]) {
+      a.token[r] = (int)~(unsigned)x[q];
+      if (a.logprob) a.logprob[r] = z[q] - logf(__ull2float_rn(total) * 0x1p-40f);
+    }
 }
 
 template <typename T>
@@ -538,16 +709,23 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
   }
   if (C > 1) cluster_arrive();                       // list_n is ready
 
-  // ---- the block's largest key
-  unsigned top = max(max(group[0], group[1]), max(group[2], group[3]));
+  // ---- the block's largest key, and its groups' smallest above -inf
+  unsigned top = max(max(group[0], group[1]), max(group[2], group[3])), gmin = 0xffffffffu;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) gmin = min(gmin, group[q] > kKeyNegInf ? group[q] : 0xffffffffu);
   top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) sh.red[0][warp] = top;
+  gmin = __reduce_min_sync(0xffffffffu, gmin);
+  if (lane == 0) {
+    sh.red[0][warp] = top;
+    sh.red[1][warp] = gmin;
+  }
   __syncthreads();
-  for (int w = 0; w < FW; ++w) top = max(top, sh.red[0][w]);
+  top = __reduce_max_sync(0xffffffffu, sh.red[0][lane % FW]);
+  gmin = __reduce_min_sync(0xffffffffu, sh.red[1][lane % FW]);
   if (tid == 0) sh.top = top;
 
   const bool cuts = !greedy && ((k > 0 && k < a.vocab) || !(p >= 1.f));
-  const bool by_list = cuts && k > 0 && k <= TOP_K_LIST;
+  const bool by_list = cuts && k > 0 && k <= TOP_K_LIST, small = k <= SMALL_K;
   if (by_list) {
     // ---- candidates for the first k ranks.  Every group's largest logit is an
     // element, so the k-th largest of them bounds the block's k-th rank from below;
@@ -556,62 +734,74 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
     const float ltop = key_logit(top);
     const unsigned floor_key =
         top <= kKeyNegInf ? 0xffffffffu : ltop == INFINITY ? top : max(kKeyNegInf + 1, order_key(ltop - ZERO_Z * t));
-    unsigned gmin = 0xffffffffu;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (group[q] >= floor_key) gmin = min(gmin, group[q]);
-    gmin = __reduce_min_sync(0xffffffffu, gmin);
-    __syncthreads();                                 // red has been read
-    if (lane == 0) sh.red[0][warp] = gmin;
-    __syncthreads();
-    for (int w = 0; w < FW; ++w) gmin = min(gmin, sh.red[0][w]);
     unsigned bound = floor_key;
-    if (gmin <= top) {
+    if (top > kKeyNegInf) {
       // bins even in the logit; an infinite range falls into one bin
       const float range = ltop - key_logit(gmin);
       const float scale = range > 0.f && range < INFINITY ? 511.9f / range : 0.f;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (group[q] >= gmin) atomicAdd(&sh.count[0][min(FT - 1, (int)((ltop - key_logit(group[q])) * scale))], 1u);
+        if (group[q] >= floor_key)
+          atomicAdd(&sh.count[0][min(FT - 1, (int)((ltop - key_logit(group[q])) * scale))], 1u);
       __syncthreads();
-      unsigned c = sh.count[0][tid];
-      ull none = 0;
-      const unsigned own = c;
-      block_prefix(sh, c, none);
-      if (tid == 0) sh.best = FT;
-      __syncthreads();
-      if (c < (unsigned)k && c + own >= (unsigned)k) sh.best = tid;
+      if (warp == 0) {
+        const unsigned best = kth_bin(sh, k);
+        if (lane == 0) sh.best = best;
+      }
       __syncthreads();
       // the lower edge of that bin, less what the bins' rounding may be off
-      if (sh.best < FT) bound = scale > 0.f ? max(gmin, order_key(ltop - (sh.best + 1.01f) / scale)) : gmin;
+      if (sh.best < FT)
+        bound = max(floor_key, scale > 0.f ? order_key(ltop - (sh.best + 1.01f) / scale) : gmin);
       sh.count[0][tid] = 0;
     }
-    each([&](unsigned key, int i) {
-      if (key >= bound) {
-        const unsigned at = atomicAdd(&sh.local_n, 1u);
-        if (at < LOCAL) sh.local[at] = ((ull)key << 32) | (unsigned)~i;
-      }
-    });
-    __syncthreads();
     if (C > 1) cluster_wait();
-    const unsigned n = sh.local_n;
-    if (tid == 0) sh.local_at = atomicAdd(in_block(&sh.list_n, 0), n > LOCAL ? LIST + 1u : n);
-    __syncthreads();
-    const unsigned at = sh.local_at;
-    if (n <= LOCAL && at + n <= LIST) {
-      ull* list = in_block(&sh.list[0], 0);
-      for (unsigned i = tid; i < n; i += FT) list[at + i] = sh.local[i];
+    ull* list = in_block(&sh.list[0], 0);
+    if (small) {
+      // straight into the first block's list, each block's in a part of its own
+      each([&](unsigned key, int i) {
+        if (key >= bound) {
+          const unsigned at = atomicAdd(&sh.local_n, 1u);
+          if (at < SEG) list[rank * SEG + at] = ((ull)key << 32) | (unsigned)~i;
+        }
+      });
+      __syncthreads();
+      if (tid == 0) *in_block(&sh.seg_n[rank], 0) = sh.local_n;
+    } else {
+      each([&](unsigned key, int i) {
+        if (key >= bound) {
+          const unsigned at = atomicAdd(&sh.local_n, 1u);
+          if (at < LOCAL) sh.local[at] = ((ull)key << 32) | (unsigned)~i;
+        }
+      });
+      __syncthreads();
+      const unsigned n = sh.local_n;
+      if (tid == 0) sh.local_at = atomicAdd(in_block(&sh.list_n, 0), n > LOCAL ? LIST + 1u : n);
+      __syncthreads();
+      const unsigned at = sh.local_at;
+      if (n <= LOCAL && at + n <= LIST)
+        for (unsigned i = tid; i < n; i += FT) list[at + i] = sh.local[i];
     }
   } else if (C > 1) {
     cluster_wait();
   }
   sync_cluster(C);
   if (by_list) {
-    const unsigned n = *in_block(&sh.list_n, 0);
-    if (n <= LIST) {
+    unsigned n = 0;
+    bool fits = true;
+    if (small) {
+      for (int c = 0; c < C; ++c) {
+        const unsigned x = *in_block(&sh.seg_n[c], 0);
+        n += x;
+        fits &= x <= SEG;
+      }
+    } else {
+      n = *in_block(&sh.list_n, 0);
+      fits = n <= LIST;
+    }
+    if (fits) {
       // the first block has all there is to choose from
       if (rank != 0) {
-        cluster_arrive();                            // it has been read; nobody reads this block
+        cluster_arrive();                            // its counts have been read; nobody reads this block
         return;
       }
       if (n == 0) {
@@ -619,6 +809,8 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
           a.token[r] = -1;
           if (a.logprob) a.logprob[r] = -INFINITY;
         }
+      } else if (small) {
+        draw_from_few(a, sh, r, C, k, p, least, u, t);
       } else {
         draw_from_list(a, sh, r, (int)n, k, p, least, u, t);
       }
@@ -812,9 +1004,9 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
       block_prefix(sh, none, m);
       ull total = 0;
       for (int w = 0; w < FW; ++w) total += sh.scan_m[w];
-      const double bound = __dmul_rn((double)p, __ull2double_rn(total));
+      const ull bound = whole_bound(__dmul_rn((double)p, __ull2double_rn(total)));
       sync_cluster(C);                               // warp_mass has been read
-      search([&](unsigned c, ull before) { return c == 0 || __ull2double_rn(before) < bound; });
+      search([&](unsigned c, ull before) { return c == 0 || before < bound; });
     }
   }
 
@@ -838,9 +1030,12 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
   __syncthreads();
   ull total = 0;
   for (int w = 0; w < FW; ++w) total += sh.scan_m[w];
-  const double at = __dmul_rn((double)u, __ull2double_rn(total));
-  ull target = at > 0.0 ? __double2ull_rz(at) : 0;   // NaN: 0
-  if (target >= total) target = total - 1;
+  if (warp == 0) {
+    const ull x = draw_target(u, total);
+    if (lane == 0) sh.m_above = x;
+  }
+  __syncthreads();
+  const ull target = sh.m_above;
   ull before = sh.all[rank * FW + warp];
   if (before <= target && target < before + m) {
     bool found = false;
@@ -856,7 +1051,7 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
       if (past && lane == __ffs(past) - 1) {
         a.token[r] = i;
         if (a.logprob)
-          a.logprob[r] = logit_z(row, key_logit(key)) - logf((float)(__ull2double_rn(total) * 0x1p-40));
+          a.logprob[r] = logit_z(row, key_logit(key)) - logf(__ull2float_rn(total) * 0x1p-40f);
       }
       found = past != 0;
       before += __shfl_sync(0xffffffffu, run, 31);
