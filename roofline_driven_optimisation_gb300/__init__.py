@@ -83,6 +83,8 @@ def build(force: bool = False) -> str:
 def load(path: str | None = None):
     """Load the C library (built in-tree by ``build()``) and declare signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -503,29 +505,42 @@ class KVCache:
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), k.stride(0),
             k.stride(1), max(k.stride(2), dim), max(table.stride(0), table.shape[1]), fmts[k.dtype], pages,
             page_tokens, heads, dim, table.shape[0], table.shape[1])
+        self.address, self.index = ctypes.addressof(self.struct), k.device.index
 
     def rows(self, n: int) -> "KVCache":
         return KVCache(self.k, self.v, self.k_scale, self.v_scale, self.table[:n], self.struct.format)
 
 
+def _torch():
+    """torch, and the types that the calls below compare with (looked up once)."""
+    global _t, _bf16, _f32, _i32, _raw_stream
+    import torch
+    _t, _bf16, _f32, _i32 = torch, torch.bfloat16, torch.float32, torch.int32
+    # the current stream's handle without a Stream object around it
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return torch
+
+
+_t = _bf16 = _f32 = _i32 = _raw_stream = None
+
+
 def _heads(t, name: str, heads: int, dim: int, tokens: int) -> int:
     """Elements between the rows of a bf16 CUDA tensor [tokens][heads][dim] whose
     heads lie side by side."""
-    import torch
-    if t.dtype != torch.bfloat16 or not t.is_cuda:
+    if t.dtype is not _bf16 or not t.is_cuda:
         raise TypeError(f"{name} is a bf16 CUDA tensor")
-    if tuple(t.shape) != (tokens, heads, dim):
+    if t.shape != (tokens, heads, dim):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {(tokens, heads, dim)}")
-    s = t.stride()
-    if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
+    row, head, one = t.stride()
+    if (one != 1 and dim > 1) or (head != dim and heads > 1):
         raise ValueError(f"{name}: a row's heads lie side by side")
-    return max(s[0], heads * dim)
+    return row if row > heads * dim else heads * dim
 
 
-def _ints(t, name: str, n: int) -> int:
-    import torch
-    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise TypeError(f"{name} is a contiguous int32 CUDA tensor of {n} values")
+def _values(t, name: str, n: int, dtype) -> int:
+    if t.dtype is not dtype or not t.is_cuda or t.shape != (n,) or not t.is_contiguous():
+        raise TypeError(f"{name} is a contiguous {dtype} CUDA tensor of {n} values")
     return t.data_ptr()
 
 
@@ -537,26 +552,32 @@ def kv_append(cache: KVCache, Q, K, V, cos, sin, base, Qout=None, start=None, ma
     and sin (fp32 [positions][pairs]; None: no rotation).  Sequence b's rows are
     start[b] .. start[b+1]-1, at most max_new (start None: row b).  Argument
     marshalling only."""
-    import torch
-    tokens, H, D = K.shape
-    ldk, ldv = _heads(K, "K", cache.heads, cache.dim, tokens), _heads(V, "V", cache.heads, cache.dim, tokens)
+    if _t is None:
+        _torch()
+    H, D, seqs = cache.heads, cache.dim, cache.seqs
+    tokens = K.shape[0]
+    ldk, ldv = _heads(K, "K", H, D, tokens), _heads(V, "V", H, D, tokens)
     Hq = ldq = ldo = q = o = 0
     if Q is not None:
-        Qout = Q if Qout is None else Qout
+        if Qout is None:
+            Qout = Q
         Hq = Q.shape[1]
         ldq, ldo = _heads(Q, "Q", Hq, D, tokens), _heads(Qout, "Qout", Hq, D, tokens)
         q, o = Q.data_ptr(), Qout.data_ptr()
     positions, pairs, c, s = 0x7fffffff, 0, 0, 0
     if cos is not None:
-        if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape or \
+        if cos.dtype is not _f32 or sin.dtype is not _f32 or cos.dim() != 2 or cos.shape != sin.shape or \
                 not (cos.is_cuda and sin.is_cuda and cos.is_contiguous() and sin.is_contiguous()):
             raise TypeError("cos and sin are contiguous fp32 CUDA tensors [positions][pairs]")
         positions, pairs = cos.shape
         c, s = cos.data_ptr(), sin.data_ptr()
-    st = stream if stream is not None else torch.cuda.current_stream(cache.device).cuda_stream
-    gemm_kv_append(cache.struct, tokens, Hq, q, ldq, K.data_ptr(), ldk, V.data_ptr(), ldv, o, ldo, c, s, positions,
-                   2 * pairs, int(interleaved), _ints(base, "base", cache.seqs),
-                   None if start is None else _ints(start, "start", cache.seqs + 1), int(max_new), st)
+    rc = (_lib or load()).gemm_kv_append(
+        cache.address, tokens, Hq, q, ldq, K.data_ptr(), ldk, V.data_ptr(), ldv, o, ldo, c, s, positions, 2 * pairs,
+        interleaved, _values(base, "base", seqs, _i32),
+        None if start is None else _values(start, "start", seqs + 1, _i32), max_new,
+        _raw_stream(cache.index) if stream is None else stream)
+    if rc:
+        _check(rc)
     return Qout
 
 
@@ -566,14 +587,13 @@ _kv_workspaces: dict = {}
 
 
 def _kv_workspace(device, stream: int, size: int):
-    import torch
     key = (device.index, stream)
     w = _kv_workspaces.get(key)
     if w is None or w.numel() < size:
         # made on the stream that uses it, so that the zeros are there before
         # the call and the old one's memory is not reused before its last call
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-            w = torch.zeros((max(size, 1 << 20),), dtype=torch.uint8, device=device)
+        with _t.cuda.stream(_t.cuda.ExternalStream(stream, device=device)):
+            w = _t.zeros((max(size, 1 << 20),), dtype=_t.uint8, device=device)
         _kv_workspaces[key] = w
     return w
 
@@ -587,17 +607,21 @@ def kv_attention(cache: KVCache, Q, O, lengths, start=None, max_new: int = 1, sc
     sees keys j <= lengths[b] - n + i.  workspace: zeroed uint8 tensor of
     gemm_kv_attention_workspace() bytes, or None for one that this module keeps
     for the stream.  Argument marshalling only."""
-    import torch
-    tokens, Hq, D = Q.shape
-    ldq, ldo = _heads(Q, "Q", Hq, cache.dim, tokens), _heads(O, "O", Hq, cache.dim, tokens)
-    st = stream if stream is not None else torch.cuda.current_stream(cache.device).cuda_stream
+    if _t is None:
+        _torch()
+    D, seqs = cache.dim, cache.seqs
+    tokens, Hq = Q.shape[0], Q.shape[1]
+    ldq, ldo = _heads(Q, "Q", Hq, D, tokens), _heads(O, "O", Hq, D, tokens)
+    st = _raw_stream(cache.index) if stream is None else stream
+    lib = _lib or load()
     if workspace is None:
-        need = gemm_kv_attention_workspace(cache.seqs, cache.heads, Hq, cache.dim, max_new)
-        workspace = _kv_workspace(cache.device, st, need)
-    gemm_kv_attention(cache.struct, tokens, Hq, Q.data_ptr(), ldq, O.data_ptr(), ldo,
-                      _ints(lengths, "lengths", cache.seqs),
-                      None if start is None else _ints(start, "start", cache.seqs + 1), int(max_new), float(scale),
-                      workspace.data_ptr(), workspace.numel(), st)
+        workspace = _kv_workspace(cache.device, st, lib.gemm_kv_attention_workspace(seqs, cache.heads, Hq, D, max_new))
+    rc = lib.gemm_kv_attention(
+        cache.address, tokens, Hq, Q.data_ptr(), ldq, O.data_ptr(), ldo, _values(lengths, "lengths", seqs, _i32),
+        None if start is None else _values(start, "start", seqs + 1, _i32), max_new, scale, workspace.data_ptr(),
+        workspace.numel(), st)
+    if rc:
+        _check(rc)
     return O
 
 
@@ -606,26 +630,26 @@ def sample(logits, u, token, logprob=None, temperature=None, top_k=None, top_p=N
     uniform numbers u: token (int32) and, if given, its log-probability among the
     kept.  temperature, top_p, min_p (fp32) and top_k (int32) are CUDA tensors of
     one value a row, or None (1, off).  Argument marshalling only."""
-    import torch
+    if _t is None:
+        _torch()
     rows, vocab = logits.shape
-
-    def of(t, name, dtype):
-        if t is None:
-            return None
-        if t.dtype != dtype or not t.is_cuda or t.dim() != 1 or t.shape[0] != rows or not t.is_contiguous():
-            raise TypeError(f"{name} is a contiguous {dtype} CUDA tensor of one value a row")
-        return t.data_ptr()
     if not logits.is_cuda:
         raise ValueError("sample() takes CUDA tensors")
-    f32, i32 = torch.float32, torch.int32
-    s = stream if stream is not None else torch.cuda.current_stream(logits.device).cuda_stream
-    args = (rows, vocab, logits.data_ptr(), _ld(logits), of(temperature, "temperature", f32), of(top_k, "top_k", i32),
-            of(top_p, "top_p", f32), of(min_p, "min_p", f32), of(u, "u", f32), of(token, "token", i32),
-            of(logprob, "logprob", f32), s)
-    if logits.dtype == torch.bfloat16:
-        gemm_sample_bf16(*args)
-    elif logits.dtype == f32:
-        gemm_sample_f32(*args)
+    lib = _lib or load()
+    if logits.dtype is _bf16:
+        fn = lib.gemm_sample_bf16
+    elif logits.dtype is _f32:
+        fn = lib.gemm_sample_f32
     else:
         raise TypeError(f"unsupported logits dtype {logits.dtype}")
+    rc = fn(rows, vocab, logits.data_ptr(), _ld(logits),
+            None if temperature is None else _values(temperature, "temperature", rows, _f32),
+            None if top_k is None else _values(top_k, "top_k", rows, _i32),
+            None if top_p is None else _values(top_p, "top_p", rows, _f32),
+            None if min_p is None else _values(min_p, "min_p", rows, _f32),
+            _values(u, "u", rows, _f32), _values(token, "token", rows, _i32),
+            None if logprob is None else _values(logprob, "logprob", rows, _f32),
+            _raw_stream(logits.device.index) if stream is None else stream)
+    if rc:
+        _check(rc)
     return token

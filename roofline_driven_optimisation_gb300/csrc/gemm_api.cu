@@ -760,7 +760,13 @@ int kv_append(const gemm_kv_cache* cache, int tokens, int Hq, const void* Q, lon
   a.base = base; a.start = start;
   a.max_new = max_new;
   a.status = dev->status;
-  const bool fast = false;
+  // 16-byte accesses to rows, angles and codes
+  const KvCache& c = a.c;
+  const bool fast = (D == 64 || D == 128) && rotated == D && (c.P == 16 || c.P == 32 || c.P == 64 || c.P == 128) &&
+                    aligned16(c.k) && aligned16(c.v) && (c.ps | c.hs | c.ts) % 16 == 0 && aligned16(K) && aligned16(V) &&
+                    ldk % 8 == 0 && ldv % 8 == 0 && aligned16(cosine) && aligned16(sine) &&
+                    (Hq == 0 || (aligned16(Q) && aligned16(Qout) && ldq % 8 == 0 && ldqo % 8 == 0)) &&
+                    t_forced_path != GEMM_PATH_GENERIC;
   const int err = launch_kv_append(a, fast, dev->num_sms, stream);
   if (err != cudaSuccess)
     return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));

@@ -28,57 +28,62 @@ struct Item {
   int pos0, col;      // position of that row; the page's column in the table
 };
 
-// Finds item number i: items count the pages that each sequence writes, in
-// sequence order.  Called by the whole block (blockDim.x a multiple of 32, at
-// most 1024).  False when there is no such item.
+// Finds item number i: items count the pages that each sequence writes, in sequence
+// order.  Called by the whole block; the first warp looks, four sequences a lane.
+// False when there is no such item.
 __device__ bool find_item(const KvAppendArgs& a, int i, Item& out) {
-  __shared__ int warp_sum[32];
   __shared__ Item found;
   __shared__ int found_flag;
-  const int P = a.c.P;
-  if (threadIdx.x == 0) found_flag = 0;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
-  int before = 0;
-  for (int b0 = 0; b0 < a.c.seqs; b0 += blockDim.x) {
-    const int b = b0 + threadIdx.x;
-    int first = 0, n = 0, base = 0, count = 0;
-    if (b < a.c.seqs) {
-      kv_rows(a.start, b, a.tokens, a.max_new, a.status, kSiteKvAppend, first, n);
-      if (n > 0) {
-        base = a.base[b];
-        // positions base .. base+n-1 must exist in the tables of angles
-        if (base < 0 || base > a.positions - n) {
-          report_status(a.status, 1, kSiteKvAppend);
-          n = 0;
-        } else {
-          count = (base + n - 1) / P - base / P + 1;
+  constexpr int PER = 4;
+  if (threadIdx.x < 32) {
+    const int P = a.c.P, lane = threadIdx.x;
+    int before = 0;
+    bool hit = false;
+    for (int b0 = 0; b0 < a.c.seqs && !hit && before <= i; b0 += 32 * PER) {
+      int first[PER], n[PER], base[PER], count[PER], own = 0;
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const int b = b0 + lane * PER + q;
+        first[q] = n[q] = base[q] = count[q] = 0;
+        if (b < a.c.seqs) {
+          base[q] = a.base[b];
+          kv_rows(a.start, b, a.tokens, a.max_new, a.status, kSiteKvAppend, first[q], n[q]);
         }
       }
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        if (n[q] > 0) {
+          // positions base .. base+n-1 must exist in the tables of angles
+          if (base[q] < 0 || base[q] > a.positions - n[q]) report_status(a.status, 1, kSiteKvAppend);
+          else count[q] = (base[q] + n[q] - 1) / P - base[q] / P + 1;
+        }
+        own += count[q];
+      }
+      int excl = own;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, excl, o);
+        if (lane >= o) excl += t;
+      }
+      const int all = __shfl_sync(0xffffffffu, excl, 31);
+      excl += before - own;
+      bool mine = false;
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        if (count[q] > 0 && i >= excl && i < excl + count[q]) {
+          found.b = b0 + lane * PER + q;
+          found.col = base[q] / P + (i - excl);
+          const int lo = max(base[q], found.col * P), hi = min(base[q] + n[q], (found.col + 1) * P);
+          found.row0 = first[q] + (lo - base[q]);
+          found.n = hi - lo;
+          found.pos0 = lo;
+          mine = true;
+        }
+        excl += count[q];
+      }
+      hit = __any_sync(0xffffffffu, mine);
+      before += all;
     }
-    int incl = count;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    __syncthreads();   // the previous round's readers are done with warp_sum
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int excl = before + incl - count, all = before;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) excl += warp_sum[w];
-      all += warp_sum[w];
-    }
-    if (count > 0 && i >= excl && i < excl + count) {
-      found.b = b;
-      found.col = base / P + (i - excl);
-      const int lo = max(base, found.col * P), hi = min(base + n, (found.col + 1) * P);
-      found.row0 = first + (lo - base);
-      found.n = hi - lo;
-      found.pos0 = lo;
-      found_flag = 1;
-    }
-    before = all;
-    if (before > i) break;
+    if (lane == 0) found_flag = hit;
   }
   __syncthreads();
   out = found;
@@ -181,8 +186,326 @@ __global__ void __launch_bounds__(128) kv_append_generic_kernel(const KvAppendAr
   if (threadIdx.x == 0) *scale = s;
 }
 
-template <class Kernel>
-int launch(Kernel kernel, dim3 grid, dim3 block, const KvAppendArgs& a, cudaStream_t s) {
+// ------------------------------------------------------------------ fast
+// D 64 or 128, whole heads turned, pages of 16 to 128 tokens, rows on 16 bytes.
+// The bound is HBM (2 bytes in and 1 or 2 out a value); what a kernel has to do is
+// read each value once, with enough loads in flight, and keep it until its page's
+// scale is known.
+
+// eight bf16 as floats
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <int FMT>
+__device__ __forceinline__ uint2 codes8(const float* x, float r) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = kv_code2<FMT>(__fmul_rn(x[4 * i], r), __fmul_rn(x[4 * i + 1], r)) |
+           (kv_code2<FMT>(__fmul_rn(x[4 * i + 2], r), __fmul_rn(x[4 * i + 3], r)) << 16);
+  return make_uint2(w[0], w[1]);
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t recode4(uint32_t c, float s0, float r) {
+  const float2 a = kv_value2<FMT>(c & 0xffffu), b = kv_value2<FMT>(c >> 16);
+  return kv_code2<FMT>(__fmul_rn(__fmul_rn(a.x, s0), r), __fmul_rn(__fmul_rn(a.y, s0), r)) |
+         (kv_code2<FMT>(__fmul_rn(__fmul_rn(b.x, s0), r), __fmul_rn(__fmul_rn(b.y, s0), r)) << 16);
+}
+
+// A few tokens a sequence, MAXT at most (a decode step, drafted tokens): a warp for
+// each sequence, page and head with the tokens in registers, so that the latency of a
+// call is one chain of loads, and no block waits.
+constexpr int DEC_WARPS = 4;
+
+template <int FMT, int D, int MAXT>
+__global__ void __launch_bounds__(DEC_WARPS * 32) kv_append_tokens_kernel(const KvAppendArgs a, const int pages) {
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  constexpr int PP = D / 64;                       // pairs of a lane
+  const int lane = threadIdx.x % 32, hh = blockIdx.x * DEC_WARPS + threadIdx.x / 32;
+  const int b = pages == 1 ? blockIdx.y : blockIdx.y / pages, nth = blockIdx.y - b * pages;   // its nth page
+  if (hh >= a.Hq + 2 * a.c.H) return;
+  const int kind = hh < a.Hq ? 0 : hh < a.Hq + a.c.H ? 1 : 2;
+  const int h = kind == 0 ? hh : (hh - a.Hq) - (kind - 1) * a.c.H;
+  const int base = a.base[b];
+  int first, all;
+  kv_rows(a.start, b, a.tokens, a.max_new, a.status, kSiteKvAppend, first, all);
+  if (all == 0) return;
+  if (base < 0 || base > a.positions - all) {
+    report_status(a.status, 1, kSiteKvAppend);
+    return;
+  }
+  const int col = base / a.c.P + nth, pos = max(base, col * a.c.P);       // the part in this page
+  const int n = min(base + all, (col + 1) * a.c.P) - pos, held = pos - col * a.c.P;
+  if (n <= 0) return;
+  const int row = first + (pos - base);
+  const long long ld = kind == 0 ? a.ldq : kind == 1 ? a.ldk : a.ldv;
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(kind == 0 ? a.Q : kind == 1 ? a.K : a.V) +
+                             (long long)row * ld + (long long)h * D;
+  // values d0 .., d1 ..: PP each; a pair of the rotation, or neighbours
+  const bool halves = kind != 2 && !a.interleaved;
+  const int d0 = halves ? lane * PP : lane * 2 * PP, d1 = halves ? d0 + D / 2 : d0 + PP;
+  float x[MAXT][2 * PP];
+#pragma unroll
+  for (int t = 0; t < MAXT; ++t) {
+#pragma unroll
+    for (int i = 0; i < 2 * PP; ++i) x[t][i] = 0.f;
+    if (t >= n) continue;
+    const __nv_bfloat16* p = src + t * ld;
+    if constexpr (PP == 2) {
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(p + d0), v = *reinterpret_cast<const uint32_t*>(p + d1);
+      x[t][0] = __uint_as_float(u << 16);
+      x[t][1] = __uint_as_float(u & 0xffff0000u);
+      x[t][2] = __uint_as_float(v << 16);
+      x[t][3] = __uint_as_float(v & 0xffff0000u);
+    } else {
+      x[t][0] = __bfloat162float(p[d0]);
+      x[t][1] = __bfloat162float(p[d1]);
+    }
+  }
+  // the page and its scale while the rows arrive
+  const int g = kind == 0 ? 0 : kv_page(a.c, b, col, a.status, kSiteKvAppend);
+  if (g < 0) return;
+  float* scale = (kind == 1 ? a.c.ks : a.c.vs) + (long long)g * a.c.H + h;
+  const float s0 = kind != 0 && held > 0 ? *scale : 0.f;
+  if (kind != 2) {
+    // halves: pairs (x[i], x[PP + i]); interleaved: (x[2i], x[2i + 1])
+#pragma unroll
+    for (int t = 0; t < MAXT; ++t) {
+      if (t >= n) continue;
+      const long long at = (long long)(pos + t) * (D / 2) + lane * PP;
+#pragma unroll
+      for (int i = 0; i < PP; ++i) {
+        const float c = a.cos[at + i], s = a.sin[at + i];
+        float& p = halves ? x[t][i] : x[t][2 * i];
+        float& q = halves ? x[t][PP + i] : x[t][2 * i + 1];
+        const float2 y = turn(p, q, c, s);
+        p = y.x;
+        q = y.y;
+      }
+    }
+  }
+  if (kind == 0) {
+#pragma unroll
+    for (int t = 0; t < MAXT; ++t) {
+      if (t >= n) continue;
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.Qo) + (long long)(row + t) * a.ldqo + (long long)h * D;
+      if constexpr (PP == 2) {
+        *reinterpret_cast<uint32_t*>(o + d0) = pack2(x[t][0], x[t][1]);
+        *reinterpret_cast<uint32_t*>(o + d1) = pack2(x[t][2], x[t][3]);
+      } else {
+        o[d0] = __float2bfloat16_rn(x[t][0]);
+        o[d1] = __float2bfloat16_rn(x[t][1]);
+      }
+    }
+    return;
+  }
+  uint8_t* codes = (kind == 1 ? a.c.k : a.c.v) + (long long)g * a.c.ps + (long long)h * a.c.hs;
+  float m = 0.f;
+#pragma unroll
+  for (int t = 0; t < MAXT; ++t)
+#pragma unroll
+    for (int i = 0; i < 2 * PP; ++i) m = fmaxf(m, fabsf(x[t][i]));
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  const float s = fmaxf(s0, kv_scale_for<FMT>(m)), r = kv_recip(s);
+#pragma unroll
+  for (int t = 0; t < MAXT; ++t) {
+    if (t >= n) continue;
+    uint8_t* o = codes + (long long)(held + t) * a.c.ts;
+    if constexpr (PP == 2) {
+      *reinterpret_cast<uint16_t*>(o + d0) = (uint16_t)kv_code2<FMT>(__fmul_rn(x[t][0], r), __fmul_rn(x[t][1], r));
+      *reinterpret_cast<uint16_t*>(o + d1) = (uint16_t)kv_code2<FMT>(__fmul_rn(x[t][2], r), __fmul_rn(x[t][3], r));
+    } else {
+      const uint32_t c = kv_code2<FMT>(__fmul_rn(x[t][0], r), __fmul_rn(x[t][1], r));
+      o[d0] = (uint8_t)c;
+      o[d1] = (uint8_t)(c >> 8);
+    }
+  }
+  if (s > s0 && held > 0) {
+    constexpr int LANES = D / 4;                   // lanes of a row of codes
+    const int sub = lane / LANES, at = lane % LANES * 4;
+#pragma unroll 4
+    for (int t = sub; t < held; t += 32 / LANES) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(codes + (long long)t * a.c.ts + at);
+      *w = recode4<FMT>(*w, s0, r);
+    }
+  }
+  if (lane == 0) *scale = s;
+}
+
+// Prompts: a block holds one item of HG heads in registers, 16 values of a row a
+// thread (a pair of octets that turn together, or neighbours), TPT rows a thread;
+// the angles are read once for all heads of the block.
+constexpr int HG = 2;
+
+template <int FMT, int D, int TPT>
+__global__ void __launch_bounds__(512, TPT == 1 ? 2 : 1) kv_append_pages_kernel(const KvAppendArgs a, const int rounds) {
+  __shared__ unsigned big[HG];
+  constexpr int CH = D / 16;
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  if (threadIdx.x < HG) big[threadIdx.x] = 0;
+  Item it;
+  if (!find_item(a, blockIdx.x, it)) return;
+  const int qg = (a.Hq + HG - 1) / HG, kg = (a.c.H + HG - 1) / HG;   // groups of query and of key heads
+  const int t0 = threadIdx.x / CH, c = threadIdx.x % CH, step = blockDim.x / CH;
+  const int held = it.pos0 % a.c.P;
+  float co[TPT][8], si[TPT][8];
+  bool angles = false;
+  int g = -2;                                      // the page, not looked up yet
+  for (int round = 0; round < rounds; ++round) {
+    const int gr = blockIdx.y * rounds + round;
+    if (gr >= qg + 2 * kg) return;
+    const int kind = gr < qg ? 0 : gr < qg + kg ? 1 : 2;
+    const int h0 = (kind == 0 ? gr : gr - qg - (kind - 1) * kg) * HG, heads = min(HG, (kind == 0 ? a.Hq : a.c.H) - h0);
+    const bool halves = kind != 2 && !a.interleaved;
+    const int d0 = halves ? c * 8 : c * 16, d1 = halves ? d0 + D / 2 : d0 + 8;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(kind == 0 ? a.Q : kind == 1 ? a.K : a.V);
+    const long long ld = kind == 0 ? a.ldq : kind == 1 ? a.ldk : a.ldv;
+    uint4 u[HG][TPT], v[HG][TPT];
+#pragma unroll
+    for (int h = 0; h < HG; ++h)
+#pragma unroll
+      for (int q = 0; q < TPT; ++q) {
+        const int t = t0 + q * step;
+        u[h][q] = v[h][q] = make_uint4(0u, 0u, 0u, 0u);
+        if (h < heads && t < it.n) {
+          const __nv_bfloat16* x = src + (long long)(it.row0 + t) * ld + (long long)(h0 + h) * D;
+          u[h][q] = *reinterpret_cast<const uint4*>(x + d0);
+          v[h][q] = *reinterpret_cast<const uint4*>(x + d1);
+        }
+      }
+    if (kind != 2 && !angles) {
+      angles = true;
+#pragma unroll
+      for (int q = 0; q < TPT; ++q) {
+        const int t = min(t0 + q * step, it.n - 1);
+        const long long at = (long long)(it.pos0 + t) * (D / 2) + c * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          *reinterpret_cast<float4*>(&co[q][4 * i]) = *reinterpret_cast<const float4*>(a.cos + at + 4 * i);
+          *reinterpret_cast<float4*>(&si[q][4 * i]) = *reinterpret_cast<const float4*>(a.sin + at + 4 * i);
+        }
+      }
+    }
+    // the 16 values, turned
+    auto values = [&](int h, int q, float (&x)[16]) {
+      float p[8], w[8];
+      unpack8(u[h][q], p);
+      unpack8(v[h][q], w);
+      if (kind == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = p[i];
+          x[8 + i] = w[i];
+        }
+      } else if (halves) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 y = turn(p[i], w[i], co[q][i], si[q][i]);
+          x[i] = y.x;
+          x[8 + i] = y.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = turn(p[2 * i], p[2 * i + 1], co[q][i], si[q][i]);
+          const float2 z = turn(w[2 * i], w[2 * i + 1], co[q][4 + i], si[q][4 + i]);
+          x[2 * i] = y.x;
+          x[2 * i + 1] = y.y;
+          x[8 + 2 * i] = z.x;
+          x[9 + 2 * i] = z.y;
+        }
+      }
+    };
+    if (kind == 0) {
+#pragma unroll
+      for (int h = 0; h < HG; ++h)
+#pragma unroll
+        for (int q = 0; q < TPT; ++q) {
+          const int t = t0 + q * step;
+          if (h >= heads || t >= it.n) continue;
+          float x[16];
+          values(h, q, x);
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.Qo) + (long long)(it.row0 + t) * a.ldqo +
+                             (long long)(h0 + h) * D;
+          *reinterpret_cast<uint4*>(o + d0) =
+              make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+          *reinterpret_cast<uint4*>(o + d1) =
+              make_uint4(pack2(x[8], x[9]), pack2(x[10], x[11]), pack2(x[12], x[13]), pack2(x[14], x[15]));
+        }
+      continue;
+    }
+    if (g == -2) g = kv_page(a.c, it.b, it.col, a.status, kSiteKvAppend);
+    if (g < 0) return;                             // the same for the whole block; no queries follow
+    float* scale = (kind == 1 ? a.c.ks : a.c.vs) + (long long)g * a.c.H + h0;
+    float s0[HG];
+#pragma unroll
+    for (int h = 0; h < HG; ++h) s0[h] = held > 0 && h < heads ? scale[h] : 0.f;
+#pragma unroll
+    for (int h = 0; h < HG; ++h) {
+      float m = 0.f;
+#pragma unroll
+      for (int q = 0; q < TPT; ++q) {
+        float x[16];
+        values(h, q, x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
+      }
+      // magnitudes order as their bits; the atomic is a maximum, so its order is free
+      const unsigned w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+      if (threadIdx.x % 32 == 0) atomicMax(&big[h], w);
+    }
+    __syncthreads();
+    float s[HG];
+#pragma unroll
+    for (int h = 0; h < HG; ++h) s[h] = fmaxf(s0[h], kv_scale_for<FMT>(__uint_as_float(big[h])));
+    __syncthreads();                               // big has been read, and every old scale
+    if (threadIdx.x < HG) big[threadIdx.x] = 0;
+    uint8_t* codes = (kind == 1 ? a.c.k : a.c.v) + (long long)g * a.c.ps + (long long)h0 * a.c.hs;
+#pragma unroll
+    for (int h = 0; h < HG; ++h) {
+      if (h >= heads) break;
+      const float r = kv_recip(s[h]);
+#pragma unroll
+      for (int q = 0; q < TPT; ++q) {
+        const int t = t0 + q * step;
+        if (t >= it.n) continue;
+        float x[16];
+        values(h, q, x);
+        uint8_t* o = codes + (long long)h * a.c.hs + (long long)(held + t) * a.c.ts;
+        const uint2 lo = codes8<FMT>(x, r), hi = codes8<FMT>(x + 8, r);
+        if (halves) {
+          *reinterpret_cast<uint2*>(o + d0) = lo;
+          *reinterpret_cast<uint2*>(o + d1) = hi;
+        } else {
+          *reinterpret_cast<uint4*>(o + d0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
+      }
+      if (threadIdx.x == 0) scale[h] = s[h];
+      if (held > 0 && s[h] > s0[h]) {
+        for (int e = threadIdx.x; e < held * (D / 4); e += blockDim.x) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(codes + (long long)h * a.c.hs + (long long)(e / (D / 4)) * a.c.ts) +
+                        e % (D / 4);
+          *w = recode4<FMT>(*w, s0[h], r);
+        }
+      }
+    }
+    __syncthreads();                               // big is 0 again
+  }
+}
+
+template <class Kernel, class... More>
+int launch(Kernel kernel, dim3 grid, dim3 block, const KvAppendArgs& a, cudaStream_t s, More... more) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -192,16 +515,43 @@ int launch(Kernel kernel, dim3 grid, dim3 block, const KvAppendArgs& a, cudaStre
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, more...);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int FMT, int D>
+int launch_fast(const KvAppendArgs& a, long long items, int num_sms, cudaStream_t s) {
+  const int heads = a.Hq + 2 * a.c.H;
+  // up to 8 tokens a sequence: a warp keeps them, as long as the grid's second extent
+  // holds the sequences' pages
+  const long long pages = (a.max_new + a.c.P - 2) / a.c.P + 1;
+  if (a.max_new <= 8 && a.c.seqs * pages <= 65535) {
+    const dim3 grid((unsigned)((heads + DEC_WARPS - 1) / DEC_WARPS), (unsigned)(a.c.seqs * pages)), block(DEC_WARPS * 32);
+    if (a.max_new == 1) return launch(kv_append_tokens_kernel<FMT, D, 1>, grid, block, a, s, (int)pages);
+    if (a.max_new == 2) return launch(kv_append_tokens_kernel<FMT, D, 2>, grid, block, a, s, (int)pages);
+    return launch(kv_append_tokens_kernel<FMT, D, 8>, grid, block, a, s, (int)pages);
+  }
+  // a page's threads, 16 values of a row each, at most 512 with several rows a thread
+  const int threads = a.c.P * (D / 16), tpt = threads <= 512 ? 1 : threads / 512;
+  const int groups = (a.Hq + HG - 1) / HG + 2 * ((a.c.H + HG - 1) / HG);
+  const int rounds = items * groups >= 32ll * num_sms ? 4 : items * groups >= 16ll * num_sms ? 2 : 1;
+  const dim3 grid((unsigned)items, (unsigned)((groups + rounds - 1) / rounds)), block((unsigned)(threads / tpt));
+  if (tpt == 1) return launch(kv_append_pages_kernel<FMT, D, 1>, grid, block, a, s, rounds);
+  if constexpr (D == 128) return launch(kv_append_pages_kernel<FMT, D, 2>, grid, block, a, s, rounds);   // P 128
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 int launch_kv_append(const KvAppendArgs& a, bool fast, int num_sms, cudaStream_t s) {
   // a sequence of n rows writes at most (n - 1) / P + 2 pages
-  const long long items = a.max_new == 1 ? a.tokens : (long long)a.tokens / a.c.P + 2ll * min(a.c.seqs, a.tokens);
+  const long long items = (long long)a.tokens / a.c.P + 2ll * (a.c.seqs < a.tokens ? a.c.seqs : a.tokens);
   if (items > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (fast) {
+    if (a.c.fmt == kKvE4M3)
+      return a.c.D == 128 ? launch_fast<kKvE4M3, 128>(a, items, num_sms, s) : launch_fast<kKvE4M3, 64>(a, items, num_sms, s);
+    return a.c.D == 128 ? launch_fast<kKvInt8, 128>(a, items, num_sms, s) : launch_fast<kKvInt8, 64>(a, items, num_sms, s);
+  }
   const dim3 grid((unsigned)items, (unsigned)(a.Hq + 2 * a.c.H));
   if (a.c.fmt == kKvE4M3) return launch(kv_append_generic_kernel<kKvE4M3>, grid, dim3(128), a, s);
   return launch(kv_append_generic_kernel<kKvInt8>, grid, dim3(128), a, s);

@@ -31,8 +31,9 @@ __device__ __forceinline__ uint32_t kv_code2(float lo, float hi) {   // two code
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
   } else {
-    const int a = lo == lo ? __float2int_rn(fminf(fmaxf(lo, -127.f), 127.f)) : 0;
-    const int b = hi == hi ? __float2int_rn(fminf(fmaxf(hi, -127.f), 127.f)) : 0;
+    // rounded first, then held to 127: the conversion takes NaN to 0 and saturates
+    const int a = min(max(__float2int_rn(lo), -127), 127);
+    const int b = min(max(__float2int_rn(hi), -127), 127);
     return (uint32_t)(a & 0xff) | ((uint32_t)(b & 0xff) << 8);
   }
 }

@@ -103,6 +103,15 @@ def test_one_token(cuda_lib, fmt, dim, interleaved, base):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("most", [2, 5, 8, 9])
+def test_a_few_tokens(cuda_lib, fmt, dim, most):
+    # a few tokens each, across a page's edge, none at all
+    for interleaved in (False, True):
+        run(fmt, 2, 3, dim, 16, [0, 15, 14, 3, 32, 9], [most, most, 2, 0, 1, most], interleaved=interleaved, seed=most)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dim,page", [(128, 16), (128, 64), (64, 32), (128, 128), (64, 16), (64, 128), (128, 32)])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_prompts(cuda_lib, fmt, dim, page, interleaved):
