@@ -177,14 +177,14 @@ struct StageMeta {
 struct Slot {           // a warp's partial result
   u64 unit;             // first unit of its item (~0: none)
   float* part;          // in shared memory or in the workspace
-  int b, idx;           // sequence; head * tiles + tile
+  int S, rows, h, t, first;   // the item's slabs and rows, head, tile, first row of its sequence
+  int count;            // index of its counter
 };
 
 struct Open {           // an item that more than one warp worked on
   u64 unit;
   int e0, e1;           // its parts: slots e0 .. e1 (warp * 2 + slot)
-  int S, rows, h, t, first, n;
-  int count;            // index of its counter
+  int S, rows, h, t, first, count;
   bool whole;           // no other block has a part of it
 };
 
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     cw.b = lo;
     cw.q = plan.seq(lo);
     const u64 rel = u0 - pref[lo];
-    cw.idx = (int)(rel / cw.q.S);
+    cw.idx = rel >> 32 ? (int)(rel / cw.q.S) : (int)((unsigned)rel / (unsigned)cw.q.S);
     cw.s = (int)(rel - (u64)cw.idx * cw.q.S);
     cw.split();
   }
@@ -401,25 +401,23 @@ __global__ void __launch_bounds__(NW * 32, 1)
 
   // ---- producer side
   const int total = (int)(u1 - u0);
-  // page of the slab's part that this lane fetches, -1 if it has none to fetch
+  // the table's entry for the part of a slab that this lane fetches, -1 where no row
+  // sees it.  Only loaded here: the check waits for the value, so it comes with the
+  // copy, a slab later.
   auto page_of = [&](const Walk& w) -> int {
-    if (lane >= npg) return -1;
     const int key = w.s * SLAB + lane * 16;
-    if (key >= plan.visible(w.q, w.t)) return -1;
-    const int p = a.c.table[(long long)w.b * a.c.tstride + key / a.c.P];
-    if (p < 0 || p >= a.c.pages) {
-      report_status(a.status, 1, kSiteKvAttn);
-      return -1;
-    }
-    return p;
+    if (lane >= npg || key >= plan.visible(w.q, w.t)) return -1;
+    return __ldg(a.c.table + (long long)w.b * a.c.tstride + key / a.c.P);
   };
   auto issue = [&](int st, const Walk& w, int p) {
     if (lane < npg) {
       const uint32_t bar = smem_u32(&sh.full[warp][st]);
       StageMeta& m = sh.meta[warp][st];
-      m.ok[lane] = p >= 0;
-      if (p >= 0) {
-        const int key = w.s * SLAB + lane * 16, rows = SLAB / npg;
+      const int key = w.s * SLAB + lane * 16, rows = SLAB / npg;
+      const bool ok = p >= 0 && p < a.c.pages;
+      if (!ok && key < plan.visible(w.q, w.t)) report_status(a.status, 1, kSiteKvAttn);
+      m.ok[lane] = ok;
+      if (ok) {
         const uint32_t dst = ring + st * C::STAGE + lane * 16 * D;
         mbar_arrive_expect_tx(bar, 2 * rows * D);
         tma_load_4d(dst, &mapK, bar, 0, key % a.c.P, w.h, p);
@@ -644,13 +642,12 @@ __global__ void __launch_bounds__(NW * 32, 1)
         // O^T += V^T P^T.  Transposed ldmatrix of byte pairs: lane (g, t4) has values
         // 2g, 2g+1 of keys 2*t4, 2*t4+1; row g of the operand is value 2g, row g + 8
         // value 2g + 1.
-        auto products = [&](int limit, int query) {
+        auto products = [&](auto masked, int limit, bool all) {
 #pragma unroll
           for (int sub = 0; sub < 2; ++sub) {
             const int kk = k0 + sub * 16 + 2 * t4;
             const bool there = (sub ? ok1 : ok0) != 0;
-            const uint32_t mk0 = query < 0 ? ~0u : there ? key_mask(kk, limit) : 0u;
-            const uint32_t mk1 = query < 0 ? ~0u : there ? key_mask(kk + 8, limit) : 0u;
+            const uint32_t mk0 = there ? key_mask(kk, limit) : 0u, mk1 = there ? key_mask(kk + 8, limit) : 0u;
             const int r = sub * 16 + (lane & 15);
             const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
 #pragma unroll
@@ -661,7 +658,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
               for (int cc = 0; cc < 2; ++cc) {
                 widen_pairs<FMT>(x[2 * cc], a0, a1);
                 widen_pairs<FMT>(x[2 * cc + 1], a2, a3);
-                if (query >= 0) {
+                if constexpr (decltype(masked)::value) {
                   a0 &= mk0;
                   a1 &= mk0;
                   a2 &= mk1;
@@ -669,28 +666,40 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  if (query < 0) {
+                  if constexpr (!decltype(masked)::value) {
                     mma16816(acc[nt][c + cc], a0, a1, a2, a3, pf[sub][nt][0], pf[sub][nt][1]);
                   } else {
                     float y[4] = {0.f, 0.f, 0.f, 0.f};
                     mma16816(y, a0, a1, a2, a3, pf[sub][nt][0], pf[sub][nt][1]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[nt][c + cc][k] += lim[nt][k & 1] == limit ? y[k] : 0.f;
+                    for (int k = 0; k < 4; ++k) acc[nt][c + cc][k] += all || lim[nt][k & 1] == limit ? y[k] : 0.f;
                   }
                 }
               }
             }
           }
         };
-        if (whole) {
-          products(0, -1);
+        // any INT8 code is finite, so a probability of 0 hides what a row does not see
+        if (whole || FMT == kKvInt8) {
+          products(std::false_type{}, 0, true);
         } else {
-          // a zero probability does not hide a NaN, so keys that a query does not see
-          // are cut out of V itself, and only that query's rows take the product
+          // A probability of 0 does not hide a NaN.  Keys that no row sees are cut out
+          // of V itself; if one that only some rows see holds a NaN, V is cut for each
+          // query in turn, and only that query's rows take the product.
+          bool nan = false;
+          {
+            for (int r = max(lim_min - k0, 0); r < min(lim_max - k0, SLAB); ++r)
+              if (lane < D / 4) {
+                uint32_t x;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(vt + r * D + lane * 4) : "memory");
+                nan |= (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+              }
+            nan = __any_sync(0xffffffffu, nan);
+          }
           const int q_lo = cw.t * RT / group, q_hi = (min(q.n * group, (cw.t + 1) * RT) - 1) / group;
-          for (int i = q_lo; i <= q_hi; ++i) {
+          for (int i = nan ? q_lo : q_hi; i <= q_hi; ++i) {
             const int limit = q.len - q.n + i + 1;
-            if (limit > k0) products(limit, i);
+            if (limit > k0) products(std::true_type{}, limit, !nan);
           }
         }
       }
@@ -752,8 +761,12 @@ __global__ void __launch_bounds__(NW * 32, 1)
             Slot& s = sh.slot[warp * 2 + (head ? 0 : 1)];
             s.unit = u0 + j - done.s;
             s.part = part;
-            s.b = done.b;
-            s.idx = done.idx;
+            s.S = done.q.S;
+            s.rows = rows;
+            s.h = done.h;
+            s.t = done.t;
+            s.first = done.q.first;
+            s.count = (done.b * a.c.H + done.h) * max_tiles + done.t;
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -786,30 +799,32 @@ __global__ void __launch_bounds__(NW * 32, 1)
   // ---- parts of items that more than one warp worked on
   __syncthreads();
   if (sh.abort) return;
-  if (threadIdx.x == 0) {
-    int n = 0;
-    for (int e = 0; e < NW * 2; ++e) {
-      const Slot& s = sh.slot[e];
-      if (s.unit == ~0ull) continue;
-      if (n > 0 && sh.open[n - 1].unit == s.unit) {
-        sh.open[n - 1].e1 = e;
-        continue;
-      }
-      Open& o = sh.open[n];
-      const Seq q = plan.seq(s.b);
-      o.unit = s.unit;
-      o.e0 = o.e1 = e;
-      o.S = q.S;
-      o.h = s.idx / q.tiles;
-      o.t = s.idx % q.tiles;
-      o.rows = min(RT, q.n * group - o.t * RT);
-      o.first = q.first;
-      o.n = q.n;
-      o.count = (s.b * a.c.H + o.h) * max_tiles + o.t;
-      o.whole = s.unit >= A && s.unit + q.S <= B;
-      ++n;
+  if (warp == 0) {
+    // a lane for each slot: an item's first slot makes its entry
+    const u64 unit = lane < NW * 2 ? sh.slot[lane].unit : ~0ull;
+    const unsigned valid = __ballot_sync(0xffffffffu, unit != ~0ull);
+    const unsigned below = valid & ((1u << lane) - 1u);
+    const int prev = below ? 31 - __clz(below) : lane;
+    const u64 before = __shfl_sync(0xffffffffu, unit, prev);
+    const bool starts = unit != ~0ull && (below == 0 || before != unit);
+    const unsigned firsts = __ballot_sync(0xffffffffu, starts);
+    if (starts) {
+      const Slot& s = sh.slot[lane];
+      Open& o = sh.open[__popc(firsts & ((1u << lane) - 1u))];
+      const unsigned later = lane < 31 ? firsts & ~((2u << lane) - 1u) : 0u;
+      const unsigned own = later ? valid & ((1u << (__ffs(later) - 1)) - 1u) : valid;   // slots before the next item's
+      o.unit = unit;
+      o.e0 = lane;
+      o.e1 = 31 - __clz(own);
+      o.S = s.S;
+      o.rows = s.rows;
+      o.h = s.h;
+      o.t = s.t;
+      o.first = s.first;
+      o.count = s.count;
+      o.whole = unit >= A && unit + s.S <= B;
     }
-    sh.opens = n;
+    if (lane == 0) sh.opens = __popc(firsts);
   }
   __syncthreads();
   float* parts = static_cast<float*>(a.ws);
@@ -887,23 +902,46 @@ __global__ void __launch_bounds__(NW * 32, 1)
     if (!sh.last[j]) continue;
     __threadfence();
     const Open& o = sh.open[j];
-    const int c0 = (int)(((o.unit + 1) * G - 1) / T), c1 = (int)(((o.unit + o.S) * G - 1) / T);
+    const int c0 = (int)(((o.unit + 1) * G - 1) / T), n = (int)(((o.unit + o.S) * G - 1) / T) - c0 + 1;
+    // it is the last item of its first block, and the first item of the others
+    const float* first = parts + ((size_t)c0 * 2 + 1) * PART_FLOATS;
+    const float* rest = parts + (size_t)c0 * 2 * PART_FLOATS;
+    auto part = [&](int c) { return c == 0 ? first : rest + (size_t)c * 2 * PART_FLOATS; };
+    // every part's weight for every row, in the drained rings
+    float* wt = reinterpret_cast<float*>(base_ptr);                // [row][part]
+    float* sums = wt + MAX_ROWS * MAX_CTAS;                        // [row][part], then the rows' totals
+    float* totals = sums + MAX_ROWS * MAX_CTAS;
+    static_assert((2 * MAX_ROWS * MAX_CTAS + MAX_ROWS) * 4 <= NW * RING, "weights fit in the rings");
+    for (int i = threadIdx.x; i < o.rows * n; i += NW * 32) {
+      const int r = i / n, c = i - r * n;
+      wt[r * MAX_CTAS + c] = __ldcg(part(c) + RT * D + r);
+      sums[r * MAX_CTAS + c] = __ldcg(part(c) + RT * D + RT + r);
+    }
+    __syncthreads();
+    for (int r = warp; r < o.rows; r += NW) {
+      float M = -INFINITY;
+      for (int c = lane; c < n; c += 32) M = fmaxf(M, wt[r * MAX_CTAS + c]);
+      for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+      const float Mu = M == -INFINITY ? 0.f : M;
+      float sum = 0.f;
+      for (int c = lane; c < n; c += 32) {
+        const float w = ex2(wt[r * MAX_CTAS + c] - Mu);
+        wt[r * MAX_CTAS + c] = w;
+        sum = fmaf(w, sums[r * MAX_CTAS + c], sum);
+      }
+      for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+      if (lane == 0) totals[r] = sum;
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < o.rows * (D / 4); i += NW * 32) {
       const int r = i / (D / 4), d4 = i % (D / 4);
-      auto part = [&](int c) { return parts + ((u64)c * 2 + (o.unit < (u64)c * T / G ? 0 : 1)) * PART_FLOATS; };
-      float M = -INFINITY;
-      for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part(c) + RT * D + r));
-      const float Mu = M == -INFINITY ? 0.f : M;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f;
-      for (int c = c0; c <= c1; ++c) {
-        const float* p = part(c);
-        const float w = ex2(__ldcg(p + RT * D + r) - Mu);
-        sum = fmaf(w, __ldcg(p + RT * D + RT + r), sum);
-        add(x, w, __ldcg(reinterpret_cast<const float4*>(p + r * D + d4 * 4)));
-      }
-      store(o, r, d4, x, sum);
+#pragma unroll 8
+      for (int c = 0; c < n; ++c)
+        add(x, wt[r * MAX_CTAS + c], __ldcg(reinterpret_cast<const float4*>(part(c) + r * D + d4 * 4)));
+      store(o, r, d4, x, totals[r]);
     }
+    __syncthreads();                               // the weights have been read
   }
 }
 
