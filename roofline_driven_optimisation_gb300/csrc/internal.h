@@ -248,7 +248,7 @@ int launch_kv_attention_generic(const KvAttnArgs& a, cudaStream_t s);
 // D x min(P, 32) codes, swizzle of D bytes.
 int launch_kv_attention(const KvAttnArgs& a, const CUtensorMap* mK, const CUtensorMap* mV, int num_sms,
                         cudaStream_t s);
-constexpr int kKvMaxSeqs = 16384, kKvSlab = 32;
+constexpr int kKvMaxSeqs = 8192, kKvSlab = 32;
 size_t kv_attention_ws_bytes(int seqs, int heads, int group, int max_new);
 
 // Sampling (gemm_sample_*).

@@ -151,6 +151,7 @@ constexpr int MAX_ROWS = 32;             // rows of a tile, at most
 constexpr int RING = 3 * 2 * SLAB * 128; // bytes of a warp's ring
 constexpr int PV_EXP = 14;               // P times the page's scale is below 2^PV_EXP in fp16
 constexpr int MIN_EXP = -112;
+constexpr int WHOLE_EXTRA = 8;          // of 8-row slabs; see its use
 
 template <int D>
 struct Cfg {
@@ -188,6 +189,12 @@ struct Open {           // an item that more than one warp worked on
   bool whole;           // no other block has a part of it
 };
 
+struct SeqRec {         // a sequence on the line: units and items before it
+  u64 at;
+  int items, len, first, n;
+};
+static_assert(kKvMaxSeqs * sizeof(SeqRec) <= NW * RING, "the records fit in the rings");
+
 struct Shared {
   StageMeta meta[NW][6];
   u64 full[NW][6];
@@ -195,6 +202,7 @@ struct Shared {
   Open open[NW + 1];
   int opens;
   u64 scan[NW];
+  int scan_items[NW], scan_longest[NW];
   int last[NW + 1];     // this block finishes the item
   int abort;
 };
@@ -207,36 +215,55 @@ struct Seq {
 struct Plan {
   const KvAttnArgs* a;
   int group, rt;        // query heads of a head; rows of a tile
+  __device__ __forceinline__ Seq seq(int len, int first, int n) const {
+    return Seq{len, first, n, max(1, (len + SLAB - 1) / SLAB), (n * group + rt - 1) / rt};
+  }
   __device__ __forceinline__ Seq seq(int b) const {
-    Seq q;
-    q.len = kv_length(*a, b);
-    kv_rows(a->start, b, a->tokens, a->max_new, a->status, kSiteKvAttn, q.first, q.n);
-    q.S = max(1, (q.len + SLAB - 1) / SLAB);
-    q.tiles = (q.n * group + rt - 1) / rt;
-    return q;
+    // every load before the first check, which waits for it
+    int len = __ldg(a->lengths + b), first = b, end = b + 1;
+    if (a->start != nullptr) {
+      first = __ldg(a->start + b);
+      end = __ldg(a->start + b + 1);
+    }
+    const long long most = (long long)a->c.cols * a->c.P;
+    if (len < 0 || len > most) {
+      report_status(a->status, 1, kSiteKvAttn);
+      len = len < 0 ? 0 : (int)most;
+    }
+    if (first < 0 || end < first || end > a->tokens || end - first > a->max_new) {
+      report_status(a->status, 1, kSiteKvAttn);
+      first = end = 0;
+    }
+    return seq(len, first, end - first);
   }
   __device__ __forceinline__ u64 units(const Seq& q) const { return (u64)a->c.H * q.tiles * q.S; }
   // keys that the last row of tile t sees
   __device__ __forceinline__ int visible(const Seq& q, int t) const {
-    const int i = (min(q.n * group, (t + 1) * rt) - 1) / group;
-    return q.len - q.n + i + 1;
+    if ((t + 1) * rt >= q.n * group) return q.len;
+    return q.len - q.n + ((t + 1) * rt - 1) / group + 1;
   }
 };
+
+// x / d, by the 32-bit division wherever both fit
+__device__ __forceinline__ u64 quotient(u64 x, u64 d) {
+  return (x | d) >> 32 ? x / d : (u64)((unsigned)x / (unsigned)d);
+}
 
 // A place on the line of slabs
 struct Walk {
   int b, idx, s;        // sequence, head * tiles + tile, slab
-  int h, t;
+  int h, t, vis;        // head, tile, keys that the tile's last row sees
   Seq q;
-  __device__ __forceinline__ void split() {
-    h = idx / q.tiles;
+  __device__ __forceinline__ void split(const Plan& p) {
+    h = q.tiles == 1 ? idx : idx / q.tiles;
     t = idx - h * q.tiles;
+    vis = p.visible(q, t);
   }
   __device__ __forceinline__ void next(const Plan& p) {
     if (++s < q.S) return;
     s = 0;
     if (++idx < p.a->c.H * q.tiles) {
-      split();
+      split(p);
       return;
     }
     idx = 0;
@@ -244,7 +271,7 @@ struct Walk {
       if (++b >= p.a->c.seqs) return;
       q = p.seq(b);
     } while (q.tiles == 0);
-    split();
+    split(p);
   }
 };
 
@@ -335,6 +362,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   const uint32_t ring = smem_u32(ring_ptr);
   const Plan plan{&a, group, RT};
   const int npg = a.c.P < SLAB ? 2 : 1;           // pages of a slab
+  const int p_shift = 31 - __clz(a.c.P);          // P is a power of two
 
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&mapK);
@@ -347,56 +375,94 @@ __global__ void __launch_bounds__(NW * 32, 1)
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
 
-  // ---- the line of slabs: units before each sequence, in the ring's memory
-  u64* pref = reinterpret_cast<u64*>(base_ptr);
+  // ---- the line of slabs: every sequence's place on it, in the rings' memory
+  SeqRec* rec = reinterpret_cast<SeqRec*>(base_ptr);
   const int per = (a.c.seqs + NW * 32 - 1) / (NW * 32);
   const int b_lo = min(a.c.seqs, (int)threadIdx.x * per), b_hi = min(a.c.seqs, b_lo + per);
   u64 mine = 0;
+  int items = 0, longest = 0;
   for (int b = b_lo; b < b_hi; ++b) {
-    const u64 n = plan.units(plan.seq(b));
-    pref[b] = n;
-    mine += n;
+    const Seq q = plan.seq(b);
+    rec[b].at = mine;
+    rec[b].items = items;
+    rec[b].len = q.len;
+    rec[b].first = q.first;
+    rec[b].n = q.n;
+    mine += plan.units(q);
+    items += a.c.H * q.tiles;
+    if (q.tiles > 0) longest = max(longest, q.S);
   }
   u64 incl = mine;
+  int item_incl = items;
   for (int o = 1; o < 32; o <<= 1) {
     const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const int z = __shfl_up_sync(0xffffffffu, item_incl, o);
+    if (lane >= o) {
+      incl += y;
+      item_incl += z;
+    }
   }
-  if (lane == 31) sh.scan[warp] = incl;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) {
+    sh.scan[warp] = incl;
+    sh.scan_items[warp] = item_incl;
+    sh.scan_longest[warp] = longest;
+  }
   __syncthreads();
   u64 at = incl - mine, T = 0;
+  int item_at = item_incl - items, I = 0;
   for (int w = 0; w < NW; ++w) {
-    if (w < warp) at += sh.scan[w];
+    if (w < warp) {
+      at += sh.scan[w];
+      item_at += sh.scan_items[w];
+    }
     T += sh.scan[w];
+    I += sh.scan_items[w];
+    longest = max(longest, sh.scan_longest[w]);
   }
   for (int b = b_lo; b < b_hi; ++b) {
-    const u64 n = pref[b];
-    pref[b] = at;
-    at += n;
+    rec[b].at += at;
+    rec[b].items += item_at;
   }
   __syncthreads();
-  const u64 G = T < gridDim.x ? T : gridDim.x;   // every block up to G has a unit
+  // Blocks take equal shares of the line, or whole items.  Whole items need no exchange
+  // between blocks, which costs a call about as much time as WHOLE_EXTRA slabs a warp;
+  // so they are taken unless the fullest block's warps get longer than that.
+  const u64 share = quotient(T + gridDim.x * NW - 1, gridDim.x * NW);
+  const int blocks = min((int)gridDim.x, I);
+  const bool by_item = I > 0 && ((u64)((I + blocks - 1) / blocks) * longest + NW - 1) / NW <= share + WHOLE_EXTRA / NT;
+  const u64 G = by_item ? (u64)blocks : T < gridDim.x ? T : gridDim.x;   // every block up to G has a unit
   const u64 cta = blockIdx.x;
   if (cta >= G) return;
-  const u64 W = G * NW, me = cta * NW + warp;
-  const u64 u0 = me * T / W, u1 = (me + 1) * T / W;
-  const u64 A = cta * T / G, B = (cta + 1) * T / G;
-  Walk cw;
-  if (u0 < u1) {
-    int lo = 0, hi = a.c.seqs;                    // the last b with pref[b] <= u0 that has units
+  auto record = [&](auto before) {                // the last sequence for which before() holds
+    int lo = 0, hi = a.c.seqs;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (pref[mid] <= u0) lo = mid;
+      if (before(rec[mid])) lo = mid;
       else hi = mid;
     }
-    cw.b = lo;
-    cw.q = plan.seq(lo);
-    const u64 rel = u0 - pref[lo];
-    cw.idx = rel >> 32 ? (int)(rel / cw.q.S) : (int)((unsigned)rel / (unsigned)cw.q.S);
+    return lo;
+  };
+  auto item_unit = [&](u64 i) -> u64 {            // first unit of item i
+    if (i >= (u64)I) return T;
+    const SeqRec& q = rec[record([&](const SeqRec& x) { return x.items <= (int)i; })];
+    return q.at + (i - q.items) * (u64)max(1, (q.len + SLAB - 1) / SLAB);
+  };
+  const u64 A = by_item ? item_unit(quotient(cta * I, G)) : quotient(cta * T, G);
+  const u64 B = by_item ? item_unit(quotient((cta + 1) * I, G)) : quotient((cta + 1) * T, G);
+  const u64 me = cta * NW + warp;
+  const u64 u0 = A + warp * (B - A) / NW, u1 = A + (warp + 1) * (B - A) / NW;
+  Walk cw;
+  if (u0 < u1) {
+    cw.b = record([&](const SeqRec& x) { return x.at <= u0; });
+    const SeqRec& x = rec[cw.b];
+    cw.q = plan.seq(x.len, x.first, x.n);
+    const u64 rel = u0 - x.at;
+    cw.idx = (int)quotient(rel, cw.q.S);
     cw.s = (int)(rel - (u64)cw.idx * cw.q.S);
-    cw.split();
+    cw.split(plan);
   }
-  __syncthreads();                                // pref's memory becomes the rings
+  __syncthreads();                                // the records' memory becomes the rings
   fence_proxy_async_smem();
 
   // ---- producer side
@@ -406,8 +472,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
   // copy, a slab later.
   auto page_of = [&](const Walk& w) -> int {
     const int key = w.s * SLAB + lane * 16;
-    if (lane >= npg || key >= plan.visible(w.q, w.t)) return -1;
-    return __ldg(a.c.table + (long long)w.b * a.c.tstride + key / a.c.P);
+    if (lane >= npg || key >= w.vis) return -1;
+    return __ldg(a.c.table + (long long)w.b * a.c.tstride + (key >> p_shift));
   };
   auto issue = [&](int st, const Walk& w, int p) {
     if (lane < npg) {
@@ -415,13 +481,13 @@ __global__ void __launch_bounds__(NW * 32, 1)
       StageMeta& m = sh.meta[warp][st];
       const int key = w.s * SLAB + lane * 16, rows = SLAB / npg;
       const bool ok = p >= 0 && p < a.c.pages;
-      if (!ok && key < plan.visible(w.q, w.t)) report_status(a.status, 1, kSiteKvAttn);
+      if (!ok && key < w.vis) report_status(a.status, 1, kSiteKvAttn);
       m.ok[lane] = ok;
       if (ok) {
         const uint32_t dst = ring + st * C::STAGE + lane * 16 * D;
         mbar_arrive_expect_tx(bar, 2 * rows * D);
-        tma_load_4d(dst, &mapK, bar, 0, key % a.c.P, w.h, p);
-        tma_load_4d(dst + C::TILE, &mapV, bar, 0, key % a.c.P, w.h, p);
+        tma_load_4d(dst, &mapK, bar, 0, key & (a.c.P - 1), w.h, p);
+        tma_load_4d(dst + C::TILE, &mapV, bar, 0, key & (a.c.P - 1), w.h, p);
         cp_async_4(smem_u32(&m.ks[lane]), a.c.ks + (long long)p * a.c.H + w.h);
         cp_async_4(smem_u32(&m.vs[lane]), a.c.vs + (long long)p * a.c.H + w.h);
       } else {
@@ -523,7 +589,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         }
         ev = MIN_EXP;
         lim_min = q.len - q.n + cw.t * RT / group + 1;
-        lim_max = plan.visible(q, cw.t);
+        lim_max = cw.vis;
       }
 
       // ---- the slab
@@ -829,7 +895,6 @@ __global__ void __launch_bounds__(NW * 32, 1)
   __syncthreads();
   float* parts = static_cast<float*>(a.ws);
   int* counters = reinterpret_cast<int*>(parts + PARTS * PART_FLOATS);
-  constexpr int QUADS = RT * (D / 4);
   auto store = [&](const Open& o, int r, int d4, float4 x, float sum) {
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int rr = o.t * RT + r;
@@ -853,31 +918,48 @@ __global__ void __launch_bounds__(NW * 32, 1)
     x.w = fmaf(w, y.w, x.w);
   };
   const int opens = sh.opens;
-  for (int i = threadIdx.x; i < opens * QUADS; i += NW * 32) {
-    const Open& o = sh.open[i / QUADS];
-    const int r = i % QUADS / (D / 4), d4 = i % (D / 4);
-    if (r >= o.rows) continue;
-    float M = -INFINITY;
-    for (int e = o.e0; e <= o.e1; ++e)
-      if (sh.slot[e].unit == o.unit) M = fmaxf(M, sh.slot[e].part[RT * D + r]);
-    const float Mu = M == -INFINITY ? 0.f : M;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    for (int e = o.e0; e <= o.e1; ++e) {
-      if (sh.slot[e].unit != o.unit) continue;
-      const float* p = sh.slot[e].part;
-      const float w = ex2(p[RT * D + r] - Mu);
-      sum = fmaf(w, p[RT * D + RT + r], sum);
-      add(x, w, *reinterpret_cast<const float4*>(p + r * D + d4 * 4));
+  // weights of every slot for every row, behind the part in the first ring
+  float* wt = reinterpret_cast<float*>(base_ptr + PART_FLOATS * 4);   // [slot][row]
+  float* tops = wt + NW * 2 * MAX_ROWS;                               // [item][row]: maximum
+  float* totals = tops + (NW + 1) * MAX_ROWS;                         // [item][row]: sum
+  static_assert((PART_FLOATS + (2 * NW + 2 * NW + 2) * MAX_ROWS) * 4 <= RING, "weights fit behind a part");
+  int rmax = 0;
+  for (int i = 0; i < opens; ++i) rmax = max(rmax, sh.open[i].rows);
+  for (int i = threadIdx.x / 16; i < (opens * rmax + 1) / 2 * 2; i += NW * 2) {
+    // half a warp a row, a lane a slot
+    const int j = min(i / rmax, opens - 1), r = i - j * rmax, e = lane % 16;
+    const Open& o = sh.open[j];
+    const Slot& s = sh.slot[e];
+    const bool mine = r < o.rows && s.unit == o.unit;
+    const float top = mine ? s.part[RT * D + r] : -INFINITY, l = mine ? s.part[RT * D + RT + r] : 0.f;
+    float M = top;
+    for (int k = 8; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+    const float w = mine ? ex2(top - (M == -INFINITY ? 0.f : M)) : 0.f;
+    float sum = mine ? w * l : 0.f;
+    for (int k = 8; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    if (mine) wt[e * MAX_ROWS + r] = w;
+    if (e == 0 && r < o.rows) {
+      tops[j * MAX_ROWS + r] = M;
+      totals[j * MAX_ROWS + r] = sum;
     }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < opens * rmax * (D / 4); i += NW * 32) {
+    const int j = i / (D / 4) / rmax, r = i / (D / 4) - j * rmax, d4 = i % (D / 4);
+    const Open& o = sh.open[j];
+    if (r >= o.rows) continue;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int e = o.e0; e <= o.e1; ++e)
+      if (sh.slot[e].unit == o.unit)
+        add(x, wt[e * MAX_ROWS + r], *reinterpret_cast<const float4*>(sh.slot[e].part + r * D + d4 * 4));
     if (o.whole) {
-      store(o, r, d4, x, sum);
+      store(o, r, d4, x, totals[j * MAX_ROWS + r]);
     } else {
       float* p = parts + (cta * 2 + (o.unit < A ? 0 : 1)) * PART_FLOATS;
       *reinterpret_cast<float4*>(p + r * D + d4 * 4) = x;
       if (d4 == 0) {
-        p[RT * D + r] = M;
-        p[RT * D + RT + r] = sum;
+        p[RT * D + r] = tops[j * MAX_ROWS + r];
+        p[RT * D + RT + r] = totals[j * MAX_ROWS + r];
       }
     }
   }
@@ -891,7 +973,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const Open& o = sh.open[threadIdx.x];
     int last = 0;
     if (!o.whole) {
-      const int c0 = (int)(((o.unit + 1) * G - 1) / T), c1 = (int)(((o.unit + o.S) * G - 1) / T);
+      const int c0 = (int)quotient((o.unit + 1) * G - 1, T), c1 = (int)quotient((o.unit + o.S) * G - 1, T);
       last = atomicAdd(counters + o.count, 1) == c1 - c0;
       if (last) counters[o.count] = 0;             // ready for the next call
     }
@@ -902,15 +984,15 @@ __global__ void __launch_bounds__(NW * 32, 1)
     if (!sh.last[j]) continue;
     __threadfence();
     const Open& o = sh.open[j];
-    const int c0 = (int)(((o.unit + 1) * G - 1) / T), n = (int)(((o.unit + o.S) * G - 1) / T) - c0 + 1;
+    const int c0 = (int)quotient((o.unit + 1) * G - 1, T), n = (int)quotient((o.unit + o.S) * G - 1, T) - c0 + 1;
     // it is the last item of its first block, and the first item of the others
     const float* first = parts + ((size_t)c0 * 2 + 1) * PART_FLOATS;
     const float* rest = parts + (size_t)c0 * 2 * PART_FLOATS;
     auto part = [&](int c) { return c == 0 ? first : rest + (size_t)c * 2 * PART_FLOATS; };
     // every part's weight for every row, in the drained rings
     float* wt = reinterpret_cast<float*>(base_ptr);                // [row][part]
-    float* sums = wt + MAX_ROWS * MAX_CTAS;                        // [row][part], then the rows' totals
-    float* totals = sums + MAX_ROWS * MAX_CTAS;
+    float* sums = wt + MAX_ROWS * MAX_CTAS;                        // [row][part]
+    float* totals = sums + MAX_ROWS * MAX_CTAS;                    // [row]
     static_assert((2 * MAX_ROWS * MAX_CTAS + MAX_ROWS) * 4 <= NW * RING, "weights fit in the rings");
     for (int i = threadIdx.x; i < o.rows * n; i += NW * 32) {
       const int r = i / n, c = i - r * n;
