@@ -22,6 +22,39 @@ __device__ __forceinline__ float2 turn(float a, float b, float c, float s) {
   return make_float2(__fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)), __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s)));
 }
 
+// Two fp32 values in one register pair; each half of a packed product is rounded by
+// itself.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 halves_of(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// Sums of packed products, in scalar form: a packed sum was seen contracted with the
+// packed products before it into a fused multiply-add, which skips a rounding.
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  const float2 x = halves_of(a), y = halves_of(b);
+  return pair(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  const float2 x = halves_of(a), y = halves_of(b);
+  return pair(__fsub_rn(x.x, y.x), __fsub_rn(x.y, y.y));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // One item: the rows of sequence b's call that fall into one page.
 struct Item {
   int b, row0, n;     // sequence; first of its rows in this page, and how many
@@ -192,13 +225,20 @@ __global__ void __launch_bounds__(128) kv_append_generic_kernel(const KvAppendAr
 // read each value once, with enough loads in flight, and keep it until its page's
 // scale is known.
 
-// eight bf16 as floats
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+// eight bf16 as four pairs of floats: neighbours
+__device__ __forceinline__ void unpack8(const uint4& v, uint64_t (&x)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+// eight bf16 of each vector as pairs (x[i], x[i + 1]) of the firsts and the seconds of
+// each neighbours
+__device__ __forceinline__ void split8(const uint4& v, uint64_t (&even)[2], uint64_t (&odd)[2]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    even[i] = pair(__uint_as_float(w[2 * i] << 16), __uint_as_float(w[2 * i + 1] << 16));
+    odd[i] = pair(__uint_as_float(w[2 * i] & 0xffff0000u), __uint_as_float(w[2 * i + 1] & 0xffff0000u));
   }
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -206,13 +246,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 template <int FMT>
-__device__ __forceinline__ uint2 codes8(const float* x, float r) {
-  uint32_t w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    w[i] = kv_code2<FMT>(__fmul_rn(x[4 * i], r), __fmul_rn(x[4 * i + 1], r)) |
-           (kv_code2<FMT>(__fmul_rn(x[4 * i + 2], r), __fmul_rn(x[4 * i + 3], r)) << 16);
-  return make_uint2(w[0], w[1]);
+__device__ __forceinline__ uint32_t codes4(uint64_t lo, uint64_t hi, uint64_t r2) {
+  const float2 a = halves_of(mul2(lo, r2)), b = halves_of(mul2(hi, r2));
+  return kv_code2<FMT>(a.x, a.y) | (kv_code2<FMT>(b.x, b.y) << 16);
 }
 template <int FMT>
 __device__ __forceinline__ uint32_t recode4(uint32_t c, float s0, float r) {
@@ -359,7 +395,7 @@ __global__ void __launch_bounds__(512, TPT == 1 ? 2 : 1) kv_append_pages_kernel(
   const int qg = (a.Hq + HG - 1) / HG, kg = (a.c.H + HG - 1) / HG;   // groups of query and of key heads
   const int t0 = threadIdx.x / CH, c = threadIdx.x % CH, step = blockDim.x / CH;
   const int held = it.pos0 % a.c.P;
-  float co[TPT][8], si[TPT][8];
+  uint64_t co[TPT][4], si[TPT][4];                 // angles of eight pairs, two in each
   bool angles = false;
   int g = -2;                                      // the page, not looked up yet
   for (int round = 0; round < rounds; ++round) {
@@ -392,38 +428,45 @@ __global__ void __launch_bounds__(512, TPT == 1 ? 2 : 1) kv_append_pages_kernel(
         const long long at = (long long)(it.pos0 + t) * (D / 2) + c * 8;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          *reinterpret_cast<float4*>(&co[q][4 * i]) = *reinterpret_cast<const float4*>(a.cos + at + 4 * i);
-          *reinterpret_cast<float4*>(&si[q][4 * i]) = *reinterpret_cast<const float4*>(a.sin + at + 4 * i);
+          const float4 x = *reinterpret_cast<const float4*>(a.cos + at + 4 * i);
+          const float4 y = *reinterpret_cast<const float4*>(a.sin + at + 4 * i);
+          co[q][2 * i] = pair(x.x, x.y);
+          co[q][2 * i + 1] = pair(x.z, x.w);
+          si[q][2 * i] = pair(y.x, y.y);
+          si[q][2 * i + 1] = pair(y.z, y.w);
         }
       }
     }
-    // the 16 values, turned
-    auto values = [&](int h, int q, float (&x)[16]) {
-      float p[8], w[8];
-      unpack8(u[h][q], p);
-      unpack8(v[h][q], w);
+    // the 16 values, turned: neighbours in pairs, d0's octet then d1's
+    auto values = [&](int h, int q, uint64_t (&x)[8]) {
       if (kind == 2) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = p[i];
-          x[8 + i] = w[i];
-        }
-      } else if (halves) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 y = turn(p[i], w[i], co[q][i], si[q][i]);
-          x[i] = y.x;
-          x[8 + i] = y.y;
-        }
-      } else {
+        uint64_t p[4], w[4];
+        unpack8(u[h][q], p);
+        unpack8(v[h][q], w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 y = turn(p[2 * i], p[2 * i + 1], co[q][i], si[q][i]);
-          const float2 z = turn(w[2 * i], w[2 * i + 1], co[q][4 + i], si[q][4 + i]);
-          x[2 * i] = y.x;
-          x[2 * i + 1] = y.y;
-          x[8 + 2 * i] = z.x;
-          x[9 + 2 * i] = z.y;
+          x[i] = p[i];
+          x[4 + i] = w[i];
+        }
+      } else if (halves) {
+        uint64_t p[4], w[4];
+        unpack8(u[h][q], p);
+        unpack8(v[h][q], w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = sub2(mul2(p[i], co[q][i]), mul2(w[i], si[q][i]));
+          x[4 + i] = add2(mul2(w[i], co[q][i]), mul2(p[i], si[q][i]));
+        }
+      } else {
+        uint64_t even[4], odd[4];
+        split8(u[h][q], reinterpret_cast<uint64_t(&)[2]>(even[0]), reinterpret_cast<uint64_t(&)[2]>(odd[0]));
+        split8(v[h][q], reinterpret_cast<uint64_t(&)[2]>(even[2]), reinterpret_cast<uint64_t(&)[2]>(odd[2]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = halves_of(sub2(mul2(even[i], co[q][i]), mul2(odd[i], si[q][i])));
+          const float2 z = halves_of(add2(mul2(odd[i], co[q][i]), mul2(even[i], si[q][i])));
+          x[2 * i] = pair(y.x, z.x);
+          x[2 * i + 1] = pair(y.y, z.y);
         }
       }
     };
@@ -434,14 +477,18 @@ __global__ void __launch_bounds__(512, TPT == 1 ? 2 : 1) kv_append_pages_kernel(
         for (int q = 0; q < TPT; ++q) {
           const int t = t0 + q * step;
           if (h >= heads || t >= it.n) continue;
-          float x[16];
+          uint64_t x[8];
           values(h, q, x);
+          uint32_t y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 f = halves_of(x[i]);
+            y[i] = pack2(f.x, f.y);
+          }
           __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.Qo) + (long long)(it.row0 + t) * a.ldqo +
                              (long long)(h0 + h) * D;
-          *reinterpret_cast<uint4*>(o + d0) =
-              make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
-          *reinterpret_cast<uint4*>(o + d1) =
-              make_uint4(pack2(x[8], x[9]), pack2(x[10], x[11]), pack2(x[12], x[13]), pack2(x[14], x[15]));
+          *reinterpret_cast<uint4*>(o + d0) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(o + d1) = make_uint4(y[4], y[5], y[6], y[7]);
         }
       continue;
     }
@@ -456,10 +503,13 @@ __global__ void __launch_bounds__(512, TPT == 1 ? 2 : 1) kv_append_pages_kernel(
       float m = 0.f;
 #pragma unroll
       for (int q = 0; q < TPT; ++q) {
-        float x[16];
+        uint64_t x[8];
         values(h, q, x);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = halves_of(x[i]);
+          m = max3(m, fabsf(f.x), fabsf(f.y));
+        }
       }
       // magnitudes order as their bits; the atomic is a maximum, so its order is free
       const unsigned w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
@@ -480,10 +530,12 @@ __global__ void __launch_bounds__(512, TPT == 1 ? 2 : 1) kv_append_pages_kernel(
       for (int q = 0; q < TPT; ++q) {
         const int t = t0 + q * step;
         if (t >= it.n) continue;
-        float x[16];
+        uint64_t x[8];
         values(h, q, x);
         uint8_t* o = codes + (long long)h * a.c.hs + (long long)(held + t) * a.c.ts;
-        const uint2 lo = codes8<FMT>(x, r), hi = codes8<FMT>(x + 8, r);
+        const uint64_t r2 = pair(r, r);
+        const uint2 lo = make_uint2(codes4<FMT>(x[0], x[1], r2), codes4<FMT>(x[2], x[3], r2));
+        const uint2 hi = make_uint2(codes4<FMT>(x[4], x[5], r2), codes4<FMT>(x[6], x[7], r2));
         if (halves) {
           *reinterpret_cast<uint2*>(o + d0) = lo;
           *reinterpret_cast<uint2*>(o + d1) = hi;
