@@ -9,6 +9,9 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <type_traits>
+
 #include "internal.h"
 #include "kv_cache.cuh"
 #include "ptx.cuh"
@@ -378,197 +381,250 @@ __global__ void __launch_bounds__(DEC_WARPS * 32) kv_append_tokens_kernel(const 
   if (lane == 0) *scale = s;
 }
 
-// Prompts: a block holds one item of HG heads in registers, 16 values of a row a
-// thread (a pair of octets that turn together, or neighbours), TPT rows a thread;
-// the angles are read once for all heads of the block.
-constexpr int HG = 2;
+// Prompts: a block takes one item and walks through `per` heads of it, 16 values of a
+// row a thread (a pair of octets that turn together, or neighbours), TPT rows a
+// thread.  The angles are read once for all heads.  Every thread copies its own bytes
+// of the next STAGES heads ahead into shared memory, so nothing waits for them but the
+// thread itself; the one barrier a head is for the largest magnitude.
+constexpr int STAGES = 4;
+constexpr int PAGE_THREADS = 512;
 
 template <int FMT, int D, int TPT>
-__global__ void __launch_bounds__(512, TPT == 1 ? 2 : 1) kv_append_pages_kernel(const KvAppendArgs a, const int rounds) {
-  __shared__ unsigned big[HG];
+__global__ void __launch_bounds__(PAGE_THREADS, TPT == 1 ? 2 : 1) kv_append_pages_kernel(const KvAppendArgs a, const int per) {
+  extern __shared__ __align__(16) uint8_t ahead[];   // [stage][row of the thread][octet][thread] 16 bytes
+  __shared__ unsigned big[3];
   constexpr int CH = D / 16;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  if (threadIdx.x < HG) big[threadIdx.x] = 0;
+  if (threadIdx.x < 3) big[threadIdx.x] = 0;
   Item it;
   if (!find_item(a, blockIdx.x, it)) return;
-  const int qg = (a.Hq + HG - 1) / HG, kg = (a.c.H + HG - 1) / HG;   // groups of query and of key heads
   const int t0 = threadIdx.x / CH, c = threadIdx.x % CH, step = blockDim.x / CH;
-  const int held = it.pos0 % a.c.P;
-  uint64_t co[TPT][4], si[TPT][4];                 // angles of eight pairs, two in each
-  bool angles = false;
-  int g = -2;                                      // the page, not looked up yet
-  for (int round = 0; round < rounds; ++round) {
-    const int gr = blockIdx.y * rounds + round;
-    if (gr >= qg + 2 * kg) return;
-    const int kind = gr < qg ? 0 : gr < qg + kg ? 1 : 2;
-    const int h0 = (kind == 0 ? gr : gr - qg - (kind - 1) * kg) * HG, heads = min(HG, (kind == 0 ? a.Hq : a.c.H) - h0);
-    const bool halves = kind != 2 && !a.interleaved;
-    const int d0 = halves ? c * 8 : c * 16, d1 = halves ? d0 + D / 2 : d0 + 8;
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(kind == 0 ? a.Q : kind == 1 ? a.K : a.V);
+  const int held = it.pos0 % a.c.P, n = it.n;
+  const int from = blockIdx.y * per, to = min(a.Hq + 2 * a.c.H, from + per);   // query, key, value heads
+  const int k_from = a.Hq, v_from = a.Hq + a.c.H;
+  // octets of this thread: of a rotation by halves, or neighbours
+  const int dn0 = c * 16, dn1 = dn0 + 8, dr0 = a.interleaved ? dn0 : c * 8, dr1 = a.interleaved ? dn1 : dr0 + D / 2;
+
+  // ---- the copies ahead: a running place in Q, then K, then V
+  const uint32_t mine = smem_u32(ahead) + threadIdx.x * 16, octet = blockDim.x * 16;   // [stage][row][octet][thread]
+  const uint32_t stage_bytes = octet * 2 * TPT;
+  const __nv_bfloat16* fetch_row[TPT];
+  int fetch_head = from;
+  uint32_t fetch_to = mine;
+  auto fetch_start = [&]() {                         // the row in the tensor that fetch_head is in
+    const int kind = fetch_head < k_from ? 0 : fetch_head < v_from ? 1 : 2;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(kind == 0 ? a.Q : kind == 1 ? a.K : a.V) +
+                               (long long)(fetch_head - (kind == 0 ? 0 : kind == 1 ? k_from : v_from)) * D;
     const long long ld = kind == 0 ? a.ldq : kind == 1 ? a.ldk : a.ldv;
-    uint4 u[HG][TPT], v[HG][TPT];
 #pragma unroll
-    for (int h = 0; h < HG; ++h)
+    for (int q = 0; q < TPT; ++q) {
+      const int t = t0 + q * step;
+      fetch_row[q] = src + (long long)(it.row0 + (t < n ? t : 0)) * ld;
+    }
+  };
+  auto fetch = [&]() {
+    if (fetch_head < to) {
+      const bool value = fetch_head >= v_from;
+      const int d0 = value ? dn0 : dr0, d1 = value ? dn1 : dr1;
 #pragma unroll
       for (int q = 0; q < TPT; ++q) {
-        const int t = t0 + q * step;
-        u[h][q] = v[h][q] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < heads && t < it.n) {
-          const __nv_bfloat16* x = src + (long long)(it.row0 + t) * ld + (long long)(h0 + h) * D;
-          u[h][q] = *reinterpret_cast<const uint4*>(x + d0);
-          v[h][q] = *reinterpret_cast<const uint4*>(x + d1);
-        }
+        const bool read = t0 + q * step < n;
+        cp_async_16(fetch_to + q * 2 * octet, fetch_row[q] + d0, read);
+        cp_async_16(fetch_to + q * 2 * octet + octet, fetch_row[q] + d1, read);
+        fetch_row[q] += D;
       }
-    if (kind != 2 && !angles) {
-      angles = true;
+      ++fetch_head;
+      if (fetch_head == k_from || fetch_head == v_from) fetch_start();
+      fetch_to = fetch_to + stage_bytes == mine + STAGES * stage_bytes ? mine : fetch_to + stage_bytes;
+    }
+    cp_async_commit();                               // one group a head, also an empty one
+  };
+  fetch_start();
 #pragma unroll
-      for (int q = 0; q < TPT; ++q) {
-        const int t = min(t0 + q * step, it.n - 1);
-        const long long at = (long long)(it.pos0 + t) * (D / 2) + c * 8;
+  for (int i = 0; i < STAGES; ++i) fetch();
+  uint64_t co[TPT][4], si[TPT][4];                   // angles of eight pairs, two in each
+  if (from < v_from) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float4 x = *reinterpret_cast<const float4*>(a.cos + at + 4 * i);
-          const float4 y = *reinterpret_cast<const float4*>(a.sin + at + 4 * i);
-          co[q][2 * i] = pair(x.x, x.y);
-          co[q][2 * i + 1] = pair(x.z, x.w);
-          si[q][2 * i] = pair(y.x, y.y);
-          si[q][2 * i + 1] = pair(y.z, y.w);
-        }
+    for (int q = 0; q < TPT; ++q) {
+      const int t = min(t0 + q * step, n - 1);
+      const long long at = (long long)(it.pos0 + t) * (D / 2) + c * 8;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(a.cos + at + 4 * i);
+        const float4 y = *reinterpret_cast<const float4*>(a.sin + at + 4 * i);
+        co[q][2 * i] = pair(x.x, x.y);
+        co[q][2 * i + 1] = pair(x.z, x.w);
+        si[q][2 * i] = pair(y.x, y.y);
+        si[q][2 * i + 1] = pair(y.z, y.w);
       }
     }
-    // the 16 values, turned: neighbours in pairs, d0's octet then d1's
-    auto values = [&](int h, int q, uint64_t (&x)[8]) {
-      if (kind == 2) {
+  }
+  int stage = 0, turn = 0;
+  // the next head's 16 values, turned: neighbours in pairs, d0's octet then d1's
+  auto values = [&](auto turned, auto by_halves, uint64_t (&x)[TPT][8]) {
+    cp_async_wait<STAGES - 1>();
+    const uint4* in = reinterpret_cast<const uint4*>(ahead + stage * stage_bytes) + threadIdx.x;
+#pragma unroll
+    for (int q = 0; q < TPT; ++q) {
+      const uint4 u = in[q * 2 * blockDim.x], v = in[(q * 2 + 1) * blockDim.x];
+      if constexpr (!decltype(turned)::value || decltype(by_halves)::value) {
         uint64_t p[4], w[4];
-        unpack8(u[h][q], p);
-        unpack8(v[h][q], w);
+        unpack8(u, p);
+        unpack8(v, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[i] = p[i];
-          x[4 + i] = w[i];
-        }
-      } else if (halves) {
-        uint64_t p[4], w[4];
-        unpack8(u[h][q], p);
-        unpack8(v[h][q], w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = sub2(mul2(p[i], co[q][i]), mul2(w[i], si[q][i]));
-          x[4 + i] = add2(mul2(w[i], co[q][i]), mul2(p[i], si[q][i]));
+          if constexpr (decltype(turned)::value) {
+            x[q][i] = sub2(mul2(p[i], co[q][i]), mul2(w[i], si[q][i]));
+            x[q][4 + i] = add2(mul2(w[i], co[q][i]), mul2(p[i], si[q][i]));
+          } else {
+            x[q][i] = p[i];
+            x[q][4 + i] = w[i];
+          }
         }
       } else {
         uint64_t even[4], odd[4];
-        split8(u[h][q], reinterpret_cast<uint64_t(&)[2]>(even[0]), reinterpret_cast<uint64_t(&)[2]>(odd[0]));
-        split8(v[h][q], reinterpret_cast<uint64_t(&)[2]>(even[2]), reinterpret_cast<uint64_t(&)[2]>(odd[2]));
+        split8(u, reinterpret_cast<uint64_t(&)[2]>(even[0]), reinterpret_cast<uint64_t(&)[2]>(odd[0]));
+        split8(v, reinterpret_cast<uint64_t(&)[2]>(even[2]), reinterpret_cast<uint64_t(&)[2]>(odd[2]));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 y = halves_of(sub2(mul2(even[i], co[q][i]), mul2(odd[i], si[q][i])));
           const float2 z = halves_of(add2(mul2(odd[i], co[q][i]), mul2(even[i], si[q][i])));
-          x[2 * i] = pair(y.x, z.x);
-          x[2 * i + 1] = pair(y.y, z.y);
+          x[q][2 * i] = pair(y.x, z.x);
+          x[q][2 * i + 1] = pair(y.y, z.y);
         }
       }
-    };
-    if (kind == 0) {
-#pragma unroll
-      for (int h = 0; h < HG; ++h)
-#pragma unroll
-        for (int q = 0; q < TPT; ++q) {
-          const int t = t0 + q * step;
-          if (h >= heads || t >= it.n) continue;
-          uint64_t x[8];
-          values(h, q, x);
-          uint32_t y[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 f = halves_of(x[i]);
-            y[i] = pack2(f.x, f.y);
-          }
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.Qo) + (long long)(it.row0 + t) * a.ldqo +
-                             (long long)(h0 + h) * D;
-          *reinterpret_cast<uint4*>(o + d0) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(o + d1) = make_uint4(y[4], y[5], y[6], y[7]);
-        }
-      continue;
     }
-    if (g == -2) g = kv_page(a.c, it.b, it.col, a.status, kSiteKvAppend);
-    if (g < 0) return;                             // the same for the whole block; no queries follow
-    float* scale = (kind == 1 ? a.c.ks : a.c.vs) + (long long)g * a.c.H + h0;
-    float s0[HG];
+    stage = (stage + 1) % STAGES;
+    fetch();                                         // into the slots just read
+  };
+  auto queries = [&](auto by_halves, int h0, int h1) {
+    constexpr bool H = decltype(by_halves)::value;
+    const int d0 = H ? c * 8 : dn0, d1 = H ? d0 + D / 2 : dn1;
+    __nv_bfloat16* out[TPT];
 #pragma unroll
-    for (int h = 0; h < HG; ++h) s0[h] = held > 0 && h < heads ? scale[h] : 0.f;
-#pragma unroll
-    for (int h = 0; h < HG; ++h) {
-      float m = 0.f;
+    for (int q = 0; q < TPT; ++q)
+      out[q] = static_cast<__nv_bfloat16*>(a.Qo) + (long long)(it.row0 + t0 + q * step) * a.ldqo + (long long)h0 * D;
+    for (int h = h0; h < h1; ++h) {
+      uint64_t x[TPT][8];
+      values(std::true_type{}, by_halves, x);
 #pragma unroll
       for (int q = 0; q < TPT; ++q) {
-        uint64_t x[8];
-        values(h, q, x);
+        uint32_t y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 f = halves_of(x[i]);
+          const float2 f = halves_of(x[q][i]);
+          y[i] = pack2(f.x, f.y);
+        }
+        if (t0 + q * step < n) {
+          *reinterpret_cast<uint4*>(out[q] + d0) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(out[q] + d1) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        out[q] += D;
+      }
+    }
+  };
+  // Key or value heads h0 .. h1-1 of page g.  Three words take the magnitudes by
+  // turns: one fills, one is read, one is set back.
+  auto stored = [&](auto turned, auto by_halves, uint8_t* all, float* scales, int g, int h0, int h1) {
+    constexpr bool H = decltype(turned)::value && decltype(by_halves)::value;
+    const int d0 = H ? c * 8 : dn0, d1 = d0 + D / 2;
+    uint8_t* codes = all + (long long)g * a.c.ps + (long long)h0 * a.c.hs;
+    float* scale = scales + (long long)g * a.c.H + h0;
+    const long long at = (long long)(held + t0) * a.c.ts + d0, row_step = (long long)step * a.c.ts;
+    for (int h = h0; h < h1; ++h, codes += a.c.hs, ++scale) {
+      const float s0 = held > 0 ? *scale : 0.f;
+      uint64_t x[TPT][8];
+      values(turned, by_halves, x);
+      float m = 0.f;
+#pragma unroll
+      for (int q = 0; q < TPT; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = halves_of(x[q][i]);
           m = max3(m, fabsf(f.x), fabsf(f.y));
         }
-      }
       // magnitudes order as their bits; the atomic is a maximum, so its order is free
       const unsigned w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-      if (threadIdx.x % 32 == 0) atomicMax(&big[h], w);
-    }
-    __syncthreads();
-    float s[HG];
-#pragma unroll
-    for (int h = 0; h < HG; ++h) s[h] = fmaxf(s0[h], kv_scale_for<FMT>(__uint_as_float(big[h])));
-    __syncthreads();                               // big has been read, and every old scale
-    if (threadIdx.x < HG) big[threadIdx.x] = 0;
-    uint8_t* codes = (kind == 1 ? a.c.k : a.c.v) + (long long)g * a.c.ps + (long long)h0 * a.c.hs;
-#pragma unroll
-    for (int h = 0; h < HG; ++h) {
-      if (h >= heads) break;
-      const float r = kv_recip(s[h]);
+      if (threadIdx.x % 32 == 0) atomicMax(&big[turn], w);
+      __syncthreads();                               // and every thread has the old scale
+      const float s = fmaxf(s0, kv_scale_for<FMT>(__uint_as_float(big[turn]))), r = kv_recip(s);
+      const int back = turn == 0 ? 2 : turn - 1;
+      turn = turn == 2 ? 0 : turn + 1;
+      if (threadIdx.x == 0) {
+        big[back] = 0;
+        *scale = s;
+      }
+      const uint64_t r2 = pair(r, r);
 #pragma unroll
       for (int q = 0; q < TPT; ++q) {
-        const int t = t0 + q * step;
-        if (t >= it.n) continue;
-        uint64_t x[8];
-        values(h, q, x);
-        uint8_t* o = codes + (long long)h * a.c.hs + (long long)(held + t) * a.c.ts;
-        const uint64_t r2 = pair(r, r);
-        const uint2 lo = make_uint2(codes4<FMT>(x[0], x[1], r2), codes4<FMT>(x[2], x[3], r2));
-        const uint2 hi = make_uint2(codes4<FMT>(x[4], x[5], r2), codes4<FMT>(x[6], x[7], r2));
-        if (halves) {
-          *reinterpret_cast<uint2*>(o + d0) = lo;
-          *reinterpret_cast<uint2*>(o + d1) = hi;
-        } else {
-          *reinterpret_cast<uint4*>(o + d0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        const uint2 lo = make_uint2(codes4<FMT>(x[q][0], x[q][1], r2), codes4<FMT>(x[q][2], x[q][3], r2));
+        const uint2 hi = make_uint2(codes4<FMT>(x[q][4], x[q][5], r2), codes4<FMT>(x[q][6], x[q][7], r2));
+        if (t0 + q * step < n) {
+          uint8_t* o = codes + at + q * row_step;
+          if constexpr (H) {
+            *reinterpret_cast<uint2*>(o) = lo;
+            *reinterpret_cast<uint2*>(o + (d1 - d0)) = hi;
+          } else {
+            *reinterpret_cast<uint4*>(o) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          }
         }
       }
-      if (threadIdx.x == 0) scale[h] = s[h];
-      if (held > 0 && s[h] > s0[h]) {
+      if (held > 0 && s > s0) {
         for (int e = threadIdx.x; e < held * (D / 4); e += blockDim.x) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(codes + (long long)h * a.c.hs + (long long)(e / (D / 4)) * a.c.ts) +
-                        e % (D / 4);
-          *w = recode4<FMT>(*w, s0[h], r);
+          uint32_t* w4 = reinterpret_cast<uint32_t*>(codes + (long long)(e / (D / 4)) * a.c.ts) + e % (D / 4);
+          *w4 = recode4<FMT>(*w4, s0, r);
         }
       }
     }
-    __syncthreads();                               // big is 0 again
+  };
+  using std::false_type;
+  using std::true_type;
+  if (from < k_from) {
+    if (a.interleaved) queries(false_type{}, from, min(to, k_from));
+    else queries(true_type{}, from, min(to, k_from));
   }
+  const int g = to > k_from ? kv_page(a.c, it.b, it.col, a.status, kSiteKvAppend) : -1;
+  if (g >= 0) {                                      // the same for the whole block
+    const int k0 = max(from, k_from), k1 = min(to, v_from), v0 = max(from, v_from);
+    if (k0 < k1) {
+      if (a.interleaved) stored(true_type{}, false_type{}, a.c.k, a.c.ks, g, k0 - k_from, k1 - k_from);
+      else stored(true_type{}, true_type{}, a.c.k, a.c.ks, g, k0 - k_from, k1 - k_from);
+    }
+    if (v0 < to) stored(false_type{}, false_type{}, a.c.v, a.c.vs, g, v0 - v_from, to - v_from);
+  }
+  cp_async_wait<0>();                                // nothing lands after the block has left
 }
 
 template <class Kernel, class... More>
-int launch(Kernel kernel, dim3 grid, dim3 block, const KvAppendArgs& a, cudaStream_t s, More... more) {
+int launch(Kernel kernel, dim3 grid, dim3 block, size_t smem, const KvAppendArgs& a, cudaStream_t s, More... more) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, more...);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int FMT, int D, int TPT>
+int launch_pages(const KvAppendArgs& a, long long items, int threads, int num_sms, cudaStream_t s) {
+  static std::atomic<uint64_t> smem_set{0};
+  cudaError_t e = set_smem_once(smem_set, kv_append_pages_kernel<FMT, D, TPT>, STAGES * TPT * 32 * PAGE_THREADS);
+  if (e != cudaSuccess) return e;
+  // heads of a block: as many as leave the GPU four rounds of blocks
+  const int heads = a.Hq + 2 * a.c.H;
+  const long long resident = (long long)num_sms * (2 * PAGE_THREADS / threads);
+  long long groups = (4 * resident + items - 1) / items;
+  groups = groups < 1 ? 1 : groups > (heads + 1) / 2 ? (heads + 1) / 2 : groups;
+  const int per = (int)((heads + groups - 1) / groups);
+  return launch(kv_append_pages_kernel<FMT, D, TPT>, dim3((unsigned)items, (unsigned)((heads + per - 1) / per)),
+                dim3((unsigned)threads), (size_t)STAGES * TPT * 32 * threads, a, s, per);
 }
 
 template <int FMT, int D>
@@ -579,18 +635,15 @@ int launch_fast(const KvAppendArgs& a, long long items, int num_sms, cudaStream_
   const long long pages = (a.max_new + a.c.P - 2) / a.c.P + 1;
   if (a.max_new <= 8 && a.c.seqs * pages <= 65535) {
     const dim3 grid((unsigned)((heads + DEC_WARPS - 1) / DEC_WARPS), (unsigned)(a.c.seqs * pages)), block(DEC_WARPS * 32);
-    if (a.max_new == 1) return launch(kv_append_tokens_kernel<FMT, D, 1>, grid, block, a, s, (int)pages);
-    if (a.max_new == 2) return launch(kv_append_tokens_kernel<FMT, D, 2>, grid, block, a, s, (int)pages);
-    return launch(kv_append_tokens_kernel<FMT, D, 8>, grid, block, a, s, (int)pages);
+    if (a.max_new == 1) return launch(kv_append_tokens_kernel<FMT, D, 1>, grid, block, 0, a, s, (int)pages);
+    if (a.max_new == 2) return launch(kv_append_tokens_kernel<FMT, D, 2>, grid, block, 0, a, s, (int)pages);
+    return launch(kv_append_tokens_kernel<FMT, D, 8>, grid, block, 0, a, s, (int)pages);
   }
-  // a page's threads, 16 values of a row each, at most 512 with several rows a thread
-  const int threads = a.c.P * (D / 16), tpt = threads <= 512 ? 1 : threads / 512;
-  const int groups = (a.Hq + HG - 1) / HG + 2 * ((a.c.H + HG - 1) / HG);
-  const int rounds = items * groups >= 32ll * num_sms ? 4 : items * groups >= 16ll * num_sms ? 2 : 1;
-  const dim3 grid((unsigned)items, (unsigned)((groups + rounds - 1) / rounds)), block((unsigned)(threads / tpt));
-  if (tpt == 1) return launch(kv_append_pages_kernel<FMT, D, 1>, grid, block, a, s, rounds);
-  if constexpr (D == 128) return launch(kv_append_pages_kernel<FMT, D, 2>, grid, block, a, s, rounds);   // P 128
-  return cudaErrorInvalidValue;
+  // a page's threads, 16 values of a row each, two rows where that is above 512
+  const int threads = a.c.P * (D / 16), tpt = threads <= PAGE_THREADS ? 1 : threads / PAGE_THREADS;
+  if constexpr (D == 128)
+    if (tpt == 2) return launch_pages<FMT, D, 2>(a, items, threads / 2, num_sms, s);
+  return launch_pages<FMT, D, 1>(a, items, threads, num_sms, s);
 }
 
 }  // namespace
@@ -605,8 +658,8 @@ int launch_kv_append(const KvAppendArgs& a, bool fast, int num_sms, cudaStream_t
     return a.c.D == 128 ? launch_fast<kKvInt8, 128>(a, items, num_sms, s) : launch_fast<kKvInt8, 64>(a, items, num_sms, s);
   }
   const dim3 grid((unsigned)items, (unsigned)(a.Hq + 2 * a.c.H));
-  if (a.c.fmt == kKvE4M3) return launch(kv_append_generic_kernel<kKvE4M3>, grid, dim3(128), a, s);
-  return launch(kv_append_generic_kernel<kKvInt8>, grid, dim3(128), a, s);
+  if (a.c.fmt == kKvE4M3) return launch(kv_append_generic_kernel<kKvE4M3>, grid, dim3(128), 0, a, s);
+  return launch(kv_append_generic_kernel<kKvInt8>, grid, dim3(128), 0, a, s);
 }
 
 }  // namespace g3
