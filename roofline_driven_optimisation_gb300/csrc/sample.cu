@@ -308,15 +308,20 @@ struct Place {
 };
 
 struct alignas(16) Cluster {
-  ull mass[2][FT];          // histograms by turns: one is read by the cluster while the other fills
-  unsigned count[2][FT];
+  union {
+    // the search's histograms by turns: one is read by the cluster while the other fills
+    struct {
+      unsigned count[2][FT], mass[2][3][FT];
+    };
+    ull local[LOCAL];       // the list's: gathered or sorted values
+  };
+  unsigned bins[FT];        // the threshold's histogram
   ull list[LIST];           // first block: candidates, key << 32 | ~index
-  ull local[LOCAL];
   ull all[MAX_C * FW];      // every warp's kept mass
   ull warp_mass[FW];        // read by the cluster
   unsigned warp_count[FW];  // read by the cluster
   unsigned red[2][FW];
-  unsigned top;             // read by the cluster
+  unsigned top, low;        // read by the cluster
   unsigned lo[2], hi[2];    // read by the cluster, by turns
   unsigned list_n;          // first block: candidates of the cluster
   unsigned seg_n[MAX_C];    // first block: of each block, in parts of the list
@@ -324,7 +329,7 @@ struct alignas(16) Cluster {
   ulonglong2 few_mass[SMALL_K];   // index, mass
   unsigned local_n, local_at;
   unsigned best, n_above;
-  ull m_above;
+  ull m_above, bound;
   ull scan_m[FW];
   unsigned scan_c[FW];
   Place cut;                // first block's, or the tie's owner's: read by the cluster
@@ -412,20 +417,22 @@ __device__ __forceinline__ void sort_list(Cluster& sh, int n2) {
     }
 }
 
+// Zeros behind the list's first m entries, up to a power of two, which is returned
+__device__ __forceinline__ int pad_list(Cluster& sh, int m) {
+  int n2 = 64;
+  while (n2 < m) n2 <<= 1;
+  for (int i = m + threadIdx.x; i < n2; i += FT) sh.list[i] = 0;
+  __syncthreads();
+  return n2;
+}
+
 // The draw where the first block's list holds every token that can be kept: both
 // cuts in rank order, then the running mass in index order.
 __device__ __forceinline__ void draw_from_list(const SampleArgs& a, Cluster& sh, int r, int n, int k, float p, float least,
                                float u, float t) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   constexpr int PER = TOP_K_LIST / FT;               // places of a thread
-  auto pad = [&](int m) {                            // zeros up to a power of two
-    int n2 = 64;
-    while (n2 < m) n2 <<= 1;
-    for (int i = m + tid; i < n2; i += FT) sh.list[i] = 0;
-    __syncthreads();
-    return n2;
-  };
-  sort_list(sh, pad(n));
+  sort_list(sh, pad_list(sh, n));
   const unsigned top = (unsigned)(sh.list[0] >> 32);
   const Row row{key_logit(top), __fdiv_rn(1.f, t)};
   int kept = min(n, k);
@@ -469,8 +476,7 @@ __device__ __forceinline__ void draw_from_list(const SampleArgs& a, Cluster& sh,
     const ull x = sh.list[i];
     sh.list[i] = (x << 32) | (x >> 32);
   }
-  const int n2 = pad(kept);
-  sort_list(sh, n2);
+  sort_list(sh, pad_list(sh, kept));
   ull m[PER], before = 0;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
@@ -504,14 +510,14 @@ __device__ __forceinline__ void draw_from_list(const SampleArgs& a, Cluster& sh,
   }
 }
 
-// The bin of sh.count[0] in which the k-th count is, FT if there are fewer; one warp
+// The bin of sh.bins in which the k-th count is, FT if there are fewer; one warp
 __device__ __forceinline__ unsigned kth_bin(const Cluster& sh, int k) {
   constexpr int PER = FT / 32;
   const int lane = threadIdx.x % 32;
   unsigned c[PER], own = 0;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
-    c[q] = sh.count[0][lane * PER + q];
+    c[q] = sh.bins[lane * PER + q];
     own += c[q];
   }
   unsigned before = own;
@@ -563,7 +569,7 @@ __device__ __forceinline__ void draw_from_few(const SampleArgs& a, Cluster& sh, 
     const float ltop = key_logit(hi), range = ltop - key_logit(lo);
     const float scale = range > 0.f && range < INFINITY ? 511.9f / range : 0.f;
     auto bin = [&](ull x) { return min(FT - 1, (int)((ltop - key_logit((unsigned)(x >> 32))) * scale)); };
-    for (int i = tid; i < n; i += FT) atomicAdd(&sh.count[0][bin(list[i])], 1u);
+    for (int i = tid; i < n; i += FT) atomicAdd(&sh.bins[bin(list[i])], 1u);
     __syncthreads();
     if (warp == 0) {
       const unsigned best = kth_bin(sh, k);
@@ -699,10 +705,7 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
       f(x.w, i + 96);
     }
   };
-  for (int i = tid; i < FT; i += FT) {
-    sh.mass[0][i] = 0;
-    sh.count[0][i] = 0;
-  }
+  sh.bins[tid] = 0;
   if (tid == 0) {
     sh.list_n = 0;
     sh.local_n = 0;
@@ -725,6 +728,15 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
   if (tid == 0) sh.top = top;
 
   const bool cuts = !greedy && ((k > 0 && k < a.vocab) || !(p >= 1.f));
+  auto block_low = [&]() {                           // the block's smallest key above -inf, for the search
+    unsigned low = 0xffffffffu;
+    each([&](unsigned key, int) { low = min(low, key > kKeyNegInf ? key : 0xffffffffu); });
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (lane == 0) sh.warp_count[warp] = low;
+    __syncthreads();
+    low = __reduce_min_sync(0xffffffffu, sh.warp_count[lane % FW]);
+    if (tid == 0) sh.low = low;
+  };
   const bool by_list = cuts && k > 0 && k <= TOP_K_LIST, small = k <= SMALL_K;
   if (by_list) {
     // ---- candidates for the first k ranks.  Every group's largest logit is an
@@ -742,7 +754,7 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         if (group[q] >= floor_key)
-          atomicAdd(&sh.count[0][min(FT - 1, (int)((ltop - key_logit(group[q])) * scale))], 1u);
+          atomicAdd(&sh.bins[min(FT - 1, (int)((ltop - key_logit(group[q])) * scale))], 1u);
       __syncthreads();
       if (warp == 0) {
         const unsigned best = kth_bin(sh, k);
@@ -752,7 +764,7 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
       // the lower edge of that bin, less what the bins' rounding may be off
       if (sh.best < FT)
         bound = max(floor_key, scale > 0.f ? order_key(ltop - (sh.best + 1.01f) / scale) : gmin);
-      sh.count[0][tid] = 0;
+      sh.bins[tid] = 0;
     }
     if (C > 1) cluster_wait();
     ull* list = in_block(&sh.list[0], 0);
@@ -781,8 +793,9 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
       if (n <= LOCAL && at + n <= LIST)
         for (unsigned i = tid; i < n; i += FT) list[at + i] = sh.local[i];
     }
-  } else if (C > 1) {
-    cluster_wait();
+  } else {
+    if (cuts) block_low();
+    if (C > 1) cluster_wait();
   }
   sync_cluster(C);
   if (by_list) {
@@ -850,69 +863,130 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
     sync_cluster(C);                                 // warp_count has been read
   }
   if (cuts) {
-    // ---- the general search.  First bins even in the logit over the range that has
-    // mass, then bins even in the key, until one key is left
-    int turn = 0;                                    // histogram in use; it is zero
-    unsigned low = top;                              // the lowest key above -inf
-    each([&](unsigned key, int) {
-      if (key > kKeyNegInf) low = min(low, key);
-    });
-    low = __reduce_min_sync(0xffffffffu, low);
-    if (lane == 0) sh.warp_count[warp] = low;
-    sync_cluster(C);
-    if (tid < C * FW) low = *in_block(&sh.warp_count[tid % FW], tid / FW);
-    low = __reduce_min_sync(0xffffffffu, low);
-    if (lane == 0) sh.red[0][warp] = low;
-    __syncthreads();
-    for (int w = 0; w < FW; ++w) low = min(low, sh.red[0][w]);
-    sync_cluster(C);                                 // warp_count has been read
-    auto search = [&](auto keep) {
+    // ---- the general search: bins even in the logit over the range that has mass; the
+    // tokens of the bin with the cut are sorted in the first block's list, or, if
+    // they are too many (equal logits), binned again by their keys until one is left
+    if (by_list) block_low();
+    if (by_list) sync_cluster(C);
+    unsigned low = sh.low;
+    for (int c = 0; c < C; ++c) low = min(low, *in_block(&sh.low, c));
+    // The last place kept by count (the first k) or by mass (less than p of all before)
+    auto search = [&](bool by_count) {
       const float range = fminf(ZERO_Z * t, row.top - key_logit(low));
       const float scale = range > 0.f ? 511.9f / range : 0.f;
       auto first_bin = [&](unsigned key) { return min(FT - 1, (int)((row.top - key_logit(key)) * scale)); };
       unsigned n_above = 0, lo = 0, hi = 0;
-      ull m_above = 0;
-      int bin0 = -1, shift = 0;
+      ull m_above = 0, bound = 0;
+      int bin0 = -1, shift = 0, turn = 0;            // turn: the histogram in use, zero when its turn comes
+      __syncthreads();                               // its memory may have held a list
+      sh.count[0][tid] = 0;
+      for (int w = 0; w < 3; ++w) sh.mass[0][w][tid] = 0;
+      __syncthreads();
+      // the present level's bin of a token, -1 if it is not one of those in question
+      auto bin = [&](unsigned key, int i) {
+        if (key <= kKeyNegInf || !cut.keeps(key, i)) return -1;
+        if (bin0 < 0) return first_bin(key);
+        return key < lo || key > hi || first_bin(key) != bin0 ? -1 : (int)((hi - key) >> shift);
+      };
+      auto keep = [&](unsigned c, ull m) { return by_count ? c < (unsigned)k : c == 0 || m < bound; };
       while (true) {
-        // histogram
+        // Histogram.  A mass has 41 bits and shared memory adds 32 at a time: three
+        // words of 14, 13 and 14 bits, whose sums over a block's 45056 tokens at most
+        // stay below 2^32.
         each([&](unsigned key, int i) {
-          if (key <= kKeyNegInf || !cut.keeps(key, i)) return;
-          if (bin0 >= 0 && (key < lo || key > hi || first_bin(key) != bin0)) return;
-          const ull m = mass_at(key);
+          const int x = bin(key, i);
+          const ull m = x < 0 ? 0 : mass_at(key);
           if (m == 0) return;
-          const int b = bin0 < 0 ? first_bin(key) : (int)((hi - key) >> shift);
-          atomicAdd(&sh.count[turn][b], 1u);
-          atomicAdd(&sh.mass[turn][b], m);
+          atomicAdd(&sh.count[turn][x], 1u);
+          atomicAdd(&sh.mass[turn][0][x], (unsigned)m & 0x3fffu);
+          if (m >> 14) atomicAdd(&sh.mass[turn][1][x], (unsigned)(m >> 14) & 0x1fffu);
+          if (m >> 27) atomicAdd(&sh.mass[turn][2][x], (unsigned)(m >> 27));
         });
         sync_cluster(C);
-        sh.count[turn ^ 1][tid] = 0;                 // the last turn's: every block has read it by now
-        sh.mass[turn ^ 1][tid] = 0;
-        unsigned c = 0;
+        // the last turn's: every block has read it by now
+        sh.count[turn ^ 1][tid] = 0;
+        for (int w = 0; w < 3; ++w) sh.mass[turn ^ 1][w][tid] = 0;
+        unsigned c = 0, earlier = 0;                 // earlier: of the blocks before this one
         ull m = 0;
+#pragma unroll 4
         for (int q = 0; q < C; ++q) {
+          if (q == rank) earlier = c;
           c += in_block(&sh.count[turn][0], q)[tid];
-          m += in_block(&sh.mass[turn][0], q)[tid];
+          const unsigned* w = in_block(&sh.mass[turn][0][0], q) + tid;
+          m += (ull)w[0] + ((ull)w[FT] << 14) + ((ull)w[2 * FT] << 27);
         }
         const unsigned own = c;
         block_prefix(sh, c, m);
+        if (tid == 0) sh.best = 0;
+        if (bin0 < 0 && !by_count) {
+          if (warp == 0) {
+            ull total = 0;
+            for (int w = 0; w < FW; ++w) total += sh.scan_m[w];
+            const ull x = whole_bound(__dmul_rn((double)p, __ull2double_rn(total)));
+            if (lane == 0) sh.bound = x;
+          }
+          __syncthreads();
+          bound = sh.bound;
+        } else {
+          __syncthreads();
+        }
         c += n_above;
         m += m_above;
-        if (tid == 0) sh.best = 0;
-        __syncthreads();
         if (own && keep(c, m)) atomicMax(&sh.best, (unsigned)tid);
         __syncthreads();
         if (tid == (int)sh.best) {
           sh.n_above = c;
           sh.m_above = m;
           sh.red[0][0] = own;
+          sh.local_at = earlier;
+          sh.local_n = 0;
         }
         __syncthreads();
-        const unsigned best = sh.best, n_equal = sh.red[0][0];
+        const int best = (int)sh.best;
+        const unsigned n_equal = sh.red[0][0];
         n_above = sh.n_above;
         m_above = sh.m_above;
+        if (n_equal <= TOP_K_LIST) {
+          // few enough to sort: the blocks' tokens of that bin, one block's after another's
+          ull* list = in_block(&sh.list[0], 0) + sh.local_at;
+          each([&](unsigned key, int i) {
+            if (bin(key, i) == best && mass_at(key)) list[atomicAdd(&sh.local_n, 1u)] = ((ull)key << 32) | (unsigned)~i;
+          });
+          sync_cluster(C);
+          if (rank == 0) {
+            sort_list(sh, pad_list(sh, (int)n_equal));
+            constexpr int PER = TOP_K_LIST / FT;
+            ull own_m[PER], before = 0;
+#pragma unroll
+            for (int q = 0; q < PER; ++q) {
+              const int i = tid * PER + q;
+              own_m[q] = i < (int)n_equal ? mass_at((unsigned)(sh.list[i] >> 32)) : 0;
+              before += own_m[q];
+            }
+            unsigned none = 0;
+            block_prefix(sh, none, before);
+            before += m_above;
+            int last = 0;
+#pragma unroll
+            for (int q = 0; q < PER; ++q) {
+              const int i = tid * PER + q;
+              if (i < (int)n_equal && keep(n_above + i, before)) last = i;
+              before += own_m[q];
+            }
+            last = __reduce_max_sync(0xffffffffu, last);
+            if (lane == 0) sh.red[0][warp] = last;
+            __syncthreads();
+            last = __reduce_max_sync(0xffffffffu, (int)sh.red[0][lane % FW]);
+            const ull x = sh.list[last];
+            if (tid < C) *in_block(&sh.cut, tid) = Place{(unsigned)(x >> 32), (int)~(unsigned)x};
+          }
+          sync_cluster(C);
+          cut = sh.cut;
+          return;
+        }
         if (bin0 < 0) {
           // the keys in that bin
-          bin0 = (int)best;
+          bin0 = best;
           lo = 0xffffffffu;
           hi = 0;
           each([&](unsigned key, int i) {
@@ -943,7 +1017,7 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
             hi = max(hi, *in_block(&sh.hi[0], q));
           }
         } else {
-          const unsigned from = best << shift;       // bins are counted from hi down
+          const unsigned from = (unsigned)best << shift;   // bins are counted from hi down
           const unsigned span = (1u << shift) - 1u;
           hi -= from;
           lo = max(lo, hi >= span ? hi - span : 0u);
@@ -990,24 +1064,8 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
         shift = max(0, 32 - __clz(hi - lo) - 9);
       }
     };
-    if (k > 0 && k < a.vocab) search([&](unsigned c, ull) { return c < (unsigned)k; });
-    if (!(p >= 1.f)) {
-      ull m = 0;
-      each([&](unsigned key, int i) {
-        if (cut.keeps(key, i)) m += mass_at(key);
-      });
-      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-      if (lane == 0) sh.warp_mass[warp] = m;
-      sync_cluster(C);
-      m = tid < C * FW ? in_block(&sh.warp_mass[0], tid / FW)[tid % FW] : 0;
-      unsigned none = 0;
-      block_prefix(sh, none, m);
-      ull total = 0;
-      for (int w = 0; w < FW; ++w) total += sh.scan_m[w];
-      const ull bound = whole_bound(__dmul_rn((double)p, __ull2double_rn(total)));
-      sync_cluster(C);                               // warp_mass has been read
-      search([&](unsigned c, ull before) { return c == 0 || before < bound; });
-    }
+    if (k > 0 && k < a.vocab) search(true);
+    if (!(p >= 1.f)) search(false);
   }
 
   // ---- the draw: every warp's kept mass, then the warp in which the target falls
