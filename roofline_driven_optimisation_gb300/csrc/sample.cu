@@ -293,10 +293,10 @@ constexpr int FT = 512, FW = FT / 32;         // threads and warps of a block
 constexpr int MAX_C = 8;
 constexpr int MAX_Q = 22;                     // quads of a thread: 8 * FT * 88 logits, 180 KB of keys
 constexpr int LIST = 2048;                    // candidates that the first block can sort
-constexpr int LOCAL = 2048;                   // candidates that a block can gather
+constexpr int LOCAL = 2048;                   // room for a list's copies
 constexpr int SMALL_K = 64;                   // largest top_k whose ranks fit two to a lane of one warp
 constexpr int SEG = LIST / MAX_C;             // a block's part of the list then
-constexpr int TOP_K_LIST = 1024;              // largest top_k for the candidate list: half of the 4 * FT groups
+constexpr int TOP_K_LIST = 1024;              // ranks that the first block can draw from: two a thread
 constexpr int SAMPLE_Q = 4;                   // quads of a thread before a row takes more blocks
 constexpr float ZERO_Z = 28.f;                // expf(-28) < 2^-40: no mass
 
@@ -313,7 +313,7 @@ struct alignas(16) Cluster {
     struct {
       unsigned count[2][FT], mass[2][3][FT];
     };
-    ull local[LOCAL];       // the list's: gathered or sorted values
+    ull local[LOCAL];       // copies of a list
   };
   unsigned bins[FT];        // the threshold's histogram
   ull list[LIST];           // first block: candidates, key << 32 | ~index
@@ -323,7 +323,6 @@ struct alignas(16) Cluster {
   unsigned red[2][FW];
   unsigned top, low;        // read by the cluster
   unsigned lo[2], hi[2];    // read by the cluster, by turns
-  unsigned list_n;          // first block: candidates of the cluster
   unsigned seg_n[MAX_C];    // first block: of each block, in parts of the list
   ull few[SMALL_K];         // the first ranks
   ulonglong2 few_mass[SMALL_K];   // index, mass
@@ -707,10 +706,9 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
   };
   sh.bins[tid] = 0;
   if (tid == 0) {
-    sh.list_n = 0;
     sh.local_n = 0;
   }
-  if (C > 1) cluster_arrive();                       // list_n is ready
+  if (C > 1) cluster_arrive();                       // this block is there
 
   // ---- the block's largest key, and its groups' smallest above -inf
   unsigned top = max(max(group[0], group[1]), max(group[2], group[3])), gmin = 0xffffffffu;
@@ -737,7 +735,7 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
     low = __reduce_min_sync(0xffffffffu, sh.warp_count[lane % FW]);
     if (tid == 0) sh.low = low;
   };
-  const bool by_list = cuts && k > 0 && k <= TOP_K_LIST, small = k <= SMALL_K;
+  const bool by_list = cuts && k > 0 && k <= SMALL_K;
   if (by_list) {
     // ---- candidates for the first k ranks.  Every group's largest logit is an
     // element, so the k-th largest of them bounds the block's k-th rank from below;
@@ -768,31 +766,15 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
     }
     if (C > 1) cluster_wait();
     ull* list = in_block(&sh.list[0], 0);
-    if (small) {
-      // straight into the first block's list, each block's in a part of its own
-      each([&](unsigned key, int i) {
-        if (key >= bound) {
-          const unsigned at = atomicAdd(&sh.local_n, 1u);
-          if (at < SEG) list[rank * SEG + at] = ((ull)key << 32) | (unsigned)~i;
-        }
-      });
-      __syncthreads();
-      if (tid == 0) *in_block(&sh.seg_n[rank], 0) = sh.local_n;
-    } else {
-      each([&](unsigned key, int i) {
-        if (key >= bound) {
-          const unsigned at = atomicAdd(&sh.local_n, 1u);
-          if (at < LOCAL) sh.local[at] = ((ull)key << 32) | (unsigned)~i;
-        }
-      });
-      __syncthreads();
-      const unsigned n = sh.local_n;
-      if (tid == 0) sh.local_at = atomicAdd(in_block(&sh.list_n, 0), n > LOCAL ? LIST + 1u : n);
-      __syncthreads();
-      const unsigned at = sh.local_at;
-      if (n <= LOCAL && at + n <= LIST)
-        for (unsigned i = tid; i < n; i += FT) list[at + i] = sh.local[i];
-    }
+    // straight into the first block's list, each block's in a part of its own
+    each([&](unsigned key, int i) {
+      if (key >= bound) {
+        const unsigned at = atomicAdd(&sh.local_n, 1u);
+        if (at < SEG) list[rank * SEG + at] = ((ull)key << 32) | (unsigned)~i;
+      }
+    });
+    __syncthreads();
+    if (tid == 0) *in_block(&sh.seg_n[rank], 0) = sh.local_n;
   } else {
     if (cuts) block_low();
     if (C > 1) cluster_wait();
@@ -801,15 +783,10 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
   if (by_list) {
     unsigned n = 0;
     bool fits = true;
-    if (small) {
-      for (int c = 0; c < C; ++c) {
-        const unsigned x = *in_block(&sh.seg_n[c], 0);
-        n += x;
-        fits &= x <= SEG;
-      }
-    } else {
-      n = *in_block(&sh.list_n, 0);
-      fits = n <= LIST;
+    for (int c = 0; c < C; ++c) {
+      const unsigned x = *in_block(&sh.seg_n[c], 0);
+      n += x;
+      fits &= x <= SEG;
     }
     if (fits) {
       // the first block has all there is to choose from
@@ -822,10 +799,8 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
           a.token[r] = -1;
           if (a.logprob) a.logprob[r] = -INFINITY;
         }
-      } else if (small) {
-        draw_from_few(a, sh, r, C, k, p, least, u, t);
       } else {
-        draw_from_list(a, sh, r, (int)n, k, p, least, u, t);
+        draw_from_few(a, sh, r, C, k, p, least, u, t);
       }
       if (C > 1) cluster_sync();
       return;
@@ -871,7 +846,7 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
     unsigned low = sh.low;
     for (int c = 0; c < C; ++c) low = min(low, *in_block(&sh.low, c));
     // The last place kept by count (the first k) or by mass (less than p of all before)
-    auto search = [&](bool by_count) {
+    auto search = [&](bool by_count) -> bool {
       const float range = fminf(ZERO_Z * t, row.top - key_logit(low));
       const float scale = range > 0.f ? 511.9f / range : 0.f;
       auto first_bin = [&](unsigned key) { return min(FT - 1, (int)((row.top - key_logit(key)) * scale)); };
@@ -882,9 +857,12 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
       sh.count[0][tid] = 0;
       for (int w = 0; w < 3; ++w) sh.mass[0][w][tid] = 0;
       __syncthreads();
-      // the present level's bin of a token, -1 if it is not one of those in question
+      // The present level's bin of a token, -1 if it is not one of those in question.
+      // Below the floor no token has mass: by rank they come after all that have, and
+      // where a cut falls among them does not matter.
+      const unsigned floor_key = row.top == INFINITY ? top : max(kKeyNegInf + 1, order_key(row.top - ZERO_Z * t));
       auto bin = [&](unsigned key, int i) {
-        if (key <= kKeyNegInf || !cut.keeps(key, i)) return -1;
+        if (key < floor_key || !cut.keeps(key, i)) return -1;
         if (bin0 < 0) return first_bin(key);
         return key < lo || key > hi || first_bin(key) != bin0 ? -1 : (int)((hi - key) >> shift);
       };
@@ -895,7 +873,12 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
         // stay below 2^32.
         each([&](unsigned key, int i) {
           const int x = bin(key, i);
-          const ull m = x < 0 ? 0 : mass_at(key);
+          if (x < 0) return;
+          if (by_count) {
+            atomicAdd(&sh.count[turn][x], 1u);
+            return;
+          }
+          const ull m = mass_at(key);
           if (m == 0) return;
           atomicAdd(&sh.count[turn][x], 1u);
           atomicAdd(&sh.mass[turn][0][x], (unsigned)m & 0x3fffu);
@@ -946,11 +929,27 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
         const unsigned n_equal = sh.red[0][0];
         n_above = sh.n_above;
         m_above = sh.m_above;
+        if (by_count && bin0 < 0 && k <= TOP_K_LIST && n_above + n_equal <= LIST) {
+          // the first k ranks and the rest of the last one's bin fit the first block's
+          // list, one block's after another's: what is left is its to do
+          const unsigned mine = __reduce_add_sync(0xffffffffu, tid <= best ? earlier : 0u);
+          if (lane == 0) sh.scan_c[warp] = mine;
+          if (tid == 0) sh.local_n = 0;
+          __syncthreads();
+          ull* list = in_block(&sh.list[0], 0) + __reduce_add_sync(0xffffffffu, lane < FW ? sh.scan_c[lane] : 0u);
+          each([&](unsigned key, int i) {
+            const int x = bin(key, i);
+            if (x >= 0 && x <= best) list[atomicAdd(&sh.local_n, 1u)] = ((ull)key << 32) | (unsigned)~i;
+          });
+          sync_cluster(C);
+          if (rank == 0) draw_from_list(a, sh, r, (int)(n_above + n_equal), k, p, least, u, t);
+          return true;
+        }
         if (n_equal <= TOP_K_LIST) {
           // few enough to sort: the blocks' tokens of that bin, one block's after another's
           ull* list = in_block(&sh.list[0], 0) + sh.local_at;
           each([&](unsigned key, int i) {
-            if (bin(key, i) == best && mass_at(key)) list[atomicAdd(&sh.local_n, 1u)] = ((ull)key << 32) | (unsigned)~i;
+            if (bin(key, i) == best && (by_count || mass_at(key))) list[atomicAdd(&sh.local_n, 1u)] = ((ull)key << 32) | (unsigned)~i;
           });
           sync_cluster(C);
           if (rank == 0) {
@@ -982,15 +981,14 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
           }
           sync_cluster(C);
           cut = sh.cut;
-          return;
+          return false;
         }
         if (bin0 < 0) {
           // the keys in that bin
-          bin0 = best;
           lo = 0xffffffffu;
           hi = 0;
           each([&](unsigned key, int i) {
-            if (key > kKeyNegInf && cut.keeps(key, i) && first_bin(key) == bin0 && mass_at(key)) {
+            if (bin(key, i) == best && (by_count || mass_at(key))) {
               lo = min(lo, key);
               hi = max(hi, key);
             }
@@ -1016,6 +1014,7 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
             lo = min(lo, *in_block(&sh.lo[0], q));
             hi = max(hi, *in_block(&sh.hi[0], q));
           }
+          bin0 = best;
         } else {
           const unsigned from = (unsigned)best << shift;   // bins are counted from hi down
           const unsigned span = (1u << shift) - 1u;
@@ -1034,7 +1033,7 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
           }
           if (least_n == n_equal) {
             if (hi > cut.key) cut = Place{hi, 0x7fffffff};
-            return;
+            return false;
           }
           // the index of that token
           unsigned seen = 0;
@@ -1059,12 +1058,15 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
           }
           sync_cluster(C);
           cut = sh.cut;
-          return;
+          return false;
         }
         shift = max(0, 32 - __clz(hi - lo) - 9);
       }
     };
-    if (k > 0 && k < a.vocab) search(true);
+    if (k > 0 && k < a.vocab && search(true)) {
+      if (C > 1) cluster_sync();                     // nobody leaves while its memory is read
+      return;
+    }
     if (!(p >= 1.f)) search(false);
   }
 
