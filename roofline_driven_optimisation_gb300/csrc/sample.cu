@@ -45,7 +45,14 @@ __device__ __forceinline__ float logit_weight(const Row& r, float l) {
   const float w = expf(logit_z(r, l));
   return l > -INFINITY && w == w ? w : 0.f;   // -inf never, whatever the temperature
 }
-__device__ __forceinline__ ull mass_of(float w) { return __float2ull_rz(__fmul_rn(w, 1099511627776.f)); }
+// floor(2^40 w) for 0 <= w <= 1, from w's own bits: 24 of them, shifted by its exponent
+// (the conversion instruction to 64 bits is slow)
+__device__ __forceinline__ ull mass_of(float w) {
+  const uint32_t u = __float_as_uint(w);
+  const int e = (int)(u >> 23) - (127 + 23 - 40);            // the last bit's place
+  const uint32_t f = (u & 0x7fffffu) | 0x800000u;
+  return e >= 0 ? (ull)f << e : e > -24 ? (ull)(f >> -e) : 0;   // subnormals are far below 2^-40
+}
 
 // What is kept: keys above `key`, and the first `ties` (by index) equal to it
 struct Cut {
@@ -373,47 +380,57 @@ __device__ __forceinline__ void block_prefix(Cluster& sh, unsigned& c, ull& m) {
   }
 }
 
-// Sorts list[0 .. n2) (n2 a power of two, 64 .. LIST), largest first; whole block.
-__device__ __forceinline__ void sort_list(Cluster& sh, int n2) {
-  const int tid = threadIdx.x;
-  if (n2 <= FT) {
-    // a value a thread: steps within a warp by shuffles, others through shared
-    // memory, in two buffers by turns
-    if (tid < n2) {
-    ull x = sh.list[tid];
-    ull* other = sh.local;
-    for (int size = 2; size <= n2; size <<= 1)
-      for (int step = size >> 1; step > 0; step >>= 1) {
-        ull y;
-        if (step < 32) {
-          y = __shfl_xor_sync(0xffffffffu, x, step);
-        } else {
-          other[tid] = x;
-          asm volatile("bar.sync 1, %0;" ::"r"(n2) : "memory");   // the warps that hold values
-          y = other[tid ^ step];
-          other = other == sh.local ? sh.local + FT : sh.local;
-        }
-        // the lower place of a pair keeps the larger value in a descending run
-        const bool larger = ((tid & step) == 0) == ((tid & size) == 0);
-        x = (x < y) == larger ? y : x;
-      }
-    sh.list[tid] = x;
-    }
-    __syncthreads();
-    return;
-  }
+// Sorts list[0 .. n2), largest first: E values a thread in registers, neighbours; steps
+// within a thread, within a warp by shuffles, others through shared memory.  The
+// warps that hold values.
+template <int E>
+__device__ __forceinline__ void sort_values(Cluster& sh, int n2) {
+  const int tid = threadIdx.x, threads = n2 / E;
+  ull x[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = sh.list[tid * E + e];
+  // of a pair in a descending run the lower place keeps the larger value
+  auto keep = [](ull& v, ull other, bool larger) { v = (v < other) == larger ? other : v; };
   for (int size = 2; size <= n2; size <<= 1)
     for (int step = size >> 1; step > 0; step >>= 1) {
-      for (int i = tid; i < n2 / 2; i += FT) {
-        const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
-        const ull x = sh.list[lo], y = sh.list[hi];
-        if ((x < y) == ((lo & size) == 0)) {
-          sh.list[lo] = y;
-          sh.list[hi] = x;
+      if (step < E) {
+        ull y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const ull z1 = x[e ^ 1], z2 = E > 2 ? x[(e ^ 2) % E] : z1;
+          y[e] = step == 1 ? z1 : z2;
         }
+#pragma unroll
+        for (int e = 0; e < E; ++e) keep(x[e], y[e], ((e & step) == 0) == (((tid * E + e) & size) == 0));
+      } else if (step < 32 * E) {
+        const bool larger = ((tid * E & step) == 0) == ((tid * E & size) == 0);
+#pragma unroll
+        for (int e = 0; e < E; ++e) keep(x[e], __shfl_xor_sync(0xffffffffu, x[e], step / E), larger);
+      } else {
+        const bool larger = ((tid * E & step) == 0) == ((tid * E & size) == 0);
+        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");   // the last step's values have been read
+#pragma unroll
+        for (int e = 0; e < E; ++e) sh.local[e * threads + tid] = x[e];
+        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+#pragma unroll
+        for (int e = 0; e < E; ++e) keep(x[e], sh.local[e * threads + (tid ^ (step / E))], larger);
       }
-      __syncthreads();
     }
+#pragma unroll
+  for (int e = 0; e < E; ++e) sh.list[tid * E + e] = x[e];
+}
+// n2 a power of two, 64 .. LIST; whole block
+__device__ __forceinline__ void sort_list(Cluster& sh, int n2) {
+  static_assert(LIST == 4 * FT && LOCAL >= LIST, "four values a thread");
+  const int tid = threadIdx.x;
+  if (n2 <= FT) {
+    if (tid < n2) sort_values<1>(sh, n2);
+  } else if (n2 <= 2 * FT) {
+    sort_values<2>(sh, n2);
+  } else {
+    sort_values<4>(sh, n2);
+  }
+  __syncthreads();
 }
 
 // Zeros behind the list's first m entries, up to a power of two, which is returned
