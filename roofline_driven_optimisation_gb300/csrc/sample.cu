@@ -23,6 +23,7 @@ namespace {
 using ull = unsigned long long;
 constexpr int THREADS = 1024, WARPS = THREADS / 32;
 constexpr uint32_t kKeyNegInf = 0x007fffffu;   // order_key(-inf), the lowest key
+constexpr int kNotDone = -2;                   // token of a row that sample_stream_kernel gives up
 
 // A logit as an unsigned number in the same order; NaN counts as -inf and -0 as 0
 __device__ __forceinline__ uint32_t order_key(float l) {
@@ -305,6 +306,7 @@ constexpr int SMALL_K = 64;                   // largest top_k whose ranks fit t
 constexpr int SEG = LIST / MAX_C;             // a block's part of the list then
 constexpr int TOP_K_LIST = 1024;              // ranks that the first block can draw from: two a thread
 constexpr int SAMPLE_Q = 4;                   // quads of a thread before a row takes more blocks
+constexpr int STREAM_VOCAB = 16384;           // shortest rows of the streaming kernel
 constexpr float ZERO_Z = 28.f;                // expf(-28) < 2^-40: no mass
 
 // A cut by rank: kept are larger keys, and equal ones up to index idx
@@ -669,7 +671,7 @@ __device__ __forceinline__ void draw_from_few(const SampleArgs& a, Cluster& sh, 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs a, const int C, const int Q) {
+__global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs a, const int C, const int Q, const int rest) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Cluster& sh = *reinterpret_cast<Cluster*>(smem_raw);
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -680,6 +682,15 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
   griddep_wait();
   if (tid == 0) griddep_launch_dependents();
 
+  const float t_in = a.temperature ? a.temperature[r] : 1.f;
+  const int k = a.top_k ? a.top_k[r] : 0;
+  const float p = a.top_p ? a.top_p[r] : 1.f;
+  const float least = a.min_p ? a.min_p[r] : 0.f;
+  const float u = a.u[r];
+  // only the first rank: also where no weight, 1 at most, can reach min_p
+  const bool greedy = !(t_in >= FLT_MIN) || k == 1 || !(least <= 1.f);
+  const float t = t_in >= FLT_MIN ? t_in : 1.f;
+  if (rest && (greedy || (k > 0 && k <= SMALL_K)) && a.token[r] != kNotDone) return;   // sample_stream_kernel's
   // ---- read the row.  Groups are the keys at one place k of a thread's quads.
   unsigned group[4] = {0, 0, 0, 0};
   {
@@ -701,14 +712,6 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
       keys[q * 32] = make_uint4(key[0], key[1], key[2], key[3]);
     }
   }
-  const float t_in = a.temperature ? a.temperature[r] : 1.f;
-  const int k = a.top_k ? a.top_k[r] : 0;
-  const float p = a.top_p ? a.top_p[r] : 1.f;
-  const float least = a.min_p ? a.min_p[r] : 0.f;
-  const float u = a.u[r];
-  // only the first rank: also where no weight, 1 at most, can reach min_p
-  const bool greedy = !(t_in >= FLT_MIN) || k == 1 || !(least <= 1.f);
-  const float t = t_in >= FLT_MIN ? t_in : 1.f;
   // f(key, index) for this thread's keys, in index order
   auto each = [&](auto f) {
 #pragma unroll 2
@@ -1137,8 +1140,185 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
   if (C > 1) cluster_sync();                         // nobody leaves while its memory is read
 }
 
+// ------------------------------------------------------------------ a row a block
+// Many rows at once, for those whose draw is among the first SMALL_K ranks (or the
+// first alone): a block streams through a row in tiles and lists what may be among
+// them.  The k-th largest of the first tile's groups bounds the k-th rank of the row
+// from below, so a later logit is mostly one comparison; where the list gets long, its
+// own k-th rank is a better bound.  A row whose single tile holds more than the list
+// (ascending logits, say) is left to the other kernel.
+constexpr int TILE = 16;                      // logits of a thread in a tile
+
+// The list's bound for the k-th rank: a histogram of its keys; drops what is below it.
+// Whole block, after a barrier.
+__device__ __forceinline__ unsigned tighten(Cluster& sh, int k) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, n = (int)sh.local_n;
+  unsigned hi = 0, lo = 0xffffffffu;
+  for (int i = tid; i < n; i += FT) {
+    const unsigned key = (unsigned)(sh.list[i] >> 32);
+    hi = max(hi, key);
+    lo = min(lo, key);
+    sh.local[i] = sh.list[i];
+  }
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  if (lane == 0) {
+    sh.red[0][warp] = hi;
+    sh.red[1][warp] = lo;
+  }
+  sh.bins[tid] = 0;
+  __syncthreads();
+  hi = __reduce_max_sync(0xffffffffu, sh.red[0][lane % FW]);
+  lo = __reduce_min_sync(0xffffffffu, sh.red[1][lane % FW]);
+  const float ltop = key_logit(hi), range = ltop - key_logit(lo);
+  const float scale = range > 0.f && range < INFINITY ? 511.9f / range : 0.f;
+  auto bin = [&](ull x) { return min(FT - 1, (int)((ltop - key_logit((unsigned)(x >> 32))) * scale)); };
+  for (int i = tid; i < n; i += FT) atomicAdd(&sh.bins[bin(sh.local[i])], 1u);
+  if (tid == 0) sh.local_n = 0;
+  __syncthreads();
+  if (warp == 0) {
+    const unsigned best = kth_bin(sh, k);
+    if (lane == 0) sh.best = best;
+  }
+  __syncthreads();
+  const int best = (int)sh.best;
+  unsigned bound = 0xffffffffu;                      // the lowest key kept
+  for (int i = tid; i < n; i += FT) {
+    const ull x = sh.local[i];
+    if (bin(x) <= best) {
+      sh.list[atomicAdd(&sh.local_n, 1u)] = x;
+      bound = min(bound, (unsigned)(x >> 32));
+    }
+  }
+  bound = __reduce_min_sync(0xffffffffu, bound);
+  if (lane == 0) sh.red[0][warp] = bound;
+  __syncthreads();
+  bound = __reduce_min_sync(0xffffffffu, sh.red[0][lane % FW]);
+  __syncthreads();
+  return bound;
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(FT, 2) sample_stream_kernel(const SampleArgs a) {
+  __shared__ Cluster sh;
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, r = blockIdx.x;
+  const float t_in = a.temperature ? a.temperature[r] : 1.f;
+  const int k_in = a.top_k ? a.top_k[r] : 0;
+  const float p_in = a.top_p ? a.top_p[r] : 1.f;
+  const float least_in = a.min_p ? a.min_p[r] : 0.f;
+  const float u = a.u[r];
+  const bool greedy = !(t_in >= FLT_MIN) || k_in == 1 || !(least_in <= 1.f);
+  if (!greedy && !(k_in > 0 && k_in <= SMALL_K)) return;
+  const int k = greedy ? 1 : k_in;
+  const float p = greedy ? 1.f : p_in, least = greedy ? 0.f : least_in, t = t_in >= FLT_MIN ? t_in : 1.f;
+  const T* row = static_cast<const T*>(a.logits) + (long long)r * a.ld;
+  // logit e of vector v of tile x: index ((x * (TILE / VEC) + v) * FT + tid) * VEC + e
+  auto index = [&](int x, int v) { return ((x * (TILE / VEC) + v) * FT + tid) * VEC; };
+  auto load = [&](int x, float (&l)[TILE]) {
+#pragma unroll
+    for (int v = 0; v < TILE / VEC; ++v) {
+      const int i = index(x, v);
+      if constexpr (VEC == 1) {
+        l[v] = i < a.vocab ? (float)row[i] : -INFINITY;
+      } else if (i + VEC <= a.vocab) {
+        if constexpr (sizeof(T) == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(row + i);
+          l[v * 4] = y.x;
+          l[v * 4 + 1] = y.y;
+          l[v * 4 + 2] = y.z;
+          l[v * 4 + 3] = y.w;
+        } else {
+          const uint2 y = *reinterpret_cast<const uint2*>(row + i);
+          l[v * 4] = __uint_as_float(y.x << 16);
+          l[v * 4 + 1] = __uint_as_float(y.x & 0xffff0000u);
+          l[v * 4 + 2] = __uint_as_float(y.y << 16);
+          l[v * 4 + 3] = __uint_as_float(y.y & 0xffff0000u);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) l[v * VEC + e] = i + e < a.vocab ? (float)row[i + e] : -INFINITY;
+      }
+    }
+  };
+  const int tiles = (a.vocab + FT * TILE - 1) / (FT * TILE);
+  float l[TILE], next[TILE];
+  load(0, l);
+  if (tiles > 1) load(1, next);
+  sh.bins[tid] = 0;
+  if (tid == 0) sh.local_n = 0;
+
+  // ---- the first tile's bound
+  unsigned group[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < TILE; ++i) group[i % 4] = max(group[i % 4], order_key(l[i]));
+  unsigned top = max(max(group[0], group[1]), max(group[2], group[3])), gmin = 0xffffffffu;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) gmin = min(gmin, group[q] > kKeyNegInf ? group[q] : 0xffffffffu);
+  top = __reduce_max_sync(0xffffffffu, top);
+  gmin = __reduce_min_sync(0xffffffffu, gmin);
+  if (lane == 0) {
+    sh.red[0][warp] = top;
+    sh.red[1][warp] = gmin;
+  }
+  __syncthreads();
+  top = __reduce_max_sync(0xffffffffu, sh.red[0][lane % FW]);
+  gmin = __reduce_min_sync(0xffffffffu, sh.red[1][lane % FW]);
+  unsigned bound = kKeyNegInf + 1;                   // -inf is never taken
+  if (top > kKeyNegInf) {
+    const float ltop = key_logit(top);
+    bound = ltop == INFINITY ? top : max(bound, order_key(ltop - ZERO_Z * t));   // below: no mass
+    const float range = ltop - key_logit(gmin);
+    const float scale = range > 0.f && range < INFINITY ? 511.9f / range : 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (group[q] >= bound) atomicAdd(&sh.bins[min(FT - 1, (int)((ltop - key_logit(group[q])) * scale))], 1u);
+    __syncthreads();
+    if (warp == 0) {
+      const unsigned best = kth_bin(sh, k);
+      if (lane == 0) sh.best = best;
+    }
+    __syncthreads();
+    // the lower edge of that bin, less what the bins' rounding may be off
+    if (sh.best < FT) bound = max(bound, scale > 0.f ? order_key(ltop - (sh.best + 1.01f) / scale) : gmin);
+  }
+  // ---- the tiles
+  for (int x = 0; x < tiles; ++x) {
+    const float lbound = key_logit(bound);           // NaN compares false
+#pragma unroll
+    for (int v = 0; v < TILE; ++v)
+      if (l[v] >= lbound) {
+        const unsigned at = atomicAdd(&sh.local_n, 1u);
+        if (at < LIST) sh.list[at] = ((ull)order_key(l[v]) << 32) | (unsigned)~(index(x, v / VEC) + v % VEC);
+      }
+#pragma unroll
+    for (int v = 0; v < TILE; ++v) l[v] = next[v];
+    if (x + 2 < tiles) load(x + 2, next);
+    __syncthreads();
+    const unsigned n = sh.local_n;
+    if (n > LIST) {
+      if (tid == 0) a.token[r] = kNotDone;
+      return;
+    }
+    __syncthreads();                                 // n has been read
+    if (n > LIST / 2) bound = max(bound, tighten(sh, k));
+  }
+  if (sh.local_n == 0) {
+    if (tid == 0) {
+      a.token[r] = -1;
+      if (a.logprob) a.logprob[r] = -INFINITY;
+    }
+    return;
+  }
+  if (tid == 0) sh.seg_n[0] = sh.local_n;
+  sh.bins[tid] = 0;
+  __syncthreads();
+  draw_from_few(a, sh, r, 1, k, p, least, u, t);
+}
+
 template <typename T>
-int launch_cluster(const SampleArgs& a, int C, int Q, cudaStream_t s) {
+int launch_cluster(const SampleArgs& a, int C, int Q, int rest, cudaStream_t s) {
   constexpr int most = (int)sizeof(Cluster) + MAX_Q * FT * 16;
   static_assert(most <= 227 * 1024, "shared memory");
   static std::atomic<uint64_t> smem_set{0};
@@ -1157,18 +1337,18 @@ int launch_cluster(const SampleArgs& a, int C, int Q, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, sample_cluster_kernel<T>, a, C, Q);
+  e = cudaLaunchKernelEx(&cfg, sample_cluster_kernel<T>, a, C, Q, rest);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <class Kernel>
-int launch(Kernel kernel, dim3 grid, const SampleArgs& a, cudaStream_t s) {
+int launch(Kernel kernel, dim3 grid, int threads, const SampleArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -1178,21 +1358,28 @@ int launch(Kernel kernel, dim3 grid, const SampleArgs& a, cudaStream_t s) {
 
 
 template <typename T>
-int launch_any(const SampleArgs& a, cudaStream_t s) {
+int launch_any(const SampleArgs& a, int num_sms, cudaStream_t s) {
   const long long most = (long long)MAX_C * FT * 4 * MAX_Q;
   if (a.vocab > most || a.rows > 0x7fffffff / MAX_C)
-    return launch(sample_kernel<T>, dim3((unsigned)a.rows), a, s);
+    return launch(sample_kernel<T>, dim3((unsigned)a.rows), THREADS, a, s);
   int C = 1;
   while (C < MAX_C && C * FT * SAMPLE_Q * 4 < a.vocab) C <<= 1;
   const int Q = (a.vocab + C * FT * 4 - 1) / (C * FT * 4);
-  return launch_cluster<T>(a, C, Q, s);
+  // enough rows to fill the GPU a block each, and long enough for the second launch
+  const bool stream = a.rows >= num_sms && a.vocab >= STREAM_VOCAB;
+  if (stream) {
+    const bool vec = reinterpret_cast<uintptr_t>(a.logits) % (4 * sizeof(T)) == 0 && a.ld % 4 == 0;
+    const int e = vec ? launch(sample_stream_kernel<T, 4>, dim3((unsigned)a.rows), FT, a, s)
+                      : launch(sample_stream_kernel<T, 1>, dim3((unsigned)a.rows), FT, a, s);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_cluster<T>(a, C, Q, stream, s);
 }
 
 }  // namespace
 
 int launch_sample(const SampleArgs& a, int num_sms, cudaStream_t s) {
-  (void)num_sms;
-  return a.bf16 ? launch_any<__nv_bfloat16>(a, s) : launch_any<float>(a, s);
+  return a.bf16 ? launch_any<__nv_bfloat16>(a, num_sms, s) : launch_any<float>(a, num_sms, s);
 }
 
 }  // namespace g3

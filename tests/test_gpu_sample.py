@@ -219,3 +219,39 @@ def test_without_logprob_and_in_a_graph(cuda_lib):
     gr.replay()
     check_status()
     assert torch.equal(token, g.sample(x, v, torch.empty_like(token)))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab,ld", [(16384, None), (40000, 40003), (40004, 40008), (131071, None)])
+def test_many_long_rows(cuda_lib, dtype, vocab, ld):
+    # a row for each SM and more: rows with few ranks stream through one block each, the
+    # others and those that do not suit it go to a second kernel
+    rows = 333
+    gen = torch.Generator().manual_seed(vocab)
+    l = 2.5 * torch.randn(rows, vocab, generator=gen)
+    l.masked_fill_(torch.rand(rows, vocab, generator=gen) < 0.01, -math.inf)
+    l[1] = l[1].sort().values                       # ascending: every tile beats the ones before
+    l[2] = 0.5                                      # all equal
+    l[3, :20000] = -math.inf                        # the first tile has nothing
+    l[4] = -math.inf
+    l[4, vocab - 1] = 1.0
+    l[5, :9000] -= 50.0
+    l[6] = torch.arange(vocab) / vocab
+    l[7] = -torch.arange(vocab) / vocab
+    l = l.to(dtype)
+    u = np.random.default_rng(vocab).random(rows).astype(np.float32)
+
+    def of(*v):
+        x = torch.tensor(v)[torch.randint(len(v), (rows,), generator=gen)]
+        x[1:8] = v[-1]
+        return x
+    t, k, p, m = of(0.3, 2.0, 0.8), of(0, 1, 3, 64, 65, 900, 50), of(1.0, 0.5, 0.95), of(0.0, 0.2, 0.01)
+    token, logprob = call(l, u, ld=ld, temperature=t.tolist(), top_k=k.tolist(), top_p=p.tolist(), min_p=m.tolist())
+    some = (l > -math.inf).any(1).numpy()           # row 3 of the shortest has none
+    assert np.array_equal(token, np.where(some, _rule(l, u, t, k, p, m), -1))
+    assert np.isfinite(logprob[some]).all() and (logprob <= 0).all() and (logprob[~some] == -math.inf).all()
+    greedy, lp = call(l, u, ld=ld, temperature=[0.0] * rows)
+    assert np.array_equal(greedy, np.where(some, l.float().argmax(1).numpy(), -1)) and (lp[some] == 0).all()
+    l[0] = math.nan
+    none, lp = call(l[:1].expand(rows, -1).contiguous(), u, top_k=[5] * rows)
+    assert (none == -1).all() and (lp == -math.inf).all()
