@@ -25,6 +25,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -148,26 +149,33 @@ constexpr int NW = 8;                    // warps of a block, one block an SM
 constexpr int SLAB = kKvSlab;
 constexpr int MAX_CTAS = 160;            // blocks that the workspace has room for
 constexpr int MAX_ROWS = 32;             // rows of a tile, at most
+constexpr int MAX_TW = 4;                // warps that share a slab's keys, a tile of rows each
 constexpr int RING = 3 * 2 * SLAB * 128; // bytes of a warp's ring
 constexpr int PV_EXP = 14;               // P times the page's scale is below 2^PV_EXP in fp16
 constexpr int MIN_EXP = -112;
 constexpr int WHOLE_EXTRA = 8;          // of 8-row slabs; see its use
 
-template <int D>
+template <int D, int NT>
 struct Cfg {
   static constexpr int TILE = SLAB * D;              // bytes of a slab's keys
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int STAGES = RING / STAGE;        // 3 (D 128) or 6
+  // 24 and 32 rows of 128 values do not fit the registers beside their sums: such
+  // queries lie in the last third of the ring, in the order in which lanes read them
+  static constexpr bool Q_SHARED = D == 128 && NT > 2;
+  static constexpr int Q_BYTES = Q_SHARED ? D / 16 * NT * 32 * 8 : 0;
+  static constexpr int STAGES = (RING - (Q_SHARED ? RING / 3 : 0)) / STAGE;   // 3 or 2 (D 128), 6
+  static_assert(STAGES * STAGE + Q_BYTES <= RING, "ring");
 };
 
 // A partial result: O [rows][D], then m [rows], l [rows].  In the workspace: two of
-// every block (its first and last item may go on in other blocks), one of every
+// every block and tile (its first and last item may go on in other blocks), one of every
 // warp (its first item's, while its ring is in use), then a counter for each item.
 // The parts' places are of fixed size, so that no call's parts reach another's
 // counters.
 constexpr int PART_FLOATS = MAX_ROWS * 128 + 2 * MAX_ROWS;
 static_assert(PART_FLOATS * 4 <= RING, "a partial result fits in a drained ring");
-constexpr size_t PARTS = (size_t)MAX_CTAS * (2 + NW);
+constexpr size_t PARTS = (size_t)MAX_CTAS * (2 * MAX_TW + NW);
+constexpr int MAX_OPENS = NW + MAX_TW;   // a tile's warps meet at one more place than they are
 
 struct StageMeta {
   float ks[2], vs[2];   // scales of the slab's one or two pages
@@ -186,6 +194,7 @@ struct Open {           // an item that more than one warp worked on
   u64 unit;
   int e0, e1;           // its parts: slots e0 .. e1 (warp * 2 + slot)
   int S, rows, h, t, first, count;
+  int tl;               // the tile's place in its pass
   bool whole;           // no other block has a part of it
 };
 
@@ -199,24 +208,27 @@ struct Shared {
   StageMeta meta[NW][6];
   u64 full[NW][6];
   Slot slot[NW * 2];
-  Open open[NW + 1];
+  Open open[MAX_OPENS];
   int opens;
   u64 scan[NW];
   int scan_items[NW], scan_longest[NW];
-  int last[NW + 1];     // this block finishes the item
+  int last[MAX_OPENS];  // this block finishes the item
   int abort;
 };
 
-// Units of sequence b: heads * tiles * slabs
+// Units of sequence b: heads * passes * slabs; a pass is the tiles that the warps of
+// a group take side by side
 struct Seq {
-  int len, first, n, S, tiles;
+  int len, first, n, S, tiles, passes;
 };
 
 struct Plan {
   const KvAttnArgs* a;
   int group, rt;        // query heads of a head; rows of a tile
+  int tw, tl;           // warps of a group; this warp's place in it
   __device__ __forceinline__ Seq seq(int len, int first, int n) const {
-    return Seq{len, first, n, max(1, (len + SLAB - 1) / SLAB), (n * group + rt - 1) / rt};
+    const int tiles = (n * group + rt - 1) / rt;
+    return Seq{len, first, n, max(1, (len + SLAB - 1) / SLAB), tiles, (tiles + tw - 1) / tw};
   }
   __device__ __forceinline__ Seq seq(int b) const {
     // every load before the first check, which waits for it
@@ -236,9 +248,10 @@ struct Plan {
     }
     return seq(len, first, end - first);
   }
-  __device__ __forceinline__ u64 units(const Seq& q) const { return (u64)a->c.H * q.tiles * q.S; }
-  // keys that the last row of tile t sees
+  __device__ __forceinline__ u64 units(const Seq& q) const { return (u64)a->c.H * q.passes * q.S; }
+  // keys that the last row of tile t sees (none if there is no such tile)
   __device__ __forceinline__ int visible(const Seq& q, int t) const {
+    if (t >= q.tiles) return 0;
     if ((t + 1) * rt >= q.n * group) return q.len;
     return q.len - q.n + ((t + 1) * rt - 1) / group + 1;
   }
@@ -251,18 +264,18 @@ __device__ __forceinline__ u64 quotient(u64 x, u64 d) {
 
 // A place on the line of slabs
 struct Walk {
-  int b, idx, s;        // sequence, head * tiles + tile, slab
+  int b, idx, s;        // sequence, head * passes + pass, slab
   int h, t, vis;        // head, tile, keys that the tile's last row sees
   Seq q;
   __device__ __forceinline__ void split(const Plan& p) {
-    h = q.tiles == 1 ? idx : idx / q.tiles;
-    t = idx - h * q.tiles;
+    h = q.passes == 1 ? idx : idx / q.passes;
+    t = (idx - h * q.passes) * p.tw + p.tl;
     vis = p.visible(q, t);
   }
   __device__ __forceinline__ void next(const Plan& p) {
     if (++s < q.S) return;
     s = 0;
-    if (++idx < p.a->c.H * q.tiles) {
+    if (++idx < p.a->c.H * q.passes) {
       split(p);
       return;
     }
@@ -270,7 +283,7 @@ struct Walk {
     do {
       if (++b >= p.a->c.seqs) return;
       q = p.seq(b);
-    } while (q.tiles == 0);
+    } while (q.passes == 0);
     split(p);
   }
 };
@@ -350,8 +363,8 @@ template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(NW * 32, 1)
     kv_attention_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                         const __grid_constant__ KvAttnArgs a, const int group, const int max_tiles,
-                        const int vec) {
-  using C = Cfg<D>;
+                        const int tw, const int vec) {
+  using C = Cfg<D, NT>;
   constexpr int ST = C::STAGES, CH = D / 16, RT = NT * 8;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
@@ -360,7 +373,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t4 = lane % 4;
   uint8_t* ring_ptr = base_ptr + warp * RING;
   const uint32_t ring = smem_u32(ring_ptr);
-  const Plan plan{&a, group, RT};
+  // groups of tw warps walk the same slabs, each for its own tile of rows: what one
+  // fetches, the others find in L2
+  const int tl = warp & (tw - 1), worker = warp / tw, workers = NW / tw;
+  const Plan plan{&a, group, RT, tw, tl};
   const int npg = a.c.P < SLAB ? 2 : 1;           // pages of a slab
   const int p_shift = 31 - __clz(a.c.P);          // P is a power of two
 
@@ -389,8 +405,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
     rec[b].first = q.first;
     rec[b].n = q.n;
     mine += plan.units(q);
-    items += a.c.H * q.tiles;
-    if (q.tiles > 0) longest = max(longest, q.S);
+    items += a.c.H * q.passes;
+    if (q.passes > 0) longest = max(longest, q.S);
   }
   u64 incl = mine;
   int item_incl = items;
@@ -428,9 +444,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
   // Blocks take equal shares of the line, or whole items.  Whole items need no exchange
   // between blocks, which costs a call about as much time as WHOLE_EXTRA slabs a warp;
   // so they are taken unless the fullest block's warps get longer than that.
-  const u64 share = quotient(T + gridDim.x * NW - 1, gridDim.x * NW);
+  const u64 share = quotient(T + gridDim.x * workers - 1, gridDim.x * workers);
   const int blocks = min((int)gridDim.x, I);
-  const bool by_item = I > 0 && ((u64)((I + blocks - 1) / blocks) * longest + NW - 1) / NW <= share + WHOLE_EXTRA / NT;
+  const bool by_item = I > 0 && ((u64)((I + blocks - 1) / blocks) * longest + workers - 1) / workers <= share + WHOLE_EXTRA / NT;
   const u64 G = by_item ? (u64)blocks : T < gridDim.x ? T : gridDim.x;   // every block up to G has a unit
   const u64 cta = blockIdx.x;
   if (cta >= G) return;
@@ -451,7 +467,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   const u64 A = by_item ? item_unit(quotient(cta * I, G)) : quotient(cta * T, G);
   const u64 B = by_item ? item_unit(quotient((cta + 1) * I, G)) : quotient((cta + 1) * T, G);
   const u64 me = cta * NW + warp;
-  const u64 u0 = A + warp * (B - A) / NW, u1 = A + (warp + 1) * (B - A) / NW;
+  const u64 u0 = A + worker * (B - A) / workers, u1 = A + (worker + 1) * (B - A) / workers;
   Walk cw;
   if (u0 < u1) {
     cw.b = record([&](const SeqRec& x) { return x.at <= u0; });
@@ -498,7 +514,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
   };
 
-  if (lane < 2) sh.slot[warp * 2 + lane].unit = ~0ull;
+  const int slot0 = (tl * workers + worker) * 2;    // a tile's warps side by side, in the order of the line
+  if (lane < 2) sh.slot[slot0 + lane].unit = ~0ull;
   if (total > 0) {
     Walk pw = cw;                                 // next slab to fetch
     int issued = 0, pg;
@@ -519,7 +536,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
 
     // ---- consumer state of one item
-    uint32_t qf[NT][CH][2];
+    uint32_t qf[C::Q_SHARED ? 1 : NT][CH][2];
+    uint2* const q_shared = reinterpret_cast<uint2*>(ring_ptr + ST * C::STAGE) + lane;   // [(chunk * NT + nt) * 32]
     float acc[NT][CH][4];
     float m[NT][2], l[NT][2], rs[NT][2];
     int lim[NT][2];                               // keys that this lane's columns see
@@ -570,8 +588,13 @@ __global__ void __launch_bounds__(NW * 32, 1)
           const float f = pow2i(14 - e);
 #pragma unroll
           for (int c = 0; c < CH; ++c) {
-            qf[nt][c][0] = pack_f16(x[c][0] * f, x[c][1] * f);
-            qf[nt][c][1] = pack_f16(x[c][2] * f, x[c][3] * f);
+            const uint32_t lo = pack_f16(x[c][0] * f, x[c][1] * f), hi = pack_f16(x[c][2] * f, x[c][3] * f);
+            if constexpr (C::Q_SHARED) {
+              q_shared[(c * NT + nt) * 32] = make_uint2(lo, hi);
+            } else {
+              qf[nt][c][0] = lo;
+              qf[nt][c][1] = hi;
+            }
           }
           const float back = a.scale * 1.4426950408889634f * pow2i(e - 14);
 #pragma unroll
@@ -613,24 +636,39 @@ __global__ void __launch_bounds__(NW * 32, 1)
         // others its k + 8; Q is held in the same order.
         float sc[2][NT][4];
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
+        for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 4; ++k) sc[sub][nt][k] = 0.f;
-          const int r = sub * 16 + (lane & 15);
-          const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+        const int row = lane & 15, sw = D == 128 ? (row & 7) : ((row >> 1) & 3);   // rows 16 apart swizzle alike
 #pragma unroll
-          for (int c = 0; c < CH; c += 2) {
+        for (int c = 0; c < CH; c += 2) {
+          uint32_t q[2][NT][2];
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (C::Q_SHARED) {
+                const uint2 v = q_shared[((c + cc) * NT + nt) * 32];
+                q[cc][nt][0] = v.x;
+                q[cc][nt][1] = v.y;
+              } else {
+                q[cc][nt][0] = qf[nt][c + cc][0];
+                q[cc][nt][1] = qf[nt][c + cc][1];
+              }
+            }
+          const uint32_t at = kt + row * D + (((c + (lane >> 4)) ^ sw) << 4);
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub) {
             uint32_t x[4], a0, a1, a2, a3;
-            ldsm_x4(kt + r * D + (((c + (lane >> 4)) ^ sw) << 4), x);
+            ldsm_x4(at + sub * 16 * D, x);
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
               widen<FMT>(x[2 * cc], a0, a2);
               widen<FMT>(x[2 * cc + 1], a1, a3);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma16816(sc[sub][nt], a0, a1, a2, a3, qf[nt][c + cc][0], qf[nt][c + cc][1]);
+              for (int nt = 0; nt < NT; ++nt) mma16816(sc[sub][nt], a0, a1, a2, a3, q[cc][nt][0], q[cc][nt][1]);
             }
           }
         }
@@ -710,16 +748,15 @@ __global__ void __launch_bounds__(NW * 32, 1)
         // value 2g + 1.
         auto products = [&](auto masked, int limit, bool all) {
 #pragma unroll
-          for (int sub = 0; sub < 2; ++sub) {
-            const int kk = k0 + sub * 16 + 2 * t4;
-            const bool there = (sub ? ok1 : ok0) != 0;
-            const uint32_t mk0 = there ? key_mask(kk, limit) : 0u, mk1 = there ? key_mask(kk + 8, limit) : 0u;
-            const int r = sub * 16 + (lane & 15);
-            const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+          for (int c = 0; c < CH; c += 2) {
+            const uint32_t at = vt + row * D + (((c + (lane >> 4)) ^ sw) << 4);
 #pragma unroll
-            for (int c = 0; c < CH; c += 2) {
+            for (int sub = 0; sub < 2; ++sub) {
+              const int kk = k0 + sub * 16 + 2 * t4;
+              const bool there = (sub ? ok1 : ok0) != 0;
+              const uint32_t mk0 = there ? key_mask(kk, limit) : 0u, mk1 = there ? key_mask(kk + 8, limit) : 0u;
               uint32_t x[4], a0, a1, a2, a3;
-              ldsm_x4_t(vt + r * D + (((c + (lane >> 4)) ^ sw) << 4), x);
+              ldsm_x4_t(at + sub * 16 * D, x);
 #pragma unroll
               for (int cc = 0; cc < 2; ++cc) {
                 widen_pairs<FMT>(x[2 * cc], a0, a1);
@@ -819,12 +856,13 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 }
               }
             }
-        } else {
+        } else if (rows > 0) {
           // into the drained ring, or into the workspace while the ring is in use
-          float* part = j + 1 == total ? reinterpret_cast<float*>(ring_ptr)
-                                       : static_cast<float*>(a.ws) + (MAX_CTAS * 2 + me) * (size_t)PART_FLOATS;
+          float* part = j + 1 == total
+                            ? reinterpret_cast<float*>(ring_ptr)
+                            : static_cast<float*>(a.ws) + (MAX_CTAS * 2 * MAX_TW + me) * (size_t)PART_FLOATS;
           if (lane == 0) {
-            Slot& s = sh.slot[warp * 2 + (head ? 0 : 1)];
+            Slot& s = sh.slot[slot0 + (head ? 0 : 1)];
             s.unit = u0 + j - done.s;
             s.part = part;
             s.S = done.q.S;
@@ -872,7 +910,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const unsigned below = valid & ((1u << lane) - 1u);
     const int prev = below ? 31 - __clz(below) : lane;
     const u64 before = __shfl_sync(0xffffffffu, unit, prev);
-    const bool starts = unit != ~0ull && (below == 0 || before != unit);
+    const int tile = lane / (2 * workers), tile_before = prev / (2 * workers);
+    const bool starts = unit != ~0ull && (below == 0 || before != unit || tile != tile_before);
     const unsigned firsts = __ballot_sync(0xffffffffu, starts);
     if (starts) {
       const Slot& s = sh.slot[lane];
@@ -888,6 +927,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
       o.t = s.t;
       o.first = s.first;
       o.count = s.count;
+      o.tl = tile;
       o.whole = unit >= A && unit + s.S <= B;
     }
     if (lane == 0) sh.opens = __popc(firsts);
@@ -921,8 +961,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
   // weights of every slot for every row, behind the part in the first ring
   float* wt = reinterpret_cast<float*>(base_ptr + PART_FLOATS * 4);   // [slot][row]
   float* tops = wt + NW * 2 * MAX_ROWS;                               // [item][row]: maximum
-  float* totals = tops + (NW + 1) * MAX_ROWS;                         // [item][row]: sum
-  static_assert((PART_FLOATS + (2 * NW + 2 * NW + 2) * MAX_ROWS) * 4 <= RING, "weights fit behind a part");
+  float* totals = tops + MAX_OPENS * MAX_ROWS;                        // [item][row]: sum
+  static_assert((PART_FLOATS + (2 * NW + 2 * MAX_OPENS) * MAX_ROWS) * 4 <= RING, "weights fit behind a part");
   int rmax = 0;
   for (int i = 0; i < opens; ++i) rmax = max(rmax, sh.open[i].rows);
   for (int i = threadIdx.x / 16; i < (opens * rmax + 1) / 2 * 2; i += NW * 2) {
@@ -930,7 +970,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const int j = min(i / rmax, opens - 1), r = i - j * rmax, e = lane % 16;
     const Open& o = sh.open[j];
     const Slot& s = sh.slot[e];
-    const bool mine = r < o.rows && s.unit == o.unit;
+    const bool mine = r < o.rows && e >= o.e0 && e <= o.e1 && s.unit == o.unit;
     const float top = mine ? s.part[RT * D + r] : -INFINITY, l = mine ? s.part[RT * D + RT + r] : 0.f;
     float M = top;
     for (int k = 8; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
@@ -955,7 +995,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     if (o.whole) {
       store(o, r, d4, x, totals[j * MAX_ROWS + r]);
     } else {
-      float* p = parts + (cta * 2 + (o.unit < A ? 0 : 1)) * PART_FLOATS;
+      float* p = parts + ((cta * 2 + (o.unit < A ? 0 : 1)) * MAX_TW + o.tl) * PART_FLOATS;
       *reinterpret_cast<float4*>(p + r * D + d4 * 4) = x;
       if (d4 == 0) {
         p[RT * D + r] = tops[j * MAX_ROWS + r];
@@ -986,9 +1026,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const Open& o = sh.open[j];
     const int c0 = (int)quotient((o.unit + 1) * G - 1, T), n = (int)quotient((o.unit + o.S) * G - 1, T) - c0 + 1;
     // it is the last item of its first block, and the first item of the others
-    const float* first = parts + ((size_t)c0 * 2 + 1) * PART_FLOATS;
-    const float* rest = parts + (size_t)c0 * 2 * PART_FLOATS;
-    auto part = [&](int c) { return c == 0 ? first : rest + (size_t)c * 2 * PART_FLOATS; };
+    const float* first = parts + (((size_t)c0 * 2 + 1) * MAX_TW + o.tl) * PART_FLOATS;
+    const float* rest = parts + ((size_t)c0 * 2 * MAX_TW + o.tl) * PART_FLOATS;
+    auto part = [&](int c) { return c == 0 ? first : rest + (size_t)c * 2 * MAX_TW * PART_FLOATS; };
     // every part's weight for every row, in the drained rings
     float* wt = reinterpret_cast<float*>(base_ptr);                // [row][part]
     float* sums = wt + MAX_ROWS * MAX_CTAS;                        // [row][part]
@@ -1028,8 +1068,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
 }
 
 template <int FMT, int D, int NT>
-int launch_fast(const KvAttnArgs& a, const CUtensorMap* mK, const CUtensorMap* mV, int group, int max_tiles, int vec,
-                int num_sms, cudaStream_t s) {
+int launch_fast(const KvAttnArgs& a, const CUtensorMap* mK, const CUtensorMap* mV, int group, int max_tiles, int tw,
+                int vec, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> smem_set{0};
   constexpr int smem = NW * RING + 1024;
   cudaError_t e = set_smem_once(smem_set, kv_attention_kernel<FMT, D, NT>, smem);
@@ -1044,12 +1084,22 @@ int launch_fast(const KvAttnArgs& a, const CUtensorMap* mK, const CUtensorMap* m
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<FMT, D, NT>, *mK, *mV, a, group, max_tiles, vec);
+  e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<FMT, D, NT>, *mK, *mV, a, group, max_tiles, tw, vec);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Rows of a tile for a call whose sequences have up to `rows` query rows a head.
-int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+// How a call's query rows a head (its longest sequence's) are cut: tiles of 8 NT rows,
+// one of each of tw warps side by side.  A tile as high as the rows allow spares
+// widening the same codes for another one; beyond 32 rows the warps share evenly.
+struct Tiling {
+  int nt, tw, tiles;
+};
+Tiling tiling(long long rows) {
+  const long long eights = (rows + 7) / 8;
+  const int tw = eights <= 4 ? 1 : eights <= 8 ? 2 : MAX_TW;
+  const int nt = (int)std::min<long long>(4, (eights + tw - 1) / tw);
+  return {nt, tw, (int)((eights + nt - 1) / nt)};
+}
 
 template <class Kernel>
 int launch(Kernel kernel, dim3 grid, dim3 block, const KvAttnArgs& a, cudaStream_t s) {
@@ -1069,23 +1119,24 @@ int launch(Kernel kernel, dim3 grid, dim3 block, const KvAttnArgs& a, cudaStream
 }  // namespace
 
 size_t kv_attention_ws_bytes(int seqs, int heads, int group, int max_new) {
-  const long long rows = (long long)max_new * group;
-  const long long tiles = rows > 0x7fffffff ? 0 : (rows + tile_rows((int)rows) - 1) / tile_rows((int)rows);
-  return PARTS * PART_FLOATS * sizeof(float) + (((size_t)seqs * heads * tiles + 3) / 4) * 16;
+  const size_t tiles = (size_t)tiling((long long)max_new * group).tiles;
+  return PARTS * PART_FLOATS * sizeof(float) + ((size_t)seqs * heads * tiles + 3) / 4 * 16;
 }
 
 int launch_kv_attention(const KvAttnArgs& a, const CUtensorMap* mK, const CUtensorMap* mV, int num_sms,
                         cudaStream_t s) {
-  const int group = a.Hq / a.c.H, rows = a.max_new * group, rt = tile_rows(rows), tiles = (rows + rt - 1) / rt;
+  const int group = a.Hq / a.c.H;
+  const Tiling x = tiling((long long)a.max_new * group);
   // pairs of outputs and quads of queries as one access
   const int vec = reinterpret_cast<uintptr_t>(a.Q) % 8 == 0 && a.ldq % 4 == 0 &&
                   reinterpret_cast<uintptr_t>(a.O) % 4 == 0 && a.ldo % 2 == 0;
   auto go = [&](auto fmt, auto dim) -> int {
     constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
-    switch (rt) {
-      case 8: return launch_fast<F, D, 1>(a, mK, mV, group, tiles, vec, num_sms, s);
-      case 16: return launch_fast<F, D, 2>(a, mK, mV, group, tiles, vec, num_sms, s);
-      default: return launch_fast<F, D, 4>(a, mK, mV, group, tiles, vec, num_sms, s);
+    switch (x.nt) {
+      case 1: return launch_fast<F, D, 1>(a, mK, mV, group, x.tiles, x.tw, vec, num_sms, s);
+      case 2: return launch_fast<F, D, 2>(a, mK, mV, group, x.tiles, x.tw, vec, num_sms, s);
+      case 3: return launch_fast<F, D, 3>(a, mK, mV, group, x.tiles, x.tw, vec, num_sms, s);
+      default: return launch_fast<F, D, 4>(a, mK, mV, group, x.tiles, x.tw, vec, num_sms, s);
     }
   };
   using std::integral_constant;
