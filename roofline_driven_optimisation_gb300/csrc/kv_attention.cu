@@ -213,6 +213,7 @@ struct Shared {
   u64 scan[NW];
   int scan_items[NW], scan_longest[NW];
   int last[MAX_OPENS];  // this block finishes the item
+  int blocks[MAX_OPENS];   // that have a part of it
   int abort;
 };
 
@@ -984,25 +985,44 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < opens * rmax * (D / 4); i += NW * 32) {
-    const int j = i / (D / 4) / rmax, r = i / (D / 4) - j * rmax, d4 = i % (D / 4);
-    const Open& o = sh.open[j];
-    if (r >= o.rows) continue;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int e = o.e0; e <= o.e1; ++e)
-      if (sh.slot[e].unit == o.unit)
-        add(x, wt[e * MAX_ROWS + r], *reinterpret_cast<const float4*>(sh.slot[e].part + r * D + d4 * 4));
-    if (o.whole) {
-      store(o, r, d4, x, totals[j * MAX_ROWS + r]);
-    } else {
+  // A warp takes some rows of an item: a lane holds a quad of each of U rows (of U
+  // pairs of rows where a row is half a warp wide), whose loads are in flight together.
+  constexpr int QUADS = D / 4, RPW = 32 / QUADS;
+  const int lane_row = lane / QUADS, lane_quad = lane % QUADS;
+  auto merge = [&](auto batch) {
+    constexpr int U = decltype(batch)::value;
+    const int groups = (rmax + U * RPW - 1) / (U * RPW);
+    for (int i = warp; i < opens * groups; i += NW) {
+      const int j = i / groups, r0 = (i - j * groups) * U * RPW + lane_row;
+      const Open& o = sh.open[j];
+      float4 x[U] = {};
+      for (int e = o.e0; e <= o.e1; ++e) {
+        if (sh.slot[e].unit != o.unit) continue;
+        const float* p = sh.slot[e].part + r0 * D + lane_quad * 4;
+        const float* w = wt + e * MAX_ROWS + r0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (r0 + u * RPW < o.rows) add(x[u], w[u * RPW], *reinterpret_cast<const float4*>(p + u * RPW * D));
+      }
       float* p = parts + ((cta * 2 + (o.unit < A ? 0 : 1)) * MAX_TW + o.tl) * PART_FLOATS;
-      *reinterpret_cast<float4*>(p + r * D + d4 * 4) = x;
-      if (d4 == 0) {
-        p[RT * D + r] = tops[j * MAX_ROWS + r];
-        p[RT * D + RT + r] = totals[j * MAX_ROWS + r];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * RPW;
+        if (r >= o.rows) continue;
+        if (o.whole) {
+          store(o, r, lane_quad, x[u], totals[j * MAX_ROWS + r]);
+        } else {
+          *reinterpret_cast<float4*>(p + r * D + lane_quad * 4) = x[u];
+          if (lane_quad == 0) {
+            p[RT * D + r] = tops[j * MAX_ROWS + r];
+            p[RT * D + RT + r] = totals[j * MAX_ROWS + r];
+          }
+        }
       }
     }
-  }
+  };
+  if (opens * rmax <= 2 * NW) merge(std::integral_constant<int, 1>{});
+  else merge(std::integral_constant<int, 4>{});
   // ---- and more than one block: the last to arrive adds the blocks' parts in order
   bool any = false;
   for (int i = 0; i < opens; ++i) any |= !sh.open[i].whole;
@@ -1015,55 +1035,124 @@ __global__ void __launch_bounds__(NW * 32, 1)
     if (!o.whole) {
       const int c0 = (int)quotient((o.unit + 1) * G - 1, T), c1 = (int)quotient((o.unit + o.S) * G - 1, T);
       last = atomicAdd(counters + o.count, 1) == c1 - c0;
+      sh.blocks[threadIdx.x] = c1 - c0 + 1;
       if (last) counters[o.count] = 0;             // ready for the next call
     }
     sh.last[threadIdx.x] = last;
   }
   __syncthreads();
-  for (int j = 0; j < opens; ++j) {
-    if (!sh.last[j]) continue;
-    __threadfence();
-    const Open& o = sh.open[j];
-    const int c0 = (int)quotient((o.unit + 1) * G - 1, T), n = (int)quotient((o.unit + o.S) * G - 1, T) - c0 + 1;
-    // it is the last item of its first block, and the first item of the others
-    const float* first = parts + (((size_t)c0 * 2 + 1) * MAX_TW + o.tl) * PART_FLOATS;
-    const float* rest = parts + ((size_t)c0 * 2 * MAX_TW + o.tl) * PART_FLOATS;
-    auto part = [&](int c) { return c == 0 ? first : rest + (size_t)c * 2 * MAX_TW * PART_FLOATS; };
-    // every part's weight for every row, in the drained rings
-    float* wt = reinterpret_cast<float*>(base_ptr);                // [row][part]
-    float* sums = wt + MAX_ROWS * MAX_CTAS;                        // [row][part]
-    float* totals = sums + MAX_ROWS * MAX_CTAS;                    // [row]
-    static_assert((2 * MAX_ROWS * MAX_CTAS + MAX_ROWS) * 4 <= NW * RING, "weights fit in the rings");
-    for (int i = threadIdx.x; i < o.rows * n; i += NW * 32) {
-      const int r = i / n, c = i - r * n;
-      wt[r * MAX_CTAS + c] = __ldcg(part(c) + RT * D + r);
-      sums[r * MAX_CTAS + c] = __ldcg(part(c) + RT * D + RT + r);
+  // every part's weight for every row of the items that fall to this block, in the
+  // drained rings: [item's rows][its parts], as many items at a time as fit
+  constexpr int ROOM = (NW * RING / 4 - MAX_OPENS * MAX_ROWS - NW * 32 * 4) / 2;
+  static_assert(MAX_ROWS * MAX_CTAS <= ROOM, "one item always fits");
+  float* weight = reinterpret_cast<float*>(base_ptr);
+  float* part_sum = weight + ROOM;
+  float* item_sum = part_sum + ROOM;                 // [item][row]
+  float4* shared_sum = reinterpret_cast<float4*>(item_sum + MAX_OPENS * MAX_ROWS);   // [thread]
+  static_assert(ROOM % 2 == 0, "16-byte places");
+  auto first_block = [&](const Open& o) { return (int)quotient((o.unit + 1) * G - 1, T); };
+  // an item is the last of its first block, and the first of the others
+  auto part = [&](const Open& o, int c0, int c) {
+    return parts + (((size_t)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * MAX_TW + o.tl) * PART_FLOATS;
+  };
+  __threadfence();
+  for (int from = 0; from < opens;) {
+    // items from .. to - 1; each thread finds the same places
+    int to = from, used = 0;
+    for (; to < opens; ++to) {
+      if (!sh.last[to]) continue;
+      const int need = sh.open[to].rows * sh.blocks[to];
+      if (used + need > ROOM) break;
+      used += need;
     }
-    __syncthreads();
-    for (int r = warp; r < o.rows; r += NW) {
-      float M = -INFINITY;
-      for (int c = lane; c < n; c += 32) M = fmaxf(M, wt[r * MAX_CTAS + c]);
-      for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
-      const float Mu = M == -INFINITY ? 0.f : M;
-      float sum = 0.f;
-      for (int c = lane; c < n; c += 32) {
-        const float w = ex2(wt[r * MAX_CTAS + c] - Mu);
-        wt[r * MAX_CTAS + c] = w;
-        sum = fmaf(w, sums[r * MAX_CTAS + c], sum);
+    auto place = [&](int j) {
+      int at = 0;
+      for (int i = from; i < j; ++i)
+        if (sh.last[i]) at += sh.open[i].rows * sh.blocks[i];
+      return at;
+    };
+    // a warp an item: the rows' maxima and sums in every block, then the weights
+    for (int j = from + warp; j < to; j += NW) {
+      if (!sh.last[j]) continue;
+      const Open& o = sh.open[j];
+      const int n = sh.blocks[j], at = place(j), c0 = first_block(o);
+#pragma unroll 4
+      for (int i = lane; i < o.rows * n; i += 32) {
+        const float* p = part(o, c0, i % n) + RT * D + i / n;
+        weight[at + i] = __ldcg(p);
+        part_sum[at + i] = __ldcg(p + RT);
       }
-      for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-      if (lane == 0) totals[r] = sum;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < o.rows * (D / 4); i += NW * 32) {
-      const int r = i / (D / 4), d4 = i % (D / 4);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int c = 0; c < n; ++c)
-        add(x, wt[r * MAX_CTAS + c], __ldcg(reinterpret_cast<const float4*>(part(c) + r * D + d4 * 4)));
-      store(o, r, d4, x, totals[r]);
+    for (int j = from; j < to; ++j) {
+      if (!sh.last[j]) continue;
+      const int n = sh.blocks[j], rows = sh.open[j].rows, at = place(j);
+      const int width = n <= 16 ? 16 : 32;           // lanes a row
+      for (int r = threadIdx.x / width; r < (rows + 1) / 2 * 2; r += NW * 32 / width) {
+        float* w = weight + at + r * n;
+        const int lane_c = lane % width, end = r < rows ? n : 0;
+        float M = -INFINITY;
+        for (int c = lane_c; c < end; c += width) M = fmaxf(M, w[c]);
+        for (int k = width / 2; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+        const float Mu = M == -INFINITY ? 0.f : M;
+        float sum = 0.f;
+        for (int c = lane_c; c < end; c += width) {
+          const float x = ex2(w[c] - Mu);
+          w[c] = x;
+          sum = fmaf(x, part_sum[at + r * n + c], sum);
+        }
+        for (int k = width / 2; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        if (lane_c == 0 && r < rows) item_sum[j * MAX_ROWS + r] = sum;
+      }
     }
-    __syncthreads();                               // the weights have been read
+    __syncthreads();
+    // As above.  Few rows leave warps over, so that `split` of them share a row's
+    // parts (every split-th each) and meet in shared memory.
+    auto finish = [&](auto batch, int split) {
+      constexpr int U = decltype(batch)::value;
+      const int groups = (rmax + U * RPW - 1) / (U * RPW), s = warp % split, all = (to - from) * groups;
+      // the same number of rounds for every warp: each is at the barrier in each round
+      for (int i0 = 0; i0 < all; i0 += NW / split) {
+        const int i = i0 + warp / split, nth = min(i, all - 1) / groups;
+        const int j = from + nth, r0 = (i - nth * groups) * U * RPW + lane_row;
+        const bool mine = i < all && sh.last[j];
+        const Open& o = sh.open[j];
+        float4 x[U] = {};
+        if (mine) {
+          const int n = sh.blocks[j], c0 = first_block(o);
+          const float* w = weight + place(j) + r0 * n;
+          // part c: the second of block c0, the first of block c0 + c
+          const float* p = parts + ((size_t)c0 * 2 * MAX_TW + o.tl) * PART_FLOATS + r0 * D + lane_quad * 4;
+          constexpr size_t next = (size_t)2 * MAX_TW * PART_FLOATS;
+#pragma unroll 8
+          for (int c = s; c < n; c += split) {
+            const float* q = p + (c == 0 ? next / 2 : c * next);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              if (r0 + u * RPW < o.rows)
+                add(x[u], w[u * RPW * n + c], __ldcg(reinterpret_cast<const float4*>(q + u * RPW * D)));
+          }
+        }
+        if constexpr (U == 1) {
+          if (split > 1) {
+            shared_sum[threadIdx.x] = x[0];
+            __syncthreads();
+            if (s == 0)
+              for (int k = 1; k < split; ++k) add(x[0], 1.f, shared_sum[threadIdx.x + k * 32]);
+            __syncthreads();
+          }
+        }
+        if (!mine || s != 0) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (r0 + u * RPW < o.rows) store(o, r0 + u * RPW, lane_quad, x[u], item_sum[j * MAX_ROWS + r0 + u * RPW]);
+      }
+    };
+    const int pairs = (to - from) * ((rmax + RPW - 1) / RPW);
+    if (pairs <= NW) finish(std::integral_constant<int, 1>{}, pairs <= 1 ? 8 : pairs <= 2 ? 4 : pairs <= 4 ? 2 : 1);
+    else finish(std::integral_constant<int, 4>{}, 1);
+    __syncthreads();                                 // the weights have been read
+    from = to;
   }
 }
 
