@@ -153,7 +153,7 @@ constexpr int MAX_TW = 4;                // warps that share a slab's keys, a ti
 constexpr int RING = 3 * 2 * SLAB * 128; // bytes of a warp's ring
 constexpr int PV_EXP = 14;               // P times the page's scale is below 2^PV_EXP in fp16
 constexpr int MIN_EXP = -112;
-constexpr int WHOLE_EXTRA = 8;          // of 8-row slabs; see its use
+constexpr int WHOLE_EXTRA = 6;          // see its use
 
 template <int D, int NT>
 struct Cfg {
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   // so they are taken unless the fullest block's warps get longer than that.
   const u64 share = quotient(T + gridDim.x * workers - 1, gridDim.x * workers);
   const int blocks = min((int)gridDim.x, I);
-  const bool by_item = I > 0 && ((u64)((I + blocks - 1) / blocks) * longest + workers - 1) / workers <= share + WHOLE_EXTRA / NT;
+  const bool by_item = I > 0 && ((u64)((I + blocks - 1) / blocks) * longest + workers - 1) / workers <= share + WHOLE_EXTRA;
   const u64 G = by_item ? (u64)blocks : T < gridDim.x ? T : gridDim.x;   // every block up to G has a unit
   const u64 cta = blockIdx.x;
   if (cta >= G) return;

@@ -13,6 +13,7 @@
 
 #include <atomic>
 #include <cfloat>
+#include <cstddef>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -327,10 +328,11 @@ struct alignas(16) Cluster {
   unsigned bins[FT];        // the threshold's histogram
   ull list[LIST];           // first block: candidates, key << 32 | ~index
   ull all[MAX_C * FW];      // every warp's kept mass
-  ull warp_mass[FW];        // read by the cluster
+  ull warp_mass[FW], warp_above[FW];   // read by the cluster
   unsigned warp_count[FW];  // read by the cluster
   unsigned red[2][FW];
-  unsigned top, low;        // read by the cluster
+  unsigned top, low, bound_key;   // read by the cluster
+  float group_mass[FW], block_mass;   // the latter too
   unsigned lo[2], hi[2];    // read by the cluster, by turns
   unsigned seg_n[MAX_C];    // first block: of each block, in parts of the list
   ull few[SMALL_K];         // the first ranks
@@ -444,12 +446,13 @@ __device__ __forceinline__ int pad_list(Cluster& sh, int m) {
   return n2;
 }
 
-// The draw where the first block's list holds every token that can be kept: both
-// cuts in rank order, then the running mass in index order.
-__device__ __forceinline__ void draw_from_list(const SampleArgs& a, Cluster& sh, int r, int n, int k, float p, float least,
-                               float u, float t) {
+// The draw where the first block's list holds every token that can be kept, the list
+// sorted by rank for both cuts, then by index for the draw.  `mass`: what top-p takes
+// its share of, 0 for the mass of the k first.
+__device__ __forceinline__ void draw_by_sorting(const SampleArgs& a, Cluster& sh, int r, int n, int k, float p,
+                                                float least, float u, float t, ull mass) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  constexpr int PER = TOP_K_LIST / FT;               // places of a thread
+  constexpr int PER = LIST / FT;                     // places of a thread
   sort_list(sh, pad_list(sh, n));
   const unsigned top = (unsigned)(sh.list[0] >> 32);
   const Row row{key_logit(top), __fdiv_rn(1.f, t)};
@@ -470,7 +473,7 @@ __device__ __forceinline__ void draw_from_list(const SampleArgs& a, Cluster& sh,
     unsigned none = 0;
     block_prefix(sh, none, before);
     if (warp == 0) {
-      const ull x = whole_bound(__dmul_rn((double)p, __ull2double_rn(totals())));
+      const ull x = whole_bound(__dmul_rn((double)p, __ull2double_rn(mass ? mass : totals())));
       if (lane == 0) sh.m_above = x;
     }
     __syncthreads();
@@ -551,6 +554,210 @@ __device__ __forceinline__ unsigned kth_bin(const Cluster& sh, int k) {
     before += c[q];
   }
   return __reduce_min_sync(0xffffffffu, best);
+}
+
+// The same without sorting, where no bin of the three histograms is crowded: the k-th
+// rank and top-p's cut by bins even in the logit, the draw by bins even in the index;
+// the tokens of the bin in question are compared with one another.  False (and the
+// list as it was, but for dropped entries of 0) if a bin is crowded.
+constexpr int EDGE = 512;                            // tokens of a bin that are compared
+
+__device__ __forceinline__ bool draw_by_bins(const SampleArgs& a, Cluster& sh, int r, int n, int k, float p, float least,
+                                             float u, float t, ull mass) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  // the tokens of the bin in question and their masses lie in the unused parts of the
+  // histograms' memory
+  unsigned (*hist)[FT] = sh.mass[0];                 // three words, as in the search
+  ull* edge = reinterpret_cast<ull*>(&sh.mass[1][0][0]);
+  ull* edge_mass = reinterpret_cast<ull*>(&sh.count[0][0]);
+  static_assert(sizeof(sh.count) >= EDGE * 8 && sizeof(sh.mass[1]) >= EDGE * 8 && offsetof(Cluster, mass) % 8 == 0 &&
+                    sizeof(sh.mass[0]) % 8 == 0, "edge");
+  unsigned hi = 0, lo = 0xffffffffu;
+  for (int i = tid; i < n; i += FT) {
+    const unsigned key = (unsigned)(sh.list[i] >> 32);
+    hi = max(hi, key);
+    lo = min(lo, key);
+  }
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  if (lane == 0) {
+    sh.red[0][warp] = hi;
+    sh.red[1][warp] = lo;
+  }
+  sh.bins[tid] = 0;
+  for (int w = 0; w < 3; ++w) hist[w][tid] = 0;
+  __syncthreads();
+  const unsigned top = __reduce_max_sync(0xffffffffu, sh.red[0][lane % FW]);
+  lo = __reduce_min_sync(0xffffffffu, sh.red[1][lane % FW]);
+  const Row row{key_logit(top), __fdiv_rn(1.f, t)};
+  const float range = row.top - key_logit(lo), scale = range > 0.f && range < INFINITY ? 511.9f / range : 0.f;
+  auto bin = [&](ull x) { return min(FT - 1, (int)((row.top - key_logit((unsigned)(x >> 32))) * scale)); };
+  auto mass_at = [&](ull x) { return mass_of(logit_weight(row, key_logit((unsigned)(x >> 32)))); };
+  auto add = [&](int b, ull m) {
+    atomicAdd(&hist[0][b], (unsigned)m & 0x3fffu);
+    atomicAdd(&hist[1][b], (unsigned)(m >> 14) & 0x1fffu);
+    if (m >> 27) atomicAdd(&hist[2][b], (unsigned)(m >> 27));
+  };
+  auto sum = [&](int b) { return (ull)hist[0][b] + ((ull)hist[1][b] << 14) + ((ull)hist[2][b] << 27); };
+  // f(entry, place) for this thread's entries
+  auto each = [&](auto f) {
+    for (int i = tid; i < n; i += FT)
+      if (sh.list[i]) f(sh.list[i], i);
+  };
+
+  // ---- the k-th rank
+  if (n > k) {
+    each([&](ull x, int) { atomicAdd(&sh.bins[bin(x)], 1u); });
+    __syncthreads();
+    unsigned c = sh.bins[tid];
+    const unsigned own = c;
+    ull none = 0;
+    block_prefix(sh, c, none);
+    if (c < (unsigned)k && c + own >= (unsigned)k) {
+      sh.best = tid;
+      sh.n_above = c;
+    }
+    if (tid == 0) sh.local_n = 0;
+    __syncthreads();
+    const int best = (int)sh.best, above = (int)sh.n_above;
+    if (sh.bins[best] > EDGE) return false;
+    each([&](ull x, int i) {
+      const int b = bin(x);
+      if (b == best) edge[atomicAdd(&sh.local_n, 1u)] = x;
+      if (b > best) sh.list[i] = 0;
+    });
+    __syncthreads();
+    const int m = (int)sh.local_n;
+    each([&](ull x, int i) {
+      if (bin(x) != best) return;
+      int rank = above;
+      for (int j = 0; j < m; ++j) rank += edge[j] > x;
+      if (rank >= k) sh.list[i] = 0;
+    });
+    __syncthreads();
+    sh.bins[tid] = 0;
+    __syncthreads();
+  }
+
+  // ---- top-p
+  if (!(p >= 1.f)) {
+    each([&](ull x, int) {
+      const ull m = mass_at(x);
+      const int b = bin(x);
+      if (m) add(b, m);
+      atomicAdd(&sh.bins[b], 1u);
+    });
+    __syncthreads();
+    const ull own = sum(tid);
+    ull before = own;
+    unsigned none = 0;
+    block_prefix(sh, none, before);
+    if (warp == 0) {
+      ull total = mass;
+      if (total == 0)
+        for (int w = 0; w < FW; ++w) total += sh.scan_m[w];
+      const ull x = whole_bound(__dmul_rn((double)p, __ull2double_rn(total)));
+      if (lane == 0) sh.bound = x;
+    }
+    if (tid == 0) {
+      sh.best = 0;
+      sh.local_n = 0;
+    }
+    __syncthreads();
+    const ull bound = sh.bound;
+    if (own && (before == 0 || before < bound)) atomicMax(&sh.best, (unsigned)tid);
+    __syncthreads();
+    const int best = (int)sh.best;
+    if (tid == best) sh.m_above = before;
+    __syncthreads();
+    if (sh.bins[best] > EDGE) return false;
+    each([&](ull x, int i) {
+      const int b = bin(x);
+      if (b == best) {
+        const unsigned at = atomicAdd(&sh.local_n, 1u);
+        edge[at] = x;
+        edge_mass[at] = mass_at(x);
+      }
+      if (b > best) sh.list[i] = 0;
+    });
+    __syncthreads();
+    const int m = (int)sh.local_n;
+    const ull above = sh.m_above;
+    each([&](ull x, int i) {
+      if (bin(x) != best) return;
+      ull y = above;
+      for (int j = 0; j < m; ++j) y += edge[j] > x ? edge_mass[j] : 0;
+      if (y != 0 && y >= bound) sh.list[i] = 0;
+    });
+    __syncthreads();
+    sh.bins[tid] = 0;
+    for (int w = 0; w < 3; ++w) hist[w][tid] = 0;
+    __syncthreads();
+  }
+
+  // ---- min-p, and the draw in index order
+  const int width = (a.vocab + FT - 1) / FT;
+  auto place = [&](ull x) { return (int)((unsigned)~(unsigned)x / (unsigned)width); };
+  auto kept = [&](ull x) -> ull {
+    const float w = logit_weight(row, key_logit((unsigned)(x >> 32)));
+    return w >= least ? mass_of(w) : 0;
+  };
+  each([&](ull x, int) {
+    const ull m = kept(x);
+    if (m == 0) return;
+    add(place(x), m);
+    atomicAdd(&sh.bins[place(x)], 1u);
+  });
+  __syncthreads();
+  const ull own = sum(tid);
+  ull before = own;
+  unsigned none = 0;
+  block_prefix(sh, none, before);
+  ull total = 0;
+  for (int w = 0; w < FW; ++w) total += sh.scan_m[w];
+  if (warp == 0) {
+    const ull x = draw_target(u, total);
+    if (lane == 0) sh.bound = x;
+  }
+  if (tid == 0) sh.local_n = 0;
+  __syncthreads();
+  const ull target = sh.bound;
+  if (before <= target && target < before + own) {
+    sh.best = tid;
+    sh.m_above = before;
+  }
+  __syncthreads();
+  const int best = (int)sh.best;
+  if (sh.bins[best] > EDGE) return false;
+  each([&](ull x, int) {
+    if (place(x) != best) return;
+    const ull m = kept(x);
+    if (m == 0) return;
+    const unsigned at = atomicAdd(&sh.local_n, 1u);
+    edge[at] = x;
+    edge_mass[at] = m;
+  });
+  __syncthreads();
+  const int m = (int)sh.local_n;
+  for (int i = tid; i < m; i += FT) {
+    const ull x = edge[i];
+    const unsigned index = ~(unsigned)x;
+    ull y = sh.m_above;
+    for (int j = 0; j < m; ++j) y += ~(unsigned)edge[j] < index ? edge_mass[j] : 0;
+    if (y <= target && target < y + edge_mass[i]) {
+      a.token[r] = (int)index;
+      if (a.logprob)
+        a.logprob[r] = logit_z(row, key_logit((unsigned)(x >> 32))) - logf(__ull2float_rn(total) * 0x1p-40f);
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ void draw_from_list(const SampleArgs& a, Cluster& sh, int r, int n, int k, float p, float least,
+                                               float u, float t, ull mass) {
+  if (draw_by_bins(a, sh, r, n, k, p, least, u, t, mass)) return;
+  __syncthreads();
+  draw_by_sorting(a, sh, r, n, k, p, least, u, t, mass);
 }
 
 // The same for k up to SMALL_K, with the candidates in the list's C parts: ranks by
@@ -755,16 +962,18 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
     low = __reduce_min_sync(0xffffffffu, sh.warp_count[lane % FW]);
     if (tid == 0) sh.low = low;
   };
-  const bool by_list = cuts && k > 0 && k <= SMALL_K;
-  if (by_list) {
-    // ---- candidates for the first k ranks.  Every group's largest logit is an
+  const bool by_list = cuts && k > 0 && k <= SMALL_K, by_mass = cuts && !(k > 0 && k < a.vocab);
+  unsigned bound = 0;
+  if (by_list || by_mass) {
+    // ---- candidates for the first k ranks (top-p alone: for as many as the list may
+    // take).  Every group's largest logit is an
     // element, so the k-th largest of them bounds the block's k-th rank from below;
     // a histogram of them finds a bound just under it.  What has no mass is no
     // candidate.
     const float ltop = key_logit(top);
     const unsigned floor_key =
         top <= kKeyNegInf ? 0xffffffffu : ltop == INFINITY ? top : max(kKeyNegInf + 1, order_key(ltop - ZERO_Z * t));
-    unsigned bound = floor_key;
+    bound = floor_key;
     if (top > kKeyNegInf) {
       // bins even in the logit; an infinite range falls into one bin
       const float range = ltop - key_logit(gmin);
@@ -775,7 +984,7 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
           atomicAdd(&sh.bins[min(FT - 1, (int)((ltop - key_logit(group[q])) * scale))], 1u);
       __syncthreads();
       if (warp == 0) {
-        const unsigned best = kth_bin(sh, k);
+        const unsigned best = kth_bin(sh, by_list ? k : LIST * 3 / 4 / C);
         if (lane == 0) sh.best = best;
       }
       __syncthreads();
@@ -783,8 +992,18 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
       if (sh.best < FT)
         bound = max(floor_key, scale > 0.f ? order_key(ltop - (sh.best + 1.01f) / scale) : gmin);
       sh.bins[tid] = 0;
+      if (by_mass) {
+        // about how much mass the groups' largest have, in the block's largest
+        float x = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x += logit_weight(Row{ltop, __fdiv_rn(1.f, t)}, key_logit(group[q]));
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0) sh.group_mass[warp] = x;
+      }
     }
-    if (C > 1) cluster_wait();
+  }
+  if (C > 1) cluster_wait();
+  if (by_list) {
     ull* list = in_block(&sh.list[0], 0);
     // straight into the first block's list, each block's in a part of its own
     each([&](unsigned key, int i) {
@@ -795,9 +1014,16 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
     });
     __syncthreads();
     if (tid == 0) *in_block(&sh.seg_n[rank], 0) = sh.local_n;
-  } else {
-    if (cuts) block_low();
-    if (C > 1) cluster_wait();
+  } else if (by_mass) {
+    __syncthreads();
+    float x = top > kKeyNegInf ? sh.group_mass[lane % FW] : 0.f;
+    for (int o = FW / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (tid == 0) {
+      sh.bound_key = bound;
+      sh.block_mass = x;
+    }
+  } else if (cuts) {
+    block_low();
   }
   sync_cluster(C);
   if (by_list) {
@@ -838,6 +1064,92 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
   const Row row{key_logit(top), __fdiv_rn(1.f, t)};
   auto mass_at = [&](unsigned key) { return mass_of(logit_weight(row, key_logit(key))); };
 
+  bool few = false;
+  if (by_mass) {
+    // top-p alone: will the keys that every block's bound lets through reach the cut?
+    // Those below it have at most its weight each, a quarter of that on average say.
+    // Both ways give the same token; this one costs a pass more where it fails.
+    float sum = 0.f;
+    for (int c = 0; c < C; ++c) {
+      bound = max(bound, *in_block(&sh.bound_key, c));
+      sum += *in_block(&sh.block_mass, c) * logit_weight(row, key_logit(*in_block(&sh.top, c)));
+    }
+    few = 0.25f * (float)a.vocab * logit_weight(row, key_logit(bound)) <= (1.f - p) * sum;
+  }
+  if (few) {
+    // ---- the mass of all, and of those keys.  Where that reaches the cut, they are
+    // all there is to choose from.
+    ull all = 0, above = 0;
+    unsigned n = 0;
+    each([&](unsigned key, int) {
+      if (key <= kKeyNegInf) return;
+      const ull m = mass_at(key);
+      all += m;
+      if (key >= bound) {
+        above += m;
+        ++n;
+      }
+    });
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      above += __shfl_xor_sync(0xffffffffu, above, o);
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) {
+      sh.warp_mass[warp] = all;
+      sh.warp_above[warp] = above;
+      sh.warp_count[warp] = n;
+    }
+    sync_cluster(C);
+    // a thread a warp of the cluster: totals, and the list places of the blocks before
+    all = above = 0;
+    n = 0;
+    if (tid < C * FW) {
+      all = in_block(&sh.warp_mass[0], tid / FW)[tid % FW];
+      above = in_block(&sh.warp_above[0], tid / FW)[tid % FW];
+      n = in_block(&sh.warp_count[0], tid / FW)[tid % FW];
+    }
+    unsigned at = tid < rank * FW ? n : 0u;
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      above += __shfl_xor_sync(0xffffffffu, above, o);
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    at = __reduce_add_sync(0xffffffffu, at);
+    if (lane == 0 && warp < MAX_C * FW / 32) {
+      sh.scan_m[warp] = all;
+      sh.all[warp] = above;
+      sh.scan_c[warp] = n;
+      sh.red[0][warp] = at;
+    }
+    if (tid == 0) sh.local_n = 0;
+    __syncthreads();
+    all = above = 0;
+    n = at = 0;
+    for (int w = 0; w < MAX_C * FW / 32; ++w) {
+      all += sh.scan_m[w];
+      above += sh.all[w];
+      n += sh.scan_c[w];
+      at += sh.red[0][w];
+    }
+    if (warp == 0) {
+      const ull x = whole_bound(__dmul_rn((double)p, __ull2double_rn(all)));
+      if (lane == 0) sh.bound = x;
+    }
+    __syncthreads();
+    if (n <= LIST && above >= sh.bound) {
+      ull* list = in_block(&sh.list[0], 0) + at;
+      each([&](unsigned key, int i) {
+        if (key >= bound) list[atomicAdd(&sh.local_n, 1u)] = ((ull)key << 32) | (unsigned)~i;
+      });
+      sync_cluster(C);
+      if (rank == 0) draw_from_list(a, sh, r, (int)n, (int)n, p, least, u, t, all);
+      if (C > 1) cluster_sync();                     // nobody leaves while its memory is read
+      return;
+    }
+    sync_cluster(C);                                 // the sums have been read
+  }
+
   // ---- cuts, as the last place kept
   Place cut{0u, 0x7fffffff};
   if (greedy) {
@@ -861,8 +1173,10 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
     // ---- the general search: bins even in the logit over the range that has mass; the
     // tokens of the bin with the cut are sorted in the first block's list, or, if
     // they are too many (equal logits), binned again by their keys until one is left
-    if (by_list) block_low();
-    if (by_list) sync_cluster(C);
+    if (by_list || by_mass) {
+      block_low();
+      sync_cluster(C);
+    }
     unsigned low = sh.low;
     for (int c = 0; c < C; ++c) low = min(low, *in_block(&sh.low, c));
     // The last place kept by count (the first k) or by mass (less than p of all before)
@@ -962,7 +1276,7 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
             if (x >= 0 && x <= best) list[atomicAdd(&sh.local_n, 1u)] = ((ull)key << 32) | (unsigned)~i;
           });
           sync_cluster(C);
-          if (rank == 0) draw_from_list(a, sh, r, (int)(n_above + n_equal), k, p, least, u, t);
+          if (rank == 0) draw_from_list(a, sh, r, (int)(n_above + n_equal), k, p, least, u, t, 0);
           return true;
         }
         if (n_equal <= TOP_K_LIST) {
