@@ -255,3 +255,38 @@ def test_many_long_rows(cuda_lib, dtype, vocab, ld):
     l[0] = math.nan
     none, lp = call(l[:1].expand(rows, -1).contiguous(), u, top_k=[5] * rows)
     assert (none == -1).all() and (lp == -math.inf).all()
+
+
+@pytest.mark.parametrize("vocab", [400003, 1 << 20])
+def test_largest_vocabularies(cuda_lib, vocab):
+    # longer than a cluster's shared memory holds
+    rows = 5
+    l, u = make(rows, vocab, torch.bfloat16, vocab)
+    t, k = torch.tensor([0.8, 1.0, 0.5, 1.0, 2.0]), torch.tensor([50, 0, 0, 1000, 7])
+    p, m = torch.tensor([0.95, 1.0, 0.7, 0.9, 1.0]), torch.tensor([0.0, 0.1, 0.0, 0.0, 0.0])
+    token, _ = call(l, u, temperature=t.tolist(), top_k=k.tolist(), top_p=p.tolist(), min_p=m.tolist())
+    assert np.array_equal(token, _rule(l, u, t, k, p, m))
+
+
+@pytest.mark.parametrize("vocab", [5000, 32000, 131071])
+def test_crowded_bins(cuda_lib, vocab):
+    # runs of equal and of nearly equal logits where the cuts and the draw fall
+    rows = 64
+    gen = torch.Generator().manual_seed(vocab)
+    l = torch.randn(rows, vocab, generator=gen)
+    at = torch.randperm(vocab, generator=gen)
+    l[:16, at[:1500]] = 6.0                                   # equal, anywhere
+    l[16:32, :1500] = 6.0                                     # equal, side by side
+    l[32:40, at[:2000]] = 6.0 + 1e-6 * torch.rand(8, 2000, generator=gen)
+    l[40:48] = torch.round(l[40:48])                          # a few values in all
+    l[48:52] = 1.0
+    l[52:, :3] += 30.0                                        # a few far above
+    u = np.random.default_rng(vocab).random(rows).astype(np.float32)
+
+    def of(*v):
+        return torch.tensor(v)[torch.arange(rows) % len(v)]
+    for t, k, p in ((of(1.0, 0.7), of(1000, 700, 300), of(1.0, 0.9, 0.5, 0.99, 0.2)),
+                    (of(1.0, 3.0, 0.2), of(0), of(0.9, 0.5, 0.99, 0.05)), (of(1.0), of(50, 64, 3000), of(0.97, 0.5, 1.0, 0.1))):
+        m = of(0.0, 0.0, 0.3)
+        token, _ = call(l, u, temperature=t.tolist(), top_k=k.tolist(), top_p=p.tolist(), min_p=m.tolist())
+        assert np.array_equal(token, _rule(l, u, t, k, p, m))
