@@ -104,7 +104,7 @@ def test_one_token(cuda_lib, fmt, dim, interleaved, base):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("most", [2, 5, 8, 9])
+@pytest.mark.parametrize("most", [2, 5, 8, 9, 16, 17])
 def test_a_few_tokens(cuda_lib, fmt, dim, most):
     # a few tokens each, across a page's edge, none at all
     for interleaved in (False, True):

@@ -222,7 +222,7 @@ def test_without_logprob_and_in_a_graph(cuda_lib):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("vocab,ld", [(16384, None), (40000, 40003), (40004, 40008), (131071, None)])
+@pytest.mark.parametrize("vocab,ld", [(8000, None), (16384, None), (40000, 40003), (40004, 40008), (131071, None)])
 def test_many_long_rows(cuda_lib, dtype, vocab, ld):
     # a row for each SM and more: rows with few ranks stream through one block each, the
     # others and those that do not suit it go to a second kernel
@@ -232,7 +232,7 @@ def test_many_long_rows(cuda_lib, dtype, vocab, ld):
     l.masked_fill_(torch.rand(rows, vocab, generator=gen) < 0.01, -math.inf)
     l[1] = l[1].sort().values                       # ascending: every tile beats the ones before
     l[2] = 0.5                                      # all equal
-    l[3, :20000] = -math.inf                        # the first tile has nothing
+    l[3, :20000] = -math.inf                        # the first tile has nothing (the shortest: the row)
     l[4] = -math.inf
     l[4, vocab - 1] = 1.0
     l[5, :9000] -= 50.0
@@ -247,7 +247,7 @@ def test_many_long_rows(cuda_lib, dtype, vocab, ld):
         return x
     t, k, p, m = of(0.3, 2.0, 0.8), of(0, 1, 3, 64, 65, 900, 50), of(1.0, 0.5, 0.95), of(0.0, 0.2, 0.01)
     token, logprob = call(l, u, ld=ld, temperature=t.tolist(), top_k=k.tolist(), top_p=p.tolist(), min_p=m.tolist())
-    some = (l > -math.inf).any(1).numpy()           # row 3 of the shortest has none
+    some = (l > -math.inf).any(1).numpy()           # row 3 of short ones has none
     assert np.array_equal(token, np.where(some, _rule(l, u, t, k, p, m), -1))
     assert np.isfinite(logprob[some]).all() and (logprob <= 0).all() and (logprob[~some] == -math.inf).all()
     greedy, lp = call(l, u, ld=ld, temperature=[0.0] * rows)
