@@ -1475,9 +1475,10 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
 // Many rows at once, for those whose draw is among the first SMALL_K ranks (or the
 // first alone): a block streams through a row in tiles and lists what may be among
 // them.  The k-th largest of the first tile's groups bounds the k-th rank of the row
-// from below, so a later logit is mostly one comparison; where the list gets long, its
-// own k-th rank is a better bound.  A row whose single tile holds more than the list
-// (ascending logits, say) is left to the other kernel.
+// from below, so a thread's later logits are mostly a maximum and one comparison a
+// tile; every fourth tile a long list's own k-th rank is a better bound.  A row of
+// which four tiles hold more than the list (ascending logits, say) is left to the
+// other kernel.
 constexpr int TILE = 16;                      // logits of a thread in a tile
 
 // The list's bound for the k-th rank: a histogram of its keys; drops what is below it.
@@ -1548,12 +1549,13 @@ __global__ void __launch_bounds__(FT, 2) sample_stream_kernel(const SampleArgs a
   // logit e of vector v of tile x: index ((x * (TILE / VEC) + v) * FT + tid) * VEC + e
   auto index = [&](int x, int v) { return ((x * (TILE / VEC) + v) * FT + tid) * VEC; };
   auto load = [&](int x, float (&l)[TILE]) {
+    const bool full = (x + 1) * (FT * TILE) <= a.vocab;   // no logit of the tile is past the row
 #pragma unroll
     for (int v = 0; v < TILE / VEC; ++v) {
       const int i = index(x, v);
       if constexpr (VEC == 1) {
-        l[v] = i < a.vocab ? (float)row[i] : -INFINITY;
-      } else if (i + VEC <= a.vocab) {
+        l[v] = full || i < a.vocab ? (float)row[i] : -INFINITY;
+      } else if (full || i + VEC <= a.vocab) {
         if constexpr (sizeof(T) == 4) {
           const float4 y = *reinterpret_cast<const float4*>(row + i);
           l[v * 4] = y.x;
@@ -1615,25 +1617,35 @@ __global__ void __launch_bounds__(FT, 2) sample_stream_kernel(const SampleArgs a
     if (sh.best < FT) bound = max(bound, scale > 0.f ? order_key(ltop - (sh.best + 1.01f) / scale) : gmin);
   }
   // ---- the tiles
-  for (int x = 0; x < tiles; ++x) {
-    const float lbound = key_logit(bound);           // NaN compares false
+  auto look = [&](int x, const float (&l)[TILE]) {
+    const float lbound = key_logit(bound);
+    float most = fmaxf(l[0], l[1]);                  // NaN is passed over
+#pragma unroll
+    for (int v = 2; v < TILE; ++v) most = fmaxf(most, l[v]);
+    if (!(most >= lbound)) return;
 #pragma unroll
     for (int v = 0; v < TILE; ++v)
       if (l[v] >= lbound) {
         const unsigned at = atomicAdd(&sh.local_n, 1u);
         if (at < LIST) sh.list[at] = ((ull)order_key(l[v]) << 32) | (unsigned)~(index(x, v / VEC) + v % VEC);
       }
-#pragma unroll
-    for (int v = 0; v < TILE; ++v) l[v] = next[v];
-    if (x + 2 < tiles) load(x + 2, next);
-    __syncthreads();
-    const unsigned n = sh.local_n;
-    if (n > LIST) {
-      if (tid == 0) a.token[r] = kNotDone;
-      return;
+  };
+  for (int x = 0; x < tiles; x += 2) {
+    look(x, l);
+    if (x + 2 < tiles) load(x + 2, l);
+    if (x + 1 < tiles) look(x + 1, next);
+    if (x + 3 < tiles) load(x + 3, next);
+    // every fourth tile, and after the last: is the list long?
+    if (x % 4 == 2 || x + 2 >= tiles) {
+      __syncthreads();
+      const unsigned n = sh.local_n;
+      if (n > LIST) {
+        if (tid == 0) a.token[r] = kNotDone;
+        return;
+      }
+      __syncthreads();                               // n has been read
+      if (n > LIST / 2) bound = max(bound, tighten(sh, k));
     }
-    __syncthreads();                                 // n has been read
-    if (n > LIST / 2) bound = max(bound, tighten(sh, k));
   }
   if (sh.local_n == 0) {
     if (tid == 0) {
@@ -1701,8 +1713,8 @@ int launch_any(const SampleArgs& a, int num_sms, cudaStream_t s) {
   const int Q = (a.vocab + C * FT * 4 - 1) / (C * FT * 4);
   // Enough rows to fill the GPU a block each, and long enough for the second launch.
   // Measured (bf16, top-k 50), with it and by the cluster kernel alone: 152 x 16384
-  // 11.9 and 10.0 us, 304 x 16384 13.3 and 19.2, 152 x 32000 16.0 and 28.0,
-  // 152 x 131071 36.6 and 60.4, 384 x 131071 92.8 and 150.9.  Where every row is the
+  // 11.9 and 10.0 us, 304 x 16384 13.2 and 19.2, 152 x 32000 15.6 and 28.0,
+  // 152 x 131071 35.8 and 60.4, 384 x 131071 92.1 and 150.9.  Where every row is the
   // other kernel's it costs about 1 us.
   const bool stream = a.rows >= num_sms && (long long)a.rows * a.vocab >= (long long)num_sms * STREAM_VOCAB;
   if (stream) {
