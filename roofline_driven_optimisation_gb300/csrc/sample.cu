@@ -15,16 +15,17 @@
 //     through, ranked in one warp.  Longer top-k, and top-p alone: a list of up to 2048
 //     candidates in the first block, cut and drawn by histograms.  What does not fit:
 //     a search by histograms over the cluster.
-//   * sample_stream_kernel: many rows with up to 64 ranks, a block a row.
+//   * sample_stream_kernel: many rows with up to 64 ranks, a block or a few a row.
 //   * sample_kernel: rows beyond the cluster's shared memory, radix searches over
 //     global memory.
 // Measured on one GB300, GPU time: one row of 32000 with top-k 50, top-p and min-p
 // 9 us; 64 rows of 32000 bf16: the same settings 11 us, top-k 1000 with top-p 25 us,
 // top-p alone 21 to 35 us (flat rows need the search), no cut 13 us; 384 rows of
-// 131071 fp32 (201 MB): 72 us, 2.8 TB/s, against 141 us by the cluster kernel.
+// 131071 fp32 (201 MB): 68 us, 3.0 TB/s, against 141 us by the cluster kernel.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cfloat>
 #include <cstddef>
@@ -321,7 +322,7 @@ constexpr int SMALL_K = 64;                   // largest top_k whose ranks fit t
 constexpr int SEG = LIST / MAX_C;             // a block's part of the list then
 constexpr int TOP_K_LIST = 1024;              // ranks that the first block can draw from: two a thread
 constexpr int SAMPLE_Q = 4;                   // quads of a thread before a row takes more blocks
-constexpr int STREAM_VOCAB = 24576;           // logits an SM from which rows stream, see its use
+constexpr int STREAM_PART = 15000;            // logits of a row that are worth a block, see its use
 constexpr float ZERO_Z = 28.f;                // expf(-28) < 2^-40: no mass
 
 // A cut by rank: kept are larger keys, and equal ones up to index idx
@@ -892,16 +893,13 @@ __device__ __forceinline__ void draw_from_few(const SampleArgs& a, Cluster& sh, 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs a, const int C, const int Q, const int rest) {
+__device__ __forceinline__ void cluster_row(const SampleArgs& a, const int C, const int Q, const int r, const bool more) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Cluster& sh = *reinterpret_cast<Cluster*>(smem_raw);
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   uint4* const keys = reinterpret_cast<uint4*>(smem_raw + sizeof(Cluster)) + warp * Q * 32 + lane;   // quad q at [q * 32]
   const int rank = C == 1 ? 0 : (int)cluster_ctarank();
-  const int r = blockIdx.x / C;
   const int base = (rank * FW + warp) * 128 * Q + lane;   // index of key k of quad q: base + (4 q + k) * 32
-  griddep_wait();
-  if (tid == 0) griddep_launch_dependents();
 
   const float t_in = a.temperature ? a.temperature[r] : 1.f;
   const int k = a.top_k ? a.top_k[r] : 0;
@@ -911,7 +909,6 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
   // only the first rank: also where no weight, 1 at most, can reach min_p
   const bool greedy = !(t_in >= FLT_MIN) || k == 1 || !(least <= 1.f);
   const float t = t_in >= FLT_MIN ? t_in : 1.f;
-  if (rest && (greedy || (k > 0 && k <= SMALL_K)) && a.token[r] != kNotDone) return;   // sample_stream_kernel's
   // ---- read the row.  Groups are the keys at one place k of a thread's quads.
   unsigned group[4] = {0, 0, 0, 0};
   {
@@ -1052,6 +1049,7 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
       // the first block has all there is to choose from
       if (rank != 0) {
         cluster_arrive();                            // its counts have been read; nobody reads this block
+        if (more) cluster_wait();
         return;
       }
       if (n == 0) {
@@ -1471,15 +1469,47 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
   if (C > 1) cluster_sync();                         // nobody leaves while its memory is read
 }
 
+// Whether sample_stream_kernel takes row r; all settings are read at once
+__device__ __forceinline__ bool streams(const SampleArgs& a, long long r) {
+  const float t = a.temperature ? a.temperature[r] : 1.f, least = a.min_p ? a.min_p[r] : 0.f;
+  const int k = a.top_k ? a.top_k[r] : 0;
+  return !(t >= FLT_MIN) | !(least <= 1.f) | (k > 0) & (k <= SMALL_K);
+}
+
+// A cluster takes every n-th row of its n clusters, after sample_stream_kernel (`rest`)
+// those that it left.
+template <typename T>
+__global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs a, const int C, const int Q, const int rest) {
+  const int n = (int)gridDim.x / C;
+  long long r0 = blockIdx.x / C;
+  auto mine = [&]() { return r0 + (long long)(threadIdx.x % 32) * n; };
+  // the settings are older than sample_stream_kernel, which has waited for all before it
+  bool streamed = rest && mine() < a.rows && streams(a, mine());
+  griddep_wait();
+  // after sample_stream_kernel not early: the next call's blocks would gather on the SMs
+  // that these leave first (608 x 131071 86 us, now 78)
+  if (!rest && threadIdx.x == 0) griddep_launch_dependents();
+  while (r0 < a.rows) {
+    const bool left = mine() < a.rows && (!streamed || a.token[mine()] == kNotDone);
+    for (unsigned m = __ballot_sync(0xffffffffu, left); m; m &= m - 1) {
+      cluster_row<T>(a, C, Q, (int)(r0 + (long long)(__ffs(m) - 1) * n), rest);
+      __syncthreads();                               // shared memory is free
+    }
+    r0 += 32ll * n;
+    streamed = rest && mine() < a.rows && streams(a, mine());
+  }
+}
+
 // ------------------------------------------------------------------ a row a block
 // Many rows at once, for those whose draw is among the first SMALL_K ranks (or the
-// first alone): a block streams through a row in tiles and lists what may be among
-// them.  The k-th largest of the first tile's groups bounds the k-th rank of the row
-// from below, so a thread's later logits are mostly a maximum and one comparison a
-// tile; every fourth tile a long list's own k-th rank is a better bound.  A row of
-// which four tiles hold more than the list (ascending logits, say) is left to the
-// other kernel.
-constexpr int TILE = 16;                      // logits of a thread in a tile
+// first alone): a block, or C of them for every C-th tile, streams through a row and
+// lists what may be among them.  The k-th largest of the first tile's groups bounds the
+// k-th rank of the row from below, so a thread's later logits are mostly a maximum and
+// one comparison a tile; every fourth tile a long list's own k-th rank is a better
+// bound.  A row of which four tiles hold more than the list (ascending logits, say) is
+// left to the other kernel.  The next tiles' loads are in flight meanwhile, as they
+// came: widened on arrival, bf16 rows wait for them (304 x 131071 44 us, now 34 us).
+constexpr int TILE_BYTES = 64;                // of a thread, in 16-byte vectors
 
 // The list's bound for the k-th rank: a histogram of its keys; drops what is below it.
 // Whole block, after a barrier.
@@ -1530,12 +1560,13 @@ __device__ __forceinline__ unsigned tighten(Cluster& sh, int k) {
   return bound;
 }
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(FT, 2) sample_stream_kernel(const SampleArgs a) {
+template <typename T>
+__global__ void __launch_bounds__(FT, 2) sample_stream_kernel(const SampleArgs a, const int C) {
   __shared__ Cluster sh;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, r = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int rank = C == 1 ? 0 : (int)cluster_ctarank(), r = blockIdx.x / C;
   const float t_in = a.temperature ? a.temperature[r] : 1.f;
   const int k_in = a.top_k ? a.top_k[r] : 0;
   const float p_in = a.top_p ? a.top_p[r] : 1.f;
@@ -1546,37 +1577,61 @@ __global__ void __launch_bounds__(FT, 2) sample_stream_kernel(const SampleArgs a
   const int k = greedy ? 1 : k_in;
   const float p = greedy ? 1.f : p_in, least = greedy ? 0.f : least_in, t = t_in >= FLT_MIN ? t_in : 1.f;
   const T* row = static_cast<const T*>(a.logits) + (long long)r * a.ld;
-  // logit e of vector v of tile x: index ((x * (TILE / VEC) + v) * FT + tid) * VEC + e
-  auto index = [&](int x, int v) { return ((x * (TILE / VEC) + v) * FT + tid) * VEC; };
-  auto load = [&](int x, float (&l)[TILE]) {
-    const bool full = (x + 1) * (FT * TILE) <= a.vocab;   // no logit of the tile is past the row
+  // 16-byte vectors from the boundary below the row on: logit e of vector v of the
+  // block's tile x has index ((x * C + rank) * VECS + v) * FT + tid) * VEC + e - head.
+  constexpr int VEC = 16 / (int)sizeof(T), VECS = TILE_BYTES / 16, TILE = VEC * VECS;
+  const int head = (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
+  struct Tile {
+    uint32_t w[TILE_BYTES / 4];
+    __device__ __forceinline__ float operator[](int v) const {
+      if constexpr (sizeof(T) == 4) return __uint_as_float(w[v]);
+      else return __uint_as_float(v % 2 ? w[v / 2] & 0xffff0000u : w[v / 2] << 16);
+    }
+    __device__ __forceinline__ float most() const {  // NaN is passed over
+      if constexpr (sizeof(T) == 4) {
+        float m = fmaxf((*this)[0], (*this)[1]);
 #pragma unroll
-    for (int v = 0; v < TILE / VEC; ++v) {
-      const int i = index(x, v);
-      if constexpr (VEC == 1) {
-        l[v] = full || i < a.vocab ? (float)row[i] : -INFINITY;
-      } else if (full || i + VEC <= a.vocab) {
-        if constexpr (sizeof(T) == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(row + i);
-          l[v * 4] = y.x;
-          l[v * 4 + 1] = y.y;
-          l[v * 4 + 2] = y.z;
-          l[v * 4 + 3] = y.w;
-        } else {
-          const uint2 y = *reinterpret_cast<const uint2*>(row + i);
-          l[v * 4] = __uint_as_float(y.x << 16);
-          l[v * 4 + 1] = __uint_as_float(y.x & 0xffff0000u);
-          l[v * 4 + 2] = __uint_as_float(y.y << 16);
-          l[v * 4 + 3] = __uint_as_float(y.y & 0xffff0000u);
-        }
+        for (int v = 2; v < TILE; ++v) m = fmaxf(m, (*this)[v]);
+        return m;
       } else {
+        auto two = [&](int i) { return *reinterpret_cast<const __nv_bfloat162*>(&w[i]); };
+        __nv_bfloat162 m = __hmax2(two(0), two(1));
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) l[v * VEC + e] = i + e < a.vocab ? (float)row[i + e] : -INFINITY;
+        for (int i = 2; i < TILE / 2; ++i) m = __hmax2(m, two(i));
+        return fmaxf(__low2float(m), __high2float(m));
       }
     }
   };
-  const int tiles = (a.vocab + FT * TILE - 1) / (FT * TILE);
-  float l[TILE], next[TILE];
+  auto index = [&](int x, int v) { return (((x * C + rank) * VECS + v) * FT + tid) * VEC - head; };
+  auto load = [&](int x, Tile& l) {
+    // all of the tile is within the row
+    const bool inside = (x * C + rank > 0 || head == 0) && (x * C + rank + 1) * (FT * TILE) - head <= a.vocab;
+#pragma unroll
+    for (int v = 0; v < VECS; ++v) {
+      const int i = index(x, v);
+      if (inside || (i >= 0 && i + VEC <= a.vocab)) {
+        const uint4 y = *reinterpret_cast<const uint4*>(row + i);
+        l.w[v * 4] = y.x;
+        l.w[v * 4 + 1] = y.y;
+        l.w[v * 4 + 2] = y.z;
+        l.w[v * 4 + 3] = y.w;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if constexpr (sizeof(T) == 4) {
+            l.w[v * 4 + q] = __float_as_uint(i + q >= 0 && i + q < a.vocab ? (float)row[i + q] : -INFINITY);
+          } else {
+            const int j = i + 2 * q;
+            const float lo = j >= 0 && j < a.vocab ? (float)row[j] : -INFINITY;
+            const float hi = j + 1 >= 0 && j + 1 < a.vocab ? (float)row[j + 1] : -INFINITY;
+            l.w[v * 4 + q] = __float_as_uint(lo) >> 16 | __float_as_uint(hi);
+          }
+        }
+      }
+    }
+  };
+  const int tiles = ((a.vocab + head + FT * TILE - 1) / (FT * TILE) - rank + C - 1) / C;   // this block's
+  Tile l, next;
   load(0, l);
   if (tiles > 1) load(1, next);
   sh.bins[tid] = 0;
@@ -1617,12 +1672,9 @@ __global__ void __launch_bounds__(FT, 2) sample_stream_kernel(const SampleArgs a
     if (sh.best < FT) bound = max(bound, scale > 0.f ? order_key(ltop - (sh.best + 1.01f) / scale) : gmin);
   }
   // ---- the tiles
-  auto look = [&](int x, const float (&l)[TILE]) {
+  auto look = [&](int x, const Tile& l) {
     const float lbound = key_logit(bound);
-    float most = fmaxf(l[0], l[1]);                  // NaN is passed over
-#pragma unroll
-    for (int v = 2; v < TILE; ++v) most = fmaxf(most, l[v]);
-    if (!(most >= lbound)) return;
+    if (!(l.most() >= lbound)) return;
 #pragma unroll
     for (int v = 0; v < TILE; ++v)
       if (l[v] >= lbound) {
@@ -1630,6 +1682,7 @@ __global__ void __launch_bounds__(FT, 2) sample_stream_kernel(const SampleArgs a
         if (at < LIST) sh.list[at] = ((ull)order_key(l[v]) << 32) | (unsigned)~(index(x, v / VEC) + v % VEC);
       }
   };
+  bool fits = true;
   for (int x = 0; x < tiles; x += 2) {
     look(x, l);
     if (x + 2 < tiles) load(x + 2, l);
@@ -1639,91 +1692,119 @@ __global__ void __launch_bounds__(FT, 2) sample_stream_kernel(const SampleArgs a
     if (x % 4 == 2 || x + 2 >= tiles) {
       __syncthreads();
       const unsigned n = sh.local_n;
-      if (n > LIST) {
-        if (tid == 0) a.token[r] = kNotDone;
-        return;
-      }
       __syncthreads();                               // n has been read
+      fits = n <= LIST;
+      if (!fits) break;
       if (n > LIST / 2) bound = max(bound, tighten(sh, k));
     }
   }
-  if (sh.local_n == 0) {
+  unsigned n = fits ? sh.local_n : 0;
+  if (C > 1) {
+    // the row's first block gets the others' lists, in parts of its own
+    if (n > SEG) {
+      __syncthreads();                               // n has been read
+      tighten(sh, k);
+      n = sh.local_n;
+      fits = n <= SEG;
+    }
+    cluster_sync();                                  // it needs no more of the list than its part
+    if (fits && rank > 0)
+      for (int i = tid; i < (int)n; i += FT) in_block(&sh.list[0], 0)[rank * SEG + i] = sh.list[i];
+    if (tid == 0) *in_block(&sh.seg_n[rank], 0) = fits ? n : LIST + 1;
+    cluster_sync();
+    if (rank > 0) return;
+    n = 0;
+    for (int c = 0; c < C; ++c) n += sh.seg_n[c];
+    fits = n <= LIST;
+  } else if (tid == 0) {
+    sh.seg_n[0] = n;
+  }
+  if (!fits || n == 0) {
     if (tid == 0) {
-      a.token[r] = -1;
-      if (a.logprob) a.logprob[r] = -INFINITY;
+      a.token[r] = fits ? -1 : kNotDone;
+      if (fits && a.logprob) a.logprob[r] = -INFINITY;
     }
     return;
   }
-  if (tid == 0) sh.seg_n[0] = sh.local_n;
   sh.bins[tid] = 0;
   __syncthreads();
-  draw_from_few(a, sh, r, 1, k, p, least, u, t);
+  draw_from_few(a, sh, r, C, k, p, least, u, t);
 }
 
-template <typename T>
-int launch_cluster(const SampleArgs& a, int C, int Q, int rest, cudaStream_t s) {
-  constexpr int most = (int)sizeof(Cluster) + MAX_Q * FT * 16;
-  static_assert(most <= 227 * 1024, "shared memory");
-  static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = set_smem_once(smem_set, sample_cluster_kernel<T>, most);
-  if (e != cudaSuccess) return e;
+// A launch of `grid` blocks, `cluster` at a time, that may begin before its stream's
+// last kernel has ended
+struct Launch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)C;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)a.rows * (unsigned)C);
-  cfg.blockDim = dim3(FT);
-  cfg.dynamicSmemBytes = sizeof(Cluster) + (size_t)Q * FT * 16;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = C > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, sample_cluster_kernel<T>, a, C, Q, rest);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-template <class Kernel>
-int launch(Kernel kernel, dim3 grid, int threads, const SampleArgs& a, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
+  Launch(long long grid, int threads, int cluster, size_t smem, cudaStream_t s) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+  }
+  template <class... Params, class... Args>
+  int operator()(void (*kernel)(Params...), Args... args) {
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
+};
 
 template <typename T>
 int launch_any(const SampleArgs& a, int num_sms, cudaStream_t s) {
   const long long most = (long long)MAX_C * FT * 4 * MAX_Q;
   if (a.vocab > most || a.rows > 0x7fffffff / MAX_C)
-    return launch(sample_kernel<T>, dim3((unsigned)a.rows), THREADS, a, s);
+    return Launch(a.rows, THREADS, 1, 0, s)(sample_kernel<T>, a);
   // Blocks of a row: more shorten its passes, and lengthen the exchanges.  Quads a
   // thread 2, 4, 8, 16: one row of 32000 8.4, 8.4, 8.7, 9.9 us, 64 rows with settings
   // of their own 41, 37, 49, 53 us.
   int C = 1;
   while (C < MAX_C && C * FT * SAMPLE_Q * 4 < a.vocab) C <<= 1;
   const int Q = (a.vocab + C * FT * 4 - 1) / (C * FT * 4);
-  // Enough rows to fill the GPU a block each, and long enough for the second launch.
-  // Measured (bf16, top-k 50), with it and by the cluster kernel alone: 152 x 16384
-  // 11.9 and 10.0 us, 304 x 16384 13.2 and 19.2, 152 x 32000 15.6 and 28.0,
-  // 152 x 131071 35.8 and 60.4, 384 x 131071 92.1 and 150.9.  Where every row is the
-  // other kernel's it costs about 1 us.
-  const bool stream = a.rows >= num_sms && (long long)a.rows * a.vocab >= (long long)num_sms * STREAM_VOCAB;
-  if (stream) {
-    const bool vec = reinterpret_cast<uintptr_t>(a.logits) % (4 * sizeof(T)) == 0 && a.ld % 4 == 0;
-    const int e = vec ? launch(sample_stream_kernel<T, 4>, dim3((unsigned)a.rows), FT, a, s)
-                      : launch(sample_stream_kernel<T, 1>, dim3((unsigned)a.rows), FT, a, s);
-    if (e != cudaSuccess) return e;
+  constexpr int most_smem = (int)sizeof(Cluster) + MAX_Q * FT * 16;
+  static_assert(most_smem <= 227 * 1024, "shared memory");
+  static std::atomic<uint64_t> smem_set{0};
+  cudaError_t e = set_smem_once(smem_set, sample_cluster_kernel<T>, most_smem);
+  if (e != cudaSuccess) return e;
+  const size_t smem = sizeof(Cluster) + (size_t)Q * FT * 16;
+  // More rows than the GPU holds clusters at once: what can stream does, a row a block
+  // or a few.  Measured (bf16, top-k 50), by the cluster kernel alone and with it:
+  // 140 x 16384 10.8 and 10.9 us, 170 x 16384 17.6 and 11.9, 72 x 32000 11.5 and 12.0,
+  // 80 x 32000 19.4 and 12.9, 36 x 131071 15.0 and 16.0, 40 x 131071 25.2 and 17.0.  A
+  // row of one block is quicker there: 512 x 8192 16.7 and 20.5 us.  Where every row is
+  // the cluster kernel's the other costs 3 us (152 x 32000, no cut, 28.9 and 31.5).
+  int stream = 0;
+  if (C > 1) {
+    static std::atomic<int> held[MAX_C + 1][MAX_Q + 1];   // the devices of a process are alike
+    int n = held[C][Q].load(std::memory_order_relaxed);
+    if (n == 0) {
+      Launch one(C, FT, C, smem, s);
+      e = cudaOccupancyMaxActiveClusters(&n, sample_cluster_kernel<T>, &one.cfg);
+      if (e != cudaSuccess) return e;
+      held[C][Q].store(n, std::memory_order_relaxed);
+    }
+    stream = a.rows > n;
   }
-  return launch_cluster<T>(a, C, Q, stream, s);
+  int clusters = a.rows;
+  if (stream) {
+    // Blocks of a row: while two an SM hold them all.  1, 2 and 4: 152 x 16384 11.3,
+    // 12.2, 22 us, 152 x 131071 31.8, 24.6, 34 us, 48 x 131071 23.7, 21.1, 18.4 us.
+    int S = 1;
+    while (S < 4 && a.rows * S <= num_sms && a.vocab >= 2 * S * STREAM_PART) S <<= 1;
+    e = (cudaError_t)Launch((long long)a.rows * S, FT, S, 0, s)(sample_stream_kernel<T>, a, S);
+    if (e != cudaSuccess) return e;
+    // Clusters for the rows that are left: few are soon done where there are none, many
+    // share them evenly.  4, 12 and 24 blocks an SM: 384 x 131071 (f32, top-k 50) 63,
+    // 68 and 74 us, all of them flat top-p rows 755, 632 and 630 us.
+    clusters = std::min(a.rows, 12 * num_sms / C);
+  }
+  return Launch((long long)clusters * C, FT, C, smem, s)(sample_cluster_kernel<T>, a, C, Q, stream);
 }
 
 }  // namespace

@@ -257,6 +257,42 @@ def test_many_long_rows(cuda_lib, dtype, vocab, ld):
     assert (none == -1).all() and (lp == -math.inf).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,vocab", [(41, 131071), (76, 65536), (100, 40001), (152, 32000), (17, 260001), (304, 32001)])
+@pytest.mark.parametrize("first", [0, 1, 3])
+def test_rows_over_several_blocks(cuda_lib, dtype, rows, vocab, first):
+    # fewer long rows: each is streamed by one, two or four blocks; rows begin at any
+    # element, with what must not be read on either side
+    gen = torch.Generator().manual_seed(vocab + first)
+    l = 2.5 * torch.randn(rows, vocab, generator=gen)
+    l[1] = l[1].sort().values
+    l[2] = 0.5
+    l[3, :vocab - 7] = -math.inf
+    l[4] = -math.inf
+    l[5] = l[5].sort(descending=True).values
+    l[6, vocab // 2:] = math.nan
+    l[7, 8192 * 3:] += 40.0                          # a later block's part has all
+    l[8] = -math.inf
+    l[8, 0] = l[8, vocab - 1] = -3.0
+    l[9, 20:] = -math.inf
+    l = l.to(dtype)
+    wide = torch.full((rows, vocab + 6), math.inf, dtype=dtype)
+    wide[:, first:first + vocab] = l
+    x = wide.cuda()[:, first:first + vocab]
+    u = np.random.default_rng(vocab).random(rows).astype(np.float32)
+    some = (l > -math.inf).any(1).numpy()
+    clean = torch.where(l.isnan(), -math.inf, l.float()).to(dtype)
+    for k in (1, 7, 64):
+        t, kk, p, m = torch.full((rows,), 0.8), torch.full((rows,), k), torch.full((rows,), 0.95), torch.full((rows,), 0.01)
+        token = torch.full((rows,), -7, dtype=torch.int32, device="cuda")
+        logprob = torch.full((rows,), math.nan, device="cuda")
+        g.sample(x, torch.as_tensor(u).cuda(), token, logprob, temperature=t.cuda(), top_k=kk.int().cuda(), top_p=p.cuda(),
+                 min_p=m.cuda())
+        check_status()
+        assert np.array_equal(token.cpu().numpy(), np.where(some, _rule(clean, u, t, kk, p, m), -1))
+        assert (logprob.cpu().numpy()[some] <= 0).all() and (logprob.cpu().numpy()[~some] == -math.inf).all()
+
+
 @pytest.mark.parametrize("vocab", [400003, 1 << 20])
 def test_largest_vocabularies(cuda_lib, vocab):
     # longer than a cluster's shared memory holds
