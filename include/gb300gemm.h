@@ -332,10 +332,11 @@ typedef enum {
  * but the struct itself is DEVICE memory owned by the caller; the struct is
  * read during the call only.  The fast kernels need dim 64 or 128, page_tokens
  * 16, 32, 64 or 128 and k, v and the strides multiples of 16 bytes; others run a
- * generic kernel (dim at most 512).  A cache whose codes, scales or table
- * disagree with the call (a page number outside 0 .. pages-1, a token past the
- * table's columns) is not followed out of bounds: the kernel skips what it
- * cannot place, and gemm_device_status() reports GEMM_ERR_INVALID_ARG.
+ * generic kernel (dim at most 512), and so does gemm_kv_attention with more than
+ * 8192 sequences.  A cache whose codes, scales or table disagree with the call (a
+ * page number outside 0 .. pages-1, a token past the table's columns) is not
+ * followed out of bounds: the kernel skips what it cannot place, and
+ * gemm_device_status() reports GEMM_ERR_INVALID_ARG.
  */
 typedef struct {
   void* k;

@@ -21,7 +21,7 @@
 // Measured on one GB300, GPU time: one row of 32000 with top-k 50, top-p and min-p
 // 9 us; 64 rows of 32000 bf16: the same settings 11 us, top-k 1000 with top-p 25 us,
 // top-p alone 21 to 35 us (flat rows need the search), no cut 13 us; 384 rows of
-// 131071 fp32 (201 MB): 68 us, 3.0 TB/s, against 141 us by the cluster kernel.
+// 131071 fp32 (201 MB): 61 us, 3.3 TB/s, against 141 us by the cluster kernel.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -322,6 +322,7 @@ constexpr int SMALL_K = 64;                   // largest top_k whose ranks fit t
 constexpr int SEG = LIST / MAX_C;             // a block's part of the list then
 constexpr int TOP_K_LIST = 1024;              // ranks that the first block can draw from: two a thread
 constexpr int SAMPLE_Q = 4;                   // quads of a thread before a row takes more blocks
+constexpr int STREAM_LONG = 160;              // length from which a list's own bound is taken, see its use
 constexpr int STREAM_PART = 15000;            // logits of a row that are worth a block, see its use
 constexpr float ZERO_Z = 28.f;                // expf(-28) < 2^-40: no mass
 
@@ -1503,12 +1504,17 @@ __global__ void __launch_bounds__(FT, 2) sample_cluster_kernel(const SampleArgs 
 // ------------------------------------------------------------------ a row a block
 // Many rows at once, for those whose draw is among the first SMALL_K ranks (or the
 // first alone): a block, or C of them for every C-th tile, streams through a row and
-// lists what may be among them.  The k-th largest of the first tile's groups bounds the
+// lists what may be among them.  The k-th largest of its first logits' groups bounds the
 // k-th rank of the row from below, so a thread's later logits are mostly a maximum and
 // one comparison a tile; every fourth tile a long list's own k-th rank is a better
 // bound.  A row of which four tiles hold more than the list (ascending logits, say) is
-// left to the other kernel.  The next tiles' loads are in flight meanwhile, as they
-// came: widened on arrival, bf16 rows wait for them (304 x 131071 44 us, now 34 us).
+// left to the other kernel.
+//
+// What bounds it: latency and issue; two blocks an SM (64 registers a thread) each wait
+// for their loads, the bound and the draw in turn.  384 x 131071, top-k 50: fp32 61 us
+// (201 MB), bf16 46 us (101 MB), of which the second launch takes 3 to 6 us; the 80 rows
+// that 304 blocks leave take half as long as the 304.  The next tiles' loads stay as
+// they came until their turn: widened on arrival, bf16 rows wait for them (62 us).
 constexpr int TILE_BYTES = 64;                // of a thread, in 16-byte vectors
 
 // The list's bound for the k-th rank: a histogram of its keys; drops what is below it.
@@ -1637,10 +1643,14 @@ __global__ void __launch_bounds__(FT, 2) sample_stream_kernel(const SampleArgs a
   sh.bins[tid] = 0;
   if (tid == 0) sh.local_n = 0;
 
-  // ---- the first tile's bound
+  // ---- the first logits' bound
   unsigned group[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < TILE; ++i) group[i % 4] = max(group[i % 4], order_key(l[i]));
+  if (TILE == 16 && tiles > 1) {                     // 32 logits a thread for either type
+#pragma unroll
+    for (int i = 0; i < TILE; ++i) group[i % 4] = max(group[i % 4], order_key(next[i]));
+  }
   unsigned top = max(max(group[0], group[1]), max(group[2], group[3])), gmin = 0xffffffffu;
 #pragma unroll
   for (int q = 0; q < 4; ++q) gmin = min(gmin, group[q] > kKeyNegInf ? group[q] : 0xffffffffu);
@@ -1675,12 +1685,17 @@ __global__ void __launch_bounds__(FT, 2) sample_stream_kernel(const SampleArgs a
   auto look = [&](int x, const Tile& l) {
     const float lbound = key_logit(bound);
     if (!(l.most() >= lbound)) return;
+    // a warp is here almost always before the bound is tight, seldom after; one loop
+    // over what was found, not a branch a logit: 384 x 131071 bf16 62 us, now 46 us
+    unsigned found = 0;
 #pragma unroll
-    for (int v = 0; v < TILE; ++v)
-      if (l[v] >= lbound) {
-        const unsigned at = atomicAdd(&sh.local_n, 1u);
-        if (at < LIST) sh.list[at] = ((ull)order_key(l[v]) << 32) | (unsigned)~(index(x, v / VEC) + v % VEC);
-      }
+    for (int v = 0; v < TILE; ++v) found |= l[v] >= lbound ? 1u << v : 0u;
+#pragma unroll 1
+    for (; found; found &= found - 1) {
+      const int v = __ffs(found) - 1, i = index(x, v / VEC) + v % VEC;
+      const unsigned at = atomicAdd(&sh.local_n, 1u);
+      if (at < LIST) sh.list[at] = ((ull)order_key((float)row[i]) << 32) | (unsigned)~i;
+    }
   };
   bool fits = true;
   for (int x = 0; x < tiles; x += 2) {
@@ -1695,7 +1710,8 @@ __global__ void __launch_bounds__(FT, 2) sample_stream_kernel(const SampleArgs a
       __syncthreads();                               // n has been read
       fits = n <= LIST;
       if (!fits) break;
-      if (n > LIST / 2) bound = max(bound, tighten(sh, k));
+      // from 1024, 512, 256, 160 on: 200 x 260000 bf16 58, 55, 52, 51 us
+      if (n > STREAM_LONG) bound = max(bound, tighten(sh, k));
     }
   }
   unsigned n = fits ? sh.local_n : 0;
@@ -1776,7 +1792,7 @@ int launch_any(const SampleArgs& a, int num_sms, cudaStream_t s) {
   // More rows than the GPU holds clusters at once: what can stream does, a row a block
   // or a few.  Measured (bf16, top-k 50), by the cluster kernel alone and with it:
   // 140 x 16384 10.8 and 10.9 us, 170 x 16384 17.6 and 11.9, 72 x 32000 11.5 and 12.0,
-  // 80 x 32000 19.4 and 12.9, 36 x 131071 15.0 and 16.0, 40 x 131071 25.2 and 17.0.  A
+  // 80 x 32000 19.4 and 12.8, 36 x 131071 15.0 and 16.0, 40 x 131071 25.2 and 17.0.  A
   // row of one block is quicker there: 512 x 8192 16.7 and 20.5 us.  Where every row is
   // the cluster kernel's the other costs 3 us (152 x 32000, no cut, 28.9 and 31.5).
   int stream = 0;
