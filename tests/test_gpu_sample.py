@@ -293,6 +293,35 @@ def test_rows_over_several_blocks(cuda_lib, dtype, rows, vocab, first):
         assert (logprob.cpu().numpy()[some] <= 0).all() and (logprob.cpu().numpy()[~some] == -math.inf).all()
 
 
+def test_offsets_past_32_bits(cuda_lib):
+    # rows that begin 2^31 elements into a tensor and later
+    rows, vocab, ld = 17500, 1000, 131071
+    wide = torch.zeros(rows * ld, dtype=torch.bfloat16, device="cuda")
+    x = wide.as_strided((rows, vocab), (ld, 1))
+    gen = torch.Generator().manual_seed(1)
+    last, u = make(40, vocab, torch.bfloat16, 5)
+    x[-40:] = last.cuda()
+    for k in (1, 20, 0):
+        token = torch.full((rows,), -7, dtype=torch.int32, device="cuda")
+        kk = torch.full((rows,), k, dtype=torch.int32)
+        p = torch.full((rows,), 0.9)
+        uu = torch.rand(rows, generator=gen)
+        uu[-40:] = torch.as_tensor(u)
+        g.sample(x, uu.cuda(), token, top_k=kk.cuda(), top_p=p.cuda())
+        check_status()
+        want = _rule(last, u, torch.ones(40), kk[-40:], p[-40:], torch.zeros(40))
+        assert np.array_equal(token[-40:].cpu().numpy(), want)
+    del wide, x
+    full = torch.zeros(8300, 1 << 18, dtype=torch.bfloat16, device="cuda")       # 2^31, in rows that stream
+    at = torch.randint(1 << 18, (8300,), generator=gen).cuda()
+    full.scatter_(1, at[:, None], 5.0)
+    kk = torch.full((8300,), 1, dtype=torch.int32)
+    token = g.sample(full, torch.rand(8300, generator=gen).cuda(), torch.full((8300,), -7, dtype=torch.int32, device="cuda"),
+                     top_k=kk.cuda())
+    check_status()
+    assert torch.equal(token.long(), at)
+
+
 @pytest.mark.parametrize("vocab", [400003, 1 << 20])
 def test_largest_vocabularies(cuda_lib, vocab):
     # longer than a cluster's shared memory holds
