@@ -237,10 +237,10 @@ struct Seq {
 struct Plan {
   const KvAttnArgs* a;
   int group, rt;        // query heads of a head; rows of a tile
-  int tw, tl;           // warps of a group; this warp's place in it
+  int tw_log, tl;       // log2 of a group's warps; this warp's place in it
   __device__ __forceinline__ Seq seq(int len, int first, int n) const {
     const int tiles = (n * group + rt - 1) / rt;
-    return Seq{len, first, n, max(1, (len + SLAB - 1) / SLAB), tiles, (tiles + tw - 1) / tw};
+    return Seq{len, first, n, max(1, (len + SLAB - 1) / SLAB), tiles, (tiles + (1 << tw_log) - 1) >> tw_log};
   }
   __device__ __forceinline__ Seq seq(int b) const {
     // every load before the first check, which waits for it
@@ -281,7 +281,7 @@ struct Walk {
   Seq q;
   __device__ __forceinline__ void split(const Plan& p) {
     h = q.passes == 1 ? idx : idx / q.passes;
-    t = (idx - h * q.passes) * p.tw + p.tl;
+    t = ((idx - h * q.passes) << p.tw_log) + p.tl;
     vis = p.visible(q, t);
   }
   __device__ __forceinline__ void next(const Plan& p) {
@@ -386,9 +386,12 @@ __global__ void __launch_bounds__(NW * 32, 1)
   uint8_t* ring_ptr = base_ptr + warp * RING;
   const uint32_t ring = smem_u32(ring_ptr);
   // groups of tw warps walk the same slabs, each for its own tile of rows: what one
-  // fetches, the others find in L2
-  const int tl = warp & (tw - 1), worker = warp / tw, workers = NW / tw;
-  const Plan plan{&a, group, RT, tw, tl};
+  // fetches, the others find in L2.  All are powers of two: a division of 64 bits in the
+  // plan would cost a small call more than a slab.
+  static_assert((NW & (NW - 1)) == 0, "a power of two");
+  const int tw_log = 31 - __clz(tw), tl = warp & (tw - 1), worker = warp >> tw_log, workers = NW >> tw_log;
+  const int workers_log = 31 - __clz(workers);
+  const Plan plan{&a, group, RT, tw_log, tl};
   const int npg = a.c.P < SLAB ? 2 : 1;           // pages of a slab
   const int p_shift = 31 - __clz(a.c.P);          // P is a power of two
 
@@ -461,7 +464,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   // heads (63 slabs) 18.3 and 14.0, 1 x 4000 28.4 and 12.4.
   const u64 share = quotient(T + gridDim.x * workers - 1, gridDim.x * workers);
   const int blocks = min((int)gridDim.x, I);
-  const bool by_item = I > 0 && ((u64)((I + blocks - 1) / blocks) * longest + workers - 1) / workers <= share + WHOLE_EXTRA;
+  const bool by_item = I > 0 && (((u64)((I + blocks - 1) / blocks) * longest + workers - 1) >> workers_log) <= share + WHOLE_EXTRA;
   const u64 G = by_item ? (u64)blocks : T < gridDim.x ? T : gridDim.x;   // every block up to G has a unit
   const u64 cta = blockIdx.x;
   if (cta >= G) return;
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   const u64 A = by_item ? item_unit(quotient(cta * I, G)) : quotient(cta * T, G);
   const u64 B = by_item ? item_unit(quotient((cta + 1) * I, G)) : quotient((cta + 1) * T, G);
   const u64 me = cta * NW + warp;
-  const u64 u0 = A + worker * (B - A) / workers, u1 = A + (worker + 1) * (B - A) / workers;
+  const u64 u0 = A + (worker * (B - A) >> workers_log), u1 = A + ((worker + 1) * (B - A) >> workers_log);
   Walk cw;
   if (u0 < u1) {
     cw.b = record([&](const SeqRec& x) { return x.at <= u0; });
@@ -925,7 +928,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const unsigned below = valid & ((1u << lane) - 1u);
     const int prev = below ? 31 - __clz(below) : lane;
     const u64 before = __shfl_sync(0xffffffffu, unit, prev);
-    const int tile = lane / (2 * workers), tile_before = prev / (2 * workers);
+    const int tile = lane >> (workers_log + 1), tile_before = prev >> (workers_log + 1);
     const bool starts = unit != ~0ull && (below == 0 || before != unit || tile != tile_before);
     const unsigned firsts = __ballot_sync(0xffffffffu, starts);
     if (starts) {
