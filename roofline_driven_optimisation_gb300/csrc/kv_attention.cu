@@ -23,7 +23,7 @@
 //     parts in block order.
 //
 // Measured on one GB300 (6.79 TB/s copied), GPU time:
-//   128 sequences of about 8192, 32 over 8 heads of 128, E4M3   2152 MB  347 us  6.2 TB/s
+//   128 sequences of about 8192, 32 over 8 heads of 128, E4M3   2152 MB  351 us  6.1 TB/s
 //   16 of about 4096, 32 heads of 128, INT8                      537 MB   94 us  5.7 TB/s
 //   1 of 131071, 32 over 8 heads of 128, E4M3                    269 MB   55 us  4.9 TB/s
 //   24 of about 1500, 5 tokens, 16 over 4 heads of 64, INT8       19 MB   27 us
@@ -386,8 +386,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
   uint8_t* ring_ptr = base_ptr + warp * RING;
   const uint32_t ring = smem_u32(ring_ptr);
   // groups of tw warps walk the same slabs, each for its own tile of rows: what one
-  // fetches, the others find in L2.  All are powers of two: a division of 64 bits in the
-  // plan would cost a small call more than a slab.
+  // fetches, the others find in L2.  All are powers of two: the plan's divisions by them
+  // in 64 bits took 0.4 us of a call.
   static_assert((NW & (NW - 1)) == 0, "a power of two");
   const int tw_log = 31 - __clz(tw), tl = warp & (tw - 1), worker = warp >> tw_log, workers = NW >> tw_log;
   const int workers_log = 31 - __clz(workers);
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   // Blocks take equal shares of the line, or whole items.  Whole items need no exchange
   // between blocks, which costs a call about as much time as WHOLE_EXTRA slabs a warp;
   // so they are taken unless the fullest block's warps get longer than that.  Measured,
-  // whole items and shares: 1 x 777 of 32 heads (25 slabs an item) 12.2 and 13.8 us,
+  // whole items and shares: 1 x 777 of 32 heads (25 slabs an item) 11.8 and 13.4 us,
   // 60 x 200 of 8 heads 14.6 and 17.6, 32 x 600 of 8 heads 21.9 and 24.9; 1 x 2000 of 8
   // heads (63 slabs) 18.3 and 14.0, 1 x 4000 28.4 and 12.4.
   const u64 share = quotient(T + gridDim.x * workers - 1, gridDim.x * workers);
