@@ -464,7 +464,7 @@ __device__ __forceinline__ int pad_list(Cluster& sh, int m) {
 
 // The draw where the first block's list holds every token that can be kept, the list
 // sorted by rank for both cuts, then by index for the draw.  `mass`: what top-p takes
-// its share of, 0 for the mass of the k first.
+// its share of, 0 for the mass of the k first.  Entries of 0 are no tokens.
 __device__ __forceinline__ void draw_by_sorting(const SampleArgs& a, Cluster& sh, int r, int n, int k, float p,
                                                 float least, float u, float t, ull mass) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -574,11 +574,12 @@ __device__ __forceinline__ unsigned kth_bin(const Cluster& sh, int k) {
 
 // The same without sorting, where no bin of the three histograms is crowded: the k-th
 // rank and top-p's cut by bins even in the logit, the draw by bins even in the index;
-// the tokens of the bin in question are compared with one another.  False (and the
-// list as it was, but for dropped entries of 0) if a bin is crowded.
+// the tokens of the bin in question are compared with one another.  Where a bin is
+// crowded, the cuts before it stand: what they drop is 0 in the list.
 constexpr int EDGE = 512;                            // tokens of a bin that are compared
+enum class Bins { drawn, crowded, cut_and_crowded }; // the last: top-p is in the list already
 
-__device__ __forceinline__ bool draw_by_bins(const SampleArgs& a, Cluster& sh, int r, int n, int k, float p, float least,
+__device__ __forceinline__ Bins draw_by_bins(const SampleArgs& a, Cluster& sh, int r, int n, int k, float p, float least,
                                              float u, float t, ull mass) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   // the tokens of the bin in question and their masses lie in the unused parts of the
@@ -636,7 +637,7 @@ __device__ __forceinline__ bool draw_by_bins(const SampleArgs& a, Cluster& sh, i
     if (tid == 0) sh.local_n = 0;
     __syncthreads();
     const int best = (int)sh.best, above = (int)sh.n_above;
-    if (sh.bins[best] > EDGE) return false;
+    if (sh.bins[best] > EDGE) return Bins::crowded;
     each([&](ull x, int i) {
       const int b = bin(x);
       if (b == best) edge[atomicAdd(&sh.local_n, 1u)] = x;
@@ -686,7 +687,7 @@ __device__ __forceinline__ bool draw_by_bins(const SampleArgs& a, Cluster& sh, i
     const int best = (int)sh.best;
     if (tid == best) sh.m_above = before;
     __syncthreads();
-    if (sh.bins[best] > EDGE) return false;
+    if (sh.bins[best] > EDGE) return Bins::crowded;
     each([&](ull x, int i) {
       const int b = bin(x);
       if (b == best) {
@@ -744,7 +745,7 @@ __device__ __forceinline__ bool draw_by_bins(const SampleArgs& a, Cluster& sh, i
   }
   __syncthreads();
   const int best = (int)sh.best;
-  if (sh.bins[best] > EDGE) return false;
+  if (sh.bins[best] > EDGE) return Bins::cut_and_crowded;
   each([&](ull x, int) {
     if (place(x) != best) return;
     const ull m = kept(x);
@@ -766,14 +767,16 @@ __device__ __forceinline__ bool draw_by_bins(const SampleArgs& a, Cluster& sh, i
         a.logprob[r] = logit_z(row, key_logit((unsigned)(x >> 32))) - logf(__ull2float_rn(total) * 0x1p-40f);
     }
   }
-  return true;
+  return Bins::drawn;
 }
 
 __device__ __forceinline__ void draw_from_list(const SampleArgs& a, Cluster& sh, int r, int n, int k, float p, float least,
                                                float u, float t, ull mass) {
-  if (draw_by_bins(a, sh, r, n, k, p, least, u, t, mass)) return;
+  const Bins done = draw_by_bins(a, sh, r, n, k, p, least, u, t, mass);
+  if (done == Bins::drawn) return;
   __syncthreads();
-  draw_by_sorting(a, sh, r, n, k, p, least, u, t, mass);
+  // top-p's share is of the tokens before it cut: it must not cut again
+  draw_by_sorting(a, sh, r, n, k, done == Bins::cut_and_crowded ? 1.f : p, least, u, t, mass);
 }
 
 // The same for k up to SMALL_K, with the candidates in the list's C parts: ranks by

@@ -1,0 +1,45 @@
+"""gemm_sample_* where a cut, a bound or a list is at its limit: held, token for token,
+to the rule written out in torch with the same whole-number masses."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_sample import _rule, call
+
+pytestmark = pytest.mark.gpu
+
+
+def _logprob(l, token, temperature, top_k, top_p):
+    """The token's log-probability among the kept, from the rule in 64 bits."""
+    out = []
+    for r, x in enumerate(l.double().numpy()):
+        z = (x - x.max()) / float(temperature[r])
+        order = np.argsort(-x, kind="stable")
+        w = np.exp(z[order])
+        if top_k[r] > 0:
+            w[int(top_k[r]):] = 0
+        before = np.cumsum(w) - w
+        keep = before < float(top_p[r]) * w.sum()
+        keep[0] = True
+        out.append(z[token[r]] - math.log(w[keep].sum()))
+    return np.array(out)
+
+
+@pytest.mark.parametrize("rows", [6, 40])
+@pytest.mark.parametrize("vocab", [300000, 360448])
+def test_top_p_cuts_once_where_the_kept_lie_side_by_side(cuda_lib, vocab, rows):
+    # an index bin is ceil(vocab / 512) wide, so that more than 512 kept tokens fit into
+    # one: the draw then sorts a list that top-p has cut already
+    gen = torch.Generator().manual_seed(vocab)
+    l = torch.randn(rows, vocab, generator=gen)
+    width = -(-vocab // 512)
+    l[:, :width] = 10.0 + torch.rand(rows, width, generator=gen)
+    l[rows // 2:, :width] = l[rows // 2:, :width].flip(1)
+    u = ((np.arange(rows) + 0.5) / rows).astype(np.float32)
+    t, k, p = torch.ones(rows), torch.full((rows,), width + 114), torch.full((rows,), 0.97)
+    token, logprob = call(l, u, temperature=t.tolist(), top_k=k.tolist(), top_p=p.tolist())
+    assert np.array_equal(token, _rule(l, u, t, k, p, torch.zeros(rows)))
+    # the cut falls on a token of about 1/600 of the mass: one token more or less
+    assert np.abs(logprob - _logprob(l, token, t, k, p)).max() < 2.5 / 500
