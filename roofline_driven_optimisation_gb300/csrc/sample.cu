@@ -1034,7 +1034,8 @@ __device__ __forceinline__ void cluster_row(const SampleArgs& a, const int C, co
     float x = top > kKeyNegInf ? sh.group_mass[lane % FW] : 0.f;
     for (int o = FW / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (tid == 0) {
-      sh.bound_key = bound;
+      // a block without candidates (behind the row's end, or all -inf) bounds nothing
+      sh.bound_key = top > kKeyNegInf ? bound : 0u;
       sh.block_mass = x;
     }
   } else if (cuts) {
@@ -1088,7 +1089,9 @@ __device__ __forceinline__ void cluster_row(const SampleArgs& a, const int C, co
     // Measured on 64 rows of 32000 bf16, with the list and by the search: p 0.5 at
     // temperature 0.3 20 and 24 us; p 0.95 at 0.8, which the list seldom reaches, 35
     // and 31 us.
+    // Of what the blocks have published alone, so that all of them decide alike.
     float sum = 0.f;
+    bound = 0;
     for (int c = 0; c < C; ++c) {
       bound = max(bound, *in_block(&sh.bound_key, c));
       sum += *in_block(&sh.block_mass, c) * logit_weight(row, key_logit(*in_block(&sh.top, c)));

@@ -43,3 +43,23 @@ def test_top_p_cuts_once_where_the_kept_lie_side_by_side(cuda_lib, vocab, rows):
     assert np.array_equal(token, _rule(l, u, t, k, p, torch.zeros(rows)))
     # the cut falls on a token of about 1/600 of the mass: one token more or less
     assert np.abs(logprob - _logprob(l, token, t, k, p)).max() < 2.5 / 500
+
+
+@pytest.mark.parametrize("vocab", [16385, 40960, 50257, 65537, 100277])
+def test_top_p_alone_where_a_block_has_nothing(cuda_lib, vocab):
+    # rows whose last blocks begin behind the vocabulary's end, and rows of which one
+    # block's whole part is forbidden; top_p that keeps the first rank only among them
+    rows = 12
+    gen = torch.Generator().manual_seed(vocab)
+    l = 2.5 * torch.randn(rows, vocab, generator=gen)
+    l[4:8, :8192 * (vocab // 16385)] = -math.inf
+    l[8:, 8192:] = -math.inf
+    u = np.random.default_rng(vocab).random(rows).astype(np.float32)
+    t, k, m = torch.full((rows,), 0.8), torch.zeros(rows, dtype=torch.int64), torch.zeros(rows)
+    for p in (torch.tensor([0.0, -1.0, math.nan, 1e-30]), torch.tensor([0.5, 0.9, 0.999, 0.05])):
+        p = p.repeat(rows // 4)
+        for top_k in (k, k + 2 * vocab):                      # off, or all of the vocabulary
+            token, logprob = call(l, u, temperature=t.tolist(), top_k=top_k.tolist(), top_p=p.tolist())
+            assert np.array_equal(token, _rule(l, u, t, k, p, m))
+            assert np.isfinite(logprob).all() and (logprob <= 0).all()
+            assert (logprob[~(p > 1e-20).numpy()] == 0).all()      # one rank is kept
