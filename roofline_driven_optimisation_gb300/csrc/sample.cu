@@ -1389,6 +1389,9 @@ __device__ __forceinline__ void cluster_row(const SampleArgs& a, const int C, co
           }
           if (least_n == n_equal) {
             if (hi > cut.key) cut = Place{hi, 0x7fffffff};
+            // the next search sets this block's histograms to zero: not before every
+            // block has read them
+            sync_cluster(C);
             return false;
           }
           // the index of that token

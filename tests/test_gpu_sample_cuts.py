@@ -63,3 +63,27 @@ def test_top_p_alone_where_a_block_has_nothing(cuda_lib, vocab):
             assert np.array_equal(token, _rule(l, u, t, k, p, m))
             assert np.isfinite(logprob).all() and (logprob <= 0).all()
             assert (logprob[~(p > 1e-20).numpy()] == 0).all()      # one rank is kept
+
+
+@pytest.mark.parametrize("vocab", [20000, 40000, 131071])
+def test_both_cuts_where_the_lowest_logit_is_shared(cuda_lib, vocab):
+    # logits clipped from below, a top-k beyond all that is not forbidden, then top-p: the
+    # cut by count ends at the third level of keys, with every equal logit kept, and the
+    # cut by mass begins at once with the histogram that the blocks have just read
+    rows = 12
+    gen = torch.Generator().manual_seed(vocab)
+    l = torch.full((rows, vocab), -math.inf)
+    at = torch.randperm(vocab, generator=gen)
+    l[:, at[:3000]] = 1.0                                       # the lowest, 3000 times
+    # the same bin of logits, 2^20 keys and fewer above it
+    l[:, at[3000:3400]] = 1.0 + 1e-3 * torch.rand(rows, 400, generator=gen)
+    l[:, at[3400:3410]] = 2.0 + 9.0 * torch.rand(rows, 10, generator=gen)
+    u = np.random.default_rng(vocab).random(rows).astype(np.float32)
+    t, m = torch.tensor([1.0, 3.0, 30.0]).repeat(rows // 3), torch.zeros(rows)
+    for k in (3410, 4000, 9000):
+        for p in (0.2, 0.9, 0.9999):
+            kk, pp = torch.full((rows,), k), torch.full((rows,), p)
+            want = _rule(l, u, t, kk, pp, m)
+            for _ in range(4):
+                token, _ = call(l, u, temperature=t.tolist(), top_k=kk.tolist(), top_p=pp.tolist())
+                assert np.array_equal(token, want)
