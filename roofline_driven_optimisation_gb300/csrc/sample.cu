@@ -326,6 +326,14 @@ constexpr int STREAM_LONG = 160;              // length from which a list's own 
 constexpr int STREAM_PART = 15000;            // logits of a row that are worth a block, see its use
 constexpr float ZERO_Z = 28.f;                // expf(-28) < 2^-40: no mass
 
+// Bins a unit of the logit, for FT bins even in it.  No range, or an infinite one: all in
+// one bin.  Below 1.5e-36 the quotient would be infinite, and a bin's lower edge the
+// range's upper end; held to the largest number, fewer bins cover the range.
+__device__ __forceinline__ float bins_over(float range) {
+  static_assert(FT == 512, "bins");
+  return range > 0.f && range < INFINITY ? fminf(511.9f / range, FLT_MAX) : 0.f;
+}
+
 // A cut by rank: kept are larger keys, and equal ones up to index idx
 struct Place {
   uint32_t key;
@@ -607,7 +615,7 @@ __device__ __forceinline__ Bins draw_by_bins(const SampleArgs& a, Cluster& sh, i
   const unsigned top = __reduce_max_sync(0xffffffffu, sh.red[0][lane % FW]);
   lo = __reduce_min_sync(0xffffffffu, sh.red[1][lane % FW]);
   const Row row{key_logit(top), __fdiv_rn(1.f, t)};
-  const float range = row.top - key_logit(lo), scale = range > 0.f && range < INFINITY ? 511.9f / range : 0.f;
+  const float scale = bins_over(row.top - key_logit(lo));
   auto bin = [&](ull x) { return min(FT - 1, (int)((row.top - key_logit((unsigned)(x >> 32))) * scale)); };
   auto mass_at = [&](ull x) { return mass_of(logit_weight(row, key_logit((unsigned)(x >> 32)))); };
   auto add = [&](int b, ull m) {
@@ -810,8 +818,7 @@ __device__ __forceinline__ void draw_from_few(const SampleArgs& a, Cluster& sh, 
     __syncthreads();
     hi = __reduce_max_sync(0xffffffffu, sh.red[0][lane % FW]);
     lo = __reduce_min_sync(0xffffffffu, sh.red[1][lane % FW]);
-    const float ltop = key_logit(hi), range = ltop - key_logit(lo);
-    const float scale = range > 0.f && range < INFINITY ? 511.9f / range : 0.f;
+    const float ltop = key_logit(hi), scale = bins_over(ltop - key_logit(lo));
     auto bin = [&](ull x) { return min(FT - 1, (int)((ltop - key_logit((unsigned)(x >> 32))) * scale)); };
     for (int i = tid; i < n; i += FT) atomicAdd(&sh.bins[bin(list[i])], 1u);
     __syncthreads();
@@ -990,9 +997,7 @@ __device__ __forceinline__ void cluster_row(const SampleArgs& a, const int C, co
         top <= kKeyNegInf ? 0xffffffffu : ltop == INFINITY ? top : max(kKeyNegInf + 1, order_key(ltop - ZERO_Z * t));
     bound = floor_key;
     if (top > kKeyNegInf) {
-      // bins even in the logit; an infinite range falls into one bin
-      const float range = ltop - key_logit(gmin);
-      const float scale = range > 0.f && range < INFINITY ? 511.9f / range : 0.f;
+      const float scale = bins_over(ltop - key_logit(gmin));
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         if (group[q] >= floor_key)
@@ -1203,8 +1208,7 @@ __device__ __forceinline__ void cluster_row(const SampleArgs& a, const int C, co
     for (int c = 0; c < C; ++c) low = min(low, *in_block(&sh.low, c));
     // The last place kept by count (the first k) or by mass (less than p of all before)
     auto search = [&](bool by_count) -> bool {
-      const float range = fminf(ZERO_Z * t, row.top - key_logit(low));
-      const float scale = range > 0.f ? 511.9f / range : 0.f;
+      const float scale = bins_over(fminf(ZERO_Z * t, row.top - key_logit(low)));
       auto first_bin = [&](unsigned key) { return min(FT - 1, (int)((row.top - key_logit(key)) * scale)); };
       unsigned n_above = 0, lo = 0, hi = 0;
       ull m_above = 0, bound = 0;
@@ -1547,8 +1551,7 @@ __device__ __forceinline__ unsigned tighten(Cluster& sh, int k) {
   __syncthreads();
   hi = __reduce_max_sync(0xffffffffu, sh.red[0][lane % FW]);
   lo = __reduce_min_sync(0xffffffffu, sh.red[1][lane % FW]);
-  const float ltop = key_logit(hi), range = ltop - key_logit(lo);
-  const float scale = range > 0.f && range < INFINITY ? 511.9f / range : 0.f;
+  const float ltop = key_logit(hi), scale = bins_over(ltop - key_logit(lo));
   auto bin = [&](ull x) { return min(FT - 1, (int)((ltop - key_logit((unsigned)(x >> 32))) * scale)); };
   for (int i = tid; i < n; i += FT) atomicAdd(&sh.bins[bin(sh.local[i])], 1u);
   if (tid == 0) sh.local_n = 0;
@@ -1676,8 +1679,7 @@ __global__ void __launch_bounds__(FT, 2) sample_stream_kernel(const SampleArgs a
   if (top > kKeyNegInf) {
     const float ltop = key_logit(top);
     bound = ltop == INFINITY ? top : max(bound, order_key(ltop - ZERO_Z * t));   // below: no mass
-    const float range = ltop - key_logit(gmin);
-    const float scale = range > 0.f && range < INFINITY ? 511.9f / range : 0.f;
+    const float scale = bins_over(ltop - key_logit(gmin));
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       if (group[q] >= bound) atomicAdd(&sh.bins[min(FT - 1, (int)((ltop - key_logit(group[q])) * scale))], 1u);

@@ -87,3 +87,18 @@ def test_both_cuts_where_the_lowest_logit_is_shared(cuda_lib, vocab):
             for _ in range(4):
                 token, _ = call(l, u, temperature=t.tolist(), top_k=kk.tolist(), top_p=pp.tolist())
                 assert np.array_equal(token, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,vocab", [(5, 3000), (5, 40000), (333, 40000)])
+@pytest.mark.parametrize("size", [1e-36, 3e-37, 1e-38, 1e-40])
+def test_logits_that_differ_by_next_to_nothing(cuda_lib, dtype, rows, vocab, size):
+    # 512 bins over such a range are narrower than fp32's largest number can count
+    gen = torch.Generator().manual_seed(vocab)
+    l = (size * torch.rand(rows, vocab, generator=gen)).to(dtype)
+    u = ((np.arange(rows) + 0.5) / rows).astype(np.float32)
+    t, m = torch.ones(rows), torch.zeros(rows)
+    for k, p in ((5, 1.0), (64, 0.5), (300, 0.9), (3000, 0.99), (0, 0.001)):
+        k, p = torch.full((rows,), k), torch.full((rows,), p)
+        token, _ = call(l, u, temperature=t.tolist(), top_k=k.tolist(), top_p=p.tolist())
+        assert np.array_equal(token, _rule(l, u, t, k, p, m))
