@@ -324,6 +324,8 @@ def _ld(t) -> int:
     """Leading dimension of a row-major 2-D tensor (unit stride along columns)."""
     if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
         raise ValueError("expected a 2-D row-major tensor with unit column stride")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"rows of {t.shape[1]} values lie {t.stride(0)} apart (an expanded tensor?)")
     return max(int(t.stride(0)), int(t.shape[1]), 1)
 
 
@@ -492,11 +494,15 @@ class KVCache:
         pages, heads, page_tokens, dim = k.shape
         if v.shape != k.shape or v.stride() != k.stride() or (dim > 1 and k.stride(3) != 1):
             raise ValueError("KVCache: k and v have one shape and one set of strides, with dim contiguous")
+        if page_tokens > 1 and k.stride(2) < dim:
+            raise ValueError(f"KVCache: tokens of {dim} values lie {k.stride(2)} apart (an expanded tensor?)")
         for s in (k_scale, v_scale):
             if s.dtype != torch.float32 or tuple(s.shape) != (pages, heads) or not s.is_contiguous():
                 raise TypeError("KVCache: scales are contiguous fp32 [pages][heads]")
         if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
             raise TypeError("KVCache: table is int32 [seqs][columns] with contiguous columns")
+        if table.shape[0] > 1 and table.stride(0) < table.shape[1]:
+            raise ValueError(f"KVCache: table rows of {table.shape[1]} lie {table.stride(0)} apart (an expanded tensor?)")
         if not all(t.is_cuda and t.device == k.device for t in (k, v, k_scale, v_scale, table)):
             raise ValueError("KVCache takes CUDA tensors of one device")
         self.k, self.v, self.k_scale, self.v_scale, self.table = k, v, k_scale, v_scale, table
@@ -535,7 +541,11 @@ def _heads(t, name: str, heads: int, dim: int, tokens: int) -> int:
     row, head, one = t.stride()
     if (one != 1 and dim > 1) or (head != dim and heads > 1):
         raise ValueError(f"{name}: a row's heads lie side by side")
-    return row if row > heads * dim else heads * dim
+    if row < heads * dim:
+        if tokens > 1:
+            raise ValueError(f"{name}: rows of {heads * dim} values lie {row} apart (an expanded tensor?)")
+        row = heads * dim                             # of a single row it says nothing
+    return row
 
 
 def _values(t, name: str, n: int, dtype) -> int:
