@@ -592,19 +592,35 @@ def kv_append(cache: KVCache, Q, K, V, cos, sin, base, Qout=None, start=None, ma
 
 
 # kv_attention's workspaces, one for each device and stream (the C ABI leaves them
-# to the caller): zeroed when made, ready again after every call
+# to the caller): zeroed when made, ready again after every call.  Calls that are being
+# captured into a graph never get one of these.
 _kv_workspaces: dict = {}
 
 
-def _kv_workspace(device, stream: int, size: int):
+def _kv_workspace(device, stream: int, *sizes):
+    """The workspace of one call on `stream`; sizes: the arguments of
+    gemm_kv_attention_workspace."""
+    if stream == _raw_stream(device.index):
+        return _kv_workspace_here(device, stream, *sizes)
+    # made on the stream that uses it, so that the zeros are there before the call and
+    # the old one's memory is not reused before its last call
+    with _t.cuda.stream(_t.cuda.ExternalStream(stream, device=device)):
+        return _kv_workspace_here(device, stream, *sizes)
+
+
+def _kv_workspace_here(device, stream: int, seqs: int, *sizes):
+    size = (_lib or load()).gemm_kv_attention_workspace
+    need = size(seqs, *sizes)
+    if _t.cuda.is_current_stream_capturing():
+        # The graph's own: its memory is of the graph's pool, and its counters (what lies
+        # behind the workspace of no sequences) are set to zero by every replay.
+        w = _t.empty((need,), dtype=_t.uint8, device=device)
+        w[size(0, *sizes):].zero_()
+        return w
     key = (device.index, stream)
     w = _kv_workspaces.get(key)
-    if w is None or w.numel() < size:
-        # made on the stream that uses it, so that the zeros are there before
-        # the call and the old one's memory is not reused before its last call
-        with _t.cuda.stream(_t.cuda.ExternalStream(stream, device=device)):
-            w = _t.zeros((max(size, 1 << 20),), dtype=_t.uint8, device=device)
-        _kv_workspaces[key] = w
+    if w is None or w.numel() < need:
+        w = _kv_workspaces[key] = _t.zeros((max(need, 1 << 20),), dtype=_t.uint8, device=device)
     return w
 
 
@@ -616,7 +632,9 @@ def kv_attention(cache: KVCache, Q, O, lengths, start=None, max_new: int = 1, sc
     start[b+1]-1, at most max_new (start None: one token, row b); query i of n
     sees keys j <= lengths[b] - n + i.  workspace: zeroed uint8 tensor of
     gemm_kv_attention_workspace() bytes, or None for one that this module keeps
-    for the stream.  Argument marshalling only."""
+    for the stream.  A call captured by torch.cuda.graph gets one of the graph's own,
+    zeroed by every replay; a capture that torch does not know of needs `workspace`.
+    Argument marshalling only."""
     if _t is None:
         _torch()
     D, seqs = cache.dim, cache.seqs
@@ -625,7 +643,7 @@ def kv_attention(cache: KVCache, Q, O, lengths, start=None, max_new: int = 1, sc
     st = _raw_stream(cache.index) if stream is None else stream
     lib = _lib or load()
     if workspace is None:
-        workspace = _kv_workspace(cache.device, st, lib.gemm_kv_attention_workspace(seqs, cache.heads, Hq, D, max_new))
+        workspace = _kv_workspace(cache.device, st, seqs, cache.heads, Hq, D, max_new)
     rc = lib.gemm_kv_attention(
         cache.address, tokens, Hq, Q.data_ptr(), ldq, O.data_ptr(), ldo, _values(lengths, "lengths", seqs, _i32),
         None if start is None else _values(start, "start", seqs + 1, _i32), max_new, scale, workspace.data_ptr(),

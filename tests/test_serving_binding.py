@@ -1,4 +1,6 @@
 """What the serving operators' binding makes of tensors before a call, on the CPU."""
+import contextlib
+
 import pytest
 import torch
 
@@ -53,3 +55,98 @@ def test_caches_that_overlap_are_refused():
         g.KVCache(k, k, s, s, t[:1].expand(3, 4))
     with pytest.raises(ValueError, match="CUDA"):      # nothing else is wrong with them
         g.KVCache(k, k, s, s, t)
+
+
+class Calls:
+    """Stands for the C library: workspaces of 100 bytes and one for each sequence, and
+    what each attention call was given."""
+
+    def __init__(self):
+        self.workspaces = []
+
+    def gemm_kv_attention_workspace(self, seqs, heads, Hq, dim, max_new):
+        return 100 + seqs
+
+    def gemm_kv_attention(self, *args):
+        self.workspaces.append((args[11], args[12]))
+        return 0
+
+
+class Cache:
+    def __init__(self, seqs):
+        self.heads, self.dim, self.seqs, self.address, self.index = 1, 8, seqs, 0, 0
+        self.device = torch.device("cuda", 0)
+
+
+class Torch:
+    """Stands for torch: CPU tensors, and a stream that may be capturing."""
+    uint8 = torch.uint8
+
+    def __init__(self):
+        self.capturing, self.made = False, []
+        self.cuda = self
+
+    def is_current_stream_capturing(self):
+        return self.capturing
+
+    def ExternalStream(self, stream, device):
+        return stream
+
+    def stream(self, stream):
+        return contextlib.nullcontext()
+
+    def _make(self, fill, shape, dtype, device):
+        self.made.append(torch.full(shape, fill, dtype=dtype))
+        return self.made[-1]
+
+    def empty(self, shape, dtype, device):
+        return self._make(7, shape, dtype, device)
+
+    def zeros(self, shape, dtype, device):
+        return self._make(0, shape, dtype, device)
+
+
+@pytest.fixture
+def stubs(monkeypatch):
+    g._torch()
+    calls, fake = Calls(), Torch()
+    monkeypatch.setattr(g, "_lib", calls)
+    monkeypatch.setattr(g, "_t", fake)
+    monkeypatch.setattr(g, "_raw_stream", lambda index: 5)
+    monkeypatch.setattr(g, "_kv_workspaces", {})
+    monkeypatch.setattr(g, "_values", lambda *a: 0)
+    monkeypatch.setattr(g, "_heads", lambda *a: 8)
+    return calls, fake
+
+
+def attend(seqs):
+    q = torch.zeros(seqs, 1, 8, dtype=torch.bfloat16)
+    g.kv_attention(Cache(seqs), q, q, None)
+
+
+def test_captured_calls_have_workspaces_of_their_own(stubs):
+    calls, fake = stubs
+    fake.capturing = True
+    attend(3)
+    attend(3)
+    fake.capturing = False
+    attend(3)
+    attend(2)
+    attend(1 << 20)                                    # outgrows the kept one
+    at = [p for p, _ in calls.workspaces]
+    assert at[0] != at[1] and at[2] == at[3] and len(set(at)) == 4
+    for w in fake.made[:2]:                            # the counters are zeroed, the rest needs no value
+        assert w.numel() == 103 and (w[100:] == 0).all() and (w[:100] == 7).all()
+    # nothing that a graph uses is kept, so nothing of it can be handed out or dropped
+    assert [w.data_ptr() for w in g._kv_workspaces.values()] == at[4:]
+
+
+def test_kept_workspaces_are_of_the_stream(stubs, monkeypatch):
+    calls, _ = stubs
+    attend(3)
+    monkeypatch.setattr(g, "_raw_stream", lambda index: 6)
+    attend(3)
+    monkeypatch.setattr(g, "_raw_stream", lambda index: 5)
+    attend(3)
+    at = [p for p, _ in calls.workspaces]
+    assert at[0] == at[2] != at[1]
