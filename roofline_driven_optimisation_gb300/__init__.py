@@ -272,6 +272,10 @@ def device_status(stream=0) -> tuple[int, int]:
     """(status code, location code) of the device status word; clears it."""
     where = ctypes.c_int(0)
     rc = load().gemm_device_status(stream, ctypes.byref(where))
+    if rc != GEMM_OK:
+        # A call that gave up a wait leaves counts in its workspace, and the word holds
+        # the first failure alone: the next calls get new ones.
+        _kv_workspaces.clear()
     return rc, where.value
 
 
@@ -592,8 +596,9 @@ def kv_append(cache: KVCache, Q, K, V, cos, sin, base, Qout=None, start=None, ma
 
 
 # kv_attention's workspaces, one for each device and stream (the C ABI leaves them
-# to the caller): zeroed when made, ready again after every call.  Calls that are being
-# captured into a graph never get one of these.
+# to the caller): zeroed when made, ready again after every call, dropped by
+# device_status() when a call has failed.  Calls that are being captured into a graph
+# never get one of these.
 _kv_workspaces: dict = {}
 
 

@@ -95,3 +95,21 @@ def test_overlapping_rows_are_refused(cuda_lib):
     l = torch.randn(1, 1000, device="cuda").expand(3, 1000)
     with pytest.raises(ValueError, match="apart"):
         g.sample(l, torch.rand(3, device="cuda"), torch.empty(3, dtype=torch.int32, device="cuda"))
+
+
+def test_after_a_timeout_the_counters_are_zero_again(cuda_lib):
+    # counts as a call that gave up leaves them: the status that reports it ends their use
+    c, lens, Q, want = case([9000, 40])
+    O = torch.empty_like(Q)
+    g.kv_attention(c.cache, Q, O, lens)
+    check_status()
+    for w in g._kv_workspaces.values():
+        w.view(torch.int32).fill_(1)
+    g.selftest_wait_timeout(2_000_000)
+    torch.cuda.synchronize()
+    assert g.device_status()[0] == g.GEMM_ERR_DEVICE_TIMEOUT
+    for _ in range(2):
+        O.fill_(float("nan"))
+        g.kv_attention(c.cache, Q, O, lens)
+        check_status()
+        assert torch.equal(O, want)

@@ -150,3 +150,25 @@ def test_kept_workspaces_are_of_the_stream(stubs, monkeypatch):
     attend(3)
     at = [p for p, _ in calls.workspaces]
     assert at[0] == at[2] != at[1]
+
+
+@pytest.mark.parametrize("status", [g.GEMM_ERR_DEVICE_TIMEOUT, g.GEMM_ERR_INVALID_ARG])
+def test_a_failure_on_the_device_drops_the_kept_workspaces(stubs, status):
+    # a call that gave up leaves counts behind, and the status names the first failure only
+    calls, fake = stubs
+    word = [0]
+
+    def gemm_device_status(stream, where):
+        got, word[0] = word[0], 0
+        return got
+    calls.gemm_device_status = gemm_device_status
+    attend(3)
+    fake.made[-1].fill_(1)
+    assert g.device_status()[0] == g.GEMM_OK
+    attend(3)
+    assert len(fake.made) == 1                         # no failure: kept
+    word[0] = status
+    assert g.device_status()[0] == status
+    attend(3)
+    assert len(fake.made) == 2 and (fake.made[1] == 0).all()
+    assert calls.workspaces[2][0] == fake.made[1].data_ptr()
