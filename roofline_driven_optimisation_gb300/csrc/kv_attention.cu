@@ -198,14 +198,15 @@ struct Slot {           // a warp's partial result
   u64 unit;             // first unit of its item (~0: none)
   float* part;          // in shared memory or in the workspace
   int S, rows, h, t, first;   // the item's slabs and rows, head, tile, first row of its sequence
-  int count;            // index of its counter
+  long long count;      // index of its counter (max_new, so tiles, may be far above what is there)
 };
 
 struct Open {           // an item that more than one warp worked on
   u64 unit;
   int e0, e1;           // its parts: slots e0 .. e1 (warp * 2 + slot)
-  int S, rows, h, t, first, count;
+  int S, rows, h, t, first;
   int tl;               // the tile's place in its pass
+  long long count;
   bool whole;           // no other block has a part of it
 };
 
@@ -374,7 +375,7 @@ __device__ __forceinline__ uint32_t key_mask(int k0, int lim) {
 template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(NW * 32, 1)
     kv_attention_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-                        const __grid_constant__ KvAttnArgs a, const int group, const int max_tiles,
+                        const __grid_constant__ KvAttnArgs a, const int group, const long long max_tiles,
                         const int tw, const int vec) {
   using C = Cfg<D, NT>;
   constexpr int ST = C::STAGES, CH = D / 16, RT = NT * 8;
@@ -888,7 +889,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             s.h = done.h;
             s.t = done.t;
             s.first = done.q.first;
-            s.count = (done.b * a.c.H + done.h) * max_tiles + done.t;
+            s.count = ((long long)done.b * a.c.H + done.h) * max_tiles + done.t;
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -1174,8 +1175,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
 }
 
 template <int FMT, int D, int NT>
-int launch_fast(const KvAttnArgs& a, const CUtensorMap* mK, const CUtensorMap* mV, int group, int max_tiles, int tw,
-                int vec, int num_sms, cudaStream_t s) {
+int launch_fast(const KvAttnArgs& a, const CUtensorMap* mK, const CUtensorMap* mV, int group, long long max_tiles,
+                int tw, int vec, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> smem_set{0};
   constexpr int smem = NW * RING + 1024;
   cudaError_t e = set_smem_once(smem_set, kv_attention_kernel<FMT, D, NT>, smem);
@@ -1200,13 +1201,14 @@ int launch_fast(const KvAttnArgs& a, const CUtensorMap* mK, const CUtensorMap* m
 // Measured: 40 rows of 128 (9 x 20000 x 8 tokens) as three tiles of 16 297 us, two of
 // 24 205; 20 rows of 64 (24 x 1500 x 5) as two of 16 35.3, one of 24 28.5.
 struct Tiling {
-  int nt, tw, tiles;
+  int nt, tw;
+  long long tiles;
 };
 Tiling tiling(long long rows) {
   const long long eights = (rows + 7) / 8;
   const int tw = eights <= 4 ? 1 : eights <= 8 ? 2 : MAX_TW;
   const int nt = (int)std::min<long long>(4, (eights + tw - 1) / tw);
-  return {nt, tw, (int)((eights + nt - 1) / nt)};
+  return {nt, tw, (eights + nt - 1) / nt};
 }
 
 template <class Kernel>

@@ -113,3 +113,25 @@ def test_after_a_timeout_the_counters_are_zero_again(cuda_lib):
         g.kv_attention(c.cache, Q, O, lens)
         check_status()
         assert torch.equal(O, want)
+
+
+def test_counters_past_32_bits(cuda_lib):
+    # max_new is a bound, and every tile that it allows has a counter: 2.7 billion here,
+    # those of the long sequence's items behind 2^31
+    lengths, heads, hq, most = [40, 3, 0, 17, 5000], 32, 256, 1 << 26
+    c = Case(g.KV_INT8, heads, 128, 64, lengths)
+    lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    Q = torch.randn(5, hq, 128, device="cuda").bfloat16()
+    start = torch.arange(6, dtype=torch.int32, device="cuda")
+    want = g.kv_attention(c.cache, Q, torch.empty_like(Q), lens, start=start, max_new=1)
+    size = g.gemm_kv_attention_workspace(5, heads, hq, 128, most)
+    assert size > 10 * 2 ** 30
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        O = torch.full_like(Q, float("nan"))
+        g.kv_attention(c.cache, Q, O, lens, start=start, max_new=most, workspace=ws)
+        check_status()
+        # other tiles, so another order of sums: each side a bf16 rounding (2^-8) and
+        # 2^-10 of its row's size, at most the largest value (127 codes of 0.02), off
+        assert ((O.float() - want.float()).abs() <= 2.0 ** -7 * want.float().abs() + 2.0 ** -9 * 2.54).all()
+    assert (ws[g.gemm_kv_attention_workspace(0, heads, hq, 128, most):].view(torch.int32) == 0).all()
