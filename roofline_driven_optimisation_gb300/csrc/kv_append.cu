@@ -108,7 +108,9 @@ __device__ bool find_item(const KvAppendArgs& a, int i, Item& out) {
         if (count[q] > 0 && i >= excl && i < excl + count[q]) {
           found.b = b0 + lane * PER + q;
           found.col = base[q] / P + (i - excl);
-          const int lo = max(base[q], found.col * P), hi = min(base[q] + n[q], (found.col + 1) * P);
+          // the page's end may lie behind 2^31 - 1, the last row does not
+          const int lo = max(base[q], found.col * P);
+          const int hi = (int)min((long long)base[q] + n[q], ((long long)found.col + 1) * P);
           found.row0 = first[q] + (lo - base[q]);
           found.n = hi - lo;
           found.pos0 = lo;
@@ -288,9 +290,10 @@ __global__ void __launch_bounds__(DEC_WARPS * 32) kv_append_tokens_kernel(const 
     report_status(a.status, 1, kSiteKvAppend);
     return;
   }
-  const int col = base / a.c.P + nth, pos = max(base, col * a.c.P);       // the part in this page
-  const int n = min(base + all, (col + 1) * a.c.P) - pos, held = pos - col * a.c.P;
-  if (n <= 0) return;
+  const int col = base / a.c.P + nth, end = base + all;
+  const long long page = (long long)col * a.c.P;   // the page's first position, and its end: up to 2^31 and more
+  if (page >= end) return;
+  const int pos = max(base, (int)page), n = (int)min((long long)end, page + a.c.P) - pos, held = pos - (int)page;
   const int row = first + (pos - base);
   const long long ld = kind == 0 ? a.ldq : kind == 1 ? a.ldk : a.ldv;
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(kind == 0 ? a.Q : kind == 1 ? a.K : a.V) +
