@@ -15,6 +15,7 @@
 #include "internal.h"
 #include "kv_cache.cuh"
 #include "ptx.cuh"
+#include "row_walk.cuh"
 
 namespace g3 {
 namespace {
@@ -185,9 +186,9 @@ __global__ void __launch_bounds__(128) kv_append_generic_kernel(const KvAppendAr
   int d0, d1;
   if (kind == 0) {
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.Qo);
-    for (int e = threadIdx.x; e < it.n * units; e += blockDim.x) {
-      const int t = e / units;
-      const float2 y = value(t, e % units, d0, d1);
+    for (RowWalk e(threadIdx.x, blockDim.x, units); e.within(it.n); e.next()) {
+      const int t = (int)e.row;
+      const float2 y = value(t, e.at, d0, d1);
       __nv_bfloat16* o = out + (long long)(it.row0 + t) * a.ldqo + (long long)h * D;
       o[d0] = __float2bfloat16_rn(y.x);
       if (d1 >= 0) o[d1] = __float2bfloat16_rn(y.y);
@@ -199,25 +200,25 @@ __global__ void __launch_bounds__(128) kv_append_generic_kernel(const KvAppendAr
   float* scale = (kind == 1 ? a.c.ks : a.c.vs) + (long long)g * a.c.H + h;
   uint8_t* codes = (kind == 1 ? a.c.k : a.c.v) + (long long)g * a.c.ps + (long long)h * a.c.hs;
   float m = 0.f;
-  for (int e = threadIdx.x; e < it.n * units; e += blockDim.x) {
-    const float2 y = value(e / units, e % units, d0, d1);
+  for (RowWalk e(threadIdx.x, blockDim.x, units); e.within(it.n); e.next()) {
+    const float2 y = value((int)e.row, e.at, d0, d1);
     m = fmaxf(m, fmaxf(fabsf(y.x), fabsf(y.y)));
   }
   const int held = it.pos0 % a.c.P;              // earlier tokens of this page
   const float s0 = held > 0 ? *scale : 0.f;
   m = block_max(m, red);                         // every thread has read *scale
   const float s = fmaxf(s0, kv_scale_for<FMT>(m)), r = kv_recip(s);
-  for (int e = threadIdx.x; e < it.n * units; e += blockDim.x) {
-    const int t = e / units;
-    const float2 y = value(t, e % units, d0, d1);
+  for (RowWalk e(threadIdx.x, blockDim.x, units); e.within(it.n); e.next()) {
+    const int t = (int)e.row;
+    const float2 y = value(t, e.at, d0, d1);
     uint8_t* o = codes + (long long)(held + t) * a.c.ts;
     const uint32_t c2 = kv_code2<FMT>(__fmul_rn(y.x, r), __fmul_rn(y.y, r));
     o[d0] = (uint8_t)c2;
     if (d1 >= 0) o[d1] = (uint8_t)(c2 >> 8);
   }
   if (s > s0 && held > 0) {
-    for (int e = threadIdx.x; e < held * D; e += blockDim.x) {
-      uint8_t* o = codes + (long long)(e / D) * a.c.ts + e % D;
+    for (RowWalk e(threadIdx.x, blockDim.x, D); e.within(held); e.next()) {
+      uint8_t* o = codes + (long long)e.row * a.c.ts + e.at;
       *o = (uint8_t)recode<FMT>(*o, s0, r);
     }
   }
