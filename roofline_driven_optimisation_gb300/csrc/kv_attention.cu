@@ -95,20 +95,21 @@ __global__ void __launch_bounds__(GT) kv_attention_generic_kernel(const KvAttnAr
   const int D = a.c.D, row = blockIdx.x, hq = blockIdx.y, h = hq / (a.Hq / a.c.H);
   int b, i, n;
   if (!find_row(a, row, b, i, n)) return;
-  const int keys = kv_length(a, b) - n + i + 1;   // keys this row sees
+  // keys this row sees; unsigned, since a chunk may end behind 2^31 - 1
+  const unsigned keys = (unsigned)max(0, kv_length(a, b) - n + i + 1), P = (unsigned)a.c.P;
   const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.Q) + (long long)row * a.ldq + (long long)hq * D;
   for (int d = threadIdx.x; d < D; d += GT) q[d] = __bfloat162float(qr[d]);
   float acc[GD / GT] = {};
   float m = -INFINITY, l = 0.f;
-  for (int j0 = 0; j0 < keys; j0 += GT) {
-    const int j = j0 + threadIdx.x;
+  for (unsigned j0 = 0; j0 < keys; j0 += GT) {
+    const unsigned j = j0 + threadIdx.x;
     float s = -INFINITY, vs = 0.f;
     long long off = -1;
     __syncthreads();   // q is written; the previous chunk's readers are done
     if (j < keys) {
-      const int g = kv_page(a.c, b, j / a.c.P, a.status, kSiteKvAttn);
+      const int g = kv_page(a.c, b, (int)(j / P), a.status, kSiteKvAttn);
       if (g >= 0) {
-        off = (long long)g * a.c.ps + (long long)h * a.c.hs + (long long)(j % a.c.P) * a.c.ts;
+        off = (long long)g * a.c.ps + (long long)h * a.c.hs + (long long)(j % P) * a.c.ts;
         const uint8_t* kc = a.c.k + off;
         float dot = 0.f;
         for (int d = 0; d < D; ++d) dot = fmaf(q[d], kv_value2<FMT>(kc[d]).x, dot);
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(GT) kv_attention_generic_kernel(const KvAttnAr
       const int d = c * GT + threadIdx.x;
       if (d >= D) break;
       float x = acc[c] * alpha;
-      for (int t = 0; t < min(GT, keys - j0); ++t)
+      for (int t = 0; t < (int)min((unsigned)GT, keys - j0); ++t)
         if (at[t] >= 0) x = fmaf(p[t], kv_value2<FMT>(a.c.v[at[t] + d]).x, x);
       acc[c] = x;
     }
@@ -235,13 +236,16 @@ struct Seq {
   int len, first, n, S, tiles, passes;
 };
 
+// Slabs of a sequence of len keys; one, of which no row sees a key, where it has none
+__device__ __forceinline__ int slabs(int len) { return max(1, (int)(((unsigned)len + SLAB - 1) / SLAB)); }
+
 struct Plan {
   const KvAttnArgs* a;
   int group, rt;        // query heads of a head; rows of a tile
   int tw_log, tl;       // log2 of a group's warps; this warp's place in it
   __device__ __forceinline__ Seq seq(int len, int first, int n) const {
     const int tiles = (n * group + rt - 1) / rt;
-    return Seq{len, first, n, max(1, (len + SLAB - 1) / SLAB), tiles, (tiles + (1 << tw_log) - 1) >> tw_log};
+    return Seq{len, first, n, slabs(len), tiles, (tiles + (1 << tw_log) - 1) >> tw_log};
   }
   __device__ __forceinline__ Seq seq(int b) const {
     // every load before the first check, which waits for it
@@ -481,7 +485,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   auto item_unit = [&](u64 i) -> u64 {            // first unit of item i
     if (i >= (u64)I) return T;
     const SeqRec& q = rec[record([&](const SeqRec& x) { return x.items <= (int)i; })];
-    return q.at + (i - q.items) * (u64)max(1, (q.len + SLAB - 1) / SLAB);
+    return q.at + (i - q.items) * (u64)slabs(q.len);
   };
   const u64 A = by_item ? item_unit(quotient(cta * I, G)) : quotient(cta * T, G);
   const u64 B = by_item ? item_unit(quotient((cta + 1) * I, G)) : quotient((cta + 1) * T, G);
@@ -648,7 +652,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         ks[1] = npg == 2 ? meta.ks[1] : ks[0];
         vs[1] = npg == 2 ? meta.vs[1] : vs[0];
         // every key of the slab is there for every row
-        const bool whole = k0 + SLAB <= lim_min && (ok0 & ok1);
+        const bool whole = lim_min - SLAB >= k0 && (ok0 & ok1);   // the slab may end at 2^31
 
         // S^T = K Q^T.  ldmatrix gives lane (g, t4) bytes 4*t4 .. 4*t4+3 of row g of
         // each 16-byte chunk: the first two are the operand's k = 2*t4, 2*t4+1, the

@@ -29,3 +29,34 @@ def test_positions_up_to_the_last_of_32_bits(cuda_lib, new):
     assert g.device_status() == (g.GEMM_ERR_INVALID_ARG, 60)
     assert torch.equal(out, Q) and (all_out[new:] == 0).all()
     assert all(np.array_equal(before[n], c.got(n)) for n in before)
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 16, 2 ** 31 - 19])
+def test_contexts_up_to_the_last_position_of_32_bits(cuda_lib, length):
+    # 4097 pages under a table of 2^27 - 1 columns; the last column has a page of its own,
+    # whose keys have all the weight (scores of 40 and more against 0 of 2^31 others,
+    # e^40 > 10^8 * 2^31), and behind the length keys with still more
+    cols, P, D = 2 ** 27 - 1, 16, 64
+    rng = np.random.default_rng(length)
+    table = torch.arange(cols, dtype=torch.int32, device="cuda").remainder_(4096)
+    table[-1] = 4096
+    k = torch.zeros(4097, 1, P, D, dtype=torch.int8, device="cuda")
+    code = 100 + rng.integers(0, 4, P)
+    code[length % P or P:] = 127
+    k[4096, 0] = torch.from_numpy(code.astype(np.int8)).cuda()[:, None]
+    v = torch.randint(-127, 128, (4097, 1, P, D), device="cuda", dtype=torch.int8)
+    scale = torch.full((4097, 1), 0.05, device="cuda")
+    cache = g.KVCache(k, v, scale, scale, table[None])
+    Q = torch.ones(1, 4, D, device="cuda").bfloat16()
+    O = g.kv_attention(cache, Q, torch.empty_like(Q), ints(length))
+    assert g.last_path() == g.PATH_KV
+    check_status()
+    n = length % P or P
+    s = code[:n] * 0.05 * D / np.sqrt(D)
+    p = np.exp(s - s.max())
+    x = v[4096, 0, :n].double().cpu().numpy() * float(np.float32(0.05))
+    want = (p / p.sum()) @ x
+    # the bounds of test_gpu_kv_attention: one rounding to bf16, P in fp16 and the scores
+    size = (p / p.sum()) @ np.abs(x)
+    off = np.abs(O[0].float().cpu().numpy() - want)
+    assert (off <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * size.max() + 1e-6).all()
