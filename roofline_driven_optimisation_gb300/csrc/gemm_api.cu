@@ -17,6 +17,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <unordered_map>
 
@@ -157,6 +158,16 @@ void trim_maps() {
   if (t_maps.size() > 1024) t_maps.clear();
 }
 
+// Keeps a new map.  No C++ exception leaves an entry point of the C ABI.
+int keep_map(const MapKey& key, const CUtensorMap& map, const CUtensorMap** out) {
+  try {
+    *out = &t_maps.emplace(key, map).first->second;
+  } catch (const std::exception&) {
+    return fail(GEMM_ERR_CUDA, "out of host memory for a tensor map");
+  }
+  return GEMM_OK;
+}
+
 // 2-D row-major matrix (rows x cols, leading dimension ld_bytes) as a TMA
 // tensor with box (box_cols x box_rows); elements outside read as zero.
 int make_map(const void* ptr, uint64_t cols, uint64_t rows, uint64_t ld_bytes, uint32_t box_cols,
@@ -182,9 +193,7 @@ int make_map(const void* ptr, uint64_t cols, uint64_t rows, uint64_t ld_bytes, u
   if (r != CUDA_SUCCESS)
     return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %llux%llu ld=%llu", (int)r,
                 (unsigned long long)rows, (unsigned long long)cols, (unsigned long long)ld_bytes);
-  auto ins = t_maps.emplace(key, map);
-  *out = &ins.first->second;
-  return GEMM_OK;
+  return keep_map(key, map, out);
 }
 
 // A 3-D tiled map: cols x rows x depth with row stride ld_bytes and depth
@@ -211,9 +220,7 @@ int make_map_3d(const void* ptr, uint64_t cols, uint64_t rows, uint64_t depth, u
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled (3-D) failed (%d)", (int)r);
-  auto ins = t_maps.emplace(key, map);
-  *out = &ins.first->second;
-  return GEMM_OK;
+  return keep_map(key, map, out);
 }
 
 // A paged cache's codes as a 4-D tensor of bytes (dim, page row, head, page) with
@@ -240,9 +247,7 @@ int make_map_kv(const void* ptr, const KvCache& c, uint32_t rows, const CUtensor
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled (paged cache) failed (%d)", (int)r);
-  auto ins = t_maps.emplace(key, map);
-  *out = &ins.first->second;
-  return GEMM_OK;
+  return keep_map(key, map, out);
 }
 
 // ---------------------------------------------------------------- dispatch
