@@ -390,9 +390,13 @@ typedef struct {
  * NaN is ignored in a, and stored as E4M3's NaN or as INT8's 0.
  *
  * Pages that the call writes belong to one sequence each (two sequences may
- * share pages that only hold earlier tokens).  At most 65535 heads; tokens
- * past the table, or at positions >= `positions`, are not stored (see
- * gemm_kv_cache).  Asynchronous, no allocation, deterministic.
+ * share pages that only hold earlier tokens).  At most 65535 heads.  Tokens past
+ * the table, or in a page that is not there, are not stored; their queries are
+ * rotated like the others.  A sequence of which any row is at a position >=
+ * `positions` or below 0, or whose rows do not fit the call, is skipped as a
+ * whole: none of its tokens is stored, and its rows of Qout are not written.
+ * gemm_device_status() reports either (see gemm_kv_cache).  Asynchronous, no
+ * allocation, deterministic.
  */
 int gemm_kv_append(const gemm_kv_cache* cache, int tokens, int Hq, const gemm_bf16_t* Q, long long ldq,
                    const gemm_bf16_t* K, long long ldk, const gemm_bf16_t* V, long long ldv, gemm_bf16_t* Qout,

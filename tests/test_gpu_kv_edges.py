@@ -60,3 +60,55 @@ def test_contexts_up_to_the_last_position_of_32_bits(cuda_lib, length):
     size = (p / p.sum()) @ np.abs(x)
     off = np.abs(O[0].float().cpu().numpy() - want)
     assert (off <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * size.max() + 1e-6).all()
+
+
+# new tokens a sequence and the width that is turned: the kernel of a few tokens, the
+# kernel of pages, the generic one
+KERNELS = [(2, 64), (24, 64), (3, 32)]
+
+
+@pytest.mark.parametrize("new,turned", KERNELS)
+def test_a_sequence_past_the_angles_is_skipped_as_a_whole(cuda_lib, new, turned):
+    # the second sequence's last row has no angles: its other rows are not stored either,
+    # and its queries are not written; the others are not touched by that
+    base, rows = [3, 40, 0], 3 * new
+    c = Case(g.KV_INT8, 2, 64, 16, [b + new for b in base])
+    start = np.arange(4) * new
+    angle = np.random.default_rng(1).normal(size=(40 + new - 1, turned // 2)).astype(np.float32)
+    cos, sin = np.cos(angle), np.sin(angle)
+    Q, K = torch.randn(rows, 3, 64).bfloat16(), torch.randn(rows, 2, 64).bfloat16()
+    out = torch.full((rows, 3, 64), 7.0, device="cuda").bfloat16()
+    g.kv_append(c.cache, Q.cuda(), K.cuda(), K.cuda(), torch.from_numpy(cos).cuda(), torch.from_numpy(sin).cuda(), ints(*base),
+                out, start=ints(*start), max_new=new)
+    assert (g.last_path() == g.PATH_KV) == (turned == 64)
+    torch.cuda.synchronize()
+    assert g.device_status() == (g.GEMM_ERR_INVALID_ARG, 60)
+    none = np.array([0, new, new, 2 * new])            # the call without that sequence's rows
+    keep = np.r_[0:new, 2 * new:rows]
+    want = S.append(c.np, g.KV_INT8, *(t.float().numpy()[keep] for t in (Q, K, K)), cos, sin, base, none, False, np.float32)
+    for n in ("k", "v", "ks", "vs"):
+        assert np.array_equal(c.got(n), c.np[n])
+    out = out.float().cpu()
+    assert (out[new:2 * new] == 7).all() and torch.equal(out[keep], torch.from_numpy(want).bfloat16().float())
+
+
+@pytest.mark.parametrize("new,turned", KERNELS)
+def test_queries_of_tokens_without_a_page_are_turned(cuda_lib, new, turned):
+    # a table that ends before the new tokens do, and a page number that is none
+    c = Case(g.KV_INT8, 2, 64, 16, [16])
+    before = {n: c.got(n).copy() for n in ("k", "v", "ks", "vs")}
+    angle = np.random.default_rng(1).normal(size=(64, turned // 2)).astype(np.float32)
+    cos, sin = np.cos(angle), np.sin(angle)
+    Q, K = torch.randn(new, 3, 64).bfloat16(), torch.randn(new, 2, 64).bfloat16().cuda()
+    for base, page in ((16, None), (0, 99)):
+        if page is not None:
+            c.table[0, 0] = page
+        out = torch.full((new, 3, 64), 7.0, device="cuda").bfloat16()
+        g.kv_append(c.cache, Q.cuda(), K, K, torch.from_numpy(cos).cuda(), torch.from_numpy(sin).cuda(), ints(base), out,
+                    start=ints(0, new), max_new=new)
+        torch.cuda.synchronize()
+        assert g.device_status() == (g.GEMM_ERR_INVALID_ARG, 60)
+        pos = base + np.arange(new)
+        want = S.rotate(Q.float().numpy(), cos[pos], sin[pos], False, np.float32)
+        assert torch.equal(out.float().cpu(), torch.from_numpy(want).bfloat16().float())
+        assert all(np.array_equal(before[n], c.got(n)) for n in before)
