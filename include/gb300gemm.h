@@ -384,7 +384,11 @@ typedef struct {
  *
  * and when s is larger than the page's present scale s0, the earlier tokens'
  * codes c become (c * s0) * (1/s), rounded the same way.  So no value is ever
- * clipped, and appending again what is there changes nothing.  A page that a
+ * clipped, and appending again what is there changes nothing; but a token is
+ * rounded once more each time that its page's scale grows after it, so its error
+ * is a sum: half a step of every scale that it was held at (INT8: 0.5 s each;
+ * E4M3: 2^-4 of the value, or 2^-10 s below 2^-6 s).  Tokens appended one at a
+ * time meet a few such growths a page, those of one call none.  A page that a
  * sequence enters at its first row starts with a new scale.  Infinities are
  * stored as the largest finite value of a page whose scale is FLT_MAX / qmax;
  * NaN is ignored in a, and stored as E4M3's NaN or as INT8's 0.

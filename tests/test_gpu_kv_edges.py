@@ -112,3 +112,19 @@ def test_queries_of_tokens_without_a_page_are_turned(cuda_lib, new, turned):
         want = S.rotate(Q.float().numpy(), cos[pos], sin[pos], False, np.float32)
         assert torch.equal(out.float().cpu(), torch.from_numpy(want).bfloat16().float())
         assert all(np.array_equal(before[n], c.got(n)) for n in before)
+
+
+@pytest.mark.parametrize("fmt", [g.KV_E4M3, g.KV_INT8])
+def test_pages_filled_a_token_at_a_time(cuda_lib, fmt):
+    # every growth of a scale rounds what the page holds: the same bits as the oracle's
+    # after each token, for tokens of growing size
+    c = Case(fmt, 2, 128, 16, [0, 5], new=20)
+    rng = np.random.default_rng(fmt)
+    none = np.zeros((64, 0), np.float32)
+    for t in range(20):
+        x = torch.from_numpy((rng.normal(size=(2, 2, 128)) * 1.2 ** t).astype(np.float32)).bfloat16()
+        g.kv_append(c.cache, None, x.cuda(), x.cuda(), None, None, ints(t, 5 + t))
+        S.append(c.np, fmt, None, x.float().numpy(), x.float().numpy(), none, none, [t, 5 + t], [0, 1, 2], False, np.float32)
+        check_status()
+        for n in ("k", "v", "ks", "vs"):
+            assert np.array_equal(c.got(n), c.np[n]), (t, n)
