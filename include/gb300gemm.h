@@ -423,8 +423,8 @@ int gemm_kv_append(const gemm_kv_cache* cache, int tokens, int Hq, const gemm_bf
  *
  * Scores, softmax statistics and sums are fp32; the codes, and the queries after
  * an exact power-of-two scaling of each row, enter the products in fp16 (a query
- * value 2^40 times smaller than its row's largest may lose bits), and so do the
- * probabilities times the page's scale.  O is rounded once to bf16.
+ * value more than 2^31 times smaller than its row's largest may lose bits), and so
+ * do the probabilities times the page's scale.  O is rounded once to bf16.
  *
  * workspace: gemm_kv_attention_workspace() bytes of DEVICE memory, 16-byte
  * aligned, zeroed once before its first use and owned by one call at a time (every

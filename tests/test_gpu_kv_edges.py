@@ -128,3 +128,24 @@ def test_pages_filled_a_token_at_a_time(cuda_lib, fmt):
         check_status()
         for n in ("k", "v", "ks", "vs"):
             assert np.array_equal(c.got(n), c.np[n]), (t, n)
+
+
+def test_small_query_values_keep_their_bits(cuda_lib):
+    # a row's largest value is scaled to 2^14 and more, so a bf16 value 2^31 times smaller
+    # ends at fp16's smallest step, 2^-24: all of its weight is there
+    c = Case(g.KV_INT8, 1, 64, 16, [40])
+    c.np["k"][:, :, :, 0] = 0
+    c.np["k"][:, :, :, 1] = c.rng.integers(-127, 128, c.np["k"][:, :, :, 1].shape).astype(np.int8).view(np.uint8)
+    c.np["k"][:, :, :, 2:] = 0
+    c.np["ks"][:] = 1.0
+    c.put()
+    for e in (-30, -31):
+        Q = torch.zeros(1, 2, 64)
+        Q[0, :, 0], Q[0, 0, 1], Q[0, 1, 1] = 1.0, 2.0 ** e * 255 / 128, -2.0 ** e * 129 / 128
+        O = torch.empty(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+        # scores up to 31: the last of the value's eight bits is a share of 0.2 of a weight
+        scale = 2.0 ** (-3 - e)
+        g.kv_attention(c.cache, Q.bfloat16().cuda(), O, ints(40), scale=scale)
+        check_status()
+        want, size = S.attention(c.np, g.KV_INT8, Q.numpy(), [40], [0, 1], scale)
+        assert (np.abs(O.float().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * size[..., None]).all()
