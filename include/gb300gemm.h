@@ -45,11 +45,14 @@
  *     on a device sets kernel attributes and queries occupancy.
  *
  * Errors: every entry point returns a gemm_status.  On a non-zero return
- * nothing was launched (except when the second launch of a two-launch call,
- * the FP32 path's split last wave, fails after the first was queued) and
+ * nothing was launched (except when the second launch of a two-launch call
+ * fails after the first was queued: the FP32 path's split last wave, and
+ * gemm_sample_* of more rows than the GPU takes at once, whose token may then
+ * be -2 for the rows that the second launch was to draw, or not written) and
  * gemm_get_last_error() describes the cause.  Errors
- * found on the device (a bounded wait that ran out) are recorded in a status
- * word that gemm_device_status() reads.
+ * found on the device (a bounded wait that ran out, an index of a paged cache
+ * that does not fit) are recorded in a status word that gemm_device_status()
+ * reads.
  */
 #ifndef GB300GEMM_H
 #define GB300GEMM_H
