@@ -1128,17 +1128,46 @@ __global__ void __launch_bounds__(NW * 32, 1)
       }
     }
     __syncthreads();
-    // As above.  Few rows leave warps over, so that `split` of them share a row's
-    // parts (every split-th each) and meet in shared memory.
-    auto finish = [&](auto batch, int split) {
+    // As above, in an order of adding that is the item's own: which block is the last to
+    // arrive, and so what other items it adds beside this one, changes from run to run.
+    // Few rows of many parts leave warps over: 2^ways_log of them share a row's parts
+    // (every 2^ways_log-th each) and meet in shared memory.  Up to 4 parts are one warp's
+    // loads in flight together.
+    auto ways_log = [&](int j) {
+      const int pairs = (sh.open[j].rows + RPW - 1) / RPW;
+      return sh.blocks[j] <= 4 || pairs > 4 ? 0 : pairs > 2 ? 1 : pairs > 1 ? 2 : 3;
+    };
+    // the place of the first share behind item j, the items' shares side by side and each
+    // item's at a multiple of its ways
+    auto shares = [&](int at, int j, int batch) {
+      const int w = ways_log(j), rows = w > 0 ? RPW : batch * RPW;
+      return ((at + (1 << w) - 1) >> w << w) + ((sh.open[j].rows + rows - 1) / rows << w);
+    };
+    auto finish = [&](auto batch) {
       constexpr int U = decltype(batch)::value;
-      const int groups = (rmax + U * RPW - 1) / (U * RPW), s = warp % split, all = (to - from) * groups;
+      int all = 0;
+      bool meet = false;
+      for (int j = from; j < to; ++j)
+        if (sh.last[j]) {
+          all = shares(all, j, U);
+          meet |= ways_log(j) > 0;
+        }
       // the same number of rounds for every warp: each is at the barrier in each round
-      for (int i0 = 0; i0 < all; i0 += NW / split) {
-        const int i = i0 + warp / split, nth = min(i, all - 1) / groups;
-        const int j = from + nth, r0 = (i - nth * groups) * U * RPW + lane_row;
-        const bool mine = i < all && sh.last[j];
-        const Open& o = sh.open[j];
+      for (int i0 = 0; i0 < all; i0 += NW) {
+        int j = from, wl = 0, k = -1;                  // this warp's share of item j
+        for (int at = 0; j < to; ++j) {
+          if (!sh.last[j]) continue;
+          wl = ways_log(j);
+          const int end = shares(at, j, U);
+          if (i0 + warp < end) {
+            k = i0 + warp - ((at + (1 << wl) - 1) >> wl << wl);
+            break;
+          }
+          at = end;
+        }
+        const bool mine = k >= 0;                      // not between two items' shares, nor behind the last
+        const int ways = 1 << wl, s = k & (ways - 1), r0 = (k >> wl) * (wl > 0 ? RPW : U * RPW) + lane_row;
+        const Open& o = sh.open[mine ? j : from];
         float4 x[U] = {};
         if (mine) {
           const int n = sh.blocks[j], c0 = first_block(o);
@@ -1146,33 +1175,35 @@ __global__ void __launch_bounds__(NW * 32, 1)
           // part c: the second of block c0, the first of block c0 + c
           const float* p = parts + ((size_t)c0 * 2 * MAX_TW + o.tl) * PART_FLOATS + r0 * D + lane_quad * 4;
           constexpr size_t next = (size_t)2 * MAX_TW * PART_FLOATS;
+          const int rows = wl > 0 ? min(o.rows, r0 + 1) : o.rows;   // one row a lane where parts are shared
 #pragma unroll 8
-          for (int c = s; c < n; c += split) {
+          for (int c = s; c < n; c += ways) {
             const float* q = p + (c == 0 ? next / 2 : c * next);
 #pragma unroll
             for (int u = 0; u < U; ++u)
-              if (r0 + u * RPW < o.rows)
+              if (r0 + u * RPW < rows)
                 add(x[u], w[u * RPW * n + c], __ldcg(reinterpret_cast<const float4*>(q + u * RPW * D)));
           }
         }
-        if constexpr (U == 1) {
-          if (split > 1) {
-            shared_sum[threadIdx.x] = x[0];
-            __syncthreads();
-            if (s == 0)
-              for (int k = 1; k < split; ++k) add(x[0], 1.f, shared_sum[threadIdx.x + k * 32]);
-            __syncthreads();
-          }
+        if (meet) {
+          shared_sum[threadIdx.x] = x[0];
+          __syncthreads();
+          if (mine && s == 0)
+            for (int q = 1; q < ways; ++q) add(x[0], 1.f, shared_sum[threadIdx.x + q * 32]);
+          __syncthreads();
         }
         if (!mine || s != 0) continue;
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (r0 + u * RPW < o.rows) store(o, r0 + u * RPW, lane_quad, x[u], item_sum[j * MAX_ROWS + r0 + u * RPW]);
+          if (r0 + u * RPW < o.rows && (u == 0 || wl == 0))
+            store(o, r0 + u * RPW, lane_quad, x[u], item_sum[j * MAX_ROWS + r0 + u * RPW]);
       }
     };
-    const int pairs = (to - from) * ((rmax + RPW - 1) / RPW);
-    if (pairs <= NW) finish(std::integral_constant<int, 1>{}, pairs <= 1 ? 8 : pairs <= 2 ? 4 : pairs <= 4 ? 2 : 1);
-    else finish(std::integral_constant<int, 4>{}, 1);
+    int one = 0;                                       // shares of a row, or a pair of them
+    for (int j = from; j < to; ++j)
+      if (sh.last[j]) one = shares(one, j, 1);
+    if (one <= NW) finish(std::integral_constant<int, 1>{});
+    else finish(std::integral_constant<int, 4>{});
     __syncthreads();                                 // the weights have been read
     from = to;
   }
