@@ -16,8 +16,9 @@
 //     candidates in the first block, cut and drawn by histograms.  What does not fit:
 //     a search by histograms over the cluster.
 //   * sample_stream_kernel: many rows with up to 64 ranks, a block or a few a row.
-//   * sample_kernel: rows beyond the cluster's shared memory, radix searches over
-//     global memory.
+//   * sample_kernel: rows beyond the cluster's shared memory (360448), radix searches
+//     over global memory by one block a row: 8 rows of 2^20 bf16 0.76 ms greedy, 16 ms
+//     with top-k and top-p (a pass of the row for each of eight digits and more).
 // Measured on one GB300, GPU time: one row of 32000 with top-k 50, top-p and min-p
 // 9 us; 64 rows of 32000 bf16: the same settings 11 us, top-k 1000 with top-p 25 us,
 // top-p alone 21 to 35 us (flat rows need the search), no cut 13 us; 384 rows of
@@ -1039,7 +1040,9 @@ __device__ __forceinline__ void cluster_row(const SampleArgs& a, const int C, co
     float x = top > kKeyNegInf ? sh.group_mass[lane % FW] : 0.f;
     for (int o = FW / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (tid == 0) {
-      // a block without candidates (behind the row's end, or all -inf) bounds nothing
+      // A block without candidates (behind the row's end, or all -inf) bounds nothing.
+      // 64 rows of 50257 bf16, whose eighth block is empty: p 0.5 at temperature 0.3
+      // 74 us where it did, now 44.
       sh.bound_key = top > kKeyNegInf ? bound : 0u;
       sh.block_mass = x;
     }
