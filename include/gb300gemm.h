@@ -460,7 +460,8 @@ size_t gemm_kv_attention_workspace(int seqs, int heads, int Hq, int dim, int max
  * With T the kept tokens' total mass, the token is the first, in index order, at
  * which the running mass of the kept exceeds floor(u * T) (products with u and
  * top_p in fp64; u outside [0, 1) is taken to the nearest of the range, NaN to
- * 0).  t <= 0 (or below 2^-126): the first rank.  logprob = (l - m) * (1/t) -
+ * 0).  t <= 0 (or below 2^-126): the first rank alone; so with t, top_p or min_p of
+ * NaN, and with min_p above 1.  logprob = (l - m) * (1/t) -
  * log(T / 2^40), the token's log-probability among the kept (0 for t <= 0).
  *
  * NaN logits count as -inf; a logit of -inf is never taken.  A row whose logits

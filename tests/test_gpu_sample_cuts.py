@@ -102,3 +102,17 @@ def test_logits_that_differ_by_next_to_nothing(cuda_lib, dtype, rows, vocab, siz
         k, p = torch.full((rows,), k), torch.full((rows,), p)
         token, _ = call(l, u, temperature=t.tolist(), top_k=k.tolist(), top_p=p.tolist())
         assert np.array_equal(token, _rule(l, u, t, k, p, m))
+
+
+@pytest.mark.parametrize("rows,vocab", [(6, 100), (6, 50257), (333, 40000), (2, 400003)])
+def test_settings_that_are_no_numbers_keep_the_first_rank(cuda_lib, rows, vocab):
+    gen = torch.Generator().manual_seed(vocab)
+    l = torch.randn(rows, vocab, generator=gen).bfloat16()
+    u = np.random.default_rng(vocab).random(rows).astype(np.float32)
+    nan = [math.nan] * rows
+    first = l.float().argmax(1).numpy()
+    for kw in (dict(temperature=nan), dict(top_p=nan), dict(min_p=nan), dict(min_p=[1.5] * rows), dict(top_p=[0.0] * rows),
+               dict(top_k=[7] * rows, top_p=nan), dict(top_k=[700] * rows, min_p=nan), dict(temperature=nan, top_p=[0.5] * rows)):
+        token, logprob = call(l, u, **kw)
+        assert np.array_equal(token, first), kw
+        assert (logprob == 0).all(), kw
