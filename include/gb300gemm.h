@@ -46,8 +46,9 @@
  *
  * Errors: every entry point returns a gemm_status.  On a non-zero return
  * nothing was launched (except when the second launch of a two-launch call
- * fails after the first was queued: the FP32 path's split last wave, and
- * gemm_sample_* of more rows than the GPU takes at once, whose token may then
+ * fails after the first was queued: the FP32 path's split last wave,
+ * gemm_route_* of more tokens than one block takes (offsets and order are then not
+ * written), gemm_experts, and gemm_sample_* of more rows than the GPU takes at once, whose token may then
  * be -2 for the rows that the second launch was to draw, or not written) and
  * gemm_get_last_error() describes the cause.  Errors
  * found on the device (a bounded wait that ran out, an index of a paged cache
@@ -478,6 +479,144 @@ int gemm_sample_f32(int rows, int vocab, const float* logits, long long ld, cons
                     const int* top_k, const float* top_p, const float* min_p, const float* u, int* token,
                     float* logprob, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A layer of routed experts in 8 bits: routing, quantisation, block-scaled
+ * products and the experts' products of the routed tokens.  The source pages
+ * name none of them; they are this library's additions.  No gradients.
+ * ------------------------------------------------------------------------ */
+
+/* How a router's logits become scores. */
+typedef enum {
+  GEMM_ROUTE_SOFTMAX = 0, /* over all experts */
+  GEMM_ROUTE_SIGMOID = 1  /* each expert by itself */
+} gemm_route_score;
+
+/*
+ * Routing of tokens to experts.  With l a token's logits (tokens x experts, ld
+ * elements between rows; bf16 or fp32):
+ *
+ *     s = softmax(l) or 1 / (1 + exp(-l)),   c = s + bias   (bias: experts fp32 values)
+ *
+ * The experts form `groups` groups of neighbours; a group's score is the sum of
+ * its group_best (1 or 2) largest c, and the top_groups groups of the largest
+ * scores are kept (groups == 1: all experts).  Of their experts the top_k with the
+ * largest c are taken, in that order; without a bias (NULL) they rank by l.  What is
+ * equal ranks by lowest index, groups as well.  c and the groups' scores are
+ * compared as they are in 64 bits, so the choice is that of exact arithmetic: fp32
+ * is used only where it can tell.
+ *
+ *     ids[t][j]: the expert,   weights[t][j] = s * scale, fp32
+ *
+ * s divided by the sum of the token's top_k scores first if renormalise != 0 (0 if
+ * that sum is 0).  NaN logits count as -inf.  Softmax: where some of a row are +inf,
+ * they alone have scores, equal ones; a row that is all -inf has scores of 0.  A bias
+ * of -inf, +inf or NaN makes an expert come last.
+ *
+ * offsets and order (both or neither NULL) receive the slots t * top_k + j by expert:
+ * expert e's are order[offsets[e]] .. order[offsets[e+1] - 1], in ascending order.
+ * offsets has experts + 1 values, order tokens * top_k.
+ *
+ * At most 1024 experts, 32 groups, top_k 32 and 2^31 - 1 slots.  workspace:
+ * gemm_route_workspace() bytes of DEVICE memory, 16-byte aligned (0 bytes: NULL will
+ * do; without offsets and order none is needed), of any contents, owned by one call
+ * at a time.  Asynchronous, no allocation, deterministic.
+ */
+int gemm_route_bf16(int tokens, int experts, int top_k, const gemm_bf16_t* logits, long long ld, const float* bias,
+                    int score, int groups, int top_groups, int group_best, int renormalise, float scale, int* ids,
+                    float* weights, int* offsets, int* order, void* workspace, size_t workspace_bytes,
+                    cudaStream_t stream);
+int gemm_route_f32(int tokens, int experts, int top_k, const float* logits, long long ld, const float* bias, int score,
+                   int groups, int top_groups, int group_best, int renormalise, float scale, int* ids, float* weights,
+                   int* offsets, int* order, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace of a gemm_route_* call with offsets and order (0 on bad arguments too). */
+size_t gemm_route_workspace(int tokens, int experts);
+
+/*
+ * E4M3 codes of a rows x cols matrix X (bf16 or fp32) with one fp32 scale for each
+ * block of block_rows x 128 values: 1 row (activations) or 128 (weights).  Blocks at
+ * the edges are smaller.  With a the largest magnitude of a block:
+ *
+ *     s = a / 448, or 0 below 2^-126;   code = x * (1/s) to nearest even, at most 448
+ *
+ * (0 where s is 0), every operation rounded to fp32.  Infinities are taken as FLT_MAX
+ * in a, and stored as 448; NaN is left out of a, and stored as NaN.  codes has ldq >=
+ * cols bytes between rows, scales ceil(rows / block_rows) rows of ceil(cols / 128)
+ * values, lds elements apart; ldx, ldq, lds may be larger than the rows.
+ * Asynchronous, no allocation, deterministic.
+ */
+int gemm_fp8_quantise_bf16(int rows, int cols, const gemm_bf16_t* X, long long ldx, uint8_t* codes, long long ldq,
+                           float* scales, long long lds, int block_rows, cudaStream_t stream);
+int gemm_fp8_quantise_f32(int rows, int cols, const float* X, long long ldx, uint8_t* codes, long long ldq,
+                          float* scales, long long lds, int block_rows, cudaStream_t stream);
+
+/*
+ * Product of E4M3 matrices with a scale for each 1 x 128 block of A (a_scale: M rows
+ * of ceil(K/128), ldsa apart) and each 128 x 128 block of B (b_scale: ceil(K/128) rows
+ * of ceil(N/128), ldsb apart), as gemm_fp8_quantise_* writes them:
+ *
+ *     C = alpha * sum over blocks b of K of  a_scale[m][b] * b_scale[b][n/128] * (A_b B_b)[m][n]  +  beta * C
+ *
+ * The products of a block are exact and added in fp32, and so are the blocks' sums
+ * times their scales, at any M; C is bf16 or fp32 and rounded once.  The fast path
+ * (tcgen05 kind::f8f6f4) needs 16-byte-aligned A and B with lda and ldb multiples of
+ * 16; anything else runs a generic kernel.  Small M (a decode step) splits K over
+ * clusters.  Conventions, errors and asynchrony are those of gemm_fp8.
+ */
+int gemm_fp8_blocks(int M, int N, int K, float alpha, const uint8_t* A, int lda, const float* a_scale, int ldsa,
+                    const uint8_t* B, int ldb, const float* b_scale, int ldsb, float beta, gemm_bf16_t* C, int ldc,
+                    cudaStream_t stream);
+int gemm_fp8_blocks_f32out(int M, int N, int K, float alpha, const uint8_t* A, int lda, const float* a_scale, int ldsa,
+                           const uint8_t* B, int ldb, const float* b_scale, int ldsb, float beta, float* C, int ldc,
+                           cudaStream_t stream);
+
+/*
+ * The weights of a layer's experts as E4M3 codes: gate and up are hidden x width, down
+ * is width x hidden, each with ld_* >= its columns between rows and stride_* between
+ * experts (in elements = bytes; gate and up share theirs).  Scales: experts x
+ * ceil(rows/128) x ceil(columns/128) fp32, contiguous, a scale for each 128 x 128
+ * block.  DEVICE memory owned by the caller; the struct is read during the call only.
+ */
+typedef struct {
+  const uint8_t* gate;
+  const uint8_t* up;
+  const uint8_t* down;
+  const float* gate_scale;
+  const float* up_scale;
+  const float* down_scale;
+  long long ld_up, stride_up, ld_down, stride_down;
+  int experts, hidden, width;
+} gemm_expert_weights;
+
+/*
+ * The experts' FFN of the routed tokens.  X is tokens x hidden bf16 (ldx), O tokens x
+ * hidden bf16 (ldo); offsets, order and token_weights (tokens x top_k) as gemm_route_*
+ * writes them:
+ *
+ *     h[e] = silu(x Wgate[e]) .* (x Wup[e]),   y[e] = h[e] Wdown[e]
+ *     O[t] = sum over j of token_weights[t][j] * y[expert of slot t*top_k + j]
+ *
+ * X is quantised once in rows of 128-blocks (gemm_fp8_quantise_bf16), the products are
+ * those of gemm_fp8_blocks, h is quantised the same way from its fp32 values, each y is
+ * rounded to bf16 and the sum to bf16 once.  The fast path needs 16-byte-aligned
+ * weights with leading dimensions and strides that are multiples of 16; others run
+ * generic kernels.  At most 1024 experts.
+ *
+ * offsets must ascend from 0 to tokens * top_k and order hold every slot once.  An
+ * expert's range that does not fit the call is taken as empty and a slot number outside
+ * it is skipped, both reported by gemm_device_status(); rows of O that such slots belong
+ * to hold anything then.  O may not overlap X.  workspace: gemm_experts_workspace() bytes
+ * of DEVICE memory, 16-byte aligned, of any contents, owned by one call at a time.
+ * Asynchronous, no allocation, deterministic.  A call makes four launches; if a later
+ * one fails, the earlier ones have been queued and O is not written.
+ */
+int gemm_experts(const gemm_expert_weights* weights, int tokens, int top_k, const gemm_bf16_t* X, long long ldx,
+                 const int* offsets, const int* order, const float* token_weights, gemm_bf16_t* O, long long ldo,
+                 void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace of a gemm_experts call (0 on bad arguments). */
+size_t gemm_experts_workspace(int tokens, int top_k, int hidden, int width);
+
 /*
  * Message for the last non-OK return on the calling host thread ("" if none).
  * The string is owned by the library and valid until the next call on this
@@ -493,8 +632,8 @@ const char* gemm_get_last_error(void);
  * stream is either in the value taken or left for the next call, never lost.
  * Returns GEMM_OK, GEMM_ERR_DEVICE_TIMEOUT (a kernel gave up a bounded wait
  * and returned early; its C is unspecified), GEMM_ERR_INVALID_ARG (a paged
- * cache's kernel met a page number, length or row range that does not fit the
- * call, and skipped it), or GEMM_ERR_CUDA if the launch
+ * cache's kernel met a page number, length or row range, or gemm_experts a range or
+ * number of slots, that does not fit the call, and skipped it), or GEMM_ERR_CUDA if the launch
  * or synchronisation itself failed.  If `where` is not NULL it receives the
  * kernel-specific location code of the first failure (0 if none).  The
  * `where` argument is this library's addition to the surveyed
@@ -522,7 +661,11 @@ typedef enum {
                              one-block-per-row fallback reports GEMM_PATH_GENERIC) */
   GEMM_PATH_KV = 8,       /* paged cache, fast append or attention kernel (reported only; the
                              fallbacks report GEMM_PATH_GENERIC) */
-  GEMM_PATH_SAMPLE = 9    /* sampling (reported only) */
+  GEMM_PATH_SAMPLE = 9,   /* sampling (reported only) */
+  GEMM_PATH_BLOCKS = 10,  /* block-scaled E4M3 products and experts, tcgen05 kernel (reported
+                             only; the fallback reports GEMM_PATH_GENERIC) */
+  GEMM_PATH_ROUTE = 11,   /* routing to experts (reported only) */
+  GEMM_PATH_QUANTISE = 12 /* E4M3 codes with block scales (reported only) */
 } gemm_path;
 
 /*

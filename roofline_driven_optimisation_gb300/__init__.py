@@ -32,20 +32,24 @@ GEMM_ERR_CUDA = 4
 GEMM_ERR_DEVICE_TIMEOUT = 5
 
 PATH_AUTO, PATH_GENERIC, PATH_F32_SIMT, PATH_BF16_TC, PATH_SKINNY, PATH_INT4, PATH_W4, PATH_ATTN, \
-    PATH_KV, PATH_SAMPLE = range(10)
+    PATH_KV, PATH_SAMPLE, PATH_BLOCKS, PATH_ROUTE, PATH_QUANTISE = range(13)
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = range(4)
 FP8_E4M3, FP8_E5M2 = 0, 1
 KV_E4M3, KV_INT8 = 0, 1
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
 PATH_NAMES = {PATH_AUTO: "none", PATH_GENERIC: "generic", PATH_F32_SIMT: "f32_simt",
               PATH_BF16_TC: "bf16_tc", PATH_SKINNY: "skinny", PATH_INT4: "int4", PATH_W4: "w4",
-              PATH_ATTN: "attention", PATH_KV: "kv", PATH_SAMPLE: "sample"}
+              PATH_ATTN: "attention", PATH_KV: "kv", PATH_SAMPLE: "sample",
+              PATH_BLOCKS: "blocks", PATH_ROUTE: "route", PATH_QUANTISE: "quantise"}
 
 # every symbol the public header declares
 EXPORTS = ("gemm_f32", "gemm_f32_noalloc", "gemm_bf16", "gemm_bf16_f32out", "gemm_f32_ex", "gemm_bf16_ex",
            "gemm_bf16_f32out_ex", "gemm_bf16_swiglu", "gemm_fp8", "gemm_fp8_f32out",
            "gemm_int4_dequant", "gemm_int4_dequant_f32", "gemm_w4a16", "gemm_w4a16_f32out",
            "gemm_int4_repack", "gemm_w4_packed_bytes", "gemm_attention", "gemm_kv_append", "gemm_kv_attention",
-           "gemm_kv_attention_workspace", "gemm_sample_bf16", "gemm_sample_f32", "gemm_get_last_error",
+           "gemm_kv_attention_workspace", "gemm_sample_bf16", "gemm_sample_f32", "gemm_route_bf16", "gemm_route_f32",
+           "gemm_route_workspace", "gemm_fp8_quantise_bf16", "gemm_fp8_quantise_f32", "gemm_fp8_blocks",
+           "gemm_fp8_blocks_f32out", "gemm_experts", "gemm_experts_workspace", "gemm_get_last_error",
            "gemm_device_status", "gemm_force_path", "gemm_last_path", "gemm_force_tile_n",
            "gemm_last_tile_n", "gemm_force_tc_pair", "gemm_last_tc_pair", "gemm_force_split_tiles",
            "gemm_last_k_split", "gemm_set_wait_timeout_ns",
@@ -64,6 +68,13 @@ class KVCacheStruct(ctypes.Structure):
                 ("format", ctypes.c_int), ("pages", ctypes.c_int), ("page_tokens", ctypes.c_int),
                 ("heads", ctypes.c_int), ("dim", ctypes.c_int), ("seqs", ctypes.c_int),
                 ("table_cols", ctypes.c_int)]
+
+
+class ExpertWeightsStruct(ctypes.Structure):
+    """gemm_expert_weights of the C ABI."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "up", "down", "gate_scale", "up_scale", "down_scale")] + \
+        [(n, ctypes.c_longlong) for n in ("ld_up", "stride_up", "ld_down", "stride_down")] + \
+        [(n, ctypes.c_int) for n in ("experts", "hidden", "width")]
 
 
 class GemmError(RuntimeError):
@@ -126,6 +137,24 @@ def load(path: str | None = None):
             fn = getattr(lib, name)
             fn.argtypes = [i, i, vp, ll, vp, vp, vp, vp, vp, vp, vp, vp]
             fn.restype = i
+        for name in ("gemm_route_bf16", "gemm_route_f32"):
+            fn = getattr(lib, name)
+            fn.argtypes = [i, i, i, vp, ll, vp, i, i, i, i, i, f, vp, vp, vp, vp, vp, sz, vp]
+            fn.restype = i
+        lib.gemm_route_workspace.argtypes = [i, i]
+        lib.gemm_route_workspace.restype = sz
+        for name in ("gemm_fp8_quantise_bf16", "gemm_fp8_quantise_f32"):
+            fn = getattr(lib, name)
+            fn.argtypes = [i, i, vp, ll, vp, ll, vp, ll, i, vp]
+            fn.restype = i
+        for name in ("gemm_fp8_blocks", "gemm_fp8_blocks_f32out"):
+            fn = getattr(lib, name)
+            fn.argtypes = [i, i, i, f, vp, i, vp, i, vp, i, vp, i, f, vp, i, vp]
+            fn.restype = i
+        lib.gemm_experts.argtypes = [vp, i, i, vp, ll, vp, vp, vp, vp, ll, vp, sz, vp]
+        lib.gemm_experts.restype = i
+        lib.gemm_experts_workspace.argtypes = [i, i, i, i]
+        lib.gemm_experts_workspace.restype = sz
         lib.gemm_w4_packed_bytes.argtypes = [i, i]
         lib.gemm_w4_packed_bytes.restype = ctypes.c_size_t
         for name in ("gemm_fp8", "gemm_fp8_f32out"):
@@ -266,6 +295,50 @@ def gemm_sample_bf16(rows, vocab, logits, ld, temperature, top_k, top_p, min_p, 
 def gemm_sample_f32(rows, vocab, logits, ld, temperature, top_k, top_p, min_p, u, token, logprob, stream=0):
     _check(load().gemm_sample_f32(rows, vocab, logits, ld, temperature, top_k, top_p, min_p, u, token, logprob,
                                   stream))
+
+
+def gemm_route_bf16(tokens, experts, top_k, logits, ld, bias, score, groups, top_groups, group_best, renormalise, scale,
+                    ids, weights, offsets, order, workspace, workspace_bytes, stream=0):
+    _check(load().gemm_route_bf16(tokens, experts, top_k, logits, ld, bias, score, groups, top_groups, group_best,
+                                  renormalise, scale, ids, weights, offsets, order, workspace, workspace_bytes, stream))
+
+
+def gemm_route_f32(tokens, experts, top_k, logits, ld, bias, score, groups, top_groups, group_best, renormalise, scale,
+                   ids, weights, offsets, order, workspace, workspace_bytes, stream=0):
+    _check(load().gemm_route_f32(tokens, experts, top_k, logits, ld, bias, score, groups, top_groups, group_best,
+                                 renormalise, scale, ids, weights, offsets, order, workspace, workspace_bytes, stream))
+
+
+def gemm_route_workspace(tokens, experts) -> int:
+    return int(load().gemm_route_workspace(tokens, experts))
+
+
+def gemm_fp8_quantise_bf16(rows, cols, X, ldx, codes, ldq, scales, lds, block_rows, stream=0):
+    _check(load().gemm_fp8_quantise_bf16(rows, cols, X, ldx, codes, ldq, scales, lds, block_rows, stream))
+
+
+def gemm_fp8_quantise_f32(rows, cols, X, ldx, codes, ldq, scales, lds, block_rows, stream=0):
+    _check(load().gemm_fp8_quantise_f32(rows, cols, X, ldx, codes, ldq, scales, lds, block_rows, stream))
+
+
+def gemm_fp8_blocks(M, N, K, alpha, A, lda, a_scale, ldsa, B, ldb, b_scale, ldsb, beta, C, ldc, stream=0):
+    _check(load().gemm_fp8_blocks(M, N, K, alpha, A, lda, a_scale, ldsa, B, ldb, b_scale, ldsb, beta, C, ldc, stream))
+
+
+def gemm_fp8_blocks_f32out(M, N, K, alpha, A, lda, a_scale, ldsa, B, ldb, b_scale, ldsb, beta, C, ldc, stream=0):
+    _check(load().gemm_fp8_blocks_f32out(M, N, K, alpha, A, lda, a_scale, ldsa, B, ldb, b_scale, ldsb, beta, C, ldc,
+                                         stream))
+
+
+def gemm_experts(weights, tokens, top_k, X, ldx, offsets, order, token_weights, O, ldo, workspace, workspace_bytes,
+                 stream=0):
+    """`weights`: an ExpertWeightsStruct."""
+    _check(load().gemm_experts(ctypes.addressof(weights), tokens, top_k, X, ldx, offsets, order, token_weights, O, ldo,
+                               workspace, workspace_bytes, stream))
+
+
+def gemm_experts_workspace(tokens, top_k, hidden, width) -> int:
+    return int(load().gemm_experts_workspace(tokens, top_k, hidden, width))
 
 
 def device_status(stream=0) -> tuple[int, int]:
@@ -686,3 +759,196 @@ def sample(logits, u, token, logprob=None, temperature=None, top_k=None, top_p=N
     if rc:
         _check(rc)
     return token
+
+
+# ------------------------------------------------------------------ routed experts
+def _scratch(nbytes: int, device, stream: int):
+    """Memory for one call on `stream`, of any contents: the allocator gives it out again
+    only behind the call, and a captured call's is its graph's."""
+    if stream == _raw_stream(device.index):
+        return _t.empty((nbytes,), dtype=_t.uint8, device=device)
+    with _t.cuda.stream(_t.cuda.ExternalStream(stream, device=device)):
+        return _t.empty((nbytes,), dtype=_t.uint8, device=device)
+
+
+def _codes(t, name: str):
+    """A 2-D CUDA tensor of E4M3 codes (float8_e4m3fn or uint8), rows apart from each other."""
+    if t.dtype is not _t.float8_e4m3fn and t.dtype is not _t.uint8 or not t.is_cuda:
+        raise TypeError(f"{name} is a CUDA tensor of E4M3 codes (float8_e4m3fn or uint8)")
+    return _ld(t)
+
+
+def _scales(t, name: str, rows: int, cols: int) -> int:
+    if t.dtype is not _f32 or not t.is_cuda or t.shape != (rows, cols):
+        raise TypeError(f"{name} is a fp32 CUDA tensor {(rows, cols)}")
+    return _ld(t)
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def _one_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("the tensors of a call are on one device")
+    return first.device.index
+
+
+def route(logits, ids, weights, offsets=None, order=None, bias=None, score: int = ROUTE_SOFTMAX, groups: int = 1,
+          top_groups: int = 1, group_best: int = 2, renormalise: bool = True, scale: float = 1.0, workspace=None,
+          stream=None):
+    """The top_k experts of each row of logits ([tokens][experts], bf16 or fp32): ids
+    (int32) and weights (fp32), both [tokens][top_k] and contiguous.  offsets
+    ([experts + 1]) and order ([tokens * top_k], int32) receive the slots t * top_k + j
+    by expert.  bias: [experts] fp32, added to the scores (ROUTE_SOFTMAX or
+    ROUTE_SIGMOID) for the choice alone.  workspace: uint8, gemm_route_workspace()
+    bytes, or None for memory of this call's own.  Argument marshalling only."""
+    if _t is None:
+        _torch()
+    tokens, experts = logits.shape
+    top_k = ids.shape[-1]
+    lib = _lib or load()
+    if not logits.is_cuda:
+        raise ValueError("route() takes CUDA tensors")
+    if logits.dtype is _bf16:
+        fn = lib.gemm_route_bf16
+    elif logits.dtype is _f32:
+        fn = lib.gemm_route_f32
+    else:
+        raise TypeError(f"unsupported logits dtype {logits.dtype}")
+    for t, name, dtype in ((ids, "ids", _i32), (weights, "weights", _f32)):
+        if t.dtype is not dtype or not t.is_cuda or t.shape != (tokens, top_k) or not t.is_contiguous():
+            raise TypeError(f"{name} is a contiguous {dtype} CUDA tensor {(tokens, top_k)}")
+    index = _one_device(logits, ids, weights, offsets, order, bias, workspace)
+    st = _raw_stream(index) if stream is None else stream
+    if workspace is None and order is not None:
+        need = lib.gemm_route_workspace(tokens, experts)
+        workspace = _scratch(need, logits.device, st) if need else None
+    rc = fn(tokens, experts, top_k, logits.data_ptr(), _ld(logits),
+            None if bias is None else _values(bias, "bias", experts, _f32), score, groups, top_groups, group_best,
+            renormalise, scale, ids.data_ptr(), weights.data_ptr(),
+            None if offsets is None else _values(offsets, "offsets", experts + 1, _i32),
+            None if order is None else _values(order, "order", tokens * top_k, _i32),
+            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), st)
+    if rc:
+        _check(rc)
+    return ids, weights
+
+
+def fp8_quantise(X, codes, scales, block_rows: int = 1, stream=None):
+    """E4M3 codes of X ([rows][cols], bf16 or fp32; codes: float8_e4m3fn or uint8 of its
+    shape) with a scale for each block of block_rows (1: activations, 128: weights) x
+    128 values (scales: fp32).  Argument marshalling only."""
+    if _t is None:
+        _torch()
+    rows, cols = X.shape
+    if X.dtype is not _bf16 and X.dtype is not _f32 or not X.is_cuda:
+        raise TypeError("X is a bf16 or fp32 CUDA tensor")
+    if codes.shape != X.shape:
+        raise ValueError(f"codes have shape {tuple(codes.shape)}, not {(rows, cols)}")
+    if block_rows not in (1, 128):
+        raise ValueError(f"blocks of {block_rows} x 128: 1 and 128 rows are there")
+    lib = _lib or load()
+    fn = lib.gemm_fp8_quantise_bf16 if X.dtype is _bf16 else lib.gemm_fp8_quantise_f32
+    rc = fn(rows, cols, X.data_ptr(), _ld(X), codes.data_ptr(), _codes(codes, "codes"), scales.data_ptr(),
+            _scales(scales, "scales", -(-rows // block_rows), _blocks(cols)), block_rows,
+            _raw_stream(_one_device(X, codes, scales)) if stream is None else stream)
+    if rc:
+        _check(rc)
+    return codes, scales
+
+
+def fp8_blocks(A, a_scale, B, b_scale, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
+    """C = alpha * A@B + beta * C for E4M3 codes A ([M][K]) and B ([K][N]) with a scale for
+    each 1 x 128 block of A and each 128 x 128 block of B, as fp8_quantise makes them; C
+    bf16 or fp32.  Argument marshalling only."""
+    if _t is None:
+        _torch()
+    M, K = A.shape
+    K2, N = B.shape
+    if K2 != K or C.shape != (M, N):
+        raise ValueError(f"shape mismatch {tuple(A.shape)} @ {tuple(B.shape)} -> {tuple(C.shape)}")
+    lib = _lib or load()
+    if C.dtype is _bf16:
+        fn = lib.gemm_fp8_blocks
+    elif C.dtype is _f32:
+        fn = lib.gemm_fp8_blocks_f32out
+    else:
+        raise TypeError(f"unsupported output dtype {C.dtype}")
+    index = _one_device(C, A, a_scale, B, b_scale)
+    if index is None:
+        raise ValueError("fp8_blocks() takes CUDA tensors")
+    rc = fn(M, N, K, alpha, A.data_ptr(), _codes(A, "A"), a_scale.data_ptr(), _scales(a_scale, "a_scale", M, _blocks(K)),
+            B.data_ptr(), _codes(B, "B"), b_scale.data_ptr(), _scales(b_scale, "b_scale", _blocks(K), _blocks(N)), beta,
+            C.data_ptr(), _ld(C), _raw_stream(index) if stream is None else stream)
+    if rc:
+        _check(rc)
+    return C
+
+
+class ExpertWeights:
+    """A layer's experts as E4M3 codes (gemm_expert_weights): gate and up
+    [experts][hidden][width], down [experts][width][hidden] (float8_e4m3fn or uint8,
+    columns contiguous, gate and up of one set of strides), scales fp32
+    [experts][ceil(rows/128)][ceil(columns/128)], contiguous.  The tensors are the
+    caller's and are used in place."""
+
+    def __init__(self, gate, gate_scale, up, up_scale, down, down_scale):
+        if _t is None:
+            _torch()
+        for t, name in ((gate, "gate"), (up, "up"), (down, "down")):
+            if t.dim() != 3 or t.dtype not in (_t.float8_e4m3fn, _t.uint8) or t.shape[2] > 1 and t.stride(2) != 1:
+                raise TypeError(f"{name}: 3-D tensor of E4M3 codes (float8_e4m3fn or uint8) with contiguous columns")
+        experts, hidden, width = gate.shape
+        if up.shape != gate.shape or up.stride() != gate.stride() or down.shape != (experts, width, hidden):
+            raise ValueError("gate and up have one shape and one set of strides, down the transposed shape")
+        for t in (gate, down):
+            rows, cols = t.shape[1:]
+            if rows > 1 and t.stride(1) < cols or experts > 1 and t.stride(0) < (rows - 1) * t.stride(1) + cols:
+                raise ValueError("rows or experts overlap (an expanded tensor?)")
+        for t, s in ((gate, gate_scale), (up, up_scale), (down, down_scale)):
+            if s.dtype is not _f32 or s.shape != (experts, _blocks(t.shape[1]), _blocks(t.shape[2])) or \
+                    not s.is_contiguous():
+                raise TypeError("scales are contiguous fp32 [experts][ceil(rows/128)][ceil(columns/128)]")
+        if not all(t.is_cuda and t.device == gate.device for t in (gate, up, down, gate_scale, up_scale, down_scale)):
+            raise ValueError("ExpertWeights takes CUDA tensors of one device")
+        self.tensors = (gate, gate_scale, up, up_scale, down, down_scale)
+        self.experts, self.hidden, self.width, self.device = experts, hidden, width, gate.device
+        self.struct = ExpertWeightsStruct(
+            gate.data_ptr(), up.data_ptr(), down.data_ptr(), gate_scale.data_ptr(), up_scale.data_ptr(),
+            down_scale.data_ptr(), max(gate.stride(1), width), max(gate.stride(0), 0), max(down.stride(1), hidden),
+            max(down.stride(0), 0), experts, hidden, width)
+        self.address, self.index = ctypes.addressof(self.struct), gate.device.index
+
+
+def experts(weights: ExpertWeights, X, offsets, order, token_weights, O, workspace=None, stream=None):
+    """O = the weighted sum of each token's experts: X and O [tokens][hidden] bf16; offsets,
+    order and token_weights ([tokens][top_k]) as route() makes them.  workspace: uint8,
+    gemm_experts_workspace() bytes, or None for memory of this call's own.  Argument
+    marshalling only."""
+    if _t is None:
+        _torch()
+    tokens, hidden = X.shape
+    for t, name in ((X, "X"), (O, "O")):
+        if t.dtype is not _bf16 or not t.is_cuda:
+            raise TypeError(f"{name} is a bf16 CUDA tensor")
+        if t.shape != (tokens, weights.hidden):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {(tokens, weights.hidden)}")
+    if token_weights.dim() != 2 or token_weights.shape[0] != tokens or token_weights.dtype is not _f32 or \
+            not token_weights.is_cuda or not token_weights.is_contiguous():
+        raise TypeError("token_weights is a contiguous fp32 CUDA tensor [tokens][top_k]")
+    top_k = token_weights.shape[1]
+    if _one_device(X, O, offsets, order, token_weights, workspace) != weights.index:
+        raise ValueError("the tensors of a call are on one device")
+    st = _raw_stream(weights.index) if stream is None else stream
+    lib = _lib or load()
+    if workspace is None and tokens:
+        workspace = _scratch(lib.gemm_experts_workspace(tokens, top_k, hidden, weights.width), X.device, st)
+    rc = lib.gemm_experts(
+        weights.address, tokens, top_k, X.data_ptr(), _ld(X), _values(offsets, "offsets", weights.experts + 1, _i32),
+        _values(order, "order", tokens * top_k, _i32), token_weights.data_ptr(), O.data_ptr(), _ld(O),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), st)
+    if rc:
+        _check(rc)
+    return O

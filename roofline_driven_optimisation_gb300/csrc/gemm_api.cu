@@ -23,6 +23,7 @@
 
 #include "gb300gemm.h"
 #include "internal.h"
+#include "plan.h"
 #include "ptx.cuh"
 
 namespace g3 {
@@ -874,6 +875,282 @@ int sample(int rows, int vocab, const void* logits, bool bf16, long long ld, con
   return GEMM_OK;
 }
 
+// ---------------------------------------------------------------- routed experts
+int route(int tokens, int experts, int top_k, const void* logits, bool bf16, long long ld, const float* bias, int score,
+          int groups, int top_groups, int group_best, int renormalise, float scale, int* ids, float* weights,
+          int* offsets, int* order, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  t_msg[0] = '\0';
+  t_last_path = GEMM_PATH_AUTO;
+  t_last_k_split = 1;
+  if (tokens < 0 || experts < 1 || top_k < 1)
+    return fail(GEMM_ERR_INVALID_ARG, "bad sizes tokens=%d experts=%d top_k=%d", tokens, experts, top_k);
+  if (experts > kRouteMaxExperts) return fail(GEMM_ERR_UNSUPPORTED, "%d experts: %d at most", experts, kRouteMaxExperts);
+  if (top_k > kRouteMaxTopK) return fail(GEMM_ERR_UNSUPPORTED, "top_k %d: %d at most", top_k, kRouteMaxTopK);
+  if (score != GEMM_ROUTE_SOFTMAX && score != GEMM_ROUTE_SIGMOID)
+    return fail(GEMM_ERR_INVALID_ARG, "unknown score %d", score);
+  if (groups < 1 || top_groups < 1 || top_groups > groups || experts % groups != 0)
+    return fail(GEMM_ERR_INVALID_ARG, "%d experts in %d groups of which %d are kept", experts, groups, top_groups);
+  if (groups > kRouteMaxGroups) return fail(GEMM_ERR_UNSUPPORTED, "%d groups: %d at most", groups, kRouteMaxGroups);
+  if (group_best != 1 && group_best != 2)
+    return fail(GEMM_ERR_INVALID_ARG, "a group's score is the sum of its 1 or 2 best, not of %d", group_best);
+  if (top_k > experts / groups * top_groups)
+    return fail(GEMM_ERR_INVALID_ARG, "top_k %d of %d experts in the kept groups", top_k, experts / groups * top_groups);
+  if (!std::isfinite(scale)) return fail(GEMM_ERR_INVALID_ARG, "bad scale");
+  if (ld < experts) return fail(GEMM_ERR_INVALID_ARG, "leading dimension too small (ld=%lld, experts=%d)", ld, experts);
+  if (tokens > 0 && (offsets == nullptr) != (order == nullptr))     // without a token order has no element
+    return fail(GEMM_ERR_INVALID_ARG, "offsets and order come together");
+  if ((long long)tokens * top_k > 0x7fffffffll)
+    return fail(GEMM_ERR_UNSUPPORTED, "%d tokens of %d slots: more than 2^31 - 1", tokens, top_k);
+  if (!(bf16 ? aligned2(logits) : aligned4(logits)) || !aligned4(bias) || !aligned4(ids) || !aligned4(weights) ||
+      !aligned4(offsets) || !aligned4(order))
+    return fail(GEMM_ERR_MISALIGNED, "a pointer is not aligned to its element size");
+  if (tokens == 0 && offsets == nullptr) return GEMM_OK;
+  if (tokens > 0 && (logits == nullptr || ids == nullptr || weights == nullptr))
+    return fail(GEMM_ERR_INVALID_ARG, "logits, ids or weights is NULL");
+  const size_t need = offsets != nullptr ? route_ws_bytes(tokens, experts) : 0;
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(GEMM_ERR_INVALID_ARG, "workspace of %zu bytes: %zu are needed", workspace ? workspace_bytes : 0, need);
+    if (!aligned16(workspace)) return fail(GEMM_ERR_MISALIGNED, "workspace is not aligned to 16 bytes");
+  }
+  DeviceInfo* dev = nullptr;
+  const int rc = device_info(&dev);
+  if (rc != GEMM_OK) return rc;
+  RouteArgs a;
+  a.tokens = tokens; a.experts = experts; a.top_k = top_k;
+  a.logits = logits; a.ld = ld; a.bf16 = bf16;
+  a.softmax = score == GEMM_ROUTE_SOFTMAX;
+  a.renormalise = renormalise != 0;
+  a.groups = groups; a.top_groups = top_groups; a.group_best = group_best;
+  a.scale = scale; a.bias = bias;
+  a.ids = ids; a.weights = weights; a.offsets = offsets; a.order = order;
+  a.counts = static_cast<int*>(workspace);
+  a.choices = bias != nullptr || groups > 1;
+  a.vec = aligned16(logits) && ((size_t)ld * (bf16 ? 2 : 4)) % 16 == 0;
+  const int err = launch_route(a, stream);
+  if (err != cudaSuccess)
+    return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
+  t_last_path = GEMM_PATH_ROUTE;
+  return GEMM_OK;
+}
+
+int fp8_quantise(int rows, int cols, const void* X, bool bf16, long long ldx, uint8_t* codes, long long ldq, float* scales,
+                 long long lds, int block_rows, cudaStream_t stream) {
+  t_msg[0] = '\0';
+  t_last_path = GEMM_PATH_AUTO;
+  t_last_k_split = 1;
+  if (rows < 0 || cols < 0) return fail(GEMM_ERR_INVALID_ARG, "negative size rows=%d cols=%d", rows, cols);
+  if (block_rows != 1 && block_rows != kBlocksK)
+    return fail(GEMM_ERR_INVALID_ARG, "blocks of %d x 128: 1 and 128 rows are there", block_rows);
+  const int blocks = cols / kBlocksK + (cols % kBlocksK != 0);
+  if (ldx < cols || ldq < cols || lds < blocks)
+    return fail(GEMM_ERR_INVALID_ARG, "leading dimension too small (ldx=%lld ldq=%lld lds=%lld)", ldx, ldq, lds);
+  if (rows == 0 || cols == 0) return GEMM_OK;
+  if (X == nullptr || codes == nullptr || scales == nullptr)
+    return fail(GEMM_ERR_INVALID_ARG, "X, codes or scales is NULL");
+  if (!(bf16 ? aligned2(X) : aligned4(X)) || !aligned4(scales))
+    return fail(GEMM_ERR_MISALIGNED, "a pointer is not aligned to its element size");
+  DeviceInfo* dev = nullptr;
+  const int rc = device_info(&dev);
+  if (rc != GEMM_OK) return rc;
+  QuantiseArgs a;
+  a.rows = rows; a.cols = cols; a.x = X; a.ldx = ldx; a.bf16 = bf16;
+  a.codes = codes; a.ldq = ldq; a.scales = scales; a.lds = lds; a.block_rows = block_rows;
+  a.vec_x = aligned16(X) && ((size_t)ldx * (bf16 ? 2 : 4)) % 16 == 0;
+  a.vec_q = (reinterpret_cast<uintptr_t>(codes) & 7u) == 0 && ldq % 8 == 0;
+  const int err = launch_fp8_quantise(a, dev->num_sms, stream);
+  if (err != cudaSuccess)
+    return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
+  t_last_path = GEMM_PATH_QUANTISE;
+  return GEMM_OK;
+}
+
+// Launches one block-scaled product, on the tcgen05 kernel where `fast`.
+int blocks_product(BlocksArgs& a, bool fast, DeviceInfo* dev, cudaStream_t stream) {
+  a.status = dev->status;
+  a.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
+  a.stall = t_stall;
+  int err;
+  if (fast) {
+    BlocksPlan plan;
+    const int kblocks = (a.K + kBlocksK - 1) / kBlocksK, tiles_n = (a.N + kBlocksN - 1) / kBlocksN;
+    const plan::BlocksChoice c = plan::blocks_choice(a.rows, a.offsets != nullptr ? a.experts : 1, tiles_n, kblocks,
+                                                     a.B2 != nullptr, dev->num_sms);
+    plan.nt = c.nt;
+    plan.split = c.split;
+    const bool gather = a.gather != 0;
+    const CUtensorMap *mA = nullptr, *mB = nullptr, *mB2 = nullptr;
+    int rc;
+    if ((rc = make_map(a.A, a.K, a.a_rows, (uint64_t)a.lda, kBlocksK, blocks_box_rows(plan.nt, gather),
+                       CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, &mA)) != GEMM_OK)
+      return rc;
+    for (int i = 0; i < (a.B2 != nullptr ? 2 : 1); ++i)
+      if ((rc = make_map_3d(i ? a.B2 : a.B, a.N, a.K, a.experts, (uint64_t)a.ldb, (uint64_t)a.b_stride, kBlocksN, kBlocksK,
+                            CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, i ? &mB2 : &mB)) != GEMM_OK)
+        return rc;
+    err = launch_blocks(a, plan, mA, mB, mB2, dev->num_sms, stream);
+    t_last_k_split = plan.split;
+  } else {
+    err = launch_blocks_generic(a, dev->num_sms, stream);
+  }
+  if (err != cudaSuccess)
+    return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
+  return GEMM_OK;
+}
+
+// What a tensor map asks of a matrix of bytes
+bool map_ok(const void* p, long long ld) { return aligned16(p) && ld % 16 == 0 && ld < (1ll << 40); }
+
+int fp8_blocks(int M, int N, int K, float alpha, const uint8_t* A, int lda, const float* a_scale, int ldsa,
+               const uint8_t* B, int ldb, const float* b_scale, int ldsb, float beta, void* C, int ldc, bool out_bf16,
+               cudaStream_t stream) {
+  trim_maps();
+  t_msg[0] = '\0';
+  t_last_path = GEMM_PATH_AUTO;
+  t_last_k_split = 1;
+  if (M < 0 || N < 0 || K < 0) return fail(GEMM_ERR_INVALID_ARG, "negative size M=%d N=%d K=%d", M, N, K);
+  const int kblocks = K / kBlocksK + (K % kBlocksK != 0), nblocks = N / kBlocksN + (N % kBlocksN != 0);
+  if (lda < (K > 1 ? K : 1) || ldb < (N > 1 ? N : 1) || ldc < (N > 1 ? N : 1) || ldsa < kblocks || ldsb < nblocks)
+    return fail(GEMM_ERR_INVALID_ARG, "leading dimension too small (lda=%d ldb=%d ldc=%d, scales %d %d)", lda, ldb, ldc,
+                ldsa, ldsb);
+  if (M == 0 || N == 0) return GEMM_OK;
+  if (C == nullptr) return fail(GEMM_ERR_INVALID_ARG, "C is NULL");
+  if (K > 0 && (A == nullptr || B == nullptr || a_scale == nullptr || b_scale == nullptr))
+    return fail(GEMM_ERR_INVALID_ARG, "A, B or a scale is NULL");
+  if (!aligned4(a_scale) || !aligned4(b_scale) || !(out_bf16 ? aligned2(C) : aligned4(C)))
+    return fail(GEMM_ERR_MISALIGNED, "a pointer is not aligned to its element size");
+  const int forced = t_forced_path;
+  const bool can = K > 0 && map_ok(A, lda) && map_ok(B, ldb);
+  if ((forced != GEMM_PATH_AUTO && forced != GEMM_PATH_GENERIC && forced != GEMM_PATH_BF16_TC) ||
+      (forced == GEMM_PATH_BF16_TC && !can))
+    return fail(GEMM_ERR_UNSUPPORTED, "forced path %d cannot run this call", forced);
+  const bool fast = can && forced != GEMM_PATH_GENERIC;
+  DeviceInfo* dev = nullptr;
+  int rc = device_info(&dev);
+  if (rc != GEMM_OK) return rc;
+  BlocksArgs a{};
+  a.experts = 1; a.rows = M; a.N = N; a.K = K;
+  a.A = A; a.lda = lda; a.a_rows = M; a.sa = a_scale; a.ldsa = ldsa;
+  a.B = B; a.ldb = ldb; a.b_stride = (long long)ldb * (K > 0 ? K : 1); a.sb = b_scale; a.ldsb = ldsb;
+  a.C = C; a.ldc = ldc; a.out_bf16 = out_bf16; a.alpha = alpha; a.beta = beta;
+  if ((rc = blocks_product(a, fast, dev, stream)) != GEMM_OK) return rc;
+  t_last_path = fast ? GEMM_PATH_BLOCKS : GEMM_PATH_GENERIC;
+  return GEMM_OK;
+}
+
+// Where the parts of an experts call's workspace begin, and how large it is.
+struct ExpertsWorkspace {
+  size_t xq, xs, hq, hs, y, bytes;
+  long long ldx, ldxs, ldh, ldhs, ldy;   // codes and y in elements: rows of whole 16-byte vectors
+};
+ExpertsWorkspace experts_ws(int tokens, int top_k, int hidden, int width) {
+  auto up = [](size_t v, size_t to) { return (v + to - 1) / to * to; };
+  const size_t slots = (size_t)tokens * top_k;
+  ExpertsWorkspace w;
+  w.ldx = (long long)up(hidden, 16);
+  w.ldxs = (hidden + kBlocksK - 1) / kBlocksK;
+  w.ldh = (long long)up(width, 16);
+  w.ldhs = (width + kBlocksK - 1) / kBlocksK;
+  w.ldy = (long long)up(hidden, 8);
+  w.xq = 0;
+  w.xs = up(w.xq + (size_t)tokens * w.ldx, 256);
+  w.hq = up(w.xs + (size_t)tokens * w.ldxs * 4, 256);
+  w.hs = up(w.hq + slots * w.ldh, 256);
+  w.y = up(w.hs + slots * w.ldhs * 4, 256);
+  w.bytes = up(w.y + slots * w.ldy * 2, 256);
+  return w;
+}
+
+size_t experts_workspace(int tokens, int top_k, int hidden, int width) {
+  if (tokens < 0 || top_k < 1 || hidden < 1 || width < 1 || (long long)tokens * top_k > 0x7fffffffll) return 0;
+  return experts_ws(tokens, top_k, hidden, width).bytes;
+}
+
+int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, long long ldx, const int* offsets,
+            const int* order, const float* weights, void* O, long long ldo, void* workspace, size_t workspace_bytes,
+            cudaStream_t stream) {
+  trim_maps();
+  t_msg[0] = '\0';
+  t_last_path = GEMM_PATH_AUTO;
+  t_last_k_split = 1;
+  if (w == nullptr) return fail(GEMM_ERR_INVALID_ARG, "the weights are NULL");
+  const int E = w->experts, H = w->hidden, F = w->width;
+  if (tokens < 0 || top_k < 1 || E < 1 || H < 1 || F < 1)
+    return fail(GEMM_ERR_INVALID_ARG, "bad sizes tokens=%d top_k=%d experts=%d hidden=%d width=%d", tokens, top_k, E, H, F);
+  if (E > kBlocksMaxExperts) return fail(GEMM_ERR_UNSUPPORTED, "%d experts: %d at most", E, kBlocksMaxExperts);
+  if ((long long)tokens * top_k > 0x7fffffffll)
+    return fail(GEMM_ERR_UNSUPPORTED, "%d tokens of %d slots: more than 2^31 - 1", tokens, top_k);
+  if (H > 0x7fffffff - 127 || F > 0x7fffffff - 127)
+    return fail(GEMM_ERR_UNSUPPORTED, "hidden %d or width %d too large", H, F);
+  if (w->ld_up < F || w->ld_down < H || w->stride_up < 0 || w->stride_down < 0 || ldx < H || ldo < H)
+    return fail(GEMM_ERR_INVALID_ARG, "leading dimension too small (weights %lld %lld, ldx=%lld ldo=%lld)", w->ld_up,
+                w->ld_down, ldx, ldo);
+  if (E > 1 && (w->stride_up < (long long)(H - 1) * w->ld_up + F || w->stride_down < (long long)(F - 1) * w->ld_down + H))
+    return fail(GEMM_ERR_INVALID_ARG, "experts' matrices overlap (strides %lld and %lld)", w->stride_up, w->stride_down);
+  if (tokens == 0) return GEMM_OK;
+  if (w->gate == nullptr || w->up == nullptr || w->down == nullptr || w->gate_scale == nullptr ||
+      w->up_scale == nullptr || w->down_scale == nullptr)
+    return fail(GEMM_ERR_INVALID_ARG, "a weight or its scale is NULL");
+  if (X == nullptr || offsets == nullptr || order == nullptr || weights == nullptr || O == nullptr)
+    return fail(GEMM_ERR_INVALID_ARG, "X, offsets, order, weights or O is NULL");
+  if (!aligned4(w->gate_scale) || !aligned4(w->up_scale) || !aligned4(w->down_scale) || !aligned2(X) || !aligned2(O) ||
+      !aligned4(offsets) || !aligned4(order) || !aligned4(weights))
+    return fail(GEMM_ERR_MISALIGNED, "a pointer is not aligned to its element size");
+  const ExpertsWorkspace ws = experts_ws(tokens, top_k, H, F);
+  if (workspace == nullptr || workspace_bytes < ws.bytes)
+    return fail(GEMM_ERR_INVALID_ARG, "workspace of %zu bytes: %zu are needed", workspace ? workspace_bytes : 0, ws.bytes);
+  if (!aligned16(workspace)) return fail(GEMM_ERR_MISALIGNED, "workspace is not aligned to 16 bytes");
+  DeviceInfo* dev = nullptr;
+  int rc = device_info(&dev);
+  if (rc != GEMM_OK) return rc;
+  // a stride that nothing steps over may hold anything
+  const long long su = E > 1 ? w->stride_up : w->ld_up * H, sd = E > 1 ? w->stride_down : w->ld_down * F;
+  const bool fast = map_ok(w->gate, w->ld_up) && map_ok(w->up, w->ld_up) && map_ok(w->down, w->ld_down) &&
+                    su % 16 == 0 && sd % 16 == 0 && su < (1ll << 40) && sd < (1ll << 40) &&
+                    t_forced_path != GEMM_PATH_GENERIC;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+
+  QuantiseArgs q;
+  q.rows = tokens; q.cols = H; q.x = X; q.ldx = ldx; q.bf16 = true;
+  q.codes = base + ws.xq; q.ldq = ws.ldx;
+  q.scales = reinterpret_cast<float*>(base + ws.xs); q.lds = ws.ldxs;
+  q.block_rows = 1;
+  q.vec_x = aligned16(X) && ldx % 8 == 0;
+  q.vec_q = true;
+  int err = launch_fp8_quantise(q, dev->num_sms, stream);
+  if (err != cudaSuccess)
+    return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
+
+  BlocksArgs a{};
+  a.experts = E; a.rows = tokens * top_k; a.offsets = offsets; a.order = order;
+  a.N = F; a.K = H; a.gather = top_k;
+  a.A = q.codes; a.lda = ws.ldx; a.a_rows = tokens; a.sa = q.scales; a.ldsa = ws.ldxs;
+  a.B = w->gate; a.B2 = w->up; a.ldb = w->ld_up; a.b_stride = su;
+  a.sb = w->gate_scale; a.sb2 = w->up_scale; a.ldsb = ws.ldhs; a.sb_stride = ws.ldxs * ws.ldhs;
+  a.alpha = 1.f;
+  a.hq = base + ws.hq; a.ldh = ws.ldh; a.hs = reinterpret_cast<float*>(base + ws.hs); a.ldhs = ws.ldhs;
+  if ((rc = blocks_product(a, fast, dev, stream)) != GEMM_OK) return rc;
+
+  BlocksArgs d{};
+  d.experts = E; d.rows = tokens * top_k; d.offsets = offsets; d.order = order;
+  d.N = H; d.K = F; d.scatter = 1;
+  d.A = a.hq; d.lda = ws.ldh; d.a_rows = d.rows; d.sa = a.hs; d.ldsa = ws.ldhs;
+  d.B = w->down; d.ldb = w->ld_down; d.b_stride = sd;
+  d.sb = w->down_scale; d.ldsb = ws.ldxs; d.sb_stride = ws.ldxs * ws.ldhs;
+  d.C = base + ws.y; d.ldc = ws.ldy; d.out_bf16 = true; d.alpha = 1.f;
+  if ((rc = blocks_product(d, fast, dev, stream)) != GEMM_OK) return rc;
+
+  CombineArgs c;
+  c.tokens = tokens; c.top_k = top_k; c.cols = H;
+  c.y = d.C; c.ldy = ws.ldy; c.weights = weights; c.out = O; c.ldo = ldo;
+  c.vec = aligned16(O) && ldo % 8 == 0;
+  err = launch_experts_combine(c, dev->num_sms, stream);
+  if (err != cudaSuccess)
+    return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
+  t_last_path = fast ? GEMM_PATH_BLOCKS : GEMM_PATH_GENERIC;
+  return GEMM_OK;
+}
+
 __global__ void selftest_wait_kernel(int* status, uint64_t timeout_ns) {
   __shared__ uint64_t bar;
   if (threadIdx.x == 0) {
@@ -1025,6 +1302,59 @@ int gemm_bf16_f32out_ex(int M, int N, int K, float alpha, const gemm_bf16_t* A, 
                         const float* bias, int activation, cudaStream_t stream) {
   return g3::run(Elem::BF16, Elem::F32, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, bias,
                  activation, stream);
+}
+
+int gemm_route_bf16(int tokens, int experts, int top_k, const gemm_bf16_t* logits, long long ld, const float* bias,
+                    int score, int groups, int top_groups, int group_best, int renormalise, float scale, int* ids,
+                    float* weights, int* offsets, int* order, void* workspace, size_t workspace_bytes,
+                    cudaStream_t stream) {
+  return g3::route(tokens, experts, top_k, logits, true, ld, bias, score, groups, top_groups, group_best, renormalise,
+                   scale, ids, weights, offsets, order, workspace, workspace_bytes, stream);
+}
+
+int gemm_route_f32(int tokens, int experts, int top_k, const float* logits, long long ld, const float* bias, int score,
+                   int groups, int top_groups, int group_best, int renormalise, float scale, int* ids, float* weights,
+                   int* offsets, int* order, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return g3::route(tokens, experts, top_k, logits, false, ld, bias, score, groups, top_groups, group_best, renormalise,
+                   scale, ids, weights, offsets, order, workspace, workspace_bytes, stream);
+}
+
+size_t gemm_route_workspace(int tokens, int experts) {
+  if (tokens < 0 || experts < 1 || experts > g3::kRouteMaxExperts) return 0;
+  return g3::route_ws_bytes(tokens, experts);
+}
+
+int gemm_fp8_quantise_bf16(int rows, int cols, const gemm_bf16_t* X, long long ldx, uint8_t* codes, long long ldq,
+                           float* scales, long long lds, int block_rows, cudaStream_t stream) {
+  return g3::fp8_quantise(rows, cols, X, true, ldx, codes, ldq, scales, lds, block_rows, stream);
+}
+
+int gemm_fp8_quantise_f32(int rows, int cols, const float* X, long long ldx, uint8_t* codes, long long ldq,
+                          float* scales, long long lds, int block_rows, cudaStream_t stream) {
+  return g3::fp8_quantise(rows, cols, X, false, ldx, codes, ldq, scales, lds, block_rows, stream);
+}
+
+int gemm_fp8_blocks(int M, int N, int K, float alpha, const uint8_t* A, int lda, const float* a_scale, int ldsa,
+                    const uint8_t* B, int ldb, const float* b_scale, int ldsb, float beta, gemm_bf16_t* C, int ldc,
+                    cudaStream_t stream) {
+  return g3::fp8_blocks(M, N, K, alpha, A, lda, a_scale, ldsa, B, ldb, b_scale, ldsb, beta, C, ldc, true, stream);
+}
+
+int gemm_fp8_blocks_f32out(int M, int N, int K, float alpha, const uint8_t* A, int lda, const float* a_scale, int ldsa,
+                           const uint8_t* B, int ldb, const float* b_scale, int ldsb, float beta, float* C, int ldc,
+                           cudaStream_t stream) {
+  return g3::fp8_blocks(M, N, K, alpha, A, lda, a_scale, ldsa, B, ldb, b_scale, ldsb, beta, C, ldc, false, stream);
+}
+
+int gemm_experts(const gemm_expert_weights* weights, int tokens, int top_k, const gemm_bf16_t* X, long long ldx,
+                 const int* offsets, const int* order, const float* token_weights, gemm_bf16_t* O, long long ldo,
+                 void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return g3::experts(weights, tokens, top_k, X, ldx, offsets, order, token_weights, O, ldo, workspace, workspace_bytes,
+                     stream);
+}
+
+size_t gemm_experts_workspace(int tokens, int top_k, int hidden, int width) {
+  return g3::experts_workspace(tokens, top_k, hidden, width);
 }
 
 const char* gemm_get_last_error(void) { return g3::t_msg; }

@@ -85,6 +85,12 @@ enum WaitSite : int {
   kSiteKvAppend = 60,      // a row range, position or page number that does not fit the call
   kSiteKvAttn = 61,        // the same, in attention over the paged cache
   kSiteKvAttnLoad = 62,    // a wait for a tile of the paged cache
+  kSiteBlocksProducer = 70,
+  kSiteBlocksMma = 71,
+  kSiteBlocksScales = 72,
+  kSiteBlocksEpilogue = 73,
+  kSiteBlocksDrain = 74,
+  kSiteExperts = 75,       // an expert's slots, or a slot's number, that do not fit the call
 };
 
 // Each launcher returns a cudaError_t (as int) from the launch.
@@ -265,6 +271,97 @@ struct SampleArgs {
 };
 constexpr int kSampleMaxVocab = 1 << 20;
 int launch_sample(const SampleArgs& a, int num_sms, cudaStream_t s);
+
+// Routing of tokens to experts (gemm_route_*).
+struct RouteArgs {
+  int tokens, experts, top_k;
+  const void* logits;
+  long long ld;
+  bool bf16, softmax, renormalise;
+  int groups, top_groups, group_best;
+  float scale;
+  const float* bias;
+  int* ids;
+  float* weights;
+  int *offsets, *order;   // null: the order by expert is not wanted
+  int* counts;            // workspace: counts by block and expert
+  bool choices;           // a bias or groups: choices are kept in shared memory
+  bool vec;               // 16-byte-aligned rows
+};
+constexpr int kRouteMaxExperts = 1024, kRouteMaxTopK = 32, kRouteMaxGroups = 32;
+size_t route_ws_bytes(int tokens, int experts);
+int launch_route(const RouteArgs& a, cudaStream_t s);
+
+// E4M3 codes with a scale for each block of block_rows (1 or 128) x 128 values.
+struct QuantiseArgs {
+  int rows, cols;
+  const void* x;
+  long long ldx;
+  bool bf16;
+  uint8_t* codes;
+  long long ldq;
+  float* scales;
+  long long lds;
+  int block_rows;
+  bool vec_x, vec_q;      // rows of 16-byte-aligned vectors of 8 values; of 8-byte-aligned ones
+};
+int launch_fp8_quantise(const QuantiseArgs& a, int num_sms, cudaStream_t s);
+
+// Block-scaled products of E4M3 codes, for one matrix or for the slots of experts:
+// rows [offsets[e], offsets[e+1]) are multiplied with B's e-th matrix.
+struct BlocksArgs {
+  int experts, rows, N, K;
+  const int* offsets;           // null: one matrix, all rows
+  const int* order;             // slot number of each row (scatter, gather), or null
+  int gather;                   // row p of the product is row order[p] / gather of A; 0: row p
+  int scatter;                  // row p of the product is row order[p] of C
+  const uint8_t* A;
+  long long lda;
+  int a_rows;
+  const float* sa;              // a_rows x ceil(K/128)
+  long long ldsa;
+  const uint8_t *B, *B2;        // experts x K x N; B2: the up-projection (SwiGLU), else null
+  long long ldb, b_stride;
+  const float *sb, *sb2;        // experts x ceil(K/128) x ceil(N/128)
+  long long ldsb, sb_stride;
+  void* C;
+  long long ldc;
+  bool out_bf16;
+  float alpha, beta;
+  uint8_t* hq;                  // SwiGLU: codes and scales (rows x ceil(N/128)) of silu(A*B) .* (A*B2)
+  float* hs;
+  long long ldh, ldhs;
+  int* status;
+  uint64_t timeout_ns;
+  int stall;                    // as GemmArgs::stall
+};
+constexpr int kBlocksK = 128, kBlocksN = 128, kBlocksMaxExperts = 1024;
+// The tcgen05 kernel: row tiles of nt, K split over clusters of `split` CTAs.  Maps: A
+// with boxes of 128 k x blocks_box_rows(nt, gather) rows; B and B2 3-D with boxes of 128
+// columns x 128 k; 128-byte swizzle.
+struct BlocksPlan {
+  int nt = 32, split = 1;
+};
+constexpr int blocks_box_rows(int nt, bool gather) { return gather ? 1 : nt >= 128 ? 64 : 16; }
+// The most row tiles that `rows` rows of `experts` experts can make.
+constexpr long long blocks_row_tiles(long long rows, int experts, int nt) {
+  return experts == 1 ? (rows + nt - 1) / nt : rows / nt + (experts < rows ? experts : rows);
+}
+int launch_blocks(const BlocksArgs& a, const BlocksPlan& plan, const CUtensorMap* mapA, const CUtensorMap* mapB,
+                  const CUtensorMap* mapB2, int num_sms, cudaStream_t s);
+int launch_blocks_generic(const BlocksArgs& a, int num_sms, cudaStream_t s);
+
+// O[t] = sum over j of weights[t][j] * Y[t * top_k + j]
+struct CombineArgs {
+  int tokens, top_k, cols;
+  const void* y;                // bf16, cols values a row, ldy apart
+  long long ldy;
+  const float* weights;
+  void* out;
+  long long ldo;
+  bool vec;
+};
+int launch_experts_combine(const CombineArgs& a, int num_sms, cudaStream_t s);
 
 int launch_selftest_wait(int* status, uint64_t timeout_ns, cudaStream_t s);
 

@@ -220,5 +220,26 @@ inline int cluster_split(int tiles_n, int k_units, int num_sms, int forced, int 
   return s;
 }
 
+// Block-scaled products: the row tile (32, 64, 128 or 256; 128 at most with two weights)
+// and the CTAs that share a tile's K.  `mean`: rows of an expert if all that can have some
+// have as many.  A tile as wide as the mean reads each weight once; narrower ones (from L2
+// then) are taken while there are fewer items than SMs.  K is split where even those
+// leave SMs idle, with at least four blocks of 128 a CTA.
+struct BlocksChoice {
+  int nt, split;
+};
+inline BlocksChoice blocks_choice(long long rows, int experts, int tiles_n, int kblocks, bool two_weights, int num_sms) {
+  const long long met = experts < rows ? experts : rows;
+  const long long mean = met > 0 ? (rows + met - 1) / met : 1;
+  const int most = two_weights ? 128 : 256;
+  BlocksChoice c = {32, 1};
+  while (c.nt < most && c.nt < mean) c.nt *= 2;
+  while (c.nt > 32 && met * ((mean + c.nt - 1) / c.nt) * tiles_n < num_sms) c.nt /= 2;
+  const long long items = met * ((mean + c.nt - 1) / c.nt) * tiles_n;
+  if (c.nt <= 64)
+    while (c.split < 8 && items * c.split * 2 <= num_sms && kblocks >= 8 * c.split) c.split *= 2;
+  return c;
+}
+
 }  // namespace plan
 }  // namespace g3
