@@ -687,13 +687,15 @@ int gemm_last_path(void);
  * The tensor-core kernel takes every width; the FP32 SIMT kernel takes 128
  * (8 x 8 register tiles, two CTAs per SM) or 256 (8 x 16 register tiles, one
  * CTA per SM), and an FP32 call with another forced width returns
- * GEMM_ERR_UNSUPPORTED.  Other values return GEMM_ERR_INVALID_ARG.  For A/B
- * measurements and tests.
+ * GEMM_ERR_UNSUPPORTED.  The block-scaled products (gemm_fp8_blocks*,
+ * gemm_experts) take 128 and 256 as rows of A a tile (single CTAs; CTA pairs).
+ * Other values return GEMM_ERR_INVALID_ARG.  For A/B measurements and tests.
  */
 int gemm_force_tile_n(int bn);
 
 /* Tile width the last tensor-core or FP32 SIMT call on this host thread used
- * (0 if none). */
+ * (0 if none); rows of A a tile of the last block-scaled product (32, 64, 128 or
+ * 256; gemm_experts: of its down product). */
 int gemm_last_tile_n(void);
 
 /*

@@ -40,6 +40,70 @@ __device__ __forceinline__ void expert_row(const BlocksArgs& a, int p, int& from
   if (a.scatter != 0) to = fits ? slot : -1;
 }
 
+// ---------------------------------------------------------------- items of the tcgen05 kernels
+// One item: `rows` rows p0 .. of expert e, column tile nb.
+struct Item {
+  int e, p0, rows, nb;
+};
+// Walks the items of one CTA; every role has its own.  pre[e]: row tiles of the experts
+// before e; beg, num: their rows.
+struct Walk {
+  const int *pre, *beg, *num;
+  int nt, tiles_n, e;
+  __device__ __forceinline__ Item at(long long it) {
+    while (it >= (long long)pre[e + 1] * tiles_n) ++e;
+    const int x = (int)(it - (long long)pre[e] * tiles_n), tiles = pre[e + 1] - pre[e];
+    const int t = x % tiles;
+    Item i;
+    i.e = e;
+    i.nb = x / tiles;
+    i.p0 = beg[e] + t * nt;
+    i.rows = min(nt, num[e] - t * nt);
+    return i;
+  }
+};
+
+// The lists of a Walk, in shared memory, by one warp: row tiles of NT.
+constexpr int kListBytes = (3 * kBlocksMaxExperts + 4) * 4;
+template <int NT>
+__device__ __forceinline__ void list_row_tiles(const BlocksArgs& a, int* pre, int* beg, int* num, int lane) {
+  int run = 0;
+  for (int e0 = 0; e0 < a.experts; e0 += 32) {
+    const int e = e0 + lane;
+    int b = 0, n = 0;
+    if (e < a.experts) expert_rows(a, e, b, n);
+    const int tiles = (n + NT - 1) / NT;
+    int s = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) s += o;
+    }
+    if (e < a.experts) {
+      pre[e] = run + s - tiles;
+      beg[e] = b;
+      num[e] = n;
+    }
+    run += __shfl_sync(0xffffffffu, s, 31);
+  }
+  if (lane == 0) pre[a.experts] = run;
+}
+
+// ---------------------------------------------------------------- two sums in one instruction
+__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ float part2(uint64_t v, int i) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+  return __uint_as_float(i ? hi : lo);
+}
+
 // alpha * v + beta * C, rounded once to C's type
 __device__ __forceinline__ void blocks_store(const BlocksArgs& a, long long m, int n, float v) {
   v *= a.alpha;

@@ -48,7 +48,6 @@ namespace {
 constexpr int BK = kBlocksK, BN = kBlocksN;
 constexpr int THREADS = 384, EPI_WARPS = 8, EPI_FIRST = 4;
 constexpr int W_BYTES = BN * BK;               // a weight tile: 128 k rows of 128 columns
-constexpr int MAX_EXPERTS = kBlocksMaxExperts;
 constexpr int SMEM_LIMIT = 232448;
 
 template <int NT, bool SW>
@@ -62,7 +61,7 @@ struct Cfg {
   // SwiGLU: codes of one half's columns on their way to rows of 128 bytes, and the
   // columns' largest magnitudes by TMEM quarter
   static constexpr int OUT_BYTES = SW ? NT * BN + 4 * NT * 4 : 0;
-  static constexpr int LIST_BYTES = (3 * MAX_EXPERTS + 4) * 4;
+  static constexpr int LIST_BYTES = kListBytes;
   static constexpr int BAR_BYTES = 512;
   static constexpr int REST = SCALE_BYTES + OUT_BYTES + LIST_BYTES + BAR_BYTES + 1024;
   static constexpr int FIT = (SMEM_LIMIT - REST) / STAGE_BYTES;
@@ -84,11 +83,6 @@ struct Params {
   int kblocks, tiles_n, split;
 };
 
-__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) { return (uint64_t)lo | ((uint64_t)hi << 32); }
-
 // Barrier `id` of 128 threads; and the same, returning whether any of them has `p`.
 __device__ __forceinline__ void sync_128(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool any_of_128(int id, bool p) {
@@ -107,27 +101,6 @@ __device__ __forceinline__ void tmem_read(uint32_t addr, uint32_t (&r)[CW]) {
   else tmem_ld_32x32b_x16(addr, r);
 }
 
-// One item: `rows` rows p0 .. of expert e, columns n0 .. n0+127.
-struct Item {
-  int e, p0, rows, nb;
-};
-// Walks the items of one CTA; every role has its own.  pre[e]: row tiles of the experts
-// before e; beg, num: their rows.
-struct Walk {
-  const int *pre, *beg, *num;
-  int nt, tiles_n, e;
-  __device__ __forceinline__ Item at(long long it) {
-    while (it >= (long long)pre[e + 1] * tiles_n) ++e;
-    const int x = (int)(it - (long long)pre[e] * tiles_n), tiles = pre[e + 1] - pre[e];
-    const int t = x % tiles;
-    Item i;
-    i.e = e;
-    i.nb = x / tiles;
-    i.p0 = beg[e] + t * nt;
-    i.rows = min(nt, num[e] - t * nt);
-    return i;
-  }
-};
 __device__ __forceinline__ int mma_rows(int rows) { return (rows + 15) & ~15; }
 
 // The sums of four neighbouring columns of B for one row of A, over the cluster's ranks
@@ -172,8 +145,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* bar_ptr = at;
   at += C::BAR_BYTES;
   int* pre = reinterpret_cast<int*>(at);                         // [experts + 1]
-  int* beg = pre + MAX_EXPERTS + 1;
-  int* num = beg + MAX_EXPERTS;
+  int* beg = pre + kBlocksMaxExperts + 1;
+  int* num = beg + kBlocksMaxExperts;
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
   auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
   auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + b); };
@@ -211,28 +184,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_relinquish();
   }
   griddep_wait();
-  if (warp == 3) {
-    int run = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 32) {
-      const int e = e0 + lane;
-      int b = 0, n = 0;
-      if (e < a.experts) expert_rows(a, e, b, n);
-      const int tiles = (n + NT - 1) / NT;
-      int s = tiles;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, s, d);
-        if (lane >= d) s += o;
-      }
-      if (e < a.experts) {
-        pre[e] = run + s - tiles;
-        beg[e] = b;
-        num[e] = n;
-      }
-      run += __shfl_sync(0xffffffffu, s, 31);
-    }
-    if (lane == 0) pre[a.experts] = run;
-  }
+  if (warp == 3) list_row_tiles<NT>(a, pre, beg, num, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -468,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (!ok) break;
       auto value = [&](int op, int j) {
-        return __uint_as_float((uint32_t)(j & 1 ? acc[op][j / 2] >> 32 : acc[op][j / 2]));
+        return part2(acc[op][j / 2], j & 1);
       };
       const int nl = quarter * 32 + lane, n = i.nb * BN + nl;
       if (split > 1) {
@@ -634,7 +586,6 @@ int launch_blocks(const BlocksArgs& a, const BlocksPlan& plan, const CUtensorMap
     case 32: return launch_impl<32, false, false>(a, mapA, mapB, mapB2, split, num_sms, s);
     case 64: return launch_impl<64, false, false>(a, mapA, mapB, mapB2, split, num_sms, s);
     case 128: return launch_impl<128, false, false>(a, mapA, mapB, mapB2, split, num_sms, s);
-    case 256: return launch_impl<256, false, false>(a, mapA, mapB, mapB2, split, num_sms, s);
   }
   return cudaErrorInvalidValue;
 }

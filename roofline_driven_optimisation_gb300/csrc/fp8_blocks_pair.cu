@@ -1,0 +1,560 @@
+// Block-scaled products (the formulas are those of fp8_blocks.cu) on CTA pairs, for calls
+// with many rows: an item is 256 rows of A and 256 columns of B, or, with gate and up
+// weights, 256 rows and 128 columns of each.
+//
+// Why another kernel.  With many rows the products are compute-bound, and what the
+// swapped kernel does a block of 128 k is then too much: 48 KB into shared memory and
+// out of it again against 512 tensor cycles, and a scale of shared memory for each
+// column of the accumulator.  Here rows of A are TMEM lanes, so that a drain thread has
+// one row, and one scale (two with gate and up) a block; and a pair of CTAs
+// (cta_group::2) issues one M = 256 MMA in which each CTA holds its 128 rows of A and
+// half of B's columns: 32 KB a block and CTA.
+//
+// Per block of 128 k and CTA the MMAs take 512 cycles at the nominal rate.  The drain's
+// 128 x 256 sums take 256 cycles of fma.rn.f32x2 (64 a warp, two warps a scheduler, two
+// cycles each), in registers for the whole of K: 128 a thread.
+//
+// Roles (384 threads a CTA): warp 0 copies (each CTA its rows of A, gathered by
+// tile::gather4 where rows are an expert's, and its half of B; all complete on the
+// leader's barrier), warp 1 of the leader issues the MMAs, warp 2 copies the scales of
+// its CTA's rows into a ring of eight blocks (cp.async, no registers), warps 4-11 drain:
+// warp w the TMEM lanes 32*(w%4)..+31 and half of the columns.
+//
+// h of gate and up: a thread has 64 columns of its row in both, so the largest magnitude
+// of 128 columns is found in registers and one exchange with the thread of the other
+// half; its 64 codes leave in four vector stores.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+#include <mutex>
+
+#include "epilogue.cuh"
+#include "experts.cuh"
+#include "internal.h"
+#include "kv_cache.cuh"
+#include "ptx.cuh"
+
+namespace g3 {
+namespace {
+
+constexpr int BK = kBlocksK, BM = kBlocksPairRows, BM_CTA = BM / 2;
+constexpr int THREADS = 384, EPI_WARPS = 8, EPI_FIRST = 4;
+constexpr int A_BYTES = BM_CTA * BK, B_BYTES = BK * 128;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES, STAGES = 6;
+constexpr int TMEM_COLS = 512, COLS = 256, NBUF = 2;
+constexpr int RING = 8, RING_WORDS = BM_CTA + 4;       // scales of a block: the rows', then B's one or two
+constexpr int BOX = 64;
+constexpr int BAR_BYTES = 512;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + RING * RING_WORDS * 4 + 2 * BM_CTA * 4 + kListBytes + BAR_BYTES + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory");
+static_assert(8 * (2 * STAGES + 2 * NBUF + 2 * RING + 4) <= BAR_BYTES, "barrier area");
+static_assert(blocks_box_rows(kBlocksPairRows, false) == BOX, "boxes of A");
+constexpr uint64_t kDrainGraceNs = 50000;              // after an abort, time for the peer's copies to land
+constexpr uint16_t kBothCtas = 0x3;
+
+struct Params {
+  BlocksArgs a;
+  int kblocks, tiles_n;
+  int c_vec;                                           // C's rows are 16-byte-aligned vectors
+};
+
+// Barrier 1 of the 256 drain threads; and the same, returning whether any of them has `p`.
+__device__ __forceinline__ void sync_drain() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool any_drain(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(p ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// 32 columns n .. of row m of C from this thread's sums
+template <bool OUT_BF16>
+__device__ __forceinline__ void store32(const Params& p, long long m, int n, const uint64_t* v) {
+  const BlocksArgs& a = p.a;
+  if (p.c_vec && n + 32 <= a.N) {
+    if constexpr (OUT_BF16) {
+      __nv_bfloat16* c = static_cast<__nv_bfloat16*>(a.C) + m * a.ldc + n;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = a.alpha * part2(v[q * 4 + i / 2], i & 1);
+        if (a.beta != 0.f) {
+          const uint4 o = *reinterpret_cast<const uint4*>(c + q * 8);
+          const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[2 * i] = fmaf(a.beta, __uint_as_float(w[i] << 16), f[2 * i]);
+            f[2 * i + 1] = fmaf(a.beta, __uint_as_float(w[i] & 0xffff0000u), f[2 * i + 1]);
+          }
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(c + q * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+      float* c = static_cast<float*>(a.C) + m * a.ldc + n;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = a.alpha * part2(v[q * 2 + i / 2], i & 1);
+        if (a.beta != 0.f) {
+          const float4 o = *reinterpret_cast<const float4*>(c + q * 4);
+          f[0] = fmaf(a.beta, o.x, f[0]);
+          f[1] = fmaf(a.beta, o.y, f[1]);
+          f[2] = fmaf(a.beta, o.z, f[2]);
+          f[3] = fmaf(a.beta, o.w, f[3]);
+        }
+        *reinterpret_cast<float4*>(c + q * 4) = make_float4(f[0], f[1], f[2], f[3]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (n + i < a.N) blocks_store(a, m, n + i, part2(v[i / 2], i & 1));
+  }
+}
+
+// SW: gate and up weights, codes out.  GATHER: A's rows through tile::gather4.
+template <bool SW, bool OUT_BF16>
+__global__ void __launch_bounds__(THREADS, 1)
+    blocks_pair_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+                       const __grid_constant__ CUtensorMap mapB2, const Params p) {
+  constexpr bool GATHER = SW;
+  constexpr int BN = SW ? 128 : 256;                   // columns of C (or of h) an item
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;        // the same offset in both CTAs
+  uint8_t* base_ptr = smem_raw + (base - raw);
+  auto a_tile = [&](int s) { return base + s * STAGE_BYTES; };
+  auto b_tile = [&](int s) { return base + s * STAGE_BYTES + A_BYTES; };
+  uint8_t* at = base_ptr + STAGES * STAGE_BYTES;
+  float* ring = reinterpret_cast<float*>(at);          // [RING][RING_WORDS]
+  at += RING * RING_WORDS * 4;
+  float* big = reinterpret_cast<float*>(at);           // [2][BM_CTA]
+  at += 2 * BM_CTA * 4;
+  const uint32_t bar_base = base + (uint32_t)(at - base_ptr);
+  uint8_t* bar_ptr = at;
+  at += BAR_BYTES;
+  int* pre = reinterpret_cast<int*>(at);
+  int* beg = pre + kBlocksMaxExperts + 1;
+  int* num = beg + kBlocksMaxExperts;
+  auto full_bar = [&](int s) { return bar_base + 8u * s; };
+  auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + b); };
+  auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + NBUF + b); };
+  auto sfull_bar = [&](int r) { return bar_base + 8u * (2 * STAGES + 2 * NBUF + r); };
+  auto sempty_bar = [&](int r) { return bar_base + 8u * (2 * STAGES + 2 * NBUF + RING + r); };
+  const uint32_t drain_bar = bar_base + 8u * (2 * STAGES + 2 * NBUF + 2 * RING);
+  const uint32_t stall_bar = drain_bar + 8u;           // test hook: nothing arrives
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (2 * STAGES + 2 * NBUF + 2 * RING + 2));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const BlocksArgs& a = p.a;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank() & 1u;        // clusters hold one pair
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < NBUF; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), 2 * EPI_WARPS);
+    }
+    for (int r = 0; r < RING; ++r) {
+      mbar_init(sfull_bar(r), 32);
+      mbar_init(sempty_bar(r), EPI_WARPS);
+    }
+    mbar_init(drain_bar, 1);
+    mbar_init(stall_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&mapA);
+    tma_prefetch_desc(&mapB);
+    if (SW) tma_prefetch_desc(&mapB2);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  griddep_wait();
+  if (warp == 3) list_row_tiles<BM>(a, pre, beg, num, lane);
+  tc_fence_before();
+  cluster_sync();                                      // barriers, lists and TMEM of both CTAs
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const long long items = (long long)pre[a.experts] * p.tiles_n;
+  const long long first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  Walk walk{pre, beg, num, BM, p.tiles_n, 0};
+
+  if (warp < EPI_FIRST) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0) {
+      // ------------------------------------------------------------ copies
+      uint32_t issued = 0, issued_par = 0;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      const bool one = elect_one_sync();
+      for (long long it = first; ok && it < items; it += step) {
+        const Item i = walk.at(it);
+        const int mine = min(max(i.rows - (int)rank * BM_CTA, 0), BM_CTA);      // this CTA's rows
+        const int other = i.rows - mine;
+        const int p0 = i.p0 + (int)rank * BM_CTA;
+        // rows that are not there are not copied: what their lanes sum up is not read
+        auto copied = [&](int rows) { return GATHER ? (rows + 3) / 4 * 4 : (rows + BOX - 1) / BOX * BOX; };
+        const uint32_t bytes = (uint32_t)(2 * B_BYTES + (copied(mine) + copied(other)) * BK);
+        int y[4];
+        if (GATHER) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            int from = -1, to;
+            if (lane * 4 + q < mine) expert_row(a, p0 + lane * 4 + q, from, to);
+            y[q] = from >= 0 ? from : a.a_rows;        // outside: zeros
+          }
+        }
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if ((GATHER || one) && !mbar_wait(empty_bar(stage), phase ^ 1u, a.timeout_ns, abort_flag)) {
+            if (!*abort_flag) report_status(a.status, 5, kSiteBlocks2Producer);
+            *abort_flag = 1;
+            ok = false;
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t full = map_to_rank(full_bar(stage), 0);                // both CTAs' copies
+          if (one) {
+            if (leader) mbar_arrive_expect_tx(full_bar(stage), bytes);
+            tma_load_3d_pair(b_tile(stage), SW && rank == 1 ? &mapB2 : &mapB, full,
+                             i.nb * BN + (SW ? 0 : (int)rank * 128), kb * BK, i.e);
+            if (!GATHER)
+              for (int c = 0; c * BOX < mine; ++c)
+                tma_load_2d_pair(a_tile(stage) + c * BOX * BK, &mapA, full, kb * BK, p0 + c * BOX);
+          }
+          if (GATHER) {
+            __syncwarp();
+            if (lane * 4 < mine)
+              tma_gather4_pair(a_tile(stage) + lane * 4 * BK, &mapA, full, kb * BK, y[0], y[1], y[2], y[3]);
+          }
+          issued |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (*abort_flag && one) {
+        if (leader)
+          for (int s = 0; s < STAGES; ++s)
+            if (((issued >> s) & 1u) && !mbar_wait(full_bar(s), (issued_par >> s) & 1u, kDrainWaitNs, nullptr))
+              report_status(a.status, 5, kSiteBlocks2Drain);
+        // the peer's copies complete on a barrier this CTA cannot wait on
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < kDrainGraceNs) {
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA (leader)
+      if (leader && elect_one_sync()) {
+        constexpr uint32_t idesc = idesc_f8_f32(BM, COLS, kE4M3, kE4M3, /*A K-major*/ 0, /*B MN-major*/ 1);
+        int stage = 0, b = 0;
+        uint32_t phase = 0, bphase = 0;
+        bool ok = true, issued_any = false;
+        if (a.stall && first == 0 && !mbar_wait(stall_bar, 0, a.timeout_ns / 4, abort_flag)) {
+          if (!*abort_flag) report_status(a.status, 5, kSiteBlocks2Mma);
+          *abort_flag = 1;
+          ok = false;
+        }
+        for (long long it = first; ok && it < items; it += step) {
+          for (int kb = 0; kb < p.kblocks; ++kb) {
+            if (!mbar_wait(tempty_bar(b), bphase ^ 1u, a.timeout_ns, abort_flag) ||
+                !mbar_wait(full_bar(stage), phase, a.timeout_ns, abort_flag)) {
+              if (!*abort_flag) report_status(a.status, 5, kSiteBlocks2Mma);
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem_base + (uint32_t)(b * COLS);
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk)
+              tc_mma_f8_pair(d, smem_desc_sw128(a_tile(stage) + kk * 32, 16, 1024),
+                             smem_desc_sw128(b_tile(stage) + kk * 32 * 128, B_BYTES, 1024), idesc, kk != 0 ? 1u : 0u);
+            issued_any = true;
+            tc_commit_pair_mc(empty_bar(stage), kBothCtas);
+            tc_commit_pair_mc(tfull_bar(b), kBothCtas);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            if (++b == NBUF) {
+              b = 0;
+              bphase ^= 1u;
+            }
+          }
+        }
+        if (*abort_flag && issued_any) {
+          tc_commit_pair_mc(drain_bar, 0x1);
+          if (!mbar_wait(drain_bar, 0, kDrainWaitNs, nullptr)) report_status(a.status, 5, kSiteBlocks2Drain);
+        }
+      }
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ scales
+      int r = 0;
+      uint32_t rphase = 0;
+      bool ok = true;
+      for (long long it = first; ok && it < items; it += step) {
+        const Item i = walk.at(it);
+        const float* row[BM_CTA / 32];
+#pragma unroll
+        for (int q = 0; q < BM_CTA / 32; ++q) {
+          const int m = (int)rank * BM_CTA + q * 32 + lane;
+          int from = -1, to;
+          if (m < i.rows) expert_row(a, i.p0 + m, from, to);
+          row[q] = from >= 0 ? a.sa + (long long)from * a.ldsa : nullptr;
+        }
+        // B's scales of the item's column blocks: lane 0 the first, lane 1 the second
+        const int col = SW ? i.nb : 2 * i.nb + lane;
+        const float* sb = nullptr;
+        if (lane < 2 && (SW || col * 128 < a.N)) sb = (SW && lane == 1 ? a.sb2 : a.sb) + i.e * a.sb_stride + col;
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (!__all_sync(0xffffffffu, mbar_wait(sempty_bar(r), rphase ^ 1u, a.timeout_ns, abort_flag))) {
+            if (!*abort_flag) report_status(a.status, 5, kSiteBlocks2Scales);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          const uint32_t to = smem_u32(ring + r * RING_WORDS);
+#pragma unroll
+          for (int q = 0; q < BM_CTA / 32; ++q)
+            if (row[q] != nullptr) cp_async_4(to + (q * 32 + lane) * 4, row[q] + kb);
+          if (sb != nullptr) cp_async_4(to + (BM_CTA + lane) * 4, sb + kb * a.ldsb);
+          cp_async_arrive(sfull_bar(r));
+          if (++r == RING) {
+            r = 0;
+            rphase ^= 1u;
+          }
+        }
+      }
+      cp_async_commit();
+      cp_async_wait<0>();                              // none in flight when the CTA leaves
+    }
+  } else {
+    // ------------------------------------------------------------ drain and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int quarter = warp % 4, half = (warp - EPI_FIRST) / 4;
+    const int lrow = quarter * 32 + lane, m = (int)rank * BM_CTA + lrow;       // row of the CTA, of the item
+    const uint32_t t_lane = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t lead_tempty = map_to_rank(tempty_bar(0), 0);
+    int b = 0, r = 0;
+    uint32_t bphase = 0, rphase = 0;
+    bool ok = true;
+    for (long long it = first; ok && it < items; it += step) {
+      const Item i = walk.at(it);
+      // columns of the accumulator: plain half * 128 .., 128 of them; gate and up half * 64 ..
+      // and 128 + half * 64 .., 64 of each
+      uint64_t acc[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = 0;
+      // the block's scales are taken out of the ring while the block before is drained
+      float s0 = 0.f, s1 = 0.f;
+      auto scales = [&]() {
+        const bool got = mbar_wait(sfull_bar(r), rphase, a.timeout_ns, abort_flag);
+        const float* at = ring + r * RING_WORDS;
+        const float sa = at[lrow];
+        s0 = sa * at[BM_CTA + (SW ? 0 : half)];
+        s1 = SW ? sa * at[BM_CTA + 1] : s0;
+        return got;
+      };
+      auto column = [&](int c) {
+        return (uint32_t)(SW ? (c / 4) * 128 + half * 64 + (c % 4) * 16 : half * 128 + c * 16);
+      };
+      ok = scales();
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        ok = ok && mbar_wait(tfull_bar(b), bphase, a.timeout_ns, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (!*abort_flag) report_status(a.status, 5, kSiteBlocks2Epilogue);
+          *abort_flag = 1;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = t_lane + (uint32_t)(b * COLS);
+        const uint64_t d0 = pack2(__float_as_uint(s0), __float_as_uint(s0));
+        const uint64_t d1 = pack2(__float_as_uint(s1), __float_as_uint(s1));
+        // 16 columns are read while the 16 before are added
+        uint32_t v[2][16];
+        tmem_ld_32x32b_x16(d + column(0), v[0]);
+        const int used = r;
+        if (++r == RING) {
+          r = 0;
+          rphase ^= 1u;
+        }
+        if (kb + 1 < p.kblocks) ok = scales();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          tc_wait_ld();
+          if (c < 7) {
+            tmem_ld_32x32b_x16(d + column(c + 1), v[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_remote_light(lead_tempty + 8u * b);
+              mbar_arrive(sempty_bar(used));
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) fma2(acc[c * 8 + j], pack2(v[c & 1][2 * j], v[c & 1][2 * j + 1]), c < 4 ? d0 : d1);
+        }
+        if (++b == NBUF) {
+          b = 0;
+          bphase ^= 1u;
+        }
+      }
+      if constexpr (SW) {
+        // the eight warps meet below: they go on or give up together
+        ok = !any_drain(!ok);
+        if (!ok) break;
+        const int n = i.nb * BN + half * 64;
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          float h[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            h[q] = n + 2 * j + q < a.N ? swiglu_combine(part2(acc[j], q), part2(acc[32 + j], q)) : 0.f;
+            top = fmaxf(top, fabsf(h[q]));             // fmaxf leaves NaN out
+          }
+          acc[j] = pack2(__float_as_uint(h[0]), __float_as_uint(h[1]));
+        }
+        big[half * BM_CTA + lrow] = top;
+        sync_drain();
+        const float s = kv_scale_for<kKvE4M3>(fmaxf(top, big[(1 - half) * BM_CTA + lrow]));
+        const float f = kv_recip(s);
+        if (m < i.rows) {
+          const long long row = (long long)i.p0 + m;
+          uint8_t* q = a.hq + row * a.ldh + n;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint64_t x = acc[c * 8 + 2 * k], y = acc[c * 8 + 2 * k + 1];
+              w[k] = kv_code2<kKvE4M3>(__fmul_rn(part2(x, 0), f), __fmul_rn(part2(x, 1), f)) |
+                     (kv_code2<kKvE4M3>(__fmul_rn(part2(y, 0), f), __fmul_rn(part2(y, 1), f)) << 16);
+            }
+            // rows of a.hq are whole vectors; codes past N are 0
+            if (n + c * 16 < a.ldh) *reinterpret_cast<uint4*>(q + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (half == 0) a.hs[row * a.ldhs + i.nb] = s;
+        }
+      } else {
+        if (!ok) break;
+        if (m < i.rows) {
+          int from, to;
+          expert_row(a, i.p0 + m, from, to);
+          if (to >= 0)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int n = i.nb * BN + half * 128 + c * 32;
+              if (n < a.N) store32<OUT_BF16>(p, to, n, acc + c * 16);
+            }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  griddep_launch_dependents();
+  tc_fence_before();
+  cluster_sync();                                      // both CTAs are done with the pair's TMEM and barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+struct PairInfo {
+  std::atomic<bool> ready{false};
+  int max_clusters = 0;
+};
+
+template <bool SW, bool OUT_BF16>
+int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap* mapB, const CUtensorMap* mapB2,
+                int num_sms, cudaStream_t s) {
+  static PairInfo info[64];
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  auto kernel = blocks_pair_kernel<SW, OUT_BF16>;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (!info[dev].ready.load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!info[dev].ready.load(std::memory_order_relaxed)) {
+      cudaFuncAttributes fa;
+      if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+      // 128 threads at 88 registers and 256 at 208 are 384 * 168: with fewer at launch the
+      // warps that take some would wait forever
+      if (fa.numRegs < 168) return cudaErrorInvalidConfiguration;
+      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES)) != cudaSuccess)
+        return e;
+      int n = 0;
+      cfg.gridDim = dim3(2 * (num_sms / 2), 1, 1);
+      if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+      info[dev].max_clusters = n > 0 ? n : 1;
+      info[dev].ready.store(true, std::memory_order_release);
+    }
+  }
+  Params p;
+  p.a = a;
+  p.kblocks = (a.K + BK - 1) / BK;
+  p.tiles_n = (a.N + (SW ? 128 : 256) - 1) / (SW ? 128 : 256);
+  const int osz = OUT_BF16 ? 2 : 4;
+  p.c_vec = ((reinterpret_cast<uintptr_t>(a.C) & 15u) == 0 && (a.ldc * osz) % 16 == 0) ? 1 : 0;
+  const long long items = blocks_row_tiles(a.rows, a.offsets != nullptr ? a.experts : 1, BM) * p.tiles_n;
+  const long long clusters = items < info[dev].max_clusters ? items : info[dev].max_clusters;
+  cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, *mapA, *mapB, SW ? *mapB2 : *mapB, p);
+}
+
+}  // namespace
+
+int launch_blocks_pair(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap* mapB, const CUtensorMap* mapB2,
+                       int num_sms, cudaStream_t s) {
+  if ((a.B2 != nullptr) != (a.gather != 0)) return cudaErrorInvalidValue;
+  if (a.B2 != nullptr) return launch_impl<true, true>(a, mapA, mapB, mapB2, num_sms, s);
+  return a.out_bf16 ? launch_impl<false, true>(a, mapA, mapB, mapB2, num_sms, s)
+                    : launch_impl<false, false>(a, mapA, mapB, mapB2, num_sms, s);
+}
+
+}  // namespace g3

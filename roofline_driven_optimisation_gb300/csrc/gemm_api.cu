@@ -973,9 +973,11 @@ int blocks_product(BlocksArgs& a, bool fast, DeviceInfo* dev, cudaStream_t strea
   int err;
   if (fast) {
     BlocksPlan plan;
-    const int kblocks = (a.K + kBlocksK - 1) / kBlocksK, tiles_n = (a.N + kBlocksN - 1) / kBlocksN;
-    const plan::BlocksChoice c = plan::blocks_choice(a.rows, a.offsets != nullptr ? a.experts : 1, tiles_n, kblocks,
-                                                     a.B2 != nullptr, dev->num_sms);
+    if (t_forced_bn != 0 && t_forced_bn != 128 && t_forced_bn != kBlocksPairRows)
+      return fail(GEMM_ERR_UNSUPPORTED, "block-scaled products have no tile of %d rows", t_forced_bn);
+    const plan::BlocksChoice c = plan::blocks_choice(a.rows, a.offsets != nullptr ? a.experts : 1, a.N,
+                                                     (a.K + kBlocksK - 1) / kBlocksK, a.B2 != nullptr, dev->num_sms,
+                                                     t_forced_bn);
     plan.nt = c.nt;
     plan.split = c.split;
     const bool gather = a.gather != 0;
@@ -988,8 +990,10 @@ int blocks_product(BlocksArgs& a, bool fast, DeviceInfo* dev, cudaStream_t strea
       if ((rc = make_map_3d(i ? a.B2 : a.B, a.N, a.K, a.experts, (uint64_t)a.ldb, (uint64_t)a.b_stride, kBlocksN, kBlocksK,
                             CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, i ? &mB2 : &mB)) != GEMM_OK)
         return rc;
-    err = launch_blocks(a, plan, mA, mB, mB2, dev->num_sms, stream);
+    err = plan.nt == kBlocksPairRows ? launch_blocks_pair(a, mA, mB, mB2, dev->num_sms, stream)
+                                     : launch_blocks(a, plan, mA, mB, mB2, dev->num_sms, stream);
     t_last_k_split = plan.split;
+    t_last_bn = plan.nt;
   } else {
     err = launch_blocks_generic(a, dev->num_sms, stream);
   }

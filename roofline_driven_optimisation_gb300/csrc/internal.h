@@ -90,6 +90,11 @@ enum WaitSite : int {
   kSiteBlocksScales = 72,
   kSiteBlocksEpilogue = 73,
   kSiteBlocksDrain = 74,
+  kSiteBlocks2Producer = 76,
+  kSiteBlocks2Mma = 77,
+  kSiteBlocks2Scales = 78,
+  kSiteBlocks2Epilogue = 79,
+  kSiteBlocks2Drain = 80,
   kSiteExperts = 75,       // an expert's slots, or a slot's number, that do not fit the call
 };
 
@@ -349,6 +354,11 @@ constexpr long long blocks_row_tiles(long long rows, int experts, int nt) {
 }
 int launch_blocks(const BlocksArgs& a, const BlocksPlan& plan, const CUtensorMap* mapA, const CUtensorMap* mapB,
                   const CUtensorMap* mapB2, int num_sms, cudaStream_t s);
+// The CTA-pair kernel: row tiles of kBlocksPairRows; the same maps, A's boxes of
+// blocks_box_rows(kBlocksPairRows, gather) rows.
+constexpr int kBlocksPairRows = 256;
+int launch_blocks_pair(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap* mapB, const CUtensorMap* mapB2,
+                       int num_sms, cudaStream_t s);
 int launch_blocks_generic(const BlocksArgs& a, int num_sms, cudaStream_t s);
 
 // O[t] = sum over j of weights[t][j] * Y[t * top_k + j]

@@ -220,7 +220,7 @@ inline int cluster_split(int tiles_n, int k_units, int num_sms, int forced, int 
   return s;
 }
 
-// Block-scaled products: the row tile (32, 64, 128 or 256; 128 at most with two weights)
+// Block-scaled products: the row tile (32, 64 or 128: the swapped kernel; 256: CTA pairs)
 // and the CTAs that share a tile's K.  `mean`: rows of an expert if all that can have some
 // have as many.  A tile as wide as the mean reads each weight once; narrower ones (from L2
 // then) are taken while there are fewer items than SMs.  K is split where even those
@@ -228,12 +228,22 @@ inline int cluster_split(int tiles_n, int k_units, int num_sms, int forced, int 
 struct BlocksChoice {
   int nt, split;
 };
-inline BlocksChoice blocks_choice(long long rows, int experts, int tiles_n, int kblocks, bool two_weights, int num_sms) {
+inline BlocksChoice blocks_choice(long long rows, int experts, int N, int kblocks, bool two_weights, int num_sms,
+                                  int forced) {
   const long long met = experts < rows ? experts : rows;
   const long long mean = met > 0 ? (rows + met - 1) / met : 1;
-  const int most = two_weights ? 128 : 256;
+  const int tiles_n = (N + 127) / 128;
   BlocksChoice c = {32, 1};
-  while (c.nt < most && c.nt < mean) c.nt *= 2;
+  if (forced != 0) {
+    c.nt = forced;
+    return c;
+  }
+  const long long pairs = met * ((mean + 255) / 256) * (two_weights ? tiles_n : (N + 255) / 256);
+  if (mean > 128 && pairs * 2 >= num_sms) {
+    c.nt = 256;
+    return c;
+  }
+  while (c.nt < 128 && c.nt < mean) c.nt *= 2;
   while (c.nt > 32 && met * ((mean + c.nt - 1) / c.nt) * tiles_n < num_sms) c.nt /= 2;
   const long long items = met * ((mean + c.nt - 1) / c.nt) * tiles_n;
   if (c.nt <= 64)

@@ -42,6 +42,18 @@ def test_sizes(tokens, experts, top_k, hidden, width):
     check(Layer(experts, hidden, width), tokens, top_k)
 
 
+@pytest.mark.parametrize("rows", [128, 256])
+@pytest.mark.parametrize("tokens,experts,top_k,hidden,width", [
+    (1, 4, 2, 144, 16), (300, 4, 2, 272, 400), (260, 1, 1, 128, 128), (900, 3, 2, 400, 144)])
+def test_each_kernel(tokens, experts, top_k, hidden, width, rows):
+    g.force_tile_n(rows)
+    try:
+        check(Layer(experts, hidden, width), tokens, top_k)
+        assert g.last_tile_n() == rows
+    finally:
+        g.force_tile_n(0)
+
+
 def test_many_tokens():
     check(Layer(4, 272, 400), 1500, 2)
 

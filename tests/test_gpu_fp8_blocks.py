@@ -56,6 +56,24 @@ def test_many_rows(M, N, K, out):
     Case(M, N, K).run(out, want_path=g.PATH_BLOCKS)
 
 
+@pytest.fixture(params=[128, 256])
+def rows_a_tile(request):
+    """Single CTAs with row tiles of 128, and CTA pairs, whatever the sizes ask for."""
+    g.force_tile_n(request.param)
+    yield request.param
+    g.force_tile_n(0)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("M,N,K", [(1, 16, 16), (130, 272, 144), (256, 256, 128), (257, 400, 1040), (700, 1376, 512)])
+def test_each_kernel(M, N, K, out, rows_a_tile):
+    c = Case(M, N, K)
+    c.run(out, 1.0, 0.0, want_path=g.PATH_BLOCKS)
+    assert g.last_tile_n() == rows_a_tile
+    c.run(out, -1.5, 0.5, (16, 32, 3), (0, 16, 1))
+    c.run(out, 2.0, 1.0, (0, 0, 8), (0, 0, 8))
+
+
 @pytest.mark.parametrize("M", [1, 40])
 @pytest.mark.parametrize("N,K", [(1024, 8192), (128, 4096), (4096, 4096), (512, 1000)])
 def test_split_k(M, N, K):
