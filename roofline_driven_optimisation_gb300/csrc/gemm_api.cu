@@ -922,6 +922,13 @@ int route(int tokens, int experts, int top_k, const void* logits, bool bf16, lon
   a.softmax = score == GEMM_ROUTE_SOFTMAX;
   a.renormalise = renormalise != 0;
   a.groups = groups; a.top_groups = top_groups; a.group_best = group_best;
+  a.group_size = experts / groups;
+  const int per = route_experts_per_lane(experts);
+  int lanes = 32;                                   // the largest power of two that all groups can have
+  while (lanes * groups > 32) lanes >>= 1;
+  const int whole = a.group_size / per;
+  a.group_whole = a.group_size % per == 0 && (whole & (whole - 1)) == 0;
+  a.group_lanes = a.group_whole ? whole : lanes;
   a.scale = scale; a.bias = bias;
   a.ids = ids; a.weights = weights; a.offsets = offsets; a.order = order;
   a.counts = static_cast<int*>(workspace);

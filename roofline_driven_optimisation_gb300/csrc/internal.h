@@ -284,6 +284,8 @@ struct RouteArgs {
   long long ld;
   bool bf16, softmax, renormalise;
   int groups, top_groups, group_best;
+  int group_size, group_lanes;   // experts of a group; lanes that look through one (a power of two)
+  bool group_whole;       // a group is group_lanes lanes' experts
   float scale;
   const float* bias;
   int* ids;
@@ -294,6 +296,12 @@ struct RouteArgs {
   bool vec;               // 16-byte-aligned rows
 };
 constexpr int kRouteMaxExperts = 1024, kRouteMaxTopK = 32, kRouteMaxGroups = 32;
+// a power of two: 1 to 32 for up to 1024 experts
+constexpr int route_experts_per_lane(int experts) {
+  int per = 1;
+  while (per * 32 < experts) per *= 2;
+  return per;
+}
 size_t route_ws_bytes(int tokens, int experts);
 int launch_route(const RouteArgs& a, cudaStream_t s);
 

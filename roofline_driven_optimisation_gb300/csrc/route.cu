@@ -37,7 +37,6 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kPlaceWarps = 8;                 // segments of a block's slots in place_slots
-constexpr int kPlaceThreads = kPlaceWarps * 32;
 
 template <typename T>
 __device__ __forceinline__ float route_f32(T v);
@@ -47,7 +46,7 @@ template <>
 __device__ __forceinline__ float route_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 // Logits as the scores see them: NaN counts as -inf.
-__device__ __forceinline__ float clean(float l) { return l == l ? l : -INFINITY; }
+__device__ __forceinline__ float clean(float l) { return fmaxf(l, -INFINITY); }
 
 // A whole number that orders as the float does (-0 as +0); 0 is below every float's.
 __device__ __forceinline__ uint32_t key_of(float f) {
@@ -56,6 +55,18 @@ __device__ __forceinline__ uint32_t key_of(float f) {
 }
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// The same of a double; compared as a whole number (a handful of cycles, where the few
+// fp64 units take tens).
+__device__ __forceinline__ uint64_t key_of(double f) {
+  const uint64_t u = (uint64_t)__double_as_longlong(f + 0.0);
+  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+  const uint32_t hi = __reduce_max_sync(kFull, (uint32_t)(v >> 32));
+  const uint32_t lo = __reduce_max_sync(kFull, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return ((uint64_t)hi << 32) | lo;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -84,6 +95,20 @@ __device__ __forceinline__ F score_of(bool softmax, float l, float m, F sum) {
   return (F)1 / ((F)1 + exp(-(F)l));
 }
 
+// exp and 1/x a few units of 2^-24 off (exp by one more for each unit of |x|, as its
+// argument is rounded); what is below 2^-126 is 0
+__device__ __forceinline__ float exp_near(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
+  return e;
+}
+__device__ __forceinline__ float rcp_near(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float sigmoid_near(float l) { return rcp_near(1.f + exp_near(-l)); }
+
 // How far apart two choices in 64 bits may be whose fp32 forms are equal, for a score s
 // and a choice c: 128 units of the last place of s cover expf of arguments down to its
 // underflow and the sum of 1024 terms; a sigmoid is off by at most 3 * 2^-24; and the
@@ -93,72 +118,108 @@ __device__ __forceinline__ float slack(bool softmax, float s, float c) {
   return of_s + 0x1p-22f * fabsf(c);
 }
 
-// A token done again in fp64 by its warp: choices in `ch` (E values of shared memory),
-// winners to lane j's return value.  `bias` may be null (groups alone decide by sums).
+// fp64 scores, out of line: the code of the rare paths is read from L2 when it is met, and
+// every kilobyte of it costs about a microsecond.
+__device__ __noinline__ double score_64(bool softmax, float l, float m, double sum) {
+  return score_of<double>(softmax, l, m, sum);
+}
+
+// A token done again in fp64 by its block (all threads call it): an expert a thread, so
+// that the scores take one fp64 latency, then one warp ranks.  ch: E values of shared
+// memory.
 template <typename T>
-__device__ __noinline__ int route_exactly(const RouteArgs& a, const T* logits, double* ch, float m, int lane) {
-  const int E = a.experts;
-  double sum = 0.0;
+__device__ __noinline__ void route_exactly(const RouteArgs& a, long long t, double* ch, int* hist) {
+  __shared__ double all;
+  const T* logits = static_cast<const T*>(a.logits) + t * a.ld;
+  const int E = a.experts, lane = threadIdx.x % 32;
+  float m = -INFINITY;
   if (a.softmax) {
-    for (int e = lane; e < E; e += 32) sum += soft_term<double>(clean(route_f32(logits[e])), m);
-    sum = warp_sum(sum);
+    for (int e = lane; e < E; e += 32) m = fmaxf(m, clean(route_f32(logits[e])));
+    m = warp_max(m);
+#pragma unroll 1
+    for (int e = threadIdx.x; e < E; e += blockDim.x) ch[e] = score_64(true, clean(route_f32(logits[e])), m, 1.0);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      double sum = 0.0;
+      for (int e = lane; e < E; e += 32) sum += ch[e];
+      sum = warp_sum(sum);
+      if (lane == 0) all = sum;
+    }
+    __syncthreads();
   }
-  for (int e = lane; e < E; e += 32) {
-    double c = score_of<double>(a.softmax, clean(route_f32(logits[e])), m, sum);
+  const double sum = a.softmax ? all : 0.0;
+#pragma unroll 1
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    double c = a.softmax ? (sum > 0.0 ? ch[e] / sum : 0.0) : score_64(false, clean(route_f32(logits[e])), m, sum);
     if (a.bias != nullptr) {
       const float b = a.bias[e];
-      c = b < INFINITY ? c + (double)b : -INFINITY;
+      c = b < INFINITY ? c + (double)b : -INFINITY;      // NaN and +inf too: such an expert comes last
     }
     ch[e] = c;
   }
-  __syncwarp();
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
   uint32_t kept = kFull;
-  const int G = a.groups, S = E / G;
+  const int G = a.groups, S = a.group_size;
   if (G > 1) {
-    double g = -INFINITY;
+    uint64_t g = 0;
     if (lane < G) {
-      double b1 = -INFINITY, b2 = -INFINITY;
+      uint64_t b1 = 0, b2 = 0;
+      double v1 = -INFINITY, v2 = -INFINITY;
+#pragma unroll 1
       for (int i = 0; i < S; ++i) {
         const double c = ch[lane * S + i];
-        if (c > b1) { b2 = b1; b1 = c; } else if (c > b2) { b2 = c; }
+        const uint64_t k = key_of(c);
+        if (k > b1) { b2 = b1; v2 = v1; b1 = k; v1 = c; } else if (k > b2) { b2 = k; v2 = c; }
       }
-      g = a.group_best == 2 && S > 1 ? b1 + b2 : b1;
+      g = key_of(a.group_best == 2 && S > 1 ? v1 + v2 : v1);
     }
     int ahead = 0;
+#pragma unroll 1
     for (int o = 0; o < G; ++o) {
-      const double v = __shfl_sync(kFull, g, o);
+      const uint64_t v = __shfl_sync(kFull, g, o);
       ahead += v > g || (v == g && o < lane);
     }
     kept = __ballot_sync(kFull, lane < G && ahead < a.top_groups);
   }
-  // without a bias experts rank by their logits
-  int mine = 0;
-  double last = INFINITY;
-  int last_e = -1;                       // ranks so far end at (last, last_e)
-  for (int j = 0; j < a.top_k; ++j) {
-    double best = 0.0;
-    int at = E;
-    for (int e = lane; e < E; e += 32) {
-      if (G > 1 && !((kept >> (e / S)) & 1u)) continue;
-      const double c = a.bias != nullptr ? ch[e] : (double)clean(route_f32(logits[e]));
-      if (j > 0 && !(c < last || (c == last && e > last_e))) continue;
-      if (at == E || c > best) { best = c; at = e; }
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-      const double ob = __shfl_xor_sync(kFull, best, d);
-      const int oe = __shfl_xor_sync(kFull, at, d);
-      if (oe < E && (at == E || ob > best || (ob == best && oe < at))) { best = ob; at = oe; }
-    }
-    last = best;
-    last_e = at;
-    if (lane == j) mine = at;
+  // keys in the choices' place; without a bias experts rank by their logits
+  uint64_t* key = reinterpret_cast<uint64_t*>(ch);
+  __syncwarp();
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) {
+    const double c = a.bias != nullptr ? ch[e] : (double)clean(route_f32(logits[e]));
+    key[e] = G == 1 || ((kept >> (e / S)) & 1u) ? key_of(c) : 0ull;
   }
-  return mine;
+  int id = 0;
+#pragma unroll 1
+  for (int j = 0; j < a.top_k; ++j) {
+    uint64_t best = 0;
+    int at = lane;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32)
+      if (key[e] > best) { best = key[e]; at = e; }
+    const uint64_t top = warp_max(best);
+    // of the lanes that have it the one with the lowest expert
+    const uint32_t e = __reduce_min_sync(kFull, best == top ? (uint32_t)at : 0xffffffffu);
+    if (lane == j) id = (int)e;
+    if ((uint32_t)at == e && best == top) key[e] = 0;
+  }
+  double w = lane < a.top_k ? score_64(a.softmax, clean(route_f32(logits[id])), m, sum) : 0.0;
+  if (a.renormalise) {
+    const double total = warp_sum(w);
+    w = total > 0.0 ? w / total : 0.0;
+  }
+  if (lane < a.top_k) {
+    a.ids[t * a.top_k + lane] = id;
+    a.weights[t * a.top_k + lane] = (float)w * a.scale;
+    if (hist != nullptr) atomicAdd(hist + id, 1);
+  }
 }
 
 // The ranking of one token in fp32.  key[i]: lane's experts, 0 where there is none.
-// Lane j returns the j-th expert; *close is set where fp32 cannot tell.
+// Lane j returns the j-th expert.  Where fp32 cannot tell two neighbours apart, the
+// experts down to the first that is clearly behind the last rank (32 at most) are ranked
+// again by their choices in fp64, a lane each; *close is set where that does not do.
 template <typename T, int PER>
 __device__ __forceinline__ int rank_keys(const RouteArgs& a, const T* logits, uint32_t (&key)[PER], float m, float sum,
                                          int lane, bool* close) {
@@ -167,8 +228,9 @@ __device__ __forceinline__ int rank_keys(const RouteArgs& a, const T* logits, ui
 #pragma unroll
   for (int i = 0; i < PER; ++i)
     if (key[i] > best) { best = key[i]; at = i; }
-  int mine = 0, prev = -1;
-  float prev_c = 0.f;
+  int mine = 0, prev = -1, ranked = 0;
+  float prev_c = 0.f, last_c = 0.f;
+  bool unsure = false;
   for (int j = 0;; ++j) {
     if (j >= a.top_k && a.bias == nullptr) break;       // ranks of logits are exact
     const uint32_t k = __reduce_max_sync(kFull, best);
@@ -183,16 +245,20 @@ __device__ __forceinline__ int rank_keys(const RouteArgs& a, const T* logits, ui
         const float bp = a.bias[prev], be = a.bias[e];
         tie = (lp == le && bp == be) || (c == -INFINITY && prev_c == -INFINITY);
         const float s = fmaxf(score_of<float>(a.softmax, lp, m, sum), score_of<float>(a.softmax, le, m, sum));
-        if (!tie && !(prev_c - c > slack(a.softmax, s, fmaxf(fabsf(c), fabsf(prev_c))))) {
-          *close = true;
-          break;
-        }
+        if (!tie && !(prev_c - c > slack(a.softmax, s, fmaxf(fabsf(c), fabsf(prev_c))))) unsure = true;
       }
-      if (j >= a.top_k && !tie) break;
+      // past the last rank: on while it may still belong before it
+      if (j >= a.top_k && !tie && !(unsure && !(last_c - c > 0x1p-15f * (1.f + fabsf(c))))) break;
+      if (j == a.top_k - 1) last_c = c;
+      if (j == 32) {                                    // no lane is left for the next
+        *close = true;
+        break;
+      }
       prev = e;
       prev_c = c;
     }
     if (lane == j) mine = e;
+    ranked = j + 1;
     if (lane == w) {
       best = 0;
       const int gone = at;
@@ -203,29 +269,123 @@ __device__ __forceinline__ int rank_keys(const RouteArgs& a, const T* logits, ui
       }
     }
   }
+  if (unsure && !*close) {
+    double all = 0.0;
+    if (a.softmax) {
+#pragma unroll 1
+      for (int e = lane; e < a.experts; e += 32) all += score_64(true, clean(route_f32(logits[e])), m, 1.0);
+      all = warp_sum(all);
+    }
+    uint64_t c = 0;
+    if (lane < ranked) {
+      const float b = a.bias[mine];
+      c = key_of(b < INFINITY ? score_64(a.softmax, clean(route_f32(logits[mine])), m, all) + (double)b : -INFINITY);
+    }
+    int rank = 0;
+    for (int o = 0; o < ranked; ++o) {
+      const uint64_t v = __shfl_sync(kFull, c, o);
+      const int e = __shfl_sync(kFull, mine, o);
+      rank += v > c || (v == c && e < mine);
+    }
+    int sorted = 0;
+    for (int o = 0; o < ranked; ++o) {
+      const int e = __shfl_sync(kFull, mine, o);
+      if (__shfl_sync(kFull, rank, o) == lane) sorted = e;
+    }
+    mine = sorted;
+  }
   return mine;
 }
 
-// Groups: choices are in ch (E floats of shared memory).  Returns the kept groups as
-// bits; *close is set where fp32 cannot tell the last kept from the first left out.
-__device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const float* ch, int lane, bool* close) {
-  const int G = a.groups, S = a.experts / G;
-  // lanes of a group: the largest power of two that all groups can have
-  int per = 32;
-  while (per * G > 32) per >>= 1;
-  const int group = lane / per, part = lane % per;
-  float b1 = -INFINITY, b2 = -INFINITY;
-  if (group < G)
-    for (int i = part; i < S; i += per) {
-      const float c = ch[group * S + i];
-      b2 = fmaxf(b2, fminf(b1, c));
-      b1 = fmaxf(b1, c);
+// The same for up to 256 experts, with keys whose last 8 bits are the expert's number
+// (inverted: of equal ones the lowest is largest), so that one redux gives a rank.  Each
+// lane's keys are sorted once, and a lane that won moves its keys up.  24 bits of a choice
+// tell most neighbours apart; *unsure is set where they do not, and rank_keys decides.
+template <int PER>
+__device__ __forceinline__ int rank_packed(const RouteArgs& a, const uint32_t (&key)[PER], int lane, bool* unsure) {
+  uint32_t q[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) q[i] = key[i] ? (key[i] & ~0xffu) | (0xffu - (uint32_t)(lane * PER + i)) : 0u;
+  auto order = [&](int i, int j) {
+    const uint32_t hi = max(q[i], q[j]), lo = min(q[i], q[j]);
+    q[i] = hi;
+    q[j] = lo;
+  };
+  if constexpr (PER == 2) {
+    order(0, 1);
+  } else if constexpr (PER >= 4) {
+#pragma unroll
+    for (int h = 0; h < PER; h += 4) {                  // networks of 5 and of 19 comparators
+      order(h, h + 1); order(h + 2, h + 3); order(h, h + 2); order(h + 1, h + 3); order(h + 1, h + 2);
     }
-  for (int d = per >> 1; d; d >>= 1) {
+    if constexpr (PER == 8) {
+      order(0, 4); order(1, 5); order(2, 6); order(3, 7); order(2, 4); order(3, 5); order(1, 2); order(3, 4); order(5, 6);
+    }
+  }
+  uint32_t mine = 0;                                    // lane j: the j-th key
+  for (int j = 0; j <= a.top_k; ++j) {
+    const uint32_t k = __reduce_max_sync(kFull, q[0]);
+    if (lane == j) mine = k;
+    const bool won = q[0] == k;
+#pragma unroll
+    for (int i = 0; i + 1 < PER; ++i) q[i] = won ? q[i + 1] : q[i];
+    q[PER - 1] = won ? 0u : q[PER - 1];
+  }
+  // neighbours; a key of 0 is none.  24 bits hold a bf16 logit whole, and order fp32 logits
+  // where they differ
+  const uint32_t before = __shfl_up_sync(kFull, mine, 1);
+  bool near = false;
+  if (lane > 0 && lane <= a.top_k && mine != 0) {
+    if (a.bias == nullptr) {
+      near = !a.bf16 && (before >> 8) == (mine >> 8);
+    } else {
+      const float hi = of_key(before & ~0xffu), lo = of_key(mine | 0xffu);
+      near = !(hi - lo > 0x1p-15f * (1.f + fabsf(lo)));               // well above slack()
+    }
+  }
+  *unsure = __any_sync(kFull, near) || a.top_k == 32;    // of 33 ranks the last has no lane
+  return (int)(0xffu - (mine & 0xffu));
+}
+
+// The two largest of this lane's and the others' (lanes that differ in bits below `span`).
+__device__ __forceinline__ void best_two(float& b1, float& b2, int span) {
+  for (int d = span >> 1; d; d >>= 1) {
     const float o1 = __shfl_xor_sync(kFull, b1, d), o2 = __shfl_xor_sync(kFull, b2, d);
     b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
     b1 = fmaxf(b1, o1);
   }
+}
+
+// Which groups are kept, as bits.  c: this lane's choices (-inf where there is no expert);
+// ch: E floats of shared memory.  *close is set where fp32 cannot tell the last kept group
+// from the first left out.
+template <int PER>
+__device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const float (&c)[PER], float* ch, int lane, bool* close) {
+  const int G = a.groups, S = a.group_size;
+  int per = a.group_lanes;             // lanes of a group, a power of two
+  float b1 = -INFINITY, b2 = -INFINITY;
+  if (a.group_whole) {                 // each group is whole lanes: all in registers
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      b2 = fmaxf(b2, fminf(b1, c[i]));
+      b1 = fmaxf(b1, c[i]);
+    }
+  } else {
+    const int e0 = lane * PER;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (e0 + i < a.experts) ch[e0 + i] = c[i];
+    __syncwarp();
+    const int group = lane / per, part = lane % per;
+    if (group < G)
+      for (int i = part; i < S; i += per) {
+        const float v = ch[group * S + i];
+        b2 = fmaxf(b2, fminf(b1, v));
+        b1 = fmaxf(b1, v);
+      }
+    __syncwarp();
+  }
+  best_two(b1, b2, per);
   const float g = a.group_best == 2 && S > 1 ? b1 + b2 : b1;
   // ranks of the groups: lane i < G looks at group i
   const float mine = __shfl_sync(kFull, g, min(lane * per, 31));
@@ -245,10 +405,12 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const float*
   return kept;
 }
 
-// Shared memory of a block: E counts, then per warp E choices of 8 bytes (fp64 path; as
-// floats for the groups).
+// bias: this lane's experts' (0 without one); ch: E floats of the warp's own, where groups
+// are not whole lanes.  A token that fp32 cannot route is marked by ids of -1 and counted
+// in *slow.
 template <typename T, int PER>
-__device__ __forceinline__ void route_token(const RouteArgs& a, long long t, double* ch, int* hist, int lane) {
+__device__ __forceinline__ void route_token(const RouteArgs& a, long long t, const float (&bias)[PER], float* ch, int* hist,
+                                            int* slow, int lane) {
   const T* logits = static_cast<const T*>(a.logits) + t * a.ld;
   const int E = a.experts;
   float l[PER];
@@ -273,46 +435,46 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, long long t, dou
     for (int i = 0; i < PER; ++i) l[i] = e0 + i < E ? clean(route_f32(logits[e0 + i])) : -INFINITY;
   }
   float m = 0.f, sum = 0.f;
+  float c[PER];
   if (a.softmax) {
     m = l[0];
 #pragma unroll
     for (int i = 1; i < PER; ++i) m = fmaxf(m, l[i]);
     m = warp_max(m);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) sum += e0 + i < E ? soft_term<float>(l[i], m) : 0.f;
+    for (int i = 0; i < PER; ++i) {
+      c[i] = e0 + i < E ? soft_term<float>(l[i], m) : 0.f;
+      sum += c[i];
+    }
     sum = warp_sum(sum);
   }
   uint32_t key[PER];
   bool close = false;
-  if (a.bias != nullptr || a.groups > 1) {
+  if (a.choices) {
     const float r = a.softmax && sum > 0.f ? 1.f / sum : 0.f;
-    float c[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      // __expf and the product with 1/sum stay inside slack()'s 128 units
-      float s = a.softmax ? soft_term<float>(l[i], m) * r : __fdividef(1.f, 1.f + __expf(-l[i]));
-      if (!a.softmax && l[i] < -80.f) s = score_of<float>(false, l[i], 0.f, 0.f);   // __fdividef's own range ends there
-      if (a.bias != nullptr && e0 + i < E) {
-        const float b = __ldg(a.bias + e0 + i);
-        s = b < INFINITY ? s + b : -INFINITY;      // NaN and +inf too: such an expert comes last
-      }
-      c[i] = s;
+      // the approximate operations and the product with 1/sum stay inside slack()'s units
+      float s = a.softmax ? c[i] * r : sigmoid_near(l[i]);
+      if (a.bias != nullptr) s += bias[i];               // -inf: the expert comes last
+      c[i] = e0 + i < E ? s : -INFINITY;
       key[i] = e0 + i < E ? key_of(a.bias != nullptr ? s : l[i]) : 0u;
     }
     if (a.groups > 1) {
-      float* chf = reinterpret_cast<float*>(ch);
+      const uint32_t kept = keep_groups<PER>(a, c, ch, lane, &close);
+      if (a.group_whole) {
+        if (!((kept >> ((lane / a.group_lanes) & 31)) & 1u)) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (e0 + i < E) chf[e0 + i] = c[i];
-      __syncwarp();
-      const uint32_t kept = keep_groups(a, chf, lane, &close);
-      __syncwarp();
-      const int S = E / a.groups;
-      int g = e0 / S, left = S - e0 % S;     // this lane's experts run through the groups in order
+          for (int i = 0; i < PER; ++i) key[i] = 0u;
+        }
+      } else {
+        const int S = a.group_size;
+        int g = e0 / S, left = S - e0 % S;     // this lane's experts run through the groups in order
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        if (!((kept >> (g & 31)) & 1u)) key[i] = 0u;
-        if (--left == 0) { ++g; left = S; }
+        for (int i = 0; i < PER; ++i) {
+          if (!((kept >> (g & 31)) & 1u)) key[i] = 0u;
+          if (--left == 0) { ++g; left = S; }
+        }
       }
     }
   } else {
@@ -320,14 +482,31 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, long long t, dou
     for (int i = 0; i < PER; ++i) key[i] = e0 + i < E ? key_of(l[i]) : 0u;
   }
   int id = 0;
-  if (!close) id = rank_keys<T, PER>(a, logits, key, m, sum, lane, &close);
-  if (close) id = route_exactly<T>(a, logits, ch, m, lane);
+  bool unsure = true;
+  if (!close) {
+    if constexpr (PER <= 8) id = rank_packed<PER>(a, key, lane, &unsure);
+    if (unsure) id = rank_keys<T, PER>(a, logits, key, m, sum, lane, &close);
+  }
+  if (close) {
+    if (lane == 0) {
+      a.ids[t * a.top_k] = -1;
+      atomicAdd(slow, 1);
+    }
+    return;
+  }
   // weights of the chosen, from their logits again
   const bool mine = lane < a.top_k;
-  float w = mine ? score_of<float>(a.softmax, clean(route_f32(logits[id])), m, sum) : 0.f;
+  const float lw = mine ? clean(route_f32(logits[id])) : 0.f;
+  float w = 0.f;
+  if (mine) {
+    if (a.softmax) w = sum > 0.f && m < INFINITY ? exp_near(lw - m) * rcp_near(sum) : score_of<float>(true, lw, m, sum);
+    else w = rcp_near(1.f + exp_near(-lw));
+  }
+  // scores so small that the fast operations lose them: the others' way
+  if (__any_sync(kFull, mine && !(w > 0x1p-100f)) && mine) w = score_of<float>(a.softmax, lw, m, sum);
   if (a.renormalise) {
     const float all = warp_sum(w);
-    w = all > 0.f ? w / all : 0.f;
+    w = all > 0x1p-100f ? w * rcp_near(all) : all > 0.f ? w / all : 0.f;
   }
   if (mine) {
     a.ids[t * a.top_k + lane] = id;
@@ -361,12 +540,18 @@ __device__ __forceinline__ void place_slots(const RouteArgs& a, long long s0, lo
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = a.experts;
   const long long each = ((s1 - s0 + kPlaceWarps - 1) / kPlaceWarps + 31) / 32 * 32;
   const long long b = s0 + warp * each, e = b + each < s1 ? b + each : s1;
+  constexpr int U = 4;                   // loads in flight
   if (warp < kPlaceWarps)
-    for (long long s = b; s < e; s += 32) {
-      const int id = s + lane < e ? a.ids[s + lane] : -1;
-      const uint32_t same = __match_any_sync(kFull, id);
-      if (id >= 0 && (same & ((1u << lane) - 1u)) == 0) at[warp * E + id] += __popc(same);
-      __syncwarp();
+    for (long long s = b; s < e; s += 32 * U) {
+      int id[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) id[u] = s + u * 32 + lane < e ? a.ids[s + u * 32 + lane] : -1;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t same = __match_any_sync(kFull, id[u]);
+        if (id[u] >= 0 && (same & ((1u << lane) - 1u)) == 0) at[warp * E + id[u]] += __popc(same);
+        __syncwarp();
+      }
     }
   __syncthreads();
   for (int x = threadIdx.x; x < E; x += blockDim.x) {
@@ -380,19 +565,32 @@ __device__ __forceinline__ void place_slots(const RouteArgs& a, long long s0, lo
   }
   __syncthreads();
   if (warp < kPlaceWarps)
-    for (long long s = b; s < e; s += 32) {
-      const int id = s + lane < e ? a.ids[s + lane] : -1;
-      const uint32_t same = __match_any_sync(kFull, id);
-      const uint32_t before = same & ((1u << lane) - 1u);
-      int first = 0;
-      if (id >= 0) first = at[warp * E + id];
-      __syncwarp();
-      if (id >= 0) {
-        a.order[first + __popc(before)] = (int)(s + lane);
-        if (before == 0) at[warp * E + id] = first + __popc(same);
+    for (long long s = b; s < e; s += 32 * U) {
+      int id[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) id[u] = s + u * 32 + lane < e ? a.ids[s + u * 32 + lane] : -1;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t same = __match_any_sync(kFull, id[u]);
+        const uint32_t before = same & ((1u << lane) - 1u);
+        int first = 0;
+        if (id[u] >= 0) first = at[warp * E + id[u]];
+        __syncwarp();
+        if (id[u] >= 0) {
+          a.order[first + __popc(before)] = (int)(s + u * 32 + lane);
+          if (before == 0) at[warp * E + id[u]] = first + __popc(same);
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
+}
+
+// Counts of a block: rows of whole 16-byte vectors
+__host__ __device__ constexpr int count_stride(int experts) { return (experts + 3) / 4 * 4; }
+
+// Doubles of shared memory for choices: a token's in fp64, and a row of floats for each warp
+__host__ __device__ inline int route_smem_choices(const RouteArgs& a, int warps) {
+  return a.choices ? a.experts + (a.groups > 1 && !a.group_whole ? (warps * a.experts + 1) / 2 : 0) : 0;
 }
 
 template <int PER>
@@ -400,25 +598,48 @@ constexpr int route_threads() { return PER <= 8 ? 1024 : 256; }
 
 // Block b routes tokens [b*chunk, (b+1)*chunk).  One block alone also places them.
 template <typename T, int PER>
-__global__ void __launch_bounds__(route_threads<PER>()) route_kernel(const RouteArgs a, int chunk) {
+__global__ void __launch_bounds__(route_threads<PER>()) route_kernel(const __grid_constant__ RouteArgs a, int chunk) {
   extern __shared__ double route_smem[];
+  __shared__ int slow, list[route_threads<PER>()];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32, E = a.experts;
-  const int wide = a.choices ? E : 0;
-  double* ch = route_smem + (size_t)warp * wide;
-  int* hist = reinterpret_cast<int*>(route_smem + (size_t)warps * wide);
+  double* exact = route_smem;                            // E choices in fp64, of one token at a time
+  float* ch = reinterpret_cast<float*>(exact + (a.choices ? E : 0)) + (a.groups > 1 && !a.group_whole ? warp * E : 0);
+  int* hist = reinterpret_cast<int*>(route_smem + route_smem_choices(a, warps));
   const bool plan = a.offsets != nullptr;
+  if (threadIdx.x == 0) slow = 0;
   if (plan)
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
   griddep_wait();
   __syncthreads();
   const long long t0 = (long long)blockIdx.x * chunk;
   const long long t1 = t0 + chunk < a.tokens ? t0 + chunk : a.tokens;
-  for (long long t = t0 + warp; t < t1; t += warps) route_token<T, PER>(a, t, ch, plan ? hist : nullptr, lane);
-  if (!plan) return;
+  float bias[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const float b = a.bias != nullptr && lane * PER + i < E ? a.bias[lane * PER + i] : 0.f;
+    bias[i] = b < INFINITY ? b : -INFINITY;              // NaN and +inf too: such an expert comes last
+  }
+  for (long long t = t0 + warp; t < t1; t += warps) route_token<T, PER>(a, t, bias, ch, plan ? hist : nullptr, &slow, lane);
   __syncthreads();
+  if (slow > 0) {                                        // marked by warps of this block: a list, then one by one
+    __syncthreads();
+    for (long long at = t0; at < t1; at += blockDim.x) {
+      if (threadIdx.x == 0) slow = 0;
+      __syncthreads();
+      const long long t = at + threadIdx.x;
+      if (t < t1 && a.ids[t * a.top_k] < 0) list[atomicAdd(&slow, 1)] = (int)(t - at);
+      __syncthreads();
+      const int n = slow;
+      for (int i = 0; i < n; ++i) {
+        route_exactly<T>(a, at + list[i], exact, plan ? hist : nullptr);
+        __syncthreads();
+      }
+    }
+  }
+  if (!plan) return;
   if (gridDim.x > 1) {
     griddep_launch_dependents();
-    for (int e = threadIdx.x; e < E; e += blockDim.x) a.counts[(size_t)blockIdx.x * E + e] = hist[e];
+    for (int e = threadIdx.x; e < E; e += blockDim.x) a.counts[(size_t)blockIdx.x * count_stride(E) + e] = hist[e];
     return;
   }
   // ids written by this block's other warps are read back below: __syncthreads orders them
@@ -433,31 +654,46 @@ __global__ void __launch_bounds__(route_threads<PER>()) route_kernel(const Route
   place_slots(a, t0 * a.top_k, t1 * a.top_k, hist, at);
 }
 
-// The same blocks' slots, placed: counts of all blocks and of those before.
-__global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteArgs a, int chunk) {
+// The same blocks' slots, placed: counts of all blocks and of those before.  A thread
+// adds four experts' counts of some of the blocks, eight rows in flight at a time.
+constexpr int kPlaceKernelThreads = 1024;
+__global__ void __launch_bounds__(kPlaceKernelThreads) route_place_kernel(const __grid_constant__ RouteArgs a, int chunk) {
   extern __shared__ int place_smem[];
   const int E = a.experts, lane = threadIdx.x % 32;
   int *total = place_smem, *before = total + E, *at = before + E;
   for (int x = threadIdx.x; x < (2 + kPlaceWarps) * E; x += blockDim.x) place_smem[x] = 0;
   griddep_wait();
   __syncthreads();
-  // columns of 32 experts by warps: each warp takes a column's rows in turn with the others
-  const int warp = threadIdx.x / 32, blocks = gridDim.x, columns = (E + 31) / 32;
-  const int share = columns >= kPlaceWarps ? 1 : kPlaceWarps / columns;     // warps of a column
-  for (int c = warp / share; c < columns; c += kPlaceWarps / share) {
-    const int e = c * 32 + lane;
-    int all = 0, mine = 0;
-    if (e < E)
-#pragma unroll 16
-      for (int b = warp % share; b < blocks; b += share) {
-        const int n = __ldcg(a.counts + (size_t)b * E + e);
-        all += n;
-        mine += b < (int)blockIdx.x ? n : 0;
+  const int stride4 = count_stride(E) / 4, blocks = gridDim.x;
+  const int parts = kPlaceKernelThreads / stride4;       // at least 4: E is 1024 at most
+  const int part = threadIdx.x / stride4, e4 = threadIdx.x % stride4;
+  if (part < parts) {
+    const int4* rows = reinterpret_cast<const int4*>(a.counts) + e4;
+    int all[4] = {0, 0, 0, 0}, mine[4] = {0, 0, 0, 0};
+    for (int b0 = part; b0 < blocks; b0 += 8 * parts) {
+      int4 n[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int b = b0 + u * parts;
+        n[u] = b < blocks ? rows[(size_t)b * stride4] : make_int4(0, 0, 0, 0);
       }
-    if (e < E) {
-      atomicAdd(total + e, all);            // whole numbers: any order gives the same sum
-      atomicAdd(before + e, mine);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const bool earlier = b0 + u * parts < (int)blockIdx.x;
+        const int v[4] = {n[u].x, n[u].y, n[u].z, n[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          all[i] += v[i];
+          mine[i] += earlier ? v[i] : 0;
+        }
+      }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e4 * 4 + i < E) {                  // whole numbers: any order gives the same sum
+        atomicAdd(total + e4 * 4 + i, all[i]);
+        atomicAdd(before + e4 * 4 + i, mine[i]);
+      }
   }
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -474,23 +710,25 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteA
   place_slots(a, t0 * a.top_k, t1 * a.top_k, before, at);
 }
 
-// Blocks and tokens a block.  One block where its warps have at most four tokens each
-// (a second launch costs 2 to 3 us, four tokens a warp about as much); else up to a block
-// of 32 warps, or four of 8, on each of a GB300's 152 SMs.
+// Warps a block, blocks and tokens a block.  A token is some 700 instructions of a warp, so
+// that 32 warps of one SM take 3 us for a token each: one block alone (which saves the
+// second launch, 2 us) for a token a warp of 16 at most, then blocks of 8 warps on as many
+// SMs as there are tokens for, and blocks of 32 warps (8 for more than 256 experts, whose
+// registers allow no more) once all of a GB300's 152 SMs have one.
+constexpr int kRouteMaxBlocks = 152;
 struct RoutePlan {
-  int blocks, chunk;
+  int warps, blocks, chunk;
 };
 RoutePlan plan_route(int tokens, int experts) {
-  const int warps = experts <= 256 ? 32 : 8;
-  const int most = experts <= 256 ? 152 : 608;
   RoutePlan p;
-  if (tokens <= 4 * warps) {
+  p.warps = tokens <= 8 ? 8 : tokens <= 16 && experts <= 256 ? 16 : tokens <= 8 * kRouteMaxBlocks || experts > 256 ? 8 : 32;
+  if (tokens <= p.warps) {
     p.blocks = 1;
     p.chunk = tokens;
     return p;
   }
-  const long long want = ((long long)tokens + warps - 1) / warps;
-  const int blocks = want < most ? (int)want : most;
+  const long long want = ((long long)tokens + p.warps - 1) / p.warps;
+  const int blocks = want < kRouteMaxBlocks ? (int)want : kRouteMaxBlocks;
   p.chunk = (tokens + blocks - 1) / blocks;
   p.blocks = (tokens + p.chunk - 1) / p.chunk;
   return p;
@@ -499,12 +737,12 @@ RoutePlan plan_route(int tokens, int experts) {
 template <typename T, int PER>
 int launch_impl(const RouteArgs& a, cudaStream_t s) {
   const RoutePlan p = plan_route(a.tokens, a.experts);
-  const int threads = route_threads<PER>();
-  const size_t smem = (size_t)(threads / 32) * (a.choices ? a.experts : 0) * sizeof(double) +
+  const int threads = p.warps * 32;
+  const size_t smem = (size_t)route_smem_choices(a, p.warps) * sizeof(double) +
                       (size_t)a.experts * (1 + kPlaceWarps) * sizeof(int);
   static std::atomic<uint64_t> done{0};
   cudaError_t e = set_smem_once(done, route_kernel<T, PER>,
-                                (int)((threads / 32) * 32 * PER * sizeof(double) + 32 * PER * (1 + kPlaceWarps) * sizeof(int)));
+                                (int)((route_threads<PER>() / 64 + 1) * 32 * PER * sizeof(double) + 32 * PER * (1 + kPlaceWarps) * sizeof(int)));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.blocks, 1, 1);
@@ -518,18 +756,20 @@ int launch_impl(const RouteArgs& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, route_kernel<T, PER>, a, p.chunk);
   if (e != cudaSuccess || p.blocks == 1 || a.offsets == nullptr) return e;
-  cfg.blockDim = dim3(kPlaceThreads, 1, 1);
+  cfg.blockDim = dim3(kPlaceKernelThreads, 1, 1);
   cfg.dynamicSmemBytes = (size_t)a.experts * (2 + kPlaceWarps) * sizeof(int);
   return cudaLaunchKernelEx(&cfg, route_place_kernel, a, p.chunk);
 }
 
 template <typename T>
 int launch_type(const RouteArgs& a, cudaStream_t s) {
-  if (a.experts <= 32) return launch_impl<T, 1>(a, s);
-  if (a.experts <= 64) return launch_impl<T, 2>(a, s);
-  if (a.experts <= 128) return launch_impl<T, 4>(a, s);
-  if (a.experts <= 256) return launch_impl<T, 8>(a, s);
-  if (a.experts <= 512) return launch_impl<T, 16>(a, s);
+  switch (route_experts_per_lane(a.experts)) {
+    case 1: return launch_impl<T, 1>(a, s);
+    case 2: return launch_impl<T, 2>(a, s);
+    case 4: return launch_impl<T, 4>(a, s);
+    case 8: return launch_impl<T, 8>(a, s);
+    case 16: return launch_impl<T, 16>(a, s);
+  }
   return launch_impl<T, 32>(a, s);
 }
 
@@ -537,7 +777,7 @@ int launch_type(const RouteArgs& a, cudaStream_t s) {
 
 size_t route_ws_bytes(int tokens, int experts) {
   const RoutePlan p = plan_route(tokens, experts);
-  return p.blocks > 1 ? (size_t)p.blocks * experts * sizeof(int) : 0;
+  return p.blocks > 1 ? (size_t)p.blocks * count_stride(experts) * sizeof(int) : 0;
 }
 
 int launch_route(const RouteArgs& a, cudaStream_t s) {
