@@ -573,11 +573,11 @@ int launch_blocks(const BlocksArgs& a, const BlocksPlan& plan, const CUtensorMap
                   const CUtensorMap* mapB2, int num_sms, cudaStream_t s) {
   const int split = plan.split;
   if (a.B2 != nullptr) {
-    if (a.gather == 0) return cudaErrorInvalidValue;
+    if ((a.gather != 0) != (plan.nt == 32)) return cudaErrorInvalidValue;
     switch (plan.nt) {
       case 32: return launch_impl<32, true, true>(a, mapA, mapB, mapB2, split, num_sms, s);
-      case 64: return launch_impl<64, true, true>(a, mapA, mapB, mapB2, split, num_sms, s);
-      case 128: return launch_impl<128, true, true>(a, mapA, mapB, mapB2, split, num_sms, s);
+      case 64: return launch_impl<64, true, false>(a, mapA, mapB, mapB2, split, num_sms, s);
+      case 128: return launch_impl<128, true, false>(a, mapA, mapB, mapB2, split, num_sms, s);
     }
     return cudaErrorInvalidValue;
   }

@@ -14,9 +14,8 @@
 // 128 x 256 sums take 256 cycles of fma.rn.f32x2 (64 a warp, two warps a scheduler, two
 // cycles each), in registers for the whole of K: 128 a thread.
 //
-// Roles (384 threads a CTA): warp 0 copies (each CTA its rows of A, gathered by
-// tile::gather4 where rows are an expert's, and its half of B; all complete on the
-// leader's barrier), warp 1 of the leader issues the MMAs, warp 2 copies the scales of
+// Roles (384 threads a CTA): warp 0 copies (each CTA its rows of A and its half of B; all
+// complete on the leader's barrier), warp 1 of the leader issues the MMAs, warp 2 copies the scales of
 // its CTA's rows into a ring of eight blocks (cp.async, no registers), warps 4-11 drain:
 // warp w the TMEM lanes 32*(w%4)..+31 and half of the columns.
 //
@@ -43,14 +42,22 @@ namespace {
 constexpr int BK = kBlocksK, BM = kBlocksPairRows, BM_CTA = BM / 2;
 constexpr int THREADS = 384, EPI_WARPS = 8, EPI_FIRST = 4;
 constexpr int A_BYTES = BM_CTA * BK, B_BYTES = BK * 128;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES, STAGES = 6;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int TMEM_COLS = 512, COLS = 256, NBUF = 2;
 constexpr int RING = 8, RING_WORDS = BM_CTA + 4;       // scales of a block: the rows', then B's one or two
 constexpr int BOX = 64;
 constexpr int BAR_BYTES = 512;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + RING * RING_WORDS * 4 + 2 * BM_CTA * 4 + kListBytes + BAR_BYTES + 1024;
-static_assert(SMEM_BYTES <= 232448, "shared memory");
-static_assert(8 * (2 * STAGES + 2 * NBUF + 2 * RING + 4) <= BAR_BYTES, "barrier area");
+// Shared memory: the ring of operands, and for each drain warp the rows it is about to
+// store (32 rows of 128 bytes of C, or of 64 codes).
+template <bool SW>
+struct Mem {
+  static constexpr int STAGES = SW ? 6 : 5;
+  static constexpr int OUT_WARP = 32 * (SW ? 64 : 128), OUT_BYTES = EPI_WARPS * OUT_WARP;
+  static constexpr int BYTES = STAGES * STAGE_BYTES + OUT_BYTES + RING * RING_WORDS * 4 + 2 * BM_CTA * 4 + kListBytes +
+                               BAR_BYTES + 1024;
+  static_assert(BYTES <= 232448, "shared memory");
+  static_assert(8 * (2 * STAGES + 2 * NBUF + 2 * RING + 4) <= BAR_BYTES, "barrier area");
+};
 static_assert(blocks_box_rows(kBlocksPairRows, false) == BOX, "boxes of A");
 constexpr uint64_t kDrainGraceNs = 50000;              // after an abort, time for the peer's copies to land
 constexpr uint16_t kBothCtas = 0x3;
@@ -59,6 +66,7 @@ struct Params {
   BlocksArgs a;
   int kblocks, tiles_n;
   int c_vec;                                           // C's rows are 16-byte-aligned vectors
+  int c_rows;                                          // and whole ones, and beta is 0: stored row by row
 };
 
 // Barrier 1 of the 256 drain threads; and the same, returning whether any of them has `p`.
@@ -126,13 +134,51 @@ __device__ __forceinline__ void store32(const Params& p, long long m, int n, con
   }
 }
 
-// SW: gate and up weights, codes out.  GATHER: A's rows through tile::gather4.
+// Rows of 128 bytes (64 bf16 or 32 fp32 columns from n) of a warp's 32 rows of C, by way of
+// shared memory: a thread has a row, and 32 threads writing 16 bytes each of 32 rows take
+// 32 wavefronts where four whole rows of 128 bytes take four.  The 16-byte vectors of a row
+// are permuted by the row's number, so neither side meets a bank twice.  to: this lane's
+// row of C, or -1.
+template <bool OUT_BF16>
+__device__ __forceinline__ void store_rows(const Params& p, uint8_t* out, int to, int n, const uint64_t* v, int lane) {
+  const BlocksArgs& a = p.a;
+  constexpr int PER = OUT_BF16 ? 8 : 4;                // columns of a vector
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (OUT_BF16) {
+        const uint64_t x = v[q * 4 + i];
+        const __nv_bfloat162 b = __floats2bfloat162_rn(a.alpha * part2(x, 0), a.alpha * part2(x, 1));
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      } else {
+        w[i] = __float_as_uint(a.alpha * part2(v[q * 2 + i / 2], i & 1));
+      }
+    }
+    *reinterpret_cast<uint4*>(out + lane * 128 + ((q ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();
+  uint8_t* C = static_cast<uint8_t*>(a.C);
+  const int c = lane & 7;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int row = q * 4 + lane / 8;
+    const long long o = __shfl_sync(0xffffffffu, to, row);
+    if (o >= 0 && n + c * PER < a.N)
+      *reinterpret_cast<uint4*>(C + (o * a.ldc + n) * (OUT_BF16 ? 2 : 4) + c * 16) =
+          *reinterpret_cast<const uint4*>(out + row * 128 + ((c ^ (row & 7)) * 16));
+  }
+  __syncwarp();                                        // read before the next rows are written
+}
+
+// SW: gate and up weights, codes out.
 template <bool SW, bool OUT_BF16>
 __global__ void __launch_bounds__(THREADS, 1)
     blocks_pair_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                        const __grid_constant__ CUtensorMap mapB2, const Params p) {
-  constexpr bool GATHER = SW;
   constexpr int BN = SW ? 128 : 256;                   // columns of C (or of h) an item
+  constexpr int STAGES = Mem<SW>::STAGES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;        // the same offset in both CTAs
@@ -140,6 +186,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto a_tile = [&](int s) { return base + s * STAGE_BYTES; };
   auto b_tile = [&](int s) { return base + s * STAGE_BYTES + A_BYTES; };
   uint8_t* at = base_ptr + STAGES * STAGE_BYTES;
+  uint8_t* out = at;                                   // [EPI_WARPS][OUT_WARP]
+  at += Mem<SW>::OUT_BYTES;
   float* ring = reinterpret_cast<float*>(at);          // [RING][RING_WORDS]
   at += RING * RING_WORDS * 4;
   float* big = reinterpret_cast<float*>(at);           // [2][BM_CTA]
@@ -216,19 +264,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int other = i.rows - mine;
         const int p0 = i.p0 + (int)rank * BM_CTA;
         // rows that are not there are not copied: what their lanes sum up is not read
-        auto copied = [&](int rows) { return GATHER ? (rows + 3) / 4 * 4 : (rows + BOX - 1) / BOX * BOX; };
-        const uint32_t bytes = (uint32_t)(2 * B_BYTES + (copied(mine) + copied(other)) * BK);
-        int y[4];
-        if (GATHER) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            int from = -1, to;
-            if (lane * 4 + q < mine) expert_row(a, p0 + lane * 4 + q, from, to);
-            y[q] = from >= 0 ? from : a.a_rows;        // outside: zeros
-          }
-        }
+        auto copies = [](int rows) { return (rows + BOX - 1) / BOX; };
+        const uint32_t bytes = (uint32_t)(2 * B_BYTES + (copies(mine) + copies(other)) * BOX * BK);
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          if ((GATHER || one) && !mbar_wait(empty_bar(stage), phase ^ 1u, a.timeout_ns, abort_flag)) {
+          if (one && !mbar_wait(empty_bar(stage), phase ^ 1u, a.timeout_ns, abort_flag)) {
             if (!*abort_flag) report_status(a.status, 5, kSiteBlocks2Producer);
             *abort_flag = 1;
             ok = false;
@@ -240,14 +279,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (leader) mbar_arrive_expect_tx(full_bar(stage), bytes);
             tma_load_3d_pair(b_tile(stage), SW && rank == 1 ? &mapB2 : &mapB, full,
                              i.nb * BN + (SW ? 0 : (int)rank * 128), kb * BK, i.e);
-            if (!GATHER)
-              for (int c = 0; c * BOX < mine; ++c)
-                tma_load_2d_pair(a_tile(stage) + c * BOX * BK, &mapA, full, kb * BK, p0 + c * BOX);
-          }
-          if (GATHER) {
-            __syncwarp();
-            if (lane * 4 < mine)
-              tma_gather4_pair(a_tile(stage) + lane * 4 * BK, &mapA, full, kb * BK, y[0], y[1], y[2], y[3]);
+            for (int c = 0; c < copies(mine); ++c)
+              tma_load_2d_pair(a_tile(stage) + c * BOX * BK, &mapA, full, kb * BK, p0 + c * BOX);
           }
           issued |= 1u << stage;
           issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
@@ -446,34 +479,47 @@ __global__ void __launch_bounds__(THREADS, 1)
         sync_drain();
         const float s = kv_scale_for<kKvE4M3>(fmaxf(top, big[(1 - half) * BM_CTA + lrow]));
         const float f = kv_recip(s);
-        if (m < i.rows) {
-          const long long row = (long long)i.p0 + m;
-          uint8_t* q = a.hq + row * a.ldh + n;
+        // 64 codes of this thread's row, then rows of 64 bytes (as store_rows)
+        uint8_t* mine = out + (warp - EPI_FIRST) * Mem<SW>::OUT_WARP;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[4];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint64_t x = acc[c * 8 + 2 * k], y = acc[c * 8 + 2 * k + 1];
-              w[k] = kv_code2<kKvE4M3>(__fmul_rn(part2(x, 0), f), __fmul_rn(part2(x, 1), f)) |
-                     (kv_code2<kKvE4M3>(__fmul_rn(part2(y, 0), f), __fmul_rn(part2(y, 1), f)) << 16);
-            }
-            // rows of a.hq are whole vectors; codes past N are 0
-            if (n + c * 16 < a.ldh) *reinterpret_cast<uint4*>(q + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t x = acc[c * 8 + 2 * k], y = acc[c * 8 + 2 * k + 1];
+            w[k] = kv_code2<kKvE4M3>(__fmul_rn(part2(x, 0), f), __fmul_rn(part2(x, 1), f)) |
+                   (kv_code2<kKvE4M3>(__fmul_rn(part2(y, 0), f), __fmul_rn(part2(y, 1), f)) << 16);
           }
-          if (half == 0) a.hs[row * a.ldhs + i.nb] = s;
+          *reinterpret_cast<uint4*>(mine + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        if (half == 0 && m < i.rows) a.hs[((long long)i.p0 + m) * a.ldhs + i.nb] = s;
+        __syncwarp();
+        const int rows = i.rows - ((int)rank * BM_CTA + quarter * 32);         // of this warp
+        const int c = lane & 3;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = q * 8 + lane / 4;
+          // rows of a.hq are whole vectors; codes past N are 0
+          if (row < rows && n + c * 16 < a.ldh)
+            *reinterpret_cast<uint4*>(a.hq + ((long long)i.p0 + i.rows - rows + row) * a.ldh + n + c * 16) =
+                *reinterpret_cast<const uint4*>(mine + row * 64 + ((c ^ ((row >> 1) & 3)) * 16));
+        }
+        __syncwarp();
       } else {
         if (!ok) break;
-        if (m < i.rows) {
-          int from, to;
-          expert_row(a, i.p0 + m, from, to);
-          if (to >= 0)
+        int from, to = -1;
+        if (m < i.rows) expert_row(a, i.p0 + m, from, to);
+        const int n = i.nb * BN + half * 128;
+        if (p.c_rows) {
+          constexpr int WIDE = OUT_BF16 ? 64 : 32;
+          uint8_t* mine = out + (warp - EPI_FIRST) * Mem<SW>::OUT_WARP;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int n = i.nb * BN + half * 128 + c * 32;
-              if (n < a.N) store32<OUT_BF16>(p, to, n, acc + c * 16);
-            }
+          for (int c = 0; c < 128 / WIDE; ++c)
+            if (n + c * WIDE < a.N) store_rows<OUT_BF16>(p, mine, to, n + c * WIDE, acc + c * WIDE / 2, lane);
+        } else if (to >= 0) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (n + c * 32 < a.N) store32<OUT_BF16>(p, to, n + c * 32, acc + c * 16);
         }
       }
     }
@@ -513,7 +559,7 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.dynamicSmemBytes = Mem<SW>::BYTES;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -525,7 +571,7 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
       // 128 threads at 88 registers and 256 at 208 are 384 * 168: with fewer at launch the
       // warps that take some would wait forever
       if (fa.numRegs < 168) return cudaErrorInvalidConfiguration;
-      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES)) != cudaSuccess)
+      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Mem<SW>::BYTES)) != cudaSuccess)
         return e;
       int n = 0;
       cfg.gridDim = dim3(2 * (num_sms / 2), 1, 1);
@@ -540,6 +586,7 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
   p.tiles_n = (a.N + (SW ? 128 : 256) - 1) / (SW ? 128 : 256);
   const int osz = OUT_BF16 ? 2 : 4;
   p.c_vec = ((reinterpret_cast<uintptr_t>(a.C) & 15u) == 0 && (a.ldc * osz) % 16 == 0) ? 1 : 0;
+  p.c_rows = p.c_vec != 0 && a.N % (16 / osz) == 0 && a.beta == 0.f ? 1 : 0;
   const long long items = blocks_row_tiles(a.rows, a.offsets != nullptr ? a.experts : 1, BM) * p.tiles_n;
   const long long clusters = items < info[dev].max_clusters ? items : info[dev].max_clusters;
   cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
@@ -551,7 +598,7 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
 
 int launch_blocks_pair(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap* mapB, const CUtensorMap* mapB2,
                        int num_sms, cudaStream_t s) {
-  if ((a.B2 != nullptr) != (a.gather != 0)) return cudaErrorInvalidValue;
+  if (a.gather != 0) return cudaErrorInvalidValue;
   if (a.B2 != nullptr) return launch_impl<true, true>(a, mapA, mapB, mapB2, num_sms, s);
   return a.out_bf16 ? launch_impl<false, true>(a, mapA, mapB, mapB2, num_sms, s)
                     : launch_impl<false, false>(a, mapA, mapB, mapB2, num_sms, s);

@@ -71,37 +71,59 @@ __device__ __forceinline__ void store8(uint8_t* q, int n, bool vec, float r, con
   }
 }
 
-// 1 x 128: sixteen lanes a block of values, U blocks of a half warp in flight
-// (consecutive in memory across the half warps, so that a warp reads 512 bytes).
-template <typename T, int U>
-__global__ void __launch_bounds__(THREADS) quantise_rows_kernel(const QuantiseArgs a, long long blocks, int per_row) {
+// 1 x 128: a warp 8 blocks of a row, sixteen lanes a block, every load in flight before
+// the first maximum.  With `place`, row r is written `copies` times, to rows place[r *
+// copies + j] of the codes and scales (each slot of a token's, in the order of experts).
+template <typename T, bool PLACED>
+__global__ void __launch_bounds__(THREADS) quantise_rows_kernel(const __grid_constant__ QuantiseArgs a, int groups) {
+  constexpr int U = 4;
   griddep_wait();
-  const int lane = threadIdx.x % HALF;
-  const long long half = (long long)blockIdx.x * HALVES + threadIdx.x / HALF;
-  const long long step = (long long)gridDim.x * HALVES;
-  const T* X = static_cast<const T*>(a.x);
-  for (long long b0 = half; (b0 & ~1ll) < blocks; b0 += step * U) {     // a warp's halves together: they shuffle
-    float v[U][8];
-    long long row[U];
-    int col[U], n[U];
+  const int lane = threadIdx.x % 32;
+  const long long unit = (long long)blockIdx.x * (THREADS / 32) + threadIdx.x / 32;
+  const long long row = unit / groups;
+  if (row >= a.rows) return;
+  const int col0 = (int)(unit - row * groups) * (2 * U * QB) + lane * 8;       // lanes 16 .. 31 the next block
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  float v[U][8];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long b = b0 + u * step;
-      row[u] = b / per_row;
-      col[u] = (int)(b % per_row) * QB + lane * 8;
-      n[u] = b < blocks ? min(max(a.cols - col[u], 0), 8) : 0;
-      load8(X + row[u] * a.ldx + col[u], n[u], a.vec_x, v[u]);
+  for (int u = 0; u < U; ++u) {
+    const int col = col0 + u * 2 * QB;
+    load8(x + col, min(max(a.cols - col, 0), 8), a.vec_x, v[u]);
+  }
+  float s[U], r[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float big = big8(v[u]);
+#pragma unroll
+    for (int d = HALF / 2; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+    s[u] = kv_scale_for<kKvE4M3>(big);
+    r[u] = kv_recip(s[u]);
+  }
+  const int copies = PLACED ? a.copies : 1;
+  for (int j = 0; j < copies; ++j) {
+    long long to = row;
+    if (PLACED) {
+      to = a.place[row * copies + j];
+      // a slot that `order` does not have was given no row: what is there is by chance
+      if (to < 0 || to >= (long long)a.rows * copies || a.order[to] != (int)(row * copies + j)) continue;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float big = big8(v[u]);
-#pragma unroll
-      for (int d = HALF / 2; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-      const float s = kv_scale_for<kKvE4M3>(big);
-      store8(a.codes + row[u] * a.ldq + col[u], n[u], a.vec_q, kv_recip(s), v[u]);
-      if (lane == 0 && n[u] > 0) a.scales[row[u] * a.lds + col[u] / QB] = s;
+      const int col = col0 + u * 2 * QB, n = min(max(a.cols - col, 0), 8);
+      store8(a.codes + to * a.ldq + col, n, a.vec_q, r[u], v[u]);
+      if (lane % HALF == 0 && n > 0) a.scales[to * a.lds + col / QB] = s[u];
     }
   }
+}
+
+// place[order[p]] = p, for the numbers that fit
+__global__ void __launch_bounds__(THREADS) invert_kernel(const int* order, int n, int* place, int* status) {
+  griddep_wait();
+  const int p = (int)(blockIdx.x * (long long)THREADS + threadIdx.x);
+  if (p >= n) return;
+  const int slot = order[p];
+  if (slot >= 0 && slot < n) place[slot] = p;
+  else report_status(status, 1, kSiteExperts);
 }
 
 // 128 x 128: a thread block a block of values, 8 rows a half warp, all in registers.
@@ -141,7 +163,7 @@ __global__ void __launch_bounds__(THREADS) quantise_tiles_kernel(const QuantiseA
 }
 
 template <typename T>
-int launch_type(const QuantiseArgs& a, int num_sms, cudaStream_t s) {
+int launch_type(const QuantiseArgs& a, cudaStream_t s) {
   const int per_row = (a.cols + QB - 1) / QB;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(THREADS, 1, 1);
@@ -152,12 +174,12 @@ int launch_type(const QuantiseArgs& a, int num_sms, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (a.block_rows == 1) {
-    constexpr int U = 4;
-    const long long blocks = (long long)a.rows * per_row;
-    const long long want = (blocks + HALVES - 1) / HALVES;
-    const long long most = 8ll * num_sms;             // 2048 threads an SM
-    cfg.gridDim = dim3((unsigned)(want < most ? want : most), 1, 1);
-    return cudaLaunchKernelEx(&cfg, quantise_rows_kernel<T, U>, a, blocks, per_row);
+    const int groups = (per_row + 7) / 8;
+    const long long blocks = ((long long)a.rows * groups + THREADS / 32 - 1) / (THREADS / 32);
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+    return a.place != nullptr ? cudaLaunchKernelEx(&cfg, quantise_rows_kernel<T, true>, a, groups)
+                              : cudaLaunchKernelEx(&cfg, quantise_rows_kernel<T, false>, a, groups);
   }
   const int tiles = (a.rows + QB - 1) / QB;
   cfg.gridDim = dim3((unsigned)per_row, (unsigned)(tiles < 65535 ? tiles : 65535), 1);
@@ -166,8 +188,21 @@ int launch_type(const QuantiseArgs& a, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-int launch_fp8_quantise(const QuantiseArgs& a, int num_sms, cudaStream_t s) {
-  return a.bf16 ? launch_type<__nv_bfloat16>(a, num_sms, s) : launch_type<float>(a, num_sms, s);
+int launch_fp8_quantise(const QuantiseArgs& a, cudaStream_t s) {
+  return a.bf16 ? launch_type<__nv_bfloat16>(a, s) : launch_type<float>(a, s);
+}
+
+int launch_invert(const int* order, int n, int* place, int* status, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((long long)n + THREADS - 1) / THREADS), 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, invert_kernel, order, n, place, status);
 }
 
 }  // namespace g3

@@ -965,42 +965,46 @@ int fp8_quantise(int rows, int cols, const void* X, bool bf16, long long ldx, ui
   a.codes = codes; a.ldq = ldq; a.scales = scales; a.lds = lds; a.block_rows = block_rows;
   a.vec_x = aligned16(X) && ((size_t)ldx * (bf16 ? 2 : 4)) % 16 == 0;
   a.vec_q = (reinterpret_cast<uintptr_t>(codes) & 7u) == 0 && ldq % 8 == 0;
-  const int err = launch_fp8_quantise(a, dev->num_sms, stream);
+  const int err = launch_fp8_quantise(a, stream);
   if (err != cudaSuccess)
     return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
   t_last_path = GEMM_PATH_QUANTISE;
   return GEMM_OK;
 }
 
-// Launches one block-scaled product, on the tcgen05 kernel where `fast`.
-int blocks_product(BlocksArgs& a, bool fast, DeviceInfo* dev, cudaStream_t stream) {
+// The plan of a block-scaled product on the tcgen05 kernels.
+int blocks_plan(const BlocksArgs& a, const DeviceInfo* dev, BlocksPlan* out) {
+  if (t_forced_bn != 0 && t_forced_bn != 128 && t_forced_bn != kBlocksPairRows)
+    return fail(GEMM_ERR_UNSUPPORTED, "block-scaled products have no tile of %d rows", t_forced_bn);
+  const plan::BlocksChoice c = plan::blocks_choice(a.rows, a.offsets != nullptr ? a.experts : 1, a.N,
+                                                   (a.K + kBlocksK - 1) / kBlocksK, a.B2 != nullptr, dev->num_sms,
+                                                   t_forced_bn);
+  out->nt = c.nt;
+  out->split = c.split;
+  return GEMM_OK;
+}
+
+// Launches one block-scaled product: on a tcgen05 kernel by `plan`, or (null) the generic one.
+int blocks_product(BlocksArgs& a, const BlocksPlan* plan, DeviceInfo* dev, cudaStream_t stream) {
   a.status = dev->status;
   a.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
   a.stall = t_stall;
   int err;
-  if (fast) {
-    BlocksPlan plan;
-    if (t_forced_bn != 0 && t_forced_bn != 128 && t_forced_bn != kBlocksPairRows)
-      return fail(GEMM_ERR_UNSUPPORTED, "block-scaled products have no tile of %d rows", t_forced_bn);
-    const plan::BlocksChoice c = plan::blocks_choice(a.rows, a.offsets != nullptr ? a.experts : 1, a.N,
-                                                     (a.K + kBlocksK - 1) / kBlocksK, a.B2 != nullptr, dev->num_sms,
-                                                     t_forced_bn);
-    plan.nt = c.nt;
-    plan.split = c.split;
+  if (plan != nullptr) {
     const bool gather = a.gather != 0;
     const CUtensorMap *mA = nullptr, *mB = nullptr, *mB2 = nullptr;
     int rc;
-    if ((rc = make_map(a.A, a.K, a.a_rows, (uint64_t)a.lda, kBlocksK, blocks_box_rows(plan.nt, gather),
+    if ((rc = make_map(a.A, a.K, a.a_rows, (uint64_t)a.lda, kBlocksK, blocks_box_rows(plan->nt, gather),
                        CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, &mA)) != GEMM_OK)
       return rc;
     for (int i = 0; i < (a.B2 != nullptr ? 2 : 1); ++i)
       if ((rc = make_map_3d(i ? a.B2 : a.B, a.N, a.K, a.experts, (uint64_t)a.ldb, (uint64_t)a.b_stride, kBlocksN, kBlocksK,
                             CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, i ? &mB2 : &mB)) != GEMM_OK)
         return rc;
-    err = plan.nt == kBlocksPairRows ? launch_blocks_pair(a, mA, mB, mB2, dev->num_sms, stream)
-                                     : launch_blocks(a, plan, mA, mB, mB2, dev->num_sms, stream);
-    t_last_k_split = plan.split;
-    t_last_bn = plan.nt;
+    err = plan->nt == kBlocksPairRows ? launch_blocks_pair(a, mA, mB, mB2, dev->num_sms, stream)
+                                      : launch_blocks(a, *plan, mA, mB, mB2, dev->num_sms, stream);
+    t_last_k_split = plan->split;
+    t_last_bn = plan->nt;
   } else {
     err = launch_blocks_generic(a, dev->num_sms, stream);
   }
@@ -1044,14 +1048,16 @@ int fp8_blocks(int M, int N, int K, float alpha, const uint8_t* A, int lda, cons
   a.A = A; a.lda = lda; a.a_rows = M; a.sa = a_scale; a.ldsa = ldsa;
   a.B = B; a.ldb = ldb; a.b_stride = (long long)ldb * (K > 0 ? K : 1); a.sb = b_scale; a.ldsb = ldsb;
   a.C = C; a.ldc = ldc; a.out_bf16 = out_bf16; a.alpha = alpha; a.beta = beta;
-  if ((rc = blocks_product(a, fast, dev, stream)) != GEMM_OK) return rc;
+  BlocksPlan plan;
+  if (fast && (rc = blocks_plan(a, dev, &plan)) != GEMM_OK) return rc;
+  if ((rc = blocks_product(a, fast ? &plan : nullptr, dev, stream)) != GEMM_OK) return rc;
   t_last_path = fast ? GEMM_PATH_BLOCKS : GEMM_PATH_GENERIC;
   return GEMM_OK;
 }
 
 // Where the parts of an experts call's workspace begin, and how large it is.
 struct ExpertsWorkspace {
-  size_t xq, xs, hq, hs, y, bytes;
+  size_t xq, xs, hq, hs, y, place, bytes;
   long long ldx, ldxs, ldh, ldhs, ldy;   // codes and y in elements: rows of whole 16-byte vectors
 };
 ExpertsWorkspace experts_ws(int tokens, int top_k, int hidden, int width) {
@@ -1064,11 +1070,12 @@ ExpertsWorkspace experts_ws(int tokens, int top_k, int hidden, int width) {
   w.ldhs = (width + kBlocksK - 1) / kBlocksK;
   w.ldy = (long long)up(hidden, 8);
   w.xq = 0;
-  w.xs = up(w.xq + (size_t)tokens * w.ldx, 256);
-  w.hq = up(w.xs + (size_t)tokens * w.ldxs * 4, 256);
+  w.xs = up(w.xq + slots * w.ldx, 256);          // a row a slot where X is laid out by expert
+  w.hq = up(w.xs + slots * w.ldxs * 4, 256);
   w.hs = up(w.hq + slots * w.ldh, 256);
   w.y = up(w.hs + slots * w.ldhs * 4, 256);
-  w.bytes = up(w.y + slots * w.ldy * 2, 256);
+  w.place = up(w.y + slots * w.ldy * 2, 256);
+  w.bytes = up(w.place + slots * 4, 256);
   return w;
 }
 
@@ -1120,7 +1127,34 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
                     su % 16 == 0 && sd % 16 == 0 && su < (1ll << 40) && sd < (1ll << 40) &&
                     t_forced_path != GEMM_PATH_GENERIC;
   uint8_t* base = static_cast<uint8_t*>(workspace);
+  const int slots = tokens * top_k;
 
+  BlocksArgs a{};
+  a.experts = E; a.rows = slots; a.offsets = offsets; a.order = order;
+  a.N = F; a.K = H;
+  a.A = base + ws.xq; a.lda = ws.ldx; a.sa = reinterpret_cast<float*>(base + ws.xs); a.ldsa = ws.ldxs;
+  a.B = w->gate; a.B2 = w->up; a.ldb = w->ld_up; a.b_stride = su;
+  a.sb = w->gate_scale; a.sb2 = w->up_scale; a.ldsb = ws.ldhs; a.sb_stride = ws.ldxs * ws.ldhs;
+  a.alpha = 1.f;
+  a.hq = base + ws.hq; a.ldh = ws.ldh; a.hs = reinterpret_cast<float*>(base + ws.hs); a.ldhs = ws.ldhs;
+  BlocksArgs d{};
+  d.experts = E; d.rows = slots; d.offsets = offsets; d.order = order;
+  d.N = H; d.K = F; d.scatter = 1;
+  d.A = a.hq; d.lda = ws.ldh; d.a_rows = d.rows; d.sa = a.hs; d.ldsa = ws.ldhs;
+  d.B = w->down; d.ldb = w->ld_down; d.b_stride = sd;
+  d.sb = w->down_scale; d.ldsb = ws.ldxs; d.sb_stride = ws.ldxs * ws.ldhs;
+  d.C = base + ws.y; d.ldc = ws.ldy; d.out_bf16 = true; d.alpha = 1.f;
+  BlocksPlan plan_up, plan_down;
+  if (fast && ((rc = blocks_plan(a, dev, &plan_up)) != GEMM_OK || (rc = blocks_plan(d, dev, &plan_down)) != GEMM_OK))
+    return rc;
+  // Row tiles of 32 gather a token's one row for each of its slots (a decode step's rows
+  // are few); larger ones find the rows laid out by expert: a gathered row costs the copy
+  // engine's issue about 20 cycles, and 256 rows a block of 128 k would be all it does.
+  const bool gather = fast && plan_up.nt == 32;
+  a.gather = gather || !fast ? top_k : 0;
+  a.a_rows = a.gather != 0 ? tokens : slots;
+
+  int err = cudaSuccess;
   QuantiseArgs q;
   q.rows = tokens; q.cols = H; q.x = X; q.ldx = ldx; q.bf16 = true;
   q.codes = base + ws.xq; q.ldq = ws.ldx;
@@ -1128,28 +1162,18 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
   q.block_rows = 1;
   q.vec_x = aligned16(X) && ldx % 8 == 0;
   q.vec_q = true;
-  int err = launch_fp8_quantise(q, dev->num_sms, stream);
+  if (a.gather == 0) {
+    int* place = reinterpret_cast<int*>(base + ws.place);
+    err = launch_invert(order, slots, place, dev->status, stream);
+    q.place = place;
+    q.copies = top_k;
+    q.order = order;
+  }
+  if (err == cudaSuccess) err = launch_fp8_quantise(q, stream);
   if (err != cudaSuccess)
     return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
-
-  BlocksArgs a{};
-  a.experts = E; a.rows = tokens * top_k; a.offsets = offsets; a.order = order;
-  a.N = F; a.K = H; a.gather = top_k;
-  a.A = q.codes; a.lda = ws.ldx; a.a_rows = tokens; a.sa = q.scales; a.ldsa = ws.ldxs;
-  a.B = w->gate; a.B2 = w->up; a.ldb = w->ld_up; a.b_stride = su;
-  a.sb = w->gate_scale; a.sb2 = w->up_scale; a.ldsb = ws.ldhs; a.sb_stride = ws.ldxs * ws.ldhs;
-  a.alpha = 1.f;
-  a.hq = base + ws.hq; a.ldh = ws.ldh; a.hs = reinterpret_cast<float*>(base + ws.hs); a.ldhs = ws.ldhs;
-  if ((rc = blocks_product(a, fast, dev, stream)) != GEMM_OK) return rc;
-
-  BlocksArgs d{};
-  d.experts = E; d.rows = tokens * top_k; d.offsets = offsets; d.order = order;
-  d.N = H; d.K = F; d.scatter = 1;
-  d.A = a.hq; d.lda = ws.ldh; d.a_rows = d.rows; d.sa = a.hs; d.ldsa = ws.ldhs;
-  d.B = w->down; d.ldb = w->ld_down; d.b_stride = sd;
-  d.sb = w->down_scale; d.ldsb = ws.ldxs; d.sb_stride = ws.ldxs * ws.ldhs;
-  d.C = base + ws.y; d.ldc = ws.ldy; d.out_bf16 = true; d.alpha = 1.f;
-  if ((rc = blocks_product(d, fast, dev, stream)) != GEMM_OK) return rc;
+  if ((rc = blocks_product(a, fast ? &plan_up : nullptr, dev, stream)) != GEMM_OK) return rc;
+  if ((rc = blocks_product(d, fast ? &plan_down : nullptr, dev, stream)) != GEMM_OK) return rc;
 
   CombineArgs c;
   c.tokens = tokens; c.top_k = top_k; c.cols = H;

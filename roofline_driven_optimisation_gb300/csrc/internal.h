@@ -317,8 +317,13 @@ struct QuantiseArgs {
   long long lds;
   int block_rows;
   bool vec_x, vec_q;      // rows of 16-byte-aligned vectors of 8 values; of 8-byte-aligned ones
+  const int* place = nullptr;   // row r goes to rows place[r * copies + j], j < copies (1 x 128 only)
+  int copies = 1;
+  const int* order = nullptr;   // what place was made from
 };
-int launch_fp8_quantise(const QuantiseArgs& a, int num_sms, cudaStream_t s);
+int launch_fp8_quantise(const QuantiseArgs& a, cudaStream_t s);
+// place[order[p]] = p for p < n
+int launch_invert(const int* order, int n, int* place, int* status, cudaStream_t s);
 
 // Block-scaled products of E4M3 codes, for one matrix or for the slots of experts:
 // rows [offsets[e], offsets[e+1]) are multiplied with B's e-th matrix.

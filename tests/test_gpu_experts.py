@@ -110,7 +110,16 @@ def test_no_tokens():
     check_status()
 
 
-def test_slots_that_do_not_fit_are_skipped_and_reported():
+@pytest.mark.parametrize("rows", [0, 128, 256])
+def test_slots_that_do_not_fit_are_skipped_and_reported(rows):
+    g.force_tile_n(rows)
+    try:
+        _slots_that_do_not_fit()
+    finally:
+        g.force_tile_n(0)
+
+
+def _slots_that_do_not_fit():
     layer = Layer(4, 256, 144)
     ids, w, offsets, order = routing(30, 4, 2)
     x = inputs(30, 256).cuda()
