@@ -44,7 +44,9 @@ constexpr int THREADS = 384, EPI_WARPS = 8, EPI_FIRST = 4;
 constexpr int A_BYTES = BM_CTA * BK, B_BYTES = BK * 128;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int TMEM_COLS = 512, COLS = 256, NBUF = 2;
-constexpr int RING = 8, RING_WORDS = BM_CTA + 4;       // scales of a block: the rows', then B's one or two
+// The ring of scales: a slot holds four blocks of k, four floats for each row and for B's
+// one or two column blocks, so that a drain thread waits and reads once in four blocks.
+constexpr int RING = 2, RING_BLOCKS = 4, RING_WORDS = RING_BLOCKS * (BM_CTA + 2);
 constexpr int BOX = 64;
 constexpr int BAR_BYTES = 512;
 // Shared memory: the ring of operands, and for each drain warp the rows it is about to
@@ -66,6 +68,7 @@ struct Params {
   BlocksArgs a;
   int kblocks, tiles_n;
   int c_vec;                                           // C's rows are 16-byte-aligned vectors
+  int sa_vec;                                          // A's scales: 16-byte-aligned vectors of four blocks
   int c_rows;                                          // and whole ones, and beta is 0: stored row by row
 };
 
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int col = SW ? i.nb : 2 * i.nb + lane;
         const float* sb = nullptr;
         if (lane < 2 && (SW || col * 128 < a.N)) sb = (SW && lane == 1 ? a.sb2 : a.sb) + i.e * a.sb_stride + col;
-        for (int kb = 0; kb < p.kblocks; ++kb) {
+        for (int kb = 0; kb < p.kblocks; kb += RING_BLOCKS) {
           if (!__all_sync(0xffffffffu, mbar_wait(sempty_bar(r), rphase ^ 1u, a.timeout_ns, abort_flag))) {
             if (!*abort_flag) report_status(a.status, 5, kSiteBlocks2Scales);
             *abort_flag = 1;
@@ -374,8 +377,20 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t to = smem_u32(ring + r * RING_WORDS);
 #pragma unroll
           for (int q = 0; q < BM_CTA / 32; ++q)
-            if (row[q] != nullptr) cp_async_4(to + (q * 32 + lane) * 4, row[q] + kb);
-          if (sb != nullptr) cp_async_4(to + (BM_CTA + lane) * 4, sb + kb * a.ldsb);
+            if (row[q] != nullptr) {
+              const uint32_t at_row = to + (q * 32 + lane) * 16;
+              if (p.sa_vec && kb + RING_BLOCKS <= p.kblocks) {
+                cp_async_16(at_row, row[q] + kb, true);
+              } else {
+#pragma unroll
+                for (int u = 0; u < RING_BLOCKS; ++u)
+                  if (kb + u < p.kblocks) cp_async_4(at_row + u * 4, row[q] + kb + u);
+              }
+            }
+          if (sb != nullptr)
+#pragma unroll
+            for (int u = 0; u < RING_BLOCKS; ++u)
+              if (kb + u < p.kblocks) cp_async_4(to + ((BM_CTA + lane) * 4 + u) * 4, sb + (kb + u) * a.ldsb);
           cp_async_arrive(sfull_bar(r));
           if (++r == RING) {
             r = 0;
@@ -403,21 +418,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint64_t acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0;
-      // the block's scales are taken out of the ring while the block before is drained
-      float s0 = 0.f, s1 = 0.f;
-      auto scales = [&]() {
-        const bool got = mbar_wait(sfull_bar(r), rphase, a.timeout_ns, abort_flag);
-        const float* at = ring + r * RING_WORDS;
-        const float sa = at[lrow];
-        s0 = sa * at[BM_CTA + (SW ? 0 : half)];
-        s1 = SW ? sa * at[BM_CTA + 1] : s0;
-        return got;
-      };
       auto column = [&](int c) {
-        return (uint32_t)(SW ? (c / 4) * 128 + half * 64 + (c % 4) * 16 : half * 128 + c * 16);
+        return (uint32_t)(SW ? (c / 2) * 128 + half * 64 + (c % 2) * 32 : half * 128 + c * 32);
       };
-      ok = scales();
+      float4 sa = make_float4(0.f, 0.f, 0.f, 0.f), sb0 = sa, sb1 = sa;
       for (int kb = 0; kb < p.kblocks; ++kb) {
+        const int u = kb % RING_BLOCKS;
+        if (u == 0) {                                  // the scales of four blocks
+          ok = mbar_wait(sfull_bar(r), rphase, a.timeout_ns, abort_flag);
+          const float4* slot = reinterpret_cast<const float4*>(ring + r * RING_WORDS);
+          sa = slot[lrow];
+          sb0 = slot[BM_CTA + (SW ? 0 : half)];
+          if (SW) sb1 = slot[BM_CTA + 1];
+        }
         ok = ok && mbar_wait(tfull_bar(b), bphase, a.timeout_ns, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
@@ -426,33 +439,32 @@ __global__ void __launch_bounds__(THREADS, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t d = t_lane + (uint32_t)(b * COLS);
+        const float s0 = sa.x * sb0.x, s1 = sa.x * sb1.x;
         const uint64_t d0 = pack2(__float_as_uint(s0), __float_as_uint(s0));
-        const uint64_t d1 = pack2(__float_as_uint(s1), __float_as_uint(s1));
-        // 16 columns are read while the 16 before are added
-        uint32_t v[2][16];
-        tmem_ld_32x32b_x16(d + column(0), v[0]);
-        const int used = r;
-        if (++r == RING) {
-          r = 0;
-          rphase ^= 1u;
-        }
-        if (kb + 1 < p.kblocks) ok = scales();
+        const uint64_t d1 = SW ? pack2(__float_as_uint(s1), __float_as_uint(s1)) : d0;
+        // the next block's to the front
+        sa = make_float4(sa.y, sa.z, sa.w, 0.f);
+        sb0 = make_float4(sb0.y, sb0.z, sb0.w, 0.f);
+        if (SW) sb1 = make_float4(sb1.y, sb1.z, sb1.w, 0.f);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(t_lane + (uint32_t)(b * COLS) + column(c), v);
           tc_wait_ld();
-          if (c < 7) {
-            tmem_ld_32x32b_x16(d + column(c + 1), v[(c + 1) & 1]);
-          } else {
+          if (c == 3) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-              mbar_arrive_remote_light(lead_tempty + 8u * b);
-              mbar_arrive(sempty_bar(used));
-            }
+            if (lane == 0) mbar_arrive_remote_light(lead_tempty + 8u * b);
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) fma2(acc[c * 8 + j], pack2(v[c & 1][2 * j], v[c & 1][2 * j + 1]), c < 4 ? d0 : d1);
+          for (int j = 0; j < 16; ++j) fma2(acc[c * 16 + j], pack2(v[2 * j], v[2 * j + 1]), c < 2 ? d0 : d1);
+        }
+        if (u == RING_BLOCKS - 1 || kb + 1 == p.kblocks) {
+          if (lane == 0) mbar_arrive(sempty_bar(r));   // its lanes have read: __syncwarp above
+          if (++r == RING) {
+            r = 0;
+            rphase ^= 1u;
+          }
         }
         if (++b == NBUF) {
           b = 0;
@@ -585,6 +597,7 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
   p.kblocks = (a.K + BK - 1) / BK;
   p.tiles_n = (a.N + (SW ? 128 : 256) - 1) / (SW ? 128 : 256);
   const int osz = OUT_BF16 ? 2 : 4;
+  p.sa_vec = ((reinterpret_cast<uintptr_t>(a.sa) & 15u) == 0 && a.ldsa % 4 == 0) ? 1 : 0;
   p.c_vec = ((reinterpret_cast<uintptr_t>(a.C) & 15u) == 0 && (a.ldc * osz) % 16 == 0) ? 1 : 0;
   p.c_rows = p.c_vec != 0 && a.N % (16 / osz) == 0 && a.beta == 0.f ? 1 : 0;
   const long long items = blocks_row_tiles(a.rows, a.offsets != nullptr ? a.experts : 1, BM) * p.tiles_n;

@@ -1065,9 +1065,10 @@ ExpertsWorkspace experts_ws(int tokens, int top_k, int hidden, int width) {
   const size_t slots = (size_t)tokens * top_k;
   ExpertsWorkspace w;
   w.ldx = (long long)up(hidden, 16);
-  w.ldxs = (hidden + kBlocksK - 1) / kBlocksK;
+  // scales: rows of whole vectors too
+  w.ldxs = (long long)up((hidden + kBlocksK - 1) / kBlocksK, 4);
   w.ldh = (long long)up(width, 16);
-  w.ldhs = (width + kBlocksK - 1) / kBlocksK;
+  w.ldhs = (long long)up((width + kBlocksK - 1) / kBlocksK, 4);
   w.ldy = (long long)up(hidden, 8);
   w.xq = 0;
   w.xs = up(w.xq + slots * w.ldx, 256);          // a row a slot where X is laid out by expert
@@ -1127,14 +1128,14 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
                     su % 16 == 0 && sd % 16 == 0 && su < (1ll << 40) && sd < (1ll << 40) &&
                     t_forced_path != GEMM_PATH_GENERIC;
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  const int slots = tokens * top_k;
+  const int slots = tokens * top_k, hblocks = (H + kBlocksK - 1) / kBlocksK, fblocks = (F + kBlocksN - 1) / kBlocksN;
 
   BlocksArgs a{};
   a.experts = E; a.rows = slots; a.offsets = offsets; a.order = order;
   a.N = F; a.K = H;
   a.A = base + ws.xq; a.lda = ws.ldx; a.sa = reinterpret_cast<float*>(base + ws.xs); a.ldsa = ws.ldxs;
   a.B = w->gate; a.B2 = w->up; a.ldb = w->ld_up; a.b_stride = su;
-  a.sb = w->gate_scale; a.sb2 = w->up_scale; a.ldsb = ws.ldhs; a.sb_stride = ws.ldxs * ws.ldhs;
+  a.sb = w->gate_scale; a.sb2 = w->up_scale; a.ldsb = fblocks; a.sb_stride = (long long)hblocks * fblocks;
   a.alpha = 1.f;
   a.hq = base + ws.hq; a.ldh = ws.ldh; a.hs = reinterpret_cast<float*>(base + ws.hs); a.ldhs = ws.ldhs;
   BlocksArgs d{};
@@ -1142,7 +1143,7 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
   d.N = H; d.K = F; d.scatter = 1;
   d.A = a.hq; d.lda = ws.ldh; d.a_rows = d.rows; d.sa = a.hs; d.ldsa = ws.ldhs;
   d.B = w->down; d.ldb = w->ld_down; d.b_stride = sd;
-  d.sb = w->down_scale; d.ldsb = ws.ldxs; d.sb_stride = ws.ldxs * ws.ldhs;
+  d.sb = w->down_scale; d.ldsb = hblocks; d.sb_stride = (long long)hblocks * fblocks;
   d.C = base + ws.y; d.ldc = ws.ldy; d.out_bf16 = true; d.alpha = 1.f;
   BlocksPlan plan_up, plan_down;
   if (fast && ((rc = blocks_plan(a, dev, &plan_up)) != GEMM_OK || (rc = blocks_plan(d, dev, &plan_down)) != GEMM_OK))
