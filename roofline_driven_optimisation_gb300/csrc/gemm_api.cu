@@ -974,7 +974,7 @@ int fp8_quantise(int rows, int cols, const void* X, bool bf16, long long ldx, ui
 
 // The plan of a block-scaled product on the tcgen05 kernels.
 int blocks_plan(const BlocksArgs& a, const DeviceInfo* dev, BlocksPlan* out) {
-  if (t_forced_bn != 0 && t_forced_bn != 128 && t_forced_bn != kBlocksPairRows)
+  if (t_forced_bn != 0 && t_forced_bn != 128 && t_forced_bn != kBlocksWide)
     return fail(GEMM_ERR_UNSUPPORTED, "block-scaled products have no tile of %d rows", t_forced_bn);
   const plan::BlocksChoice c = plan::blocks_choice(a.rows, a.offsets != nullptr ? a.experts : 1, a.N,
                                                    (a.K + kBlocksK - 1) / kBlocksK, a.B2 != nullptr, dev->num_sms,
@@ -1001,7 +1001,7 @@ int blocks_product(BlocksArgs& a, const BlocksPlan* plan, DeviceInfo* dev, cudaS
       if ((rc = make_map_3d(i ? a.B2 : a.B, a.N, a.K, a.experts, (uint64_t)a.ldb, (uint64_t)a.b_stride, kBlocksN, kBlocksK,
                             CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, i ? &mB2 : &mB)) != GEMM_OK)
         return rc;
-    err = plan->nt == kBlocksPairRows ? launch_blocks_pair(a, mA, mB, mB2, dev->num_sms, stream)
+    err = plan->nt == kBlocksWide ? launch_blocks_wide(a, mA, mB, mB2, dev->num_sms, stream)
                                       : launch_blocks(a, *plan, mA, mB, mB2, dev->num_sms, stream);
     t_last_k_split = plan->split;
     t_last_bn = plan->nt;

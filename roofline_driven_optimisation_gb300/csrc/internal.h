@@ -90,11 +90,11 @@ enum WaitSite : int {
   kSiteBlocksScales = 72,
   kSiteBlocksEpilogue = 73,
   kSiteBlocksDrain = 74,
-  kSiteBlocks2Producer = 76,
-  kSiteBlocks2Mma = 77,
-  kSiteBlocks2Scales = 78,
-  kSiteBlocks2Epilogue = 79,
-  kSiteBlocks2Drain = 80,
+  kSiteWideProducer = 76,
+  kSiteWideMma = 77,
+  kSiteWideScales = 78,
+  kSiteWideEpilogue = 79,
+  kSiteWideDrain = 80,
   kSiteExperts = 75,       // an expert's slots, or a slot's number, that do not fit the call
 };
 
@@ -367,10 +367,10 @@ constexpr long long blocks_row_tiles(long long rows, int experts, int nt) {
 }
 int launch_blocks(const BlocksArgs& a, const BlocksPlan& plan, const CUtensorMap* mapA, const CUtensorMap* mapB,
                   const CUtensorMap* mapB2, int num_sms, cudaStream_t s);
-// The CTA-pair kernel: row tiles of kBlocksPairRows; the same maps, A's boxes of
-// blocks_box_rows(kBlocksPairRows, gather) rows.
-constexpr int kBlocksPairRows = 256;
-int launch_blocks_pair(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap* mapB, const CUtensorMap* mapB2,
+// The kernel for many rows: items of 128 rows and 256 columns; the same maps, A's boxes of
+// blocks_box_rows(kBlocksWide, false) rows.  kBlocksWide in a plan's nt selects it.
+constexpr int kBlocksWide = 256;
+int launch_blocks_wide(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap* mapB, const CUtensorMap* mapB2,
                        int num_sms, cudaStream_t s);
 int launch_blocks_generic(const BlocksArgs& a, int num_sms, cudaStream_t s);
 
