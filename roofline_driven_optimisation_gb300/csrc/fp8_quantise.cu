@@ -26,79 +26,85 @@ constexpr int HALF = 16;           // lanes that share 128 values of a row: 8 ea
 constexpr int THREADS = 256;
 constexpr int HALVES = THREADS / HALF;
 
+// 8 values from x[0..7], of which `n` exist (0 in the place of the others), as they came:
+// bf16 values take half the registers that way
 template <typename T>
-__device__ __forceinline__ float q_f32(T v);
-template <>
-__device__ __forceinline__ float q_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float q_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-// 8 values from x[0..7], of which `n` exist (0 in the place of the others)
-template <typename T>
-__device__ __forceinline__ void load8(const T* x, int n, bool vec, float (&v)[8]) {
-  if (vec && n >= 8) {
+struct Eight {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* x, int n, bool vec) {
+    if (vec && n >= 8) {
 #pragma unroll
-    for (int q = 0; q < (int)sizeof(T) / 2; ++q) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(x) + q);
-      alignas(16) T part[16 / sizeof(T)];
-      *reinterpret_cast<uint4*>(part) = w;
+      for (int q = 0; q < (int)sizeof(T) / 2; ++q) w[q] = __ldg(reinterpret_cast<const uint4*>(x) + q);
+    } else {
+      alignas(16) T part[8];
 #pragma unroll
-      for (int i = 0; i < (int)(16 / sizeof(T)); ++i) v[q * (int)(16 / sizeof(T)) + i] = q_f32(part[i]);
+      for (int i = 0; i < 8; ++i) part[i] = i < n ? x[i] : T(0.f);
+#pragma unroll
+      for (int q = 0; q < (int)sizeof(T) / 2; ++q) w[q] = *reinterpret_cast<const uint4*>(part + q * 16 / sizeof(T));
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? q_f32(x[i]) : 0.f;
   }
-}
-
-__device__ __forceinline__ float big8(const float (&v)[8]) {
-  float a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));     // fmaxf leaves NaN out
-  return a;
-}
-
-__device__ __forceinline__ void store8(uint8_t* q, int n, bool vec, float r, const float (&v)[8]) {
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = kv_code2<kKvE4M3>(__fmul_rn(v[2 * i], r), __fmul_rn(v[2 * i + 1], r));
-  if (vec && n >= 8) {
-    *reinterpret_cast<uint2*>(q) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) q[i] = (uint8_t)(c[i / 2] >> (8 * (i & 1)));
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t u[4] = {w[i * sizeof(T) / 16].x, w[i * sizeof(T) / 16].y, w[i * sizeof(T) / 16].z, w[i * sizeof(T) / 16].w};
+    if constexpr (sizeof(T) == 4) return __uint_as_float(u[i % 4]);
+    else return __uint_as_float(i % 2 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
   }
-}
+  __device__ __forceinline__ float big() const {
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(at(i)));     // fmaxf leaves NaN out
+    return a;
+  }
+  __device__ __forceinline__ void store(uint8_t* q, int n, bool vec, float r) const {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = kv_code2<kKvE4M3>(__fmul_rn(at(2 * i), r), __fmul_rn(at(2 * i + 1), r));
+    if (vec && n >= 8) {
+      *reinterpret_cast<uint2*>(q) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) q[i] = (uint8_t)(c[i / 2] >> (8 * (i & 1)));
+    }
+  }
+};
 
-// 1 x 128: a warp 8 blocks of a row, sixteen lanes a block, every load in flight before
-// the first maximum.  With `place`, row r is written `copies` times, to rows place[r *
-// copies + j] of the codes and scales (each slot of a token's, in the order of experts).
+// 1 x 128: a warp 2 U blocks of a row, sixteen lanes a block, every load in flight before
+// the first maximum, and as many warps as an SM takes (16384 x 4096 bf16: 83 us with four
+// blocks a half warp of 1024 threads an SM in turn, 61 one unit a warp).  With `place`, row
+// r is written `copies` times, to rows place[r * copies + j] of the codes and scales (each
+// slot of a token's, in the order of experts).
+template <typename T>
+constexpr int units_u() { return sizeof(T) == 2 ? 4 : 2; }
+
 template <typename T, bool PLACED>
-__global__ void __launch_bounds__(THREADS) quantise_rows_kernel(const __grid_constant__ QuantiseArgs a, int groups) {
-  constexpr int U = 4;
+__global__ void __launch_bounds__(THREADS, 5) quantise_rows_kernel(const __grid_constant__ QuantiseArgs a, int groups) {
+  constexpr int U = units_u<T>();
   griddep_wait();
   const int lane = threadIdx.x % 32;
   const long long unit = (long long)blockIdx.x * (THREADS / 32) + threadIdx.x / 32;
-  const long long row = unit / groups;
+  const long long row = a.units32 ? (unsigned)unit / (unsigned)groups : unit / groups;
   if (row >= a.rows) return;
-  const int col0 = (int)(unit - row * groups) * (2 * U * QB) + lane * 8;       // lanes 16 .. 31 the next block
+  const int first = (int)(unit - row * groups) * 2 * U;             // its first block
+  const int col0 = first * QB + lane * 8;                           // lanes 16 .. 31 the next block
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-  float v[U][8];
+  Eight<T> v[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int col = col0 + u * 2 * QB;
-    load8(x + col, min(max(a.cols - col, 0), 8), a.vec_x, v[u]);
+    v[u].load(x + col, min(max(a.cols - col, 0), 8), a.vec_x);
   }
-  float s[U], r[U];
+  float s[U], mine = 0.f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    float big = big8(v[u]);
+    float big = v[u].big();
 #pragma unroll
     for (int d = HALF / 2; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
     s[u] = kv_scale_for<kKvE4M3>(big);
-    r[u] = kv_recip(s[u]);
+    // lane i < 2 U: the i-th block's scale, so that the row's are stored side by side
+    const float other = __shfl_sync(0xffffffffu, s[u], (lane & 1) * HALF);
+    if (lane / 2 == u) mine = other;
   }
+  const int blocks = (a.cols + QB - 1) / QB;
   const int copies = PLACED ? a.copies : 1;
   for (int j = 0; j < copies; ++j) {
     long long to = row;
@@ -109,10 +115,10 @@ __global__ void __launch_bounds__(THREADS) quantise_rows_kernel(const __grid_con
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int col = col0 + u * 2 * QB, n = min(max(a.cols - col, 0), 8);
-      store8(a.codes + to * a.ldq + col, n, a.vec_q, r[u], v[u]);
-      if (lane % HALF == 0 && n > 0) a.scales[to * a.lds + col / QB] = s[u];
+      const int col = col0 + u * 2 * QB;
+      v[u].store(a.codes + to * a.ldq + col, min(max(a.cols - col, 0), 8), a.vec_q, kv_recip(s[u]));
     }
+    if (lane < 2 * U && first + lane < blocks) a.scales[to * a.lds + first + lane] = mine;
   }
 }
 
@@ -135,15 +141,15 @@ __global__ void __launch_bounds__(THREADS) quantise_tiles_kernel(const QuantiseA
   const T* X = static_cast<const T*>(a.x);
   const int col = (int)blockIdx.x * QB + lane * 8;
   for (long long tile = blockIdx.y; tile * QB < a.rows; tile += gridDim.y) {
-    float v[QB / HALVES][8];
+    Eight<T> v[QB / HALVES];
     float big = 0.f;
 #pragma unroll
     for (int i = 0; i < QB / HALVES; ++i) {
       const long long row = tile * QB + i * HALVES + half;
-      const int n = row < a.rows ? min(max(a.cols - col, 0), 8) : 0;
-      load8(X + row * a.ldx + col, n, a.vec_x, v[i]);
-      big = fmaxf(big, big8(v[i]));
+      v[i].load(X + row * a.ldx + col, row < a.rows ? min(max(a.cols - col, 0), 8) : 0, a.vec_x);
     }
+#pragma unroll
+    for (int i = 0; i < QB / HALVES; ++i) big = fmaxf(big, v[i].big());
 #pragma unroll
     for (int d = 16; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = big;
@@ -154,8 +160,7 @@ __global__ void __launch_bounds__(THREADS) quantise_tiles_kernel(const QuantiseA
 #pragma unroll
     for (int i = 0; i < QB / HALVES; ++i) {
       const long long row = tile * QB + i * HALVES + half;
-      const int n = row < a.rows ? min(max(a.cols - col, 0), 8) : 0;
-      store8(a.codes + row * a.ldq + col, n, a.vec_q, r, v[i]);
+      v[i].store(a.codes + row * a.ldq + col, row < a.rows ? min(max(a.cols - col, 0), 8) : 0, a.vec_q, r);
     }
     if (threadIdx.x == 0) a.scales[tile * a.lds + blockIdx.x] = s;
     __syncthreads();                      // part[] is read by all before the next tile's
@@ -174,12 +179,15 @@ int launch_type(const QuantiseArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (a.block_rows == 1) {
-    const int groups = (per_row + 7) / 8;
+    constexpr int each = 2 * units_u<T>();
+    const int groups = (per_row + each - 1) / each;
     const long long blocks = ((long long)a.rows * groups + THREADS / 32 - 1) / (THREADS / 32);
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     cfg.gridDim = dim3((unsigned)blocks, 1, 1);
-    return a.place != nullptr ? cudaLaunchKernelEx(&cfg, quantise_rows_kernel<T, true>, a, groups)
-                              : cudaLaunchKernelEx(&cfg, quantise_rows_kernel<T, false>, a, groups);
+    QuantiseArgs q = a;
+    q.units32 = blocks * (THREADS / 32) < 0x7fffffffll;
+    return a.place != nullptr ? cudaLaunchKernelEx(&cfg, quantise_rows_kernel<T, true>, q, groups)
+                              : cudaLaunchKernelEx(&cfg, quantise_rows_kernel<T, false>, q, groups);
   }
   const int tiles = (a.rows + QB - 1) / QB;
   cfg.gridDim = dim3((unsigned)per_row, (unsigned)(tiles < 65535 ? tiles : 65535), 1);

@@ -320,6 +320,7 @@ struct QuantiseArgs {
   const int* place = nullptr;   // row r goes to rows place[r * copies + j], j < copies (1 x 128 only)
   int copies = 1;
   const int* order = nullptr;   // what place was made from
+  bool units32 = false;         // warps counted in 32 bits
 };
 int launch_fp8_quantise(const QuantiseArgs& a, cudaStream_t s);
 // place[order[p]] = p for p < n
