@@ -10,19 +10,26 @@
 // (N-major in shared memory) and up to NT rows of A its N columns.  A decode step's few
 // rows then cost what they are (N is a multiple of 16, set tile by tile at run time, so
 // an expert with 5 rows pays for 16), and a tile lies inside one column of B's scales.
+// Calls with many rows go to fp8_blocks_wide.cu.
 //
 // Scales.  The tensor core sums one block of 128 k; its sum S_b is read out of TMEM and
 // added with its scale to a sum in registers, so every sum is fp32 and no scale is
-// rounded into a code.  That is what the kernel is built around: TMEM holds NBUF
-// accumulators, the MMA fills one while the epilogue warps drain another, and a warp of
-// its own multiplies sa with sb for them a block ahead.  Per block of 128 k and a
-// 256-wide tile the MMAs take 512 cycles at the nominal rate, the drain 256 (packed
-// fma.rn.f32x2, two columns an instruction, and as many cycles to read TMEM).
+// rounded into a code.  With few rows the weights' bytes bound the call, and a block's
+// 16 KB arrive every 250 cycles or so: handing one accumulator at a time to the drain
+// warps, with their polls, cost 650 cycles a block and was what bounded it.  So TMEM holds two
+// groups of up to four blocks' accumulators: MMA, scales and drain meet once a group,
+// and the eight drain warps wait at a hardware barrier with a signal warp that polls
+// for them.
 //
 // Roles (384 threads, one CTA an SM): warp 0 copies (TMA; the experts' rows of A through
-// tile::gather4, four rows an instruction, so that they are never laid out by expert),
-// warp 1 issues the MMAs, warp 2 the scales, warps 4-11 drain: warp w the TMEM lanes
-// 32*(w%4)..+31 (columns of B) and half of the tile's rows of A.
+// tile::gather4, four rows an instruction, so that they are never laid out by expert; the
+// first stages' weights before the rows' numbers are known), warp 1 issues the MMAs,
+// warp 2 multiplies sa with sb for the drain, warp 3 signals, warps 4-11 drain: warp w
+// the TMEM lanes 32*(w%4)..+31 (columns of B) and half of the tile's rows of A.
+//
+// Epilogue: the sums go through shared memory, 32 rows of A at a time, and a warp then has
+// a whole row's 128 columns: a row of C or of codes leaves as one piece, the largest
+// magnitude for h's scale is one warp's, and rows that are not there cost nothing.
 //
 // Schedule: items (row tile of an expert, column tile) in a line, expert by expert,
 // columns outermost inside an expert; CTA c takes items c, c + grid, ...  The counts are
@@ -49,51 +56,42 @@ constexpr int BK = kBlocksK, BN = kBlocksN;
 constexpr int THREADS = 384, EPI_WARPS = 8, EPI_FIRST = 4;
 constexpr int W_BYTES = BN * BK;               // a weight tile: 128 k rows of 128 columns
 constexpr int SMEM_LIMIT = 232448;
+constexpr int CHUNK = 32;                      // rows of A that go through shared memory at a time
 
 template <int NT, bool SW>
 struct Cfg {
   static constexpr int OPS = SW ? 2 : 1;
   static constexpr int COLS = NT * OPS;                       // TMEM columns of an accumulator
-  static constexpr int NBUF = 512 / COLS > 8 ? 8 : 512 / COLS;
-  static constexpr int TMEM_COLS = NBUF * COLS;
+  static constexpr int GROUP = 256 / COLS > 4 ? 4 : 256 / COLS;      // blocks that are handed over together
+  static constexpr int TMEM_COLS = 2 * GROUP * COLS;
   static constexpr int STAGE_BYTES = OPS * W_BYTES + NT * BK;
-  static constexpr int SCALE_BYTES = NBUF * COLS * 4;
-  // SwiGLU: codes of one half's columns on their way to rows of 128 bytes, and the
-  // columns' largest magnitudes by TMEM quarter
-  static constexpr int OUT_BYTES = SW ? NT * BN + 4 * NT * 4 : 0;
-  static constexpr int LIST_BYTES = kListBytes;
+  static constexpr int SCALE_BYTES = 2 * GROUP * COLS * 4;
+  static constexpr int OUT_BYTES = OPS * CHUNK * BN * 4;
   static constexpr int BAR_BYTES = 512;
-  static constexpr int REST = SCALE_BYTES + OUT_BYTES + LIST_BYTES + BAR_BYTES + 1024;
+  static constexpr int REST = SCALE_BYTES + OUT_BYTES + kListBytes + BAR_BYTES + 1024;
   static constexpr int FIT = (SMEM_LIMIT - REST) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 10 ? 10 : FIT;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + REST;
   static constexpr int BOX = NT >= 128 ? 64 : 16;             // rows of A in one copy
   static constexpr int CH = NT / 2;                           // rows of A a drain thread holds
   static constexpr int CW = CH >= 32 ? 32 : 16;               // TMEM columns read at a time
-  // 128 sums a drain thread: its warps take registers from the others.  128 threads at
-  // 88 and 256 at 208 are the 384 * 168 of the launch (checked before the first launch).
-  static constexpr bool MOVE_REGS = CH * OPS >= 128;
   static_assert(TMEM_COLS == 512 || TMEM_COLS == 256, "TMEM allocations are powers of two");
-  static_assert(STAGES >= 3, "the ring needs three stages");
-  static_assert(8 * (2 * STAGES + 3 * NBUF + 4) <= BAR_BYTES, "barrier area");
+  static_assert(STAGES >= 4, "the ring holds a group of blocks");
+  static_assert(OPS * NT * BN * 4 <= STAGES * STAGE_BYTES, "a split's sums lie over the ring");
+  static_assert(8 * (2 * STAGES + 8) <= BAR_BYTES, "barrier area");
 };
 
 struct Params {
   BlocksArgs a;
   int kblocks, tiles_n, split;
+  int c_vec;                    // four neighbouring columns of C (or codes) are one aligned vector
 };
 
-// Barrier `id` of 128 threads; and the same, returning whether any of them has `p`.
-__device__ __forceinline__ void sync_128(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool any_of_128(int id, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.or.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(id), "r"(p ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
+// Hardware barriers: 1 + g the drain warps and the signal warp at group buffer g, 3 the 256
+// drain threads.  Nobody can be left waiting: both sides go through the same groups and
+// items to the end, after an abort without results.
+__device__ __forceinline__ void sync_signal(int g) { asm volatile("bar.sync %0, 288;" ::"r"(1 + g) : "memory"); }
+__device__ __forceinline__ void sync_drain() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
 template <int CW>
 __device__ __forceinline__ void tmem_read(uint32_t addr, uint32_t (&r)[CW]) {
@@ -122,13 +120,75 @@ __device__ __forceinline__ float4 sum_ranks(uint32_t off, int split) {
   return s;
 }
 
+// Four neighbouring columns n .. of row p0 + m of the product, by a whole warp: s their sums
+// (u the up-projection's).  Columns past N come as zeros.
+template <bool SW>
+__device__ __forceinline__ void finish_row(const Params& p, const Item& i, int m, float4 s, float4 u, int lane) {
+  const BlocksArgs& a = p.a;
+  const int n = i.nb * BN + lane * 4;
+  const float sv[4] = {s.x, s.y, s.z, s.w};
+  if constexpr (SW) {
+    const float uv[4] = {u.x, u.y, u.z, u.w};
+    float h[4], big = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      h[q] = n + q < a.N ? swiglu_combine(sv[q], uv[q]) : 0.f;
+      big = fmaxf(big, fabsf(h[q]));                            // NaN is left out
+    }
+    // as whole numbers magnitudes order as they are
+    const float sc = kv_scale_for<kKvE4M3>(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big))));
+    const float r = kv_recip(sc);
+    const uint32_t c = kv_code2<kKvE4M3>(__fmul_rn(h[0], r), __fmul_rn(h[1], r)) |
+                       (kv_code2<kKvE4M3>(__fmul_rn(h[2], r), __fmul_rn(h[3], r)) << 16);
+    const long long row = i.p0 + m;
+    // rows of a.hq are whole vectors; codes past N are 0
+    if (n < a.ldh) *reinterpret_cast<uint32_t*>(a.hq + row * a.ldh + n) = c;
+    if (lane == 0) a.hs[row * a.ldhs + i.nb] = sc;
+  } else {
+    int from, to;
+    expert_row(a, i.p0 + m, from, to);
+    if (to < 0) return;
+    if (p.c_vec && n + 4 <= a.N) {
+      float v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = a.alpha * sv[q];
+      if (a.out_bf16) {
+        uint2* c = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.C) + (long long)to * a.ldc + n);
+        if (a.beta != 0.f) {
+          const uint2 o = *c;
+          v[0] = fmaf(a.beta, __uint_as_float(o.x << 16), v[0]);
+          v[1] = fmaf(a.beta, __uint_as_float(o.x & 0xffff0000u), v[1]);
+          v[2] = fmaf(a.beta, __uint_as_float(o.y << 16), v[2]);
+          v[3] = fmaf(a.beta, __uint_as_float(o.y & 0xffff0000u), v[3]);
+        }
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+        *c = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      } else {
+        float4* c = reinterpret_cast<float4*>(static_cast<float*>(a.C) + (long long)to * a.ldc + n);
+        if (a.beta != 0.f) {
+          const float4 o = *c;
+          v[0] = fmaf(a.beta, o.x, v[0]);
+          v[1] = fmaf(a.beta, o.y, v[1]);
+          v[2] = fmaf(a.beta, o.z, v[2]);
+          v[3] = fmaf(a.beta, o.w, v[3]);
+        }
+        *c = make_float4(v[0], v[1], v[2], v[3]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (n + q < a.N) blocks_store(a, to, n + q, sv[q]);
+    }
+  }
+}
+
 // GATHER: A's rows through tile::gather4 (mapA has boxes of one row).
 template <int NT, bool SW, bool GATHER>
 __global__ void __launch_bounds__(THREADS, 1)
     blocks_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-                  const __grid_constant__ CUtensorMap mapB2, const Params p) {
+                  const __grid_constant__ CUtensorMap mapB2, const __grid_constant__ Params p) {
   using C = Cfg<NT, SW>;
-  constexpr int STAGES = C::STAGES, NBUF = C::NBUF, COLS = C::COLS, CH = C::CH, CW = C::CW;
+  constexpr int STAGES = C::STAGES, GROUP = C::GROUP, COLS = C::COLS, CH = C::CH, CW = C::CW;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -136,10 +196,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto w_tile = [&](int s) { return base + s * C::STAGE_BYTES; };
   auto t_tile = [&](int s) { return base + s * C::STAGE_BYTES + C::OPS * W_BYTES; };
   uint8_t* at = base_ptr + STAGES * C::STAGE_BYTES;
-  float* scales = reinterpret_cast<float*>(at);                  // [NBUF][COLS]
+  float* scales = reinterpret_cast<float*>(at);                  // [2][GROUP][COLS]
   at += C::SCALE_BYTES;
-  uint8_t* out_codes = at;                                       // [NT][BN]
-  float* out_big = reinterpret_cast<float*>(at + (SW ? NT * BN : 0));   // [4][NT]
+  float* out = reinterpret_cast<float*>(at);                     // [OPS][CHUNK][BN]
   at += C::OUT_BYTES;
   const uint32_t bar_base = base + (uint32_t)(at - base_ptr);
   uint8_t* bar_ptr = at;
@@ -149,12 +208,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   int* num = beg + kBlocksMaxExperts;
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
   auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
-  auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + b); };
-  auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + NBUF + b); };
-  auto sfull_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + 2 * NBUF + b); };
-  const uint32_t drain_bar = bar_base + 8u * (2 * STAGES + 3 * NBUF);
+  auto tfull_bar = [&](int g) { return bar_base + 8u * (2 * STAGES + g); };
+  auto tempty_bar = [&](int g) { return bar_base + 8u * (2 * STAGES + 2 + g); };
+  auto sfull_bar = [&](int g) { return bar_base + 8u * (2 * STAGES + 4 + g); };
+  const uint32_t drain_bar = bar_base + 8u * (2 * STAGES + 6);
   const uint32_t stall_bar = drain_bar + 8u;                     // test hook: nothing arrives
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (2 * STAGES + 3 * NBUF + 2));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (2 * STAGES + 8));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const BlocksArgs& a = p.a;
@@ -166,10 +225,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
-    for (int b = 0; b < NBUF; ++b) {
-      mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), EPI_WARPS);
-      mbar_init(sfull_bar(b), 32);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(tfull_bar(g), 1);
+      mbar_init(tempty_bar(g), EPI_WARPS);
+      mbar_init(sfull_bar(g), 32);
     }
     mbar_init(drain_bar, 1);
     mbar_init(stall_bar, 1);
@@ -195,182 +254,211 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int k_lo = (int)((long long)p.kblocks * rank / split), k_hi = (int)((long long)p.kblocks * (rank + 1) / split);
   Walk walk{pre, beg, num, NT, p.tiles_n, 0};
 
-  if (warp < EPI_FIRST) {
-    if constexpr (C::MOVE_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 0) {
-      // ------------------------------------------------------------ copies
-      uint32_t issued = 0, issued_par = 0;
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      const bool leader = elect_one_sync();
-      for (long long it = first; ok && it < items; it += step) {
-        const Item i = walk.at(it);
-        const int n_mma = mma_rows(i.rows);
-        int y[4];
-        const int group = lane * 4;                    // GATHER: this lane's four rows
-        int copies = (n_mma + C::BOX - 1) / C::BOX;
-        uint32_t bytes = (uint32_t)(C::OPS * W_BYTES + (GATHER ? n_mma : copies * C::BOX) * BK);
-        if (GATHER) {
+  if (warp == 0) {
+    // -------------------------------------------------------------- copies
+    uint32_t issued = 0, issued_par = 0;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const bool leader = elect_one_sync();
+    auto mark = [&](int s) {
+      issued |= 1u << s;
+      issued_par = (issued_par & ~(1u << s)) | (phase << s);
+    };
+    for (long long it = first; ok && it < items; it += step) {
+      const Item i = walk.at(it);
+      const int n_mma = mma_rows(i.rows);
+      const int copies = (n_mma + C::BOX - 1) / C::BOX;
+      const uint32_t bytes = (uint32_t)(C::OPS * W_BYTES + (GATHER ? n_mma : copies * C::BOX) * BK);
+      auto weights = [&](int s, int kb) {
+        mbar_arrive_expect_tx(full_bar(s), bytes);
+        tma_load_3d(w_tile(s), &mapB, full_bar(s), i.nb * BN, kb * BK, i.e);
+        if (SW) tma_load_3d(w_tile(s) + W_BYTES, &mapB2, full_bar(s), i.nb * BN, kb * BK, i.e);
+      };
+      // the ring is empty at first: its weights are on their way while `order` is read
+      const int ahead = GATHER && it == first ? min(STAGES, k_hi - k_lo) : 0;
+      if (leader)
+        for (int s = 0; s < ahead; ++s) weights(s, k_lo + s);
+      __syncwarp();
+      int y[4];
+      const int group = lane * 4;                      // GATHER: this lane's four rows
+      if (GATHER) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            int from = -1, to;
-            if (group + q < i.rows) expert_row(a, i.p0 + group + q, from, to);
-            y[q] = from >= 0 ? from : a.a_rows;       // outside: zeros
-          }
+        for (int q = 0; q < 4; ++q) {
+          int from = -1, to;
+          if (group + q < i.rows) expert_row(a, i.p0 + group + q, from, to);
+          y[q] = from >= 0 ? from : a.a_rows;         // outside: zeros
         }
-        for (int kb = k_lo; kb < k_hi; ++kb) {
-          if (GATHER || leader) {
-            if (!mbar_wait(empty_bar(stage), phase ^ 1u, a.timeout_ns, abort_flag)) {
-              if (!*abort_flag) report_status(a.status, 5, kSiteBlocksProducer);
-              *abort_flag = 1;
-              ok = false;
-            }
+      }
+      for (int kb = k_lo; kb < k_hi; ++kb) {
+        const bool sent = kb - k_lo < ahead;           // its weights are under way
+        if (!sent) {
+          if ((GATHER || leader) && !mbar_wait(empty_bar(stage), phase ^ 1u, a.timeout_ns, abort_flag)) {
+            if (!*abort_flag) report_status(a.status, 5, kSiteBlocksProducer);
+            *abort_flag = 1;
+            ok = false;
           }
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (leader) {
-            mbar_arrive_expect_tx(full_bar(stage), bytes);
-            tma_load_3d(w_tile(stage), &mapB, full_bar(stage), i.nb * BN, kb * BK, i.e);
-            if (SW) tma_load_3d(w_tile(stage) + W_BYTES, &mapB2, full_bar(stage), i.nb * BN, kb * BK, i.e);
-            if (!GATHER)
-              for (int c = 0; c < copies; ++c)
-                tma_load_2d(t_tile(stage) + c * C::BOX * BK, &mapA, full_bar(stage), kb * BK, i.p0 + c * C::BOX);
+        }
+        if (leader) {
+          if (!sent) weights(stage, kb);
+          if (!GATHER)
+            for (int c = 0; c < copies; ++c)
+              tma_load_2d(t_tile(stage) + c * C::BOX * BK, &mapA, full_bar(stage), kb * BK, i.p0 + c * C::BOX);
+        }
+        if (GATHER) {
+          __syncwarp();                                // the bytes are expected before any arrive
+          if (group < n_mma)
+            tma_gather4(t_tile(stage) + group * BK, &mapA, full_bar(stage), kb * BK, y[0], y[1], y[2], y[3]);
+        }
+        mark(stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (*abort_flag && leader)
+      for (int s = 0; s < STAGES; ++s)
+        if (((issued >> s) & 1u) && !mbar_wait(full_bar(s), (issued_par >> s) & 1u, kDrainWaitNs, nullptr))
+          report_status(a.status, 5, kSiteBlocksDrain);
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- MMA
+    if (elect_one_sync()) {
+      int stage = 0, g = 0;
+      uint32_t phase = 0, gphase = 0;
+      bool ok = true, issued_any = false;
+      if (a.stall && blockIdx.x == 0 && !mbar_wait(stall_bar, 0, a.timeout_ns / 4, abort_flag)) {
+        if (!*abort_flag) report_status(a.status, 5, kSiteBlocksMma);
+        *abort_flag = 1;
+        ok = false;
+      }
+      for (long long it = first; ok && it < items; it += step) {
+        const Item i = walk.at(it);
+        const uint32_t idesc = idesc_f8_f32(BN, (uint32_t)mma_rows(i.rows), kE4M3, kE4M3, /*B^T MN-major*/ 1, /*A K-major*/ 0);
+        for (int kb = k_lo; kb < k_hi; ++kb) {
+          const int u = (kb - k_lo) % GROUP;
+          ok = (u != 0 || mbar_wait(tempty_bar(g), gphase ^ 1u, a.timeout_ns, abort_flag)) &&
+               mbar_wait(full_bar(stage), phase, a.timeout_ns, abort_flag);
+          if (!ok) {
+            if (!*abort_flag) report_status(a.status, 5, kSiteBlocksMma);
+            *abort_flag = 1;
+            break;
           }
-          if (GATHER) {
-            __syncwarp();                              // the bytes are expected before any arrive
-            if (group < n_mma)
-              tma_gather4(t_tile(stage) + group * BK, &mapA, full_bar(stage), kb * BK, y[0], y[1], y[2], y[3]);
+          tc_fence_after();
+          const uint32_t d = tmem_base + (uint32_t)((g * GROUP + u) * COLS);
+#pragma unroll
+          for (int op = 0; op < C::OPS; ++op)
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk)
+              tc_mma_f8(d + op * NT, smem_desc_sw128(w_tile(stage) + op * W_BYTES + kk * 32 * BN, W_BYTES, 1024),
+                        smem_desc_sw128(t_tile(stage) + kk * 32, 16, 1024), idesc, kk != 0 ? 1u : 0u);
+          issued_any = true;
+          tc_commit(empty_bar(stage));
+          if (u == GROUP - 1 || kb + 1 == k_hi) {
+            tc_commit(tfull_bar(g));
+            if (++g == 2) {
+              g = 0;
+              gphase ^= 1u;
+            }
           }
-          issued |= 1u << stage;
-          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      if (*abort_flag && leader)
-        for (int s = 0; s < STAGES; ++s)
-          if (((issued >> s) & 1u) && !mbar_wait(full_bar(s), (issued_par >> s) & 1u, kDrainWaitNs, nullptr))
-            report_status(a.status, 5, kSiteBlocksDrain);
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA
-      if (elect_one_sync()) {
-        int stage = 0, b = 0;
-        uint32_t phase = 0, bphase = 0;
-        bool ok = true, issued_any = false;
-        if (a.stall && blockIdx.x == 0 && !mbar_wait(stall_bar, 0, a.timeout_ns / 4, abort_flag)) {
-          if (!*abort_flag) report_status(a.status, 5, kSiteBlocksMma);
-          *abort_flag = 1;
-          ok = false;
-        }
-        for (long long it = first; ok && it < items; it += step) {
-          const Item i = walk.at(it);
-          const uint32_t idesc = idesc_f8_f32(BN, (uint32_t)mma_rows(i.rows), kE4M3, kE4M3, /*B^T MN-major*/ 1, /*A K-major*/ 0);
-          for (int kb = k_lo; kb < k_hi; ++kb) {
-            if (!mbar_wait(tempty_bar(b), bphase ^ 1u, a.timeout_ns, abort_flag) ||
-                !mbar_wait(full_bar(stage), phase, a.timeout_ns, abort_flag)) {
-              if (!*abort_flag) report_status(a.status, 5, kSiteBlocksMma);
-              *abort_flag = 1;
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t d = tmem_base + (uint32_t)(b * COLS);
-#pragma unroll
-            for (int op = 0; op < C::OPS; ++op)
-#pragma unroll
-              for (int kk = 0; kk < BK / 32; ++kk)
-                tc_mma_f8(d + op * NT, smem_desc_sw128(w_tile(stage) + op * W_BYTES + kk * 32 * BN, W_BYTES, 1024),
-                          smem_desc_sw128(t_tile(stage) + kk * 32, 16, 1024), idesc, kk != 0 ? 1u : 0u);
-            issued_any = true;
-            tc_commit(empty_bar(stage));
-            tc_commit(tfull_bar(b));
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1u;
-            }
-            if (++b == NBUF) {
-              b = 0;
-              bphase ^= 1u;
-            }
-          }
-        }
-        if (*abort_flag && issued_any) {
-          tc_commit(drain_bar);
-          if (!mbar_wait(drain_bar, 0, kDrainWaitNs, nullptr)) report_status(a.status, 5, kSiteBlocksDrain);
-        }
-      }
-    } else if (warp == 2) {
-      // ------------------------------------------------------------ scales
-      constexpr int PER = NT / 32;
-      int b = 0;
-      uint32_t bphase = 0;
-      bool ok = true;
-      for (long long it = first; ok && it < items; it += step) {
-        const Item i = walk.at(it);
-        const float* row[PER];
-#pragma unroll
-        for (int q = 0; q < PER; ++q) {
-          int from = -1, to;
-          if (q * 32 + lane < i.rows) expert_row(a, i.p0 + q * 32 + lane, from, to);
-          row[q] = from >= 0 ? a.sa + (long long)from * a.ldsa : nullptr;
-        }
-        const float* sb = a.sb + i.e * a.sb_stride + i.nb;
-        const float* sb2 = SW ? a.sb2 + i.e * a.sb_stride + i.nb : nullptr;
-        // two blocks ahead: the loads land while the epilogue works
-        float v[2][PER], w[2], w2[2];
-        auto load = [&](int s, int kb) {
-          const bool in = kb < k_hi;
-#pragma unroll
-          for (int q = 0; q < PER; ++q) v[s][q] = in && row[q] != nullptr ? __ldg(row[q] + kb) : 0.f;
-          w[s] = in ? __ldg(sb + kb * a.ldsb) : 0.f;
-          if (SW) w2[s] = in ? __ldg(sb2 + kb * a.ldsb) : 0.f;
-        };
-        auto put = [&](int s) {
-          float* to = scales + b * COLS + lane;
-#pragma unroll
-          for (int q = 0; q < PER; ++q) {
-            to[q * 32] = v[s][q] * w[s];
-            if (SW) to[NT + q * 32] = v[s][q] * w2[s];
-          }
-          mbar_arrive(sfull_bar(b));
-          if (++b == NBUF) {
-            b = 0;
-            bphase ^= 1u;
-          }
-        };
-        load(0, k_lo);
-        load(1, k_lo + 1);
-        for (int kb = k_lo; kb < k_hi; kb += 2) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (kb + s < k_hi) {
-              if (ok && !__all_sync(0xffffffffu, mbar_wait(tempty_bar(b), bphase ^ 1u, a.timeout_ns, abort_flag))) {
-                if (!*abort_flag) report_status(a.status, 5, kSiteBlocksScales);
-                *abort_flag = 1;
-                ok = false;
-              }
-              if (ok) {
-                put(s);
-                load(s, kb + 2 + s);
-              }
-            }
-          }
-          if (!ok) break;
-        }
+      if (*abort_flag && issued_any) {
+        tc_commit(drain_bar);
+        if (!mbar_wait(drain_bar, 0, kDrainWaitNs, nullptr)) report_status(a.status, 5, kSiteBlocksDrain);
       }
     }
-  } else {
-    // ------------------------------------------------------------ drain and epilogue
-    if constexpr (C::MOVE_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int quarter = warp % 4, half = (warp - EPI_FIRST) / 4;
-    const uint32_t t_lane = tmem_base + ((uint32_t)(quarter * 32) << 16);
-    int b = 0;
-    uint32_t bphase = 0;
+  } else if (warp == 2) {
+    // -------------------------------------------------------------- scales
+    constexpr int PER = NT / 32;
+    int g = 0;
+    uint32_t gphase = 0;
     bool ok = true;
     for (long long it = first; ok && it < items; it += step) {
+      const Item i = walk.at(it);
+      const float* row[PER];
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        int from = -1, to;
+        if (q * 32 + lane < i.rows) expert_row(a, i.p0 + q * 32 + lane, from, to);
+        row[q] = from >= 0 ? a.sa + (long long)from * a.ldsa : nullptr;
+      }
+      const float* sb = a.sb + i.e * a.sb_stride + i.nb;
+      const float* sb2 = SW ? a.sb2 + i.e * a.sb_stride + i.nb : nullptr;
+      // a group ahead: the loads land while the one before is drained
+      float v[GROUP][PER], w[GROUP], w2[GROUP];
+      auto load = [&](int kb) {
+#pragma unroll
+        for (int u = 0; u < GROUP; ++u) {
+          const bool in = kb + u < k_hi;
+#pragma unroll
+          for (int q = 0; q < PER; ++q) v[u][q] = in && row[q] != nullptr ? __ldg(row[q] + kb + u) : 0.f;
+          w[u] = in ? __ldg(sb + (kb + u) * a.ldsb) : 0.f;
+          if (SW) w2[u] = in ? __ldg(sb2 + (kb + u) * a.ldsb) : 0.f;
+        }
+      };
+      load(k_lo);
+      for (int kb = k_lo; kb < k_hi; kb += GROUP) {
+        if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar(g), gphase ^ 1u, a.timeout_ns, abort_flag))) {
+          if (!*abort_flag) report_status(a.status, 5, kSiteBlocksScales);
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int u = 0; u < GROUP; ++u) {
+          float* to = scales + (g * GROUP + u) * COLS + lane;
+#pragma unroll
+          for (int q = 0; q < PER; ++q) {
+            to[q * 32] = v[u][q] * w[u];
+            if (SW) to[NT + q * 32] = v[u][q] * w2[u];
+          }
+        }
+        mbar_arrive(sfull_bar(g));
+        if (++g == 2) {
+          g = 0;
+          gphase ^= 1u;
+        }
+        load(kb + GROUP);
+      }
+    }
+  } else if (warp == 3) {
+    // -------------------------------------------------------------- signals
+    int g = 0;
+    uint32_t gphase = 0;
+    bool ok = true;
+    for (long long it = first; it < items; it += step)
+      for (int kb = k_lo; kb < k_hi; kb += GROUP) {
+        if (lane == 0 && ok) {
+          ok = mbar_wait(sfull_bar(g), gphase, a.timeout_ns, abort_flag) &&
+               mbar_wait(tfull_bar(g), gphase, a.timeout_ns, abort_flag);
+          if (!ok) {
+            if (!*abort_flag) report_status(a.status, 5, kSiteBlocksEpilogue);
+            *abort_flag = 1;
+          }
+        }
+        __syncwarp();
+        tc_fence_after();
+        tc_fence_before();
+        sync_signal(g);
+        if (++g == 2) {
+          g = 0;
+          gphase ^= 1u;
+        }
+      }
+  } else {
+    // -------------------------------------------------------------- drain and epilogue
+    const int quarter = warp % 4, half = (warp - EPI_FIRST) / 4;
+    const int nl = quarter * 32 + lane;                          // column of the tile
+    const uint32_t t_lane = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    int g = 0;
+    for (long long it = first; it < items; it += step) {
       const Item i = walk.at(it);
       const int n_mma = mma_rows(i.rows);
       uint64_t acc[C::OPS][CH / 2];
@@ -378,51 +466,39 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int op = 0; op < C::OPS; ++op)
 #pragma unroll
         for (int j = 0; j < CH / 2; ++j) acc[op][j] = 0;
-      for (int kb = k_lo; kb < k_hi; ++kb) {
-        ok = mbar_wait(sfull_bar(b), bphase, a.timeout_ns, abort_flag) &&
-             mbar_wait(tfull_bar(b), bphase, a.timeout_ns, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          if (!*abort_flag) report_status(a.status, 5, kSiteBlocksEpilogue);
-          *abort_flag = 1;
-          break;
-        }
+      for (int kb = k_lo; kb < k_hi; kb += GROUP) {
+        sync_signal(g);
         tc_fence_after();
-#pragma unroll
-        for (int op = 0; op < C::OPS; ++op)
+#pragma unroll 1
+        for (int u = 0; u < GROUP && kb + u < k_hi; ++u) {
+          const int buf = (g * GROUP + u) * COLS;
 #pragma unroll
           for (int c = 0; c < CH / CW; ++c) {
-            const int col = half * CH + c * CW;          // rows of A: col .. col + CW - 1
+            const int col = half * CH + c * CW;                  // rows of A: col .. col + CW - 1
             if (col < n_mma) {
-              uint32_t r[CW];
-              tmem_read<CW>(t_lane + (uint32_t)(b * COLS + op * NT + col), r);
-              const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scales + b * COLS + op * NT + col);
+              uint32_t r[C::OPS][CW];
+#pragma unroll
+              for (int op = 0; op < C::OPS; ++op) tmem_read<CW>(t_lane + (uint32_t)(buf + op * NT + col), r[op]);
               tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < CW / 4; ++j) {
-                const ulonglong2 s = sc[j];
-                fma2(acc[op][c * CW / 2 + 2 * j], pack2(r[4 * j], r[4 * j + 1]), s.x);
-                fma2(acc[op][c * CW / 2 + 2 * j + 1], pack2(r[4 * j + 2], r[4 * j + 3]), s.y);
+              for (int op = 0; op < C::OPS; ++op) {
+                const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scales + buf + op * NT + col);
+#pragma unroll
+                for (int j = 0; j < CW / 4; ++j) {
+                  const ulonglong2 s = sc[j];
+                  fma2(acc[op][c * CW / 2 + 2 * j], pack2(r[op][4 * j], r[op][4 * j + 1]), s.x);
+                  fma2(acc[op][c * CW / 2 + 2 * j + 1], pack2(r[op][4 * j + 2], r[op][4 * j + 3]), s.y);
+                }
               }
             }
           }
+        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tempty_bar(b));
-        if (++b == NBUF) {
-          b = 0;
-          bphase ^= 1u;
-        }
+        if (lane == 0) mbar_arrive(tempty_bar(g));
+        g ^= 1;
       }
-      if constexpr (SW) {
-        // the four warps of a half meet below: they go on or give up together
-        if (split == 1) ok = !any_of_128(1 + half, !ok);
-      }
-      if (!ok) break;
-      auto value = [&](int op, int j) {
-        return part2(acc[op][j / 2], j & 1);
-      };
-      const int nl = quarter * 32 + lane, n = i.nb * BN + nl;
+      auto value = [&](int op, int j) { return part2(acc[op][j / 2], j & 1); };
       if (split > 1) {
         // this rank's sums, [row of A][column of B], over the ring (every copy has landed
         // and every MMA has read: the last accumulator is complete)
@@ -432,44 +508,26 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int j = 0; j < CH; ++j)
             if (half * CH + j < i.rows) part[(op * NT + half * CH + j) * BN + nl] = value(op, j);
-      } else if constexpr (SW) {
-        float h[CH];
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-          h[j] = n < a.N ? swiglu_combine(value(0, j), value(1, j)) : 0.f;
-          // as whole numbers magnitudes order as they are; NaN is left out
-          const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(h[j]), 0.f)));
-          if (lane == 0) out_big[quarter * NT + half * CH + j] = __uint_as_float(big);
-        }
-        sync_128(1 + half);
-        uint8_t* codes = out_codes + half * CH * BN;
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-          const float* q = out_big + half * CH + j;
-          const float s = kv_scale_for<kKvE4M3>(fmaxf(fmaxf(q[0], q[NT]), fmaxf(q[2 * NT], q[3 * NT])));
-          codes[j * BN + nl] = (uint8_t)kv_code2<kKvE4M3>(__fmul_rn(h[j], kv_recip(s)), 0.f);
-          if (nl == j % 128 && half * CH + j < i.rows) a.hs[(long long)(i.p0 + half * CH + j) * a.ldhs + i.nb] = s;
-        }
-        sync_128(1 + half);
-        // rows of 128 codes, 16 bytes a thread (rows of a.hq are whole vectors)
-        for (int x = quarter * 32 + lane; x < CH * 8; x += 128) {
-          const int j = x / 8, c = (x % 8) * 16;
-          if (half * CH + j < i.rows && i.nb * BN + c < a.ldh)
-            *reinterpret_cast<uint4*>(a.hq + (long long)(i.p0 + half * CH + j) * a.ldh + i.nb * BN + c) =
-                *reinterpret_cast<const uint4*>(codes + j * BN + c);
-        }
       } else {
-        int to = -1;
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-          if (j % 32 == 0) {                              // lane's row of the next 32
-            const int m = half * CH + j + lane;
-            int from;
-            to = -1;
-            if (m < i.rows) expert_row(a, i.p0 + m, from, to);
-          }
-          const int o = __shfl_sync(0xffffffffu, to, j % 32);
-          if (o >= 0 && n < a.N) blocks_store(a, o, n, value(0, j));
+        for (int c = 0; c < CH / 16; ++c) {                      // 16 rows of each half
+          if (c > 0 || it != first) sync_drain();                // the chunk before is stored
+#pragma unroll
+          for (int op = 0; op < C::OPS; ++op)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (half * CH + c * 16 + j < i.rows) out[(op * CHUNK + half * 16 + j) * BN + nl] = value(op, c * 16 + j);
+          sync_drain();
+          if (!*abort_flag)
+#pragma unroll 1
+            for (int x = warp - EPI_FIRST; x < CHUNK; x += EPI_WARPS) {
+              const int m = x / 16 * CH + c * 16 + x % 16;
+              if (m < i.rows) {
+                const float4 s = *reinterpret_cast<const float4*>(out + x * BN + lane * 4);
+                const float4 u = SW ? *reinterpret_cast<const float4*>(out + (CHUNK + x) * BN + lane * 4) : s;
+                finish_row<SW>(p, i, m, s, u, lane);
+              }
+            }
         }
       }
     }
@@ -477,43 +535,19 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   __syncwarp();
   if (split > 1) {
-    cluster_sync();                                       // every rank's sums are there
+    cluster_sync();                                              // every rank's sums are there
     if (first < items && !*abort_flag && warp >= EPI_FIRST) {
       const Item i = walk.at(first);
       const uint32_t part = smem_u32(base_ptr);
+#pragma unroll 1
       for (int m = rank + split * (warp - EPI_FIRST); m < i.rows; m += split * EPI_WARPS) {
         const uint32_t off = part + (uint32_t)(m * BN + lane * 4) * 4u;
         const float4 s = sum_ranks(off, split);
-        const int n = i.nb * BN + lane * 4;
-        const float sv[4] = {s.x, s.y, s.z, s.w};
-        if constexpr (SW) {
-          const float4 u = sum_ranks(off + (uint32_t)(NT * BN) * 4u, split);
-          const float uv[4] = {u.x, u.y, u.z, u.w};
-          float h[4], big = 0.f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            h[q] = n + q < a.N ? swiglu_combine(sv[q], uv[q]) : 0.f;
-            big = fmaxf(big, fabsf(h[q]));
-          }
-          const float sc = kv_scale_for<kKvE4M3>(
-              __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big))));
-          const float r = kv_recip(sc);
-          const uint32_t c = kv_code2<kKvE4M3>(__fmul_rn(h[0], r), __fmul_rn(h[1], r)) |
-                             (kv_code2<kKvE4M3>(__fmul_rn(h[2], r), __fmul_rn(h[3], r)) << 16);
-          const long long row = i.p0 + m;
-          if (n < a.ldh) *reinterpret_cast<uint32_t*>(a.hq + row * a.ldh + n) = c;
-          if (lane == 0) a.hs[row * a.ldhs + i.nb] = sc;
-        } else {
-          int from, to;
-          expert_row(a, i.p0 + m, from, to);
-          if (to >= 0)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (n + q < a.N) blocks_store(a, to, n + q, sv[q]);
-        }
+        const float4 u = SW ? sum_ranks(off + (uint32_t)(NT * BN) * 4u, split) : s;
+        finish_row<SW>(p, i, m, s, u, lane);
       }
     }
-    cluster_sync();                                       // no rank leaves while others read its sums
+    cluster_sync();                                              // no rank leaves while others read its sums
   }
   griddep_launch_dependents();
   tc_fence_before();
@@ -529,24 +563,15 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
                 int split, int num_sms, cudaStream_t s) {
   using C = Cfg<NT, SW>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e;
-  if constexpr (C::MOVE_REGS) {
-    // a launch with fewer registers than the split adds up to would wait for them forever
-    static std::atomic<int> regs{0};
-    if (regs.load(std::memory_order_relaxed) == 0) {
-      cudaFuncAttributes attr;
-      if ((e = cudaFuncGetAttributes(&attr, blocks_kernel<NT, SW, GATHER>)) != cudaSuccess) return e;
-      regs.store(attr.numRegs, std::memory_order_relaxed);
-    }
-    if (regs.load(std::memory_order_relaxed) < 168) return cudaErrorInvalidConfiguration;
-  }
-  e = set_smem_once(done, blocks_kernel<NT, SW, GATHER>, C::SMEM_BYTES);
+  cudaError_t e = set_smem_once(done, blocks_kernel<NT, SW, GATHER>, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   Params p;
   p.a = a;
   p.kblocks = (a.K + BK - 1) / BK;
   p.tiles_n = (a.N + BN - 1) / BN;
   p.split = split;
+  const int osz = a.out_bf16 ? 2 : 4;
+  p.c_vec = reinterpret_cast<uintptr_t>(a.C) % (4 * osz) == 0 && a.ldc % 4 == 0 ? 1 : 0;
   const long long items = blocks_row_tiles(a.rows, a.offsets != nullptr ? a.experts : 1, NT) * p.tiles_n;
   long long grid = split > 1 ? items * split : items < num_sms ? items : num_sms;
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
@@ -572,15 +597,9 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
 int launch_blocks(const BlocksArgs& a, const BlocksPlan& plan, const CUtensorMap* mapA, const CUtensorMap* mapB,
                   const CUtensorMap* mapB2, int num_sms, cudaStream_t s) {
   const int split = plan.split;
-  if (a.B2 != nullptr) {
-    if ((a.gather != 0) != (plan.nt == 32)) return cudaErrorInvalidValue;
-    switch (plan.nt) {
-      case 32: return launch_impl<32, true, true>(a, mapA, mapB, mapB2, split, num_sms, s);
-      case 64: return launch_impl<64, true, false>(a, mapA, mapB, mapB2, split, num_sms, s);
-      case 128: return launch_impl<128, true, false>(a, mapA, mapB, mapB2, split, num_sms, s);
-    }
-    return cudaErrorInvalidValue;
-  }
+  if (a.B2 != nullptr)
+    return plan.nt == 32 && a.gather != 0 ? launch_impl<32, true, true>(a, mapA, mapB, mapB2, split, num_sms, s)
+                                          : cudaErrorInvalidValue;
   if (a.gather != 0) return cudaErrorInvalidValue;
   switch (plan.nt) {
     case 32: return launch_impl<32, false, false>(a, mapA, mapB, mapB2, split, num_sms, s);

@@ -220,11 +220,13 @@ inline int cluster_split(int tiles_n, int k_units, int num_sms, int forced, int 
   return s;
 }
 
-// Block-scaled products: the row tile (32, 64 or 128: the swapped kernel; 256: CTA pairs)
-// and the CTAs that share a tile's K.  `mean`: rows of an expert if all that can have some
-// have as many.  A tile as wide as the mean reads each weight once; narrower ones (from L2
-// then) are taken while there are fewer items than SMs.  K is split where even those
-// leave SMs idle, with at least four blocks of 128 a CTA.
+// Block-scaled products: the row tile (32, 64 or 128 rows as the MMA's columns; 256: items of
+// 128 rows and 256 columns) and the CTAs that share a tile's K.  `mean`: rows of an expert if
+// all that can have some have as many.  The wide items take calls with more than 32 rows an
+// expert that make at least one for every second SM; else a tile as wide as the mean reads
+// each weight once, and narrower ones (from L2 then) are taken while there are fewer items
+// than SMs.  K is split where even those leave SMs idle, with at least four blocks of 128 a
+// CTA.  Gate and up weights come in tiles of 32 rows only.
 struct BlocksChoice {
   int nt, split;
 };
@@ -235,19 +237,18 @@ inline BlocksChoice blocks_choice(long long rows, int experts, int N, int kblock
   const int tiles_n = (N + 127) / 128;
   BlocksChoice c = {32, 1};
   if (forced != 0) {
-    c.nt = forced;
+    c.nt = forced == 256 || !two_weights ? forced : 32;
     return c;
   }
-  const long long pairs = met * ((mean + 255) / 256) * (two_weights ? tiles_n : (N + 255) / 256);
-  if (mean > 128 && pairs * 2 >= num_sms) {
+  const long long wide = met * ((mean + 127) / 128) * (two_weights ? tiles_n : (N + 255) / 256);
+  if (mean > 32 && wide * 2 >= num_sms) {
     c.nt = 256;
     return c;
   }
-  while (c.nt < 128 && c.nt < mean) c.nt *= 2;
-  while (c.nt > 32 && met * ((mean + c.nt - 1) / c.nt) * tiles_n < num_sms) c.nt /= 2;
+  while (!two_weights && c.nt < 128 && c.nt < mean) c.nt *= 2;
+  while (c.nt > 32 && met * ((mean + c.nt - 1) / c.nt) * tiles_n < num_sms && kblocks < 8) c.nt /= 2;
   const long long items = met * ((mean + c.nt - 1) / c.nt) * tiles_n;
-  if (c.nt <= 64)
-    while (c.split < 8 && items * c.split * 2 <= num_sms && kblocks >= 8 * c.split) c.split *= 2;
+  while (c.split < 8 && items * c.split * 2 <= num_sms && kblocks >= 8 * c.split) c.split *= 2;
   return c;
 }
 
