@@ -89,6 +89,37 @@ __device__ __forceinline__ void list_row_tiles(const BlocksArgs& a, int* pre, in
   if (lane == 0) pre[a.experts] = run;
 }
 
+// The one item number `it` of a line as a Walk's, into out[0..3] (expert, first row, rows,
+// column tile; 0 rows where there are fewer items), by one warp.
+template <int NT>
+__device__ __forceinline__ void find_item(const BlocksArgs& a, int tiles_n, long long it, int* out, int lane) {
+  long long run = 0;                                   // items of the experts before
+  if (lane == 0) out[2] = 0;
+  __syncwarp();
+  for (int e0 = 0; e0 < a.experts; e0 += 32) {
+    const int e = e0 + lane;
+    int b = 0, n = 0;
+    if (e < a.experts) expert_rows(a, e, b, n);
+    const int tiles = (n + NT - 1) / NT;
+    long long s = (long long)tiles * tiles_n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) s += o;
+    }
+    const long long first = run + s - (long long)tiles * tiles_n;
+    if (it >= first && it < run + s) {                 // one lane at most
+      const int x = (int)(it - first), t = x % tiles;
+      out[0] = e;
+      out[1] = b + t * NT;
+      out[2] = min(NT, n - t * NT);
+      out[3] = x / tiles;
+    }
+    run += __shfl_sync(0xffffffffu, s, 31);
+    if (it < run) break;
+  }
+}
+
 // ---------------------------------------------------------------- two sums in one instruction
 __device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));

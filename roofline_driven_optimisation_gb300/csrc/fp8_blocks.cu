@@ -34,7 +34,7 @@
 // Schedule: items (row tile of an expert, column tile) in a line, expert by expert,
 // columns outermost inside an expert; CTA c takes items c, c + grid, ...  The counts are
 // read on the device, so no launch depends on the routing.  Where a call has fewer items
-// than SMs, K is split over a cluster of 2, 4 or 8 CTAs, whose sums meet in distributed
+// than SMs, K is split over a cluster of 2 to 8 CTAs, whose sums meet in distributed
 // shared memory in rank order.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -58,26 +58,34 @@ constexpr int W_BYTES = BN * BK;               // a weight tile: 128 k rows of 1
 constexpr int SMEM_LIMIT = 232448;
 constexpr int CHUNK = 32;                      // rows of A that go through shared memory at a time
 
-template <int NT, bool SW>
+// SPLIT: K is shared by a cluster, a CTA has one item, and its sums lie over the ring at the
+// end.  Tiles of 32 rows then take half of an SM: an SM's copies from HBM come to about 57
+// bytes a ns however many are in flight, so a decode step's few items have to reach every
+// SM alike, and two CTAs an SM let 86 items be 258 parts (86 CTAs: 9.3 us for the 45 MB of
+// a 4096 x 11008 weight).
+template <int NT, bool SW, bool SPLIT>
 struct Cfg {
+  static constexpr int CTAS = SPLIT && NT == 32 ? 2 : 1;      // an SM
+  static constexpr int LIMIT = CTAS == 2 ? 115200 : SMEM_LIMIT;
   static constexpr int OPS = SW ? 2 : 1;
   static constexpr int COLS = NT * OPS;                       // TMEM columns of an accumulator
   static constexpr int GROUP = 256 / COLS > 4 ? 4 : 256 / COLS;      // blocks that are handed over together
   static constexpr int TMEM_COLS = 2 * GROUP * COLS;
   static constexpr int STAGE_BYTES = OPS * W_BYTES + NT * BK;
   static constexpr int SCALE_BYTES = 2 * GROUP * COLS * 4;
-  static constexpr int OUT_BYTES = OPS * CHUNK * BN * 4;
+  static constexpr int OUT_BYTES = SPLIT ? 0 : OPS * CHUNK * BN * 4;
+  static constexpr int LIST_BYTES = SPLIT ? 64 : kListBytes;
   static constexpr int BAR_BYTES = 512;
-  static constexpr int REST = SCALE_BYTES + OUT_BYTES + kListBytes + BAR_BYTES + 1024;
-  static constexpr int FIT = (SMEM_LIMIT - REST) / STAGE_BYTES;
+  static constexpr int REST = SCALE_BYTES + OUT_BYTES + LIST_BYTES + BAR_BYTES + 1024;
+  static constexpr int FIT = (LIMIT - REST) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 10 ? 10 : FIT;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + REST;
   static constexpr int BOX = NT >= 128 ? 64 : 16;             // rows of A in one copy
   static constexpr int CH = NT / 2;                           // rows of A a drain thread holds
   static constexpr int CW = CH >= 32 ? 32 : 16;               // TMEM columns read at a time
   static_assert(TMEM_COLS == 512 || TMEM_COLS == 256, "TMEM allocations are powers of two");
-  static_assert(STAGES >= 4, "the ring holds a group of blocks");
-  static_assert(OPS * NT * BN * 4 <= STAGES * STAGE_BYTES, "a split's sums lie over the ring");
+  static_assert(STAGES >= 3, "the ring needs three stages");
+  static_assert(!SPLIT || OPS * NT * BN * 4 <= STAGES * STAGE_BYTES, "a split's sums lie over the ring");
   static_assert(8 * (2 * STAGES + 8) <= BAR_BYTES, "barrier area");
 };
 
@@ -90,7 +98,10 @@ struct Params {
 // Hardware barriers: 1 + g the drain warps and the signal warp at group buffer g, 3 the 256
 // drain threads.  Nobody can be left waiting: both sides go through the same groups and
 // items to the end, after an abort without results.
-__device__ __forceinline__ void sync_signal(int g) { asm volatile("bar.sync %0, 288;" ::"r"(1 + g) : "memory"); }
+__device__ __forceinline__ void sync_signal(int g) {
+  if (g == 0) asm volatile("bar.sync 1, 288;" ::: "memory");
+  else asm volatile("bar.sync 2, 288;" ::: "memory");
+}
 __device__ __forceinline__ void sync_drain() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
 template <int CW>
@@ -183,11 +194,11 @@ __device__ __forceinline__ void finish_row(const Params& p, const Item& i, int m
 }
 
 // GATHER: A's rows through tile::gather4 (mapA has boxes of one row).
-template <int NT, bool SW, bool GATHER>
-__global__ void __launch_bounds__(THREADS, 1)
+template <int NT, bool SW, bool GATHER, bool SPLIT>
+__global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
     blocks_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                   const __grid_constant__ CUtensorMap mapB2, const __grid_constant__ Params p) {
-  using C = Cfg<NT, SW>;
+  using C = Cfg<NT, SW, SPLIT>;
   constexpr int STAGES = C::STAGES, GROUP = C::GROUP, COLS = C::COLS, CH = C::CH, CW = C::CW;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -218,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const BlocksArgs& a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int split = p.split, rank = split > 1 ? (int)cluster_ctarank() : 0;
+  const int split = SPLIT ? p.split : 1, rank = SPLIT ? (int)cluster_ctarank() : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -243,16 +254,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_relinquish();
   }
   griddep_wait();
-  if (warp == 3) list_row_tiles<NT>(a, pre, beg, num, lane);
+  if (warp == 3) {
+    if (SPLIT) find_item<NT>(a, p.tiles_n, blockIdx.x / split, pre, lane);
+    else list_row_tiles<NT>(a, pre, beg, num, lane);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const long long items = (long long)pre[a.experts] * p.tiles_n;
-  const long long first = blockIdx.x / split, step = gridDim.x / split;
+  // SPLIT: pre[0..3] is this cluster's item, if it has one; else the lists of all
+  const long long items = SPLIT ? (pre[2] > 0 ? 1 : 0) : (long long)pre[a.experts] * p.tiles_n;
+  const long long first = SPLIT ? 0 : blockIdx.x, step = SPLIT ? 1 : gridDim.x;
   // blocks of K of this rank
   const int k_lo = (int)((long long)p.kblocks * rank / split), k_hi = (int)((long long)p.kblocks * (rank + 1) / split);
   Walk walk{pre, beg, num, NT, p.tiles_n, 0};
+  auto item_at = [&](long long it) { return SPLIT ? Item{pre[0], pre[1], pre[2], pre[3]} : walk.at(it); };
 
   if (warp == 0) {
     // -------------------------------------------------------------- copies
@@ -266,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       issued_par = (issued_par & ~(1u << s)) | (phase << s);
     };
     for (long long it = first; ok && it < items; it += step) {
-      const Item i = walk.at(it);
+      const Item i = item_at(it);
       const int n_mma = mma_rows(i.rows);
       const int copies = (n_mma + C::BOX - 1) / C::BOX;
       const uint32_t bytes = (uint32_t)(C::OPS * W_BYTES + (GATHER ? n_mma : copies * C::BOX) * BK);
@@ -335,7 +351,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         ok = false;
       }
       for (long long it = first; ok && it < items; it += step) {
-        const Item i = walk.at(it);
+        const Item i = item_at(it);
         const uint32_t idesc = idesc_f8_f32(BN, (uint32_t)mma_rows(i.rows), kE4M3, kE4M3, /*B^T MN-major*/ 1, /*A K-major*/ 0);
         for (int kb = k_lo; kb < k_hi; ++kb) {
           const int u = (kb - k_lo) % GROUP;
@@ -381,7 +397,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t gphase = 0;
     bool ok = true;
     for (long long it = first; ok && it < items; it += step) {
-      const Item i = walk.at(it);
+      const Item i = item_at(it);
       const float* row[PER];
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
@@ -459,7 +475,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t t_lane = tmem_base + ((uint32_t)(quarter * 32) << 16);
     int g = 0;
     for (long long it = first; it < items; it += step) {
-      const Item i = walk.at(it);
+      const Item i = item_at(it);
       const int n_mma = mma_rows(i.rows);
       uint64_t acc[C::OPS][CH / 2];
 #pragma unroll
@@ -476,18 +492,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int c = 0; c < CH / CW; ++c) {
             const int col = half * CH + c * CW;                  // rows of A: col .. col + CW - 1
             if (col < n_mma) {
-              uint32_t r[C::OPS][CW];
-#pragma unroll
-              for (int op = 0; op < C::OPS; ++op) tmem_read<CW>(t_lane + (uint32_t)(buf + op * NT + col), r[op]);
-              tc_wait_ld();
 #pragma unroll
               for (int op = 0; op < C::OPS; ++op) {
+                uint32_t r[CW];
+                tmem_read<CW>(t_lane + (uint32_t)(buf + op * NT + col), r);
+                tc_wait_ld();
                 const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scales + buf + op * NT + col);
 #pragma unroll
                 for (int j = 0; j < CW / 4; ++j) {
                   const ulonglong2 s = sc[j];
-                  fma2(acc[op][c * CW / 2 + 2 * j], pack2(r[op][4 * j], r[op][4 * j + 1]), s.x);
-                  fma2(acc[op][c * CW / 2 + 2 * j + 1], pack2(r[op][4 * j + 2], r[op][4 * j + 3]), s.y);
+                  fma2(acc[op][c * CW / 2 + 2 * j], pack2(r[4 * j], r[4 * j + 1]), s.x);
+                  fma2(acc[op][c * CW / 2 + 2 * j + 1], pack2(r[4 * j + 2], r[4 * j + 3]), s.y);
                 }
               }
             }
@@ -499,7 +514,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         g ^= 1;
       }
       auto value = [&](int op, int j) { return part2(acc[op][j / 2], j & 1); };
-      if (split > 1) {
+      if constexpr (SPLIT) {
         // this rank's sums, [row of A][column of B], over the ring (every copy has landed
         // and every MMA has read: the last accumulator is complete)
         float* part = reinterpret_cast<float*>(base_ptr);
@@ -534,10 +549,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 
   __syncwarp();
-  if (split > 1) {
+  if constexpr (SPLIT) {
     cluster_sync();                                              // every rank's sums are there
     if (first < items && !*abort_flag && warp >= EPI_FIRST) {
-      const Item i = walk.at(first);
+      const Item i = item_at(first);
       const uint32_t part = smem_u32(base_ptr);
 #pragma unroll 1
       for (int m = rank + split * (warp - EPI_FIRST); m < i.rows; m += split * EPI_WARPS) {
@@ -558,12 +573,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-template <int NT, bool SW, bool GATHER>
+template <int NT, bool SW, bool GATHER, bool SPLIT>
 int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap* mapB, const CUtensorMap* mapB2,
                 int split, int num_sms, cudaStream_t s) {
-  using C = Cfg<NT, SW>;
+  using C = Cfg<NT, SW, SPLIT>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = set_smem_once(done, blocks_kernel<NT, SW, GATHER>, C::SMEM_BYTES);
+  cudaError_t e = set_smem_once(done, blocks_kernel<NT, SW, GATHER, SPLIT>, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   Params p;
   p.a = a;
@@ -573,7 +588,7 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
   const int osz = a.out_bf16 ? 2 : 4;
   p.c_vec = reinterpret_cast<uintptr_t>(a.C) % (4 * osz) == 0 && a.ldc % 4 == 0 ? 1 : 0;
   const long long items = blocks_row_tiles(a.rows, a.offsets != nullptr ? a.experts : 1, NT) * p.tiles_n;
-  long long grid = split > 1 ? items * split : items < num_sms ? items : num_sms;
+  const long long grid = SPLIT ? items * split : items < num_sms ? items : num_sms;
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
@@ -588,8 +603,15 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, blocks_kernel<NT, SW, GATHER>, *mapA, *mapB, SW ? *mapB2 : *mapB, p);
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, blocks_kernel<NT, SW, GATHER, SPLIT>, *mapA, *mapB, SW ? *mapB2 : *mapB, p);
+}
+
+template <int NT, bool SW, bool GATHER>
+int launch_split(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap* mapB, const CUtensorMap* mapB2,
+                 int split, int num_sms, cudaStream_t s) {
+  return split > 1 ? launch_impl<NT, SW, GATHER, true>(a, mapA, mapB, mapB2, split, num_sms, s)
+                   : launch_impl<NT, SW, GATHER, false>(a, mapA, mapB, mapB2, split, num_sms, s);
 }
 
 }  // namespace
@@ -598,13 +620,13 @@ int launch_blocks(const BlocksArgs& a, const BlocksPlan& plan, const CUtensorMap
                   const CUtensorMap* mapB2, int num_sms, cudaStream_t s) {
   const int split = plan.split;
   if (a.B2 != nullptr)
-    return plan.nt == 32 && a.gather != 0 ? launch_impl<32, true, true>(a, mapA, mapB, mapB2, split, num_sms, s)
+    return plan.nt == 32 && a.gather != 0 ? launch_split<32, true, true>(a, mapA, mapB, mapB2, split, num_sms, s)
                                           : cudaErrorInvalidValue;
   if (a.gather != 0) return cudaErrorInvalidValue;
   switch (plan.nt) {
-    case 32: return launch_impl<32, false, false>(a, mapA, mapB, mapB2, split, num_sms, s);
-    case 64: return launch_impl<64, false, false>(a, mapA, mapB, mapB2, split, num_sms, s);
-    case 128: return launch_impl<128, false, false>(a, mapA, mapB, mapB2, split, num_sms, s);
+    case 32: return launch_split<32, false, false>(a, mapA, mapB, mapB2, split, num_sms, s);
+    case 64: return launch_split<64, false, false>(a, mapA, mapB, mapB2, split, num_sms, s);
+    case 128: return launch_split<128, false, false>(a, mapA, mapB, mapB2, split, num_sms, s);
   }
   return cudaErrorInvalidValue;
 }

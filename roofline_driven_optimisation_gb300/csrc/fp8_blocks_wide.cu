@@ -73,7 +73,10 @@ struct Params {
 // that polled mbarriers themselves kept the queue to shared memory so full that every
 // wait and arrival, the MMA warp's too, took 200 cycles and more.  Nobody can be left
 // waiting: both sides go through the same blocks to the end, after an abort without work.
-__device__ __forceinline__ void sync_signal(int b) { asm volatile("bar.sync %0, 288;" ::"r"(1 + b) : "memory"); }
+__device__ __forceinline__ void sync_signal(int b) {
+  if (b == 0) asm volatile("bar.sync 1, 288;" ::: "memory");
+  else asm volatile("bar.sync 2, 288;" ::: "memory");
+}
 // Barrier 3 of the 256 drain threads; and the same, returning whether any of them has `p`.
 __device__ __forceinline__ void sync_drain() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 __device__ __forceinline__ bool any_drain(bool p) {

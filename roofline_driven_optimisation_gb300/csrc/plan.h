@@ -246,9 +246,17 @@ inline BlocksChoice blocks_choice(long long rows, int experts, int N, int kblock
     return c;
   }
   while (!two_weights && c.nt < 128 && c.nt < mean) c.nt *= 2;
-  while (c.nt > 32 && met * ((mean + c.nt - 1) / c.nt) * tiles_n < num_sms && kblocks < 8) c.nt /= 2;
   const long long items = met * ((mean + c.nt - 1) / c.nt) * tiles_n;
-  while (c.split < 8 && items * c.split * 2 <= num_sms && kblocks >= 8 * c.split) c.split *= 2;
+  // parts of an SM's share: the fullest SM's, in items; two CTAs an SM with tiles of 32 rows
+  const long long slots = (c.nt == 32 ? 2 : 1) * num_sms;
+  double best = (double)((items + num_sms - 1) / num_sms);
+  for (int s = 2; s <= 8 && items * s <= slots && kblocks >= 4 * s; ++s) {
+    const double load = (double)((items * s + num_sms - 1) / num_sms) / s;
+    if (load < 0.95 * best) {
+      best = load;
+      c.split = s;
+    }
+  }
   return c;
 }
 
