@@ -788,11 +788,15 @@ def _blocks(n: int) -> int:
     return -(-n // 128)
 
 
-def _one_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
+def _one_device(*tensors) -> int:
+    """The index of the GPU that all tensors (or None) are on."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
             raise ValueError("the tensors of a call are on one device")
-    return first.device.index
+    if index < 0:
+        raise ValueError("the tensors of a call are on the GPU")
+    return index
 
 
 def route(logits, ids, weights, offsets=None, order=None, bias=None, score: int = ROUTE_SOFTMAX, groups: int = 1,
@@ -809,8 +813,7 @@ def route(logits, ids, weights, offsets=None, order=None, bias=None, score: int 
     tokens, experts = logits.shape
     top_k = ids.shape[-1]
     lib = _lib or load()
-    if not logits.is_cuda:
-        raise ValueError("route() takes CUDA tensors")
+    index = _one_device(logits, ids, weights, offsets, order, bias, workspace)
     if logits.dtype is _bf16:
         fn = lib.gemm_route_bf16
     elif logits.dtype is _f32:
@@ -818,9 +821,8 @@ def route(logits, ids, weights, offsets=None, order=None, bias=None, score: int 
     else:
         raise TypeError(f"unsupported logits dtype {logits.dtype}")
     for t, name, dtype in ((ids, "ids", _i32), (weights, "weights", _f32)):
-        if t.dtype is not dtype or not t.is_cuda or t.shape != (tokens, top_k) or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != (tokens, top_k) or not t.is_contiguous():
             raise TypeError(f"{name} is a contiguous {dtype} CUDA tensor {(tokens, top_k)}")
-    index = _one_device(logits, ids, weights, offsets, order, bias, workspace)
     st = _raw_stream(index) if stream is None else stream
     if workspace is None and order is not None:
         need = lib.gemm_route_workspace(tokens, experts)
@@ -877,8 +879,6 @@ def fp8_blocks(A, a_scale, B, b_scale, C, alpha: float = 1.0, beta: float = 0.0,
     else:
         raise TypeError(f"unsupported output dtype {C.dtype}")
     index = _one_device(C, A, a_scale, B, b_scale)
-    if index is None:
-        raise ValueError("fp8_blocks() takes CUDA tensors")
     rc = fn(M, N, K, alpha, A.data_ptr(), _codes(A, "A"), a_scale.data_ptr(), _scales(a_scale, "a_scale", M, _blocks(K)),
             B.data_ptr(), _codes(B, "B"), b_scale.data_ptr(), _scales(b_scale, "b_scale", _blocks(K), _blocks(N)), beta,
             C.data_ptr(), _ld(C), _raw_stream(index) if stream is None else stream)

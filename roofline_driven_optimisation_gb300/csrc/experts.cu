@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a, int c
     if (a.vec && c + 8 <= a.cols) {
 #pragma unroll 8
       for (int j = 0; j < a.top_k; ++j) {
-        const uint4 v = __ldcg(reinterpret_cast<const uint4*>(y + j * a.ldy));
+        const uint4 v = *reinterpret_cast<const uint4*>(y + j * a.ldy);
         const float f = w[j];
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -69,7 +69,8 @@ struct Cfg {
   static constexpr int LIMIT = CTAS == 2 ? 115200 : SMEM_LIMIT;
   static constexpr int OPS = SW ? 2 : 1;
   static constexpr int COLS = NT * OPS;                       // TMEM columns of an accumulator
-  static constexpr int GROUP = 256 / COLS > 4 ? 4 : 256 / COLS;      // blocks that are handed over together
+  // blocks that are handed over together; the CTAs of an SM share its 512 TMEM columns
+  static constexpr int GROUP = 256 / CTAS / COLS > 4 ? 4 : 256 / CTAS / COLS;
   static constexpr int TMEM_COLS = 2 * GROUP * COLS;
   static constexpr int STAGE_BYTES = OPS * W_BYTES + NT * BK;
   static constexpr int SCALE_BYTES = 2 * GROUP * COLS * 4;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
-  griddep_wait();
+  if (!a.early) griddep_wait();
   if (warp == 3) {
     if (SPLIT) find_item<NT>(a, p.tiles_n, blockIdx.x / split, pre, lane);
     else list_row_tiles<NT>(a, pre, beg, num, lane);
@@ -261,6 +262,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // the next kernel may take an SM as soon as this one leaves it
+  griddep_launch_dependents();
   const uint32_t tmem_base = *tmem_slot;
   // SPLIT: pre[0..3] is this cluster's item, if it has one; else the lists of all
   const long long items = SPLIT ? (pre[2] > 0 ? 1 : 0) : (long long)pre[a.experts] * p.tiles_n;
@@ -291,8 +294,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
         tma_load_3d(w_tile(s), &mapB, full_bar(s), i.nb * BN, kb * BK, i.e);
         if (SW) tma_load_3d(w_tile(s) + W_BYTES, &mapB2, full_bar(s), i.nb * BN, kb * BK, i.e);
       };
-      // the ring is empty at first: its weights are on their way while `order` is read
-      const int ahead = GATHER && it == first ? min(STAGES, k_hi - k_lo) : 0;
+      // the ring is empty at first: its weights are on their way while `order` is read, and
+      // while the kernel before writes A
+      const int ahead = it == first ? min(STAGES, k_hi - k_lo) : 0;
       if (leader)
         for (int s = 0; s < ahead; ++s) weights(s, k_lo + s);
       __syncwarp();
@@ -306,6 +310,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
           y[q] = from >= 0 ? from : a.a_rows;         // outside: zeros
         }
       }
+      if (it == first && a.early) griddep_wait();
       for (int kb = k_lo; kb < k_hi; ++kb) {
         const bool sent = kb - k_lo < ahead;           // its weights are under way
         if (!sent) {
@@ -407,16 +412,18 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
       }
       const float* sb = a.sb + i.e * a.sb_stride + i.nb;
       const float* sb2 = SW ? a.sb2 + i.e * a.sb_stride + i.nb : nullptr;
-      // a group ahead: the loads land while the one before is drained
+      if (it == first && a.early) griddep_wait();
+      // a group ahead: the loads land while the one before is drained (plain loads: read-only
+      // ones may be moved before the wait)
       float v[GROUP][PER], w[GROUP], w2[GROUP];
       auto load = [&](int kb) {
 #pragma unroll
         for (int u = 0; u < GROUP; ++u) {
           const bool in = kb + u < k_hi;
 #pragma unroll
-          for (int q = 0; q < PER; ++q) v[u][q] = in && row[q] != nullptr ? __ldg(row[q] + kb + u) : 0.f;
-          w[u] = in ? __ldg(sb + (kb + u) * a.ldsb) : 0.f;
-          if (SW) w2[u] = in ? __ldg(sb2 + (kb + u) * a.ldsb) : 0.f;
+          for (int q = 0; q < PER; ++q) v[u][q] = in && row[q] != nullptr ? row[q][kb + u] : 0.f;
+          w[u] = in ? sb[(kb + u) * a.ldsb] : 0.f;
+          if (SW) w2[u] = in ? sb2[(kb + u) * a.ldsb] : 0.f;
         }
       };
       load(k_lo);
@@ -564,7 +571,6 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
     }
     cluster_sync();                                              // no rank leaves while others read its sums
   }
-  griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -244,11 +244,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish();
   }
-  griddep_wait();
+  if (!a.early) griddep_wait();
   if (warp == 3) list_row_tiles<BM>(a, pre, beg, num, lane);
   tc_fence_before();
   __syncthreads();                                     // barriers, lists and TMEM
   tc_fence_after();
+  // the next kernel may take an SM as soon as this one leaves it
+  griddep_launch_dependents();
   const uint32_t tmem_base = *tmem_slot;
   const long long items = (long long)pre[a.experts] * p.tiles_n;
   const long long first = blockIdx.x, step = gridDim.x;
@@ -268,17 +270,26 @@ __global__ void __launch_bounds__(THREADS, 1)
         // rows that are not there are not copied: what their lanes sum up is not read
         const int copies = (i.rows + BOX - 1) / BOX;
         const uint32_t bytes = (uint32_t)(2 * B_BYTES + copies * BOX * BK);
-        for (int kb = 0; ok && kb < p.kblocks; ++kb) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, a.timeout_ns, abort_flag)) {
-            if (!*abort_flag) report_status(a.status, 5, kSiteWideProducer);
-            *abort_flag = 1;
-            ok = false;
-            break;
+        auto weights = [&](int s, int kb) {
+          mbar_arrive_expect_tx(full_bar(s), bytes);
+          tma_load_3d(b_tile(s), &mapB, full_bar(s), i.nb * BN, kb * BK, i.e);
+          tma_load_3d(b_tile(s) + B_BYTES, SW ? &mapB2 : &mapB, full_bar(s), i.nb * BN + (SW ? 0 : 128), kb * BK, i.e);
+        };
+        // the ring is empty at first: its weights are on their way while the kernel before
+        // writes A
+        const int ahead = it == first ? min(STAGES, p.kblocks) : 0;
+        for (int s = 0; s < ahead; ++s) weights(s, s);
+        if (it == first && a.early) griddep_wait();
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (kb >= ahead) {
+            if (!mbar_wait(empty_bar(stage), phase ^ 1u, a.timeout_ns, abort_flag)) {
+              if (!*abort_flag) report_status(a.status, 5, kSiteWideProducer);
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
+            weights(stage, kb);
           }
-          mbar_arrive_expect_tx(full_bar(stage), bytes);
-          tma_load_3d(b_tile(stage), &mapB, full_bar(stage), i.nb * BN, kb * BK, i.e);
-          tma_load_3d(b_tile(stage) + B_BYTES, SW ? &mapB2 : &mapB, full_bar(stage), i.nb * BN + (SW ? 0 : 128), kb * BK,
-                      i.e);
           for (int c = 0; c < copies; ++c)
             tma_load_2d(a_tile(stage) + c * BOX * BK, &mapA, full_bar(stage), kb * BK, i.p0 + c * BOX);
           issued |= 1u << stage;
@@ -354,6 +365,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (m < i.rows) expert_row(a, i.p0 + m, from, to);
           row[q] = from >= 0 ? a.sa + (long long)from * a.ldsa : nullptr;
         }
+        if (it == first && a.early) griddep_wait();
         // B's scales of the item's column blocks: lane 0 the first, lane 1 the second
         const int col = SW ? i.nb : 2 * i.nb + lane;
         const float* sb = nullptr;
@@ -538,7 +550,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 
   __syncwarp();
-  griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

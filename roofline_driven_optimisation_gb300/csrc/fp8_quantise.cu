@@ -27,14 +27,15 @@ constexpr int THREADS = 256;
 constexpr int HALVES = THREADS / HALF;
 
 // 8 values from x[0..7], of which `n` exist (0 in the place of the others), as they came:
-// bf16 values take half the registers that way
+// bf16 values take half the registers that way.  (Plain loads here and below: the compiler
+// may move read-only ones before griddep_wait.)
 template <typename T>
 struct Eight {
   uint4 w[sizeof(T) / 2];
   __device__ __forceinline__ void load(const T* x, int n, bool vec) {
     if (vec && n >= 8) {
 #pragma unroll
-      for (int q = 0; q < (int)sizeof(T) / 2; ++q) w[q] = __ldg(reinterpret_cast<const uint4*>(x) + q);
+      for (int q = 0; q < (int)sizeof(T) / 2; ++q) w[q] = reinterpret_cast<const uint4*>(x)[q];
     } else {
       alignas(16) T part[8];
 #pragma unroll
@@ -80,6 +81,7 @@ template <typename T, bool PLACED>
 __global__ void __launch_bounds__(THREADS, 5) quantise_rows_kernel(const __grid_constant__ QuantiseArgs a, int groups) {
   constexpr int U = units_u<T>();
   griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x % 32;
   const long long unit = (long long)blockIdx.x * (THREADS / 32) + threadIdx.x / 32;
   const long long row = a.units32 ? (unsigned)unit / (unsigned)groups : unit / groups;
@@ -125,6 +127,7 @@ __global__ void __launch_bounds__(THREADS, 5) quantise_rows_kernel(const __grid_
 // place[order[p]] = p, for the numbers that fit
 __global__ void __launch_bounds__(THREADS) invert_kernel(const int* order, int n, int* place, int* status) {
   griddep_wait();
+  griddep_launch_dependents();
   const int p = (int)(blockIdx.x * (long long)THREADS + threadIdx.x);
   if (p >= n) return;
   const int slot = order[p];

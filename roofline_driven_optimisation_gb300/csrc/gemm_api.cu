@@ -931,7 +931,7 @@ int route(int tokens, int experts, int top_k, const void* logits, bool bf16, lon
   a.group_lanes = a.group_whole ? whole : lanes;
   a.scale = scale; a.bias = bias;
   a.ids = ids; a.weights = weights; a.offsets = offsets; a.order = order;
-  a.counts = static_cast<int*>(workspace);
+  a.counts = need > 0 ? static_cast<int*>(workspace) : nullptr;   // few tokens: none
   a.choices = bias != nullptr || groups > 1;
   a.vec = aligned16(logits) && ((size_t)ld * (bf16 ? 2 : 4)) % 16 == 0;
   const int err = launch_route(a, stream);
@@ -1152,6 +1152,7 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
   // are few); larger ones find the rows laid out by expert: a gathered row costs the copy
   // engine's issue about 20 cycles, and 256 rows a block of 128 k would be all it does.
   const bool gather = fast && plan_up.nt == 32;
+  a.early = d.early = fast ? 1 : 0;
   a.gather = gather || !fast ? top_k : 0;
   a.a_rows = a.gather != 0 ? tokens : slots;
 

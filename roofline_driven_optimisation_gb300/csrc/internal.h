@@ -353,6 +353,9 @@ struct BlocksArgs {
   int* status;
   uint64_t timeout_ns;
   int stall;                    // as GemmArgs::stall
+  // The kernel before on the stream wrote A and sa alone: B, its scales, offsets and order
+  // may be read before it has finished.
+  int early;
 };
 constexpr int kBlocksK = 128, kBlocksN = 128, kBlocksMaxExperts = 1024;
 // The tcgen05 kernel: row tiles of nt, K split over clusters of `split` CTAs.  Maps: A

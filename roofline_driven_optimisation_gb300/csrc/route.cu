@@ -420,7 +420,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, long long t, con
     if constexpr (BYTES % 16 == 0) {
 #pragma unroll
       for (int q = 0; q < BYTES / 16; ++q) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(logits + e0) + q);
+        const uint4 v = reinterpret_cast<const uint4*>(logits + e0)[q];
         alignas(16) T part[16 / sizeof(T)];
         *reinterpret_cast<uint4*>(part) = v;
 #pragma unroll
@@ -639,6 +639,7 @@ __global__ void __launch_bounds__(route_threads<PER>()) route_kernel(const __gri
   if (!plan) return;
   if (gridDim.x > 1) {
     griddep_launch_dependents();
+    if (a.counts == nullptr) return;                     // route_order_kernel counts ids
     for (int e = threadIdx.x; e < E; e += blockDim.x) a.counts[(size_t)blockIdx.x * count_stride(E) + e] = hist[e];
     return;
   }
@@ -710,6 +711,25 @@ __global__ void __launch_bounds__(kPlaceKernelThreads) route_place_kernel(const 
   place_slots(a, t0 * a.top_k, t1 * a.top_k, before, at);
 }
 
+// All slots of a call by one block, from their ids alone.
+__global__ void __launch_bounds__(kPlaceKernelThreads) route_order_kernel(const __grid_constant__ RouteArgs a) {
+  extern __shared__ int place_smem[];
+  const int E = a.experts, lane = threadIdx.x % 32, slots = a.tokens * a.top_k;
+  int *total = place_smem, *at = total + E;
+  for (int x = threadIdx.x; x < (1 + kPlaceWarps) * E; x += blockDim.x) place_smem[x] = 0;
+  griddep_wait();
+  __syncthreads();
+  for (int s = threadIdx.x; s < slots; s += blockDim.x) atomicAdd(total + a.ids[s], 1);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int all = warp_scan(total, total, E, lane);
+    for (int e = lane; e < E; e += 32) a.offsets[e] = total[e];
+    if (lane == 0) a.offsets[E] = all;
+  }
+  __syncthreads();
+  place_slots(a, 0, slots, total, at);
+}
+
 // Warps a block, blocks and tokens a block.  A token is some 700 instructions of a warp, so
 // that 32 warps of one SM take 3 us for a token each: one block alone (which saves the
 // second launch, 2 us) for a token a warp of 16 at most, then blocks of 8 warps on as many
@@ -718,9 +738,11 @@ __global__ void __launch_bounds__(kPlaceKernelThreads) route_place_kernel(const 
 constexpr int kRouteMaxBlocks = 152;
 struct RoutePlan {
   int warps, blocks, chunk;
+  bool few;              // slots that one block orders as soon as many would
 };
 RoutePlan plan_route(int tokens, int experts) {
   RoutePlan p;
+  p.few = tokens <= 256;
   p.warps = tokens <= 8 ? 8 : tokens <= 16 && experts <= 256 ? 16 : tokens <= 8 * kRouteMaxBlocks || experts > 256 ? 8 : 32;
   if (tokens <= p.warps) {
     p.blocks = 1;
@@ -756,6 +778,12 @@ int launch_impl(const RouteArgs& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, route_kernel<T, PER>, a, p.chunk);
   if (e != cudaSuccess || p.blocks == 1 || a.offsets == nullptr) return e;
+  if (a.counts == nullptr) {
+    cfg.gridDim = dim3(1, 1, 1);
+    cfg.blockDim = dim3(kPlaceKernelThreads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)a.experts * (1 + kPlaceWarps) * sizeof(int);
+    return cudaLaunchKernelEx(&cfg, route_order_kernel, a);
+  }
   cfg.blockDim = dim3(kPlaceKernelThreads, 1, 1);
   cfg.dynamicSmemBytes = (size_t)a.experts * (2 + kPlaceWarps) * sizeof(int);
   return cudaLaunchKernelEx(&cfg, route_place_kernel, a, p.chunk);
@@ -777,7 +805,7 @@ int launch_type(const RouteArgs& a, cudaStream_t s) {
 
 size_t route_ws_bytes(int tokens, int experts) {
   const RoutePlan p = plan_route(tokens, experts);
-  return p.blocks > 1 ? (size_t)p.blocks * count_stride(experts) * sizeof(int) : 0;
+  return p.blocks > 1 && !p.few ? (size_t)p.blocks * count_stride(experts) * sizeof(int) : 0;
 }
 
 int launch_route(const RouteArgs& a, cudaStream_t s) {
