@@ -596,16 +596,17 @@ class KVCache:
 
 def _torch():
     """torch, and the types that the calls below compare with (looked up once)."""
-    global _t, _bf16, _f32, _i32, _raw_stream
+    global _t, _bf16, _f32, _i32, _e4m3, _u8, _raw_stream
     import torch
     _t, _bf16, _f32, _i32 = torch, torch.bfloat16, torch.float32, torch.int32
+    _e4m3, _u8 = torch.float8_e4m3fn, torch.uint8
     # the current stream's handle without a Stream object around it
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda index: torch.cuda.current_stream(index).cuda_stream)
     return torch
 
 
-_t = _bf16 = _f32 = _i32 = _raw_stream = None
+_t = _bf16 = _f32 = _i32 = _e4m3 = _u8 = _raw_stream = None
 
 
 def _heads(t, name: str, heads: int, dim: int, tokens: int) -> int:
@@ -771,17 +772,30 @@ def _scratch(nbytes: int, device, stream: int):
         return _t.empty((nbytes,), dtype=_t.uint8, device=device)
 
 
-def _codes(t, name: str):
-    """A 2-D CUDA tensor of E4M3 codes (float8_e4m3fn or uint8), rows apart from each other."""
-    if t.dtype is not _t.float8_e4m3fn and t.dtype is not _t.uint8 or not t.is_cuda:
-        raise TypeError(f"{name} is a CUDA tensor of E4M3 codes (float8_e4m3fn or uint8)")
-    return _ld(t)
+def _rows(t, name: str, rows: int, cols: int) -> int:
+    """Elements between the rows of a tensor [rows][cols] with contiguous columns."""
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {(rows, cols)}")
+    step, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name}: columns lie {one} apart")
+    if step < cols:
+        if rows > 1:
+            raise ValueError(f"{name}: rows of {cols} values lie {step} apart (an expanded tensor?)")
+        return cols                                   # of a single row it says nothing
+    return step
+
+
+def _codes(t, name: str, rows: int, cols: int) -> int:
+    if t.dtype is not _e4m3 and t.dtype is not _u8:
+        raise TypeError(f"{name} is a tensor of E4M3 codes (float8_e4m3fn or uint8)")
+    return _rows(t, name, rows, cols)
 
 
 def _scales(t, name: str, rows: int, cols: int) -> int:
-    if t.dtype is not _f32 or not t.is_cuda or t.shape != (rows, cols):
-        raise TypeError(f"{name} is a fp32 CUDA tensor {(rows, cols)}")
-    return _ld(t)
+    if t.dtype is not _f32:
+        raise TypeError(f"{name} is a fp32 tensor")
+    return _rows(t, name, rows, cols)
 
 
 def _blocks(n: int) -> int:
@@ -820,19 +834,25 @@ def route(logits, ids, weights, offsets=None, order=None, bias=None, score: int 
         fn = lib.gemm_route_f32
     else:
         raise TypeError(f"unsupported logits dtype {logits.dtype}")
-    for t, name, dtype in ((ids, "ids", _i32), (weights, "weights", _f32)):
-        if t.dtype is not dtype or t.shape != (tokens, top_k) or not t.is_contiguous():
-            raise TypeError(f"{name} is a contiguous {dtype} CUDA tensor {(tokens, top_k)}")
+    shape = (tokens, top_k)
+    if ids.dtype is not _i32 or ids.shape != shape or not ids.is_contiguous():
+        raise TypeError(f"ids is a contiguous int32 tensor {shape}")
+    if weights.dtype is not _f32 or weights.shape != shape or not weights.is_contiguous():
+        raise TypeError(f"weights is a contiguous fp32 tensor {shape}")
     st = _raw_stream(index) if stream is None else stream
-    if workspace is None and order is not None:
-        need = lib.gemm_route_workspace(tokens, experts)
-        workspace = _scratch(need, logits.device, st) if need else None
-    rc = fn(tokens, experts, top_k, logits.data_ptr(), _ld(logits),
+    space = size = 0
+    if workspace is not None:
+        space, size = workspace.data_ptr(), workspace.numel()
+    elif order is not None:
+        size = lib.gemm_route_workspace(tokens, experts)
+        if size:
+            workspace = _scratch(size, logits.device, st)
+            space = workspace.data_ptr()
+    rc = fn(tokens, experts, top_k, logits.data_ptr(), _rows(logits, "logits", tokens, experts),
             None if bias is None else _values(bias, "bias", experts, _f32), score, groups, top_groups, group_best,
             renormalise, scale, ids.data_ptr(), weights.data_ptr(),
             None if offsets is None else _values(offsets, "offsets", experts + 1, _i32),
-            None if order is None else _values(order, "order", tokens * top_k, _i32),
-            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), st)
+            None if order is None else _values(order, "order", tokens * top_k, _i32), space, size, st)
     if rc:
         _check(rc)
     return ids, weights
@@ -845,17 +865,19 @@ def fp8_quantise(X, codes, scales, block_rows: int = 1, stream=None):
     if _t is None:
         _torch()
     rows, cols = X.shape
-    if X.dtype is not _bf16 and X.dtype is not _f32 or not X.is_cuda:
-        raise TypeError("X is a bf16 or fp32 CUDA tensor")
-    if codes.shape != X.shape:
-        raise ValueError(f"codes have shape {tuple(codes.shape)}, not {(rows, cols)}")
-    if block_rows not in (1, 128):
-        raise ValueError(f"blocks of {block_rows} x 128: 1 and 128 rows are there")
     lib = _lib or load()
-    fn = lib.gemm_fp8_quantise_bf16 if X.dtype is _bf16 else lib.gemm_fp8_quantise_f32
-    rc = fn(rows, cols, X.data_ptr(), _ld(X), codes.data_ptr(), _codes(codes, "codes"), scales.data_ptr(),
-            _scales(scales, "scales", -(-rows // block_rows), _blocks(cols)), block_rows,
-            _raw_stream(_one_device(X, codes, scales)) if stream is None else stream)
+    if X.dtype is _bf16:
+        fn = lib.gemm_fp8_quantise_bf16
+    elif X.dtype is _f32:
+        fn = lib.gemm_fp8_quantise_f32
+    else:
+        raise TypeError("X is a bf16 or fp32 tensor")
+    if block_rows != 1 and block_rows != 128:
+        raise ValueError(f"blocks of {block_rows} x 128: 1 and 128 rows are there")
+    index = _one_device(X, codes, scales)
+    rc = fn(rows, cols, X.data_ptr(), _rows(X, "X", rows, cols), codes.data_ptr(), _codes(codes, "codes", rows, cols),
+            scales.data_ptr(), _scales(scales, "scales", -(-rows // block_rows), -(-cols // 128)), block_rows,
+            _raw_stream(index) if stream is None else stream)
     if rc:
         _check(rc)
     return codes, scales
@@ -879,9 +901,11 @@ def fp8_blocks(A, a_scale, B, b_scale, C, alpha: float = 1.0, beta: float = 0.0,
     else:
         raise TypeError(f"unsupported output dtype {C.dtype}")
     index = _one_device(C, A, a_scale, B, b_scale)
-    rc = fn(M, N, K, alpha, A.data_ptr(), _codes(A, "A"), a_scale.data_ptr(), _scales(a_scale, "a_scale", M, _blocks(K)),
-            B.data_ptr(), _codes(B, "B"), b_scale.data_ptr(), _scales(b_scale, "b_scale", _blocks(K), _blocks(N)), beta,
-            C.data_ptr(), _ld(C), _raw_stream(index) if stream is None else stream)
+    kb = -(-K // 128)
+    rc = fn(M, N, K, alpha, A.data_ptr(), max(_codes(A, "A", M, K), 1), a_scale.data_ptr(),
+            _scales(a_scale, "a_scale", M, kb), B.data_ptr(), max(_codes(B, "B", K, N), 1), b_scale.data_ptr(),
+            _scales(b_scale, "b_scale", kb, -(-N // 128)), beta, C.data_ptr(), max(_rows(C, "C", M, N), 1),
+            _raw_stream(index) if stream is None else stream)
     if rc:
         _check(rc)
     return C
@@ -929,26 +953,27 @@ def experts(weights: ExpertWeights, X, offsets, order, token_weights, O, workspa
     marshalling only."""
     if _t is None:
         _torch()
-    tokens, hidden = X.shape
-    for t, name in ((X, "X"), (O, "O")):
-        if t.dtype is not _bf16 or not t.is_cuda:
-            raise TypeError(f"{name} is a bf16 CUDA tensor")
-        if t.shape != (tokens, weights.hidden):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {(tokens, weights.hidden)}")
-    if token_weights.dim() != 2 or token_weights.shape[0] != tokens or token_weights.dtype is not _f32 or \
-            not token_weights.is_cuda or not token_weights.is_contiguous():
-        raise TypeError("token_weights is a contiguous fp32 CUDA tensor [tokens][top_k]")
-    top_k = token_weights.shape[1]
+    tokens, top_k = token_weights.shape
+    hidden = weights.hidden
+    if X.dtype is not _bf16 or O.dtype is not _bf16:
+        raise TypeError("X and O are bf16 tensors")
+    if token_weights.dtype is not _f32 or not token_weights.is_contiguous():
+        raise TypeError("token_weights is a contiguous fp32 tensor [tokens][top_k]")
     if _one_device(X, O, offsets, order, token_weights, workspace) != weights.index:
         raise ValueError("the tensors of a call are on one device")
     st = _raw_stream(weights.index) if stream is None else stream
     lib = _lib or load()
-    if workspace is None and tokens:
-        workspace = _scratch(lib.gemm_experts_workspace(tokens, top_k, hidden, weights.width), X.device, st)
+    space = size = 0
+    if workspace is not None:
+        space, size = workspace.data_ptr(), workspace.numel()
+    elif tokens:
+        size = lib.gemm_experts_workspace(tokens, top_k, hidden, weights.width)
+        workspace = _scratch(size, weights.device, st)
+        space = workspace.data_ptr()
     rc = lib.gemm_experts(
-        weights.address, tokens, top_k, X.data_ptr(), _ld(X), _values(offsets, "offsets", weights.experts + 1, _i32),
-        _values(order, "order", tokens * top_k, _i32), token_weights.data_ptr(), O.data_ptr(), _ld(O),
-        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), st)
+        weights.address, tokens, top_k, X.data_ptr(), _rows(X, "X", tokens, hidden),
+        _values(offsets, "offsets", weights.experts + 1, _i32), _values(order, "order", tokens * top_k, _i32),
+        token_weights.data_ptr(), O.data_ptr(), _rows(O, "O", tokens, hidden), space, size, st)
     if rc:
         _check(rc)
     return O

@@ -50,9 +50,9 @@ struct Item {
 struct Walk {
   const int *pre, *beg, *num;
   int nt, tiles_n, e;
-  __device__ __forceinline__ Item at(long long it) {
-    while (it >= (long long)pre[e + 1] * tiles_n) ++e;
-    const int x = (int)(it - (long long)pre[e] * tiles_n), tiles = pre[e + 1] - pre[e];
+  __device__ __forceinline__ Item at(int it) {
+    while (it >= pre[e + 1] * tiles_n) ++e;
+    const int x = it - pre[e] * tiles_n, tiles = pre[e + 1] - pre[e];
     const int t = x % tiles;
     Item i;
     i.e = e;

@@ -266,12 +266,12 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
   griddep_launch_dependents();
   const uint32_t tmem_base = *tmem_slot;
   // SPLIT: pre[0..3] is this cluster's item, if it has one; else the lists of all
-  const long long items = SPLIT ? (pre[2] > 0 ? 1 : 0) : (long long)pre[a.experts] * p.tiles_n;
-  const long long first = SPLIT ? 0 : blockIdx.x, step = SPLIT ? 1 : gridDim.x;
+  const int items = SPLIT ? (pre[2] > 0 ? 1 : 0) : pre[a.experts] * p.tiles_n;   // in 32 bits: the host has seen to it
+  const int first = SPLIT ? 0 : blockIdx.x, step = SPLIT ? 1 : gridDim.x;
   // blocks of K of this rank
   const int k_lo = (int)((long long)p.kblocks * rank / split), k_hi = (int)((long long)p.kblocks * (rank + 1) / split);
   Walk walk{pre, beg, num, NT, p.tiles_n, 0};
-  auto item_at = [&](long long it) { return SPLIT ? Item{pre[0], pre[1], pre[2], pre[3]} : walk.at(it); };
+  auto item_at = [&](int it) { return SPLIT ? Item{pre[0], pre[1], pre[2], pre[3]} : walk.at(it); };
 
   if (warp == 0) {
     // -------------------------------------------------------------- copies
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
       issued |= 1u << s;
       issued_par = (issued_par & ~(1u << s)) | (phase << s);
     };
-    for (long long it = first; ok && it < items; it += step) {
+    for (int it = first; ok && it < items; it += step) {
       const Item i = item_at(it);
       const int n_mma = mma_rows(i.rows);
       const int copies = (n_mma + C::BOX - 1) / C::BOX;
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
         *abort_flag = 1;
         ok = false;
       }
-      for (long long it = first; ok && it < items; it += step) {
+      for (int it = first; ok && it < items; it += step) {
         const Item i = item_at(it);
         const uint32_t idesc = idesc_f8_f32(BN, (uint32_t)mma_rows(i.rows), kE4M3, kE4M3, /*B^T MN-major*/ 1, /*A K-major*/ 0);
         for (int kb = k_lo; kb < k_hi; ++kb) {
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
     int g = 0;
     uint32_t gphase = 0;
     bool ok = true;
-    for (long long it = first; ok && it < items; it += step) {
+    for (int it = first; ok && it < items; it += step) {
       const Item i = item_at(it);
       const float* row[PER];
 #pragma unroll
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
     int g = 0;
     uint32_t gphase = 0;
     bool ok = true;
-    for (long long it = first; it < items; it += step)
+    for (int it = first; it < items; it += step)
       for (int kb = k_lo; kb < k_hi; kb += GROUP) {
         if (lane == 0 && ok) {
           ok = mbar_wait(sfull_bar(g), gphase, a.timeout_ns, abort_flag) &&
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
     const int nl = quarter * 32 + lane;                          // column of the tile
     const uint32_t t_lane = tmem_base + ((uint32_t)(quarter * 32) << 16);
     int g = 0;
-    for (long long it = first; it < items; it += step) {
+    for (int it = first; it < items; it += step) {
       const Item i = item_at(it);
       const int n_mma = mma_rows(i.rows);
       uint64_t acc[C::OPS][CH / 2];

@@ -1,24 +1,30 @@
-// Block-scaled products (the formulas are those of fp8_blocks.cu) for calls with many rows:
-// an item is 128 rows of A and 256 columns of B, or, with gate and up weights, 128 rows
-// and 128 columns of each.
+// Block-scaled products (the formulas are those of fp8_blocks.cu) for calls with many rows,
+// on CTA pairs: an item is 256 rows of A and 256 columns of B, or, with gate and up
+// weights, 256 rows and 128 columns of each.
 //
 // Why another kernel.  With many rows the products are compute-bound, and what the
 // swapped kernel does a block of 128 k is then too much: a scale of shared memory for each
 // column of the accumulator.  Here rows of A are TMEM lanes, so that a drain thread has
-// one row, and one scale (two with gate and up) a block.
+// one row and two scales a block.  And a single CTA's 128 x 256 item moves 48 KB a block
+// into shared memory and out of it again against 512 tensor cycles: measured 768 cycles
+// a block (128 bytes a cycle) without any drain, 1100 with it (8192 x 11008 x 4096: 366
+// us).  In a pair (cta_group::2, one M = 256 MMA) each CTA holds its 128 rows of A and half
+// of B's columns: 32 KB.
 //
-// What bounds it.  The tensor core's sum of a block of 128 k has to leave TMEM before
-// its buffer takes the next block but one, so MMA, its completion, the drain and the
-// buffer's return make a chain, and two buffers of 256 columns fill TMEM.  The MMAs take
-// 512 cycles at the nominal rate; the drain's 128 x 256 sums 256 cycles of fma.rn.f32x2
-// (64 a warp, two warps a scheduler, two cycles each).  On CTA pairs (cta_group::2, half
-// the copies) the peer's barriers are some 300 cycles away in each direction, and the
-// chain took 1050 to 1130 cycles a block (8192 x 11008 x 4096: 353 us); on single CTAs the
-// chain stays on the SM.
+// What bounds it.  The tensor core's sum of a block of 128 k has to leave TMEM before its
+// buffer takes the next block but one, so MMA, its completion, the drain and the buffer's
+// return make a chain, and a pair's far barriers are some 300 cycles away.  With one
+// 256-wide accumulator a block and two buffers the chain was 950 to 1050 cycles a block;
+// so a block is two MMAs of 128 columns (64 of each CTA's half of B), each with its own
+// buffers, barriers and four drain warps, and the two chains run beside each other.  The
+// drain's 128 x 256 sums a CTA take 256 cycles of fma.rn.f32x2 (64 a warp, two warps a
+// scheduler, two cycles each).
 //
-// Roles (384 threads): warp 0 copies, warp 1 issues the MMAs, warp 2 copies the scales of
-// the rows into a ring of eight blocks (cp.async, no registers), warps 4-11 drain: warp w
-// the TMEM lanes 32*(w%4)..+31 and half of the columns, its 128 sums in registers for the
+// Roles (384 threads a CTA): warp 0 copies (each CTA its rows of A and its half of B; all
+// complete on the leader's barrier), warp 1 of the leader issues the MMAs, warp 2 copies
+// the scales of its CTA's rows into a ring of eight blocks (cp.async, no registers), warp 3
+// waits for accumulators and scales on behalf of the drain warps, warps 4-11 drain: warp w
+// the TMEM lanes 32*(w%4)..+31 of one of the two MMAs, its 128 sums in registers for the
 // whole of K.
 //
 // h of gate and up: a thread has 64 columns of its row in both, so the largest magnitude
@@ -30,6 +36,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <mutex>
 
 #include "epilogue.cuh"
 #include "experts.cuh"
@@ -40,25 +47,30 @@
 namespace g3 {
 namespace {
 
-constexpr int BK = kBlocksK, BM = 128;
+constexpr int BK = kBlocksK, BM = kBlocksWide, BM_CTA = BM / 2;
 constexpr int THREADS = 384, EPI_WARPS = 8, EPI_FIRST = 4;
-constexpr int A_BYTES = BM * BK, B_BYTES = BK * 128;    // B: two boxes of 128 columns
-constexpr int STAGE_BYTES = A_BYTES + 2 * B_BYTES, STAGES = 4;
+constexpr int A_BYTES = BM_CTA * BK, B_BYTES = BK * 128;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int TMEM_COLS = 512, COLS = 256, NBUF = 2;
 // The ring of scales: a slot holds four blocks of k, four floats for each row and for B's
 // one or two column blocks, so that a drain thread waits and reads once in four blocks.
-constexpr int RING = 2, RING_BLOCKS = 4, RING_WORDS = RING_BLOCKS * (BM + 2);
+constexpr int RING = 2, RING_BLOCKS = 4, RING_WORDS = RING_BLOCKS * (BM_CTA + 2);
 constexpr int BOX = 64;
 constexpr int BAR_BYTES = 512;
-// Shared memory: the ring of operands, for each drain warp 32 rows of 64 bytes that it is
-// about to store, the scales, and the lists of rows.
-constexpr int OUT_WARP = 32 * 64;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * OUT_WARP + RING * RING_WORDS * 4 + 2 * BM * 4 + kListBytes +
-                           BAR_BYTES + 1024;
-static_assert(NBUF == 2, "buffers are told apart by one bit");
-static_assert(SMEM_BYTES <= 232448, "shared memory");
-static_assert(8 * (2 * STAGES + 2 * NBUF + 2 * RING + 4) <= BAR_BYTES, "barrier area");
+// Shared memory: the ring of operands, and for each drain warp the rows it is about to
+// store (32 rows of 128 bytes of C, or of 64 codes).
+template <bool SW>
+struct Mem {
+  static constexpr int STAGES = SW ? 6 : 5;
+  static constexpr int OUT_WARP = 32 * (SW ? 64 : 128), OUT_BYTES = EPI_WARPS * OUT_WARP;
+  static constexpr int BYTES = STAGES * STAGE_BYTES + OUT_BYTES + RING * RING_WORDS * 4 + 2 * BM_CTA * 4 + kListBytes +
+                               BAR_BYTES + 1024;
+  static_assert(BYTES <= 232448, "shared memory");
+  static_assert(8 * (2 * STAGES + 4 * NBUF + 2 * RING + 4) <= BAR_BYTES, "barrier area");
+};
 static_assert(blocks_box_rows(kBlocksWide, false) == BOX, "boxes of A");
+constexpr uint64_t kDrainGraceNs = 50000;              // after an abort, time for the peer's copies to land
+constexpr uint16_t kBothCtas = 0x3;
 
 struct Params {
   BlocksArgs a;
@@ -68,21 +80,35 @@ struct Params {
   int c_rows;                                          // and whole ones, and beta is 0: stored row by row
 };
 
-// Hardware barriers 1 and 2: an accumulator (1 + its buffer) and, every fourth block, its
-// scales are there; the signal warp and the eight drain warps meet there.  Eight warps
-// that polled mbarriers themselves kept the queue to shared memory so full that every
-// wait and arrival, the MMA warp's too, took 200 cycles and more.  Nobody can be left
-// waiting: both sides go through the same blocks to the end, after an abort without work.
-__device__ __forceinline__ void sync_signal(int b) {
-  if (b == 0) asm volatile("bar.sync 1, 288;" ::: "memory");
-  else asm volatile("bar.sync 2, 288;" ::: "memory");
+// Hardware barriers 1 to 4: accumulator (buffer b, half h) and, every fourth block, its
+// scales are there; the signal warp and the half's four drain warps meet there.  (Eight
+// warps that poll mbarriers themselves keep the queue to shared memory full.)  Nobody can
+// be left waiting: both sides go through the same blocks to the end, after an abort without
+// results, and then the signal warp waits for the drain warps in its turn.
+__device__ __forceinline__ void sync_signal(int b, int h) {
+  if (h == 0) {
+    if (b == 0) asm volatile("bar.sync 1, 160;" ::: "memory");
+    else asm volatile("bar.sync 2, 160;" ::: "memory");
+  } else {
+    if (b == 0) asm volatile("bar.sync 3, 160;" ::: "memory");
+    else asm volatile("bar.sync 4, 160;" ::: "memory");
+  }
 }
-// Barrier 3 of the 256 drain threads; and the same, returning whether any of them has `p`.
-__device__ __forceinline__ void sync_drain() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ void arrive_signal(int b, int h) {
+  if (h == 0) {
+    if (b == 0) asm volatile("bar.arrive 1, 160;" ::: "memory");
+    else asm volatile("bar.arrive 2, 160;" ::: "memory");
+  } else {
+    if (b == 0) asm volatile("bar.arrive 3, 160;" ::: "memory");
+    else asm volatile("bar.arrive 4, 160;" ::: "memory");
+  }
+}
+// Barrier 5 of the 256 drain threads; and the same, returning whether any of them has `p`.
+__device__ __forceinline__ void sync_drain() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
 __device__ __forceinline__ bool any_drain(bool p) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 3, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 5, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
       : "r"(p ? 1u : 0u)
       : "memory");
@@ -142,17 +168,17 @@ __device__ __forceinline__ void store32(const Params& p, long long m, int n, con
   }
 }
 
-// Rows of 64 bytes (32 bf16 or 16 fp32 columns from n) of a warp's 32 rows of C, by way of
-// shared memory: a thread has a row, and 32 threads writing 16 bytes each to 32 rows take
-// 32 wavefronts where eight rows of 64 bytes take eight.  The 16-byte vectors of a row are
-// permuted by the row's number, so neither side meets a bank twice.  to: this lane's row
-// of C, or -1.
+// Rows of 128 bytes (64 bf16 or 32 fp32 columns from n) of a warp's 32 rows of C, by way of
+// shared memory: a thread has a row, and 32 threads writing 16 bytes each of 32 rows take
+// 32 wavefronts where four whole rows of 128 bytes take four.  The 16-byte vectors of a row
+// are permuted by the row's number, so neither side meets a bank twice.  to: this lane's
+// row of C, or -1.
 template <bool OUT_BF16>
 __device__ __forceinline__ void store_rows(const Params& p, uint8_t* out, int to, int n, const uint64_t* v, int lane) {
   const BlocksArgs& a = p.a;
   constexpr int PER = OUT_BF16 ? 8 : 4;                // columns of a vector
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < 8; ++q) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -164,18 +190,18 @@ __device__ __forceinline__ void store_rows(const Params& p, uint8_t* out, int to
         w[i] = __float_as_uint(a.alpha * part2(v[q * 2 + i / 2], i & 1));
       }
     }
-    *reinterpret_cast<uint4*>(out + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(out + lane * 128 + ((q ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __syncwarp();
   uint8_t* C = static_cast<uint8_t*>(a.C);
-  const int c = lane & 3;
+  const int c = lane & 7;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int row = q * 8 + lane / 4;
+  for (int q = 0; q < 8; ++q) {
+    const int row = q * 4 + lane / 8;
     const long long o = __shfl_sync(0xffffffffu, to, row);
     if (o >= 0 && n + c * PER < a.N)
       *reinterpret_cast<uint4*>(C + (o * a.ldc + n) * (OUT_BF16 ? 2 : 4) + c * 16) =
-          *reinterpret_cast<const uint4*>(out + row * 64 + ((c ^ ((row >> 1) & 3)) * 16));
+          *reinterpret_cast<const uint4*>(out + row * 128 + ((c ^ (row & 7)) * 16));
   }
   __syncwarp();                                        // read before the next rows are written
 }
@@ -186,19 +212,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     blocks_wide_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                        const __grid_constant__ CUtensorMap mapB2, const Params p) {
   constexpr int BN = SW ? 128 : 256;                   // columns of C (or of h) an item
+  constexpr int STAGES = Mem<SW>::STAGES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t base = (raw + 1023u) & ~1023u;        // the same offset in both CTAs
   uint8_t* base_ptr = smem_raw + (base - raw);
   auto a_tile = [&](int s) { return base + s * STAGE_BYTES; };
   auto b_tile = [&](int s) { return base + s * STAGE_BYTES + A_BYTES; };
   uint8_t* at = base_ptr + STAGES * STAGE_BYTES;
   uint8_t* out = at;                                   // [EPI_WARPS][OUT_WARP]
-  at += EPI_WARPS * OUT_WARP;
+  at += Mem<SW>::OUT_BYTES;
   float* ring = reinterpret_cast<float*>(at);          // [RING][RING_WORDS]
   at += RING * RING_WORDS * 4;
-  float* big = reinterpret_cast<float*>(at);           // [2][BM]
-  at += 2 * BM * 4;
+  float* big = reinterpret_cast<float*>(at);           // [2][BM_CTA]
+  at += 2 * BM_CTA * 4;
   const uint32_t bar_base = base + (uint32_t)(at - base_ptr);
   uint8_t* bar_ptr = at;
   at += BAR_BYTES;
@@ -207,27 +234,30 @@ __global__ void __launch_bounds__(THREADS, 1)
   int* num = beg + kBlocksMaxExperts;
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
   auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
-  auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + b); };
-  auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + NBUF + b); };
-  auto sfull_bar = [&](int r) { return bar_base + 8u * (2 * STAGES + 2 * NBUF + r); };
-  auto sempty_bar = [&](int r) { return bar_base + 8u * (2 * STAGES + 2 * NBUF + RING + r); };
-  const uint32_t drain_bar = bar_base + 8u * (2 * STAGES + 2 * NBUF + 2 * RING);
+  auto tfull_bar = [&](int b, int h) { return bar_base + 8u * (2 * STAGES + 2 * b + h); };
+  auto tempty_bar = [&](int b, int h) { return bar_base + 8u * (2 * STAGES + 2 * NBUF + 2 * b + h); };
+  auto sfull_bar = [&](int r) { return bar_base + 8u * (2 * STAGES + 4 * NBUF + r); };
+  auto sempty_bar = [&](int r) { return bar_base + 8u * (2 * STAGES + 4 * NBUF + RING + r); };
+  const uint32_t drain_bar = bar_base + 8u * (2 * STAGES + 4 * NBUF + 2 * RING);
   const uint32_t stall_bar = drain_bar + 8u;           // test hook: nothing arrives
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (2 * STAGES + 2 * NBUF + 2 * RING + 2));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (2 * STAGES + 4 * NBUF + 2 * RING + 2));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const BlocksArgs& a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank() & 1u;        // clusters hold one pair
+  const bool leader = rank == 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
-    for (int b = 0; b < NBUF; ++b) {
-      mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), EPI_WARPS);
-    }
+    for (int b = 0; b < NBUF; ++b)
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(tfull_bar(b, h), 1);
+        mbar_init(tempty_bar(b, h), EPI_WARPS);        // four warps of each CTA
+      }
     for (int r = 0; r < RING; ++r) {
       mbar_init(sfull_bar(r), 32);
       mbar_init(sempty_bar(r), EPI_WARPS);
@@ -241,19 +271,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (SW) tma_prefetch_desc(&mapB2);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
   }
   if (!a.early) griddep_wait();
   if (warp == 3) list_row_tiles<BM>(a, pre, beg, num, lane);
   tc_fence_before();
-  __syncthreads();                                     // barriers, lists and TMEM
+  cluster_sync();                                      // barriers, lists and TMEM of both CTAs
   tc_fence_after();
   // the next kernel may take an SM as soon as this one leaves it
   griddep_launch_dependents();
   const uint32_t tmem_base = *tmem_slot;
-  const long long items = (long long)pre[a.experts] * p.tiles_n;
-  const long long first = blockIdx.x, step = gridDim.x;
+  const int items = pre[a.experts] * p.tiles_n;         // in 32 bits: the host has seen to it
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   Walk walk{pre, beg, num, BM, p.tiles_n, 0};
 
   if (warp < EPI_FIRST) {
@@ -261,80 +291,101 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 0) {
       // ------------------------------------------------------------ copies
       if (elect_one_sync()) {
-      uint32_t issued = 0, issued_par = 0;
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (long long it = first; ok && it < items; it += step) {
-        const Item i = walk.at(it);
-        // rows that are not there are not copied: what their lanes sum up is not read
-        const int copies = (i.rows + BOX - 1) / BOX;
-        const uint32_t bytes = (uint32_t)(2 * B_BYTES + copies * BOX * BK);
-        auto weights = [&](int s, int kb) {
-          mbar_arrive_expect_tx(full_bar(s), bytes);
-          tma_load_3d(b_tile(s), &mapB, full_bar(s), i.nb * BN, kb * BK, i.e);
-          tma_load_3d(b_tile(s) + B_BYTES, SW ? &mapB2 : &mapB, full_bar(s), i.nb * BN + (SW ? 0 : 128), kb * BK, i.e);
-        };
-        // the ring is empty at first: its weights are on their way while the kernel before
-        // writes A
-        const int ahead = it == first ? min(STAGES, p.kblocks) : 0;
-        for (int s = 0; s < ahead; ++s) weights(s, s);
-        if (it == first && a.early) griddep_wait();
-        for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (kb >= ahead) {
-            if (!mbar_wait(empty_bar(stage), phase ^ 1u, a.timeout_ns, abort_flag)) {
-              if (!*abort_flag) report_status(a.status, 5, kSiteWideProducer);
-              *abort_flag = 1;
-              ok = false;
-              break;
+        uint32_t issued = 0, issued_par = 0;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int it = first; ok && it < items; it += step) {
+          const Item i = walk.at(it);
+          const int mine = min(max(i.rows - (int)rank * BM_CTA, 0), BM_CTA);      // this CTA's rows
+          const int other = i.rows - mine;
+          const int p0 = i.p0 + (int)rank * BM_CTA;
+          // rows that are not there are not copied: what their lanes sum up is not read
+          auto copies = [](int rows) { return (rows + BOX - 1) / BOX; };
+          const uint32_t bytes = (uint32_t)(2 * B_BYTES + (copies(mine) + copies(other)) * BOX * BK);
+          // both CTAs' copies of a stage complete on the leader's barrier
+          auto weights = [&](int st, int kb) {
+            if (leader) mbar_arrive_expect_tx(full_bar(st), bytes);
+            tma_load_3d_pair(b_tile(st), SW && rank == 1 ? &mapB2 : &mapB, map_to_rank(full_bar(st), 0),
+                             i.nb * BN + (SW ? 0 : (int)rank * 128), kb * BK, i.e);
+          };
+          // the ring is empty at first: its weights are on their way while the kernel before
+          // writes A
+          const int ahead = it == first ? min(STAGES, p.kblocks) : 0;
+          for (int st = 0; st < ahead; ++st) weights(st, st);
+          if (it == first && a.early) griddep_wait();
+          for (int kb = 0; kb < p.kblocks; ++kb) {
+            if (kb >= ahead) {
+              if (!mbar_wait(empty_bar(stage), phase ^ 1u, a.timeout_ns, abort_flag)) {
+                if (!*abort_flag) report_status(a.status, 5, kSiteWideProducer);
+                *abort_flag = 1;
+                ok = false;
+                break;
+              }
+              weights(stage, kb);
             }
-            weights(stage, kb);
+            for (int c = 0; c < copies(mine); ++c)
+              tma_load_2d_pair(a_tile(stage) + c * BOX * BK, &mapA, map_to_rank(full_bar(stage), 0), kb * BK, p0 + c * BOX);
+            issued |= 1u << stage;
+            issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          for (int c = 0; c < copies; ++c)
-            tma_load_2d(a_tile(stage) + c * BOX * BK, &mapA, full_bar(stage), kb * BK, i.p0 + c * BOX);
-          issued |= 1u << stage;
-          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+        }
+        if (*abort_flag) {
+          if (leader)
+            for (int s = 0; s < STAGES; ++s)
+              if (((issued >> s) & 1u) && !mbar_wait(full_bar(s), (issued_par >> s) & 1u, kDrainWaitNs, nullptr))
+                report_status(a.status, 5, kSiteWideDrain);
+          // the peer's copies complete on a barrier this CTA cannot wait on
+          const uint64_t t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < kDrainGraceNs) {
           }
         }
       }
-      if (*abort_flag)
-        for (int s = 0; s < STAGES; ++s)
-          if (((issued >> s) & 1u) && !mbar_wait(full_bar(s), (issued_par >> s) & 1u, kDrainWaitNs, nullptr))
-            report_status(a.status, 5, kSiteWideDrain);
-      }
     } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA
-      if (elect_one_sync()) {
-        constexpr uint32_t idesc = idesc_f8_f32(BM, COLS, kE4M3, kE4M3, /*A K-major*/ 0, /*B MN-major*/ 1);
+      // ------------------------------------------------------------ MMA (leader)
+      // The whole warp goes through the loop and one lane issues: descriptors are then the
+      // same for all lanes and stay in uniform registers, where the instruction wants them.
+      if (leader) {
+        constexpr uint32_t idesc = idesc_f8_f32(BM, COLS / 2, kE4M3, kE4M3, /*A K-major*/ 0, /*B MN-major*/ 1);
+        const uint64_t a_desc = smem_desc_sw128(a_tile(0), 16, 1024), b_desc = smem_desc_sw128(b_tile(0), B_BYTES, 1024);
+        const bool one = elect_one_sync();
         int stage = 0, b = 0;
         uint32_t phase = 0, bphase = 0;
         bool ok = true, issued_any = false;
-        if (a.stall && first == 0 && !mbar_wait(stall_bar, 0, a.timeout_ns / 4, abort_flag)) {
+        if (a.stall && first == 0 && !__all_sync(0xffffffffu, mbar_wait(stall_bar, 0, a.timeout_ns / 4, abort_flag))) {
           if (!*abort_flag) report_status(a.status, 5, kSiteWideMma);
           *abort_flag = 1;
           ok = false;
         }
-        for (long long it = first; ok && it < items; it += step) {
+        for (int it = first; ok && it < items; it += step) {
           for (int kb = 0; kb < p.kblocks; ++kb) {
-            if (!mbar_wait(tempty_bar(b), bphase ^ 1u, a.timeout_ns, abort_flag) ||
-                !mbar_wait(full_bar(stage), phase, a.timeout_ns, abort_flag)) {
+            ok = __all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, a.timeout_ns, abort_flag));
+            const uint64_t off = (uint64_t)(stage * (STAGE_BYTES >> 4));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              ok = ok && __all_sync(0xffffffffu, mbar_wait(tempty_bar(b, h), bphase ^ 1u, a.timeout_ns, abort_flag));
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t d = tmem_base + (uint32_t)(b * COLS + h * (COLS / 2));
+              if (one) {
+#pragma unroll
+                for (int kk = 0; kk < BK / 32; ++kk)
+                  tc_mma_f8_pair(d, a_desc + off + (kk * 32 >> 4), b_desc + off + ((kk * 32 * 128 + h * 64) >> 4), idesc,
+                                 kk != 0 ? 1u : 0u);
+                tc_commit_pair_mc(tfull_bar(b, h), kBothCtas);
+                if (h == 1) tc_commit_pair_mc(empty_bar(stage), kBothCtas);
+              }
+              issued_any = true;
+            }
+            if (!ok) {
               if (!*abort_flag) report_status(a.status, 5, kSiteWideMma);
               *abort_flag = 1;
-              ok = false;
               break;
             }
-            tc_fence_after();
-            const uint32_t d = tmem_base + (uint32_t)(b * COLS);
-#pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk)
-              tc_mma_f8(d, smem_desc_sw128(a_tile(stage) + kk * 32, 16, 1024),
-                             smem_desc_sw128(b_tile(stage) + kk * 32 * 128, B_BYTES, 1024), idesc, kk != 0 ? 1u : 0u);
-            issued_any = true;
-            tc_commit(empty_bar(stage));
-            tc_commit(tfull_bar(b));
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
@@ -345,8 +396,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
         }
-        if (*abort_flag && issued_any) {
-          tc_commit(drain_bar);
+        if (*abort_flag && issued_any && one) {
+          tc_commit_pair_mc(drain_bar, 0x1);
           if (!mbar_wait(drain_bar, 0, kDrainWaitNs, nullptr)) report_status(a.status, 5, kSiteWideDrain);
         }
       }
@@ -355,12 +406,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       int r = 0;
       uint32_t rphase = 0;
       bool ok = true;
-      for (long long it = first; ok && it < items; it += step) {
+      for (int it = first; ok && it < items; it += step) {
         const Item i = walk.at(it);
-        const float* row[BM / 32];
+        const float* row[BM_CTA / 32];
 #pragma unroll
-        for (int q = 0; q < BM / 32; ++q) {
-          const int m = q * 32 + lane;
+        for (int q = 0; q < BM_CTA / 32; ++q) {
+          const int m = (int)rank * BM_CTA + q * 32 + lane;
           int from = -1, to;
           if (m < i.rows) expert_row(a, i.p0 + m, from, to);
           row[q] = from >= 0 ? a.sa + (long long)from * a.ldsa : nullptr;
@@ -379,7 +430,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const uint32_t to = smem_u32(ring + r * RING_WORDS);
 #pragma unroll
-          for (int q = 0; q < BM / 32; ++q)
+          for (int q = 0; q < BM_CTA / 32; ++q)
             if (row[q] != nullptr) {
               const uint32_t at_row = to + (q * 32 + lane) * 16;
               if (p.sa_vec && kb + RING_BLOCKS <= p.kblocks) {
@@ -393,7 +444,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (sb != nullptr)
 #pragma unroll
             for (int u = 0; u < RING_BLOCKS; ++u)
-              if (kb + u < p.kblocks) cp_async_4(to + ((BM + lane) * 4 + u) * 4, sb + (kb + u) * a.ldsb);
+              if (kb + u < p.kblocks) cp_async_4(to + ((BM_CTA + lane) * 4 + u) * 4, sb + (kb + u) * a.ldsb);
           cp_async_arrive(sfull_bar(r));
           if (++r == RING) {
             r = 0;
@@ -408,21 +459,27 @@ __global__ void __launch_bounds__(THREADS, 1)
       int b = 0, r = 0;
       uint32_t bphase = 0, rphase = 0;
       bool ok = true;
-      for (long long it = first; it < items; it += step) {
+      for (int it = first; it < items; it += step)
         for (int kb = 0; kb < p.kblocks; ++kb) {
           const int u = kb % RING_BLOCKS;
-          if (lane == 0 && ok) {
-            ok = (u != 0 || mbar_wait(sfull_bar(r), rphase, a.timeout_ns, abort_flag)) &&
-                 mbar_wait(tfull_bar(b), bphase, a.timeout_ns, abort_flag);
-            if (!ok) {
-              if (!*abort_flag) report_status(a.status, 5, kSiteWideEpilogue);
-              *abort_flag = 1;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (ok) {
+              if (lane == 0) {
+                ok = (h != 0 || u != 0 || mbar_wait(sfull_bar(r), rphase, a.timeout_ns, abort_flag)) &&
+                     mbar_wait(tfull_bar(b, h), bphase, a.timeout_ns, abort_flag);
+                if (!ok) {
+                  if (!*abort_flag) report_status(a.status, 5, kSiteWideEpilogue);
+                  *abort_flag = 1;
+                }
+              }
+              ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             }
+            tc_fence_after();
+            tc_fence_before();
+            if (ok) arrive_signal(b, h);
+            else sync_signal(b, h);
           }
-          __syncwarp();
-          tc_fence_after();
-          tc_fence_before();
-          sync_signal(b);
           if (u == RING_BLOCKS - 1 || kb + 1 == p.kblocks) {
             if (++r == RING) {
               r = 0;
@@ -434,45 +491,42 @@ __global__ void __launch_bounds__(THREADS, 1)
             bphase ^= 1u;
           }
         }
-      }
     }
   } else {
     // ------------------------------------------------------------ drain and epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int quarter = warp % 4, half = (warp - EPI_FIRST) / 4;
-    const int m = quarter * 32 + lane;                    // row of the item
+    const int lrow = quarter * 32 + lane, m = (int)rank * BM_CTA + lrow;       // row of the CTA, of the item
     const uint32_t t_lane = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t lead_tempty = map_to_rank(tempty_bar(0, half), 0);
     int b = 0, r = 0;
-    bool ok = true;                                    // not after an abort: then only the barriers
-    for (long long it = first; it < items; it += step) {
+    bool ok = true;                                    // not after an abort: then only the barriers count
+    for (int it = first; it < items; it += step) {
       const Item i = walk.at(it);
-      // columns of the accumulator: plain half * 128 .., 128 of them; gate and up half * 64 ..
-      // and 128 + half * 64 .., 64 of each
+      // this half's columns: 64 from each CTA's part of B (plain: half * 64 .. and 128 + half *
+      // 64 .. of the item's; gate and up: half * 64 .. of each)
       uint64_t acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0;
-      auto column = [&](int c) {
-        return (uint32_t)(SW ? (c / 2) * 128 + half * 64 + (c % 2) * 32 : half * 128 + c * 32);
-      };
       for (int kb = 0; kb < p.kblocks; ++kb) {
         const int u = kb % RING_BLOCKS;
-        sync_signal(b);
+        sync_signal(b, half);
         if (*abort_flag) ok = false;
         tc_fence_after();
         const float* slot = ring + r * RING_WORDS + u;
-        const float sa = slot[m * 4], sb0 = slot[(BM + (SW ? 0 : half)) * 4], sb1 = SW ? slot[(BM + 1) * 4] : 0.f;
-        const float s0 = sa * sb0, s1 = SW ? sa * sb1 : s0;
+        const float sa = slot[lrow * 4], sb0 = slot[BM_CTA * 4], sb1 = slot[BM_CTA * 4 + 4];
+        const float s0 = sa * sb0, s1 = sa * sb1;
         const uint64_t d0 = pack2(__float_as_uint(s0), __float_as_uint(s0));
-        const uint64_t d1 = SW ? pack2(__float_as_uint(s1), __float_as_uint(s1)) : d0;
+        const uint64_t d1 = pack2(__float_as_uint(s1), __float_as_uint(s1));
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
-          tmem_ld_32x32b_x32(t_lane + (uint32_t)(b * COLS) + column(c), v);
+          tmem_ld_32x32b_x32(t_lane + (uint32_t)(b * COLS + half * (COLS / 2) + c * 32), v);
           tc_wait_ld();
           if (c == 3) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(tempty_bar(b));
+            if (lane == 0) mbar_arrive_remote_light(lead_tempty + 16u * b);
           }
 #pragma unroll
           for (int j = 0; j < 16; ++j) fma2(acc[c * 16 + j], pack2(v[2 * j], v[2 * j + 1]), c < 2 ? d0 : d1);
@@ -499,12 +553,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           acc[j] = pack2(__float_as_uint(h[0]), __float_as_uint(h[1]));
         }
-        big[half * BM + m] = top;
+        big[half * BM_CTA + lrow] = top;
         sync_drain();
-        const float s = kv_scale_for<kKvE4M3>(fmaxf(top, big[(1 - half) * BM + m]));
+        const float s = kv_scale_for<kKvE4M3>(fmaxf(top, big[(1 - half) * BM_CTA + lrow]));
         const float f = kv_recip(s);
         // 64 codes of this thread's row, then rows of 64 bytes (as store_rows)
-        uint8_t* mine = out + (warp - EPI_FIRST) * OUT_WARP;
+        uint8_t* mine = out + (warp - EPI_FIRST) * Mem<SW>::OUT_WARP;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[4];
@@ -518,7 +572,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (half == 0 && m < i.rows) a.hs[((long long)i.p0 + m) * a.ldhs + i.nb] = s;
         __syncwarp();
-        const int rows = i.rows - quarter * 32;                // of this warp
+        const int rows = i.rows - ((int)rank * BM_CTA + quarter * 32);         // of this warp
         const int c = lane & 3;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -533,17 +587,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) continue;
         int from, to = -1;
         if (m < i.rows) expert_row(a, i.p0 + m, from, to);
-        const int n = i.nb * BN + half * 128;
+        const int n = i.nb * BN + half * 64;
         if (p.c_rows) {
-          constexpr int WIDE = OUT_BF16 ? 32 : 16;
-          uint8_t* mine = out + (warp - EPI_FIRST) * OUT_WARP;
+          constexpr int WIDE = OUT_BF16 ? 64 : 32;
+          uint8_t* mine = out + (warp - EPI_FIRST) * Mem<SW>::OUT_WARP;
 #pragma unroll
-          for (int c = 0; c < 128 / WIDE; ++c)
-            if (n + c * WIDE < a.N) store_rows<OUT_BF16>(p, mine, to, n + c * WIDE, acc + c * WIDE / 2, lane);
+          for (int c = 0; c < 128 / WIDE; ++c) {
+            const int at = n + c * WIDE / 64 * 128 + c * WIDE % 64;
+            if (at < a.N) store_rows<OUT_BF16>(p, mine, to, at, acc + c * WIDE / 2, lane);
+          }
         } else if (to >= 0) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (n + c * 32 < a.N) store32<OUT_BF16>(p, to, n + c * 32, acc + c * 16);
+          for (int c = 0; c < 4; ++c) {
+            const int at = n + c / 2 * 128 + c % 2 * 32;
+            if (at < a.N) store32<OUT_BF16>(p, to, at, acc + c * 16);
+          }
         }
       }
     }
@@ -551,29 +609,58 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();                                      // both CTAs are done with the pair's TMEM and barriers
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, TMEM_COLS);
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
   }
 }
+
+struct PairInfo {
+  std::atomic<bool> ready{false};
+  int max_clusters = 0;
+};
 
 template <bool SW, bool OUT_BF16>
 int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap* mapB, const CUtensorMap* mapB2,
                 int num_sms, cudaStream_t s) {
+  static PairInfo info[64];
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   auto kernel = blocks_wide_kernel<SW, OUT_BF16>;
-  static std::atomic<int> regs{0};
-  cudaError_t e;
-  if (regs.load(std::memory_order_relaxed) == 0) {
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
-    regs.store(fa.numRegs, std::memory_order_relaxed);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Mem<SW>::BYTES;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (!info[dev].ready.load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!info[dev].ready.load(std::memory_order_relaxed)) {
+      cudaFuncAttributes fa;
+      if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+      // 128 threads at 88 registers and 256 at 208 are 384 * 168: with fewer at launch the
+      // warps that take some would wait forever
+      if (fa.numRegs < 168) return cudaErrorInvalidConfiguration;
+      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Mem<SW>::BYTES)) != cudaSuccess)
+        return e;
+      int n = 0;
+      cfg.gridDim = dim3(2 * (num_sms / 2), 1, 1);
+      if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+      info[dev].max_clusters = n > 0 ? n : 1;
+      info[dev].ready.store(true, std::memory_order_release);
+    }
   }
-  // 128 threads at 88 registers and 256 at 208 are 384 * 168: with fewer at launch the warps
-  // that take some would wait forever
-  if (regs.load(std::memory_order_relaxed) < 168) return cudaErrorInvalidConfiguration;
-  static std::atomic<uint64_t> done{0};
-  if ((e = set_smem_once(done, kernel, SMEM_BYTES)) != cudaSuccess) return e;
   Params p;
   p.a = a;
   p.kblocks = (a.K + BK - 1) / BK;
@@ -583,16 +670,9 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
   p.c_vec = ((reinterpret_cast<uintptr_t>(a.C) & 15u) == 0 && (a.ldc * osz) % 16 == 0) ? 1 : 0;
   p.c_rows = p.c_vec != 0 && a.N % (16 / osz) == 0 && a.beta == 0.f ? 1 : 0;
   const long long items = blocks_row_tiles(a.rows, a.offsets != nullptr ? a.experts : 1, BM) * p.tiles_n;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items < num_sms ? items : num_sms), 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const long long clusters = items < info[dev].max_clusters ? items : info[dev].max_clusters;
+  cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, *mapA, *mapB, SW ? *mapB2 : *mapB, p);
 }
 

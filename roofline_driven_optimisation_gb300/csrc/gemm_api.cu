@@ -981,6 +981,9 @@ int blocks_plan(const BlocksArgs& a, const DeviceInfo* dev, BlocksPlan* out) {
                                                    t_forced_bn);
   out->nt = c.nt;
   out->split = c.split;
+  // items are counted in 32 bits (a million rows of a million columns are 16 million)
+  if (blocks_row_tiles(a.rows, a.offsets != nullptr ? a.experts : 1, 32) * ((a.N + kBlocksN - 1) / kBlocksN) > 0x3fffffffll)
+    return fail(GEMM_ERR_UNSUPPORTED, "%d rows of %d columns: too many tiles", a.rows, a.N);
   return GEMM_OK;
 }
 

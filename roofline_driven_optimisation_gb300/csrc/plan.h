@@ -240,8 +240,8 @@ inline BlocksChoice blocks_choice(long long rows, int experts, int N, int kblock
     c.nt = forced == 256 || !two_weights ? forced : 32;
     return c;
   }
-  const long long wide = met * ((mean + 127) / 128) * (two_weights ? tiles_n : (N + 255) / 256);
-  if (mean > 32 && wide * 2 >= num_sms) {
+  const long long wide = met * ((mean + 255) / 256) * (two_weights ? tiles_n : (N + 255) / 256);
+  if (mean > 32 && wide * 4 >= num_sms) {
     c.nt = 256;
     return c;
   }
