@@ -135,6 +135,22 @@ __device__ __forceinline__ float part2(uint64_t v, int i) {
   return __uint_as_float(i ? hi : lo);
 }
 
+// silu(gate) * up.  exp(-g) as 2^t * (1 + r ln 2), t the rounded g * -log2(e) and r what that
+// rounding left out, so that the approximate operations leave silu within 4 units of its
+// last place at any g; a dozen instructions where expf and a division take forty (an
+// epilogue of 128 x 256 products: 7.1 us with those).
+__device__ __forceinline__ float swiglu_near(float g, float u) {
+  constexpr float kLog2e = 1.4426950408889634f, kLog2eRest = 1.925963033500e-08f, kLn2 = 0.6931471805599453f;
+  const float t = -g * kLog2e;
+  const float r = fmaf(-g, kLog2eRest, fmaf(-g, kLog2e, -t));
+  float e, q;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  // where 2^t is 0 or infinite the remainder says nothing (and may be NaN)
+  const float d = 1.f + (t > -126.f && t < 127.f ? fmaf(e, r * kLn2, e) : e);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(d));
+  return g * q * u;
+}
+
 // alpha * v + beta * C, rounded once to C's type
 __device__ __forceinline__ void blocks_store(const BlocksArgs& a, long long m, int n, float v) {
   v *= a.alpha;

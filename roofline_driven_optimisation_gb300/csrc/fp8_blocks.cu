@@ -43,7 +43,6 @@
 #include <atomic>
 #include <cstdint>
 
-#include "epilogue.cuh"
 #include "experts.cuh"
 #include "internal.h"
 #include "kv_cache.cuh"
@@ -144,7 +143,7 @@ __device__ __forceinline__ void finish_row(const Params& p, const Item& i, int m
     float h[4], big = 0.f;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      h[q] = n + q < a.N ? swiglu_combine(sv[q], uv[q]) : 0.f;
+      h[q] = n + q < a.N ? swiglu_near(sv[q], uv[q]) : 0.f;
       big = fmaxf(big, fabsf(h[q]));                            // NaN is left out
     }
     // as whole numbers magnitudes order as they are

@@ -38,7 +38,6 @@
 #include <cstdint>
 #include <mutex>
 
-#include "epilogue.cuh"
 #include "experts.cuh"
 #include "internal.h"
 #include "kv_cache.cuh"
@@ -505,6 +504,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Item i = walk.at(it);
       // this half's columns: 64 from each CTA's part of B (plain: half * 64 .. and 128 + half *
       // 64 .. of the item's; gate and up: half * 64 .. of each)
+      int to = -1;                                     // read now, used when K is through
+      if (!SW && m < i.rows) {
+        int from;
+        expert_row(a, i.p0 + m, from, to);
+      }
       uint64_t acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0;
@@ -548,7 +552,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           float h[2];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            h[q] = n + 2 * j + q < a.N ? swiglu_combine(part2(acc[j], q), part2(acc[32 + j], q)) : 0.f;
+            h[q] = n + 2 * j + q < a.N ? swiglu_near(part2(acc[j], q), part2(acc[32 + j], q)) : 0.f;
             top = fmaxf(top, fabsf(h[q]));             // fmaxf leaves NaN out
           }
           acc[j] = pack2(__float_as_uint(h[0]), __float_as_uint(h[1]));
@@ -585,8 +589,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
       } else {
         if (!ok) continue;
-        int from, to = -1;
-        if (m < i.rows) expert_row(a, i.p0 + m, from, to);
         const int n = i.nb * BN + half * 64;
         if (p.c_rows) {
           constexpr int WIDE = OUT_BF16 ? 64 : 32;
