@@ -135,53 +135,60 @@ __global__ void __launch_bounds__(256) blocks_generic_kernel(const BlocksArgs a)
 }
 
 // ---------------------------------------------------------------- weighted sums
-// A thread 8 columns of a token: its top_k rows' parts, all in flight, added in order.
-// Reads top_k * cols * 2 bytes a token once: HBM (or L2) bounds it.
-__global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a, int chunks) {
+// A block 1024 columns of a token, a thread 8 of them: its top_k rows' parts, eight in
+// flight, added in order.  Reads top_k * cols * 2 bytes a token once: HBM (or L2) bounds it.
+constexpr int COMBINE_THREADS = 128;
+__global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const __grid_constant__ CombineArgs a) {
   griddep_wait();
-  const long long total = (long long)a.tokens * chunks;
-  const __nv_bfloat16* Y = static_cast<const __nv_bfloat16*>(a.y);
-  __nv_bfloat16* O = static_cast<__nv_bfloat16*>(a.out);
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
-    const long long t = i / chunks;
-    const int c = (int)(i % chunks) * 8;
-    const float* w = a.weights + t * a.top_k;
-    const __nv_bfloat16* y = Y + t * a.top_k * a.ldy + c;
+  const long long t = blockIdx.x;
+  const int c = (int)(blockIdx.y * COMBINE_THREADS + threadIdx.x) * 8;
+  if (c >= a.cols) return;
+  const float* w = a.weights + t * a.top_k;
+  const __nv_bfloat16* y = static_cast<const __nv_bfloat16*>(a.y) + t * a.top_k * a.ldy + c;
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + t * a.ldo + c;
+  if (a.vec && c + 8 <= a.cols) {
     float sum[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) sum[q] = 0.f;
-    if (a.vec && c + 8 <= a.cols) {
-#pragma unroll 8
-      for (int j = 0; j < a.top_k; ++j) {
-        const uint4 v = *reinterpret_cast<const uint4*>(y + j * a.ldy);
-        const float f = w[j];
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+      uint4 v[8];
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = j0 + j < a.top_k;
+        v[j] = in ? *reinterpret_cast<const uint4*>(y + (j0 + j) * a.ldy) : make_uint4(0u, 0u, 0u, 0u);
+        f[j] = in ? w[j0 + j] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j0 + j >= a.top_k) break;
+        const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          sum[2 * q] = fmaf(f, __uint_as_float(u[q] << 16), sum[2 * q]);
-          sum[2 * q + 1] = fmaf(f, __uint_as_float(u[q] & 0xffff0000u), sum[2 * q + 1]);
+          sum[2 * q] = fmaf(f[j], __uint_as_float(u[q] << 16), sum[2 * q]);
+          sum[2 * q + 1] = fmaf(f[j], __uint_as_float(u[q] & 0xffff0000u), sum[2 * q + 1]);
         }
       }
-      uint32_t o[4];
+    }
+    uint32_t r[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(sum[2 * q], sum[2 * q + 1]);
-        o[q] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-      *reinterpret_cast<uint4*>(O + t * a.ldo + c) = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
-      for (int q = 0; q < 8 && c + q < a.cols; ++q) {
-        float s = 0.f;
-        for (int j = 0; j < a.top_k; ++j) s = fmaf(w[j], __bfloat162float(y[j * a.ldy + q]), s);
-        O[t * a.ldo + c + q] = __float2bfloat16_rn(s);
-      }
+    for (int q = 0; q < 4; ++q) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(sum[2 * q], sum[2 * q + 1]);
+      r[q] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint4*>(o) = make_uint4(r[0], r[1], r[2], r[3]);
+  } else {
+    for (int q = 0; q < 8 && c + q < a.cols; ++q) {
+      float s = 0.f;
+      for (int j = 0; j < a.top_k; ++j) s = fmaf(w[j], __bfloat162float(y[j * a.ldy + q]), s);
+      o[q] = __float2bfloat16_rn(s);
     }
   }
 }
 
 }  // namespace
 
-int launch_blocks_generic(const BlocksArgs& a, int num_sms, cudaStream_t s) {
+int launch_blocks_generic(const BlocksArgs& a, cudaStream_t s) {
   const long long tiles = ((long long)a.rows + GM - 1) / GM + (a.offsets != nullptr ? a.experts : 0);
   const dim3 grid((unsigned)((a.N + GN - 1) / GN), (unsigned)(tiles < 65535 ? tiles : 65535), 1);
   if (a.B2 != nullptr)
@@ -191,20 +198,19 @@ int launch_blocks_generic(const BlocksArgs& a, int num_sms, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-int launch_experts_combine(const CombineArgs& a, int num_sms, cudaStream_t s) {
-  const int chunks = (a.cols + 7) / 8;
-  const long long blocks = ((long long)a.tokens * chunks + 255) / 256;
-  const long long most = 8ll * num_sms;
+int launch_experts_combine(const CombineArgs& a, cudaStream_t s) {
+  const int across = (a.cols + 8 * COMBINE_THREADS - 1) / (8 * COMBINE_THREADS);
+  if (across > 65535) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most), 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.gridDim = dim3((unsigned)a.tokens, (unsigned)across, 1);
+  cfg.blockDim = dim3(COMBINE_THREADS, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel, a, chunks);
+  return cudaLaunchKernelEx(&cfg, combine_kernel, a);
 }
 
 }  // namespace g3

@@ -1009,7 +1009,7 @@ int blocks_product(BlocksArgs& a, const BlocksPlan* plan, DeviceInfo* dev, cudaS
     t_last_k_split = plan->split;
     t_last_bn = plan->nt;
   } else {
-    err = launch_blocks_generic(a, dev->num_sms, stream);
+    err = launch_blocks_generic(a, stream);
   }
   if (err != cudaSuccess)
     return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
@@ -1102,7 +1102,7 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
   if (E > kBlocksMaxExperts) return fail(GEMM_ERR_UNSUPPORTED, "%d experts: %d at most", E, kBlocksMaxExperts);
   if ((long long)tokens * top_k > 0x7fffffffll)
     return fail(GEMM_ERR_UNSUPPORTED, "%d tokens of %d slots: more than 2^31 - 1", tokens, top_k);
-  if (H > 0x7fffffff - 127 || F > 0x7fffffff - 127)
+  if (H > 65535 * 1024 || F > 65535 * 1024)
     return fail(GEMM_ERR_UNSUPPORTED, "hidden %d or width %d too large", H, F);
   if (w->ld_up < F || w->ld_down < H || w->stride_up < 0 || w->stride_down < 0 || ldx < H || ldo < H)
     return fail(GEMM_ERR_INVALID_ARG, "leading dimension too small (weights %lld %lld, ldx=%lld ldo=%lld)", w->ld_up,
@@ -1184,7 +1184,7 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
   c.tokens = tokens; c.top_k = top_k; c.cols = H;
   c.y = d.C; c.ldy = ws.ldy; c.weights = weights; c.out = O; c.ldo = ldo;
   c.vec = aligned16(O) && ldo % 8 == 0;
-  err = launch_experts_combine(c, dev->num_sms, stream);
+  err = launch_experts_combine(c, stream);
   if (err != cudaSuccess)
     return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
   t_last_path = fast ? GEMM_PATH_BLOCKS : GEMM_PATH_GENERIC;

@@ -376,7 +376,7 @@ int launch_blocks(const BlocksArgs& a, const BlocksPlan& plan, const CUtensorMap
 constexpr int kBlocksWide = 256;
 int launch_blocks_wide(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap* mapB, const CUtensorMap* mapB2,
                        int num_sms, cudaStream_t s);
-int launch_blocks_generic(const BlocksArgs& a, int num_sms, cudaStream_t s);
+int launch_blocks_generic(const BlocksArgs& a, cudaStream_t s);
 
 // O[t] = sum over j of weights[t][j] * Y[t * top_k + j]
 struct CombineArgs {
@@ -388,7 +388,7 @@ struct CombineArgs {
   long long ldo;
   bool vec;
 };
-int launch_experts_combine(const CombineArgs& a, int num_sms, cudaStream_t s);
+int launch_experts_combine(const CombineArgs& a, cudaStream_t s);
 
 int launch_selftest_wait(int* status, uint64_t timeout_ns, cudaStream_t s);
 
