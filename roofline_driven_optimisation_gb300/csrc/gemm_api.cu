@@ -1107,6 +1107,8 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
   if (w->ld_up < F || w->ld_down < H || w->stride_up < 0 || w->stride_down < 0 || ldx < H || ldo < H)
     return fail(GEMM_ERR_INVALID_ARG, "leading dimension too small (weights %lld %lld, ldx=%lld ldo=%lld)", w->ld_up,
                 w->ld_down, ldx, ldo);
+  if (w->ld_up > 0x7fffffffll || w->ld_down > 0x7fffffffll)
+    return fail(GEMM_ERR_UNSUPPORTED, "leading dimension above 2^31 - 1 (weights %lld %lld)", w->ld_up, w->ld_down);
   if (E > 1 && (w->stride_up < (long long)(H - 1) * w->ld_up + F || w->stride_down < (long long)(F - 1) * w->ld_down + H))
     return fail(GEMM_ERR_INVALID_ARG, "experts' matrices overlap (strides %lld and %lld)", w->stride_up, w->stride_down);
   if (tokens == 0) return GEMM_OK;
