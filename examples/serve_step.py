@@ -6,10 +6,16 @@ token at a time.  A step is the calls a server makes:
     gemm (qkv)  ->  kv_append  ->  kv_attention  ->  gemm (o)  ->  swiglu, gemm (FFN)
     ->  gemm (LM head, fp32 logits)  ->  sample
 
-with keys and values in a paged cache of 8-bit codes.  Weights are random; run it on a
-GB300 from the repository's root, after the library is built:
+with keys and values in a paged cache of 8-bit codes.  With --experts the FFN is one of
+routed experts, and it and the attention's output product have 8-bit weights with block
+scales:
 
-    python examples/serve_step.py
+    fp8_quantise, fp8_blocks (o)  ->  gemm (router, fp32)  ->  route  ->  experts
+
+Weights are random; run it on a GB300 from the repository's root, after the library is
+built:
+
+    python examples/serve_step.py [--experts]
 """
 from __future__ import annotations
 
@@ -24,10 +30,45 @@ import roofline_driven_optimisation_gb300 as g  # noqa: E402
 BF16 = torch.bfloat16
 
 
-class Layer:
-    """One layer, an embedding and an LM head: heads query heads over kv_heads shared ones."""
+def quantised(w, block_rows):
+    """E4M3 codes of a matrix and the scales of its blocks of block_rows x 128."""
+    rows, cols = w.shape
+    codes = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device="cuda")
+    scales = torch.empty(-(-rows // block_rows), -(-cols // 128), device="cuda")
+    return g.fp8_quantise(w, codes, scales, block_rows)
 
-    def __init__(self, heads=16, kv_heads=4, dim=64, ffn=2048, vocab=32000, positions=4096, seed=0):
+
+def stacked(parts):
+    """Codes and scales of several matrices, as ExpertWeights takes them."""
+    codes, scales = zip(*parts)
+    return torch.stack([c.view(torch.uint8) for c in codes]), torch.stack(scales)
+
+
+class Experts:
+    """An FFN of `experts` experts of which each token takes top_k, in 8 bits."""
+
+    def __init__(self, hidden, width, experts, top_k, weight):
+        self.top_k = top_k
+        self.router = weight(hidden, experts) * 2
+        self.weights = g.ExpertWeights(*(t for rows, cols in ((hidden, width), (hidden, width), (width, hidden))
+                                         for t in stacked([quantised(weight(rows, cols), 128) for _ in range(experts)])))
+
+    def __call__(self, x):
+        rows, experts = x.shape[0], self.weights.experts
+        logits = torch.empty(rows, experts, dtype=torch.float32, device="cuda")
+        g.gemm(x, self.router, logits, alpha=x.shape[1] ** -0.5)
+        ints = dict(dtype=torch.int32, device="cuda")
+        ids, weights = torch.empty(rows, self.top_k, **ints), torch.empty(rows, self.top_k, device="cuda")
+        offsets, order = torch.empty(experts + 1, **ints), torch.empty(rows * self.top_k, **ints)
+        g.route(logits, ids, weights, offsets, order)
+        return g.experts(self.weights, x, offsets, order, weights, torch.empty_like(x))
+
+
+class Layer:
+    """One layer, an embedding and an LM head: heads query heads over kv_heads shared ones.
+    experts > 0: routed experts of width ffn in the dense FFN's place, and 8-bit weights."""
+
+    def __init__(self, heads=16, kv_heads=4, dim=64, ffn=2048, vocab=32000, positions=4096, seed=0, experts=0, top_k=2):
         self.heads, self.kv_heads, self.dim, self.vocab = heads, kv_heads, dim, vocab
         self.width = heads * dim
         gen = torch.Generator(device="cuda").manual_seed(seed)
@@ -38,6 +79,8 @@ class Layer:
         self.qkv = weight(self.width, (heads + 2 * kv_heads) * dim)
         self.o, self.gate, self.up = weight(self.width, self.width), weight(self.width, ffn), weight(self.width, ffn)
         self.down, self.head = weight(ffn, self.width), weight(self.width, vocab) * 4
+        self.experts = Experts(self.width, ffn, experts, top_k, weight) if experts else None
+        self.o8 = quantised(self.o, 128) if experts else None
         angle = torch.arange(positions, device="cuda")[:, None] * \
             10000.0 ** (-torch.arange(0, dim, 2, device="cuda") / dim)
         self.cos, self.sin = torch.cos(angle).contiguous(), torch.sin(angle).contiguous()
@@ -56,10 +99,14 @@ class Layer:
         out = torch.empty_like(turned)
         g.kv_attention(cache, turned, out, lengths, start=start, max_new=max_new)
         x = x.clone()
-        g.gemm(out.flatten(1), self.o, x, beta=1.0)                    # added to the residual
-        hidden = torch.empty(rows, self.gate.shape[1], dtype=BF16, device="cuda")
-        g.swiglu(x, self.gate, self.up, hidden)
-        g.gemm(hidden, self.down, x, beta=1.0)
+        if self.experts is None:
+            g.gemm(out.flatten(1), self.o, x, beta=1.0)                # added to the residual
+            hidden = torch.empty(rows, self.gate.shape[1], dtype=BF16, device="cuda")
+            g.swiglu(x, self.gate, self.up, hidden)
+            g.gemm(hidden, self.down, x, beta=1.0)
+        else:
+            g.fp8_blocks(*quantised(out.flatten(1), 1), *self.o8, x, beta=1.0)
+            x += self.experts(x)
         logits = torch.empty(rows, self.vocab, dtype=torch.float32, device="cuda")
         g.gemm(x, self.head, logits, alpha=self.width ** -0.5)
         return logits
@@ -111,7 +158,8 @@ def serve(prompts, steps, layer=None, seed=1):
 
 if __name__ == "__main__":
     torch.cuda.set_device(0)
-    chosen, lp = serve([[1, 5, 9], list(range(100, 400)), [7]], steps=16)
+    layer = Layer(ffn=512, experts=16) if "--experts" in sys.argv[1:] else None
+    chosen, lp = serve([[1, 5, 9], list(range(100, 400)), [7]], steps=16, layer=layer)
     torch.cuda.synchronize()
     status, where = g.device_status()
     for b, (t, p) in enumerate(zip(chosen.tolist(), lp.tolist())):
