@@ -300,9 +300,13 @@ __device__ __forceinline__ int rank_keys(const RouteArgs& a, const T* logits, ui
 // The same for up to 256 experts, with keys whose last 8 bits are the expert's number
 // (inverted: of equal ones the lowest is largest), so that one redux gives a rank.  Each
 // lane's keys are sorted once, and a lane that won moves its keys up.  24 bits of a choice
-// tell most neighbours apart; *unsure is set where they do not, and rank_keys decides.
-template <int PER>
-__device__ __forceinline__ int rank_packed(const RouteArgs& a, const uint32_t (&key)[PER], int lane, bool* unsure) {
+// tell most neighbours apart (of sigmoid scores near 1 two tokens in three); where they
+// tell the last rank from the next one at least, the chosen are put in order by their
+// choices in fp32, a lane each: 100 instructions in place of rank_keys' 500.  *unsure is
+// set where that does not do either, and rank_keys decides.
+template <typename T, int PER>
+__device__ __forceinline__ int rank_packed(const RouteArgs& a, const T* logits, const uint32_t (&key)[PER], float m, float sum,
+                                           int lane, bool* unsure) {
   uint32_t q[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) q[i] = key[i] ? (key[i] & ~0xffu) | (0xffu - (uint32_t)(lane * PER + i)) : 0u;
@@ -343,8 +347,39 @@ __device__ __forceinline__ int rank_packed(const RouteArgs& a, const uint32_t (&
       near = !(hi - lo > 0x1p-15f * (1.f + fabsf(lo)));               // well above slack()
     }
   }
-  *unsure = __any_sync(kFull, near) || a.top_k == 32;    // of 33 ranks the last has no lane
-  return (int)(0xffu - (mine & 0xffu));
+  const int id = (int)(0xffu - (mine & 0xffu));
+  const uint32_t some = __ballot_sync(kFull, near);
+  *unsure = a.top_k == 32 || ((some >> a.top_k) & 1u);   // of 33 ranks the last has no lane
+  if (some == 0 || *unsure) return id;
+  const bool in = lane < a.top_k;
+  const float l = in ? clean(route_f32(logits[id])) : 0.f;
+  const float b = in && a.bias != nullptr ? a.bias[id] : 0.f;
+  float s = 0.f, v = l;
+  if (a.bias != nullptr) {
+    s = score_of<float>(a.softmax, l, m, sum);
+    v = b < INFINITY ? s + b : -INFINITY;
+  }
+  const uint32_t k = key_of(v);
+  int rank = 0, from = 0;
+  for (int o = 0; o < a.top_k; ++o) {
+    const uint32_t ko = __shfl_sync(kFull, k, o);
+    const int e = __shfl_sync(kFull, id, o);
+    rank += ko > k || (ko == k && e < id);
+  }
+  for (int o = 0; o < a.top_k; ++o)
+    if (__shfl_sync(kFull, rank, o) == lane) from = o;
+  const int sorted = __shfl_sync(kFull, id, from);
+  if (a.bias != nullptr) {
+    const float v1 = __shfl_sync(kFull, v, from), s1 = __shfl_sync(kFull, s, from);
+    const float l1 = __shfl_sync(kFull, l, from), b1 = __shfl_sync(kFull, b, from);
+    const float v0 = __shfl_up_sync(kFull, v1, 1), s0 = __shfl_up_sync(kFull, s1, 1);
+    const float l0 = __shfl_up_sync(kFull, l1, 1), b0 = __shfl_up_sync(kFull, b1, 1);
+    // what was last has nothing near it behind it, whichever of the chosen it was
+    const bool apart = (l0 == l1 && b0 == b1) || v1 == -INFINITY ||
+                       v0 - v1 > slack(a.softmax, fmaxf(s0, s1), fmaxf(fabsf(v0), fabsf(v1)));
+    *unsure = __any_sync(kFull, in && lane > 0 && !apart);
+  }
+  return sorted;
 }
 
 // The two largest of this lane's and the others' (lanes that differ in bits below `span`).
@@ -484,7 +519,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, long long t, con
   int id = 0;
   bool unsure = true;
   if (!close) {
-    if constexpr (PER <= 8) id = rank_packed<PER>(a, key, lane, &unsure);
+    if constexpr (PER <= 8) id = rank_packed<T, PER>(a, logits, key, m, sum, lane, &unsure);
     if (unsure) id = rank_keys<T, PER>(a, logits, key, m, sum, lane, &close);
   }
   if (close) {
@@ -600,13 +635,16 @@ constexpr int route_threads() { return PER <= 8 ? 1024 : 256; }
 template <typename T, int PER>
 __global__ void __launch_bounds__(route_threads<PER>()) route_kernel(const __grid_constant__ RouteArgs a, int chunk) {
   extern __shared__ double route_smem[];
-  __shared__ int slow, list[route_threads<PER>()];
+  __shared__ int slow, next, list[route_threads<PER>()];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32, E = a.experts;
   double* exact = route_smem;                            // E choices in fp64, of one token at a time
   float* ch = reinterpret_cast<float*>(exact + (a.choices ? E : 0)) + (a.groups > 1 && !a.group_whole ? warp * E : 0);
   int* hist = reinterpret_cast<int*>(route_smem + route_smem_choices(a, warps));
   const bool plan = a.offsets != nullptr;
-  if (threadIdx.x == 0) slow = 0;
+  if (threadIdx.x == 0) {
+    slow = 0;
+    next = warps;
+  }
   if (plan)
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
   griddep_wait();
@@ -619,7 +657,13 @@ __global__ void __launch_bounds__(route_threads<PER>()) route_kernel(const __gri
     const float b = a.bias != nullptr && lane * PER + i < E ? a.bias[lane * PER + i] : 0.f;
     bias[i] = b < INFINITY ? b : -INFINITY;              // NaN and +inf too: such an expert comes last
   }
-  for (long long t = t0 + warp; t < t1; t += warps) route_token<T, PER>(a, t, bias, ch, plan ? hist : nullptr, &slow, lane);
+  // tokens take unlike times: a warp takes the next that none has
+  for (long long t = t0 + warp; t < t1;) {
+    route_token<T, PER>(a, t, bias, ch, plan ? hist : nullptr, &slow, lane);
+    int n = 0;
+    if (lane == 0) n = atomicAdd(&next, 1);
+    t = t0 + __shfl_sync(kFull, n, 0);
+  }
   __syncthreads();
   if (slow > 0) {                                        // marked by warps of this block: a list, then one by one
     __syncthreads();
