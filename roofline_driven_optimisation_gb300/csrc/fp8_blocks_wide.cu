@@ -517,23 +517,26 @@ __global__ void __launch_bounds__(THREADS, 1)
         sync_signal(b, half);
         if (*abort_flag) ok = false;
         tc_fence_after();
+        const uint32_t sums = t_lane + (uint32_t)(b * COLS + half * (COLS / 2));
+        uint32_t v[2][16];
+        tmem_ld_32x32b_x16(sums, v[0]);
         const float* slot = ring + r * RING_WORDS + u;
         const float sa = slot[lrow * 4], sb0 = slot[BM_CTA * 4], sb1 = slot[BM_CTA * 4 + 4];
         const float s0 = sa * sb0, s1 = sa * sb1;
         const uint64_t d0 = pack2(__float_as_uint(s0), __float_as_uint(s0));
         const uint64_t d1 = pack2(__float_as_uint(s1), __float_as_uint(s1));
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(t_lane + (uint32_t)(b * COLS + half * (COLS / 2) + c * 32), v);
-          tc_wait_ld();
-          if (c == 3) {
+        for (int c = 0; c < 8; ++c) {                  // 16 sums are added while the next 16 come
+          tc_wait_ld_x16(v[c & 1]);
+          if (c < 7) {
+            tmem_ld_32x32b_x16(sums + (uint32_t)(c * 16 + 16), v[(c + 1) & 1]);
+          } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote_light(lead_tempty + 16u * b);
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) fma2(acc[c * 16 + j], pack2(v[2 * j], v[2 * j + 1]), c < 2 ? d0 : d1);
+          for (int j = 0; j < 8; ++j) fma2(acc[c * 8 + j], pack2(v[c & 1][2 * j], v[c & 1][2 * j + 1]), c < 4 ? d0 : d1);
         }
         if (u == RING_BLOCKS - 1 || kb + 1 == p.kblocks) {
           if (lane == 0) mbar_arrive(sempty_bar(r));   // its lanes have read: __syncwarp above
