@@ -47,10 +47,10 @@
  * Errors: every entry point returns a gemm_status.  On a non-zero return
  * nothing was launched (except when the second launch of a two-launch call
  * fails after the first was queued: the FP32 path's split last wave,
- * gemm_route_* of more tokens than one block takes (offsets and order are then not
- * written), gemm_experts, and gemm_sample_* of more rows than the GPU takes at once, whose token may then
- * be -2 for the rows that the second launch was to draw, or not written) and
- * gemm_get_last_error() describes the cause.  Errors
+ * gemm_route_* of more tokens than one block takes (offsets and order are then
+ * not written), gemm_experts, and gemm_sample_* of more rows than the GPU takes
+ * at once, whose token may then be -2 for the rows that the second launch was to
+ * draw, or not written) and gemm_get_last_error() describes the cause.  Errors
  * found on the device (a bounded wait that ran out, an index of a paged cache
  * that does not fit) are recorded in a status word that gemm_device_status()
  * reads.
@@ -543,6 +543,7 @@ size_t gemm_route_workspace(int tokens, int experts);
  * in a, and stored as 448; NaN is left out of a, and stored as NaN.  codes has ldq >=
  * cols bytes between rows, scales ceil(rows / block_rows) rows of ceil(cols / 128)
  * values, lds elements apart; ldx, ldq, lds may be larger than the rows.
+ * X, codes and scales may not overlap.
  * Asynchronous, no allocation, deterministic.
  */
 int gemm_fp8_quantise_bf16(int rows, int cols, const gemm_bf16_t* X, long long ldx, uint8_t* codes, long long ldq,
@@ -607,8 +608,10 @@ typedef struct {
  * it is skipped, both reported by gemm_device_status(); rows of O that such slots belong
  * to hold anything then.  O may not overlap X.  workspace: gemm_experts_workspace() bytes
  * of DEVICE memory, 16-byte aligned, of any contents, owned by one call at a time.
- * Asynchronous, no allocation, deterministic.  A call makes four launches; if a later
- * one fails, the earlier ones have been queued and O is not written.
+ * Asynchronous, no allocation, deterministic.  A call makes four or five launches; if a
+ * later one fails, the earlier ones have been queued and O is not written.  Forced paths
+ * are those of gemm_fp8_blocks: GEMM_PATH_GENERIC, and GEMM_PATH_BF16_TC for the tcgen05
+ * kernels.
  */
 int gemm_experts(const gemm_expert_weights* weights, int tokens, int top_k, const gemm_bf16_t* X, long long ldx,
                  const int* offsets, const int* order, const float* token_weights, gemm_bf16_t* O, long long ldo,
@@ -688,7 +691,8 @@ int gemm_last_path(void);
  * (8 x 8 register tiles, two CTAs per SM) or 256 (8 x 16 register tiles, one
  * CTA per SM), and an FP32 call with another forced width returns
  * GEMM_ERR_UNSUPPORTED.  The block-scaled products (gemm_fp8_blocks*,
- * gemm_experts) take 128 and 256 as rows of A a tile (single CTAs; CTA pairs).
+ * gemm_experts) take 128 and 256 as rows of A a tile: single CTAs (32 rows with gate
+ * and up weights), CTA pairs.
  * Other values return GEMM_ERR_INVALID_ARG.  For A/B measurements and tests.
  */
 int gemm_force_tile_n(int bn);
@@ -750,11 +754,12 @@ int gemm_set_wait_timeout_ns(uint64_t timeout_ns);
 
 /*
  * Test hook for the abort paths of the CTA-pair tensor-core kernel, the
- * decode split-K kernel and the FP32 SIMT kernel (including its split last
- * wave).  With enable = 1, later calls on this host thread make one role of
+ * decode split-K kernel, the FP32 SIMT kernel (including its split last
+ * wave) and the block-scaled products' kernels.  With enable = 1, later calls on this host thread make one role of
  * the first CTA or cluster wait on a barrier that nothing arrives at: the MMA
  * issuer of the first pair, the MMA issuer of rank 0 of the first decode
- * cluster, warp 0 of the first FP32 CTA.  That bounded wait runs out after
+ * cluster, warp 0 of the first FP32 CTA, the MMA issuer of a block-scaled
+ * product's first CTA, rank 0 of its first cluster or first pair.  That bounded wait runs out after
  * a quarter of the gemm_set_wait_timeout_ns() limit (before any wait that
  * follows from it, so its location code is the one recorded), the kernel records
  * GEMM_ERR_DEVICE_TIMEOUT with that role's location code and leaves through

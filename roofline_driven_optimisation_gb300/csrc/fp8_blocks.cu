@@ -108,6 +108,10 @@ template <int CW>
 __device__ __forceinline__ void tmem_read(uint32_t addr, uint32_t (&r)[CW]) {
   if constexpr (CW == 32) tmem_ld_32x32b_x32(addr, r);
   else tmem_ld_32x32b_x16(addr, r);
+  tc_wait_ld();
+  // no value is used before the wait
+#pragma unroll
+  for (int i = 0; i < CW; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 __device__ __forceinline__ int mma_rows(int rows) { return (rows + 15) & ~15; }
@@ -502,7 +506,6 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
               for (int op = 0; op < C::OPS; ++op) {
                 uint32_t r[CW];
                 tmem_read<CW>(t_lane + (uint32_t)(buf + op * NT + col), r);
-                tc_wait_ld();
                 const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scales + buf + op * NT + col);
 #pragma unroll
                 for (int j = 0; j < CW / 4; ++j) {

@@ -1005,7 +1005,7 @@ int blocks_product(BlocksArgs& a, const BlocksPlan* plan, DeviceInfo* dev, cudaS
                             CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, i ? &mB2 : &mB)) != GEMM_OK)
         return rc;
     err = plan->nt == kBlocksWide ? launch_blocks_wide(a, mA, mB, mB2, dev->num_sms, stream)
-                                      : launch_blocks(a, *plan, mA, mB, mB2, dev->num_sms, stream);
+                                  : launch_blocks(a, *plan, mA, mB, mB2, dev->num_sms, stream);
     t_last_k_split = plan->split;
     t_last_bn = plan->nt;
   } else {
@@ -1132,6 +1132,9 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
   const bool fast = map_ok(w->gate, w->ld_up) && map_ok(w->up, w->ld_up) && map_ok(w->down, w->ld_down) &&
                     su % 16 == 0 && sd % 16 == 0 && su < (1ll << 40) && sd < (1ll << 40) &&
                     t_forced_path != GEMM_PATH_GENERIC;
+  if ((t_forced_path != GEMM_PATH_AUTO && t_forced_path != GEMM_PATH_GENERIC && t_forced_path != GEMM_PATH_BF16_TC) ||
+      (t_forced_path == GEMM_PATH_BF16_TC && !fast))
+    return fail(GEMM_ERR_UNSUPPORTED, "forced path %d cannot run this call", t_forced_path);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   const int slots = tokens * top_k, hblocks = (H + kBlocksK - 1) / kBlocksK, fblocks = (F + kBlocksN - 1) / kBlocksN;
 

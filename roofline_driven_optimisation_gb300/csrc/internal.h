@@ -371,8 +371,8 @@ constexpr long long blocks_row_tiles(long long rows, int experts, int nt) {
 }
 int launch_blocks(const BlocksArgs& a, const BlocksPlan& plan, const CUtensorMap* mapA, const CUtensorMap* mapB,
                   const CUtensorMap* mapB2, int num_sms, cudaStream_t s);
-// The kernel for many rows: items of 128 rows and 256 columns; the same maps, A's boxes of
-// blocks_box_rows(kBlocksWide, false) rows.  kBlocksWide in a plan's nt selects it.
+// The kernel for many rows, on CTA pairs: items of 256 rows and 256 columns (with B2 128 of
+// each); the same maps, A's boxes of blocks_box_rows(kBlocksWide, false) rows.  kBlocksWide in a plan's nt selects it.
 constexpr int kBlocksWide = 256;
 int launch_blocks_wide(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap* mapB, const CUtensorMap* mapB2,
                        int num_sms, cudaStream_t s);

@@ -221,12 +221,15 @@ inline int cluster_split(int tiles_n, int k_units, int num_sms, int forced, int 
 }
 
 // Block-scaled products: the row tile (32, 64 or 128 rows as the MMA's columns; 256: items of
-// 128 rows and 256 columns) and the CTAs that share a tile's K.  `mean`: rows of an expert if
-// all that can have some have as many.  The wide items take calls with more than 32 rows an
-// expert that make at least one for every second SM; else a tile as wide as the mean reads
-// each weight once, and narrower ones (from L2 then) are taken while there are fewer items
-// than SMs.  K is split where even those leave SMs idle, with at least four blocks of 128 a
-// CTA.  Gate and up weights come in tiles of 32 rows only.
+// 256 rows and 256 columns on CTA pairs) and the CTAs that share a tile's K.  `mean`: rows of
+// an expert if all that can have some have as many.  Pairs take calls with more than 96 rows
+// (64 an expert: some have more than the mean, and gate and up weights have no other tiles
+// than of 32 rows) that make an item for every second pair at least.  Measured, single CTAs against pairs: 11008 x 4096 of 64
+// rows 15.9 against 19.5 us, 128 rows 19.3 against 19.6, 192 rows 34.5 against 19.8; 64
+// experts of 4096 and 1376, 40 rows each, 221 against 305 us, 64 rows 315 both, 96 rows 410
+// against 324 (347 with pairs for gate and up alone); 4096 x 11008 of 384 rows (32 pairs' items) 38.9 against 39.7.  Else a tile as
+// wide as the mean reads each weight once.  K is split where items leave SMs idle, with at
+// least four blocks of 128 a CTA (4096 x 11008 of 64 rows: 13.0 us, unsplit 31.7).
 struct BlocksChoice {
   int nt, split;
 };
@@ -241,7 +244,7 @@ inline BlocksChoice blocks_choice(long long rows, int experts, int N, int kblock
     return c;
   }
   const long long wide = met * ((mean + 255) / 256) * (two_weights ? tiles_n : (N + 255) / 256);
-  if (mean > 32 && wide * 4 >= num_sms) {
+  if (mean > (two_weights || experts > 1 ? 64 : 96) && wide * 4 >= num_sms) {
     c.nt = 256;
     return c;
   }

@@ -32,9 +32,9 @@ def plan():
 def test_choices(plan):
     #          rows, experts, N, blocks of K, two weights
     cases = {(1, 1, 11008, 32, 0): (32, 3), (1, 1, 128, 32, 0): (32, 8), (1, 1, 128, 3, 0): (32, 1),
-             (64, 1, 4096, 86, 0): (64, 4), (8192, 1, 11008, 32, 0): (256, 1),
+             (64, 1, 4096, 86, 0): (64, 4), (64, 1, 11008, 32, 0): (64, 1), (192, 1, 11008, 32, 0): (256, 1), (8192, 1, 11008, 32, 0): (256, 1),
              # routed: 8 experts of a row each, gate and up; 64 experts of 6 rows; of 1536
-             (8, 64, 1408, 16, 1): (32, 3), (384, 64, 1408, 16, 1): (32, 1), (98304, 64, 1408, 16, 1): (256, 1)}
+             (8, 64, 1408, 16, 1): (32, 3), (384, 64, 1408, 16, 1): (32, 1), (4096, 64, 1408, 16, 1): (32, 1), (6144, 64, 1408, 16, 1): (256, 1), (98304, 64, 1408, 16, 1): (256, 1)}
     got = plan([q + (SMS, 0) for q in cases])
     assert got == list(cases.values())
 
@@ -56,4 +56,4 @@ def test_every_choice_can_run(plan):
             # every CTA of a split has an SM of its own, or half of one
             assert split == 1 or met * -(-mean // nt) * tiles * split <= (2 if nt == 32 else 1) * sms
         else:
-            assert mean > 32
+            assert mean > (64 if two or experts > 1 else 96)

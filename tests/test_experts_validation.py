@@ -136,6 +136,9 @@ def test_forced_paths(g):
         with pytest.raises(g.GemmError) as e:
             blocks(g)
         assert e.value.code == g.GEMM_ERR_UNSUPPORTED
+        with pytest.raises(g.GemmError) as e:
+            experts(g)
+        assert e.value.code in (g.GEMM_ERR_UNSUPPORTED, g.GEMM_ERR_CUDA)        # a device comes first
         g.force_path(g.PATH_BF16_TC)
         with pytest.raises(g.GemmError) as e:
             blocks(g, lda=303)

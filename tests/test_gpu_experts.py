@@ -101,6 +101,21 @@ def test_zero_and_infinite_rows():
     assert np.all(np.abs(out[rest].float().cpu().numpy() - ref) <= bound + 1e-30)
 
 
+def test_forced_paths_that_cannot_run():
+    layer = Layer(2, 129, 130)
+    ids, w, offsets, order = routing(3, 2, 1)
+    x = inputs(3, 129).cuda()
+    out = torch.empty_like(x)
+    for path in (g.PATH_SKINNY, g.PATH_BF16_TC):          # no such kernels; rows that no copy takes
+        g.force_path(path)
+        try:
+            with pytest.raises(g.GemmError) as e:
+                g.experts(layer.weights, x, offsets, order, w, out)
+        finally:
+            g.force_path(g.PATH_AUTO)
+        assert e.value.code == g.GEMM_ERR_UNSUPPORTED
+
+
 def test_no_tokens():
     layer = Layer(4, 256, 144)
     none = torch.empty(0, dtype=torch.int32, device="cuda")
