@@ -63,30 +63,35 @@ struct Walk {
   }
 };
 
-// The lists of a Walk, in shared memory, by one warp: row tiles of NT.
+// The lists of a Walk, in shared memory, by one warp: row tiles of NT.  Ranges that overlap
+// may come to more tiles than the host has counted on; there is no item then.
 constexpr int kListBytes = (3 * kBlocksMaxExperts + 4) * 4;
 template <int NT>
 __device__ __forceinline__ void list_row_tiles(const BlocksArgs& a, int* pre, int* beg, int* num, int lane) {
-  int run = 0;
+  long long run = 0;
   for (int e0 = 0; e0 < a.experts; e0 += 32) {
     const int e = e0 + lane;
     int b = 0, n = 0;
     if (e < a.experts) expert_rows(a, e, b, n);
-    const int tiles = (n + NT - 1) / NT;
-    int s = tiles;
+    const unsigned tiles = ((unsigned)n + NT - 1) / NT;   // 2^26 at most: 32 lanes' fit
+    unsigned s = tiles;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, s, d);
+      const unsigned o = __shfl_up_sync(0xffffffffu, s, d);
       if (lane >= d) s += o;
     }
     if (e < a.experts) {
-      pre[e] = run + s - tiles;
+      pre[e] = (int)(run + s - tiles);
       beg[e] = b;
       num[e] = n;
     }
     run += __shfl_sync(0xffffffffu, s, 31);
   }
-  if (lane == 0) pre[a.experts] = run;
+  if (lane == 0) {
+    const bool fits = run <= blocks_row_tiles(a.rows, a.experts, NT);
+    if (!fits) report_status(a.status, 1, kSiteExperts);
+    pre[a.experts] = fits ? (int)run : 0;
+  }
 }
 
 // The one item number `it` of a line as a Walk's, into out[0..3] (expert, first row, rows,
@@ -100,7 +105,7 @@ __device__ __forceinline__ void find_item(const BlocksArgs& a, int tiles_n, long
     const int e = e0 + lane;
     int b = 0, n = 0;
     if (e < a.experts) expert_rows(a, e, b, n);
-    const int tiles = (n + NT - 1) / NT;
+    const int tiles = (int)(((unsigned)n + NT - 1) / NT);
     long long s = (long long)tiles * tiles_n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {

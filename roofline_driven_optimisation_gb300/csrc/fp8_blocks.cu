@@ -271,6 +271,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
   // SPLIT: pre[0..3] is this cluster's item, if it has one; else the lists of all
   const int items = SPLIT ? (pre[2] > 0 ? 1 : 0) : pre[a.experts] * p.tiles_n;   // in 32 bits: the host has seen to it
   const int first = SPLIT ? 0 : blockIdx.x, step = SPLIT ? 1 : gridDim.x;
+  // a block without work waits too, so that this kernel never ends before the one before
+  if (a.early && first >= items) griddep_wait();
   // blocks of K of this rank
   const int k_lo = (int)((long long)p.kblocks * rank / split), k_hi = (int)((long long)p.kblocks * (rank + 1) / split);
   Walk walk{pre, beg, num, NT, p.tiles_n, 0};

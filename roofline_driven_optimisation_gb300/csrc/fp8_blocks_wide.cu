@@ -288,6 +288,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int items = pre[a.experts] * p.tiles_n;         // in 32 bits: the host has seen to it
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   Walk walk{pre, beg, num, BM, p.tiles_n, 0};
+  // a pair without work waits too, so that this kernel never ends before the one before
+  if (a.early && first >= items) griddep_wait();
 
   if (warp < EPI_FIRST) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");

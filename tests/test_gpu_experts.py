@@ -160,6 +160,29 @@ def _slots_that_do_not_fit():
     check_status()
 
 
+@pytest.mark.parametrize("rows", [0, 128, 256])
+def test_ranges_that_overlap_are_reported(rows):
+    layer = Layer(8, 256, 144)
+    ids, w, offsets, order = routing(640, 8, 1)
+    x = inputs(640, 256).cuda()
+    out = torch.empty(640, 256, dtype=BF16, device="cuda")
+    bad = torch.tensor([0, 640] * 4 + [0], dtype=torch.int32, device="cuda")
+    g.force_tile_n(rows)
+    try:
+        for o in (bad, torch.zeros_like(bad) - 1):          # no range fits: no work at all
+            g.experts(layer.weights, x, o, order, w, out)
+            torch.cuda.synchronize()
+            assert g.device_status()[0] == g.GEMM_ERR_INVALID_ARG
+        for _ in range(3):
+            g.experts(layer.weights, x, torch.zeros_like(bad) - 1, order, w, out)
+            g.experts(layer.weights, x, offsets, order, w, out)
+        torch.cuda.synchronize()
+        assert g.device_status()[0] == g.GEMM_ERR_INVALID_ARG
+    finally:
+        g.force_tile_n(0)
+    layer.check(x, ids, w, out)
+
+
 def test_repeats_streams_and_graphs():
     layer = Layer(8, 272, 400)
     ids, w, offsets, order = routing(100, 8, 2)
