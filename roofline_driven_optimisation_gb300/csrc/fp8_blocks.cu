@@ -146,9 +146,14 @@ __device__ __forceinline__ void finish_row(const Params& p, const Item& i, int m
     const float uv[4] = {u.x, u.y, u.z, u.w};
     float h[4], big = 0.f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      h[q] = n + q < a.N ? swiglu_near(sv[q], uv[q]) : 0.f;
-      big = fmaxf(big, fabsf(h[q]));                            // NaN is left out
+    for (int q = 0; q < 4; q += 2) {
+      const uint64_t x = swiglu_near2(pack2(__float_as_uint(sv[q]), __float_as_uint(sv[q + 1])),
+                                      pack2(__float_as_uint(uv[q]), __float_as_uint(uv[q + 1])));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        h[q + i] = n + q + i < a.N ? part2(x, i) : 0.f;
+        big = fmaxf(big, fabsf(h[q + i]));                      // NaN is left out
+      }
     }
     // as whole numbers magnitudes order as they are
     const float sc = kv_scale_for<kKvE4M3>(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big))));

@@ -557,19 +557,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int n = i.nb * BN + half * 64;
         float top = 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          float h[2];
+        for (int j = 0; j < 32; ++j) acc[j] = swiglu_near2(acc[j], acc[32 + j]);
+        if (n + 64 > a.N) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            h[q] = n + 2 * j + q < a.N ? swiglu_near(part2(acc[j], q), part2(acc[32 + j], q)) : 0.f;
-            top = fmaxf(top, fabsf(h[q]));             // fmaxf leaves NaN out
-          }
-          acc[j] = pack2(__float_as_uint(h[0]), __float_as_uint(h[1]));
+          for (int j = 0; j < 32; ++j)
+            acc[j] = pack2(n + 2 * j < a.N ? __float_as_uint(part2(acc[j], 0)) : 0u,
+                           n + 2 * j + 1 < a.N ? __float_as_uint(part2(acc[j], 1)) : 0u);
         }
+#pragma unroll
+        for (int j = 0; j < 32; ++j)                   // fmaxf leaves NaN out
+          top = fmaxf(top, fmaxf(fabsf(part2(acc[j], 0)), fabsf(part2(acc[j], 1))));
         big[half * BM_CTA + lrow] = top;
         sync_drain();
         const float s = kv_scale_for<kKvE4M3>(fmaxf(top, big[(1 - half) * BM_CTA + lrow]));
-        const float f = kv_recip(s);
+        const uint64_t f = both(kv_recip(s));
         // 64 codes of this thread's row, then rows of 64 bytes (as store_rows)
         uint8_t* mine = out + (warp - EPI_FIRST) * Mem<SW>::OUT_WARP;
 #pragma unroll
@@ -577,9 +578,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint64_t x = acc[c * 8 + 2 * k], y = acc[c * 8 + 2 * k + 1];
-            w[k] = kv_code2<kKvE4M3>(__fmul_rn(part2(x, 0), f), __fmul_rn(part2(x, 1), f)) |
-                   (kv_code2<kKvE4M3>(__fmul_rn(part2(y, 0), f), __fmul_rn(part2(y, 1), f)) << 16);
+            const uint64_t x = mul2(acc[c * 8 + 2 * k], f), y = mul2(acc[c * 8 + 2 * k + 1], f);
+            w[k] = kv_code2<kKvE4M3>(part2(x, 0), part2(x, 1)) | (kv_code2<kKvE4M3>(part2(y, 0), part2(y, 1)) << 16);
           }
           *reinterpret_cast<uint4*>(mine + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
