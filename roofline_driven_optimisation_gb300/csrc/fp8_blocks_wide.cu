@@ -20,16 +20,18 @@
 // drain's 128 x 256 sums a CTA take 256 cycles of fma.rn.f32x2 (64 a warp, two warps a
 // scheduler, two cycles each), and 16 sums leave TMEM while the 16 before them are added:
 // one after the other cost the chain a quarter (356 us; loads of 32 spill, 350; of 8, 311).
-// Measured at 76 pairs x 19 items: 0.40 us a block and 2.6 us an item besides, of which the
-// rows of C take 1.8.  Without a drain a block takes 0.36 us, at the tensor cores' rate alone
-// 0.33.  8192 x 11008 x 4096: 294 us, 2510 TFLOP/s.
+// Measured at 76 pairs x 19 items: 0.39 us a block and 1.5 us an item besides (2.6 where the
+// drain warps store the rows of C, as they do in fp32).  Without a drain a block takes 0.36
+// us, at the tensor cores' rate alone 0.33.  8192 x 11008 x 4096: 269 us, 2740 TFLOP/s.
 //
-// Roles (384 threads a CTA): warp 0 copies (each CTA its rows of A and its half of B; all
+// Roles (384 threads a CTA, 512 with bf16 rows of C): warp 0 copies (each CTA its rows of A and its half of B; all
 // complete on the leader's barrier), warp 1 of the leader issues the MMAs, warp 2 copies
 // the scales of its CTA's rows into a ring of eight blocks (cp.async, no registers), warp 3
 // waits for accumulators and scales on behalf of the drain warps, warps 4-11 drain: warp w
 // the TMEM lanes 32*(w%4)..+31 of one of the two MMAs, its 128 sums in registers for the
-// whole of K.
+// whole of K.  Warps 12-15 store the rows of C that the drain warps have laid into shared
+// memory, so that these go on with the next item (294 to 269 us; the experts' down products
+// of 11 blocks an item gain more).
 //
 // h of gate and up: a thread has 64 columns of its row in both, so the largest magnitude
 // of 128 columns is found in registers and one exchange with the thread of the other
@@ -51,7 +53,7 @@ namespace g3 {
 namespace {
 
 constexpr int BK = kBlocksK, BM = kBlocksWide, BM_CTA = BM / 2;
-constexpr int THREADS = 384, EPI_WARPS = 8, EPI_FIRST = 4;
+constexpr int EPI_WARPS = 8, EPI_FIRST = 4, STORE_FIRST = 12;
 constexpr int A_BYTES = BM_CTA * BK, B_BYTES = BK * 128;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int TMEM_COLS = 512, COLS = 256, NBUF = 2;
@@ -62,14 +64,20 @@ constexpr int BOX = 64;
 constexpr int BAR_BYTES = 512;
 // Shared memory: the ring of operands, and for each drain warp the rows it is about to
 // store (32 rows of 128 bytes of C, or of 64 codes).
-template <bool SW>
+template <bool SW, bool OUT_BF16>
 struct Mem {
-  static constexpr int STAGES = SW ? 6 : 5;
-  static constexpr int OUT_WARP = 32 * (SW ? 64 : 128), OUT_BYTES = EPI_WARPS * OUT_WARP;
+  // rows of C in bf16 are stored by four warps of their own, while the next item is multiplied
+  static constexpr bool STORERS = !SW && OUT_BF16;
+  static constexpr int THREADS = STORERS ? 512 : 384;
+  // registers: 128 threads with few and 256 with many of 384 x 168, or 256 and 256 of 512 x 128
+  static constexpr int FEW = STORERS ? 48 : 88, MANY = 208, LAUNCH = STORERS ? 128 : 168;
+  static_assert((THREADS - 256) * FEW + 256 * MANY <= THREADS * LAUNCH, "registers that a warp waits for exist");
+  static constexpr int STAGES = SW ? 6 : STORERS ? 4 : 5;
+  static constexpr int OUT_WARP = 32 * (SW ? 64 : STORERS ? 256 : 128), OUT_BYTES = EPI_WARPS * OUT_WARP;
   static constexpr int BYTES = STAGES * STAGE_BYTES + OUT_BYTES + RING * RING_WORDS * 4 + 2 * BM_CTA * 4 + kListBytes +
                                BAR_BYTES + 1024;
   static_assert(BYTES <= 232448, "shared memory");
-  static_assert(8 * (2 * STAGES + 4 * NBUF + 2 * RING + 4) <= BAR_BYTES, "barrier area");
+  static_assert(8 * (2 * STAGES + 4 * NBUF + 2 * RING + 4 + 2 * EPI_WARPS) <= BAR_BYTES, "barrier area");
 };
 static_assert(blocks_box_rows(kBlocksWide, false) == BOX, "boxes of A");
 constexpr uint64_t kDrainGraceNs = 50000;              // after an abort, time for the peer's copies to land
@@ -171,31 +179,34 @@ __device__ __forceinline__ void store32(const Params& p, long long m, int n, con
   }
 }
 
-// Rows of 128 bytes (64 bf16 or 32 fp32 columns from n) of a warp's 32 rows of C, by way of
-// shared memory: a thread has a row, and 32 threads writing 16 bytes each of 32 rows take
-// 32 wavefronts where four whole rows of 128 bytes take four.  The 16-byte vectors of a row
-// are permuted by the row's number, so neither side meets a bank twice.  to: this lane's
-// row of C, or -1.
+// Rows of 128 bytes (64 bf16 or 32 fp32 columns) of a warp's 32 rows of C, by way of shared
+// memory: a thread has a row, and 32 threads writing 16 bytes each of 32 rows take 32
+// wavefronts where four whole rows of 128 bytes take four.  The 16-byte vectors of a row
+// are permuted by the row's number, so neither side meets a bank twice.
 template <bool OUT_BF16>
-__device__ __forceinline__ void store_rows(const Params& p, uint8_t* out, int to, int n, const uint64_t* v, int lane) {
-  const BlocksArgs& a = p.a;
-  constexpr int PER = OUT_BF16 ? 8 : 4;                // columns of a vector
+__device__ __forceinline__ void stage_rows(float alpha, uint8_t* out, const uint64_t* v, int lane) {
+  const uint64_t f = both(alpha);
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const uint64_t x = mul2(v[OUT_BF16 ? q * 4 + i : q * 2 + i / 2], f);
       if constexpr (OUT_BF16) {
-        const uint64_t x = v[q * 4 + i];
-        const __nv_bfloat162 b = __floats2bfloat162_rn(a.alpha * part2(x, 0), a.alpha * part2(x, 1));
+        const __nv_bfloat162 b = __floats2bfloat162_rn(part2(x, 0), part2(x, 1));
         w[i] = *reinterpret_cast<const uint32_t*>(&b);
       } else {
-        w[i] = __float_as_uint(a.alpha * part2(v[q * 2 + i / 2], i & 1));
+        w[i] = __float_as_uint(part2(x, i & 1));
       }
     }
     *reinterpret_cast<uint4*>(out + lane * 128 + ((q ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __syncwarp();
+}
+// The rows, from column n.  to: this lane's row of C, or -1.
+template <bool OUT_BF16>
+__device__ __forceinline__ void send_rows(const Params& p, const uint8_t* out, int to, int n, int lane) {
+  const BlocksArgs& a = p.a;
+  constexpr int PER = OUT_BF16 ? 8 : 4;                // columns of a vector
   uint8_t* C = static_cast<uint8_t*>(a.C);
   const int c = lane & 7;
 #pragma unroll
@@ -206,16 +217,16 @@ __device__ __forceinline__ void store_rows(const Params& p, uint8_t* out, int to
       *reinterpret_cast<uint4*>(C + (o * a.ldc + n) * (OUT_BF16 ? 2 : 4) + c * 16) =
           *reinterpret_cast<const uint4*>(out + row * 128 + ((c ^ (row & 7)) * 16));
   }
-  __syncwarp();                                        // read before the next rows are written
 }
 
 // SW: gate and up weights, codes out.
 template <bool SW, bool OUT_BF16>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
     blocks_wide_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                        const __grid_constant__ CUtensorMap mapB2, const Params p) {
   constexpr int BN = SW ? 128 : 256;                   // columns of C (or of h) an item
-  constexpr int STAGES = Mem<SW>::STAGES;
+  using M = Mem<SW, OUT_BF16>;
+  constexpr int STAGES = M::STAGES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;        // the same offset in both CTAs
@@ -224,7 +235,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto b_tile = [&](int s) { return base + s * STAGE_BYTES + A_BYTES; };
   uint8_t* at = base_ptr + STAGES * STAGE_BYTES;
   uint8_t* out = at;                                   // [EPI_WARPS][OUT_WARP]
-  at += Mem<SW>::OUT_BYTES;
+  at += M::OUT_BYTES;
   float* ring = reinterpret_cast<float*>(at);          // [RING][RING_WORDS]
   at += RING * RING_WORDS * 4;
   float* big = reinterpret_cast<float*>(at);           // [2][BM_CTA]
@@ -243,7 +254,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto sempty_bar = [&](int r) { return bar_base + 8u * (2 * STAGES + 4 * NBUF + RING + r); };
   const uint32_t drain_bar = bar_base + 8u * (2 * STAGES + 4 * NBUF + 2 * RING);
   const uint32_t stall_bar = drain_bar + 8u;           // test hook: nothing arrives
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (2 * STAGES + 4 * NBUF + 2 * RING + 2));
+  // STORERS: the rows of drain warp w (0 to 7) are there; are stored
+  auto ofull_bar = [&](int w) { return stall_bar + 8u * (1 + w); };
+  auto oempty_bar = [&](int w) { return stall_bar + 8u * (1 + EPI_WARPS + w); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (2 * STAGES + 4 * NBUF + 2 * RING + 2 + 2 * EPI_WARPS));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const BlocksArgs& a = p.a;
@@ -265,6 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(sfull_bar(r), 32);
       mbar_init(sempty_bar(r), EPI_WARPS);
     }
+    for (int w = 0; w < 2 * EPI_WARPS; ++w) mbar_init(ofull_bar(w), 1);
     mbar_init(drain_bar, 1);
     mbar_init(stall_bar, 1);
     *abort_flag = 0;
@@ -292,7 +307,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (a.early && first >= items) griddep_wait();
 
   if (warp < EPI_FIRST) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(M::FEW));
     if (warp == 0) {
       // ------------------------------------------------------------ copies
       if (elect_one_sync()) {
@@ -497,9 +512,39 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
     }
+  } else if (M::STORERS && warp >= STORE_FIRST) {
+    // ------------------------------------------------------------ rows of C
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(M::FEW));
+    const int quarter = warp - STORE_FIRST;            // of drain warps quarter and quarter + 4
+    uint32_t phase = 0;
+    bool ok = p.c_rows != 0;
+    for (int it = first; ok && it < items; it += step) {
+      const Item i = walk.at(it);
+      const int m = (int)rank * BM_CTA + quarter * 32 + lane;
+      int from, to = -1;
+      if (m < i.rows) expert_row(a, i.p0 + m, from, to);
+      for (int half = 0; ok && half < 2; ++half) {
+        const int w = half * 4 + quarter;
+        ok = __all_sync(0xffffffffu, mbar_wait(ofull_bar(w), phase, a.timeout_ns, abort_flag));
+        if (!ok) {
+          if (!*abort_flag) report_status(a.status, 5, kSiteWideRows);
+          *abort_flag = 1;
+          break;
+        }
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          const int n = i.nb * BN + c * 128 + half * 64;
+          if (n < a.N) send_rows<true>(p, out + w * M::OUT_WARP + c * 4096, to, n, lane);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(oempty_bar(w));
+      }
+      phase ^= 1u;
+    }
   } else {
     // ------------------------------------------------------------ drain and epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(M::MANY));
+    uint32_t ophase = 0;
     const int quarter = warp % 4, half = (warp - EPI_FIRST) / 4;
     const int lrow = quarter * 32 + lane, m = (int)rank * BM_CTA + lrow;       // row of the CTA, of the item
     const uint32_t t_lane = tmem_base + ((uint32_t)(quarter * 32) << 16);
@@ -511,7 +556,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // this half's columns: 64 from each CTA's part of B (plain: half * 64 .. and 128 + half *
       // 64 .. of the item's; gate and up: half * 64 .. of each)
       int to = -1;                                     // read now, used when K is through
-      if (!SW && m < i.rows) {
+      if (!SW && !(M::STORERS && p.c_rows) && m < i.rows) {
         int from;
         expert_row(a, i.p0 + m, from, to);
       }
@@ -572,7 +617,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float s = kv_scale_for<kKvE4M3>(fmaxf(top, big[(1 - half) * BM_CTA + lrow]));
         const uint64_t f = both(kv_recip(s));
         // 64 codes of this thread's row, then rows of 64 bytes (as store_rows)
-        uint8_t* mine = out + (warp - EPI_FIRST) * Mem<SW>::OUT_WARP;
+        uint8_t* mine = out + (warp - EPI_FIRST) * M::OUT_WARP;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[4];
@@ -600,12 +645,30 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) continue;
         const int n = i.nb * BN + half * 64;
         if (p.c_rows) {
-          constexpr int WIDE = OUT_BF16 ? 64 : 32;
-          uint8_t* mine = out + (warp - EPI_FIRST) * Mem<SW>::OUT_WARP;
+          const int w = warp - EPI_FIRST;
+          uint8_t* mine = out + w * M::OUT_WARP;
+          if constexpr (M::STORERS) {
+            if (!__all_sync(0xffffffffu, mbar_wait(oempty_bar(w), ophase ^ 1u, a.timeout_ns, abort_flag))) {
+              if (!*abort_flag) report_status(a.status, 5, kSiteWideRows);
+              *abort_flag = 1;
+              ok = false;
+              continue;
+            }
+            ophase ^= 1u;
+            stage_rows<true>(a.alpha, mine, acc, lane);
+            stage_rows<true>(a.alpha, mine + 4096, acc + 32, lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ofull_bar(w));
+          } else {
 #pragma unroll
-          for (int c = 0; c < 128 / WIDE; ++c) {
-            const int at = n + c * WIDE / 64 * 128 + c * WIDE % 64;
-            if (at < a.N) store_rows<OUT_BF16>(p, mine, to, at, acc + c * WIDE / 2, lane);
+            for (int c = 0; c < 4; ++c) {
+              const int at = n + c / 2 * 128 + c % 2 * 32;
+              if (at >= a.N) break;
+              stage_rows<OUT_BF16>(a.alpha, mine, acc + c * 16, lane);
+              __syncwarp();
+              send_rows<OUT_BF16>(p, mine, to, at, lane);
+              __syncwarp();                            // read before the next rows are written
+            }
           }
         } else if (to >= 0) {
 #pragma unroll
@@ -650,8 +713,8 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = Mem<SW>::BYTES;
+  cfg.blockDim = dim3(Mem<SW, OUT_BF16>::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Mem<SW, OUT_BF16>::BYTES;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -660,10 +723,9 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
     if (!info[dev].ready.load(std::memory_order_relaxed)) {
       cudaFuncAttributes fa;
       if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
-      // 128 threads at 88 registers and 256 at 208 are 384 * 168: with fewer at launch the
-      // warps that take some would wait forever
-      if (fa.numRegs < 168) return cudaErrorInvalidConfiguration;
-      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Mem<SW>::BYTES)) != cudaSuccess)
+      // with fewer registers at launch the warps that take some would wait forever
+      if (fa.numRegs < Mem<SW, OUT_BF16>::LAUNCH) return cudaErrorInvalidConfiguration;
+      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Mem<SW, OUT_BF16>::BYTES)) != cudaSuccess)
         return e;
       int n = 0;
       cfg.gridDim = dim3(2 * (num_sms / 2), 1, 1);

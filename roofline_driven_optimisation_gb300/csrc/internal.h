@@ -95,6 +95,7 @@ enum WaitSite : int {
   kSiteWideScales = 78,
   kSiteWideEpilogue = 79,
   kSiteWideDrain = 80,
+  kSiteWideRows = 81,
   kSiteExperts = 75,       // an expert's slots, or a slot's number, that do not fit the call
 };
 
