@@ -24,14 +24,14 @@
 // drain warps store the rows of C, as they do in fp32).  Without a drain a block takes 0.36
 // us, at the tensor cores' rate alone 0.33.  8192 x 11008 x 4096: 269 us, 2740 TFLOP/s.
 //
-// Roles (384 threads a CTA, 512 with bf16 rows of C): warp 0 copies (each CTA its rows of A and its half of B; all
-// complete on the leader's barrier), warp 1 of the leader issues the MMAs, warp 2 copies
-// the scales of its CTA's rows into a ring of eight blocks (cp.async, no registers), warp 3
-// waits for accumulators and scales on behalf of the drain warps, warps 4-11 drain: warp w
-// the TMEM lanes 32*(w%4)..+31 of one of the two MMAs, its 128 sums in registers for the
-// whole of K.  Warps 12-15 store the rows of C that the drain warps have laid into shared
-// memory, so that these go on with the next item (294 to 269 us; the experts' down products
-// of 11 blocks an item gain more).
+// Roles (384 threads a CTA, 512 with bf16 rows of C): warp 0 copies (each CTA its rows of A
+// and its half of B; all complete on the leader's barrier), warp 1 of the leader issues the
+// MMAs, warp 2 copies the scales of its CTA's rows into a ring of eight blocks (cp.async, no
+// registers), warp 3 waits for accumulators and scales on behalf of the drain warps, warps
+// 4-11 drain: warp w the TMEM lanes 32*(w%4)..+31 of one of the two MMAs, its 128 sums in
+// registers for the whole of K.  Warps 12-15 store the rows of C that the drain warps have
+// laid into shared memory, so that these go on with the next item (294 to 269 us; the
+// experts' down products of 11 blocks an item gain more).
 //
 // h of gate and up: a thread has 64 columns of its row in both, so the largest magnitude
 // of 128 columns is found in registers and one exchange with the thread of the other

@@ -52,7 +52,7 @@ __device__ __forceinline__ float clean(float l) { return fmaxf(l, -INFINITY); }
 // A whole number that orders as the float does (-0 as +0); 0 is below every float's.
 __device__ __forceinline__ uint32_t key_of(float f) {
   const uint32_t u = __float_as_uint(f + 0.f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
@@ -310,7 +310,7 @@ __device__ __forceinline__ int rank_packed(const RouteArgs& a, const T* logits, 
                                            int lane, bool* unsure) {
   uint32_t q[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) q[i] = key[i] ? (key[i] & ~0xffu) | (0xffu - (uint32_t)(lane * PER + i)) : 0u;
+  for (int i = 0; i < PER; ++i) q[i] = (key[i] & ~0xffu) | (0xffu - (uint32_t)(lane * PER + i));   // below 256: none
   auto order = [&](int i, int j) {
     const uint32_t hi = max(q[i], q[j]), lo = min(q[i], q[j]);
     q[i] = hi;
@@ -336,11 +336,11 @@ __device__ __forceinline__ int rank_packed(const RouteArgs& a, const T* logits, 
     for (int i = 0; i + 1 < PER; ++i) q[i] = won ? q[i + 1] : q[i];
     q[PER - 1] = won ? 0u : q[PER - 1];
   }
-  // neighbours; a key of 0 is none.  24 bits hold a bf16 logit whole, and order fp32 logits
+  // neighbours.  24 bits hold a bf16 logit whole, and order fp32 logits
   // where they differ
   const uint32_t before = __shfl_up_sync(kFull, mine, 1);
   bool near = false;
-  if (lane > 0 && lane <= a.top_k && mine != 0) {
+  if (lane > 0 && lane <= a.top_k && mine > 0xffu) {
     if (a.bias == nullptr) {
       near = !a.bf16 && (before >> 8) == (mine >> 8);
     } else {
@@ -425,11 +425,9 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const float 
   const float g = a.group_best == 2 && S > 1 ? b1 + b2 : b1;
   // ranks of the groups: lane i < G looks at group i
   const float mine = __shfl_sync(kFull, g, min(lane * per, 31));
+  const uint32_t k = key_of(mine);
   int ahead = 0;
-  for (int o = 0; o < G; ++o) {
-    const float v = __shfl_sync(kFull, mine, o);
-    ahead += v > mine || (v == mine && o < lane);
-  }
+  for (int o = 0; o < G; ++o) ahead += __shfl_sync(kFull, k, o) >= k + (o >= lane);
   const uint32_t kept = __ballot_sync(kFull, lane < G && ahead < a.top_groups);
   if (a.top_groups < G) {
     const float in = __shfl_sync(kFull, mine, __ffs(__ballot_sync(kFull, lane < G && ahead == a.top_groups - 1)) - 1);
@@ -441,7 +439,7 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const float 
   return kept;
 }
 
-// bias: this lane's experts' (0 without one); ch: E floats of the warp's own, where groups
+// bias: this lane's experts' (0 without one, -inf where there is no expert); ch: E floats of the warp's own, where groups
 // are not whole lanes.  A token that fp32 cannot route is marked by ids of -1 and counted
 // in *slow.
 template <typename T, int PER>
@@ -479,7 +477,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, long long t, con
     m = warp_max(m);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      c[i] = e0 + i < E ? soft_term<float>(l[i], m) : 0.f;
+      c[i] = soft_term<float>(l[i], m);                  // 0 where there is no expert
       sum += c[i];
     }
     sum = warp_sum(sum);
@@ -492,9 +490,9 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, long long t, con
     for (int i = 0; i < PER; ++i) {
       // the approximate operations and the product with 1/sum stay inside slack()'s units
       float s = a.softmax ? c[i] * r : sigmoid_near(l[i]);
-      if (a.bias != nullptr) s += bias[i];               // -inf: the expert comes last
-      c[i] = e0 + i < E ? s : -INFINITY;
-      key[i] = e0 + i < E ? key_of(a.bias != nullptr ? s : l[i]) : 0u;
+      s += bias[i];                                      // -inf: the expert comes last, or there is none
+      c[i] = s;
+      key[i] = key_of(a.bias != nullptr ? s : l[i]);
     }
     if (a.groups > 1) {
       const uint32_t kept = keep_groups<PER>(a, c, ch, lane, &close);
@@ -515,7 +513,12 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, long long t, con
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = e0 + i < E ? key_of(l[i]) : 0u;
+    for (int i = 0; i < PER; ++i) key[i] = key_of(l[i]);
+  }
+  if (E < 32 * PER) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (e0 + i >= E) key[i] = 0u;
   }
   int id = 0;
   bool unsure = true;
@@ -655,7 +658,8 @@ __global__ void __launch_bounds__(route_threads<PER>()) route_kernel(const __gri
   float bias[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const float b = a.bias != nullptr && lane * PER + i < E ? a.bias[lane * PER + i] : 0.f;
+    const int e = lane * PER + i;
+    const float b = e >= E ? -INFINITY : a.bias != nullptr ? a.bias[e] : 0.f;
     bias[i] = b < INFINITY ? b : -INFINITY;              // NaN and +inf too: such an expert comes last
   }
   // tokens take unlike times: a warp takes the next that none has
