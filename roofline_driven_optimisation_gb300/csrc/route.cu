@@ -16,9 +16,9 @@
 // Layout: a warp a token.  Lane i holds the experts i*PER .. i*PER+PER-1, so that the
 // lowest lane with the largest key has the lowest index, and a round of the ranking is
 // one redux, one ballot and one shuffle.  Per token the kernel reads its logits once:
-// 4 E bytes against some 800 warp instructions at E = 256, k = 8 and 8 groups (a third of
-// them in the half-rate integer pipe), so issue bounds it, not HBM: 16384 tokens take 41
-// us, 9 of them for the order by expert, against 3 us for the bytes.
+// 4 E bytes against some 800 warp instructions at E = 256, k = 8 and 8 groups (many of them
+// in the half-rate integer pipe), so issue bounds it, not HBM: 16384 tokens take 39 us, 9
+// of them for the order by expert, against 3 us for the bytes.
 //
 // Order by expert without atomics whose order shows: blocks take consecutive tokens and
 // count them by expert; a second kernel adds the counts of the blocks before its own,
@@ -704,14 +704,35 @@ __global__ void __launch_bounds__(route_threads<PER>()) route_kernel(const __gri
   place_slots(a, t0 * a.top_k, t1 * a.top_k, hist, at);
 }
 
+constexpr int kPlaceKernelThreads = 1024;
+// The sum of all values before this thread's (an expert a thread, 0 behind the last), by the
+// whole block.
+__device__ __forceinline__ int block_scan(int v) {
+  __shared__ int sums[kPlaceKernelThreads / 32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  auto scan = [&](int x) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kFull, x, d);
+      if (lane >= d) x += o;
+    }
+    return x;
+  };
+  const int s = scan(v);
+  if (lane == 31) sums[warp] = s;
+  __syncthreads();
+  const int w = sums[lane], all = scan(w);             // every warp for itself
+  return __shfl_sync(kFull, all - w, warp) + s - v;
+}
+static_assert(kPlaceKernelThreads == 1024 && kRouteMaxExperts <= kPlaceKernelThreads, "a warp a lane, an expert a thread");
+
 // The same blocks' slots, placed: counts of all blocks and of those before.  A thread
 // adds four experts' counts of some of the blocks, eight rows in flight at a time.
-constexpr int kPlaceKernelThreads = 1024;
 __global__ void __launch_bounds__(kPlaceKernelThreads) route_place_kernel(const __grid_constant__ RouteArgs a, int chunk) {
   extern __shared__ int place_smem[];
-  const int E = a.experts, lane = threadIdx.x % 32;
+  const int E = a.experts, x = threadIdx.x;
   int *total = place_smem, *before = total + E, *at = before + E;
-  for (int x = threadIdx.x; x < (2 + kPlaceWarps) * E; x += blockDim.x) place_smem[x] = 0;
+  for (int i = x; i < (2 + kPlaceWarps) * E; i += blockDim.x) place_smem[i] = 0;
   griddep_wait();
   __syncthreads();
   const int stride4 = count_stride(E) / 4, blocks = gridDim.x;
@@ -746,14 +767,10 @@ __global__ void __launch_bounds__(kPlaceKernelThreads) route_place_kernel(const 
       }
   }
   __syncthreads();
-  if (threadIdx.x < 32) {
-    const int all = warp_scan(total, total, E, lane);
-    if (blockIdx.x == 0) {
-      for (int e = lane; e < E; e += 32) a.offsets[e] = total[e];
-      if (lane == 0) a.offsets[E] = all;
-    }
-    for (int e = lane; e < E; e += 32) before[e] += total[e];
-  }
+  const int n = x < E ? total[x] : 0, first = block_scan(n);
+  if (x < E) before[x] += first;
+  if (blockIdx.x == 0 && x < E) a.offsets[x] = first;
+  if (blockIdx.x == 0 && x == E - 1) a.offsets[E] = first + n;
   __syncthreads();
   const long long t0 = (long long)blockIdx.x * chunk;
   const long long t1 = t0 + chunk < a.tokens ? t0 + chunk : a.tokens;
@@ -763,18 +780,16 @@ __global__ void __launch_bounds__(kPlaceKernelThreads) route_place_kernel(const 
 // All slots of a call by one block, from their ids alone.
 __global__ void __launch_bounds__(kPlaceKernelThreads) route_order_kernel(const __grid_constant__ RouteArgs a) {
   extern __shared__ int place_smem[];
-  const int E = a.experts, lane = threadIdx.x % 32, slots = a.tokens * a.top_k;
+  const int E = a.experts, x = threadIdx.x, slots = a.tokens * a.top_k;
   int *total = place_smem, *at = total + E;
-  for (int x = threadIdx.x; x < (1 + kPlaceWarps) * E; x += blockDim.x) place_smem[x] = 0;
+  for (int i = x; i < (1 + kPlaceWarps) * E; i += blockDim.x) place_smem[i] = 0;
   griddep_wait();
   __syncthreads();
   for (int s = threadIdx.x; s < slots; s += blockDim.x) atomicAdd(total + a.ids[s], 1);
   __syncthreads();
-  if (threadIdx.x < 32) {
-    const int all = warp_scan(total, total, E, lane);
-    for (int e = lane; e < E; e += 32) a.offsets[e] = total[e];
-    if (lane == 0) a.offsets[E] = all;
-  }
+  const int n = x < E ? total[x] : 0, first = block_scan(n);
+  if (x < E) total[x] = a.offsets[x] = first;
+  if (x == E - 1) a.offsets[E] = first + n;
   __syncthreads();
   place_slots(a, 0, slots, total, at);
 }
