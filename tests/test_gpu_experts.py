@@ -86,6 +86,17 @@ def test_forced_generic_and_padded():
     check(layer, 33, 3, path=g.PATH_GENERIC, want=g.PATH_GENERIC)
 
 
+@pytest.mark.parametrize("rows", [0, 128, 256])
+@pytest.mark.parametrize("tokens", [3, 500])
+def test_odd_sizes_of_padded_weights(tokens, rows):
+    # 270 and 142 columns in rows of 272 and 144
+    g.force_tile_n(rows)
+    try:
+        check(Layer(3, 270, 142, pad=2), tokens, 2)
+    finally:
+        g.force_tile_n(0)
+
+
 def test_zero_and_infinite_rows():
     layer = Layer(4, 256, 144)
     ids, w, offsets, order = routing(20, 4, 2)

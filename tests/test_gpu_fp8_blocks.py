@@ -74,6 +74,16 @@ def test_each_kernel(M, N, K, out, rows_a_tile):
     c.run(out, 2.0, 1.0, (0, 0, 8), (0, 0, 8))
 
 
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("M", [40, 290])
+def test_odd_columns(M, out, rows_a_tile):
+    """Rows of B that are whole vectors but for their last columns, and of C of any kind."""
+    c = Case(M, 1003, 200)
+    for pad_c in (0, 5, 13):
+        c.run(out, 1.0, 0.0, (8, 5, pad_c), want_path=g.PATH_BLOCKS)
+    c.run(out, 0.5, -1.0, (8, 5, 5), want_path=g.PATH_BLOCKS)
+
+
 @pytest.mark.parametrize("M", [1, 40])
 @pytest.mark.parametrize("N,K", [(1024, 8192), (128, 4096), (4096, 4096), (512, 1000)])
 def test_split_k(M, N, K):

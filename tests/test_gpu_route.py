@@ -100,6 +100,25 @@ def test_choices_that_fp32_cannot_tell_apart():
     check(x.cuda(), 8, score=g.ROUTE_SOFTMAX, bias=(0.1 - s).float().cuda())
 
 
+@pytest.mark.parametrize("step", [2.0 ** -22, 2.0 ** -18, 2.0 ** -15, 2.0 ** -12])
+@pytest.mark.parametrize("experts,top_k", [(8, 3), (64, 8), (200, 1), (256, 8), (256, 31)])
+def test_neighbours_close_to_each_other(experts, top_k, step):
+    """Choices that lie `step` apart, in any order: more than a step of fp32 and less than
+    one of the 16 bits that a choice near 1 has in a packed key, or just above it."""
+    gen = torch.Generator().manual_seed(experts + top_k)
+    place = torch.stack([torch.randperm(experts, generator=gen) for _ in range(300)]).double()
+    near = (0.4 + step * place).float()                                   # fp32 values themselves
+    check(near.cuda(), top_k, score=g.ROUTE_SIGMOID)
+    check((near - 0.4).cuda(), top_k, score=g.ROUTE_SOFTMAX)
+    b = 0.05 * torch.randn(experts, generator=gen)
+    target = (0.9 + step * place).numpy()                                 # score and bias together
+    x = torch.from_numpy(target) - b.double()
+    x = torch.log(x / (1 - x)).float()
+    check(x.cuda(), top_k, score=g.ROUTE_SIGMOID, bias=b.cuda())
+    groups = 4 if experts % 4 == 0 and top_k <= experts // 2 else 1
+    check(x.cuda(), top_k, score=g.ROUTE_SIGMOID, bias=b.cuda(), groups=groups, top_groups=max(1, groups // 2))
+
+
 @pytest.mark.parametrize("score", [g.ROUTE_SOFTMAX, g.ROUTE_SIGMOID])
 def test_peaked_scores(score):
     """Scores that underflow fp32, and choices then ruled by the bias."""
