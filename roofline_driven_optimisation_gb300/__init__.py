@@ -776,6 +776,8 @@ def _rows(t, name: str, rows: int, cols: int) -> int:
     """Elements between the rows of a tensor [rows][cols] with contiguous columns."""
     if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {(rows, cols)}")
+    if t.is_contiguous():
+        return cols
     step, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{name}: columns lie {one} apart")
@@ -787,7 +789,8 @@ def _rows(t, name: str, rows: int, cols: int) -> int:
 
 
 def _codes(t, name: str, rows: int, cols: int) -> int:
-    if t.dtype is not _e4m3 and t.dtype is not _u8:
+    kind = t.dtype
+    if kind is not _e4m3 and kind is not _u8:
         raise TypeError(f"{name} is a tensor of E4M3 codes (float8_e4m3fn or uint8)")
     return _rows(t, name, rows, cols)
 
@@ -805,7 +808,7 @@ def _blocks(n: int) -> int:
 def _one_device(*tensors) -> int:
     """The index of the GPU that all tensors (or None) are on."""
     index = tensors[0].get_device()
-    for t in tensors:
+    for t in tensors[1:]:
         if t is not None and t.get_device() != index:
             raise ValueError("the tensors of a call are on one device")
     if index < 0:
@@ -828,12 +831,13 @@ def route(logits, ids, weights, offsets=None, order=None, bias=None, score: int 
     top_k = ids.shape[-1]
     lib = _lib or load()
     index = _one_device(logits, ids, weights, offsets, order, bias, workspace)
-    if logits.dtype is _bf16:
+    kind = logits.dtype
+    if kind is _bf16:
         fn = lib.gemm_route_bf16
-    elif logits.dtype is _f32:
+    elif kind is _f32:
         fn = lib.gemm_route_f32
     else:
-        raise TypeError(f"unsupported logits dtype {logits.dtype}")
+        raise TypeError(f"unsupported logits dtype {kind}")
     shape = (tokens, top_k)
     if ids.dtype is not _i32 or ids.shape != shape or not ids.is_contiguous():
         raise TypeError(f"ids is a contiguous int32 tensor {shape}")
@@ -848,7 +852,8 @@ def route(logits, ids, weights, offsets=None, order=None, bias=None, score: int 
         if size:
             workspace = _scratch(size, logits.device, st)
             space = workspace.data_ptr()
-    rc = fn(tokens, experts, top_k, logits.data_ptr(), _rows(logits, "logits", tokens, experts),
+    rc = fn(tokens, experts, top_k, logits.data_ptr(),
+            experts if logits.is_contiguous() else _rows(logits, "logits", tokens, experts),
             None if bias is None else _values(bias, "bias", experts, _f32), score, groups, top_groups, group_best,
             renormalise, scale, ids.data_ptr(), weights.data_ptr(),
             None if offsets is None else _values(offsets, "offsets", experts + 1, _i32),
@@ -866,17 +871,21 @@ def fp8_quantise(X, codes, scales, block_rows: int = 1, stream=None):
         _torch()
     rows, cols = X.shape
     lib = _lib or load()
-    if X.dtype is _bf16:
+    kind = X.dtype
+    if kind is _bf16:
         fn = lib.gemm_fp8_quantise_bf16
-    elif X.dtype is _f32:
+    elif kind is _f32:
         fn = lib.gemm_fp8_quantise_f32
     else:
         raise TypeError("X is a bf16 or fp32 tensor")
     if block_rows != 1 and block_rows != 128:
         raise ValueError(f"blocks of {block_rows} x 128: 1 and 128 rows are there")
-    index = _one_device(X, codes, scales)
-    rc = fn(rows, cols, X.data_ptr(), _rows(X, "X", rows, cols), codes.data_ptr(), _codes(codes, "codes", rows, cols),
-            scales.data_ptr(), _scales(scales, "scales", -(-rows // block_rows), -(-cols // 128)), block_rows,
+    index = X.get_device()
+    if index < 0 or not codes.get_device() == scales.get_device() == index:
+        _one_device(X, codes, scales)                 # says what is wrong
+    rc = fn(rows, cols, X.data_ptr(), cols if X.is_contiguous() else _rows(X, "X", rows, cols), codes.data_ptr(),
+            _codes(codes, "codes", rows, cols), scales.data_ptr(),
+            _scales(scales, "scales", -(-rows // block_rows), -(-cols // 128)), block_rows,
             _raw_stream(index) if stream is None else stream)
     if rc:
         _check(rc)
@@ -894,17 +903,24 @@ def fp8_blocks(A, a_scale, B, b_scale, C, alpha: float = 1.0, beta: float = 0.0,
     if K2 != K or C.shape != (M, N):
         raise ValueError(f"shape mismatch {tuple(A.shape)} @ {tuple(B.shape)} -> {tuple(C.shape)}")
     lib = _lib or load()
-    if C.dtype is _bf16:
+    kind = C.dtype
+    if kind is _bf16:
         fn = lib.gemm_fp8_blocks
-    elif C.dtype is _f32:
+    elif kind is _f32:
         fn = lib.gemm_fp8_blocks_f32out
     else:
-        raise TypeError(f"unsupported output dtype {C.dtype}")
-    index = _one_device(C, A, a_scale, B, b_scale)
+        raise TypeError(f"unsupported output dtype {kind}")
+    index = C.get_device()
+    if index < 0 or not A.get_device() == a_scale.get_device() == B.get_device() == b_scale.get_device() == index:
+        _one_device(C, A, a_scale, B, b_scale)        # says what is wrong
     kb = -(-K // 128)
-    rc = fn(M, N, K, alpha, A.data_ptr(), max(_codes(A, "A", M, K), 1), a_scale.data_ptr(),
-            _scales(a_scale, "a_scale", M, kb), B.data_ptr(), max(_codes(B, "B", K, N), 1), b_scale.data_ptr(),
-            _scales(b_scale, "b_scale", kb, -(-N // 128)), beta, C.data_ptr(), max(_rows(C, "C", M, N), 1),
+    # shapes of A, B and C are known above: contiguous ones need no other look
+    lda = K if A.dtype is _e4m3 and A.is_contiguous() else _codes(A, "A", M, K)
+    ldb = N if B.dtype is _e4m3 and B.is_contiguous() else _codes(B, "B", K, N)
+    ldc = N if C.is_contiguous() else _rows(C, "C", M, N)
+    rc = fn(M, N, K, alpha, A.data_ptr(), lda or 1, a_scale.data_ptr(), _scales(a_scale, "a_scale", M, kb),
+            B.data_ptr(), ldb or 1, b_scale.data_ptr(), _scales(b_scale, "b_scale", kb, -(-N // 128)), beta,
+            C.data_ptr(), ldc or 1,
             _raw_stream(index) if stream is None else stream)
     if rc:
         _check(rc)
