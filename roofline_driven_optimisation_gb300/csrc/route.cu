@@ -439,6 +439,18 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const float 
   return kept;
 }
 
+// Rows of padding: where all logits are one number, and all biases, all choices are equal in
+// 64 bits as well, and the ranking by index stands (16384 x 256 of them in fp64: 1600 us).
+template <typename T>
+__device__ __noinline__ bool all_equal(const RouteArgs& a, const T* logits, int lane) {
+  const float l0 = clean(route_f32(logits[0])), b0 = a.bias != nullptr ? a.bias[0] : 0.f;
+  bool same = true;
+#pragma unroll 1
+  for (int e = lane; e < a.experts; e += 32)
+    same = same && clean(route_f32(logits[e])) == l0 && (a.bias == nullptr || a.bias[e] == b0);
+  return __all_sync(kFull, same) != 0;
+}
+
 // bias: this lane's experts' (0 without one, -inf where there is no expert); ch: E floats of the warp's own, where groups
 // are not whole lanes.  A token that fp32 cannot route is marked by ids of -1 and counted
 // in *slow.
@@ -496,6 +508,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, long long t, con
     }
     if (a.groups > 1) {
       const uint32_t kept = keep_groups<PER>(a, c, ch, lane, &close);
+      if (close) close = !all_equal<T>(a, logits, lane);
       if (a.group_whole) {
         if (!((kept >> ((lane / a.group_lanes) & 31)) & 1u)) {
 #pragma unroll
@@ -524,7 +537,10 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, long long t, con
   bool unsure = true;
   if (!close) {
     if constexpr (PER <= 8) id = rank_packed<T, PER>(a, logits, key, m, sum, lane, &unsure);
-    if (unsure) id = rank_keys<T, PER>(a, logits, key, m, sum, lane, &close);
+    if (PER > 8 || (unsure && !all_equal<T>(a, logits, lane))) {
+      id = rank_keys<T, PER>(a, logits, key, m, sum, lane, &close);
+      if (PER > 8 && close) close = !all_equal<T>(a, logits, lane);
+    }
   }
   if (close) {
     if (lane == 0) {

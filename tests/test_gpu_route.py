@@ -87,6 +87,26 @@ def test_ties_go_to_the_lowest_index(score):
         check(x, 8, score=score, **kw)
 
 
+@pytest.mark.parametrize("score", [g.ROUTE_SOFTMAX, g.ROUTE_SIGMOID])
+@pytest.mark.parametrize("experts", [60, 256, 512])
+def test_rows_of_padding(experts, score):
+    """Rows of one number among others, with groups, and biases that are all equal or all but one."""
+    x = logits(400, experts, seed=2)
+    x[::3] = 0
+    x[1::7] = 1.5
+    x[2::50] = float("-inf")
+    x[5] = float("nan")
+    x[7, 1:] = x[7, 0]
+    x[8, 1:] = x[8, 0]
+    x[8, experts // 2] += 1e-6
+    check(x, 6, score=score, groups=4, top_groups=2)
+    check(x, 6, score=score, groups=4, top_groups=2, bias=torch.full((experts,), 0.25, device="cuda"))
+    b = torch.zeros(experts, device="cuda")
+    b[experts - 1] = 1e-30
+    check(x, 6, score=score, groups=4, top_groups=2, bias=b)
+    check(x, 6, score=score, groups=4, top_groups=3, group_best=1, bias=b * 0)
+
+
 def test_choices_that_fp32_cannot_tell_apart():
     """Sums of score and bias that differ by less than a step of fp32: the order is that
     of 64 bits."""
