@@ -22,7 +22,7 @@
 // one after the other cost the chain a quarter (356 us; loads of 32 spill, 350; of 8, 311).
 // Measured at 76 pairs x 19 items: 0.39 us a block and 1.5 us an item besides (2.6 where the
 // drain warps store the rows of C, as they do in fp32).  Without a drain a block takes 0.36
-// us, at the tensor cores' rate alone 0.33.  8192 x 11008 x 4096: 269 us, 2740 TFLOP/s.
+// us, at the tensor cores' rate alone 0.33.  8192 x 11008 x 4096: 262 us, 2810 TFLOP/s.
 //
 // Roles (384 threads a CTA, 512 with bf16 rows of C): warp 0 copies (each CTA its rows of A
 // and its half of B; all complete on the leader's barrier), warp 1 of the leader issues the
@@ -93,9 +93,13 @@ struct Params {
 
 // Hardware barriers 1 to 4: accumulator (buffer b, half h) and, every fourth block, its
 // scales are there; the signal warp and the half's four drain warps meet there.  (Eight
-// warps that poll mbarriers themselves keep the queue to shared memory full.)  Nobody can
-// be left waiting: both sides go through the same blocks to the end, after an abort without
-// results, and then the signal warp waits for the drain warps in its turn.
+// warps that poll mbarriers themselves keep the queue to shared memory full.)  All five wait:
+// a signal warp that only arrived would run ahead, and its second arrival in a phase (an
+// abort comes while the first is pending) would end that phase without one of the drain
+// warps, for good.  This way every phase has the same five warps, whatever the signal warp
+// has found, and nobody can be left waiting: all go through the same blocks to the end,
+// after an abort without results.  It is also faster: the polls for a block stop while the
+// drain warps are not back yet (8192 x 11008 x 4096: 262 us, 270 with arrivals).
 __device__ __forceinline__ void sync_signal(int b, int h) {
   if (h == 0) {
     if (b == 0) asm volatile("bar.sync 1, 160;" ::: "memory");
@@ -103,15 +107,6 @@ __device__ __forceinline__ void sync_signal(int b, int h) {
   } else {
     if (b == 0) asm volatile("bar.sync 3, 160;" ::: "memory");
     else asm volatile("bar.sync 4, 160;" ::: "memory");
-  }
-}
-__device__ __forceinline__ void arrive_signal(int b, int h) {
-  if (h == 0) {
-    if (b == 0) asm volatile("bar.arrive 1, 160;" ::: "memory");
-    else asm volatile("bar.arrive 2, 160;" ::: "memory");
-  } else {
-    if (b == 0) asm volatile("bar.arrive 3, 160;" ::: "memory");
-    else asm volatile("bar.arrive 4, 160;" ::: "memory");
   }
 }
 // Barrier 5 of the 256 drain threads; and the same, returning whether any of them has `p`.
@@ -497,8 +492,7 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
             }
             tc_fence_after();
             tc_fence_before();
-            if (ok) arrive_signal(b, h);
-            else sync_signal(b, h);
+            sync_signal(b, h);
           }
           if (u == RING_BLOCKS - 1 || kb + 1 == p.kblocks) {
             if (++r == RING) {
