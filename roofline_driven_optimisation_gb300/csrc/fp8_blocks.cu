@@ -90,7 +90,7 @@ struct Cfg {
   static_assert(TMEM_COLS == 512 || TMEM_COLS == 256, "TMEM allocations are powers of two");
   static_assert(STAGES >= 3, "the ring needs three stages");
   static_assert(!SPLIT || OPS * NT * BN * 4 <= STAGES * STAGE_BYTES, "a split's sums lie over the ring");
-  static_assert(8 * (2 * STAGES + 8) <= BAR_BYTES, "barrier area");
+  static_assert(8 * (2 * STAGES + 11) <= BAR_BYTES, "barrier area");
 };
 
 struct Params {
@@ -239,6 +239,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
   const uint32_t stall_bar = drain_bar + 8u;                     // test hook: nothing arrives
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (2 * STAGES + 8));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // what may still have to land when a role has given up: stages with copies, the parities
+  // of their last ones, and whether an MMA was issued
+  volatile uint32_t* landing = tmem_slot + 2;
 
   const BlocksArgs& a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -257,6 +260,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
     mbar_init(drain_bar, 1);
     mbar_init(stall_bar, 1);
     *abort_flag = 0;
+    for (int q = 0; q < 3; ++q) landing[q] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&mapA);
     tma_prefetch_desc(&mapB);
@@ -354,10 +358,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
         }
       }
     }
-    if (*abort_flag && leader)
-      for (int s = 0; s < STAGES; ++s)
-        if (((issued >> s) & 1u) && !mbar_wait(full_bar(s), (issued_par >> s) & 1u, kDrainWaitNs, nullptr))
-          report_status(a.status, 5, kSiteBlocksDrain);
+    if (leader) {
+      landing[0] = issued;
+      landing[1] = issued_par;
+    }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA
     if (elect_one_sync()) {
@@ -404,10 +408,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
           }
         }
       }
-      if (*abort_flag && issued_any) {
-        tc_commit(drain_bar);
-        if (!mbar_wait(drain_bar, 0, kDrainWaitNs, nullptr)) report_status(a.status, 5, kSiteBlocksDrain);
-      }
+      landing[2] = issued_any ? 1 : 0;
     }
   } else if (warp == 2) {
     // -------------------------------------------------------------- scales
@@ -586,6 +587,21 @@ __global__ void __launch_bounds__(THREADS, Cfg<NT, SW, SPLIT>::CTAS)
   }
   tc_fence_before();
   __syncthreads();
+  // All roles are through, so the flag is final: whichever of them gave up, and however late,
+  // no memory is given back while a copy or an MMA may still write to it.
+  if (*abort_flag) {
+    if (warp == 0 && lane == 0)
+#pragma unroll 1
+      for (int st = 0; st < STAGES; ++st)
+        if (((landing[0] >> st) & 1u) && !mbar_wait(full_bar(st), (landing[1] >> st) & 1u, kDrainWaitNs, nullptr))
+          report_status(a.status, 5, kSiteBlocksDrain);
+    // the thread that issued the MMAs: election gives the same lane again
+    if (warp == 1 && elect_one_sync() && landing[2] != 0) {
+      tc_commit(drain_bar);
+      if (!mbar_wait(drain_bar, 0, kDrainWaitNs, nullptr)) report_status(a.status, 5, kSiteBlocksDrain);
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);

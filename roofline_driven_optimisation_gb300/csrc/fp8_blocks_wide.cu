@@ -77,10 +77,10 @@ struct Mem {
   static constexpr int BYTES = STAGES * STAGE_BYTES + OUT_BYTES + RING * RING_WORDS * 4 + 2 * BM_CTA * 4 + kListBytes +
                                BAR_BYTES + 1024;
   static_assert(BYTES <= 232448, "shared memory");
-  static_assert(8 * (2 * STAGES + 4 * NBUF + 2 * RING + 4 + 2 * EPI_WARPS) <= BAR_BYTES, "barrier area");
+  static_assert(8 * (2 * STAGES + 4 * NBUF + 2 * RING + 7 + 2 * EPI_WARPS) <= BAR_BYTES, "barrier area");
 };
 static_assert(blocks_box_rows(kBlocksWide, false) == BOX, "boxes of A");
-constexpr uint64_t kDrainGraceNs = 50000;              // after an abort, time for the peer's copies to land
+constexpr uint64_t kDrainGraceNs = 50000;              // after an abort, time for the other CTA's copies to land
 constexpr uint16_t kBothCtas = 0x3;
 
 struct Params {
@@ -254,6 +254,9 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
   auto oempty_bar = [&](int w) { return stall_bar + 8u * (1 + EPI_WARPS + w); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (2 * STAGES + 4 * NBUF + 2 * RING + 2 + 2 * EPI_WARPS));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // what may still have to land when a role has given up: stages with copies, the parities
+  // of their last ones, and whether an MMA was issued
+  volatile uint32_t* landing = tmem_slot + 2;
 
   const BlocksArgs& a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -278,6 +281,7 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
     mbar_init(drain_bar, 1);
     mbar_init(stall_bar, 1);
     *abort_flag = 0;
+    for (int q = 0; q < 3; ++q) landing[q] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&mapA);
     tma_prefetch_desc(&mapB);
@@ -349,16 +353,8 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
             }
           }
         }
-        if (*abort_flag) {
-          if (leader)
-            for (int s = 0; s < STAGES; ++s)
-              if (((issued >> s) & 1u) && !mbar_wait(full_bar(s), (issued_par >> s) & 1u, kDrainWaitNs, nullptr))
-                report_status(a.status, 5, kSiteWideDrain);
-          // the peer's copies complete on a barrier this CTA cannot wait on
-          const uint64_t t0 = globaltimer_ns();
-          while (globaltimer_ns() - t0 < kDrainGraceNs) {
-          }
-        }
+        landing[0] = issued;
+        landing[1] = issued_par;
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA (leader)
@@ -411,10 +407,7 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
             }
           }
         }
-        if (*abort_flag && issued_any && one) {
-          tc_commit_pair_mc(drain_bar, 0x1);
-          if (!mbar_wait(drain_bar, 0, kDrainWaitNs, nullptr)) report_status(a.status, 5, kSiteWideDrain);
-        }
+        if (one) landing[2] = issued_any ? 1 : 0;
       }
     } else if (warp == 2) {
       // ------------------------------------------------------------ scales
@@ -677,6 +670,29 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
 
   __syncwarp();
   tc_fence_before();
+  cluster_sync();
+  // All roles of both CTAs are through, so the flag is final: whichever of them gave up, and
+  // however late, no memory is given back while a copy or an MMA may still write to it.  Both
+  // CTAs' copies of a stage complete on the leader's barrier; the peer may have issued some
+  // that the leader did not, whose barrier says nothing then.
+  if (*abort_flag) {
+    if (leader && warp == 0 && lane == 0)
+#pragma unroll 1
+      for (int st = 0; st < STAGES; ++st)
+        if (((landing[0] >> st) & 1u) && !mbar_wait(full_bar(st), (landing[1] >> st) & 1u, kDrainWaitNs, nullptr))
+          report_status(a.status, 5, kSiteWideDrain);
+    // the thread that issued the MMAs: election gives the same lane again
+    if (leader && warp == 1 && elect_one_sync() && landing[2] != 0) {
+      tc_commit_pair_mc(drain_bar, 0x1);
+      if (!mbar_wait(drain_bar, 0, kDrainWaitNs, nullptr)) report_status(a.status, 5, kSiteWideDrain);
+    }
+    if (warp == 0) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < kDrainGraceNs) {
+      }
+    }
+    __syncwarp();
+  }
   cluster_sync();                                      // both CTAs are done with the pair's TMEM and barriers
   if (warp == 1) {
     tc_fence_after();

@@ -54,3 +54,38 @@ def test_product_gives_up_midway(short_limit, M, N, blocks):
     check_status()
     want, bound = ox.product(ox.dequantise(a, sa, 1), ox.dequantise(b, sb, 128), bf16=True)
     assert np.all(np.abs(out.float().cpu().numpy() - want) <= bound)
+
+
+# the limit ends near the end of K, and with all of K in the ring: the roles that copy and
+# multiply may be through when another gives up
+@pytest.mark.parametrize("blocks", [2500, 2600, 2700, 2800, 2900])
+def test_product_gives_up_at_the_end(short_limit, blocks):
+    C = torch.empty(256, 256, dtype=BF16, device="cuda")
+    product(256, 256, blocks * 128, C)
+    assert g.device_status()[0] in (0, g.GEMM_ERR_DEVICE_TIMEOUT)
+    out = torch.empty(300, 528, dtype=BF16, device="cuda")
+    for _ in range(3):
+        product(300, 528, 512, out)
+        check_status()
+
+
+@pytest.mark.parametrize("M,rows", [(4, 0), (60, 0), (300, 128), (300, 256)])
+@pytest.mark.parametrize("blocks", [1, 2, 4])
+def test_stalled_with_all_of_k_in_the_ring(short_limit, M, rows, blocks):
+    A, sa = codes(np.random.default_rng(1), M, blocks * 128), np.ones((M, blocks), np.float32)
+    B, sb = codes(np.random.default_rng(2), blocks * 128, 528), np.ones((blocks, 5), np.float32)
+    args = [fp8(A).cuda(), torch.from_numpy(sa).cuda(), fp8(B).cuda(), torch.from_numpy(sb).cuda()]
+    out = torch.empty(M, 528, device="cuda")
+    g.force_tile_n(rows)
+    g.test_stall(1)
+    try:
+        g.fp8_blocks(*args, out)
+    finally:
+        g.test_stall(0)
+    torch.cuda.synchronize()
+    assert g.device_status()[0] == g.GEMM_ERR_DEVICE_TIMEOUT
+    for _ in range(2):
+        g.fp8_blocks(*args, out)
+        check_status()
+        want, bound = ox.product(ox.dequantise(A, sa, 1), ox.dequantise(B, sb, 128))
+        assert np.all(np.abs(out.cpu().numpy() - want) <= bound)
