@@ -146,9 +146,9 @@ def ffn(x, gate, up, down):
     return v @ down, ev @ np.abs(down) + product_bound(np.abs(v) + ev, down)
 
 
-def experts(x, ids, weights, gate, up, down):
+def experts(x, ids, weights, gate, up, down, y_bf16=True):
     """(out, bound) of the experts' FFN: x [tokens][hidden] in bf16's values, weights of
-    each expert as values."""
+    each expert as values; y_bf16: each y may be rounded to bf16 besides."""
     xv = dequantise(*quantise(x), 1)
     ids, w = np.asarray(ids), np.asarray(weights, np.float64)
     out, err = np.zeros(x.shape), np.zeros(x.shape)
@@ -157,7 +157,7 @@ def experts(x, ids, weights, gate, up, down):
         if len(t) == 0:
             continue
         y, ey = ffn(xv[t], gate[e], up[e], down[e])
-        ey = ey + U16 * (np.abs(y) + ey)
+        ey = ey + (U16 if y_bf16 else U32) * (np.abs(y) + ey)
         np.add.at(out, t, w[t, j][:, None] * y)
         np.add.at(err, t, np.abs(w[t, j])[:, None] * (ey + ids.shape[1] * U32 * np.abs(y)))
     return out, err + U16 * (np.abs(out) + err)

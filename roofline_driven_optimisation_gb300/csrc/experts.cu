@@ -135,40 +135,51 @@ __global__ void __launch_bounds__(256) blocks_generic_kernel(const BlocksArgs a)
 }
 
 // ---------------------------------------------------------------- weighted sums
-// A block 1024 columns of a token, a thread 8 of them: its top_k rows' parts, eight in
-// flight, added in order.  Reads top_k * cols * 2 bytes a token once: HBM (or L2) bounds it
-// (16384 tokens of 8 slots of 4096: 167 us for 1.2 GB, the last of them still in L2; 250
-// with tokens' columns in one line over the grid).
+// A block 1024 columns of a token, a thread 8 of them: its top_k rows' parts, 128 bytes in
+// flight, added in order.  Reads top_k * cols values of y a token once: HBM (or L2) bounds it
+// (16384 tokens of 8 slots of 4096 in bf16: 167 us for 1.2 GB, the last of them still in L2;
+// 250 with tokens' columns in one line over the grid).
 constexpr int COMBINE_THREADS = 128;
+template <typename T>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const __grid_constant__ CombineArgs a) {
+  constexpr int WORDS = (int)sizeof(T) / 2, FLIGHT = 8 / WORDS;      // 16-byte vectors of 8 values; rows in flight
   griddep_wait();
   const long long t = blockIdx.x;
   const int c = (int)(blockIdx.y * COMBINE_THREADS + threadIdx.x) * 8;
   if (c >= a.cols) return;
   const float* w = a.weights + t * a.top_k;
-  const __nv_bfloat16* y = static_cast<const __nv_bfloat16*>(a.y) + t * a.top_k * a.ldy + c;
+  const T* y = static_cast<const T*>(a.y) + t * a.top_k * a.ldy + c;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + t * a.ldo + c;
   if (a.vec && c + 8 <= a.cols) {
     float sum[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) sum[q] = 0.f;
-    for (int j0 = 0; j0 < a.top_k; j0 += 8) {
-      uint4 v[8];
-      float f[8];
+    for (int j0 = 0; j0 < a.top_k; j0 += FLIGHT) {
+      uint4 v[FLIGHT][WORDS];
+      float f[FLIGHT];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < FLIGHT; ++j) {
         const bool in = j0 + j < a.top_k;
-        v[j] = in ? *reinterpret_cast<const uint4*>(y + (j0 + j) * a.ldy) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int q = 0; q < WORDS; ++q)
+          v[j][q] = in ? reinterpret_cast<const uint4*>(y + (j0 + j) * a.ldy)[q] : make_uint4(0u, 0u, 0u, 0u);
         f[j] = in ? w[j0 + j] : 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < FLIGHT; ++j) {
         if (j0 + j >= a.top_k) break;
-        const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          sum[2 * q] = fmaf(f[j], __uint_as_float(u[q] << 16), sum[2 * q]);
-          sum[2 * q + 1] = fmaf(f[j], __uint_as_float(u[q] & 0xffff0000u), sum[2 * q + 1]);
+        for (int q = 0; q < WORDS; ++q) {
+          const uint32_t u[4] = {v[j][q].x, v[j][q].y, v[j][q].z, v[j][q].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (WORDS == 1) {
+              sum[2 * i] = fmaf(f[j], __uint_as_float(u[i] << 16), sum[2 * i]);
+              sum[2 * i + 1] = fmaf(f[j], __uint_as_float(u[i] & 0xffff0000u), sum[2 * i + 1]);
+            } else {
+              sum[4 * q + i] = fmaf(f[j], __uint_as_float(u[i]), sum[4 * q + i]);
+            }
+          }
         }
       }
     }
@@ -182,7 +193,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const __grid_c
   } else {
     for (int q = 0; q < 8 && c + q < a.cols; ++q) {
       float s = 0.f;
-      for (int j = 0; j < a.top_k; ++j) s = fmaf(w[j], __bfloat162float(y[j * a.ldy + q]), s);
+      for (int j = 0; j < a.top_k; ++j) s = fmaf(w[j], (float)y[j * a.ldy + q], s);
       o[q] = __float2bfloat16_rn(s);
     }
   }
@@ -212,7 +223,7 @@ int launch_experts_combine(const CombineArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel, a);
+  return a.y_bf16 ? cudaLaunchKernelEx(&cfg, combine_kernel<__nv_bfloat16>, a) : cudaLaunchKernelEx(&cfg, combine_kernel<float>, a);
 }
 
 }  // namespace g3

@@ -1058,10 +1058,16 @@ int fp8_blocks(int M, int N, int K, float alpha, const uint8_t* A, int lda, cons
   return GEMM_OK;
 }
 
-// Where the parts of an experts call's workspace begin, and how large it is.
+// Where the parts of an experts call's workspace begin, and how large it is.  y is held in
+// fp32 where all of it takes kExpertsY32 at most (half of L2, from where its sums are then
+// read: 64 tokens of 8 slots of 4096 take 170.0 us, 167.6 with y in bf16; 777 of 2 of 2048
+// 57.3 and 56.9), and in bf16 beyond (16384 of 8 of 4096: 2300 us, 2730 in fp32, 4 GB more through
+// memory), which costs an output 1.4 times the error of its own rounding.
+constexpr size_t kExpertsY32 = 64u << 20;
 struct ExpertsWorkspace {
   size_t xq, xs, hq, hs, y, place, bytes;
   long long ldx, ldxs, ldh, ldhs, ldy;   // codes and y in elements: rows of whole 16-byte vectors
+  bool y_bf16;
 };
 ExpertsWorkspace experts_ws(int tokens, int top_k, int hidden, int width) {
   auto up = [](size_t v, size_t to) { return (v + to - 1) / to * to; };
@@ -1078,7 +1084,11 @@ ExpertsWorkspace experts_ws(int tokens, int top_k, int hidden, int width) {
   w.hq = up(w.xs + slots * w.ldxs * 4, 256);
   w.hs = up(w.hq + slots * w.ldh, 256);
   w.y = up(w.hs + slots * w.ldhs * 4, 256);
-  w.place = up(w.y + slots * w.ldy * 2, 256);
+  const size_t y32 = slots * w.ldy * 4;
+  w.y_bf16 = y32 > kExpertsY32;
+  // never less for more tokens: a workspace of the largest call takes the smaller ones
+  const size_t y16 = y32 / 2 > kExpertsY32 ? y32 / 2 : kExpertsY32;
+  w.place = up(w.y + (w.y_bf16 ? y16 : y32), 256);
   w.bytes = up(w.place + slots * 4, 256);
   return w;
 }
@@ -1152,7 +1162,7 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
   d.A = a.hq; d.lda = ws.ldh; d.a_rows = d.rows; d.sa = a.hs; d.ldsa = ws.ldhs;
   d.B = w->down; d.ldb = w->ld_down; d.b_stride = sd;
   d.sb = w->down_scale; d.ldsb = hblocks; d.sb_stride = (long long)hblocks * fblocks;
-  d.C = base + ws.y; d.ldc = ws.ldy; d.out_bf16 = true; d.alpha = 1.f;
+  d.C = base + ws.y; d.ldc = ws.ldy; d.out_bf16 = ws.y_bf16; d.alpha = 1.f;
   BlocksPlan plan_up, plan_down;
   if (fast && ((rc = blocks_plan(a, dev, &plan_up)) != GEMM_OK || (rc = blocks_plan(d, dev, &plan_down)) != GEMM_OK))
     return rc;
@@ -1187,7 +1197,7 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
 
   CombineArgs c;
   c.tokens = tokens; c.top_k = top_k; c.cols = H;
-  c.y = d.C; c.ldy = ws.ldy; c.weights = weights; c.out = O; c.ldo = ldo;
+  c.y = d.C; c.y_bf16 = d.out_bf16; c.ldy = ws.ldy; c.weights = weights; c.out = O; c.ldo = ldo;
   c.vec = aligned16(O) && ldo % 8 == 0;
   err = launch_experts_combine(c, stream);
   if (err != cudaSuccess)

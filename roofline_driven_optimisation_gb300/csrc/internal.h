@@ -382,7 +382,8 @@ int launch_blocks_generic(const BlocksArgs& a, cudaStream_t s);
 // O[t] = sum over j of weights[t][j] * Y[t * top_k + j]
 struct CombineArgs {
   int tokens, top_k, cols;
-  const void* y;                // bf16, cols values a row, ldy apart
+  const void* y;                // bf16 or fp32, cols values a row, ldy apart
+  bool y_bf16;
   long long ldy;
   const float* weights;
   void* out;
