@@ -562,7 +562,8 @@ int gemm_fp8_quantise_f32(int rows, int cols, const float* X, long long ldx, uin
  * times their scales, at any M; C is bf16 or fp32 and rounded once.  The fast path
  * (tcgen05 kind::f8f6f4) needs 16-byte-aligned A and B with lda and ldb multiples of
  * 16; anything else runs a generic kernel.  Small M (a decode step) splits K over
- * clusters.  Conventions, errors and asynchrony are those of gemm_fp8.
+ * clusters.  N and K are at most 2^31 - 256.  Conventions, errors and asynchrony are
+ * those of gemm_fp8.
  */
 int gemm_fp8_blocks(int M, int N, int K, float alpha, const uint8_t* A, int lda, const float* a_scale, int ldsa,
                     const uint8_t* B, int ldb, const float* b_scale, int ldsb, float beta, gemm_bf16_t* C, int ldc,

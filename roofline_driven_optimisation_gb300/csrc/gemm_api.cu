@@ -1031,6 +1031,8 @@ int fp8_blocks(int M, int N, int K, float alpha, const uint8_t* A, int lda, cons
   if (lda < (K > 1 ? K : 1) || ldb < (N > 1 ? N : 1) || ldc < (N > 1 ? N : 1) || ldsa < kblocks || ldsb < nblocks)
     return fail(GEMM_ERR_INVALID_ARG, "leading dimension too small (lda=%d ldb=%d ldc=%d, scales %d %d)", lda, ldb, ldc,
                 ldsa, ldsb);
+  if (N > kBlocksMaxCols || K > kBlocksMaxCols)
+    return fail(GEMM_ERR_UNSUPPORTED, "N=%d or K=%d above %d", N, K, kBlocksMaxCols);
   if (M == 0 || N == 0) return GEMM_OK;
   if (C == nullptr) return fail(GEMM_ERR_INVALID_ARG, "C is NULL");
   if (K > 0 && (A == nullptr || B == nullptr || a_scale == nullptr || b_scale == nullptr))

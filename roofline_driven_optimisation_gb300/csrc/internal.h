@@ -359,6 +359,8 @@ struct BlocksArgs {
   int early;
 };
 constexpr int kBlocksK = 128, kBlocksN = 128, kBlocksMaxExperts = 1024;
+// N and K: a tile of 256 columns and a block behind the last still count in 32 bits
+constexpr int kBlocksMaxCols = 0x7fffffff - 255;
 // The tcgen05 kernel: row tiles of nt, K split over clusters of `split` CTAs.  Maps: A
 // with boxes of 128 k x blocks_box_rows(nt, gather) rows; B and B2 3-D with boxes of 128
 // columns x 128 k; 128-byte swizzle.
