@@ -25,6 +25,8 @@ constexpr int QB = 128;            // values of a block along a row
 constexpr int HALF = 16;           // lanes that share 128 values of a row: 8 each
 constexpr int THREADS = 256;
 constexpr int HALVES = THREADS / HALF;
+// n / 128 rounded up, for n up to 2^31 - 1
+__host__ __device__ constexpr int count_blocks(int n) { return n / QB + (n % QB != 0); }
 
 // 8 values from x[0..7], of which `n` exist (0 in the place of the others), as they came:
 // bf16 values take half the registers that way.  (Plain loads here and below: the compiler
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(THREADS, 5) quantise_rows_kernel(const __grid_
     const float other = __shfl_sync(0xffffffffu, s[u], (lane & 1) * HALF);
     if (lane / 2 == u) mine = other;
   }
-  const int blocks = (a.cols + QB - 1) / QB;
+  const int blocks = count_blocks(a.cols);
   const int copies = PLACED ? a.copies : 1;
   for (int j = 0; j < copies; ++j) {
     long long to = row;
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(THREADS) quantise_tiles_kernel(const QuantiseA
 
 template <typename T>
 int launch_type(const QuantiseArgs& a, cudaStream_t s) {
-  const int per_row = (a.cols + QB - 1) / QB;
+  const int per_row = count_blocks(a.cols);
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.stream = s;
@@ -194,7 +196,7 @@ int launch_type(const QuantiseArgs& a, cudaStream_t s) {
     return a.place != nullptr ? cudaLaunchKernelEx(&cfg, quantise_rows_kernel<T, true>, q, groups)
                               : cudaLaunchKernelEx(&cfg, quantise_rows_kernel<T, false>, q, groups);
   }
-  const int tiles = (a.rows + QB - 1) / QB;
+  const int tiles = count_blocks(a.rows);
   cfg.gridDim = dim3((unsigned)per_row, (unsigned)(tiles < 65535 ? tiles : 65535), 1);
   return cudaLaunchKernelEx(&cfg, quantise_tiles_kernel<T>, a);
 }
