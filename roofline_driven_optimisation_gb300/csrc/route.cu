@@ -113,9 +113,11 @@ __device__ __forceinline__ float sigmoid_near(float l) { return rcp_near(1.f + e
 // How far apart two choices in 64 bits may be whose fp32 forms are equal, for a score s
 // and a choice c: 128 units of the last place of s cover expf of arguments down to its
 // underflow and the sum of 1024 terms; a sigmoid is off by at most 3 * 2^-24; and the
-// sum with the bias by half a unit of c.
+// sum with the bias by half a unit of c.  Denormal numbers are whole steps of 2^-149, of which
+// a score of softmax is off by four at most (exp by two, its product with 1/sum by a half,
+// what that is off by the rest): 2^-140 is 512 of them.  A sigmoid below 2^-126 may come as 0.
 __device__ __forceinline__ float slack(bool softmax, float s, float c) {
-  const float of_s = softmax ? 0x1p-16f * s : fminf(0x1p-16f * s, 0x1p-20f);
+  const float of_s = softmax ? 0x1p-16f * s + 0x1p-140f : fminf(0x1p-16f * s, 0x1p-20f) + 0x1p-125f;
   return of_s + 0x1p-22f * fabsf(c);
 }
 
