@@ -436,7 +436,13 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const float 
     const float out = __shfl_sync(kFull, mine, __ffs(__ballot_sync(kFull, lane < G && ahead == a.top_groups)) - 1);
     // two softmax scores are at most 1 together, and relative to themselves without a bias
     const float s = a.softmax ? (a.bias != nullptr ? 1.f : fabsf(in)) : 2.f;
-    if (!(in - out > slack(a.softmax, s, fmaxf(fabsf(in), fabsf(out))) * 2.f) && in != -INFINITY) *close = true;
+    bool sure;
+    if (out == -INFINITY)      // such groups are behind all others and by index, but for sums of finite
+                               // choices that fp32 does not hold
+      sure = !__any_sync(kFull, g == -INFINITY && a.group_best == 2 && S > 1 && b2 > -INFINITY && lane / per < G);
+    else
+      sure = in - out > slack(a.softmax, s, fmaxf(fabsf(in), fabsf(out))) * 2.f;
+    if (!sure) *close = true;
   }
   return kept;
 }
