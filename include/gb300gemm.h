@@ -508,7 +508,7 @@ typedef enum {
  *     ids[t][j]: the expert,   weights[t][j] = s * scale, fp32
  *
  * s divided by the sum of the token's top_k scores first if renormalise != 0 (0 if
- * that sum is 0).  NaN logits count as -inf.  Softmax: where some of a row are +inf,
+ * that sum is 0); what is below 2^-126 may come as 0.  NaN logits count as -inf.  Softmax: where some of a row are +inf,
  * they alone have scores, equal ones; a row that is all -inf has scores of 0.  A bias
  * of -inf, +inf or NaN makes an expert come last.
  *

@@ -569,7 +569,12 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, long long t, con
   if (__any_sync(kFull, mine && !(w > 0x1p-100f)) && mine) w = score_of<float>(a.softmax, lw, m, sum);
   if (a.renormalise) {
     const float all = warp_sum(w);
-    w = all > 0x1p-100f ? w * rcp_near(all) : all > 0.f ? w / all : 0.f;
+    if (all > 0x1p-100f) {
+      w *= rcp_near(all);
+    } else {                             // scores that fp32 holds in a few bits or not at all
+      const double v = mine ? score_64(a.softmax, lw, m, (double)sum) : 0.0, total = warp_sum(v);
+      w = total > 0.0 ? (float)(v / total) : 0.f;
+    }
   }
   if (mine) {
     a.ids[t * a.top_k + lane] = id;
