@@ -508,9 +508,9 @@ typedef enum {
  *     ids[t][j]: the expert,   weights[t][j] = s * scale, fp32
  *
  * s divided by the sum of the token's top_k scores first if renormalise != 0 (0 if
- * that sum is 0); what is below 2^-126 may come as 0.  NaN logits count as -inf.  Softmax: where some of a row are +inf,
- * they alone have scores, equal ones; a row that is all -inf has scores of 0.  A bias
- * of -inf, +inf or NaN makes an expert come last.
+ * that sum is 0); what is below 2^-126 may come as 0.  NaN logits count as -inf.
+ * Softmax: where some of a row are +inf, they alone have scores, equal ones; a row that
+ * is all -inf has scores of 0.  A bias of -inf, +inf or NaN makes an expert come last.
  *
  * offsets and order (both or neither NULL) receive the slots t * top_k + j by expert:
  * expert e's are order[offsets[e]] .. order[offsets[e+1] - 1], in ascending order.
@@ -606,9 +606,10 @@ typedef struct {
  * generic kernels.  At most 1024 experts.
  *
  * offsets must ascend from 0 to tokens * top_k and order hold every slot once.  An
- * expert's range that does not fit the call is taken as empty and a slot number outside
- * it is skipped, both reported by gemm_device_status(); rows of O that such slots belong
- * to hold anything then.  O may not overlap X.  workspace: gemm_experts_workspace() bytes
+ * expert's range that does not fit the call is taken as empty, a slot number outside
+ * it is skipped, and slots before the first range or behind the last have no product, all
+ * reported by gemm_device_status(); rows of O that such slots belong to hold anything
+ * then.  O may not overlap X.  workspace: gemm_experts_workspace() bytes
  * of DEVICE memory, 16-byte aligned, of any contents, owned by one call at a time.
  * Asynchronous, no allocation, deterministic.  A call makes four or five launches; if a
  * later one fails, the earlier ones have been queued and O is not written.  Forced paths

@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(256) blocks_generic_kernel(const BlocksArgs a)
   const int kblocks = (a.K + kBlocksK - 1) / kBlocksK;
   // row tiles of all experts in a line; this block takes every gridDim.y-th
   long long tile = blockIdx.y, first = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && uncovered_rows(a)) report_status(a.status, 1, kSiteExperts);
   for (int e = 0; e < a.experts; ++e) {
     int begin, count;
     expert_rows(a, e, begin, count);

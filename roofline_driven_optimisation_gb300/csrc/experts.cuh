@@ -29,6 +29,11 @@ __device__ __forceinline__ void expert_rows(const BlocksArgs& a, int e, int& beg
   }
 }
 
+// Rows that no range covers: nothing multiplies them, so one block says so.
+__device__ __forceinline__ bool uncovered_rows(const BlocksArgs& a) {
+  return a.offsets != nullptr && (a.offsets[0] != 0 || a.offsets[a.experts] != a.rows);
+}
+
 // Row p: `from` A's row (-1: none, taken as zeros), `to` C's row (-1: not stored).
 __device__ __forceinline__ void expert_row(const BlocksArgs& a, int p, int& from, int& to) {
   from = to = p;
@@ -69,6 +74,7 @@ constexpr int kListBytes = (3 * kBlocksMaxExperts + 4) * 4;
 template <int NT>
 __device__ __forceinline__ void list_row_tiles(const BlocksArgs& a, int* pre, int* beg, int* num, int lane) {
   long long run = 0;
+  const bool uncovered = blockIdx.x == 0 && lane == 0 && uncovered_rows(a);
   for (int e0 = 0; e0 < a.experts; e0 += 32) {
     const int e = e0 + lane;
     int b = 0, n = 0;
@@ -89,7 +95,7 @@ __device__ __forceinline__ void list_row_tiles(const BlocksArgs& a, int* pre, in
   }
   if (lane == 0) {
     const bool fits = run <= blocks_row_tiles(a.rows, a.experts, NT);
-    if (!fits) report_status(a.status, 1, kSiteExperts);
+    if (!fits || uncovered) report_status(a.status, 1, kSiteExperts);
     pre[a.experts] = fits ? (int)run : 0;
   }
 }
@@ -99,6 +105,7 @@ __device__ __forceinline__ void list_row_tiles(const BlocksArgs& a, int* pre, in
 template <int NT>
 __device__ __forceinline__ void find_item(const BlocksArgs& a, int tiles_n, long long it, int* out, int lane) {
   long long run = 0;                                   // items of the experts before
+  const bool uncovered = blockIdx.x == 0 && lane == 0 && uncovered_rows(a);
   if (lane == 0) out[2] = 0;
   __syncwarp();
   for (int e0 = 0; e0 < a.experts; e0 += 32) {
@@ -123,6 +130,7 @@ __device__ __forceinline__ void find_item(const BlocksArgs& a, int tiles_n, long
     run += __shfl_sync(0xffffffffu, s, 31);
     if (it < run) break;
   }
+  if (uncovered) report_status(a.status, 1, kSiteExperts);
 }
 
 // ---------------------------------------------------------------- two sums in one instruction
