@@ -599,11 +599,11 @@ typedef struct {
  *     O[t] = sum over j of token_weights[t][j] * y[expert of slot t*top_k + j]
  *
  * X is quantised once in rows of 128-blocks (gemm_fp8_quantise_bf16), the products are
- * those of gemm_fp8_blocks, h is quantised the same way from its fp32 values, and the sum
- * is rounded to bf16 once.  y is held in fp32, but in bf16 in calls whose y would take more
- * than 64 MB (tokens * top_k * hidden * 4 bytes).  The fast path needs 16-byte-aligned
- * weights with leading dimensions and strides that are multiples of 16; others run
- * generic kernels.  At most 1024 experts.
+ * those of gemm_fp8_blocks, h is quantised the same way from its fp32 values (silu may
+ * come as 0 below -87.3), and the sum is rounded to bf16 once.  y is held in fp32, but in
+ * bf16 in calls whose y would take more than 64 MB (tokens * top_k * hidden * 4 bytes).
+ * The fast path needs 16-byte-aligned weights with leading dimensions and strides that
+ * are multiples of 16; others run generic kernels.  At most 1024 experts.
  *
  * offsets must ascend from 0 to tokens * top_k and order hold every slot once.  An
  * expert's range that does not fit the call is taken as empty, a slot number outside

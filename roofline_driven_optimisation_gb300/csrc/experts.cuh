@@ -161,11 +161,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t both(float v) { return pack2(__float_as_uint(v), __float_as_uint(v)); }
 
 // silu(gate) * up, twice.  exp(-g) as 2^-p * (1 + r ln 2), p the rounded g * log2(e) and r what
-// that rounding left out, so that the approximate operations leave silu within 4 units of
-// its last place: eight instructions in two values' place, and ex2 and rcp for each, where
-// expf and a division take forty a value (an epilogue of 128 x 256 products: 7.1 us with
-// those, 4.5 one value at a time).  Below -87.4 silu is 0 (it is less than 2^-119 there; of
-// -inf it is NaN), and g is held to 88 in the exponent alone.
+// that rounding left out, so that only the approximate operations and five roundings are left:
+// silu is off by at most 5.6 * 2^-24 of itself (of every fp32 gate; expf and a division: 4.2),
+// eight instructions in two values' place, and ex2 and rcp for each, where those take forty a
+// value (an epilogue of 128 x 256 products: 7.1 us with those, 4.5 one value at a time).  From
+// -87.34 down 1/(1 + e^-g) is below 2^-126 and silu 0 (it is less than 2^-119 there; of -inf it
+// is NaN), and g is held to 88 in the exponent alone.
 __device__ __forceinline__ uint64_t swiglu_near2(uint64_t g, uint64_t u) {
   constexpr float kLog2e = 1.4426950408889634f, kLog2eRest = 1.925963033500e-08f, kLn2 = 0.6931471805599453f;
   uint64_t c = pack2(__float_as_uint(fminf(fmaxf(part2(g, 0), -88.f), 88.f)),
