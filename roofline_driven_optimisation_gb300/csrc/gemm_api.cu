@@ -934,7 +934,7 @@ int route(int tokens, int experts, int top_k, const void* logits, bool bf16, lon
   a.counts = need > 0 ? static_cast<int*>(workspace) : nullptr;   // few tokens: none
   a.choices = bias != nullptr || groups > 1;
   a.vec = aligned16(logits) && ((size_t)ld * (bf16 ? 2 : 4)) % 16 == 0;
-  const int err = launch_route(a, stream);
+  const int err = launch_route(a, dev->num_sms, stream);
   if (err != cudaSuccess)
     return fail(GEMM_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString((cudaError_t)err));
   t_last_path = GEMM_PATH_ROUTE;

@@ -304,7 +304,7 @@ constexpr int route_experts_per_lane(int experts) {
   return per;
 }
 size_t route_ws_bytes(int tokens, int experts);
-int launch_route(const RouteArgs& a, cudaStream_t s);
+int launch_route(const RouteArgs& a, int num_sms, cudaStream_t s);
 
 // E4M3 codes with a scale for each block of block_rows (1 or 128) x 128 values.
 struct QuantiseArgs {

@@ -263,5 +263,34 @@ inline BlocksChoice blocks_choice(long long rows, int experts, int N, int kblock
   return c;
 }
 
+// Routing: warps a block, blocks and tokens a block.  A token is some 800 instructions of a
+// warp, so that 32 warps of one SM take 3 us for a token each: one block alone (which saves the
+// second launch, 2 us) for a token a warp of 16 at most, then blocks of 8 warps on as many
+// SMs as there are tokens for, and blocks of 32 warps (8 for more than 256 experts, whose
+// registers allow no more) once every SM has one: such a block fills an SM, so there is never a
+// block more than SMs.  Nor more than kRouteMaxBlocks, a GB300's SMs, for which a workspace is
+// measured without asking the device (fewer SMs never need more).
+constexpr int kRouteMaxBlocks = 152;
+struct RoutePlan {
+  int warps, blocks, chunk;
+  bool few;              // slots that one block orders as soon as many would
+};
+inline RoutePlan route_plan(int tokens, int experts, int num_sms) {
+  const int most = num_sms < 1 ? 1 : num_sms < kRouteMaxBlocks ? num_sms : kRouteMaxBlocks;
+  RoutePlan p;
+  p.few = tokens <= 256;
+  p.warps = tokens <= 8 ? 8 : tokens <= 16 && experts <= 256 ? 16 : tokens <= 8 * most || experts > 256 ? 8 : 32;
+  if (tokens <= p.warps) {
+    p.blocks = 1;
+    p.chunk = tokens;
+    return p;
+  }
+  const long long want = ((long long)tokens + p.warps - 1) / p.warps;
+  const int blocks = want < most ? (int)want : most;
+  p.chunk = (tokens + blocks - 1) / blocks;
+  p.blocks = (tokens + p.chunk - 1) / p.chunk;
+  return p;
+}
+
 }  // namespace plan
 }  // namespace g3

@@ -31,6 +31,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "plan.h"
 #include "ptx.cuh"
 
 namespace g3 {
@@ -823,35 +824,9 @@ __global__ void __launch_bounds__(kPlaceKernelThreads) route_order_kernel(const 
   place_slots(a, 0, slots, total, at);
 }
 
-// Warps a block, blocks and tokens a block.  A token is some 800 instructions of a warp, so
-// that 32 warps of one SM take 3 us for a token each: one block alone (which saves the
-// second launch, 2 us) for a token a warp of 16 at most, then blocks of 8 warps on as many
-// SMs as there are tokens for, and blocks of 32 warps (8 for more than 256 experts, whose
-// registers allow no more) once all of a GB300's 152 SMs have one.
-constexpr int kRouteMaxBlocks = 152;
-struct RoutePlan {
-  int warps, blocks, chunk;
-  bool few;              // slots that one block orders as soon as many would
-};
-RoutePlan plan_route(int tokens, int experts) {
-  RoutePlan p;
-  p.few = tokens <= 256;
-  p.warps = tokens <= 8 ? 8 : tokens <= 16 && experts <= 256 ? 16 : tokens <= 8 * kRouteMaxBlocks || experts > 256 ? 8 : 32;
-  if (tokens <= p.warps) {
-    p.blocks = 1;
-    p.chunk = tokens;
-    return p;
-  }
-  const long long want = ((long long)tokens + p.warps - 1) / p.warps;
-  const int blocks = want < kRouteMaxBlocks ? (int)want : kRouteMaxBlocks;
-  p.chunk = (tokens + blocks - 1) / blocks;
-  p.blocks = (tokens + p.chunk - 1) / p.chunk;
-  return p;
-}
-
 template <typename T, int PER>
-int launch_impl(const RouteArgs& a, cudaStream_t s) {
-  const RoutePlan p = plan_route(a.tokens, a.experts);
+int launch_impl(const RouteArgs& a, int num_sms, cudaStream_t s) {
+  const plan::RoutePlan p = plan::route_plan(a.tokens, a.experts, num_sms);
   const int threads = p.warps * 32;
   const size_t smem = (size_t)route_smem_choices(a, p.warps) * sizeof(double) +
                       (size_t)a.experts * (1 + kPlaceWarps) * sizeof(int);
@@ -883,26 +858,26 @@ int launch_impl(const RouteArgs& a, cudaStream_t s) {
 }
 
 template <typename T>
-int launch_type(const RouteArgs& a, cudaStream_t s) {
+int launch_type(const RouteArgs& a, int num_sms, cudaStream_t s) {
   switch (route_experts_per_lane(a.experts)) {
-    case 1: return launch_impl<T, 1>(a, s);
-    case 2: return launch_impl<T, 2>(a, s);
-    case 4: return launch_impl<T, 4>(a, s);
-    case 8: return launch_impl<T, 8>(a, s);
-    case 16: return launch_impl<T, 16>(a, s);
+    case 1: return launch_impl<T, 1>(a, num_sms, s);
+    case 2: return launch_impl<T, 2>(a, num_sms, s);
+    case 4: return launch_impl<T, 4>(a, num_sms, s);
+    case 8: return launch_impl<T, 8>(a, num_sms, s);
+    case 16: return launch_impl<T, 16>(a, num_sms, s);
   }
-  return launch_impl<T, 32>(a, s);
+  return launch_impl<T, 32>(a, num_sms, s);
 }
 
 }  // namespace
 
 size_t route_ws_bytes(int tokens, int experts) {
-  const RoutePlan p = plan_route(tokens, experts);
+  const plan::RoutePlan p = plan::route_plan(tokens, experts, plan::kRouteMaxBlocks);
   return p.blocks > 1 && !p.few ? (size_t)p.blocks * count_stride(experts) * sizeof(int) : 0;
 }
 
-int launch_route(const RouteArgs& a, cudaStream_t s) {
-  return a.bf16 ? launch_type<__nv_bfloat16>(a, s) : launch_type<float>(a, s);
+int launch_route(const RouteArgs& a, int num_sms, cudaStream_t s) {
+  return a.bf16 ? launch_type<__nv_bfloat16>(a, num_sms, s) : launch_type<float>(a, num_sms, s);
 }
 
 }  // namespace g3
