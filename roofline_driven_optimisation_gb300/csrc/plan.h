@@ -287,8 +287,8 @@ inline RoutePlan route_plan(int tokens, int experts, int num_sms) {
   }
   const long long want = ((long long)tokens + p.warps - 1) / p.warps;
   const int blocks = want < most ? (int)want : most;
-  p.chunk = (tokens + blocks - 1) / blocks;
-  p.blocks = (tokens + p.chunk - 1) / p.chunk;
+  p.chunk = (int)(((long long)tokens + blocks - 1) / blocks);
+  p.blocks = (int)(((long long)tokens + p.chunk - 1) / p.chunk);
   return p;
 }
 

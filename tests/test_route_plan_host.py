@@ -39,7 +39,7 @@ def test_plans(plan):
 
 def test_every_token_has_a_block(plan):
     rng = random.Random(0)
-    tokens = [int(2 ** rng.uniform(0, 30)) for _ in range(3000)]
+    tokens = [int(2 ** rng.uniform(0, 31)) for _ in range(3000)] + [2 ** 31 - d for d in range(1, 200)]
     queries = [(max(1, t), rng.choice([1, 60, 256, 257, 1024]), rng.choice([1, 2, 20, 76, 132, 148, 152, 160])) for t in tokens]
     whole = plan([(t, e, 152) for t, e, _ in queries])
     for (t, e, sms), (warps, blocks, chunk, few), (_, most, _, _) in zip(queries, plan(queries), whole):
