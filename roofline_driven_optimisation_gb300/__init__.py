@@ -805,6 +805,13 @@ def _blocks(n: int) -> int:
     return -(-n // 128)
 
 
+_INT_MAX = 0x7fffffff          # ctypes takes a larger number's last 32 bits without a word
+
+
+def _too_large(*sizes):
+    raise ValueError(f"sizes and leading dimensions {sizes}: {_INT_MAX} at most")
+
+
 def _one_device(*tensors) -> int:
     """The index of the GPU that all tensors (or None) are on."""
     index = tensors[0].get_device()
@@ -829,6 +836,8 @@ def route(logits, ids, weights, offsets=None, order=None, bias=None, score: int 
         _torch()
     tokens, experts = logits.shape
     top_k = ids.shape[-1]
+    if tokens > _INT_MAX or experts > _INT_MAX or top_k > _INT_MAX:
+        _too_large(tokens, experts, top_k)
     lib = _lib or load()
     index = _one_device(logits, ids, weights, offsets, order, bias, workspace)
     kind = logits.dtype
@@ -870,6 +879,8 @@ def fp8_quantise(X, codes, scales, block_rows: int = 1, stream=None):
     if _t is None:
         _torch()
     rows, cols = X.shape
+    if rows > _INT_MAX or cols > _INT_MAX:
+        _too_large(rows, cols)
     lib = _lib or load()
     kind = X.dtype
     if kind is _bf16:
@@ -902,6 +913,8 @@ def fp8_blocks(A, a_scale, B, b_scale, C, alpha: float = 1.0, beta: float = 0.0,
     K2, N = B.shape
     if K2 != K or C.shape != (M, N):
         raise ValueError(f"shape mismatch {tuple(A.shape)} @ {tuple(B.shape)} -> {tuple(C.shape)}")
+    if M > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+        _too_large(M, N, K)
     lib = _lib or load()
     kind = C.dtype
     if kind is _bf16:
@@ -918,10 +931,11 @@ def fp8_blocks(A, a_scale, B, b_scale, C, alpha: float = 1.0, beta: float = 0.0,
     lda = K if A.dtype is _e4m3 and A.is_contiguous() else _codes(A, "A", M, K)
     ldb = N if B.dtype is _e4m3 and B.is_contiguous() else _codes(B, "B", K, N)
     ldc = N if C.is_contiguous() else _rows(C, "C", M, N)
-    rc = fn(M, N, K, alpha, A.data_ptr(), lda or 1, a_scale.data_ptr(), _scales(a_scale, "a_scale", M, kb),
-            B.data_ptr(), ldb or 1, b_scale.data_ptr(), _scales(b_scale, "b_scale", kb, -(-N // 128)), beta,
-            C.data_ptr(), ldc or 1,
-            _raw_stream(index) if stream is None else stream)
+    ldsa, ldsb = _scales(a_scale, "a_scale", M, kb), _scales(b_scale, "b_scale", kb, -(-N // 128))
+    if lda > _INT_MAX or ldb > _INT_MAX or ldc > _INT_MAX or ldsa > _INT_MAX or ldsb > _INT_MAX:
+        _too_large(lda, ldb, ldc, ldsa, ldsb)
+    rc = fn(M, N, K, alpha, A.data_ptr(), lda or 1, a_scale.data_ptr(), ldsa, B.data_ptr(), ldb or 1,
+            b_scale.data_ptr(), ldsb, beta, C.data_ptr(), ldc or 1, _raw_stream(index) if stream is None else stream)
     if rc:
         _check(rc)
     return C
@@ -941,6 +955,8 @@ class ExpertWeights:
             if t.dim() != 3 or t.dtype not in (_t.float8_e4m3fn, _t.uint8) or t.shape[2] > 1 and t.stride(2) != 1:
                 raise TypeError(f"{name}: 3-D tensor of E4M3 codes (float8_e4m3fn or uint8) with contiguous columns")
         experts, hidden, width = gate.shape
+        if max(gate.shape) > _INT_MAX:
+            _too_large(*gate.shape)
         if up.shape != gate.shape or up.stride() != gate.stride() or down.shape != (experts, width, hidden):
             raise ValueError("gate and up have one shape and one set of strides, down the transposed shape")
         for t in (gate, down):
@@ -970,6 +986,8 @@ def experts(weights: ExpertWeights, X, offsets, order, token_weights, O, workspa
     if _t is None:
         _torch()
     tokens, top_k = token_weights.shape
+    if tokens > _INT_MAX or top_k > _INT_MAX:
+        _too_large(tokens, top_k)
     hidden = weights.hidden
     if X.dtype is not _bf16 or O.dtype is not _bf16:
         raise TypeError("X and O are bf16 tensors")
