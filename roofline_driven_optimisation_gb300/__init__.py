@@ -812,6 +812,13 @@ def _too_large(*sizes):
     raise ValueError(f"sizes and leading dimensions {sizes}: {_INT_MAX} at most")
 
 
+def _space(workspace):
+    """Address and bytes of a caller's workspace."""
+    if workspace.dtype is not _u8 or not workspace.is_contiguous():
+        raise TypeError("workspace is a contiguous uint8 tensor")
+    return workspace.data_ptr(), workspace.numel()
+
+
 def _one_device(*tensors) -> int:
     """The index of the GPU that all tensors (or None) are on."""
     index = tensors[0].get_device()
@@ -855,7 +862,7 @@ def route(logits, ids, weights, offsets=None, order=None, bias=None, score: int 
     st = _raw_stream(index) if stream is None else stream
     space = size = 0
     if workspace is not None:
-        space, size = workspace.data_ptr(), workspace.numel()
+        space, size = _space(workspace)
     elif order is not None:
         size = lib.gemm_route_workspace(tokens, experts)
         if size:
@@ -999,7 +1006,7 @@ def experts(weights: ExpertWeights, X, offsets, order, token_weights, O, workspa
     lib = _lib or load()
     space = size = 0
     if workspace is not None:
-        space, size = workspace.data_ptr(), workspace.numel()
+        space, size = _space(workspace)
     elif tokens:
         size = lib.gemm_experts_workspace(tokens, top_k, hidden, weights.width)
         workspace = _scratch(size, weights.device, st)

@@ -1,5 +1,5 @@
-"""Sizes that do not fit the C ABI's integers: the routed experts' binding refuses them (ctypes
-would pass a number's last 32 bits)."""
+"""Sizes that do not fit the C ABI's integers, and workspaces whose elements are not their bytes:
+the routed experts' binding refuses them (ctypes would pass a number's last 32 bits)."""
 import os
 import shutil
 
@@ -99,3 +99,16 @@ def test_experts(g):
     for tokens, top_k in ((BIG, 1), (1, BIG)):
         with pytest.raises(ValueError, match="at most"):
             experts(g, tokens, top_k)
+
+
+def test_workspaces(g):
+    spread = OnGpu(1, dtype=U8)
+    spread.t = spread.t.expand(1 << 20)                       # a byte that looks like many
+    gaps = OnGpu(1 << 21, dtype=U8)
+    gaps.t = gaps.t[::2]
+    for bad in (spread, gaps, OnGpu(1 << 20), OnGpu(1 << 20, dtype=torch.int8)):
+        with pytest.raises(TypeError, match="workspace"):
+            experts(g, workspace=bad)
+        with pytest.raises(TypeError, match="workspace"):
+            g.route(OnGpu(300, 8), OnGpu(300, 2, dtype=I32), OnGpu(300, 2), OnGpu(9, dtype=I32), OnGpu(600, dtype=I32),
+                    workspace=bad)
