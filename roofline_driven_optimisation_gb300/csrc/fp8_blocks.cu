@@ -21,7 +21,7 @@
 // and the eight drain warps wait at a hardware barrier with a signal warp that polls
 // for them.
 //
-// Roles (384 threads, one CTA an SM): warp 0 copies (TMA; the experts' rows of A through
+// Roles (384 threads; one CTA an SM, two where K is split over tiles of 32 rows): warp 0 copies (TMA; the experts' rows of A through
 // tile::gather4, four rows an instruction, so that they are never laid out by expert; the
 // first stages' weights before the rows' numbers are known), warp 1 issues the MMAs,
 // warp 2 multiplies sa with sb for the drain, warp 3 signals, warps 4-11 drain: warp w

@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
         sync_drain();
         const float s = kv_scale_for<kKvE4M3>(fmaxf(top, big[(1 - half) * BM_CTA + lrow]));
         const uint64_t f = both(kv_recip(s));
-        // 64 codes of this thread's row, then rows of 64 bytes (as store_rows)
+        // 64 codes of this thread's row, then rows of 64 bytes (as stage_rows)
         uint8_t* mine = out + (warp - EPI_FIRST) * M::OUT_WARP;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {

@@ -293,7 +293,7 @@ struct RouteArgs {
   float* weights;
   int *offsets, *order;   // null: the order by expert is not wanted
   int* counts;            // workspace: counts by block and expert
-  bool choices;           // a bias or groups: choices are kept in shared memory
+  bool choices;           // a bias or groups: choices are computed, and shared memory has room for a token's in fp64
   bool vec;               // 16-byte-aligned rows
 };
 constexpr int kRouteMaxExperts = 1024, kRouteMaxTopK = 32, kRouteMaxGroups = 32;

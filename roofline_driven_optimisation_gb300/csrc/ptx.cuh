@@ -437,9 +437,12 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-// The same with release order at CTA scope only, for arrivals that hand back tensor
-// memory (tcgen05 fences order that) and publish no other writes: the cluster-scope
-// release waits about 1200 cycles for the thread's earlier accesses.
+// The same with release order at CTA scope only, for arrivals that hand back memory which
+// the warp has only read, by loads whose values are there (tcgen05.wait::ld has returned in
+// every lane, and __syncwarp behind it): what the other CTA writes after it has seen the
+// arrival cannot reach a load that is over, at any scope, and no write of this CTA's is
+// published with it.  A release at cluster scope orders writes too, and waits about 1200
+// cycles for the thread's earlier accesses.
 __device__ __forceinline__ void mbar_arrive_remote_light(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
