@@ -600,8 +600,9 @@ typedef struct {
  *
  * X is quantised once in rows of 128-blocks (gemm_fp8_quantise_bf16), the products are
  * those of gemm_fp8_blocks, h is quantised the same way from its fp32 values (silu may
- * come as 0 below -87.3), and the sum is rounded to bf16 once.  y is held in fp32, but in
- * bf16 in calls whose y would take more than 64 MB (tokens * top_k * hidden * 4 bytes).
+ * come as 0 below -87.3), and the sum is rounded to bf16 once.  y is held in fp32; calls
+ * whose y takes more than 64 MB (tokens * top_k * hidden * 4 bytes) may hold it in fp16
+ * with a power of two for each 128 columns of a row.
  * The fast path needs 16-byte-aligned weights with leading dimensions and strides that
  * are multiples of 16; others run generic kernels.  At most 1024 experts.
  *

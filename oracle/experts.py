@@ -14,6 +14,7 @@ BLOCK = 128
 SOFTMAX, SIGMOID = 0, 1
 U32 = 2.0 ** -24            # half a step of fp32, of fp32 1
 U16 = 2.0 ** -8             # half a step of bf16
+UH = 2.0 ** -11             # half a step of fp16
 
 
 def blocks(n: int) -> int:
@@ -146,9 +147,22 @@ def ffn(x, gate, up, down):
     return v @ down, ev @ np.abs(down) + product_bound(np.abs(v) + ev, down)
 
 
-def experts(x, ids, weights, gate, up, down, y_bf16=True):
+def scaled16_steps(x, gate, up, down):
+    """Half a step of fp16's smallest numbers, 2^-25, times the scale of y's blocks, which is up to
+    2^-13 * 2^25 times the sum over blocks of K of h's scale times down's.  Down's scales are taken
+    from its largest values, as if each block had a code of 448, and twice that."""
+    h = _silu(x @ gate) * (x @ up)
+    k, n = down.shape
+
+    def largest(v, rows):
+        v = np.pad(np.abs(v), [(0, -v.shape[0] % rows), (0, -v.shape[1] % BLOCK)])
+        return v.reshape(-1, rows, v.shape[1] // BLOCK, BLOCK).max((1, 3)) / QMAX[E4M3]
+    return 2.0 ** -12 * spread(largest(h, 1) @ largest(down, BLOCK), 1, len(x), n)
+
+
+def experts(x, ids, weights, gate, up, down, y_half_step=U16):
     """(out, bound) of the experts' FFN: x [tokens][hidden] in bf16's values, weights of
-    each expert as values; y_bf16: each y may be rounded to bf16 besides."""
+    each expert as values; y_half_step: what rounding may take from each y, relative to it."""
     xv = dequantise(*quantise(x), 1)
     ids, w = np.asarray(ids), np.asarray(weights, np.float64)
     out, err = np.zeros(x.shape), np.zeros(x.shape)
@@ -157,7 +171,9 @@ def experts(x, ids, weights, gate, up, down, y_bf16=True):
         if len(t) == 0:
             continue
         y, ey = ffn(xv[t], gate[e], up[e], down[e])
-        ey = ey + (U16 if y_bf16 else U32) * (np.abs(y) + ey)
+        ey = ey + y_half_step * (np.abs(y) + ey)
+        if y_half_step == UH:
+            ey = ey + scaled16_steps(xv[t], gate[e], up[e], down[e])
         np.add.at(out, t, w[t, j][:, None] * y)
         np.add.at(err, t, np.abs(w[t, j])[:, None] * (ey + ids.shape[1] * U32 * np.abs(y)))
     return out, err + U16 * (np.abs(out) + err)

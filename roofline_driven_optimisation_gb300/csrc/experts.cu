@@ -9,9 +9,11 @@
 //
 // with A's and B's codes as they are in S_b, and every sum in fp32.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "epilogue.cuh"
 #include "experts.cuh"
@@ -137,53 +139,57 @@ __global__ void __launch_bounds__(256) blocks_generic_kernel(const BlocksArgs a)
 
 // ---------------------------------------------------------------- weighted sums
 // A block 1024 columns of a token, a thread 8 of them: its top_k rows' parts, 128 bytes in
-// flight, added in order.  Reads top_k * cols values of y a token once: HBM (or L2) bounds it
-// (16384 tokens of 8 slots of 4096 in bf16: 167 us for 1.2 GB, the last of them still in L2;
-// 250 with tokens' columns in one line over the grid).
+// flight, added in order.  y in fp32, or in fp16 times a scale for each 128 columns.  Reads top_k *
+// cols values of y a token once: HBM (or L2) bounds it (16384 tokens of 8 slots of 4096 in 16
+// bits: 189 us for 1.2 GB, the copy rate's 183).
 constexpr int COMBINE_THREADS = 128;
-template <typename T>
-__global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const __grid_constant__ CombineArgs a) {
-  constexpr int WORDS = (int)sizeof(T) / 2, FLIGHT = 8 / WORDS;      // 16-byte vectors of 8 values; rows in flight
+template <bool SCALED>
+__global__ void __launch_bounds__(COMBINE_THREADS, 6) combine_kernel(const __grid_constant__ CombineArgs a) {
+  constexpr int WORDS = SCALED ? 1 : 2, FLIGHT = 8 / WORDS;      // 16-byte vectors of 8 values; rows in flight
+  using T = std::conditional_t<SCALED, __half, float>;
   griddep_wait();
   const long long t = blockIdx.x;
   const int c = (int)(blockIdx.y * COMBINE_THREADS + threadIdx.x) * 8;
   if (c >= a.cols) return;
   const float* w = a.weights + t * a.top_k;
   const T* y = static_cast<const T*>(a.y) + t * a.top_k * a.ldy + c;
+  const float* ys = SCALED ? a.ys + t * a.top_k * a.ldys + c / 128 : nullptr;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + t * a.ldo + c;
-  if (a.vec && c + 8 <= a.cols) {
-    float sum[8];
+  float sum[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sum[q] = 0.f;
-    for (int j0 = 0; j0 < a.top_k; j0 += FLIGHT) {
-      uint4 v[FLIGHT][WORDS];
-      float f[FLIGHT];
+  for (int q = 0; q < 8; ++q) sum[q] = 0.f;
+  for (int j0 = 0; j0 < a.top_k; j0 += FLIGHT) {                 // rows of y are whole vectors
+    uint4 v[FLIGHT][WORDS];
+    float f[FLIGHT], s[FLIGHT];
 #pragma unroll
-      for (int j = 0; j < FLIGHT; ++j) {
-        const bool in = j0 + j < a.top_k;
+    for (int j = 0; j < FLIGHT; ++j) {
+      const bool in = j0 + j < a.top_k;
 #pragma unroll
-        for (int q = 0; q < WORDS; ++q)
-          v[j][q] = in ? reinterpret_cast<const uint4*>(y + (j0 + j) * a.ldy)[q] : make_uint4(0u, 0u, 0u, 0u);
-        f[j] = in ? w[j0 + j] : 0.f;
-      }
+      for (int q = 0; q < WORDS; ++q)
+        v[j][q] = in ? reinterpret_cast<const uint4*>(y + (j0 + j) * a.ldy)[q] : make_uint4(0u, 0u, 0u, 0u);
+      f[j] = in ? w[j0 + j] : 0.f;
+      s[j] = SCALED && in ? ys[(j0 + j) * a.ldys] : 1.f;
+    }
 #pragma unroll
-      for (int j = 0; j < FLIGHT; ++j) {
-        if (j0 + j >= a.top_k) break;
+    for (int j = 0; j < FLIGHT; ++j) {
+      if (j0 + j >= a.top_k) break;
 #pragma unroll
-        for (int q = 0; q < WORDS; ++q) {
-          const uint32_t u[4] = {v[j][q].x, v[j][q].y, v[j][q].z, v[j][q].w};
+      for (int q = 0; q < WORDS; ++q) {
+        const uint32_t u[4] = {v[j][q].x, v[j][q].y, v[j][q].z, v[j][q].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (WORDS == 1) {
-              sum[2 * i] = fmaf(f[j], __uint_as_float(u[i] << 16), sum[2 * i]);
-              sum[2 * i + 1] = fmaf(f[j], __uint_as_float(u[i] & 0xffff0000u), sum[2 * i + 1]);
-            } else {
-              sum[4 * q + i] = fmaf(f[j], __uint_as_float(u[i]), sum[4 * q + i]);
-            }
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (SCALED) {                                // the product with a power of two is exact
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+            sum[2 * i] = fmaf(f[j], x.x * s[j], sum[2 * i]);
+            sum[2 * i + 1] = fmaf(f[j], x.y * s[j], sum[2 * i + 1]);
+          } else {
+            sum[4 * q + i] = fmaf(f[j], __uint_as_float(u[i]), sum[4 * q + i]);
           }
         }
       }
     }
+  }
+  if (a.vec && c + 8 <= a.cols) {
     uint32_t r[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -192,11 +198,9 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const __grid_c
     }
     *reinterpret_cast<uint4*>(o) = make_uint4(r[0], r[1], r[2], r[3]);
   } else {
-    for (int q = 0; q < 8 && c + q < a.cols; ++q) {
-      float s = 0.f;
-      for (int j = 0; j < a.top_k; ++j) s = fmaf(w[j], (float)y[j * a.ldy + q], s);
-      o[q] = __float2bfloat16_rn(s);
-    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (c + q < a.cols) o[q] = __float2bfloat16_rn(sum[q]);
   }
 }
 
@@ -224,7 +228,7 @@ int launch_experts_combine(const CombineArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return a.y_bf16 ? cudaLaunchKernelEx(&cfg, combine_kernel<__nv_bfloat16>, a) : cudaLaunchKernelEx(&cfg, combine_kernel<float>, a);
+  return a.ys != nullptr ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, a) : cudaLaunchKernelEx(&cfg, combine_kernel<false>, a);
 }
 
 }  // namespace g3

@@ -38,6 +38,7 @@
 // half.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -62,12 +63,15 @@ constexpr int TMEM_COLS = 512, COLS = 256, NBUF = 2;
 constexpr int RING = 2, RING_BLOCKS = 4, RING_WORDS = RING_BLOCKS * (BM_CTA + 2);
 constexpr int BOX = 64;
 constexpr int BAR_BYTES = 512;
+// What C holds: fp32, bf16, or fp16 times a power of two for each 128 columns of a row (the
+// experts' y in large calls).
+constexpr int kF32 = 0, kBf16 = 1, kScaled16 = 2;
 // Shared memory: the ring of operands, and for each drain warp the rows it is about to
 // store (32 rows of 128 bytes of C, or of 64 codes).
-template <bool SW, bool OUT_BF16>
+template <bool SW, bool OUT_16>
 struct Mem {
-  // rows of C in bf16 are stored by four warps of their own, while the next item is multiplied
-  static constexpr bool STORERS = !SW && OUT_BF16;
+  // rows of C of 16 bits are stored by four warps of their own, while the next item is multiplied
+  static constexpr bool STORERS = !SW && OUT_16;
   static constexpr int THREADS = STORERS ? 512 : 384;
   // registers: 128 threads with few and 256 with many of 384 x 168, or 256 and 256 of 512 x 128
   static constexpr int FEW = STORERS ? 48 : 88, MANY = 208, LAUNCH = STORERS ? 128 : 168;
@@ -174,21 +178,36 @@ __device__ __forceinline__ void store32(const Params& p, long long m, int n, con
   }
 }
 
-// Rows of 128 bytes (64 bf16 or 32 fp32 columns) of a warp's 32 rows of C, by way of shared
+// A power of two that takes the sums of a row's 128 columns into fp16.  `scales` is the sum of
+// |sa * sb| over the blocks of K; a block's products come to 128 * 448 * 448 < 2^25 at most, so
+// with the bound 2^25 * scales below 2^15 none is past 65504, and all down to 2^-29 of that bound
+// keep 11 bits (random codes of three in four bits come to 2^-10 of it).  No look at the sums
+// is taken: their largest, found in registers, cost 0.9 us an item.  2^113 at most, which takes
+// any fp32 number, and 2^-112 at least, so that both it and its reciprocal are normal numbers.
+__device__ __forceinline__ float scale_for(float scales) {
+  const int e = (int)(__float_as_uint(scales) >> 23 & 255) + 25 - 14;
+  return __uint_as_float((uint32_t)min(max(e, 127 - 112), 127 + 113) << 23);
+}
+
+// Rows of 128 bytes (64 columns of 16 bits or 32 of fp32) of a warp's 32 rows of C, by way of shared
 // memory: a thread has a row, and 32 threads writing 16 bytes each of 32 rows take 32
 // wavefronts where four whole rows of 128 bytes take four.  The 16-byte vectors of a row
 // are permuted by the row's number, so neither side meets a bank twice.
-template <bool OUT_BF16>
+template <int KIND>
 __device__ __forceinline__ void stage_rows(float alpha, uint8_t* out, const uint64_t* v, int lane) {
   const uint64_t f = both(alpha);
+  constexpr bool WORD = KIND == kF32;                  // a value fills one
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint64_t x = mul2(v[OUT_BF16 ? q * 4 + i : q * 2 + i / 2], f);
-      if constexpr (OUT_BF16) {
+      const uint64_t x = mul2(v[WORD ? q * 2 + i / 2 : q * 4 + i], f);
+      if constexpr (KIND == kBf16) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(part2(x, 0), part2(x, 1));
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      } else if constexpr (KIND == kScaled16) {
+        const __half2 b = __floats2half2_rn(part2(x, 0), part2(x, 1));
         w[i] = *reinterpret_cast<const uint32_t*>(&b);
       } else {
         w[i] = __float_as_uint(part2(x, i & 1));
@@ -197,30 +216,30 @@ __device__ __forceinline__ void stage_rows(float alpha, uint8_t* out, const uint
     *reinterpret_cast<uint4*>(out + lane * 128 + ((q ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-// The rows, from column n.  to: this lane's row of C, or -1.
-template <bool OUT_BF16>
-__device__ __forceinline__ void send_rows(const Params& p, const uint8_t* out, int to, int n, int lane) {
+// The rows, from column n, up to column `end`.  to: this lane's row of C, or -1.
+template <int KIND>
+__device__ __forceinline__ void send_rows(const Params& p, const uint8_t* out, int to, int n, int end, int lane) {
   const BlocksArgs& a = p.a;
-  constexpr int PER = OUT_BF16 ? 8 : 4;                // columns of a vector
+  constexpr int PER = KIND == kF32 ? 4 : 8;            // columns of a vector
   uint8_t* C = static_cast<uint8_t*>(a.C);
   const int c = lane & 7;
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     const int row = q * 4 + lane / 8;
     const long long o = __shfl_sync(0xffffffffu, to, row);
-    if (o >= 0 && n + c * PER < a.N)
-      *reinterpret_cast<uint4*>(C + (o * a.ldc + n) * (OUT_BF16 ? 2 : 4) + c * 16) =
+    if (o >= 0 && n + c * PER < end)
+      *reinterpret_cast<uint4*>(C + (o * a.ldc + n) * (16 / PER) + c * 16) =
           *reinterpret_cast<const uint4*>(out + row * 128 + ((c ^ (row & 7)) * 16));
   }
 }
 
-// SW: gate and up weights, codes out.
-template <bool SW, bool OUT_BF16>
-__global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
+// SW: gate and up weights, codes out.  KIND: what C holds.
+template <bool SW, int KIND>
+__global__ void __launch_bounds__(Mem<SW, KIND != kF32>::THREADS, 1)
     blocks_wide_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                        const __grid_constant__ CUtensorMap mapB2, const Params p) {
   constexpr int BN = SW ? 128 : 256;                   // columns of C (or of h) an item
-  using M = Mem<SW, OUT_BF16>;
+  using M = Mem<SW, KIND != kF32>;
   constexpr int STAGES = M::STAGES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -233,7 +252,7 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
   at += M::OUT_BYTES;
   float* ring = reinterpret_cast<float*>(at);          // [RING][RING_WORDS]
   at += RING * RING_WORDS * 4;
-  float* big = reinterpret_cast<float*>(at);           // [2][BM_CTA]
+  float* big = reinterpret_cast<float*>(at);           // [2][BM_CTA]: largest values of halves, or scales
   at += 2 * BM_CTA * 4;
   const uint32_t bar_base = base + (uint32_t)(at - base_ptr);
   uint8_t* bar_ptr = at;
@@ -521,7 +540,10 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           const int n = i.nb * BN + c * 128 + half * 64;
-          if (n < a.N) send_rows<true>(p, out + w * M::OUT_WARP + c * 4096, to, n, lane);
+          if (n >= a.N) break;
+          send_rows<KIND>(p, out + w * M::OUT_WARP + c * 4096, to, n, KIND == kScaled16 ? (int)a.ldc : a.N, lane);
+          if (KIND == kScaled16 && half == 0 && to >= 0)
+            a.ys[to * a.ldys + n / 128] = big[c * BM_CTA + quarter * 32 + lane];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(oempty_bar(w));
@@ -550,6 +572,7 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
       uint64_t acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0;
+      float scales[2] = {0.f, 0.f};                    // kScaled16: sums of |s0| and |s1|
       for (int kb = 0; kb < p.kblocks; ++kb) {
         const int u = kb % RING_BLOCKS;
         sync_signal(b, half);
@@ -561,6 +584,10 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
         const float* slot = ring + r * RING_WORDS + u;
         const float sa = slot[lrow * 4], sb0 = slot[BM_CTA * 4], sb1 = slot[BM_CTA * 4 + 4];
         const float s0 = sa * sb0, s1 = sa * sb1;
+        if constexpr (KIND == kScaled16) {
+          scales[0] += fabsf(s0);
+          scales[1] += fabsf(s1);
+        }
         const uint64_t d0 = pack2(__float_as_uint(s0), __float_as_uint(s0));
         const uint64_t d1 = pack2(__float_as_uint(s1), __float_as_uint(s1));
 #pragma unroll
@@ -642,8 +669,16 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
               continue;
             }
             ophase ^= 1u;
-            stage_rows<true>(a.alpha, mine, acc, lane);
-            stage_rows<true>(a.alpha, mine + 4096, acc + 32, lane);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float f = a.alpha;
+              if constexpr (KIND == kScaled16) {       // 1/s is exact
+                const float s = scale_for(scales[c]);
+                f = __uint_as_float((254u << 23) - __float_as_uint(s));
+                if (half == 0) big[c * BM_CTA + lrow] = s;
+              }
+              stage_rows<KIND>(f, mine + c * 4096, acc + c * 32, lane);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(ofull_bar(w));
           } else {
@@ -651,9 +686,9 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
             for (int c = 0; c < 4; ++c) {
               const int at = n + c / 2 * 128 + c % 2 * 32;
               if (at >= a.N) break;
-              stage_rows<OUT_BF16>(a.alpha, mine, acc + c * 16, lane);
+              stage_rows<KIND>(a.alpha, mine, acc + c * 16, lane);
               __syncwarp();
-              send_rows<OUT_BF16>(p, mine, to, at, lane);
+              send_rows<KIND>(p, mine, to, at, a.N, lane);
               __syncwarp();                            // read before the next rows are written
             }
           }
@@ -661,7 +696,7 @@ __global__ void __launch_bounds__(Mem<SW, OUT_BF16>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int at = n + c / 2 * 128 + c % 2 * 32;
-            if (at < a.N) store32<OUT_BF16>(p, to, at, acc + c * 16);
+            if (at < a.N) store32<KIND == kBf16>(p, to, at, acc + c * 16);
           }
         }
       }
@@ -705,7 +740,7 @@ struct PairInfo {
   int max_clusters = 0;
 };
 
-template <bool SW, bool OUT_BF16>
+template <bool SW, int KIND>
 int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap* mapB, const CUtensorMap* mapB2,
                 int num_sms, cudaStream_t s) {
   static PairInfo info[64];
@@ -714,7 +749,7 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  auto kernel = blocks_wide_kernel<SW, OUT_BF16>;
+  auto kernel = blocks_wide_kernel<SW, KIND>;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -723,8 +758,8 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(Mem<SW, OUT_BF16>::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = Mem<SW, OUT_BF16>::BYTES;
+  cfg.blockDim = dim3(Mem<SW, KIND != kF32>::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Mem<SW, KIND != kF32>::BYTES;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -734,8 +769,8 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
       cudaFuncAttributes fa;
       if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
       // with fewer registers at launch the warps that take some would wait forever
-      if (fa.numRegs < Mem<SW, OUT_BF16>::LAUNCH) return cudaErrorInvalidConfiguration;
-      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Mem<SW, OUT_BF16>::BYTES)) != cudaSuccess)
+      if (fa.numRegs < Mem<SW, KIND != kF32>::LAUNCH) return cudaErrorInvalidConfiguration;
+      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Mem<SW, KIND != kF32>::BYTES)) != cudaSuccess)
         return e;
       int n = 0;
       cfg.gridDim = dim3(2 * (num_sms / 2), 1, 1);
@@ -748,10 +783,11 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
   p.a = a;
   p.kblocks = (a.K + BK - 1) / BK;
   p.tiles_n = (a.N + (SW ? 128 : 256) - 1) / (SW ? 128 : 256);
-  const int osz = OUT_BF16 ? 2 : 4;
+  const int osz = KIND == kF32 ? 4 : 2;
   p.sa_vec = ((reinterpret_cast<uintptr_t>(a.sa) & 15u) == 0 && a.ldsa % 4 == 0) ? 1 : 0;
   p.c_vec = ((reinterpret_cast<uintptr_t>(a.C) & 15u) == 0 && (a.ldc * osz) % 16 == 0) ? 1 : 0;
-  p.c_rows = p.c_vec != 0 && a.N % (16 / osz) == 0 && a.beta == 0.f ? 1 : 0;
+  p.c_rows = p.c_vec != 0 && (KIND == kScaled16 || a.N % (16 / osz) == 0) && a.beta == 0.f ? 1 : 0;
+  if (KIND == kScaled16 && (p.c_rows == 0 || a.alpha != 1.f)) return cudaErrorInvalidValue;
   const long long items = blocks_row_tiles(a.rows, a.offsets != nullptr ? a.experts : 1, BM) * p.tiles_n;
   const long long clusters = items < info[dev].max_clusters ? items : info[dev].max_clusters;
   cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
@@ -764,9 +800,10 @@ int launch_impl(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap*
 int launch_blocks_wide(const BlocksArgs& a, const CUtensorMap* mapA, const CUtensorMap* mapB, const CUtensorMap* mapB2,
                        int num_sms, cudaStream_t s) {
   if (a.gather != 0) return cudaErrorInvalidValue;
-  if (a.B2 != nullptr) return launch_impl<true, true>(a, mapA, mapB, mapB2, num_sms, s);
-  return a.out_bf16 ? launch_impl<false, true>(a, mapA, mapB, mapB2, num_sms, s)
-                    : launch_impl<false, false>(a, mapA, mapB, mapB2, num_sms, s);
+  if (a.B2 != nullptr) return launch_impl<true, kBf16>(a, mapA, mapB, mapB2, num_sms, s);
+  if (a.ys != nullptr) return launch_impl<false, kScaled16>(a, mapA, mapB, mapB2, num_sms, s);
+  return a.out_bf16 ? launch_impl<false, kBf16>(a, mapA, mapB, mapB2, num_sms, s)
+                    : launch_impl<false, kF32>(a, mapA, mapB, mapB2, num_sms, s);
 }
 
 }  // namespace g3

@@ -1061,15 +1061,17 @@ int fp8_blocks(int M, int N, int K, float alpha, const uint8_t* A, int lda, cons
 }
 
 // Where the parts of an experts call's workspace begin, and how large it is.  y is held in
-// fp32 where all of it takes kExpertsY32 at most (half of L2, from where its sums are then
-// read: 64 tokens of 8 slots of 4096 take 170.0 us, 167.6 with y in bf16; 777 of 2 of 2048
-// 57.3 and 56.9), and in bf16 beyond (16384 of 8 of 4096: 2300 us, 2730 in fp32, 4 GB more through
-// memory), which costs an output 1.4 times the error of its own rounding.
+// fp32; where that takes more than kExpertsY32 (half of L2, from where its sums are read
+// otherwise) and the pair kernel makes it, in fp16 times a power of two for each 128 columns
+// of a row, which is off by 2^-11 of it at most where the output's own rounding is off by 2^-8.
+// Measured: 64 tokens of 8 slots of 4096 170.0 us, 167.6 with y in bf16; 777 of 2 of 2048 57.3 and 56.9;
+// 16384 of 8 of 4096 2316 us, 2240 in bf16 (whose outputs were 1.4 times as far off), and 430 more
+// in fp32 (4 GB more through memory).
 constexpr size_t kExpertsY32 = 64u << 20;
 struct ExpertsWorkspace {
-  size_t xq, xs, hq, hs, y, place, bytes;
-  long long ldx, ldxs, ldh, ldhs, ldy;   // codes and y in elements: rows of whole 16-byte vectors
-  bool y_bf16;
+  size_t xq, xs, hq, hs, y, ys, place, bytes;   // ys: the scales, behind y in 16 bits
+  long long ldx, ldxs, ldh, ldhs, ldy, ldys;    // codes and y in elements: rows of whole 16-byte vectors
+  bool y_large;
 };
 ExpertsWorkspace experts_ws(int tokens, int top_k, int hidden, int width) {
   auto up = [](size_t v, size_t to) { return (v + to - 1) / to * to; };
@@ -1086,11 +1088,10 @@ ExpertsWorkspace experts_ws(int tokens, int top_k, int hidden, int width) {
   w.hq = up(w.xs + slots * w.ldxs * 4, 256);
   w.hs = up(w.hq + slots * w.ldh, 256);
   w.y = up(w.hs + slots * w.ldhs * 4, 256);
-  const size_t y32 = slots * w.ldy * 4;
-  w.y_bf16 = y32 > kExpertsY32;
-  // never less for more tokens: a workspace of the largest call takes the smaller ones
-  const size_t y16 = y32 / 2 > kExpertsY32 ? y32 / 2 : kExpertsY32;
-  w.place = up(w.y + (w.y_bf16 ? y16 : y32), 256);
+  w.y_large = slots * w.ldy * 4 > kExpertsY32;
+  w.ldys = (hidden + kBlocksN - 1) / kBlocksN;   // at most an eighth of ldy: both fit where fp32 does
+  w.ys = w.y + slots * w.ldy * 2;
+  w.place = up(w.y + slots * w.ldy * 4, 256);
   w.bytes = up(w.place + slots * 4, 256);
   return w;
 }
@@ -1164,10 +1165,14 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
   d.A = a.hq; d.lda = ws.ldh; d.a_rows = d.rows; d.sa = a.hs; d.ldsa = ws.ldhs;
   d.B = w->down; d.ldb = w->ld_down; d.b_stride = sd;
   d.sb = w->down_scale; d.ldsb = hblocks; d.sb_stride = (long long)hblocks * fblocks;
-  d.C = base + ws.y; d.ldc = ws.ldy; d.out_bf16 = ws.y_bf16; d.alpha = 1.f;
+  d.C = base + ws.y; d.ldc = ws.ldy; d.out_bf16 = false; d.alpha = 1.f;
   BlocksPlan plan_up, plan_down;
   if (fast && ((rc = blocks_plan(a, dev, &plan_up)) != GEMM_OK || (rc = blocks_plan(d, dev, &plan_down)) != GEMM_OK))
     return rc;
+  if (ws.y_large && fast && plan_down.nt == kBlocksWide) {
+    d.ys = reinterpret_cast<float*>(base + ws.ys);
+    d.ldys = ws.ldys;
+  }
   // Row tiles of 32 gather a token's one row for each of its slots (a decode step's rows
   // are few); larger ones find the rows laid out by expert: a gathered row costs the copy
   // engine's issue about 20 cycles, and 256 rows a block of 128 k would be all it does.
@@ -1199,7 +1204,7 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
 
   CombineArgs c;
   c.tokens = tokens; c.top_k = top_k; c.cols = H;
-  c.y = d.C; c.y_bf16 = d.out_bf16; c.ldy = ws.ldy; c.weights = weights; c.out = O; c.ldo = ldo;
+  c.y = d.C; c.ys = d.ys; c.ldys = d.ldys; c.ldy = ws.ldy; c.weights = weights; c.out = O; c.ldo = ldo;
   c.vec = aligned16(O) && ldo % 8 == 0;
   err = launch_experts_combine(c, stream);
   if (err != cudaSuccess)

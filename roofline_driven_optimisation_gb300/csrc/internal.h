@@ -348,6 +348,10 @@ struct BlocksArgs {
   long long ldc;
   bool out_bf16;
   float alpha, beta;
+  // not null (pair kernel): C is fp16 times a power of two for each 128 columns of a row of C
+  // (ldys values a row), in whole vectors up to column ldc
+  float* ys;
+  long long ldys;
   uint8_t* hq;                  // SwiGLU: codes and scales (rows x ceil(N/128)) of silu(A*B) .* (A*B2)
   float* hs;
   long long ldh, ldhs;
@@ -384,8 +388,9 @@ int launch_blocks_generic(const BlocksArgs& a, cudaStream_t s);
 // O[t] = sum over j of weights[t][j] * Y[t * top_k + j]
 struct CombineArgs {
   int tokens, top_k, cols;
-  const void* y;                // bf16 or fp32, cols values a row, ldy apart
-  bool y_bf16;
+  const void* y;                // cols values a row, ldy apart: fp32, or fp16 times ys where that is not null
+  const float* ys;              // a scale for each 128 columns, ldys a row
+  long long ldys;
   long long ldy;
   const float* weights;
   void* out;
