@@ -21,14 +21,15 @@
 // and the eight drain warps wait at a hardware barrier with a signal warp that polls
 // for them.
 //
-// Roles (384 threads; one CTA an SM, two where K is split over tiles of 32 rows): warp 0 copies (TMA; the experts' rows of A through
-// tile::gather4, four rows an instruction, so that they are never laid out by expert; the
-// first stages' weights before the rows' numbers are known), warp 1 issues the MMAs,
+// Roles (384 threads; one CTA an SM, two where K is split over tiles of 32 rows): warp 0
+// copies (TMA; the experts' rows of A through tile::gather4, four rows an instruction, so
+// that they are never laid out by expert; the first stages' weights before the rows'
+// numbers are known), warp 1 issues the MMAs,
 // warp 2 multiplies sa with sb for the drain, warp 3 signals, warps 4-11 drain: warp w
 // the TMEM lanes 32*(w%4)..+31 (columns of B) and half of the tile's rows of A.
 //
 // Measured: gate and up of 64 tokens of 64 experts of 4096 and 1376 take 113 us, 0.97 of the
-// copy rate; 1 x 11008 x 4096 takes 8.4 us, of which 6.7 are its bytes; 77 x 4096 x 11008
+// copy rate; 1 x 11008 x 4096 takes 8.3 us, of which 6.7 are its bytes; 77 x 4096 x 11008
 // takes 13 us (7), as each column tile reads the rows again.
 //
 // Epilogue: the sums go through shared memory, 32 rows of A at a time, and a warp then has

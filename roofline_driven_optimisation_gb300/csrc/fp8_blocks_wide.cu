@@ -20,8 +20,9 @@
 // drain's 128 x 256 sums a CTA take 256 cycles of fma.rn.f32x2 (64 a warp, two warps a
 // scheduler, two cycles each), and 16 sums leave TMEM while the 16 before them are added:
 // one after the other cost the chain a quarter (356 us; loads of 32 spill, 350; of 8, 311).
-// Measured at 76 pairs x 19 items: 0.39 us a block and 1.5 us an item besides (2.6 where the
-// drain warps store the rows of C, as they do in fp32).  Without a drain a block takes 0.36
+// Measured at 76 pairs x 19 items: 0.38 us a block and 1.7 us an item besides (3.6 where the
+// drain warps store the rows of C, as they do in fp32; 8192 x 11008 x 4096 takes 299 us then, and
+// with beta, which reads C by rows of a thread each, 383 in bf16 and 506).  Without a drain a block takes 0.36
 // us, at the tensor cores' rate alone 0.33.  8192 x 11008 x 4096: 262 us, 2810 TFLOP/s.
 //
 // Roles (384 threads a CTA, 512 with bf16 rows of C): warp 0 copies (each CTA its rows of A

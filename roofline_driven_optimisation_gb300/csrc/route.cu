@@ -10,8 +10,12 @@
 // fp32, and looks at the gap between each two neighbours of the ranking, the last of the
 // kept and the first of the others included: where a gap is larger than what both
 // roundings can make, the order is that of 64 bits.  Experts with a smaller gap (of one
-// token in a thousand with sigmoid scores) are ranked again in fp64; equal logits with
-// equal biases are no gap but a tie, which goes to the lowest index in both.
+// token in a thousand with sigmoid scores and biases) are ranked again in fp64; equal logits
+// with equal biases are no gap but a tie, which goes to the lowest index in both.  Where the
+// last kept group and the first left out have a smaller gap, the whole token is done again by
+// its block, at about 15 us: a call of 16384 x 256 in 8 groups of which 4 are kept takes 39 us
+// with sigmoid scores and biases, 48 with softmax and biases, and 250 with sigmoid scores alone of
+// logits of deviation 6, whose largest are all next to 1.
 //
 // Layout: a warp a token.  Lane i holds the experts i*PER .. i*PER+PER-1, so that the
 // lowest lane with the largest key has the lowest index, and a round of the ranking is
