@@ -604,7 +604,8 @@ typedef struct {
  * whose y takes more than 64 MB (tokens * top_k * hidden * 4 bytes) may hold it in fp16
  * with a power of two for each 128 columns of a row.
  * The fast path needs 16-byte-aligned weights with leading dimensions and strides that
- * are multiples of 16; others run generic kernels.  At most 1024 experts.
+ * are multiples of 16; others run generic kernels.  At most 1024 experts, hidden and
+ * width at most 65535 * 1024.
  *
  * offsets must ascend from 0 to tokens * top_k and order hold every slot once.  An
  * expert's range that does not fit the call is taken as empty, a slot number outside

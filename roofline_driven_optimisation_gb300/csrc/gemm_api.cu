@@ -1068,6 +1068,7 @@ int fp8_blocks(int M, int N, int K, float alpha, const uint8_t* A, int lda, cons
 // 16384 of 8 of 4096 2316 us, 2240 in bf16 (whose outputs were 1.4 times as far off), and 430 more
 // in fp32 (4 GB more through memory).
 constexpr size_t kExpertsY32 = 64u << 20;
+constexpr int kExpertsMaxSize = 65535 * 1024;      // hidden and width: the sums' blocks of 1024 columns
 struct ExpertsWorkspace {
   size_t xq, xs, hq, hs, y, ys, place, bytes;   // ys: the scales, behind y in 16 bits
   long long ldx, ldxs, ldh, ldhs, ldy, ldys;    // codes and y in elements: rows of whole 16-byte vectors
@@ -1097,7 +1098,9 @@ ExpertsWorkspace experts_ws(int tokens, int top_k, int hidden, int width) {
 }
 
 size_t experts_workspace(int tokens, int top_k, int hidden, int width) {
-  if (tokens < 0 || top_k < 1 || hidden < 1 || width < 1 || (long long)tokens * top_k > 0x7fffffffll) return 0;
+  if (tokens < 0 || top_k < 1 || hidden < 1 || width < 1 || (long long)tokens * top_k > 0x7fffffffll ||
+      hidden > kExpertsMaxSize || width > kExpertsMaxSize)
+    return 0;
   return experts_ws(tokens, top_k, hidden, width).bytes;
 }
 
@@ -1115,7 +1118,7 @@ int experts(const gemm_expert_weights* w, int tokens, int top_k, const void* X, 
   if (E > kBlocksMaxExperts) return fail(GEMM_ERR_UNSUPPORTED, "%d experts: %d at most", E, kBlocksMaxExperts);
   if ((long long)tokens * top_k > 0x7fffffffll)
     return fail(GEMM_ERR_UNSUPPORTED, "%d tokens of %d slots: more than 2^31 - 1", tokens, top_k);
-  if (H > 65535 * 1024 || F > 65535 * 1024)
+  if (H > kExpertsMaxSize || F > kExpertsMaxSize)
     return fail(GEMM_ERR_UNSUPPORTED, "hidden %d or width %d too large", H, F);
   if (w->ld_up < F || w->ld_down < H || w->stride_up < 0 || w->stride_down < 0 || ldx < H || ldo < H)
     return fail(GEMM_ERR_INVALID_ARG, "leading dimension too small (weights %lld %lld, ldx=%lld ldo=%lld)", w->ld_up,

@@ -23,3 +23,12 @@ def test_more_tokens_never_need_less(g, top_k, hidden, width):
     tokens = sorted({1, 2, 3, 100, 16384} | {max(1, edge + d) for d in range(-3, 4)} | {2 * edge, 2 * edge + 1, 3 * edge})
     sizes = [g.gemm_experts_workspace(t, top_k, hidden, width) for t in tokens]
     assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+def test_sizes_that_no_call_takes_need_none(g):
+    most = 65535 * 1024
+    assert g.gemm_experts_workspace(1, 1, most, 1) > 0 and g.gemm_experts_workspace(1, 1, 1, most) > 0
+    # past 32 bits in every part, the largest that a call takes
+    assert g.gemm_experts_workspace(2 ** 31 - 1, 1, most, most) >= (2 ** 31 - 1) * (most + most + 4 * most)
+    for bad in ((1, 1, most + 1, 1), (1, 1, 1, most + 1), (1, 1, 2 ** 31 - 1, 1), (2 ** 31 - 1, 1, 2 ** 31 - 1, 2 ** 31 - 1)):
+        assert g.gemm_experts_workspace(*bad) == 0
