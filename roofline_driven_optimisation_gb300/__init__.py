@@ -964,7 +964,8 @@ class ExpertWeights:
         experts, hidden, width = gate.shape
         if max(gate.shape) > _INT_MAX:
             _too_large(*gate.shape)
-        if up.shape != gate.shape or up.stride() != gate.stride() or down.shape != (experts, width, hidden):
+        alike = all(a == b for n, a, b in zip(gate.shape, gate.stride(), up.stride()) if n > 1)
+        if up.shape != gate.shape or not alike or down.shape != (experts, width, hidden):
             raise ValueError("gate and up have one shape and one set of strides, down the transposed shape")
         for t in (gate, down):
             rows, cols = t.shape[1:]

@@ -86,6 +86,24 @@ def test_expert_weights(g):
             g.ExpertWeights(up, s, up, s, down, s)
 
 
+def test_strides_that_nothing_steps_over(g):
+    """gate and up of one expert, or one row, may differ in the strides of it."""
+    def weights(shape, step_gate, step_up):
+        def make(shape, step):
+            t = OnGpu(*shape, dtype=U8)
+            t.t, t.device = t.t.as_strided(shape, step), "cuda:0"
+            return t
+        down = make((shape[0], shape[2], shape[1]), (shape[1] * shape[2], shape[1], 1))
+        s = OnGpu(shape[0], 1, 1)
+        s.device = "cuda:0"
+        return g.ExpertWeights(make(shape, step_gate), s, make(shape, step_up), s, down, s)
+    for shape, gate, up in (((1, 16, 32), (512, 32, 1), (4096, 32, 1)), ((3, 1, 32), (32, 32, 1), (32, 64, 1))):
+        assert weights(shape, gate, up).experts == shape[0]
+    for shape, gate, up in (((2, 16, 32), (512, 32, 1), (4096, 32, 1)), ((1, 16, 32), (512, 32, 1), (512, 48, 1))):
+        with pytest.raises(ValueError, match="strides"):
+            weights(shape, gate, up)
+
+
 class Weights:
     experts, hidden, width, device, index, address = 4, 64, 32, torch.device("cpu"), 0, 0
 
